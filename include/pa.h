@@ -50,7 +50,8 @@ typedef enum {
     PA_ERR_UNSUPPORTED = 5  /* valid but not built: dtype / head dim / block size / group size */
 } pa_status;
 
-typedef enum { PA_F16 = 0, PA_BF16 = 1, PA_F32 = 2 } pa_dtype;
+/* PA_E4M3: the 8-bit pools of the quantised cache (its calls, pa_copy_blocks and pa_swap_blocks). */
+typedef enum { PA_F16 = 0, PA_BF16 = 1, PA_F32 = 2, PA_E4M3 = 3 } pa_dtype;
 
 /* Bits a kernel ORs into *dev_err. */
 #define PA_DEV_ERR_SLOT 0x1      /* slot_mapping entry >= NB*B */
@@ -227,6 +228,94 @@ pa_status pa_prefill(void* out, pa_dtype out_dtype, const void* q, const void* p
                      const int32_t* ctx_lens, const int32_t* q_start, int N, int T, int H_q, int H_kv, int D, int B,
                      int MB, int NB, int max_q_len, float scale, pa_dtype kv_dtype, void* workspace, size_t ws_bytes,
                      int* dev_err, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Quantised KV cache: half the bytes per token.  A row -- the D elements of
+ * one token's K or V for one KV head -- is held as D e4m3 values and a scale
+ * byte b that stands for 2^(b - 127): element d is q_d * 2^(b - 127).
+ *   qpool:  [NB][H_kv][2][B][D] e4m3 (index 0 on the third axis is K, 1 is V);
+ *   scales: [NB][H_kv][2][B] bytes.
+ * Slots, block tables and context lengths are those of the 16-bit pool, so the
+ * allocator's calls serve both.  pa_copy_blocks and pa_swap_blocks move blocks
+ * of a quantised cache with dtype E4M3: once for qpool, and once for scales
+ * with D = 1.
+ *
+ * pa_reshape_and_cache_quant quantises as it writes.  k, v: [T][H_kv][D] of
+ * dtype F16 or BF16.  A row's scale is the smallest 2^e with max_d |x_d| <=
+ * 448 * 2^e, e clamped to [-40, 40] (-40 for a row of zeros); q_d is x_d * 2^-e
+ * rounded to the nearest e4m3 (ties to even).  Scaling is exact, so an element
+ * is off by at most 2^-4 of itself, or 2^-10 of 2^e below 2^-6 * 2^e.  A
+ * magnitude above 448 * 2^40 (4.9e14) and an infinity become 448 * 2^40; a NaN
+ * stays NaN and does not count in the row's maximum.  slot_mapping as
+ * pa_reshape_and_cache (negative: padding; >= NB*B: skipped, PA_DEV_ERR_SLOT).
+ *
+ * pa_dequant_blocks restores blocks of a 16-bit pool [NB_dst][B][2][H_kv][D] of
+ * dtype F16 or BF16 (for pa_prefill over a quantised prefix, or to leave the
+ * quantised cache): pairs [n][2] int64 device memory, dst_pool[dst] = the
+ * values of block src.  Exact in bf16 and in fp16 for magnitudes in [2^-14,
+ * 65504] (above: +-65504, below: rounded).  A pair outside [0, NB_src) x [0,
+ * NB_dst) is skipped and flagged PA_DEV_ERR_BLOCK; destinations must be
+ * distinct.
+ *
+ * A scale byte outside [87, 167], which the write never produces, is read as
+ * the nearest of the two.  Supported: D in {64, 128}, B in {8, 16, 32},
+ * NB*B < 2^31; all tensors 16-byte aligned.  T == 0 and n == 0 are no-ops.
+ * ---------------------------------------------------------------------- */
+pa_status pa_reshape_and_cache_quant(const void* k, const void* v, void* qpool, void* scales,
+                                     const int64_t* slot_mapping, int T, int NB, int B, int H_kv, int D,
+                                     pa_dtype dtype, int* dev_err, void* stream);
+pa_status pa_dequant_blocks(void* dst_pool, int NB_dst, const void* qpool, const void* scales, int NB_src,
+                            const int64_t* pairs, int n, int B, int H_kv, int D, pa_dtype dtype, int* dev_err,
+                            void* stream);
+
+/* ------------------------------------------------------------------------
+ * pa_decode over the quantised cache: the same attention with K_t and V_t the
+ * rows' values.  q: [N][H_q][D] of q_dtype (F16 or BF16); out: [N][H_q][D], F32
+ * or q_dtype; a block-table entry outside [0, NB) reads as zeros and is flagged
+ * PA_DEV_ERR_BLOCK.  Everything else, the workspace (sized by
+ * pa_decode_workspace_bytes) and partition_tokens included, is as in pa_decode.
+ * Supported: D in {64, 128}, B in {8, 16, 32}, 1 <= H_q / H_kv <= 8, NB*B < 2^31.
+ * ---------------------------------------------------------------------- */
+pa_status pa_decode_quant(void* out, pa_dtype out_dtype, const void* q, pa_dtype q_dtype, const void* qpool,
+                          const void* scales, const int32_t* block_tables, const int32_t* ctx_lens, int N, int H_q,
+                          int H_kv, int D, int B, int MB, int NB, int max_ctx, float scale, int partition_tokens,
+                          void* workspace, size_t ws_bytes, int* dev_err, void* const* attend_events, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Attention for trees of drafted tokens (verification in speculative
+ * decoding).  Sequence s holds ctx_lens[s] tokens in the pool; the last n_s =
+ * q_start[s+1] - q_start[s] of them are its draft, whose queries are rows
+ * q_start[s] .. q_start[s+1]-1 of q.  Every drafted token sees the whole context
+ * before the draft, and of the draft the tokens its mask names (its ancestors
+ * and, usually, itself): drafted token j when bit j % 32 of word j / 32 of its
+ * row of tree_mask is set.
+ *     out[row][h] = sum_{t visible} softmax_t(scale * q[row][h] . K_t) V_t;
+ * a row that sees nothing (no context before the draft, no bit set) is zeros.
+ * Bits from n_s on are ignored.  K and V of drafted tokens that no row of the
+ * sequence sees (padding), and slots past the context, may hold anything, NaN
+ * included; a non-finite V of a drafted token that some rows see can reach the
+ * sequence's other rows.  The draft's own K/V must already be in the pool (forking the sequence before the draft and
+ * freeing the fork afterwards takes it out again).
+ * q, out: [T][H_q][D] (out F32 or q_dtype); q_start: [N+1] int32, not
+ * decreasing, q_start[N] <= T (rows of out past q_start[N] are not written);
+ * tree_mask: [T][mask_words] int32 words, max_q_len <= 32 * mask_words;
+ * max_q_len >= every n_s; n_s = 0 is allowed.  A sequence with n_s outside
+ * [0, max_q_len], q_start[s+1] > T, or a context below n_s or above MB*B is
+ * flagged PA_DEV_ERR_CTX and its rows are not written.
+ * pool: [NB][B][2][H_kv][D] of kv_dtype == q_dtype with scales NULL, or a
+ * quantised qpool (kv_dtype E4M3) with its scales.
+ * workspace: ws_bytes >= pa_decode_tree_workspace_bytes(...) of device memory,
+ * contents need not be initialised, not shared by calls that overlap on the GPU.
+ * Results do not depend on the order in which the GPU runs the call's parts.
+ * Supported: q_dtype F16/BF16, D in {64, 128}, B in {8, 16, 32}, H_q / H_kv <=
+ * 128, N <= 65535, NB*B < 2^31.
+ * ---------------------------------------------------------------------- */
+size_t pa_decode_tree_workspace_bytes(int N, int H_q, int H_kv, int D, int max_q_len);
+pa_status pa_decode_tree(void* out, pa_dtype out_dtype, const void* q, pa_dtype q_dtype, const void* pool,
+                         const void* scales, pa_dtype kv_dtype, const int32_t* block_tables, const int32_t* ctx_lens,
+                         const int32_t* q_start, const int32_t* tree_mask, int mask_words, int N, int T, int H_q,
+                         int H_kv, int D, int B, int MB, int NB, int max_q_len, float scale, void* workspace,
+                         size_t ws_bytes, int* dev_err, void* stream);
 
 /* ------------------------------------------------------------------------
  * pa_decode without a caller-provided workspace.  The pages have no

@@ -8,7 +8,9 @@ library raises.
 
 Layouts (see include/pa.h): pool [NB, B, 2, H_kv, D]; k, v [T, H_kv, D];
 q, out [N, H_q, D]; block_tables [N, MB] int32; ctx_lens [N] int32;
-slot_mapping [T] int64; copy pairs [n, 2] int64.
+slot_mapping [T] int64; copy pairs [n, 2] int64.  A quantised cache is two
+tensors: qpool [NB, H_kv, 2, B, D] (float8_e4m3fn or uint8) and scales
+[NB, H_kv, 2, B] (uint8 or float8_e8m0fnu, byte b = 2^(b - 127)).
 """
 from __future__ import annotations
 
@@ -23,7 +25,7 @@ import torch
 from . import _build
 
 PA_OK, PA_ERR_INVALID, PA_ERR_OOM, PA_ERR_STATE, PA_ERR_CUDA, PA_ERR_UNSUPPORTED = range(6)
-PA_F16, PA_BF16, PA_F32 = 0, 1, 2
+PA_F16, PA_BF16, PA_F32, PA_E4M3 = 0, 1, 2, 3
 PA_DEV_ERR_SLOT, PA_DEV_ERR_BLOCK, PA_DEV_ERR_CTX, PA_DEV_ERR_REQ, PA_DEV_ERR_TIMEOUT = 1, 2, 4, 8, 16
 _STATUS = {0: "PA_OK", 1: "PA_ERR_INVALID", 2: "PA_ERR_OOM", 3: "PA_ERR_STATE", 4: "PA_ERR_CUDA",
            5: "PA_ERR_UNSUPPORTED"}
@@ -95,6 +97,13 @@ def _declare(L):
         "pa_vkv_mapped_pages": ([P, i32, P], i32),
         "pa_prefill": ([P, i32, P, P, P, P, P, i32, i32, i32, i32, i32, i32, i32, i32, i32, f32, i32, P, sz, P, P],
                        i32),
+        "pa_reshape_and_cache_quant": ([P, P, P, P, P, i32, i32, i32, i32, i32, i32, P, P], i32),
+        "pa_dequant_blocks": ([P, i32, P, P, i32, P, i32, i32, i32, i32, i32, P, P], i32),
+        "pa_decode_quant": ([P, i32, P, i32, P, P, P, P, i32, i32, i32, i32, i32, i32, i32, i32, f32, i32, P, sz, P,
+                             P, P], i32),
+        "pa_decode_tree_workspace_bytes": ([i32, i32, i32, i32, i32], sz),
+        "pa_decode_tree": ([P, i32, P, i32, P, P, i32, P, P, P, P, i32, i32, i32, i32, i32, i32, i32, i32, i32, i32,
+                            f32, P, sz, P, P], i32),
         "pa_prefill_workspace_bytes": ([i32, i32, i32, i32, i32], sz),
         "pa_alloc_fork": ([P, i32, i32], i32),
         "pa_alloc_free_seq": ([P, i32], i32),
@@ -155,6 +164,39 @@ def _dtype_code(t: torch.dtype) -> int:
     raise PAError(PA_ERR_UNSUPPORTED, f"dtype {t}")
 
 
+_E4M3_TYPES = (torch.float8_e4m3fn, torch.uint8)
+_SCALE_TYPES = (torch.uint8, torch.float8_e8m0fnu)
+
+
+def _block_shape(pool):
+    """(NB, B, 2, H_kv, D, dtype code) of a pool whose blocks are moved whole: 16-bit, or a qpool or its scales
+    (8-bit, any order of the inner dimensions: only their product counts)."""
+    if pool.dtype in _E4M3_TYPES + _SCALE_TYPES:
+        if pool.dim() not in (4, 5):
+            raise PAError(PA_ERR_INVALID, "a quantised pool is qpool [NB, H_kv, 2, B, D] or scales [NB, H_kv, 2, B]")
+        return tuple(pool.shape) + (() if pool.dim() == 5 else (1,)) + (PA_E4M3,)
+    return tuple(pool.shape) + (_dtype_code(pool.dtype),)
+
+
+def _quant_cache(qpool, scales):
+    """(NB, H_kv, B, D) of a quantised cache, after checking that the two tensors are one."""
+    if not isinstance(qpool, torch.Tensor) or not isinstance(scales, torch.Tensor):
+        raise PAError(PA_ERR_INVALID, "qpool and scales must be tensors")
+    if qpool.dtype not in _E4M3_TYPES or scales.dtype not in _SCALE_TYPES:
+        raise PAError(PA_ERR_INVALID, "qpool must be float8_e4m3fn or uint8, scales uint8 or float8_e8m0fnu")
+    if qpool.dim() != 5 or qpool.shape[2] != 2 or tuple(scales.shape) != tuple(qpool.shape[:4]):
+        raise PAError(PA_ERR_INVALID, "qpool must be [NB, H_kv, 2, B, D] and scales [NB, H_kv, 2, B]")
+    return qpool.shape[0], qpool.shape[1], qpool.shape[3], qpool.shape[4]
+
+
+def _same_device(*tensors):
+    """The tensors live on the current device, where the call's kernels run."""
+    here = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.is_cuda and t.device.index != here:
+            raise PAError(PA_ERR_INVALID, f"tensors must be on the current device (cuda:{here}), got {t.device}")
+
+
 def _dev(t: torch.Tensor, name: str, dtype=None):
     if not isinstance(t, torch.Tensor):
         raise PAError(PA_ERR_INVALID, f"{name} must be a tensor")
@@ -210,12 +252,13 @@ def pa_reshape_and_cache(k, v, pool, slot_mapping, dev_err=None, stream=None):
 
 
 def pa_copy_blocks(pool, pairs, dev_err=None, stream=None):
-    """pool[dst] = pool[src] for each (src, dst) row of pairs [n, 2] (int64, device)."""
-    NB, B, _, H_kv, D = pool.shape
+    """pool[dst] = pool[src] for each (src, dst) row of pairs [n, 2] (int64, device).  A quantised cache takes two
+    calls, one with its qpool and one with its scales."""
+    NB, B, _, H_kv, D, code = _block_shape(pool)
     n = pairs.shape[0] if pairs.numel() else 0
     L = load()
     _check(L.pa_copy_blocks(_dev(pool, "pool"), _dev(pairs, "pairs", torch.int64) if n else None, n, NB, B, H_kv, D,
-                            _dtype_code(pool.dtype), _err_ptr(dev_err), _stream_ptr(stream)))
+                            code, _err_ptr(dev_err), _stream_ptr(stream)))
 
 
 def pa_decode_workspace_bytes(N, H_q, H_kv, D, max_ctx, partition_tokens=0) -> int:
@@ -267,8 +310,9 @@ def _acc(t: torch.Tensor, name: str):
 
 def pa_swap_blocks(dst_pool, src_pool, pairs, dev_err=None, stream=None):
     """dst_pool[dst] = src_pool[src] for (src, dst) rows of pairs [n, 2] int64; pools [NB, B, 2, H_kv, D] on the
-    device or in pinned host memory (swap out: device -> host, swap in: host -> device)."""
-    NBd, B, _, H_kv, D = dst_pool.shape
+    device or in pinned host memory (swap out: device -> host, swap in: host -> device).  A quantised cache takes two
+    calls, one with its qpool and one with its scales."""
+    NBd, B, _, H_kv, D, code = _block_shape(dst_pool)
     NBs = src_pool.shape[0]
     if tuple(src_pool.shape[1:]) != tuple(dst_pool.shape[1:]) or src_pool.dtype != dst_pool.dtype:
         raise PAError(PA_ERR_INVALID, "pools differ in block shape or dtype")
@@ -277,7 +321,7 @@ def pa_swap_blocks(dst_pool, src_pool, pairs, dev_err=None, stream=None):
     n = pairs.shape[0] if pairs.numel() else 0
     L = load()
     _check(L.pa_swap_blocks(_acc(dst_pool, "dst_pool"), NBd, _acc(src_pool, "src_pool"), NBs,
-                            _acc(pairs, "pairs") if n else None, n, B, H_kv, D, _dtype_code(dst_pool.dtype),
+                            _acc(pairs, "pairs") if n else None, n, B, H_kv, D, code,
                             _err_ptr(dev_err), _stream_ptr(stream)))
 
 
@@ -370,6 +414,105 @@ def pa_prefill(out, q, pool, block_tables, ctx_lens, q_start, max_q_len, scale=N
                         _dev(q_start, "q_start", torch.int32), N, T, H_q, H_kv, D, B, MB, NB, int(max_q_len), scale,
                         _dtype_code(pool.dtype), _dev(ws, "workspace") if ws is not None else None, ws_bytes,
                         _err_ptr(dev_err), _stream_ptr(stream)))
+    return out
+
+
+def pa_reshape_and_cache_quant(k, v, qpool, scales, slot_mapping, dev_err=None, stream=None):
+    """Quantise k, v [T, H_kv, D] into a quantised cache at slot_mapping [T] (int64): e4m3 values with the smallest
+    power-of-two scale per (token, head) row that keeps the row within 448."""
+    NB, H_kv, B, D = _quant_cache(qpool, scales)
+    if k.dim() != 3 or tuple(k.shape[1:]) != (H_kv, D) or tuple(v.shape) != tuple(k.shape):
+        raise PAError(PA_ERR_INVALID, "k and v must be [T, H_kv, D] of the cache's heads and head dim")
+    T = k.shape[0]
+    if slot_mapping.numel() != T:
+        raise PAError(PA_ERR_INVALID, "slot_mapping must have T entries")
+    args = (_dev(k, "k"), _dev(v, "v", k.dtype), _dev(qpool, "qpool"), _dev(scales, "scales"),
+            _dev(slot_mapping, "slot_mapping", torch.int64))
+    _same_device(k, v, qpool, scales, slot_mapping, dev_err)
+    _check(load().pa_reshape_and_cache_quant(*args, T, NB, B, H_kv, D, _dtype_code(k.dtype), _err_ptr(dev_err),
+                                             _stream_ptr(stream)))
+
+
+def pa_dequant_blocks(dst_pool, qpool, scales, pairs, dev_err=None, stream=None):
+    """dst_pool[dst] = the values of quantised block src, for (src, dst) rows of pairs [n, 2] (int64, device);
+    dst_pool [NB_dst, B, 2, H_kv, D] fp16 or bf16."""
+    NB, H_kv, B, D = _quant_cache(qpool, scales)
+    if dst_pool.dim() != 5 or tuple(dst_pool.shape[1:]) != (B, 2, H_kv, D):
+        raise PAError(PA_ERR_INVALID, "dst_pool must be [NB_dst, B, 2, H_kv, D] of the cache's shape")
+    if pairs.dtype != torch.int64 or (pairs.numel() and (pairs.dim() != 2 or pairs.shape[1] != 2)):
+        raise PAError(PA_ERR_INVALID, "pairs must be [n, 2] int64")
+    n = pairs.shape[0] if pairs.numel() else 0
+    args = (_dev(dst_pool, "dst_pool"), dst_pool.shape[0], _dev(qpool, "qpool"), _dev(scales, "scales"), NB,
+            _dev(pairs, "pairs", torch.int64) if n else None)
+    _same_device(dst_pool, qpool, scales, pairs, dev_err)
+    _check(load().pa_dequant_blocks(*args, n, B, H_kv, D, _dtype_code(dst_pool.dtype), _err_ptr(dev_err),
+                                    _stream_ptr(stream)))
+    return dst_pool
+
+
+def pa_decode_quant(out, q, qpool, scales, block_tables, ctx_lens, max_ctx, scale=None, partition_tokens=0,
+                    workspace=None, dev_err=None, attend_events=None, stream=None):
+    """Decode attention over a quantised cache: q [N, H_q, D] fp16 or bf16, out [N, H_q, D] fp32 or q's dtype (on the
+    device or in pinned host memory); the workspace is pa_decode's."""
+    NB, H_kv, B, D = _quant_cache(qpool, scales)
+    if q.dim() != 3 or q.shape[2] != D or tuple(out.shape) != tuple(q.shape):
+        raise PAError(PA_ERR_INVALID, "q and out must be [N, H_q, D] of the cache's head dim")
+    N, H_q, _ = q.shape
+    if block_tables.dim() != 2 or block_tables.shape[0] != N or ctx_lens.numel() != N:
+        raise PAError(PA_ERR_INVALID, "block_tables must be [N, MB] and ctx_lens [N]")
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    ws = _workspace(workspace, pa_decode_workspace_bytes(N, H_q, H_kv, D, int(max_ctx), partition_tokens), q.device)
+    args = (_acc(out, "out"), _dtype_code(out.dtype), _dev(q, "q"), _dtype_code(q.dtype), _dev(qpool, "qpool"),
+            _dev(scales, "scales"), _dev(block_tables, "block_tables", torch.int32),
+            _dev(ctx_lens, "ctx_lens", torch.int32))
+    _same_device(out, q, qpool, scales, block_tables, ctx_lens, ws, dev_err)
+    _check(load().pa_decode_quant(*args, N, H_q, H_kv, D, B, block_tables.shape[1], NB, int(max_ctx), scale,
+                                  int(partition_tokens), _dev(ws, "workspace"), ws.numel() * ws.element_size(),
+                                  _err_ptr(dev_err), _events_arg(attend_events, stream), _stream_ptr(stream)))
+    return out
+
+
+def pa_decode_tree_workspace_bytes(N, H_q, H_kv, D, max_q_len) -> int:
+    n = load().pa_decode_tree_workspace_bytes(N, H_q, H_kv, D, max_q_len)
+    if n == 0:
+        raise PAError(PA_ERR_INVALID, "invalid tree workspace arguments")
+    return int(n)
+
+
+def pa_decode_tree(out, q, pool, block_tables, ctx_lens, q_start, tree_mask, max_q_len, scale=None, scales=None,
+                   workspace=None, dev_err=None, stream=None):
+    """Attention of drafted tokens (each sequence's last, already in the pool) under a tree mask: q, out [T, H_q, D];
+    q_start [N+1] int32; tree_mask [T, W] int32, bit j % 32 of word j // 32 set where a row sees its sequence's
+    drafted token j.  pool is a 16-bit pool [NB, B, 2, H_kv, D] of q's dtype, or a quantised cache's qpool with its
+    scales."""
+    if q.dim() != 3 or tuple(out.shape) != tuple(q.shape):
+        raise PAError(PA_ERR_INVALID, "q and out must be [T, H_q, D]")
+    T, H_q, D = q.shape
+    if scales is not None:
+        NB, H_kv, B, D2 = _quant_cache(pool, scales)
+        code = PA_E4M3
+    else:
+        if pool.dim() != 5 or pool.shape[2] != 2 or pool.dtype != q.dtype:
+            raise PAError(PA_ERR_INVALID, "without scales the pool must be [NB, B, 2, H_kv, D] of q's dtype")
+        NB, B, _, H_kv, D2 = pool.shape
+        code = _dtype_code(pool.dtype)
+    N = ctx_lens.numel()
+    if D2 != D or block_tables.dim() != 2 or block_tables.shape[0] != N or q_start.numel() != N + 1:
+        raise PAError(PA_ERR_INVALID, "head dims must agree, block_tables be [N, MB], ctx_lens [N], q_start [N+1]")
+    if tree_mask.dim() != 2 or tree_mask.shape[0] != T:
+        raise PAError(PA_ERR_INVALID, "tree_mask must be [T, W] int32")
+    if T == 0 or max_q_len == 0:
+        return out
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    ws = _workspace(workspace, pa_decode_tree_workspace_bytes(N, H_q, H_kv, D, int(max_q_len)), q.device)
+    args = (_dev(out, "out"), _dtype_code(out.dtype), _dev(q, "q"), _dtype_code(q.dtype), _dev(pool, "pool"),
+            _dev(scales, "scales") if scales is not None else None, code,
+            _dev(block_tables, "block_tables", torch.int32), _dev(ctx_lens, "ctx_lens", torch.int32),
+            _dev(q_start, "q_start", torch.int32), _dev(tree_mask, "tree_mask", torch.int32), tree_mask.shape[1])
+    _same_device(out, q, pool, scales, block_tables, ctx_lens, q_start, tree_mask, ws, dev_err)
+    _check(load().pa_decode_tree(*args, N, T, H_q, H_kv, D, B, block_tables.shape[1], NB, int(max_q_len), scale,
+                                 _dev(ws, "workspace"), ws.numel() * ws.element_size(), _err_ptr(dev_err),
+                                 _stream_ptr(stream)))
     return out
 
 

@@ -127,10 +127,10 @@ __global__ void __launch_bounds__(kCopyThreads) copy_blocks_kernel(uint4* __rest
     }
 }
 
-pa_status launch_copy_blocks(void* pool, const int64_t* pairs, int n, int NB, int B, int H_kv, int D, int* dev_err,
+pa_status launch_copy_blocks(void* pool, const int64_t* pairs, int n, int NB, int64_t blk_bytes, int* dev_err,
                              cudaStream_t stream) {
     if (n == 0) return PA_OK;
-    const int64_t blk_vec = (int64_t)B * 2 * H_kv * D * 2 / 16;
+    const int64_t blk_vec = blk_bytes / 16;
     const int64_t chunk = (int64_t)kCopyThreads * kCopyUnroll;
     int64_t gy = (blk_vec + chunk - 1) / chunk;
     if (gy > 65535) gy = 65535;

@@ -122,14 +122,15 @@ pa_status pa_copy_blocks(void* pool, const int64_t* pairs, int n, int NB, int B,
                          int* dev_err, void* stream) {
     const NvtxRange nvtx_range("pa_copy_blocks");
     g_msg[0] = 0;
-    if (!kv_dtype_ok(dtype)) return fail(PA_ERR_UNSUPPORTED, "dtype must be F16 or BF16");
+    if (!kv_dtype_ok(dtype) && dtype != PA_E4M3) return fail(PA_ERR_UNSUPPORTED, "dtype must be F16, BF16 or E4M3");
     if (n < 0 || NB <= 0 || B <= 0 || H_kv <= 0 || D <= 0) return fail(PA_ERR_INVALID, "bad sizes");
-    if (((long long)B * 2 * H_kv * D * 2) % 16) return fail(PA_ERR_UNSUPPORTED, "block bytes must be a multiple of 16");
+    const long long blk_bytes = (long long)B * 2 * H_kv * D * (dtype == PA_E4M3 ? 1 : 2);
+    if (blk_bytes % 16) return fail(PA_ERR_UNSUPPORTED, "block bytes must be a multiple of 16");
     if (n > (1 << 30)) return fail(PA_ERR_INVALID, "too many pairs");
     if (n == 0) return PA_OK;
     if (!pool || !pairs) return fail(PA_ERR_INVALID, "null pointer argument");
     if (!aligned16(pool)) return fail(PA_ERR_INVALID, "pool must be 16-byte aligned");
-    return launch_copy_blocks(pool, pairs, n, NB, B, H_kv, D, dev_err, static_cast<cudaStream_t>(stream));
+    return launch_copy_blocks(pool, pairs, n, NB, blk_bytes, dev_err, static_cast<cudaStream_t>(stream));
 }
 
 // A pointer the GPU may dereference: device memory, managed memory, or page-locked host memory.
@@ -148,9 +149,9 @@ pa_status pa_swap_blocks(void* dst_pool, int NB_dst, const void* src_pool, int N
                          int B, int H_kv, int D, pa_dtype dtype, int* dev_err, void* stream) {
     const NvtxRange nvtx_range("pa_swap_blocks");
     g_msg[0] = 0;
-    if (!kv_dtype_ok(dtype)) return fail(PA_ERR_UNSUPPORTED, "dtype must be F16 or BF16");
+    if (!kv_dtype_ok(dtype) && dtype != PA_E4M3) return fail(PA_ERR_UNSUPPORTED, "dtype must be F16, BF16 or E4M3");
     if (n < 0 || NB_dst <= 0 || NB_src <= 0 || B <= 0 || H_kv <= 0 || D <= 0) return fail(PA_ERR_INVALID, "bad sizes");
-    const long long blk_bytes = (long long)B * 2 * H_kv * D * 2;
+    const long long blk_bytes = (long long)B * 2 * H_kv * D * (dtype == PA_E4M3 ? 1 : 2);
     if (blk_bytes % 16) return fail(PA_ERR_UNSUPPORTED, "block bytes must be a multiple of 16");
     if (n > (1 << 30)) return fail(PA_ERR_INVALID, "too many pairs");
     if (n == 0) return PA_OK;
@@ -280,6 +281,158 @@ pa_status pa_decode_contiguous(void* out, pa_dtype out_dtype, const void* q, con
     a.attend_events = attend_events;
     a.stream = static_cast<cudaStream_t>(stream);
     return launch_decode(a);
+}
+
+// ----------------------------------------------------------------------------- quantised cache, tree attention
+
+// Sizes of a quantised cache's calls: head dim, block size, and slots an int counts.
+static pa_status check_quant_shape(int NB, int B, int H_kv, int D) {
+    if (NB <= 0 || H_kv <= 0 || H_kv > 65535) return fail(PA_ERR_INVALID, "bad sizes");
+    if (D != 64 && D != 128) return fail(PA_ERR_UNSUPPORTED, "D must be 64 or 128 (got %d)", D);
+    if (B != 8 && B != 16 && B != 32) return fail(PA_ERR_UNSUPPORTED, "B must be 8, 16 or 32 (got %d)", B);
+    if ((long long)NB * B >= (1LL << 31)) return fail(PA_ERR_UNSUPPORTED, "NB * B must be < 2^31");
+    if ((long long)NB * H_kv >= (1LL << 31) - 1) return fail(PA_ERR_UNSUPPORTED, "NB * H_kv must be < 2^31 - 1");
+    return PA_OK;
+}
+
+pa_status pa_reshape_and_cache_quant(const void* k, const void* v, void* qpool, void* scales,
+                                     const int64_t* slot_mapping, int T, int NB, int B, int H_kv, int D,
+                                     pa_dtype dtype, int* dev_err, void* stream) {
+    const NvtxRange nvtx_range("pa_reshape_and_cache_quant");
+    g_msg[0] = 0;
+    if (!kv_dtype_ok(dtype)) return fail(PA_ERR_UNSUPPORTED, "dtype must be F16 or BF16");
+    if (T < 0) return fail(PA_ERR_INVALID, "bad sizes");
+    const pa_status st = check_quant_shape(NB, B, H_kv, D);
+    if (st != PA_OK) return st;
+    if (T == 0) return PA_OK;
+    if (!k || !v || !qpool || !scales || !slot_mapping) return fail(PA_ERR_INVALID, "null pointer argument");
+    if (!aligned16(k) || !aligned16(v) || !aligned16(qpool) || !aligned16(scales))
+        return fail(PA_ERR_INVALID, "k, v, qpool and scales must be 16-byte aligned");
+    return launch_quant_cache(k, v, qpool, scales, slot_mapping, T, NB, B, H_kv, D, dtype, dev_err,
+                              static_cast<cudaStream_t>(stream));
+}
+
+pa_status pa_dequant_blocks(void* dst_pool, int NB_dst, const void* qpool, const void* scales, int NB_src,
+                            const int64_t* pairs, int n, int B, int H_kv, int D, pa_dtype dtype, int* dev_err,
+                            void* stream) {
+    const NvtxRange nvtx_range("pa_dequant_blocks");
+    g_msg[0] = 0;
+    if (!kv_dtype_ok(dtype)) return fail(PA_ERR_UNSUPPORTED, "dtype must be F16 or BF16");
+    if (n < 0 || NB_dst <= 0) return fail(PA_ERR_INVALID, "bad sizes");
+    const pa_status st = check_quant_shape(NB_src, B, H_kv, D);
+    if (st != PA_OK) return st;
+    if (n > (1 << 30)) return fail(PA_ERR_INVALID, "too many pairs");
+    if (n == 0) return PA_OK;
+    if (!dst_pool || !qpool || !scales || !pairs) return fail(PA_ERR_INVALID, "null pointer argument");
+    if (!aligned16(dst_pool) || !aligned16(qpool) || !aligned16(scales))
+        return fail(PA_ERR_INVALID, "dst_pool, qpool and scales must be 16-byte aligned");
+    return launch_dequant_blocks(dst_pool, NB_dst, qpool, scales, NB_src, pairs, n, B, H_kv, D, dtype, dev_err,
+                                 static_cast<cudaStream_t>(stream));
+}
+
+pa_status pa_decode_quant(void* out, pa_dtype out_dtype, const void* q, pa_dtype q_dtype, const void* qpool,
+                          const void* scales, const int32_t* block_tables, const int32_t* ctx_lens, int N, int H_q,
+                          int H_kv, int D, int B, int MB, int NB, int max_ctx, float scale, int partition_tokens,
+                          void* workspace, size_t ws_bytes, int* dev_err, void* const* attend_events, void* stream) {
+    const NvtxRange nvtx_range("pa_decode_quant");
+    g_msg[0] = 0;
+    pa_status st = check_decode_common(out_dtype, q_dtype, out, q, ctx_lens, N, H_q, H_kv, D, max_ctx,
+                                       partition_tokens, workspace, ws_bytes);
+    if (st != PA_OK) return st;
+    st = check_quant_shape(NB, B, H_kv, D);
+    if (st != PA_OK) return st;
+    if (MB <= 0) return fail(PA_ERR_INVALID, "MB must be positive");
+    if (!qpool || !scales || !block_tables) return fail(PA_ERR_INVALID, "null pointer argument");
+    if (!aligned16(qpool) || !aligned16(scales)) return fail(PA_ERR_INVALID, "qpool and scales must be 16-byte aligned");
+    DecodeQuantArgs a;
+    a.out = out;
+    a.out_dtype = out_dtype;
+    a.q = q;
+    a.q_dtype = q_dtype;
+    a.qpool = qpool;
+    a.scales = scales;
+    a.tables = block_tables;
+    a.ctx_lens = ctx_lens;
+    a.N = N;
+    a.H_q = H_q;
+    a.H_kv = H_kv;
+    a.D = D;
+    a.B = B;
+    a.MB = MB;
+    a.NB = NB;
+    a.max_ctx = max_ctx;
+    a.scale = scale;
+    a.partition_tokens = partition_tokens;
+    a.workspace = workspace;
+    a.ws_bytes = ws_bytes;
+    a.dev_err = dev_err;
+    a.attend_events = attend_events;
+    a.stream = static_cast<cudaStream_t>(stream);
+    return launch_decode_quant(a);
+}
+
+size_t pa_decode_tree_workspace_bytes(int N, int H_q, int H_kv, int D, int max_q_len) {
+    return tree_workspace_bytes(N, H_q, H_kv, D, max_q_len);
+}
+
+pa_status pa_decode_tree(void* out, pa_dtype out_dtype, const void* q, pa_dtype q_dtype, const void* pool,
+                         const void* scales, pa_dtype kv_dtype, const int32_t* block_tables, const int32_t* ctx_lens,
+                         const int32_t* q_start, const int32_t* tree_mask, int mask_words, int N, int T, int H_q,
+                         int H_kv, int D, int B, int MB, int NB, int max_q_len, float scale, void* workspace,
+                         size_t ws_bytes, int* dev_err, void* stream) {
+    const NvtxRange nvtx_range("pa_decode_tree");
+    g_msg[0] = 0;
+    if (!kv_dtype_ok(q_dtype)) return fail(PA_ERR_UNSUPPORTED, "q_dtype must be F16 or BF16");
+    if (kv_dtype != PA_E4M3 && kv_dtype != q_dtype)
+        return fail(PA_ERR_UNSUPPORTED, "kv_dtype must be q_dtype or E4M3");
+    if (out_dtype != PA_F32 && out_dtype != q_dtype)
+        return fail(PA_ERR_UNSUPPORTED, "out_dtype must be F32 or the query dtype");
+    if (N <= 0 || N > 65535 || T < 0 || H_q <= 0 || MB <= 0 || max_q_len < 0 || mask_words <= 0)
+        return fail(PA_ERR_INVALID, "bad sizes");
+    pa_status st = check_quant_shape(NB, B, H_kv, D);
+    if (st != PA_OK) return st;
+    if (H_q % H_kv) return fail(PA_ERR_INVALID, "H_q (%d) must be a multiple of H_kv (%d)", H_q, H_kv);
+    if (H_q / H_kv > 128) return fail(PA_ERR_UNSUPPORTED, "H_q / H_kv must be <= 128");
+    if ((long long)MB * B >= (1LL << 31)) return fail(PA_ERR_UNSUPPORTED, "MB * B must be < 2^31");
+    if (max_q_len > 32LL * mask_words)
+        return fail(PA_ERR_INVALID, "a mask of %d words per row holds %lld drafted tokens, max_q_len is %d", mask_words,
+                    32LL * mask_words, max_q_len);
+    if (T == 0 || max_q_len == 0) return PA_OK;
+    if (!out || !q || !pool || !block_tables || !ctx_lens || !q_start || !tree_mask || !workspace)
+        return fail(PA_ERR_INVALID, "null pointer argument");
+    if ((kv_dtype == PA_E4M3) != (scales != nullptr))
+        return fail(PA_ERR_INVALID, "an E4M3 pool needs its scales, another pool has none");
+    if (!aligned16(out) || !aligned16(q) || !aligned16(pool) || !aligned16(scales) || !aligned16(workspace))
+        return fail(PA_ERR_INVALID, "out, q, pool, scales and workspace must be 16-byte aligned");
+    const size_t need = tree_workspace_bytes(N, H_q, H_kv, D, max_q_len);
+    if (ws_bytes < need) return fail(PA_ERR_INVALID, "workspace too small: %zu < %zu bytes", ws_bytes, need);
+    TreeArgs a;
+    a.out = out;
+    a.out_dtype = out_dtype;
+    a.q = q;
+    a.q_dtype = q_dtype;
+    a.pool = pool;
+    a.scales = scales;
+    a.tables = block_tables;
+    a.ctx_lens = ctx_lens;
+    a.q_start = q_start;
+    a.mask = reinterpret_cast<const uint32_t*>(tree_mask);
+    a.mask_words = mask_words;
+    a.N = N;
+    a.T = T;
+    a.H_q = H_q;
+    a.H_kv = H_kv;
+    a.D = D;
+    a.B = B;
+    a.MB = MB;
+    a.NB = NB;
+    a.max_q_len = max_q_len;
+    a.scale = scale;
+    a.workspace = workspace;
+    a.ws_bytes = ws_bytes;
+    a.dev_err = dev_err;
+    a.stream = static_cast<cudaStream_t>(stream);
+    return launch_tree(a);
 }
 
 size_t pa_prefill_workspace_bytes(int N, int H_kv, int D, int B, int MB) {

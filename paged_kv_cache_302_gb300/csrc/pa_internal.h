@@ -28,8 +28,62 @@ pa_status launch_swap_blocks(void* dst, int NB_dst, const void* src, int NB_src,
                              int64_t blk_bytes, int* dev_err, cudaStream_t stream);
 pa_status launch_update_tables(int32_t* tables, int N, int MB, const int32_t* updates, int n, int* dev_err,
                                cudaStream_t stream);
-pa_status launch_copy_blocks(void* pool, const int64_t* pairs, int n, int NB, int B, int H_kv, int D, int* dev_err,
+pa_status launch_copy_blocks(void* pool, const int64_t* pairs, int n, int NB, int64_t blk_bytes, int* dev_err,
                              cudaStream_t stream);
+
+// ----------------------------------------------------------------------------- quantised cache
+
+pa_status launch_quant_cache(const void* k, const void* v, void* qpool, void* scales, const int64_t* slot_mapping,
+                             int T, int NB, int B, int H_kv, int D, int dtype, int* dev_err, cudaStream_t stream);
+pa_status launch_dequant_blocks(void* pool, int NB_dst, const void* qpool, const void* scales, int NB_src,
+                                const int64_t* pairs, int n, int B, int H_kv, int D, int dtype, int* dev_err,
+                                cudaStream_t stream);
+
+struct DecodeQuantArgs {
+    void* out;
+    int out_dtype;
+    const void* q;
+    int q_dtype;
+    const void* qpool;
+    const void* scales;
+    const int32_t* tables;
+    const int32_t* ctx_lens;
+    int N, H_q, H_kv, D, B, MB, NB, max_ctx;
+    float scale;
+    int partition_tokens;
+    void* workspace;
+    size_t ws_bytes;
+    int* dev_err;
+    void* const* attend_events;
+    cudaStream_t stream;
+};
+
+pa_status launch_decode_quant(const DecodeQuantArgs& a);
+
+// ----------------------------------------------------------------------------- tree attention
+
+struct TreeArgs {
+    void* out;
+    int out_dtype;
+    const void* q;
+    int q_dtype;
+    const void* pool;    // 16-bit pool of q_dtype, or e4m3 qpool
+    const void* scales;  // null for a 16-bit pool
+    const int32_t* tables;
+    const int32_t* ctx_lens;
+    const int32_t* q_start;
+    const uint32_t* mask;
+    int mask_words, N, T, H_q, H_kv, D, B, MB, NB, max_q_len;
+    float scale;
+    void* workspace;
+    size_t ws_bytes;
+    int* dev_err;
+    cudaStream_t stream;
+};
+
+// 0 for invalid arguments.
+size_t tree_workspace_bytes(int N, int H_q, int H_kv, int D, int max_q_len);
+pa_status launch_tree(const TreeArgs& a);
 
 // ----------------------------------------------------------------------------- decode
 
