@@ -40,6 +40,7 @@
 #include <mutex>
 
 #include "pa_device.cuh"
+#include "tensor_map.h"
 
 namespace pa {
 
@@ -1030,16 +1031,23 @@ static EncodeTiledFn encode_fn() {
     return fn;
 }
 
-static pa_status encode(CUtensorMap* m, int kv_dtype, int rank, const void* base, const cuuint64_t* dims,
-                        const cuuint64_t* strides, const cuuint32_t* box) {
+pa_status encode_tensor_map(CUtensorMap* m, CUtensorMapDataType type, int rank, const void* base,
+                            const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
+                            CUtensorMapSwizzle swizzle) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
     cuuint32_t es[5] = {1, 1, 1, 1, 1};
-    CUresult r = fn(m, kv_dtype == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                    (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    CUresult r = fn(m, type, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, es,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);
     return PA_OK;
+}
+
+static pa_status encode(CUtensorMap* m, int kv_dtype, int rank, const void* base, const cuuint64_t* dims,
+                        const cuuint64_t* strides, const cuuint32_t* box) {
+    return encode_tensor_map(m, kv_dtype == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                             rank, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 static int env_int(const char* name, int dflt) {
@@ -1125,6 +1133,22 @@ static pa_status dispatch_paged(const DecodeArgs& a, const WorkspaceLayout& L, c
     return a.paged ? run_attend<T, D, true>(a, L, ta, tb, maxrec) : run_attend<T, D, false>(a, L, ta, tb, maxrec);
 }
 
+pa_status launch_plan(const int32_t* ctx_lens, const int32_t* req_ids, int N, int H_kv, int max_ctx, int cap, int N_max,
+                      void* workspace, const WorkspaceLayout& L, int* dev_err, cudaStream_t stream) {
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    int dev = 0, sms = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    // kPlanSlice sequences per CTA, at most one CTA per SM (larger slices beyond that)
+    const int plan_ctas = std::min((N + kPlanSlice - 1) / kPlanSlice, std::max(sms, 1));
+    cudaError_t e = launch_kernel(plan_kernel, dim3(plan_ctas), dim3(kPlanThreads), 0, stream, ctx_lens, req_ids, N,
+                                  H_kv, L.PT, max_ctx, cap, N_max, plan_bins(L.PT, max_ctx),
+                                  reinterpret_cast<int*>(ws + L.header), reinterpret_cast<int4*>(ws + L.records),
+                                  reinterpret_cast<int*>(ws + L.nparts), dev_err);
+    count_launch();
+    return e == cudaSuccess ? PA_OK : cuda_fail(e, "plan launch");
+}
+
 pa_status launch_decode(const DecodeArgs& a) {
     WorkspaceLayout L;
     if (!workspace_layout(a.N, a.H_q, a.H_kv, a.D, a.max_ctx, a.partition_tokens, &L))
@@ -1155,24 +1179,13 @@ pa_status launch_decode(const DecodeArgs& a) {
     }
 
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
-    int* header = reinterpret_cast<int*>(ws + L.header);
     int* nparts = reinterpret_cast<int*>(ws + L.nparts);
-    int4* rec = reinterpret_cast<int4*>(ws + L.records);
-    const int cap = a.paged ? a.MB * a.B : a.S_max;
-    int dev = 0, sms = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    // kPlanSlice sequences per CTA, at most one CTA per SM (larger slices beyond that)
-    const int plan_ctas = std::min((a.N + kPlanSlice - 1) / kPlanSlice, std::max(sms, 1));
-    cudaError_t e = launch_kernel(plan_kernel, dim3(plan_ctas), dim3(kPlanThreads), 0, a.stream, a.ctx_lens,
-                                  a.paged ? nullptr : a.req_ids, a.N, a.H_kv, L.PT, a.max_ctx, cap, a.N_max,
-                                  plan_bins(L.PT, a.max_ctx), header, rec, nparts, a.dev_err);
-    count_launch();
-    if (e != cudaSuccess) return cuda_fail(e, "plan launch");
+    pa_status st = launch_plan(a.ctx_lens, a.paged ? nullptr : a.req_ids, a.N, a.H_kv, a.max_ctx,
+                               a.paged ? a.MB * a.B : a.S_max, a.N_max, a.workspace, L, a.dev_err, a.stream);
+    if (st != PA_OK) return st;
 
     const long maxrec_l = (long)a.N * L.P * a.H_kv;
     const int maxrec = (int)std::min<long>(maxrec_l, 1L << 30);
-    pa_status st;
     if (a.kv_dtype == PA_BF16)
         st = a.D == 128 ? dispatch_paged<__nv_bfloat16, 128>(a, L, ta, tb, maxrec)
                         : dispatch_paged<__nv_bfloat16, 64>(a, L, ta, tb, maxrec);
