@@ -2,7 +2,7 @@
 //
 // The same three kernels as the 16-bit decode (schedule, attention, merge), of which the schedule and the merge are
 // those of decode.cu.  The attention kernel: CTAs of two warps.  Warp 1 (producer) streams each work record's (block,
-// head) chunks into a ring of 64-token stages, one TMA box (K rows, then V rows, swizzled) and one bulk copy of the
+// head) chunks into a ring of 32-token stages, one TMA box (K rows, then V rows, swizzled) and one bulk copy of the
 // 2 B scale bytes per block.  Warp 0 (consumer) computes with mma.sync m16n8k16, tokens on M, the <= 8 query heads
 // of the KV head on N:
 //     raw = K8 q'^T,  q' the query in fp16 (bf16 queries scaled row by row with a power of two, exactly);
@@ -12,16 +12,19 @@
 // (here a high and a low part, 2^-22) relative to the largest contribution to the output, whatever the scales' spread.
 // |ev| <= 40 keeps p 2^-ev and l within fp32.  K8 and V8 become fp16 in registers (exact: cvt e4m3x2 -> f16x2).
 #include <algorithm>
-#include <atomic>
-#include <cstdlib>
-#include <cstring>
+#include <type_traits>
 
 #include "quant.cuh"
 #include "tensor_map.h"
 
 namespace pa {
 
-constexpr int kQStageTok = 64;   // tokens of one KV head per pipeline stage
+// A consumer warp is bound by the latency of its own chain (scores, maximum, exponentials, products), so the SM needs
+// several: with 32-token stages six CTAs of three stages (D = 128) fit.  Measured on 8-KV-head bf16 caches, 256 sequences of
+// ~1500 tokens / 8 of 32768: 4 CTAs 141 / 103 us, 6 CTAs 133 / 95, 8 CTAs (two stages each) 138 / 101; 64-token
+// stages with 4 CTAs 141 / 97.
+constexpr int kQStageTok = 32;   // tokens of one KV head per pipeline stage
+constexpr int kQCtasPerSm = 6;
 constexpr int kQThreads = 64;
 
 enum : int { kQFirst = 1, kQLast = 2, kQDone = 4 };
@@ -48,7 +51,6 @@ struct QuantParams {
     const int32_t* ctx_lens;
     int N, H_kv, max_ctx, cap;
     float scale_log2;
-    int nstage;
     uint64_t wait_ns;
     int* err;
 };
@@ -57,11 +59,13 @@ struct QuantParams {
 // the query rows, the stage's description and its two barriers.
 template <int D>
 struct QGeo {
+    static constexpr int kStages = D == 128 ? 3 : 6;
     static constexpr uint32_t kSlot = kQStageTok * D * 2;
     static constexpr uint32_t kScales = kQStageTok * 2;
     static constexpr uint32_t kQ = kMaxGroup * D * 2;
     static constexpr uint32_t kPerStage = kSlot + kScales + kQ + sizeof(QStageMeta) + 16;
-    static size_t smem(int nstage) { return 1024 + (size_t)nstage * kPerStage + 16; }
+    static constexpr size_t kSmem = 1024 + (size_t)kStages * kPerStage + 16;
+    static_assert(kQCtasPerSm * (kSmem + 1024) <= 233472, "the CTAs of an SM fit its shared memory");
 };
 
 // Token of row i (0..7) of an 8-row half of the mma's M, chosen so that the 16- and 8-byte shared-memory reads of
@@ -102,14 +106,14 @@ template <typename T, int D, int LGB>
 __global__ void __launch_bounds__(kQThreads) attend_quant_kernel(const __grid_constant__ CUtensorMap tm,
                                                                  const QuantParams p) {
     using Geo = QGeo<D>;
+    constexpr int ST = kQStageTok, nstage = Geo::kStages;
     constexpr int B = 1 << LGB;
-    constexpr int BPS = kQStageTok / B;          // blocks per stage
+    constexpr int BPS = ST / B;                  // blocks per stage
     constexpr uint32_t kBox = 2u * B * D;        // bytes of one (block, head) chunk
-    constexpr int NSUB = kQStageTok / 16;        // 16-token mma tiles per stage
+    constexpr int NSUB = ST / 16;        // 16-token mma tiles per stage
     constexpr int NT = D / 16;                   // k-steps of the score product, m-tiles of the value product
     extern __shared__ uint8_t smem_raw[];
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const int nstage = p.nstage;
     uint8_t* sc_g = base + (size_t)nstage * Geo::kSlot;
     uint8_t* q_g = sc_g + (size_t)nstage * Geo::kScales;
     QStageMeta* meta = reinterpret_cast<QStageMeta*>(q_g + (size_t)nstage * Geo::kQ);
@@ -127,14 +131,22 @@ __global__ void __launch_bounds__(kQThreads) attend_quant_kernel(const __grid_co
         *abort_flag = 0;
         fence_mbar_init();
     }
-    if (threadIdx.x == 32) prefetch_tmap(&tm);
+    // The SM hands a CTA's two warps neighbouring slots, so with fixed roles every consumer would sit on the same two
+    // of its four schedulers: the CTAs in every other group of four slots swap the roles.
+    if (threadIdx.x == 0) {
+        uint32_t wid;
+        asm volatile("mov.u32 %0, %%warpid;" : "=r"(wid));
+        abort_flag[1] = (int)(wid >> 2 & 1);
+        prefetch_tmap(&tm);
+    }
     __syncthreads();
+    const bool producer = (int)(threadIdx.x >> 5) != abort_flag[1];
     // As in the 16-bit kernel, everything up to join_schedule() overlaps the schedule kernel, right after which this
     // kernel is always launched: the call's inputs are final here, only the schedule's records need the wait.
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31;
 
-    if (threadIdx.x >= 32) {
+    if (producer) {
         // ------------------------------------------------------------------ producer warp
         int total = 0, nwhole = 0;
         bool joined = false;
@@ -216,7 +228,7 @@ __global__ void __launch_bounds__(kQThreads) attend_quant_kernel(const __grid_co
             const int t0 = part * p.PT;
             const int ntok = min(p.PT, ctx - t0);
             const int nblk = (ntok + B - 1) / B;
-            const int nst = (ntok + kQStageTok - 1) / kQStageTok;
+            const int nst = (ntok + ST - 1) / ST;
             int st = 0;
             for (int cb = 0; cb < nblk && ok; cb += 32) {
                 int ent_nx = 0;
@@ -244,7 +256,7 @@ __global__ void __launch_bounds__(kQThreads) attend_quant_kernel(const __grid_co
                         m.h = h;
                         m.part = part;
                         m.ctx = ctx;
-                        m.n_valid = min(kQStageTok, ntok - st * kQStageTok);
+                        m.n_valid = min(ST, ntok - st * ST);
                         m.flags = (first ? kQFirst : 0) | (last ? kQLast : 0);
                         m.pad0 = m.pad1 = 0;
                         meta[slot] = m;
@@ -390,123 +402,130 @@ __global__ void __launch_bounds__(kQThreads) attend_quant_kernel(const __grid_co
             l0 = l1 = 0.f;
         }
         const int nvalid = mt.n_valid;
-
-        // scores of every tile, to y = raw 2^ek c + ev
-        float y[NSUB][4], iv[NSUB][2];  // iv: 2^-ev of tokens rt and rt + 8
-        float x0 = NEG_INF, x1 = NEG_INF;
-#pragma unroll
-        for (int j = 0; j < NSUB; ++j) {
-            y[j][0] = y[j][1] = y[j][2] = y[j][3] = NEG_INF;
-            iv[j][0] = iv[j][1] = 0.f;
-            if (16 * j < nvalid) {
-                float a[4] = {0.f, 0.f, 0.f, 0.f}, b[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int c = 0; c < NT / 4; ++c) {
-                    const uint4 lo = lds128(kv + tok_ofs(16 * j) + (kofs ^ (c * 64)));
-                    const uint4 hi = lds128(kv + tok_ofs(16 * j + 8) + (kofs ^ (c * 64)));
-                    const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
-#pragma unroll
-                    for (int w = 0; w < 4; ++w)
-                        Mma<__half>::run(w & 1 ? b : a, e4m3x2_to_f16x2(wl[w]), e4m3x2_to_f16x2(wh[w]),
-                                         e4m3x2_to_f16x2(wl[w] >> 16), e4m3x2_to_f16x2(wh[w] >> 16), qf[4 * c + w][0],
-                                         qf[4 * c + w][1]);
-                }
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int tok = 16 * j + 8 * half + rt;
-                    const uint32_t at = scb + sc_ofs(16 * j + 8 * half) + rt;
-                    const int bk = (int)lds8(at), bv = (int)lds8(at + B);
-                    const float fk = pow2i(scale_of(bk));
-                    const int ev = scale_of(bv);
-                    iv[j][half] = pow2i(-ev);
-                    if (tok < nvalid) {
-                        y[j][2 * half] = fmaf((a[2 * half] + b[2 * half]) * fk, c0, (float)ev);
-                        y[j][2 * half + 1] = fmaf((a[2 * half + 1] + b[2 * half + 1]) * fk, c1, (float)ev);
+        // one copy for whole stages, without a branch between the tiles, and one for a context's last
+        auto stage = [&](auto full_c) {
+            constexpr bool kFull = decltype(full_c)::value;
+            // scores of every tile, to y = raw 2^ek c + ev
+            float y[NSUB][4], iv[NSUB][2];  // iv: 2^-ev of tokens rt and rt + 8
+            float x0 = NEG_INF, x1 = NEG_INF;
+    #pragma unroll
+            for (int j = 0; j < NSUB; ++j) {
+                y[j][0] = y[j][1] = y[j][2] = y[j][3] = NEG_INF;
+                iv[j][0] = iv[j][1] = 0.f;
+                if (kFull || 16 * j < nvalid) {
+                    float a[4] = {0.f, 0.f, 0.f, 0.f}, b[4] = {0.f, 0.f, 0.f, 0.f};
+    #pragma unroll
+                    for (int c = 0; c < NT / 4; ++c) {
+                        const uint4 lo = lds128(kv + tok_ofs(16 * j) + (kofs ^ (c * 64)));
+                        const uint4 hi = lds128(kv + tok_ofs(16 * j + 8) + (kofs ^ (c * 64)));
+                        const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
+    #pragma unroll
+                        for (int w = 0; w < 4; ++w)
+                            Mma<__half>::run(w & 1 ? b : a, e4m3x2_to_f16x2(wl[w]), e4m3x2_to_f16x2(wh[w]),
+                                             e4m3x2_to_f16x2(wl[w] >> 16), e4m3x2_to_f16x2(wh[w] >> 16), qf[4 * c + w][0],
+                                             qf[4 * c + w][1]);
                     }
-                }
-                x0 = fmaxf(x0, fmaxf(y[j][0], y[j][2]));
-                x1 = fmaxf(x1, fmaxf(y[j][1], y[j][3]));
-            }
-        }
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) {
-            x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, o));
-            x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, o));
-        }
-        const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
-        const float a0 = fast_exp2(m0 - n0), a1 = fast_exp2(m1 - n1);
-        m0 = n0;
-        m1 = n1;
-        if (__any_sync(0xffffffffu, a0 != 1.f || a1 != 1.f)) {
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                O[i][0] *= a0;
-                O[i][1] *= a1;
-                O[i][2] *= a0;
-                O[i][3] *= a1;
-            }
-            l0 *= a0;
-            l1 *= a1;
-        }
-        // O^T += V8^T p^T, p as a high and a low fp16 part transposed into B fragments
-#pragma unroll
-        for (int j = 0; j < NSUB; ++j) {
-            if (16 * j < nvalid) {
-                const float p0 = fast_exp2(y[j][0] - n0), p1 = fast_exp2(y[j][1] - n1);
-                const float p2 = fast_exp2(y[j][2] - n0), p3 = fast_exp2(y[j][3] - n1);
-                l0 = fmaf(p0, iv[j][0], fmaf(p2, iv[j][1], l0));
-                l1 = fmaf(p1, iv[j][0], fmaf(p3, iv[j][1], l1));
-                const uint32_t h01 = Mma<__half>::pack(p0, p1), h23 = Mma<__half>::pack(p2, p3);
-                const float2 f01 = Mma<__half>::unpack(h01), f23 = Mma<__half>::unpack(h23);
-                const uint32_t lo01 = Mma<__half>::pack(p0 - f01.x, p1 - f01.y),
-                               lo23 = Mma<__half>::pack(p2 - f23.x, p3 - f23.y);
-                const uint32_t bh0 = movmatrix_trans(h01), bh1 = movmatrix_trans(h23);
-                const uint32_t bl0 = movmatrix_trans(lo01), bl1 = movmatrix_trans(lo23);
-                uint32_t w[4][NT / 2];  // tokens va, vb, va + 8, vb + 8
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    const uint32_t at = kv + tok_ofs(16 * j + 8 * (t >> 1)) + (t & 1 ? vofs_b : vofs_a);
-                    if constexpr (D == 128) {
-                        const uint4 x = lds128(at);
-                        w[t][0] = x.x;
-                        w[t][1] = x.y;
-                        w[t][2] = x.z;
-                        w[t][3] = x.w;
-                    } else {
-                        const uint2 x = lds64(at);
-                        w[t][0] = x.x;
-                        w[t][1] = x.y;
+    #pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const int tok = 16 * j + 8 * half + rt;
+                        const uint32_t at = scb + sc_ofs(16 * j + 8 * half) + rt;
+                        const int bk = (int)lds8(at), bv = (int)lds8(at + B);
+                        const float fk = pow2i(scale_of(bk));
+                        const int ev = scale_of(bv);
+                        iv[j][half] = pow2i(-ev);
+                        if (kFull || tok < nvalid) {
+                            y[j][2 * half] = fmaf((a[2 * half] + b[2 * half]) * fk, c0, (float)ev);
+                            y[j][2 * half + 1] = fmaf((a[2 * half + 1] + b[2 * half + 1]) * fk, c1, (float)ev);
+                        }
                     }
+                    x0 = fmaxf(x0, fmaxf(y[j][0], y[j][2]));
+                    x1 = fmaxf(x1, fmaxf(y[j][1], y[j][3]));
                 }
-                // V rows past the context may hold anything (even NaN): they count as zeros
-                if (16 * j + 16 > nvalid) {
-#pragma unroll
+            }
+    #pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+                x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, o));
+                x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, o));
+            }
+            const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
+            const float a0 = fast_exp2(m0 - n0), a1 = fast_exp2(m1 - n1);
+            m0 = n0;
+            m1 = n1;
+            if (__any_sync(0xffffffffu, a0 != 1.f || a1 != 1.f)) {
+    #pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    O[i][0] *= a0;
+                    O[i][1] *= a1;
+                    O[i][2] *= a0;
+                    O[i][3] *= a1;
+                }
+                l0 *= a0;
+                l1 *= a1;
+            }
+            // O^T += V8^T p^T, p as a high and a low fp16 part transposed into B fragments
+    #pragma unroll
+            for (int j = 0; j < NSUB; ++j) {
+                if (kFull || 16 * j < nvalid) {
+                    const float p0 = fast_exp2(y[j][0] - n0), p1 = fast_exp2(y[j][1] - n1);
+                    const float p2 = fast_exp2(y[j][2] - n0), p3 = fast_exp2(y[j][3] - n1);
+                    l0 = fmaf(p0, iv[j][0], fmaf(p2, iv[j][1], l0));
+                    l1 = fmaf(p1, iv[j][0], fmaf(p3, iv[j][1], l1));
+                    const uint32_t h01 = Mma<__half>::pack(p0, p1), h23 = Mma<__half>::pack(p2, p3);
+                    const float2 f01 = Mma<__half>::unpack(h01), f23 = Mma<__half>::unpack(h23);
+                    const uint32_t lo01 = Mma<__half>::pack(p0 - f01.x, p1 - f01.y),
+                                   lo23 = Mma<__half>::pack(p2 - f23.x, p3 - f23.y);
+                    const uint32_t bh0 = movmatrix_trans(h01), bh1 = movmatrix_trans(h23);
+                    const uint32_t bl0 = movmatrix_trans(lo01), bl1 = movmatrix_trans(lo23);
+                    uint32_t w[4][NT / 2];  // tokens va, vb, va + 8, vb + 8
+    #pragma unroll
                     for (int t = 0; t < 4; ++t) {
-                        const bool in = 16 * j + 8 * (t >> 1) + (t & 1 ? vb : va) < nvalid;
-#pragma unroll
-                        for (int i = 0; i < NT / 2; ++i) w[t][i] = in ? w[t][i] : 0u;
+                        const uint32_t at = kv + tok_ofs(16 * j + 8 * (t >> 1)) + (t & 1 ? vofs_b : vofs_a);
+                        if constexpr (D == 128) {
+                            const uint4 x = lds128(at);
+                            w[t][0] = x.x;
+                            w[t][1] = x.y;
+                            w[t][2] = x.z;
+                            w[t][3] = x.w;
+                        } else {
+                            const uint2 x = lds64(at);
+                            w[t][0] = x.x;
+                            w[t][1] = x.y;
+                        }
                     }
-                }
-#pragma unroll
-                for (int i = 0; i < NT / 2; ++i) {
-                    // (va, vb) pairs of elements 4 i .. 4 i + 3, then the same of the tokens 8 later
-                    const uint32_t u0 = __byte_perm(w[0][i], w[1][i], 0x5140), u1 = __byte_perm(w[0][i], w[1][i], 0x7362);
-                    const uint32_t u2 = __byte_perm(w[2][i], w[3][i], 0x5140), u3 = __byte_perm(w[2][i], w[3][i], 0x7362);
-                    {
-                        const uint32_t r0 = e4m3x2_to_f16x2(u0), r1 = e4m3x2_to_f16x2(u0 >> 16),
-                                       r2 = e4m3x2_to_f16x2(u2), r3 = e4m3x2_to_f16x2(u2 >> 16);
-                        Mma<__half>::run(O[2 * i], r0, r1, r2, r3, bh0, bh1);
-                        Mma<__half>::run(O[2 * i], r0, r1, r2, r3, bl0, bl1);
+                    // V rows past the context may hold anything (even NaN): they count as zeros
+                    if (!kFull && 16 * j + 16 > nvalid) {
+    #pragma unroll
+                        for (int t = 0; t < 4; ++t) {
+                            const bool in = 16 * j + 8 * (t >> 1) + (t & 1 ? vb : va) < nvalid;
+    #pragma unroll
+                            for (int i = 0; i < NT / 2; ++i) w[t][i] = in ? w[t][i] : 0u;
+                        }
                     }
-                    {
-                        const uint32_t r0 = e4m3x2_to_f16x2(u1), r1 = e4m3x2_to_f16x2(u1 >> 16),
-                                       r2 = e4m3x2_to_f16x2(u3), r3 = e4m3x2_to_f16x2(u3 >> 16);
-                        Mma<__half>::run(O[2 * i + 1], r0, r1, r2, r3, bh0, bh1);
-                        Mma<__half>::run(O[2 * i + 1], r0, r1, r2, r3, bl0, bl1);
+    #pragma unroll
+                    for (int i = 0; i < NT / 2; ++i) {
+                        // (va, vb) pairs of elements 4 i .. 4 i + 3, then the same of the tokens 8 later
+                        const uint32_t u0 = __byte_perm(w[0][i], w[1][i], 0x5140), u1 = __byte_perm(w[0][i], w[1][i], 0x7362);
+                        const uint32_t u2 = __byte_perm(w[2][i], w[3][i], 0x5140), u3 = __byte_perm(w[2][i], w[3][i], 0x7362);
+                        {
+                            const uint32_t r0 = e4m3x2_to_f16x2(u0), r1 = e4m3x2_to_f16x2(u0 >> 16),
+                                           r2 = e4m3x2_to_f16x2(u2), r3 = e4m3x2_to_f16x2(u2 >> 16);
+                            Mma<__half>::run(O[2 * i], r0, r1, r2, r3, bh0, bh1);
+                            Mma<__half>::run(O[2 * i], r0, r1, r2, r3, bl0, bl1);
+                        }
+                        {
+                            const uint32_t r0 = e4m3x2_to_f16x2(u1), r1 = e4m3x2_to_f16x2(u1 >> 16),
+                                           r2 = e4m3x2_to_f16x2(u3), r3 = e4m3x2_to_f16x2(u3 >> 16);
+                            Mma<__half>::run(O[2 * i + 1], r0, r1, r2, r3, bh0, bh1);
+                            Mma<__half>::run(O[2 * i + 1], r0, r1, r2, r3, bl0, bl1);
+                        }
                     }
                 }
             }
-        }
+        };
+        if (nvalid == ST)
+            stage(std::true_type{});
+        else
+            stage(std::false_type{});
         __syncwarp();
         if (lane == 0) mbar_arrive(empty_s + 8 * slot);
 
@@ -564,33 +583,19 @@ __global__ void __launch_bounds__(kQThreads) attend_quant_kernel(const __grid_co
 
 // ----------------------------------------------------------------------------- host side
 
-static int quant_env(const char* name, int dflt) {
-    const char* s = std::getenv(name);
-    return s && *s ? std::atoi(s) : dflt;
-}
-
 template <typename T, int D, int LGB>
 static pa_status run_attend_quant(const DecodeQuantArgs& a, const WorkspaceLayout& L, const CUtensorMap& tm) {
     auto kern = attend_quant_kernel<T, D, LGB>;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-    int sms = 0, smem_sm = 0;
+    int sms = 0;
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    cudaDeviceGetAttribute(&smem_sm, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev);
-    const int ctas = std::max(1, quant_env("PA_QUANT_CTAS_PER_SM", 4));
-    int nstage = quant_env("PA_QUANT_STAGES", 0);
-    if (nstage <= 0) nstage = (int)(((long)smem_sm / ctas - 1024 - 1040) / (long)QGeo<D>::kPerStage);
-    nstage = std::max(2, std::min(nstage, 16));
-    const size_t smem = QGeo<D>::smem(nstage);
+    constexpr size_t smem = QGeo<D>::kSmem;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(attend_quant)");
-    int per_sm = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kQThreads, smem);
-    if (e != cudaSuccess) return cuda_fail(e, "occupancy query");
-    if (per_sm < 1) return fail(PA_ERR_CUDA, "attention kernel does not fit on an SM (smem %zu)", smem);
     const long maxrec = std::min<long>((long)a.N * L.P * a.H_kv, 1L << 30);
-    const int grid = (int)std::max<long>(1, std::min<long>((long)per_sm * sms, maxrec));
+    const int grid = (int)std::max<long>(1, std::min<long>((long)kQCtasPerSm * sms, maxrec));
 
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
     QuantParams p;
@@ -616,7 +621,6 @@ static pa_status run_attend_quant(const DecodeQuantArgs& a, const WorkspaceLayou
     p.max_ctx = a.max_ctx;
     p.cap = (int)std::min<long long>((long long)a.MB * a.B, 0x7fffffff);
     p.scale_log2 = (float)((double)a.scale * 1.4426950408889634);  // log2(e)
-    p.nstage = nstage;
     p.wait_ns = wait_limit_ns();
     p.err = a.dev_err;
     if (a.attend_events && a.attend_events[0]) {
