@@ -13,4 +13,8 @@ pa_status encode_tensor_map(CUtensorMap* m, CUtensorMapDataType type, int rank, 
                             const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
                             CUtensorMapSwizzle swizzle);
 
+// One box is the chunk of one (block, head) of a quantised cache: D bytes, 2 B rows; third coordinate block * H_kv +
+// head (NB * H_kv is past the tensor).  Swizzled by row length: 128 bytes (D = 128) or 64 (D = 64).
+pa_status quant_tensor_map(CUtensorMap* m, const void* qpool, int NB, int H_kv, int B, int D);
+
 }  // namespace pa

@@ -1,38 +1,987 @@
-// tree.cu -- attention of drafted tokens over a paged cache under a tree mask.
-#include "attend_rows.cuh"
+// tree.cu -- attention of drafted tokens over a paged cache (16-bit or quantised) under a tree mask.
+//
+// Row (drafted token i, query head) of sequence s sees the context before the draft and the drafted tokens its mask
+// names.  The query rows of one KV head -- 128 / G tokens times the G heads -- form row tiles of up to 128 (tcgen05's
+// M), so each K/V byte serves every row of a tile, and a (sequence, KV head, row tile) is a unit of ceil(ctx / 128) key
+// tiles.
+//
+// tree_kernel: one persistent CTA per SM.  All key tiles of the call, in unit order, are cut into equal runs, one per
+// CTA, so the GPU is evenly loaded whatever the lengths; a CTA walks its run as segments (consecutive tiles of one
+// unit), and a unit that several CTAs share leaves partial results (m, l, unnormalised O) that tree_merge_kernel joins.
+// A CTA leaves at most two (its first and its last segment), so the workspace has a fixed size.  Roles:
+//   * warps 0-3 and 4-7, two softmax warpgroups: warpgroup w takes the segment's key tiles w, w + 2, ...; each thread
+//     owns one TMEM lane = one query row.  It reads its S row (tcgen05.ld), masks, keeps a running maximum (O is
+//     rescaled only when it grows by more than 2^8) and writes the probabilities over S.  The two warpgroups have
+//     accumulators of their own, O_0 and O_1, joined at the segment's end: while one works on its exponentials the
+//     tensor core serves the other.  They also load (quantised: and scale) the query rows.
+//   * warp 8 (TMA): K and V tiles into rings, block by block through the block table;
+//   * warp 9 (MMA, one thread): S_w = Q K^T (TMEM columns 128 w), O_w += P V (columns 256 + D w), P read from TMEM;
+//   * quantised pool, warps 10-15: e4m3 tiles from the raw ring to fp16 tiles in the K and V rings.
+// The value product takes P in V's 16-bit type: for bf16, or an fp32 output, as a high and a low part (two products).
+//
+// Quantised pool: query rows are scaled to fp16's range by a power of two (exact); K8 is converted to fp16 times 2^(ek -
+// emax + 7), emax the tile's largest exponent (a product is off by at most 2^-32 of the largest a key of the tile could
+// give), V8 exactly; y = raw c 2^(emax - 7) + ev, p = 2^(y - M), O += p V8, l += p 2^-ev, as in decode_quant.cu.
+#include <algorithm>
+#include <cstring>
+#include <type_traits>
+
+#include "quant.cuh"
+#include "tcgen05.cuh"
+#include "tensor_map.h"
 
 namespace pa {
 
+constexpr int kTRows = 128;    // query rows per tile (tcgen05 M), one TMEM lane each
+constexpr int kTKeys = 128;    // keys per tile (N of S, K of P V)
+constexpr uint32_t kTRegion = kTRows * 128;  // [128 rows][64 columns] 16-bit, 128-byte swizzled
+constexpr uint32_t kTTmem = 512;
+constexpr int kTreeMaxCtas = 160;  // CTAs of a call at most (the workspace holds two partial results for each)
+constexpr int kTreeMinTiles = 2;   // key tiles per CTA at least: one per warpgroup
+constexpr int kConvWarps = 6;
+
+struct TreeParams {
+    const void* q;
+    int q_bf16;
+    const int32_t* tables;
+    const int32_t* ctx_lens;
+    const int32_t* q_start;
+    const uint32_t* mask;
+    const uint8_t* scales;
+    int W, N, T, H_q, H_kv, G, TQ, lgB, MB, NB, max_q_len;
+    void* out;
+    int out_dtype;
+    float scale_log2;
+    int4* desc;       // per CTA: the unit it starts and leaves unfinished (sequence, unit, pieces), pieces 0: none
+    float* part_ml;   // [2 * CTAs][128][2]
+    float* part_acc;  // [2 * CTAs][128][D]
+    uint64_t wait_ns;
+    int* err;
+};
+
+// ----------------------------------------------------------------------------- work distribution
+
+struct TreeSeq {
+    int ctx, n, qs, nt, nmt;  // nt: key tiles (0: nothing to do), nmt: row tiles
+};
+
+// A sequence's work; an invalid one has none (and is flagged when `flag`).
+__device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int s, bool flag) {
+    TreeSeq q;
+    const int a = p.q_start[s], b = p.q_start[s + 1];
+    q.ctx = p.ctx_lens[s];
+    q.qs = a;
+    q.n = b - a;
+    q.nt = 0;
+    q.nmt = 0;
+    if (a < 0 || b < a || b > p.T || q.n > p.max_q_len ||
+        (q.n > 0 && (q.ctx < q.n || (int64_t)q.ctx > ((int64_t)p.MB << p.lgB)))) {
+        if (flag) flag_error(p.err, PA_DEV_ERR_CTX);
+        return q;
+    }
+    if (q.n > 0) {
+        q.nt = (q.ctx - 1) / kTKeys + 1;
+        q.nmt = (q.n + p.TQ - 1) / p.TQ;
+    }
+    return q;
+}
+
+__device__ __forceinline__ int64_t tree_cost(const TreeParams& p, const TreeSeq& q) {
+    return (int64_t)q.nt * q.nmt * p.H_kv;
+}
+
+// Consecutive key tiles j0 .. j1 - 1 of one unit.
+struct TreeSeg {
+    int s, h, mt, j0, j1, nt, ctx, n, qs;
+};
+
+// Walks a CTA's run of tiles segment by segment.
+struct TreeWalk {
+    int s, u, j;
+    int64_t left;
+    TreeSeq q;
+    __device__ __forceinline__ void start(const TreeParams& p, int s0, int64_t rem, int64_t count) {
+        s = s0;
+        left = count;
+        q = tree_seq(p, s, false);
+        u = (int)(rem / q.nt);
+        j = (int)(rem - (int64_t)u * q.nt);
+    }
+    __device__ __forceinline__ bool next(const TreeParams& p, TreeSeg& g) {
+        if (left <= 0) return false;
+        g.s = s;
+        g.h = u / q.nmt;
+        g.mt = u - g.h * q.nmt;
+        g.j0 = j;
+        g.j1 = (int)min((int64_t)q.nt, j + left);
+        g.nt = q.nt;
+        g.ctx = q.ctx;
+        g.n = q.n;
+        g.qs = q.qs;
+        left -= g.j1 - g.j0;
+        j = 0;
+        if (++u == q.nmt * p.H_kv && left > 0) {
+            u = 0;
+            do {
+                q = tree_seq(p, ++s, false);
+            } while (q.nt == 0);
+        }
+        return true;
+    }
+};
+
+__device__ __forceinline__ int64_t shfl64(int64_t v, int src) {
+    return (int64_t)__shfl_sync(0xffffffffu, (unsigned long long)v, src);
+}
+
+// The CTA's run [lo, hi) of the call's tiles, and the sequence it starts in with the tiles of it that lie before.
+// Every thread of the block calls it; `buf`: 40 words of 8 bytes.
+struct TreeRun {
+    int64_t per, lo, hi, rem;
+    int s;
+};
+
+template <int THREADS>
+__device__ __forceinline__ TreeRun tree_run(const TreeParams& p, int cta, int ctas, bool flag, int64_t* buf) {
+    constexpr int NW = THREADS / 32;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    TreeRun r;
+    int64_t sum = 0, c0 = 0;
+    for (int s = tid; s < p.N; s += THREADS) {
+        const int64_t c = tree_cost(p, tree_seq(p, s, flag));
+        if (s < THREADS) c0 = c;
+        sum += c;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += (int64_t)__shfl_xor_sync(0xffffffffu, (unsigned long long)sum, o);
+    if (lane == 0) buf[warp] = sum;
+    __syncthreads();
+    int64_t total = 0;
+    for (int w = 0; w < NW; ++w) total += buf[w];
+    r.per = (total + ctas - 1) / ctas;
+    if (r.per < kTreeMinTiles) r.per = kTreeMinTiles;
+    r.lo = r.per * cta;
+    r.hi = min(r.lo + r.per, total);
+    r.s = 0;
+    r.rem = 0;
+    if (r.lo >= total) return r;  // uniform: nothing to do
+    int64_t before = 0;
+    for (int base = 0; base < p.N; base += THREADS) {
+        const int s = base + tid;
+        const int64_t c = base == 0 ? c0 : (s < p.N ? tree_cost(p, tree_seq(p, s, false)) : 0);
+        int64_t incl = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t u = (int64_t)__shfl_up_sync(0xffffffffu, (unsigned long long)incl, o);
+            if (lane >= o) incl += u;
+        }
+        __syncthreads();
+        if (lane == 31) buf[warp] = incl;
+        __syncthreads();
+        int64_t pre = before, chunk = 0;
+        for (int w = 0; w < NW; ++w) {
+            if (w < warp) pre += buf[w];
+            chunk += buf[w];
+        }
+        const int64_t first = pre + incl - c;
+        if (c > 0 && first <= r.lo && r.lo < first + c) {
+            buf[32] = s;
+            buf[33] = r.lo - first;
+        }
+        before += chunk;
+        if (before > r.lo) break;  // uniform
+    }
+    __syncthreads();
+    r.s = (int)buf[32];
+    r.rem = buf[33];
+    return r;
+}
+
+// ----------------------------------------------------------------------------- masks
+
+// Bits b = 0..31: whether drafted token `tok` of the sequence sees key k0 + b, j0 = k0 - (context before the draft).
+__device__ __forceinline__ uint32_t tree_word(const uint32_t* row, int n, int x) {
+    if (x < 0) return 0xffffffffu;
+    if (32 * x >= n) return 0u;
+    return row[x] & (n - 32 * x < 32 ? (1u << (n - 32 * x)) - 1u : 0xffffffffu);
+}
+__device__ __forceinline__ uint32_t tree_visible(const TreeParams& p, const TreeSeg& g, int tok, int j0) {
+    if (j0 >= g.n) return 0u;
+    if (j0 <= -32) return 0xffffffffu;
+    const uint32_t* row = p.mask + (size_t)(g.qs + tok) * p.W;
+    const int x = j0 >> 5;
+    return __funnelshift_r(tree_word(row, g.n, x), tree_word(row, g.n, x + 1), j0 & 31);
+}
+
+// Keys of a tile that some row of the row tile sees: the same four words in every lane.
+__device__ __forceinline__ void tree_union(const TreeParams& p, const TreeSeg& g, int k0, uint32_t (&u)[4]) {
+    const int lane = threadIdx.x & 31, tok0 = g.mt * p.TQ, ntok = min(p.TQ, g.n - tok0);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        uint32_t v = 0;
+        for (int t = lane; t < ntok; t += 32) v |= tree_visible(p, g, tok0 + t, k0 + 32 * c - (g.ctx - g.n));
+        u[c] = __reduce_or_sync(0xffffffffu, v);
+    }
+}
+
+// ----------------------------------------------------------------------------- the kernel
+
+template <int D, bool QUANT>
+struct TreeGeo {
+    static constexpr int DH = D / 64;
+    static constexpr uint32_t kTile = DH * kTRegion;      // one 16-bit tile, [8-row group][column half][8 rows][128 B]
+    static constexpr uint32_t kGroup = DH * 1024;
+    static constexpr int NS = QUANT ? 2 : 3;              // K and V ring slots
+    static constexpr int NR = QUANT ? (D == 128 ? 2 : 4) : 0;      // raw ring slots: K and V rows of a tile, scales
+    static constexpr uint32_t kRaw = 2u * kTKeys * D, kRawScales = 2 * kTKeys;
+    static constexpr uint32_t kExp = QUANT ? 2 * kTKeys * 4 : 0;   // per V slot: ev and 2^-ev of the keys
+    static constexpr int kThreads = QUANT ? 512 : 320;
+    // Q | K ring | V ring | raw ring | raw scales | exponents | barriers and small things
+    static constexpr uint32_t oK = kTile, oV = oK + NS * kTile, oRaw = oV + NS * kTile, oRawSc = oRaw + NR * kRaw,
+                              oExp = oRawSc + NR * kRawScales, oBar = oExp + NS * kExp;
+    static constexpr int kBars = 4 + 4 * NS + 6 + 2 * NR;
+    static constexpr uint32_t oSmall = oBar + 8 * kBars;
+    static constexpr size_t kSmem = oSmall + 64;
+    static_assert(kSmem <= 232448, "shared memory");
+    static_assert(8 * 40 <= kTile && 2 * kTRows * 8 <= kTile, "the Q tile's space also serves the start and the joins");
+};
+
+template <typename T, int D, bool QUANT, bool SPLIT>
+__global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
+    tree_kernel(const __grid_constant__ CUtensorMap tm, const TreeParams p) {
+    using Geo = TreeGeo<D, QUANT>;
+    constexpr int NS = Geo::NS, NR = Geo::NR;
+    constexpr int NK = D / 16, NT = kTKeys / 16;
+    constexpr bool kBf16 = !QUANT && std::is_same<T, __nv_bfloat16>::value;  // type of the products
+    using PT = typename std::conditional<kBf16, __nv_bfloat16, __half>::type;
+    static_assert(!kBf16 || SPLIT, "a bf16 value product takes P in two parts");
+    constexpr uint32_t idesc_s = umma_idesc(kBf16, kTRows, kTKeys, false);
+    constexpr uint32_t idesc_o = umma_idesc(kBf16, kTRows, D, true);
+    constexpr uint32_t kTile = Geo::kTile, kGroup = Geo::kGroup;
+    constexpr float NEG_INF = -INFINITY;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t sb = smem_addr(smem_raw);
+    const uint32_t sQ = sb, sK = sb + Geo::oK, sV = sb + Geo::oV, sBar = sb + Geo::oBar;
+    const uint32_t qfull = sBar, qfree = qfull + 8, ofree = qfree + 8, mmadone = ofree + 8, kfull = mmadone + 8,
+                   kfree = kfull + 8 * NS, vfull = kfree + 8 * NS, vfree = vfull + 8 * NS, sfull = vfree + 8 * NS,
+                   prdy = sfull + 16, pvd = prdy + 16, rfull = pvd + 16, rfree = rfull + 8 * NR;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_raw + Geo::oSmall);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    volatile int* armed = abort_flag + 1;  // tiles whose K / V (quantised: raw) copies have been issued
+    float* kmul = reinterpret_cast<float*>(tmem_slot + 4);  // per V slot: 2^(emax - 7) of the tile's K
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    griddep_wait();
+    griddep_launch_dependents();
+    // swizzled tiles need the 1024-byte alignment that dynamic shared memory has when there is no static
+    if (sb & 1023u) {
+        if (tid == 0) flag_error(p.err, PA_DEV_ERR_TIMEOUT);
+        return;
+    }
+    const TreeRun run =
+        tree_run<Geo::kThreads>(p, blockIdx.x, gridDim.x, blockIdx.x == 0, reinterpret_cast<int64_t*>(smem_raw));
+    if (tid == 0) p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (run.lo >= run.hi) return;
+
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_slot)),
+                     "r"(kTTmem)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (tid == 0) {
+        for (int i = 0; i < Geo::kBars; ++i) mbar_init(sBar + 8 * i, 1);
+        mbar_init(qfull, 256);
+        mbar_init(ofree, 256);
+        mbar_init(prdy, 128);
+        mbar_init(prdy + 8, 128);
+        if (QUANT) {
+            for (int i = 0; i < NS; ++i) {
+                mbar_init(kfull + 8 * i, kConvWarps);
+                mbar_init(vfull + 8 * i, kConvWarps);
+            }
+            for (int i = 0; i < NR; ++i) mbar_init(rfree + 8 * i, kConvWarps);
+        }
+        *abort_flag = 0;
+        armed[0] = armed[1] = 0;
+        fence_mbar_init();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    // A wait that runs out sets the abort flag, after which every other wait returns at once: no role leaves its loop
+    // early, so the barriers between threads are always met.
+    auto waited = [&](uint32_t bar, uint32_t parity) {
+        const bool w = mbar_wait_bounded(bar, parity, abort_flag, p.wait_ns);
+        if (!w) *abort_flag = 1;
+        return w;
+    };
+    auto slot = [](int i) { return (uint32_t)(i % NS); };
+    auto ph = [](int i) { return (uint32_t)((i / NS) & 1); };
+    bool ok = true;
+    TreeWalk walk;
+    walk.start(p, run.s, run.rem, run.hi - run.lo);
+    TreeSeg g;
+    const int B = 1 << p.lgB;
+
+    if (warp == 8) {
+        // ------------------------------------------------------------ TMA producer: lane b copies the tile's block b
+        const uint64_t pol = policy_evict_first();
+        int t = 0;  // tiles so far
+        while (ok && walk.next(p, g)) {
+            auto entry = [&](int j) {
+                const int nblk = (min(kTKeys, g.ctx - j * kTKeys) + B - 1) >> p.lgB;
+                return lane < nblk ? p.tables[(size_t)g.s * p.MB + ((size_t)j * kTKeys >> p.lgB) + lane] : 0;
+            };
+            int mine = entry(g.j0);
+            for (int j = g.j0; j < g.j1 && ok; ++j, ++t) {
+                const int nblk = (min(kTKeys, g.ctx - j * kTKeys) + B - 1) >> p.lgB;
+                int e = mine;
+                if (j + 1 < g.j1) mine = entry(j + 1);
+                const bool good = (unsigned)e < (unsigned)p.NB;
+                if (lane < nblk && !good) flag_error(p.err, PA_DEV_ERR_BLOCK);
+                if (!good) e = p.NB;  // past the tensor: TMA fills zeros
+                if constexpr (QUANT) {
+                    const uint32_t b = (uint32_t)(t % NR), bar = rfull + 8 * b;
+                    if (t >= NR) ok = waited(rfree + 8 * b, (uint32_t)((t / NR - 1) & 1));
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        armed[0] = t + 1;  // expect_tx and every copy below, with no wait in between
+                        mbar_arrive_expect_tx(bar, (uint32_t)nblk * 2 * B * (D + 1));
+                    }
+                    __syncwarp();
+                    if (lane < nblk) {
+                        tma_load_3d(sb + Geo::oRaw + b * Geo::kRaw + (uint32_t)lane * 2 * B * D, &tm, bar, 0, 0,
+                                    e * p.H_kv + g.h, pol);
+                        bulk_load(sb + Geo::oRawSc + b * Geo::kRawScales + (uint32_t)lane * 2 * B,
+                                  p.scales + ((size_t)(good ? e : 0) * p.H_kv + g.h) * (2 * B), 2 * B, bar);
+                    }
+                } else {
+                    const uint32_t b = slot(t);
+                    for (int which = 0; which < 2 && ok; ++which) {
+                        if (t >= NS) ok = waited((which ? vfree : kfree) + 8 * b, ph(t - NS));
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        const uint32_t bar = (which ? vfull : kfull) + 8 * b;
+                        if (lane == 0) {
+                            armed[which] = t + 1;  // as above
+                            mbar_arrive_expect_tx(bar, (uint32_t)nblk * B * D * 2);
+                        }
+                        __syncwarp();
+                        if (lane < nblk)
+                            tma_load_5d((which ? sV : sK) + b * kTile + (uint32_t)lane * B * D * 2, &tm, bar, 0, 0, 0,
+                                        e * (B / 8), which * p.H_kv + g.h, pol);
+                    }
+                }
+            }
+        }
+    } else if (warp == 9) {
+        // ------------------------------------------------------------ MMA issuer
+        const uint64_t dq = umma_desc(sQ, 16, 1024);
+        auto issue_s = [&](int w, int t) {
+            const uint64_t dk = umma_desc(sK + slot(t) * kTile, 16, kGroup);
+#pragma unroll
+            for (int ks = 0; ks < NK; ++ks)
+                umma_f16(tmem + (uint32_t)w * kTKeys, dq + (ks >> 2) * (kTRegion >> 4) + (ks & 3) * 2,
+                         dk + (ks >> 2) * (1024 >> 4) + (ks & 3) * 2, idesc_s, ks > 0);
+            umma_commit(sfull + 8 * w);
+            umma_commit(kfree + 8 * slot(t));
+        };
+        auto issue_pv = [&](int w, int t, bool first) {
+            const uint64_t dv = umma_desc(sV + slot(t) * kTile, 1024, kGroup);
+            const uint32_t pc = tmem + (uint32_t)w * kTKeys, oc = tmem + 2 * kTKeys + (uint32_t)w * D;
+#pragma unroll
+            for (int ks = 0; ks < NT; ++ks) {
+                const uint64_t vd = dv + (uint64_t)(ks * ((2 * kGroup) >> 4));
+                umma_f16_ta(oc, pc + ks * 8, vd, idesc_o, !first || ks > 0);
+                if (SPLIT) umma_f16_ta(oc, pc + kTKeys / 2 + ks * 8, vd, idesc_o, 1u);
+            }
+            umma_commit(pvd + 8 * w);
+            umma_commit(vfree + 8 * slot(t));
+        };
+        if (lane == 0) {
+            int t = 0, c[2] = {0, 0};  // tiles so far; tiles of each warpgroup with S issued
+            for (int seg = 0; ok && walk.next(p, g); ++seg) {
+                const int nt = g.j1 - g.j0;
+                // S of tile i: its buffer is free once the products have read the P that lay there
+                auto start_s = [&](int i) {
+                    const int w = i & 1;
+                    ok = (c[w] == 0 || waited(pvd + 8 * w, (uint32_t)((c[w] - 1) & 1))) &&
+                         waited(kfull + 8 * slot(t + i), ph(t + i));
+                    if (!ok) return;
+                    tc_fence_after();
+                    issue_s(w, t + i);
+                    ++c[w];
+                    if (i + 1 == nt) umma_commit(qfree);
+                };
+                ok = waited(qfull, (uint32_t)(seg & 1));
+                if (ok) start_s(0);
+                if (ok && nt > 1) start_s(1);
+                for (int i = 0; i < nt && ok; ++i) {
+                    const int w = i & 1;
+                    ok = waited(prdy + 8 * w, (uint32_t)((c[w] - 1) & 1)) && waited(vfull + 8 * slot(t + i), ph(t + i)) &&
+                         (i >= 2 || seg == 0 || waited(ofree, (uint32_t)((seg - 1) & 1)));
+                    if (!ok) break;
+                    tc_fence_after();
+                    issue_pv(w, t + i, i < 2);
+                    if (i + 2 < nt) start_s(i + 2);
+                }
+                t += nt;
+            }
+            umma_commit(mmadone);  // arrives once every product issued above has completed
+        }
+        __syncwarp();
+    } else if (warp >= 10) {
+        // ------------------------------------------------------------ converters (quantised pool)
+        if constexpr (QUANT) {
+            const int cw = warp - 10;
+            constexpr int L = D / 16;                     // 16-byte pieces of a row
+            constexpr int kSteps = kTKeys * L / 32;       // warp steps of a tile
+            int t = 0;
+            while (walk.next(p, g)) {
+                for (int j = g.j0; j < g.j1; ++j, ++t) {
+                    const int k0 = j * kTKeys, nvalid = min(kTKeys, g.ctx - k0);
+                    const uint32_t rb = (uint32_t)(t % NR);
+                    const uint32_t raw = sb + Geo::oRaw + rb * Geo::kRaw, rsc = sb + Geo::oRawSc + rb * Geo::kRawScales;
+                    uint32_t u[4];
+                    if (k0 + kTKeys > g.ctx - g.n) {
+                        tree_union(p, g, k0, u);
+                    } else {
+                        u[0] = u[1] = u[2] = u[3] = 0xffffffffu;
+                    }
+                    (void)nvalid;  // keys past the context are in no union
+                    ok = waited(rfull + 8 * rb, (uint32_t)((t / NR) & 1)) && ok;
+                    // lane: keys 4 lane .. + 3, all of one block
+                    const uint32_t at = ((uint32_t)(4 * lane) >> p.lgB) * 2 * B + ((4 * lane) & (B - 1));
+                    uint32_t kb;
+                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(kb) : "r"(rsc + at));
+                    int em = kScaleMin;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (u[lane >> 3] >> ((4 * lane + i) & 31) & 1u) em = max(em, scale_of((kb >> 8 * i) & 255));
+                    em = __reduce_max_sync(0xffffffffu, em);
+                    const uint32_t sl = slot(t);
+                    // K, then V; piece x: row x / L, 16 elements from 16 (x % L) on
+                    for (int which = 0; which < 2; ++which) {
+                        if (t >= NS) ok = waited((which ? vfree : kfree) + 8 * sl, ph(t - NS)) && ok;
+                        const uint32_t dst = (which ? sV : sK) + sl * kTile;
+                        for (int st = cw; st < kSteps; st += kConvWarps) {
+                            const int x = st * 32 + lane, r = x / L, c = x % L;
+                            const uint32_t blk = (uint32_t)r >> p.lgB, in = r & (B - 1);
+                            const uint32_t rr = (which ? B : 0) + in;  // row of the block's chunk, swizzled by TMA
+                            const uint32_t src = raw + blk * 2 * B * D + rr * D +
+                                                 (D == 128 ? ((c ^ (rr & 7)) << 4) : ((c ^ (rr >> 1 & 3)) << 4));
+                            uint4 v;
+                            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                                         : "r"(src));
+                            const bool seen = u[r >> 5] >> (r & 31) & 1u;
+                            uint32_t h[8] = {e4m3x2_to_f16x2(v.x), e4m3x2_to_f16x2(v.x >> 16), e4m3x2_to_f16x2(v.y),
+                                             e4m3x2_to_f16x2(v.y >> 16), e4m3x2_to_f16x2(v.z),
+                                             e4m3x2_to_f16x2(v.z >> 16), e4m3x2_to_f16x2(v.w),
+                                             e4m3x2_to_f16x2(v.w >> 16)};
+                            if (which == 0) {
+                                uint32_t b;
+                                asm volatile("ld.shared.u8 %0, [%1];" : "=r"(b) : "r"(rsc + blk * 2 * B + in));
+                                const __half2 f = __float2half2_rn(pow2i(scale_of((int)b) - em + 7));
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&h[i]), f);
+                                    h[i] = *reinterpret_cast<const uint32_t*>(&y);
+                                }
+                            }
+                            // rows nobody sees, past the context or padding, may hold anything: zeros
+                            if (!seen) {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) h[i] = 0u;
+                            }
+                            // 16-byte pieces 2 c and 2 c + 1 of the row (8 per column half); half the lanes store
+                            // them in the other order, which spreads a quarter warp's stores over all banks
+                            const uint32_t row = dst + (uint32_t)(r >> 3) * kGroup + (uint32_t)(c >> 2) * 1024 + (r & 7) * 128;
+                            const uint32_t flip = D == 128 ? (lane >> 2 & 1) : 0;
+#pragma unroll
+                            for (int o = 0; o < 2; ++o) {
+                                const uint32_t oo = o ^ flip;
+                                const uint32_t a = row + ((((c & 3) * 2 + oo) ^ (r & 7)) << 4);
+                                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a),
+                                             "r"(oo ? h[4] : h[0]), "r"(oo ? h[5] : h[1]), "r"(oo ? h[6] : h[2]),
+                                             "r"(oo ? h[7] : h[3])
+                                             : "memory");
+                            }
+                        }
+                        if (which) {
+                            float* ex = reinterpret_cast<float*>(smem_raw + Geo::oExp + sl * Geo::kExp);
+                            const int key = cw * 32 + lane;
+                            if (key < kTKeys) {
+                                uint32_t b;
+                                asm volatile("ld.shared.u8 %0, [%1];"
+                                             : "=r"(b)
+                                             : "r"(rsc + ((uint32_t)key >> p.lgB) * 2 * B + B + (key & (B - 1))));
+                                const int ev = scale_of((int)b);
+                                ex[key] = (float)ev;
+                                ex[kTKeys + key] = pow2i(-ev);
+                            }
+                            if (cw == 0 && lane == 0) kmul[sl] = pow2i(em - 7);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive((which ? vfull : kfull) + 8 * sl);
+                    }
+                    if (lane == 0) mbar_arrive(rfree + 8 * rb);
+                }
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ softmax warpgroup w: key tiles w, w + 2, ...
+        const int w = warp >> 2;
+        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t t_s = lanes + (uint32_t)w * kTKeys, t_o = lanes + 2 * kTKeys;
+        const int r = tid & (kTRows - 1);
+        int t = 0, c[2] = {0, 0};  // tiles so far, tiles of each warpgroup
+        for (int seg = 0; walk.next(p, g); ++seg) {
+            const int nt = g.j1 - g.j0;
+            const int tok0 = g.mt * p.TQ, rows = min(p.TQ, g.n - tok0) * p.G;
+            const int tok = tok0 + r / p.G;
+            const bool row_ok = r < rows, warp_ok = (warp & 3) * 32 < rows;
+            const int base = g.ctx - g.n;  // keys before the draft
+            const size_t orow = ((size_t)(g.qs + tok) * p.H_q + (size_t)g.h * p.G + r % p.G) * D;
+            float cr = p.scale_log2;
+            // The row of Q: warpgroup w stores its half (of 64 columns, or of the one region of D = 64).
+            {
+                constexpr int C = D / 8;  // 16-byte pieces of a row
+                const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + orow);
+                uint4 x[QUANT ? C : C / 2];
+                constexpr int N_ = QUANT ? C : C / 2;
+                const int c0 = QUANT ? 0 : w * (C / 2);
+#pragma unroll
+                for (int i = 0; i < N_; ++i) x[i] = row_ok ? src[c0 + i] : make_uint4(0, 0, 0, 0);
+                if constexpr (QUANT) {
+                    if (p.q_bf16) {
+                        float a = 0.f;
+#pragma unroll
+                        for (int i = 0; i < N_; ++i) {
+                            const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const float2 f = Mma<__nv_bfloat16>::unpack(v[k]);
+                                a = fmaxf(a, fmaxf(fabsf(f.x), fabsf(f.y)));
+                            }
+                        }
+                        // largest magnitude to [2^14, 2^15), as in decode_quant.cu
+                        const int ex = (int)(__float_as_uint(a) >> 23) - 127;
+                        const int e = ex > 127 || a == 0.f ? 0 : max(ex - 14, -126);
+                        const float inv = pow2i(-e);
+                        cr *= pow2i(e);
+#pragma unroll
+                        for (int i = 0; i < N_; ++i) {
+                            uint32_t* v = reinterpret_cast<uint32_t*>(&x[i]);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const float2 f = Mma<__nv_bfloat16>::unpack(v[k]);
+                                v[k] = Mma<__half>::pack(f.x * inv, f.y * inv);
+                            }
+                        }
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < C / 2; ++i) {
+                    const int ch = w * (C / 2) + i;  // piece of the row
+                    const uint4 v = QUANT ? (w ? x[(C / 2 + i) % N_] : x[i]) : x[i];
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                     sQ + (uint32_t)(ch >> 3) * kTRegion + r * 128 + (((ch & 7) ^ (r & 7)) << 4)),
+                                 "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                                 : "memory");
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(qfull);
+            }
+            float m_ref = NEG_INF, l = 0.f;
+            for (int i = w; i < nt; i += 2) {
+                const int k0 = (g.j0 + i) * kTKeys;
+                ok = waited(sfull + 8 * w, (uint32_t)(c[w] & 1)) && ok;
+                tc_fence_after();
+                if (QUANT) ok = waited(vfull + 8 * slot(t + i), ph(t + i)) && ok;  // the tile's exponents
+                const bool masked = k0 + kTKeys > base;
+                if (warp_ok) {
+                    float v[kTKeys];
+                    {
+                        uint32_t* u = reinterpret_cast<uint32_t*>(v);
+#pragma unroll
+                        for (int k = 0; k < kTKeys / 32; ++k)
+                            asm volatile(
+                                "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+                                "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+                                "%28, %29, %30, %31}, [%32];"
+                                : "=r"(u[32 * k + 0]), "=r"(u[32 * k + 1]), "=r"(u[32 * k + 2]), "=r"(u[32 * k + 3]),
+                                  "=r"(u[32 * k + 4]), "=r"(u[32 * k + 5]), "=r"(u[32 * k + 6]), "=r"(u[32 * k + 7]),
+                                  "=r"(u[32 * k + 8]), "=r"(u[32 * k + 9]), "=r"(u[32 * k + 10]), "=r"(u[32 * k + 11]),
+                                  "=r"(u[32 * k + 12]), "=r"(u[32 * k + 13]), "=r"(u[32 * k + 14]), "=r"(u[32 * k + 15]),
+                                  "=r"(u[32 * k + 16]), "=r"(u[32 * k + 17]), "=r"(u[32 * k + 18]), "=r"(u[32 * k + 19]),
+                                  "=r"(u[32 * k + 20]), "=r"(u[32 * k + 21]), "=r"(u[32 * k + 22]), "=r"(u[32 * k + 23]),
+                                  "=r"(u[32 * k + 24]), "=r"(u[32 * k + 25]), "=r"(u[32 * k + 26]), "=r"(u[32 * k + 27]),
+                                  "=r"(u[32 * k + 28]), "=r"(u[32 * k + 29]), "=r"(u[32 * k + 30]), "=r"(u[32 * k + 31])
+                                : "r"(t_s + k * 32)
+                                : "memory");
+                        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+                    }
+                    const uint32_t ex = sb + Geo::oExp + slot(t + i) * Geo::kExp;
+                    const float mul = QUANT ? cr * kmul[slot(t + i)] : cr;
+                    const float2 mul2 = make_float2(mul, mul);
+#pragma unroll
+                    for (int k = 0; k < kTKeys; k += 4) {
+                        float4 ev = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (QUANT)
+                            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                         : "=f"(ev.x), "=f"(ev.y), "=f"(ev.z), "=f"(ev.w)
+                                         : "r"(ex + 4 * k));
+                        const float2 a = ffma2(make_float2(v[k], v[k + 1]), mul2, make_float2(ev.x, ev.y));
+                        const float2 b = ffma2(make_float2(v[k + 2], v[k + 3]), mul2, make_float2(ev.z, ev.w));
+                        v[k] = a.x;
+                        v[k + 1] = a.y;
+                        v[k + 2] = b.x;
+                        v[k + 3] = b.y;
+                    }
+                    if (masked) {
+#pragma unroll
+                        for (int k = 0; k < kTKeys / 32; ++k) {
+                            const uint32_t vis = row_ok ? tree_visible(p, g, tok, k0 + 32 * k - base) : 0u;
+#pragma unroll
+                            for (int b = 0; b < 32; ++b) v[32 * k + b] = vis >> b & 1u ? v[32 * k + b] : NEG_INF;
+                        }
+                    }
+                    float mx[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
+#pragma unroll
+                    for (int k = 0; k < kTKeys; k += 8) {
+                        mx[0] = fmax3(mx[0], v[k], v[k + 1]);
+                        mx[1] = fmax3(mx[1], v[k + 2], v[k + 3]);
+                        mx[2] = fmax3(mx[2], v[k + 4], v[k + 5]);
+                        mx[3] = fmax3(mx[3], v[k + 6], v[k + 7]);
+                    }
+                    const float m_tile = fmax3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
+                    const float m_new = m_tile > m_ref + 8.f || m_ref == NEG_INF ? fmaxf(m_ref, m_tile) : m_ref;
+                    const float alpha = i == w || m_new == m_ref ? 1.f : fast_exp2(m_ref - m_new);
+                    m_ref = m_new;
+                    const float m_use = m_new == NEG_INF ? 0.f : m_new;
+                    const float2 nm2 = make_float2(-m_use, -m_use);
+                    // P over S: 64 columns of pairs, and (SPLIT) the low parts in the next 64
+                    float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                    for (int k = 0; k < kTKeys / 32; ++k) {
+                        uint32_t hi[16], lo[16];
+#pragma unroll
+                        for (int b = 0; b < 32; b += 2) {
+                            float2 x = fadd2(make_float2(v[32 * k + b], v[32 * k + b + 1]), nm2);
+                            x.x = fast_exp2(x.x);
+                            x.y = fast_exp2(x.y);
+                            if constexpr (QUANT) {
+                                float2 iv;
+                                asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
+                                             : "=f"(iv.x), "=f"(iv.y)
+                                             : "r"(ex + 4 * (kTKeys + 32 * k + b)));
+                                ls[(b >> 1) & 1] = ffma2(x, iv, ls[(b >> 1) & 1]);
+                            } else {
+                                ls[(b >> 1) & 1] = fadd2(ls[(b >> 1) & 1], x);
+                            }
+                            hi[b / 2] = Mma<PT>::pack(x.x, x.y);
+                            if (SPLIT) {
+                                const float2 f = fsub2(x, Mma<PT>::unpack(hi[b / 2]));
+                                lo[b / 2] = Mma<PT>::pack(f.x, f.y);
+                            }
+                        }
+                        tmem_st16(t_s + k * 16, hi);
+                        if (SPLIT) tmem_st16(t_s + kTKeys / 2 + k * 16, lo);
+                    }
+                    const float2 lsum = fadd2(ls[0], ls[1]);
+                    l = fmaf(l, alpha, lsum.x + lsum.y);
+                    // O_w is rescaled (rarely) after the products of the warpgroup's last tile, which have landed: S
+                    // of this tile was issued after them
+                    if (__any_sync(0xffffffffu, alpha != 1.f)) {
+                        ok = waited(pvd + 8 * w, (uint32_t)((c[w] - 1) & 1)) && ok;
+                        tc_fence_after();
+#pragma unroll
+                        for (int k = 0; k < D / 32; ++k) {
+                            float o[32];
+                            tmem_ld32(t_o + (uint32_t)w * D + k * 32, o);
+#pragma unroll
+                            for (int b = 0; b < 32; ++b) o[b] *= alpha;
+                            tmem_st32(t_o + (uint32_t)w * D + k * 32, o);
+                        }
+                    }
+                    tmem_wait_st();
+                }
+                if (!QUANT && masked) {
+                    // V rows nobody sees (past the context, padding) may hold anything, even NaN: zeros before the
+                    // products meet them with P = 0
+                    uint32_t u[4];
+                    tree_union(p, g, k0, u);
+                    ok = waited(vfull + 8 * slot(t + i), ph(t + i)) && ok;
+                    const int rr = (warp & 3) * 32 + lane;
+                    if (!(u[warp & 3] >> lane & 1u)) {
+                        const uint32_t vr = sV + slot(t + i) * kTile + (uint32_t)(rr >> 3) * kGroup + (rr & 7) * 128;
+#pragma unroll
+                        for (int k = 0; k < D / 8; ++k)
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(vr + (k >> 3) * 1024 +
+                                                                                          (k & 7) * 16),
+                                         "r"(0)
+                                         : "memory");
+                    }
+                    fence_proxy_async_smem();
+                }
+                tc_fence_before();
+                mbar_arrive(prdy + 8 * w);
+                ++c[w];
+            }
+            if (nt > (w ^ 1)) c[w ^ 1] += (nt - (w ^ 1) + 1) / 2;
+            t += nt;
+            // the warpgroups' results: every product of the segment has landed, and Q's space is free
+            ok = waited(qfree, (uint32_t)(seg & 1)) && ok;
+            for (int x = 0; x < 2; ++x)
+                if (nt > x) ok = waited(pvd + 8 * x, (uint32_t)((c[x] - 1) & 1)) && ok;
+            tc_fence_after();
+            float2* xch = reinterpret_cast<float2*>(smem_raw);
+            xch[w * kTRows + r] = make_float2(m_ref, l);
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            const float2 o0 = xch[r], o1 = xch[kTRows + r];
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            const float M = fmaxf(o0.x, o1.x);
+            const float f0 = o0.x == NEG_INF ? 0.f : fast_exp2(o0.x - M), f1 = o1.x == NEG_INF ? 0.f : fast_exp2(o1.x - M);
+            const float den = o0.y * f0 + o1.y * f1;  // (a NaN exponential sum stays one)
+            const bool whole = g.j0 == 0 && g.j1 == g.nt;
+            const int part = 2 * blockIdx.x + (g.j0 == 0 ? 1 : 0);
+            const float inv = den == 0.f ? 0.f : 1.f / den;  // a row that sees nothing is zero
+#pragma unroll
+            for (int k = 0; k < D / 64; ++k) {
+                const int col = w * (D / 2) + 32 * k;
+                float a[32];
+                if (warp_ok) {
+                    tmem_ld32(t_o + col, a);
+                    if (nt > 1) {
+                        float b[32];
+                        tmem_ld32(t_o + D + col, b);
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) a[x] = f0 == 0.f ? b[x] * f1 : f1 == 0.f ? a[x] * f0 : a[x] * f0 + b[x] * f1;
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) a[x] *= f0;
+                    }
+                }
+                if (row_ok && ok) {
+                    if (!whole) {
+                        float4* dst = reinterpret_cast<float4*>(p.part_acc + ((size_t)part * kTRows + r) * D + col);
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) dst[x] = make_float4(a[4 * x], a[4 * x + 1], a[4 * x + 2], a[4 * x + 3]);
+                    } else if (p.out_dtype == PA_F32) {
+                        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + orow + col);
+#pragma unroll
+                        for (int x = 0; x < 8; ++x)
+                            dst[x] = den == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                                : make_float4(a[4 * x] * inv, a[4 * x + 1] * inv, a[4 * x + 2] * inv,
+                                                              a[4 * x + 3] * inv);
+                    } else {
+                        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + orow + col);
+                        uint32_t h[16];
+#pragma unroll
+                        for (int x = 0; x < 16; ++x) {
+                            const float lo = den == 0.f ? 0.f : a[2 * x] * inv, up = den == 0.f ? 0.f : a[2 * x + 1] * inv;
+                            h[x] = p.out_dtype == PA_BF16 ? Mma<__nv_bfloat16>::pack(lo, up) : Mma<__half>::pack(lo, up);
+                        }
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) dst[x] = make_uint4(h[4 * x], h[4 * x + 1], h[4 * x + 2], h[4 * x + 3]);
+                    }
+                }
+            }
+            if (!whole && row_ok && ok && w == 0)
+                reinterpret_cast<float2*>(p.part_ml)[(size_t)part * kTRows + r] = make_float2(M, den);
+            if (tid == 0 && g.j0 == 0 && !whole)
+                p.desc[blockIdx.x] = make_int4(g.s, g.h, g.mt, (int)(1 + (g.nt - g.j1 + run.per - 1) / run.per));
+            tc_fence_before();
+            mbar_arrive(ofree);
+        }
+    }
+    // Nothing issued may still be running when TMEM and shared memory are released: the tensor-core products (the MMA
+    // thread's last commit) and the copies (the last arm of every stage; earlier ones were consumed before it).
+    if (warp == 9 && lane == 0) mbar_wait_bounded(mmadone, 0, nullptr);
+    if (warp == 8 && lane == 0) {
+        if constexpr (QUANT) {
+            const int n = armed[0];
+            for (int b = 0; b < NR && b < n; ++b)
+                mbar_wait_bounded(rfull + 8 * b, (uint32_t)(((n - 1 - b) / NR) & 1), nullptr);
+        } else {
+            for (int which = 0; which < 2; ++which) {
+                const int n = armed[which];
+                for (int b = 0; b < NS && b < n; ++b)
+                    mbar_wait_bounded((which ? vfull : kfull) + 8 * b, (uint32_t)(((n - 1 - b) / NS) & 1), nullptr);
+            }
+        }
+    }
+    tc_fence_before();
+    ok = __syncthreads_and(ok && !*abort_flag);
+    if (!ok && tid == 0) flag_error(p.err, PA_DEV_ERR_TIMEOUT);
+    if (warp == 0) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTTmem) : "memory");
+    }
+}
+
+// ----------------------------------------------------------------------------- joining the partial results
+
+// Block (c, y): the unit CTA c started and left unfinished, rows 8 y .. + 7, one warp each.  Piece 0 is CTA c's last
+// segment, piece i CTA c + i's first.
+template <int D>
+__global__ void __launch_bounds__(256) tree_merge_kernel(const TreeParams p) {
+    constexpr int V = D / 32, kChunk = 8;
+    griddep_wait();
+    griddep_launch_dependents();
+    const int4 d = p.desc[blockIdx.x];
+    if (d.w < 2) return;
+    const TreeSeq q = tree_seq(p, d.x, false);
+    const int tok0 = d.z * p.TQ, rows = min(p.TQ, q.n - tok0) * p.G;
+    const int r = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (r >= rows) return;
+    auto at = [&](int i) { return ((size_t)(i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i)) * kTRows + r); };
+    float M = -INFINITY, den = 0.f, o[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) o[v] = 0.f;
+    for (int b = 0; b < d.w; b += kChunk) {
+        const int n = min(kChunk, d.w - b);
+        const float2 ml = lane < n ? reinterpret_cast<const float2*>(p.part_ml)[at(b + lane)] : make_float2(-INFINITY, 0.f);
+        float a[kChunk][V];
+#pragma unroll
+        for (int j = 0; j < kChunk; ++j)
+#pragma unroll
+            for (int v = 0; v < V; ++v) a[j][v] = j < n ? p.part_acc[at(b + j) * D + lane * V + v] : 0.f;
+        float mc = ml.x;
+#pragma unroll
+        for (int k = 16; k > 0; k >>= 1) mc = fmaxf(mc, __shfl_xor_sync(0xffffffffu, mc, k));
+        const float Mn = fmaxf(M, mc);
+        const float f = M == -INFINITY ? 0.f : fast_exp2(M - Mn);
+        const float wl = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - Mn);
+        M = Mn;
+        den = den * f + wl * ml.y;
+#pragma unroll
+        for (int v = 0; v < V; ++v) o[v] *= f;
+#pragma unroll
+        for (int j = 0; j < kChunk; ++j) {
+            const float wj = __shfl_sync(0xffffffffu, wl, j);
+            if (wj != 0.f) {  // a piece in which the row sees nothing counts for nothing
+#pragma unroll
+                for (int v = 0; v < V; ++v) o[v] = fmaf(wj, a[j][v], o[v]);
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) den += __shfl_xor_sync(0xffffffffu, den, k);
+    const float inv = den == 0.f ? 0.f : 1.f / den;
+    const size_t row = ((size_t)(q.qs + tok0 + r / p.G) * p.H_q + (size_t)d.y * p.G + r % p.G) * D + lane * V;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const float x = den == 0.f ? 0.f : o[v] * inv;
+        if (p.out_dtype == PA_F32)
+            static_cast<float*>(p.out)[row + v] = x;
+        else if (p.out_dtype == PA_BF16)
+            static_cast<__nv_bfloat16*>(p.out)[row + v] = from_float<__nv_bfloat16>(x);
+        else
+            static_cast<__half*>(p.out)[row + v] = from_float<__half>(x);
+    }
+}
+
+// ----------------------------------------------------------------------------- host side
+
+struct TreeWorkspace {
+    size_t ml, acc, total;
+};
+
+static TreeWorkspace tree_workspace(int D) {
+    TreeWorkspace w;
+    w.ml = (sizeof(int4) * kTreeMaxCtas + 255) & ~size_t(255);
+    w.acc = w.ml + sizeof(float) * 2 * 2 * kTreeMaxCtas * kTRows;
+    w.total = w.acc + sizeof(float) * 2 * kTreeMaxCtas * kTRows * D;
+    return w;
+}
+
 size_t tree_workspace_bytes(int N, int H_q, int H_kv, int D, int max_q_len) {
     if (N <= 0 || H_q <= 0 || H_kv <= 0 || H_q % H_kv || (D != 64 && D != 128) || max_q_len <= 0) return 0;
-    return 256;
+    return tree_workspace(D).total;
+}
+
+template <typename T, int D, bool QUANT, bool SPLIT>
+static pa_status run_tree(const TreeParams& p, const CUtensorMap& tm, int ctas, cudaStream_t stream) {
+    using Geo = TreeGeo<D, QUANT>;
+    auto kern = tree_kernel<T, D, QUANT, SPLIT>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Geo::kSmem);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(tree)");
+    e = launch_kernel(kern, dim3(ctas), dim3(Geo::kThreads), Geo::kSmem, stream, tm, p);
+    count_launch();
+    if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
+    e = launch_kernel(tree_merge_kernel<D>, dim3(ctas, (std::min(p.TQ, p.max_q_len) * p.G + 7) / 8), dim3(256), 0, stream, p);
+    count_launch();
+    return e == cudaSuccess ? PA_OK : cuda_fail(e, "tree merge launch");
+}
+
+template <int D>
+static pa_status dispatch_tree(const TreeArgs& a, const TreeParams& p, const CUtensorMap& tm, int ctas) {
+    const bool f32 = a.out_dtype == PA_F32;
+    if (a.scales)
+        return f32 ? run_tree<__half, D, true, true>(p, tm, ctas, a.stream)
+                   : run_tree<__half, D, true, false>(p, tm, ctas, a.stream);
+    if (a.q_dtype == PA_BF16) return run_tree<__nv_bfloat16, D, false, true>(p, tm, ctas, a.stream);
+    return f32 ? run_tree<__half, D, false, true>(p, tm, ctas, a.stream)
+               : run_tree<__half, D, false, false>(p, tm, ctas, a.stream);
 }
 
 pa_status launch_tree(const TreeArgs& a) {
-    RowsParams p = {};
-    p.out = a.out;
-    p.out_dtype = a.out_dtype;
+    const TreeWorkspace w = tree_workspace(a.D);
+    uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+    TreeParams p;
     p.q = a.q;
-    p.pool = a.pool;
-    p.scales = static_cast<const uint8_t*>(a.scales);
+    p.q_bf16 = a.q_dtype == PA_BF16;
     p.tables = a.tables;
     p.ctx_lens = a.ctx_lens;
     p.q_start = a.q_start;
     p.mask = a.mask;
-    p.mask_words = a.mask_words;
+    p.scales = static_cast<const uint8_t*>(a.scales);
+    p.W = a.mask_words;
     p.N = a.N;
     p.T = a.T;
     p.H_q = a.H_q;
     p.H_kv = a.H_kv;
     p.G = a.H_q / a.H_kv;
+    p.TQ = kTRows / p.G;
     p.lgB = a.B == 8 ? 3 : a.B == 16 ? 4 : 5;
     p.MB = a.MB;
     p.NB = a.NB;
-    p.max_ctx = 0x7fffffff;
     p.max_q_len = a.max_q_len;
-    p.scale_log2 = (float)((double)a.scale * 1.4426950408889634);
+    p.out = a.out;
+    p.out_dtype = a.out_dtype;
+    p.scale_log2 = (float)((double)a.scale * 1.4426950408889634);  // log2(e)
+    p.desc = reinterpret_cast<int4*>(ws);
+    p.part_ml = reinterpret_cast<float*>(ws + w.ml);
+    p.part_acc = reinterpret_cast<float*>(ws + w.acc);
+    p.wait_ns = wait_limit_ns();
     p.err = a.dev_err;
-    return launch_attend_rows(p, a.T, a.q_dtype, a.D, a.stream);
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return cuda_fail(e, "device query");
+    const int ctas = std::max(1, std::min(sms, kTreeMaxCtas));
+    CUtensorMap tm;
+    pa_status st;
+    if (a.scales) {
+        st = quant_tensor_map(&tm, a.pool, a.NB, a.H_kv, a.B, a.D);
+    } else {
+        // the pool [NB][B][2][H_kv][D]: dims 64 columns, token within a group of 8, column half, group of 8 tokens
+        // (over all blocks), K/V x KV head; box = the K or V rows of one block and head
+        const cuuint64_t dims[5] = {64, 8, (cuuint64_t)a.D / 64, (cuuint64_t)a.NB * a.B / 8, (cuuint64_t)2 * a.H_kv};
+        const cuuint64_t str[4] = {(cuuint64_t)2 * a.H_kv * a.D * 2, 128, (cuuint64_t)8 * 2 * a.H_kv * a.D * 2,
+                                   (cuuint64_t)a.D * 2};
+        const cuuint32_t box[5] = {64, 8, (cuuint32_t)a.D / 64, (cuuint32_t)(a.B / 8), 1};
+        st = encode_tensor_map(&tm, a.q_dtype == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                               5, a.pool, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    }
+    if (st != PA_OK) return st;
+    return a.D == 128 ? dispatch_tree<128>(a, p, tm, ctas) : dispatch_tree<64>(a, p, tm, ctas);
 }
 
 }  // namespace pa
