@@ -115,6 +115,16 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
     }
 }
 
+// The same wait for hand-offs that usually take well under a microsecond: the clock, whose read takes longer than
+// that, is consulted only after some tries (at once when the limit is below a microsecond).
+__device__ __forceinline__ bool mbar_wait_spin(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
+    if (limit_ns >= 1000) {
+        for (int i = 0; i < 64; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
+    }
+    return mbar_wait_bounded(bar, parity, abort, limit_ns);
+}
+
 // ----------------------------------------------------------------------------- TMA
 
 // 5-D tiled tensor load into shared memory, completion counted on `bar`.

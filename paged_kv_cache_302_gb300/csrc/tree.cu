@@ -5,18 +5,19 @@
 // M), so each K/V byte serves every row of a tile, and a (sequence, KV head, row tile) is a unit of ceil(ctx / 128) key
 // tiles.
 //
-// tree_kernel: one persistent CTA per SM.  All key tiles of the call, in unit order, are cut into equal runs, one per
-// CTA, so the GPU is evenly loaded whatever the lengths; a CTA walks its run as segments (consecutive tiles of one
+// tree_kernel: one persistent CTA per SM.  All key tiles of the call, in unit order, are cut into runs of equal cost, one
+// per CTA, so the GPU is evenly loaded whatever the lengths; a CTA walks its run as segments (consecutive tiles of one
 // unit), and a unit that several CTAs share leaves partial results (m, l, unnormalised O) that tree_merge_kernel joins.
 // A CTA leaves at most two (its first and its last segment), so the workspace has a fixed size.  Roles:
-//   * warps 0-3 and 4-7, two softmax warpgroups: warpgroup w takes the segment's key tiles w, w + 2, ...; each thread
-//     owns one TMEM lane = one query row.  It reads its S row (tcgen05.ld), masks, keeps a running maximum (O is
-//     rescaled only when it grows by more than 2^8) and writes the probabilities over S.  The two warpgroups have
-//     accumulators of their own, O_0 and O_1, joined at the segment's end: while one works on its exponentials the
-//     tensor core serves the other.  They also load (quantised: and scale) the query rows.
-//   * warp 8 (TMA): K and V tiles into rings, block by block through the block table;
-//   * warp 9 (MMA, one thread): S_w = Q K^T (TMEM columns 128 w), O_w += P V (columns 256 + D w), P read from TMEM;
-//   * quantised pool, warps 10-15: e4m3 tiles from the raw ring to fp16 tiles in the K and V rings.
+//   * warps 0-3 and 4-7, two softmax warpgroups: warpgroup w takes keys 64 w .. 64 w + 63 of every tile; each thread owns
+//     one TMEM lane = one query row.  It reads its 64 scores (tcgen05.ld), masks, keeps a running maximum of its own
+//     (its O is rescaled only when that grows by more than 2^8) and writes the probabilities over the scores.  The
+//     warpgroups have accumulators of their own, O_0 and O_1, joined at the segment's end, so they never wait for one
+//     another in between;
+//   * warp 8 (TMA): query rows (16-bit pool), K and V tiles into rings, block by block through the block table;
+//   * warp 9 (MMA, one thread): S = Q K^T of the next tile (TMEM columns 128 (t & 1)) while the softmax works on this
+//     one, then O_w += P_w V (columns 256 + D w), P read from TMEM;
+//   * quantised pool, warps 10-15: e4m3 tiles from the raw ring to fp16 tiles in the K and V rings, and the query rows.
 // The value product takes P in V's 16-bit type: for bf16, or an fp32 output, as a high and a low part (two products).
 //
 // Quantised pool: query rows are scaled to fp16's range by a power of two (exact); K8 is converted to fp16 times 2^(ek -
@@ -37,7 +38,8 @@ constexpr int kTKeys = 128;    // keys per tile (N of S, K of P V)
 constexpr uint32_t kTRegion = kTRows * 128;  // [128 rows][64 columns] 16-bit, 128-byte swizzled
 constexpr uint32_t kTTmem = 512;
 constexpr int kTreeMaxCtas = 160;  // CTAs of a call at most (the workspace holds two partial results for each)
-constexpr int kTreeMinTiles = 2;   // key tiles per CTA at least: one per warpgroup
+// Cost of a unit's start and end (query rows, first scores, joining the warpgroups, storing) in key tiles.
+constexpr int kTreeUnitCost = 3;
 constexpr int kConvWarps = 6;
 
 struct TreeParams {
@@ -87,7 +89,7 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int s, bool fla
 }
 
 __device__ __forceinline__ int64_t tree_cost(const TreeParams& p, const TreeSeq& q) {
-    return (int64_t)q.nt * q.nmt * p.H_kv;
+    return q.nt > 0 ? (int64_t)(q.nt + kTreeUnitCost) * q.nmt * p.H_kv : 0;
 }
 
 // Consecutive key tiles j0 .. j1 - 1 of one unit.
@@ -95,46 +97,46 @@ struct TreeSeg {
     int s, h, mt, j0, j1, nt, ctx, n, qs;
 };
 
-// Walks a CTA's run of tiles segment by segment.
+// Walks a CTA's run segment by segment.  Positions count cost: a unit is kTreeUnitCost, then one per tile.
 struct TreeWalk {
-    int s, u, j;
+    int s, u, o;  // sequence, unit in it, position in the unit
     int64_t left;
     TreeSeq q;
     __device__ __forceinline__ void start(const TreeParams& p, int s0, int64_t rem, int64_t count) {
         s = s0;
         left = count;
         q = tree_seq(p, s, false);
-        u = (int)(rem / q.nt);
-        j = (int)(rem - (int64_t)u * q.nt);
+        u = (int)(rem / (q.nt + kTreeUnitCost));
+        o = (int)(rem - (int64_t)u * (q.nt + kTreeUnitCost));
     }
     __device__ __forceinline__ bool next(const TreeParams& p, TreeSeg& g) {
-        if (left <= 0) return false;
-        g.s = s;
-        g.h = u / q.nmt;
-        g.mt = u - g.h * q.nmt;
-        g.j0 = j;
-        g.j1 = (int)min((int64_t)q.nt, j + left);
-        g.nt = q.nt;
-        g.ctx = q.ctx;
-        g.n = q.n;
-        g.qs = q.qs;
-        left -= g.j1 - g.j0;
-        j = 0;
-        if (++u == q.nmt * p.H_kv && left > 0) {
-            u = 0;
-            do {
-                q = tree_seq(p, ++s, false);
-            } while (q.nt == 0);
+        while (left > 0) {
+            const int size = q.nt + kTreeUnitCost;
+            const int o1 = (int)min((int64_t)size, o + left);
+            g.s = s;
+            g.h = u / q.nmt;
+            g.mt = u - g.h * q.nmt;
+            g.j0 = max(0, o - kTreeUnitCost);
+            g.j1 = max(0, o1 - kTreeUnitCost);
+            g.nt = q.nt;
+            g.ctx = q.ctx;
+            g.n = q.n;
+            g.qs = q.qs;
+            left -= o1 - o;
+            o = 0;
+            if (++u == q.nmt * p.H_kv && left > 0) {
+                u = 0;
+                do {
+                    q = tree_seq(p, ++s, false);
+                } while (q.nt == 0);
+            }
+            if (g.j1 > g.j0) return true;
         }
-        return true;
+        return false;
     }
 };
 
-__device__ __forceinline__ int64_t shfl64(int64_t v, int src) {
-    return (int64_t)__shfl_sync(0xffffffffu, (unsigned long long)v, src);
-}
-
-// The CTA's run [lo, hi) of the call's tiles, and the sequence it starts in with the tiles of it that lie before.
+// The CTA's run [lo, hi) of the call's cost, and the sequence it starts in with the part of it that lies before.
 // Every thread of the block calls it; `buf`: 40 words of 8 bytes.
 struct TreeRun {
     int64_t per, lo, hi, rem;
@@ -159,7 +161,7 @@ __device__ __forceinline__ TreeRun tree_run(const TreeParams& p, int cta, int ct
     int64_t total = 0;
     for (int w = 0; w < NW; ++w) total += buf[w];
     r.per = (total + ctas - 1) / ctas;
-    if (r.per < kTreeMinTiles) r.per = kTreeMinTiles;
+    if (r.per < kTreeUnitCost + 1) r.per = kTreeUnitCost + 1;  // a tile at least
     r.lo = r.per * cta;
     r.hi = min(r.lo + r.per, total);
     r.s = 0;
@@ -213,15 +215,16 @@ __device__ __forceinline__ uint32_t tree_visible(const TreeParams& p, const Tree
     return __funnelshift_r(tree_word(row, g.n, x), tree_word(row, g.n, x + 1), j0 & 31);
 }
 
-// Keys of a tile that some row of the row tile sees: the same four words in every lane.
-__device__ __forceinline__ void tree_union(const TreeParams& p, const TreeSeg& g, int k0, uint32_t (&u)[4]) {
+// Keys k0 .. k0 + 32 NW - 1 that some row of the row tile sees: the same words in every lane.
+template <int NW>
+__device__ __forceinline__ void tree_union(const TreeParams& p, const TreeSeg& g, int k0, uint32_t (&u)[NW]) {
     const int lane = threadIdx.x & 31, tok0 = g.mt * p.TQ, ntok = min(p.TQ, g.n - tok0);
+    uint32_t v[NW] = {};
+    for (int t = lane; t < ntok; t += 32)
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        uint32_t v = 0;
-        for (int t = lane; t < ntok; t += 32) v |= tree_visible(p, g, tok0 + t, k0 + 32 * c - (g.ctx - g.n));
-        u[c] = __reduce_or_sync(0xffffffffu, v);
-    }
+        for (int c = 0; c < NW; ++c) v[c] |= tree_visible(p, g, tok0 + t, k0 + 32 * c - (g.ctx - g.n));
+#pragma unroll
+    for (int c = 0; c < NW; ++c) u[c] = __reduce_or_sync(0xffffffffu, v[c]);
 }
 
 // ----------------------------------------------------------------------------- the kernel
@@ -234,24 +237,29 @@ struct TreeGeo {
     static constexpr int NS = QUANT ? 2 : 3;              // K and V ring slots
     static constexpr int NR = QUANT ? (D == 128 ? 2 : 4) : 0;      // raw ring slots: K and V rows of a tile, scales
     static constexpr uint32_t kRaw = 2u * kTKeys * D, kRawScales = 2 * kTKeys;
-    static constexpr uint32_t kExp = QUANT ? 2 * kTKeys * 4 : 0;   // per V slot: ev and 2^-ev of the keys
-    static constexpr int kThreads = QUANT ? 512 : 320;
-    // Q | K ring | V ring | raw ring | raw scales | exponents | barriers and small things
+    static constexpr uint32_t kExp = QUANT ? kTKeys * 4 : 0;       // per V slot: each key's ev and 2^-ev, as bf16
+    // Registers move from the copying and converting warpgroups to the two softmax warpgroups: the launch's share is
+    // 128 (512 threads) or 168 (384) each, and 256 * kMore + (kThreads - 256) * kLess is exactly that total.
+    static constexpr int kThreads = QUANT ? 512 : 384;
+    static constexpr int kMore = QUANT ? 160 : 200, kLess = QUANT ? 96 : 104;
+    static_assert(256 * kMore + (kThreads - 256) * kLess == kThreads * (QUANT ? 128 : 168), "register split");
+    // Q | K ring | V ring | raw ring | raw scales | exponents | row exchange | query exponents | barriers, small things
     static constexpr uint32_t oK = kTile, oV = oK + NS * kTile, oRaw = oV + NS * kTile, oRawSc = oRaw + NR * kRaw,
-                              oExp = oRawSc + NR * kRawScales, oBar = oExp + NS * kExp;
-    static constexpr int kBars = 4 + 4 * NS + 6 + 2 * NR;
+                              oExp = oRawSc + NR * kRawScales, oXch = oExp + NS * kExp, oQe = oXch + 2 * kTRows * 4,
+                              oBar = oQe + (QUANT ? kTRows : 0);
+    static constexpr int kBars = 4 + 4 * NS + 8 + 2 * NR;
     static constexpr uint32_t oSmall = oBar + 8 * kBars;
-    static constexpr size_t kSmem = oSmall + 64;
+    static constexpr size_t kSmem = oSmall + 32;
     static_assert(kSmem <= 232448, "shared memory");
-    static_assert(8 * 40 <= kTile && 2 * kTRows * 8 <= kTile, "the Q tile's space also serves the start and the joins");
+    static_assert(8 * 40 <= kTile, "the Q tile's space also serves the start");
 };
 
 template <typename T, int D, bool QUANT, bool SPLIT>
 __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
-    tree_kernel(const __grid_constant__ CUtensorMap tm, const TreeParams p) {
+    tree_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUtensorMap tm_q, const TreeParams p) {
     using Geo = TreeGeo<D, QUANT>;
     constexpr int NS = Geo::NS, NR = Geo::NR;
-    constexpr int NK = D / 16, NT = kTKeys / 16;
+    constexpr int NK = D / 16, NT = kTKeys / 32;  // k-steps of S, and of each warpgroup's value product
     constexpr bool kBf16 = !QUANT && std::is_same<T, __nv_bfloat16>::value;  // type of the products
     using PT = typename std::conditional<kBf16, __nv_bfloat16, __half>::type;
     static_assert(!kBf16 || SPLIT, "a bf16 value product takes P in two parts");
@@ -262,13 +270,16 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t sb = smem_addr(smem_raw);
     const uint32_t sQ = sb, sK = sb + Geo::oK, sV = sb + Geo::oV, sBar = sb + Geo::oBar;
-    const uint32_t qfull = sBar, qfree = qfull + 8, ofree = qfree + 8, mmadone = ofree + 8, kfull = mmadone + 8,
-                   kfree = kfull + 8 * NS, vfull = kfree + 8 * NS, vfree = vfull + 8 * NS, sfull = vfree + 8 * NS,
-                   prdy = sfull + 16, pvd = prdy + 16, rfull = pvd + 16, rfree = rfull + 8 * NR;
+    // prdy: per S buffer and warpgroup; sfull, pvd: per S buffer
+    const uint32_t qfull = sBar, qfree = qfull + 8, qread = qfree + 8, mmadone = qread + 8,
+                   kfull = mmadone + 8, kfree = kfull + 8 * NS,
+                   vfull = kfree + 8 * NS, vfree = vfull + 8 * NS, sfull = vfree + 8 * NS, pvd = sfull + 16,
+                   prdy = pvd + 16, rfull = prdy + 32, rfree = rfull + 8 * NR;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_raw + Geo::oSmall);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    volatile int* armed = abort_flag + 1;  // tiles whose K / V (quantised: raw) copies have been issued
-    float* kmul = reinterpret_cast<float*>(tmem_slot + 4);  // per V slot: 2^(emax - 7) of the tile's K
+    volatile int* armed = abort_flag + 1;  // K, V (quantised: raw) tiles and query tiles whose copies have been issued
+    float* kmul = reinterpret_cast<float*>(tmem_slot + 5);  // per V slot: 2^(emax - 7) of the tile's K
+    int8_t* qexp = reinterpret_cast<int8_t*>(smem_raw + Geo::oQe);  // per query row: exponent it was scaled down by
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     griddep_wait();
@@ -291,11 +302,10 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
     }
     if (tid == 0) {
         for (int i = 0; i < Geo::kBars; ++i) mbar_init(sBar + 8 * i, 1);
-        mbar_init(qfull, 256);
-        mbar_init(ofree, 256);
-        mbar_init(prdy, 128);
-        mbar_init(prdy + 8, 128);
+        for (int i = 0; i < 4; ++i) mbar_init(prdy + 8 * i, 128);
         if (QUANT) {
+            mbar_init(qfull, kConvWarps);
+            mbar_init(qread, 8);
             for (int i = 0; i < NS; ++i) {
                 mbar_init(kfull + 8 * i, kConvWarps);
                 mbar_init(vfull + 8 * i, kConvWarps);
@@ -303,17 +313,17 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
             for (int i = 0; i < NR; ++i) mbar_init(rfree + 8 * i, kConvWarps);
         }
         *abort_flag = 0;
-        armed[0] = armed[1] = 0;
+        armed[0] = armed[1] = armed[2] = 0;
         fence_mbar_init();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    // A wait that runs out sets the abort flag, after which every other wait returns at once: no role leaves its loop
-    // early, so the barriers between threads are always met.
+    // A wait that runs out sets the abort flag, after which every other wait returns at once: the softmax warps never
+    // leave their loops early, so the barriers between them are always met.
     auto waited = [&](uint32_t bar, uint32_t parity) {
-        const bool w = mbar_wait_bounded(bar, parity, abort_flag, p.wait_ns);
+        const bool w = mbar_wait_spin(bar, parity, abort_flag, p.wait_ns);
         if (!w) *abort_flag = 1;
         return w;
     };
@@ -325,382 +335,414 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
     TreeSeg g;
     const int B = 1 << p.lgB;
 
-    if (warp == 8) {
-        // ------------------------------------------------------------ TMA producer: lane b copies the tile's block b
-        const uint64_t pol = policy_evict_first();
-        int t = 0;  // tiles so far
-        while (ok && walk.next(p, g)) {
-            auto entry = [&](int j) {
-                const int nblk = (min(kTKeys, g.ctx - j * kTKeys) + B - 1) >> p.lgB;
-                return lane < nblk ? p.tables[(size_t)g.s * p.MB + ((size_t)j * kTKeys >> p.lgB) + lane] : 0;
-            };
-            int mine = entry(g.j0);
-            for (int j = g.j0; j < g.j1 && ok; ++j, ++t) {
-                const int nblk = (min(kTKeys, g.ctx - j * kTKeys) + B - 1) >> p.lgB;
-                int e = mine;
-                if (j + 1 < g.j1) mine = entry(j + 1);
-                const bool good = (unsigned)e < (unsigned)p.NB;
-                if (lane < nblk && !good) flag_error(p.err, PA_DEV_ERR_BLOCK);
-                if (!good) e = p.NB;  // past the tensor: TMA fills zeros
-                if constexpr (QUANT) {
-                    const uint32_t b = (uint32_t)(t % NR), bar = rfull + 8 * b;
-                    if (t >= NR) ok = waited(rfree + 8 * b, (uint32_t)((t / NR - 1) & 1));
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Geo::kLess));
+        if (warp == 8) {
+            // -------------------------------------------------------- TMA producer: lane b copies the tile's block b
+            const uint64_t pol = policy_evict_first();
+            int t = 0;  // tiles so far
+            for (int seg = 0; ok && walk.next(p, g); ++seg) {
+                auto entry = [&](int j) {
+                    const int nblk = (min(kTKeys, g.ctx - j * kTKeys) + B - 1) >> p.lgB;
+                    return lane < nblk ? p.tables[(size_t)g.s * p.MB + ((size_t)j * kTKeys >> p.lgB) + lane] : 0;
+                };
+                int mine = entry(g.j0);
+                if constexpr (!QUANT) {
+                    // the query rows, once the last segment's score products have read theirs
+                    if (seg > 0) ok = waited(qfree, (uint32_t)((seg - 1) & 1));
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     if (lane == 0) {
-                        armed[0] = t + 1;  // expect_tx and every copy below, with no wait in between
-                        mbar_arrive_expect_tx(bar, (uint32_t)nblk * 2 * B * (D + 1));
+                        armed[2] = seg + 1;
+                        mbar_arrive_expect_tx(qfull, (uint32_t)(D / 64) * p.G * p.TQ * 128);
+                        for (int dh = 0; dh < D / 64; ++dh)
+                            tma_load_4d(sQ + dh * kTRegion, &tm_q, qfull, 0, dh, g.h * p.G, g.qs + g.mt * p.TQ, pol);
                     }
                     __syncwarp();
-                    if (lane < nblk) {
-                        tma_load_3d(sb + Geo::oRaw + b * Geo::kRaw + (uint32_t)lane * 2 * B * D, &tm, bar, 0, 0,
-                                    e * p.H_kv + g.h, pol);
-                        bulk_load(sb + Geo::oRawSc + b * Geo::kRawScales + (uint32_t)lane * 2 * B,
-                                  p.scales + ((size_t)(good ? e : 0) * p.H_kv + g.h) * (2 * B), 2 * B, bar);
-                    }
-                } else {
-                    const uint32_t b = slot(t);
-                    for (int which = 0; which < 2 && ok; ++which) {
-                        if (t >= NS) ok = waited((which ? vfree : kfree) + 8 * b, ph(t - NS));
+                }
+                for (int j = g.j0; j < g.j1 && ok; ++j, ++t) {
+                    const int nblk = (min(kTKeys, g.ctx - j * kTKeys) + B - 1) >> p.lgB;
+                    int e = mine;
+                    if (j + 1 < g.j1) mine = entry(j + 1);
+                    const bool good = (unsigned)e < (unsigned)p.NB;
+                    if (lane < nblk && !good) flag_error(p.err, PA_DEV_ERR_BLOCK);
+                    if (!good) e = p.NB;  // past the tensor: TMA fills zeros
+                    if constexpr (QUANT) {
+                        const uint32_t b = (uint32_t)(t % NR), bar = rfull + 8 * b;
+                        if (t >= NR) ok = waited(rfree + 8 * b, (uint32_t)((t / NR - 1) & 1));
                         ok = __all_sync(0xffffffffu, ok);
                         if (!ok) break;
-                        const uint32_t bar = (which ? vfull : kfull) + 8 * b;
                         if (lane == 0) {
-                            armed[which] = t + 1;  // as above
-                            mbar_arrive_expect_tx(bar, (uint32_t)nblk * B * D * 2);
+                            armed[0] = t + 1;  // expect_tx and every copy below, with no wait in between
+                            mbar_arrive_expect_tx(bar, (uint32_t)nblk * 2 * B * (D + 1));
                         }
                         __syncwarp();
-                        if (lane < nblk)
-                            tma_load_5d((which ? sV : sK) + b * kTile + (uint32_t)lane * B * D * 2, &tm, bar, 0, 0, 0,
-                                        e * (B / 8), which * p.H_kv + g.h, pol);
+                        if (lane < nblk) {
+                            tma_load_3d(sb + Geo::oRaw + b * Geo::kRaw + (uint32_t)lane * 2 * B * D, &tm, bar, 0, 0,
+                                        e * p.H_kv + g.h, pol);
+                            bulk_load(sb + Geo::oRawSc + b * Geo::kRawScales + (uint32_t)lane * 2 * B,
+                                      p.scales + ((size_t)(good ? e : 0) * p.H_kv + g.h) * (2 * B), 2 * B, bar);
+                        }
+                    } else {
+                        const uint32_t b = slot(t);
+                        for (int which = 0; which < 2 && ok; ++which) {
+                            if (t >= NS) ok = waited((which ? vfree : kfree) + 8 * b, ph(t - NS));
+                            ok = __all_sync(0xffffffffu, ok);
+                            if (!ok) break;
+                            const uint32_t bar = (which ? vfull : kfull) + 8 * b;
+                            if (lane == 0) {
+                                armed[which] = t + 1;  // as above
+                                mbar_arrive_expect_tx(bar, (uint32_t)nblk * B * D * 2);
+                            }
+                            __syncwarp();
+                            if (lane < nblk)
+                                tma_load_5d((which ? sV : sK) + b * kTile + (uint32_t)lane * B * D * 2, &tm, bar, 0, 0,
+                                            0, e * (B / 8), which * p.H_kv + g.h, pol);
+                        }
                     }
                 }
             }
-        }
-    } else if (warp == 9) {
-        // ------------------------------------------------------------ MMA issuer
-        const uint64_t dq = umma_desc(sQ, 16, 1024);
-        auto issue_s = [&](int w, int t) {
-            const uint64_t dk = umma_desc(sK + slot(t) * kTile, 16, kGroup);
-#pragma unroll
-            for (int ks = 0; ks < NK; ++ks)
-                umma_f16(tmem + (uint32_t)w * kTKeys, dq + (ks >> 2) * (kTRegion >> 4) + (ks & 3) * 2,
-                         dk + (ks >> 2) * (1024 >> 4) + (ks & 3) * 2, idesc_s, ks > 0);
-            umma_commit(sfull + 8 * w);
-            umma_commit(kfree + 8 * slot(t));
-        };
-        auto issue_pv = [&](int w, int t, bool first) {
-            const uint64_t dv = umma_desc(sV + slot(t) * kTile, 1024, kGroup);
-            const uint32_t pc = tmem + (uint32_t)w * kTKeys, oc = tmem + 2 * kTKeys + (uint32_t)w * D;
-#pragma unroll
-            for (int ks = 0; ks < NT; ++ks) {
-                const uint64_t vd = dv + (uint64_t)(ks * ((2 * kGroup) >> 4));
-                umma_f16_ta(oc, pc + ks * 8, vd, idesc_o, !first || ks > 0);
-                if (SPLIT) umma_f16_ta(oc, pc + kTKeys / 2 + ks * 8, vd, idesc_o, 1u);
-            }
-            umma_commit(pvd + 8 * w);
-            umma_commit(vfree + 8 * slot(t));
-        };
-        if (lane == 0) {
-            int t = 0, c[2] = {0, 0};  // tiles so far; tiles of each warpgroup with S issued
-            for (int seg = 0; ok && walk.next(p, g); ++seg) {
-                const int nt = g.j1 - g.j0;
-                // S of tile i: its buffer is free once the products have read the P that lay there
-                auto start_s = [&](int i) {
-                    const int w = i & 1;
-                    ok = (c[w] == 0 || waited(pvd + 8 * w, (uint32_t)((c[w] - 1) & 1))) &&
-                         waited(kfull + 8 * slot(t + i), ph(t + i));
+        } else if (warp == 9) {
+            // -------------------------------------------------------- MMA issuer
+            if (lane == 0) {
+                const uint64_t dq = umma_desc(sQ, 16, 1024);
+                TreeWalk ahead = walk;  // the score products run one tile ahead of the value products
+                TreeSeg gs;
+                int js = 0, segs = -1;
+                bool more = ahead.next(p, gs);
+                js = gs.j0;
+                auto issue_s = [&](int t) {
+                    if (js == gs.j0) ok = waited(qfull, (uint32_t)(++segs & 1));
+                    // the buffer is free once the value products have read the P that lay there
+                    ok = ok && (t < 2 || waited(pvd + 8 * (t & 1), (uint32_t)((t / 2 - 1) & 1))) &&
+                         waited(kfull + 8 * slot(t), ph(t));
                     if (!ok) return;
                     tc_fence_after();
-                    issue_s(w, t + i);
-                    ++c[w];
-                    if (i + 1 == nt) umma_commit(qfree);
-                };
-                ok = waited(qfull, (uint32_t)(seg & 1));
-                if (ok) start_s(0);
-                if (ok && nt > 1) start_s(1);
-                for (int i = 0; i < nt && ok; ++i) {
-                    const int w = i & 1;
-                    ok = waited(prdy + 8 * w, (uint32_t)((c[w] - 1) & 1)) && waited(vfull + 8 * slot(t + i), ph(t + i)) &&
-                         (i >= 2 || seg == 0 || waited(ofree, (uint32_t)((seg - 1) & 1)));
-                    if (!ok) break;
-                    tc_fence_after();
-                    issue_pv(w, t + i, i < 2);
-                    if (i + 2 < nt) start_s(i + 2);
-                }
-                t += nt;
-            }
-            umma_commit(mmadone);  // arrives once every product issued above has completed
-        }
-        __syncwarp();
-    } else if (warp >= 10) {
-        // ------------------------------------------------------------ converters (quantised pool)
-        if constexpr (QUANT) {
-            const int cw = warp - 10;
-            constexpr int L = D / 16;                     // 16-byte pieces of a row
-            constexpr int kSteps = kTKeys * L / 32;       // warp steps of a tile
-            int t = 0;
-            while (walk.next(p, g)) {
-                for (int j = g.j0; j < g.j1; ++j, ++t) {
-                    const int k0 = j * kTKeys, nvalid = min(kTKeys, g.ctx - k0);
-                    const uint32_t rb = (uint32_t)(t % NR);
-                    const uint32_t raw = sb + Geo::oRaw + rb * Geo::kRaw, rsc = sb + Geo::oRawSc + rb * Geo::kRawScales;
-                    uint32_t u[4];
-                    if (k0 + kTKeys > g.ctx - g.n) {
-                        tree_union(p, g, k0, u);
-                    } else {
-                        u[0] = u[1] = u[2] = u[3] = 0xffffffffu;
+                    const uint64_t dk = umma_desc(sK + slot(t) * kTile, 16, kGroup);
+#pragma unroll
+                    for (int ks = 0; ks < NK; ++ks)
+                        umma_f16(tmem + (uint32_t)(t & 1) * kTKeys, dq + (ks >> 2) * (kTRegion >> 4) + (ks & 3) * 2,
+                                 dk + (ks >> 2) * (1024 >> 4) + (ks & 3) * 2, idesc_s, ks > 0);
+                    umma_commit(sfull + 8 * (t & 1));
+                    umma_commit(kfree + 8 * slot(t));
+                    if (++js == gs.j1) {
+                        umma_commit(qfree);
+                        more = ahead.next(p, gs);
+                        js = gs.j0;
                     }
-                    (void)nvalid;  // keys past the context are in no union
-                    ok = waited(rfull + 8 * rb, (uint32_t)((t / NR) & 1)) && ok;
-                    // lane: keys 4 lane .. + 3, all of one block
-                    const uint32_t at = ((uint32_t)(4 * lane) >> p.lgB) * 2 * B + ((4 * lane) & (B - 1));
-                    uint32_t kb;
-                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(kb) : "r"(rsc + at));
-                    int em = kScaleMin;
+                };
+                if (more) issue_s(0);
+                int t = 0;
+                while (ok && walk.next(p, g)) {
+                    for (int j = g.j0; j < g.j1 && ok; ++j, ++t) {
+                        if (more) issue_s(t + 1);
+                        ok = ok && waited(vfull + 8 * slot(t), ph(t));
+                        const uint32_t par = (uint32_t)((t >> 1) & 1), rdy = prdy + 16 * (t & 1);
+                        // a segment's first products start O_0 and O_1 afresh: both warpgroups have then read the last's
+                        if (j == g.j0) ok = ok && waited(rdy, par) && waited(rdy + 8, par);
+                        const uint64_t dv = umma_desc(sV + slot(t) * kTile, 1024, kGroup);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (u[lane >> 3] >> ((4 * lane + i) & 31) & 1u) em = max(em, scale_of((kb >> 8 * i) & 255));
-                    em = __reduce_max_sync(0xffffffffu, em);
-                    const uint32_t sl = slot(t);
-                    // K, then V; piece x: row x / L, 16 elements from 16 (x % L) on
-                    for (int which = 0; which < 2; ++which) {
-                        if (t >= NS) ok = waited((which ? vfree : kfree) + 8 * sl, ph(t - NS)) && ok;
-                        const uint32_t dst = (which ? sV : sK) + sl * kTile;
-                        for (int st = cw; st < kSteps; st += kConvWarps) {
-                            const int x = st * 32 + lane, r = x / L, c = x % L;
-                            const uint32_t blk = (uint32_t)r >> p.lgB, in = r & (B - 1);
-                            const uint32_t rr = (which ? B : 0) + in;  // row of the block's chunk, swizzled by TMA
-                            const uint32_t src = raw + blk * 2 * B * D + rr * D +
-                                                 (D == 128 ? ((c ^ (rr & 7)) << 4) : ((c ^ (rr >> 1 & 3)) << 4));
-                            uint4 v;
-                            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                                         : "r"(src));
-                            const bool seen = u[r >> 5] >> (r & 31) & 1u;
-                            uint32_t h[8] = {e4m3x2_to_f16x2(v.x), e4m3x2_to_f16x2(v.x >> 16), e4m3x2_to_f16x2(v.y),
-                                             e4m3x2_to_f16x2(v.y >> 16), e4m3x2_to_f16x2(v.z),
-                                             e4m3x2_to_f16x2(v.z >> 16), e4m3x2_to_f16x2(v.w),
-                                             e4m3x2_to_f16x2(v.w >> 16)};
-                            if (which == 0) {
-                                uint32_t b;
-                                asm volatile("ld.shared.u8 %0, [%1];" : "=r"(b) : "r"(rsc + blk * 2 * B + in));
-                                const __half2 f = __float2half2_rn(pow2i(scale_of((int)b) - em + 7));
+                        for (int w = 0; w < 2; ++w) {
+                            ok = ok && waited(rdy + 8 * w, par);
+                            if (!ok) break;
+                            tc_fence_after();
+                            const uint32_t oc = tmem + 2 * kTKeys + (uint32_t)w * D;
 #pragma unroll
-                                for (int i = 0; i < 8; ++i) {
-                                    const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&h[i]), f);
-                                    h[i] = *reinterpret_cast<const uint32_t*>(&y);
+                            for (int ks = 0; ks < NT; ++ks) {
+                                const uint64_t vd = dv + (uint64_t)((w * NT + ks) * ((2 * kGroup) >> 4));
+                                const uint32_t pk = tmem + (uint32_t)(t & 1) * kTKeys + w * 64 + (ks >> 1) * 32 + (ks & 1) * 8;
+                                umma_f16_ta(oc, pk, vd, idesc_o, j > g.j0 || ks > 0);
+                                if (SPLIT) umma_f16_ta(oc, pk + 16, vd, idesc_o, 1u);
+                            }
+                        }
+                        if (!ok) break;
+                        umma_commit(pvd + 8 * (t & 1));
+                        umma_commit(vfree + 8 * slot(t));
+                    }
+                }
+                umma_commit(mmadone);  // arrives once every product issued above has completed
+            }
+            __syncwarp();
+        } else {
+            // -------------------------------------------------------- converters (quantised pool)
+            if constexpr (QUANT) {
+                const int cw = warp - 10;
+                constexpr int L = D / 16;                // 16-byte pieces of a row
+                constexpr int kSteps = kTKeys * L / 32;  // warp steps of a tile
+                int t = 0;
+                for (int seg = 0; walk.next(p, g); ++seg) {
+                    // the query rows as fp16, four lanes to a row, once the last segment's have been used
+                    if (seg > 0) {
+                        ok = waited(qfree, (uint32_t)((seg - 1) & 1)) && ok;
+                        ok = waited(qread, (uint32_t)((seg - 1) & 1)) && ok;
+                    }
+                    {
+                        constexpr int C = D / 32;  // 16-byte pieces of a row per lane
+                        const int tok0 = g.mt * p.TQ, rows = min(p.TQ, g.n - tok0) * p.G;
+                        for (int r = cw * 8 + (lane >> 2); r < kTRows; r += 8 * kConvWarps) {
+                            uint4 x[C];
+                            const size_t row = ((size_t)(g.qs + tok0 + r / p.G) * p.H_q + (size_t)g.h * p.G + r % p.G) * D;
+                            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + row);
+#pragma unroll
+                            for (int i = 0; i < C; ++i) x[i] = r < rows ? src[4 * i + (lane & 3)] : make_uint4(0, 0, 0, 0);
+                            int e = 0;
+                            if (p.q_bf16) {
+                                float a = 0.f;
+#pragma unroll
+                                for (int i = 0; i < C; ++i) {
+                                    const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k) {
+                                        const float2 f = Mma<__nv_bfloat16>::unpack(v[k]);
+                                        a = fmaxf(a, fmaxf(fabsf(f.x), fabsf(f.y)));
+                                    }
+                                }
+                                const unsigned quad = 0xfu << (lane & 28);
+                                a = fmaxf(a, __shfl_xor_sync(quad, a, 1));
+                                a = fmaxf(a, __shfl_xor_sync(quad, a, 2));
+                                // largest magnitude to [2^14, 2^15), as in decode_quant.cu
+                                const int ex = (int)(__float_as_uint(a) >> 23) - 127;
+                                e = ex > 127 || a == 0.f ? 0 : max(ex - 14, -126);
+                                const float inv = pow2i(-e);
+#pragma unroll
+                                for (int i = 0; i < C; ++i) {
+                                    uint32_t* v = reinterpret_cast<uint32_t*>(&x[i]);
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k) {
+                                        const float2 f = Mma<__nv_bfloat16>::unpack(v[k]);
+                                        v[k] = Mma<__half>::pack(f.x * inv, f.y * inv);
+                                    }
                                 }
                             }
-                            // rows nobody sees, past the context or padding, may hold anything: zeros
-                            if (!seen) {
+                            if ((lane & 3) == 0) qexp[r] = (int8_t)e;
 #pragma unroll
-                                for (int i = 0; i < 8; ++i) h[i] = 0u;
-                            }
-                            // 16-byte pieces 2 c and 2 c + 1 of the row (8 per column half); half the lanes store
-                            // them in the other order, which spreads a quarter warp's stores over all banks
-                            const uint32_t row = dst + (uint32_t)(r >> 3) * kGroup + (uint32_t)(c >> 2) * 1024 + (r & 7) * 128;
-                            const uint32_t flip = D == 128 ? (lane >> 2 & 1) : 0;
-#pragma unroll
-                            for (int o = 0; o < 2; ++o) {
-                                const uint32_t oo = o ^ flip;
-                                const uint32_t a = row + ((((c & 3) * 2 + oo) ^ (r & 7)) << 4);
-                                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a),
-                                             "r"(oo ? h[4] : h[0]), "r"(oo ? h[5] : h[1]), "r"(oo ? h[6] : h[2]),
-                                             "r"(oo ? h[7] : h[3])
+                            for (int i = 0; i < C; ++i) {
+                                const int ch = 4 * i + (lane & 3);  // piece of the row
+                                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                                 sQ + (uint32_t)(ch >> 3) * kTRegion + r * 128 + (((ch & 7) ^ (r & 7)) << 4)),
+                                             "r"(x[i].x), "r"(x[i].y), "r"(x[i].z), "r"(x[i].w)
                                              : "memory");
                             }
                         }
-                        if (which) {
-                            float* ex = reinterpret_cast<float*>(smem_raw + Geo::oExp + sl * Geo::kExp);
-                            const int key = cw * 32 + lane;
-                            if (key < kTKeys) {
-                                uint32_t b;
-                                asm volatile("ld.shared.u8 %0, [%1];"
-                                             : "=r"(b)
-                                             : "r"(rsc + ((uint32_t)key >> p.lgB) * 2 * B + B + (key & (B - 1))));
-                                const int ev = scale_of((int)b);
-                                ex[key] = (float)ev;
-                                ex[kTKeys + key] = pow2i(-ev);
-                            }
-                            if (cw == 0 && lane == 0) kmul[sl] = pow2i(em - 7);
-                        }
                         fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive((which ? vfull : kfull) + 8 * sl);
+                        if (lane == 0) mbar_arrive(qfull);
                     }
-                    if (lane == 0) mbar_arrive(rfree + 8 * rb);
+                    for (int j = g.j0; j < g.j1; ++j, ++t) {
+                        const int k0 = j * kTKeys;
+                        const uint32_t rb = (uint32_t)(t % NR);
+                        const uint32_t raw = sb + Geo::oRaw + rb * Geo::kRaw, rsc = sb + Geo::oRawSc + rb * Geo::kRawScales;
+                        uint32_t u[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+                        if (k0 + kTKeys > g.ctx - g.n) tree_union<4>(p, g, k0, u);  // keys past the context are in none
+                        ok = waited(rfull + 8 * rb, (uint32_t)((t / NR) & 1)) && ok;
+                        // lane: keys 4 lane .. + 3, all of one block
+                        const uint32_t at = ((uint32_t)(4 * lane) >> p.lgB) * 2 * B + ((4 * lane) & (B - 1));
+                        uint32_t kb;
+                        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(kb) : "r"(rsc + at));
+                        int em = kScaleMin;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (u[lane >> 3] >> ((4 * lane + i) & 31) & 1u) em = max(em, scale_of((kb >> 8 * i) & 255));
+                        em = __reduce_max_sync(0xffffffffu, em);
+                        const uint32_t sl = slot(t);
+                        // K, then V; piece x: row x / L, 16 elements from 16 (x % L) on
+                        for (int which = 0; which < 2; ++which) {
+                            if (t >= NS) ok = waited((which ? vfree : kfree) + 8 * sl, ph(t - NS)) && ok;
+                            const uint32_t dst = (which ? sV : sK) + sl * kTile;
+                            for (int st = cw; st < kSteps; st += kConvWarps) {
+                                const int x = st * 32 + lane, r = x / L, c = x % L;
+                                const uint32_t blk = (uint32_t)r >> p.lgB, in = r & (B - 1);
+                                const uint32_t rr = (which ? B : 0) + in;  // row of the block's chunk, swizzled by TMA
+                                const uint32_t src = raw + blk * 2 * B * D + rr * D +
+                                                     (D == 128 ? ((c ^ (rr & 7)) << 4) : ((c ^ (rr >> 1 & 3)) << 4));
+                                uint4 v;
+                                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                             : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                                             : "r"(src));
+                                const bool seen = u[r >> 5] >> (r & 31) & 1u;
+                                uint32_t h[8] = {e4m3x2_to_f16x2(v.x), e4m3x2_to_f16x2(v.x >> 16), e4m3x2_to_f16x2(v.y),
+                                                 e4m3x2_to_f16x2(v.y >> 16), e4m3x2_to_f16x2(v.z),
+                                                 e4m3x2_to_f16x2(v.z >> 16), e4m3x2_to_f16x2(v.w),
+                                                 e4m3x2_to_f16x2(v.w >> 16)};
+                                if (which == 0) {
+                                    uint32_t b;
+                                    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(b) : "r"(rsc + blk * 2 * B + in));
+                                    const __half2 f = __float2half2_rn(pow2i(scale_of((int)b) - em + 7));
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i) {
+                                        const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&h[i]), f);
+                                        h[i] = *reinterpret_cast<const uint32_t*>(&y);
+                                    }
+                                }
+                                // rows nobody sees, past the context or padding, may hold anything: zeros
+                                if (!seen) {
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i) h[i] = 0u;
+                                }
+                                // 16-byte pieces 2 c and 2 c + 1 of the row (8 per column half); half the lanes store
+                                // them in the other order, which spreads a quarter warp's stores over all banks
+                                const uint32_t row = dst + (uint32_t)(r >> 3) * kGroup + (uint32_t)(c >> 2) * 1024 + (r & 7) * 128;
+                                const uint32_t flip = D == 128 ? (lane >> 2 & 1) : 0;
+#pragma unroll
+                                for (int o = 0; o < 2; ++o) {
+                                    const uint32_t oo = o ^ flip;
+                                    const uint32_t a = row + ((((c & 3) * 2 + oo) ^ (r & 7)) << 4);
+                                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a),
+                                                 "r"(oo ? h[4] : h[0]), "r"(oo ? h[5] : h[1]), "r"(oo ? h[6] : h[2]),
+                                                 "r"(oo ? h[7] : h[3])
+                                                 : "memory");
+                                }
+                            }
+                            if (which) {
+                                uint32_t* ex = reinterpret_cast<uint32_t*>(smem_raw + Geo::oExp + sl * Geo::kExp);
+                                const int key = cw * 32 + lane;
+                                if (key < kTKeys) {
+                                    uint32_t b;
+                                    asm volatile("ld.shared.u8 %0, [%1];"
+                                                 : "=r"(b)
+                                                 : "r"(rsc + ((uint32_t)key >> p.lgB) * 2 * B + B + (key & (B - 1))));
+                                    const int ev = scale_of((int)b);
+                                    // both exact in bf16: the upper halves of the fp32 values
+                                    ex[key] = __float_as_uint((float)ev) >> 16 | (__float_as_uint(pow2i(-ev)) & 0xffff0000u);
+                                }
+                                if (cw == 0 && lane == 0) kmul[sl] = pow2i(em - 7);
+                            }
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive((which ? vfull : kfull) + 8 * sl);
+                        }
+                        if (lane == 0) mbar_arrive(rfree + 8 * rb);
+                    }
                 }
             }
         }
     } else {
-        // ------------------------------------------------------------ softmax warpgroup w: key tiles w, w + 2, ...
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Geo::kMore));
+        // ------------------------------------------------------------ softmax warpgroup w: keys 64 w .. of each tile
         const int w = warp >> 2;
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t t_s = lanes + (uint32_t)w * kTKeys, t_o = lanes + 2 * kTKeys;
+        const uint32_t t_o = lanes + 2 * kTKeys;
         const int r = tid & (kTRows - 1);
-        int t = 0, c[2] = {0, 0};  // tiles so far, tiles of each warpgroup
-        for (int seg = 0; walk.next(p, g); ++seg) {
-            const int nt = g.j1 - g.j0;
+        const uint32_t pair = 1 + (warp & 3);  // named barrier of the two warps that hold the same rows
+        float* xch = reinterpret_cast<float*>(smem_raw + Geo::oXch);
+        int t = 0;  // tiles so far
+        while (walk.next(p, g)) {
             const int tok0 = g.mt * p.TQ, rows = min(p.TQ, g.n - tok0) * p.G;
             const int tok = tok0 + r / p.G;
             const bool row_ok = r < rows, warp_ok = (warp & 3) * 32 < rows;
             const int base = g.ctx - g.n;  // keys before the draft
-            const size_t orow = ((size_t)(g.qs + tok) * p.H_q + (size_t)g.h * p.G + r % p.G) * D;
             float cr = p.scale_log2;
-            // The row of Q: warpgroup w stores its half (of 64 columns, or of the one region of D = 64).
-            {
-                constexpr int C = D / 8;  // 16-byte pieces of a row
-                const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + orow);
-                uint4 x[QUANT ? C : C / 2];
-                constexpr int N_ = QUANT ? C : C / 2;
-                const int c0 = QUANT ? 0 : w * (C / 2);
-#pragma unroll
-                for (int i = 0; i < N_; ++i) x[i] = row_ok ? src[c0 + i] : make_uint4(0, 0, 0, 0);
-                if constexpr (QUANT) {
-                    if (p.q_bf16) {
-                        float a = 0.f;
-#pragma unroll
-                        for (int i = 0; i < N_; ++i) {
-                            const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const float2 f = Mma<__nv_bfloat16>::unpack(v[k]);
-                                a = fmaxf(a, fmaxf(fabsf(f.x), fabsf(f.y)));
-                            }
-                        }
-                        // largest magnitude to [2^14, 2^15), as in decode_quant.cu
-                        const int ex = (int)(__float_as_uint(a) >> 23) - 127;
-                        const int e = ex > 127 || a == 0.f ? 0 : max(ex - 14, -126);
-                        const float inv = pow2i(-e);
-                        cr *= pow2i(e);
-#pragma unroll
-                        for (int i = 0; i < N_; ++i) {
-                            uint32_t* v = reinterpret_cast<uint32_t*>(&x[i]);
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const float2 f = Mma<__nv_bfloat16>::unpack(v[k]);
-                                v[k] = Mma<__half>::pack(f.x * inv, f.y * inv);
-                            }
-                        }
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < C / 2; ++i) {
-                    const int ch = w * (C / 2) + i;  // piece of the row
-                    const uint4 v = QUANT ? (w ? x[(C / 2 + i) % N_] : x[i]) : x[i];
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                     sQ + (uint32_t)(ch >> 3) * kTRegion + r * 128 + (((ch & 7) ^ (r & 7)) << 4)),
-                                 "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                                 : "memory");
-                }
-                fence_proxy_async_smem();
-                mbar_arrive(qfull);
-            }
             float m_ref = NEG_INF, l = 0.f;
-            for (int i = w; i < nt; i += 2) {
-                const int k0 = (g.j0 + i) * kTKeys;
-                ok = waited(sfull + 8 * w, (uint32_t)(c[w] & 1)) && ok;
+            for (int j = g.j0; j < g.j1; ++j, ++t) {
+                const int k0 = j * kTKeys + 64 * w;  // the warpgroup's first key
+                const uint32_t par = (uint32_t)((t >> 1) & 1);
+                const uint32_t t_s = lanes + (uint32_t)(t & 1) * kTKeys + (uint32_t)w * 64;
+                const bool masked = k0 + 64 > base;
+                uint32_t vis[2] = {0u, 0u};
+                if (masked && row_ok) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) vis[k] = tree_visible(p, g, tok, k0 + 32 * k - base);
+                }
+                ok = waited(sfull + 8 * (t & 1), par) && ok;
                 tc_fence_after();
-                if (QUANT) ok = waited(vfull + 8 * slot(t + i), ph(t + i)) && ok;  // the tile's exponents
-                const bool masked = k0 + kTKeys > base;
-                if (warp_ok) {
-                    float v[kTKeys];
-                    {
-                        uint32_t* u = reinterpret_cast<uint32_t*>(v);
-#pragma unroll
-                        for (int k = 0; k < kTKeys / 32; ++k)
-                            asm volatile(
-                                "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-                                "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
-                                "%28, %29, %30, %31}, [%32];"
-                                : "=r"(u[32 * k + 0]), "=r"(u[32 * k + 1]), "=r"(u[32 * k + 2]), "=r"(u[32 * k + 3]),
-                                  "=r"(u[32 * k + 4]), "=r"(u[32 * k + 5]), "=r"(u[32 * k + 6]), "=r"(u[32 * k + 7]),
-                                  "=r"(u[32 * k + 8]), "=r"(u[32 * k + 9]), "=r"(u[32 * k + 10]), "=r"(u[32 * k + 11]),
-                                  "=r"(u[32 * k + 12]), "=r"(u[32 * k + 13]), "=r"(u[32 * k + 14]), "=r"(u[32 * k + 15]),
-                                  "=r"(u[32 * k + 16]), "=r"(u[32 * k + 17]), "=r"(u[32 * k + 18]), "=r"(u[32 * k + 19]),
-                                  "=r"(u[32 * k + 20]), "=r"(u[32 * k + 21]), "=r"(u[32 * k + 22]), "=r"(u[32 * k + 23]),
-                                  "=r"(u[32 * k + 24]), "=r"(u[32 * k + 25]), "=r"(u[32 * k + 26]), "=r"(u[32 * k + 27]),
-                                  "=r"(u[32 * k + 28]), "=r"(u[32 * k + 29]), "=r"(u[32 * k + 30]), "=r"(u[32 * k + 31])
-                                : "r"(t_s + k * 32)
-                                : "memory");
-                        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+                if (QUANT) {
+                    ok = waited(vfull + 8 * slot(t), ph(t)) && ok;  // the tile's exponents
+                    if (j == g.j0) {
+                        cr = p.scale_log2 * pow2i((int)qexp[r]);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(qread);
                     }
-                    const uint32_t ex = sb + Geo::oExp + slot(t + i) * Geo::kExp;
-                    const float mul = QUANT ? cr * kmul[slot(t + i)] : cr;
+                }
+                if (warp_ok) {
+                    uint32_t s[2][32];
+                    tmem_ld32_async(t_s, s[0]);
+                    tmem_ld32_async(t_s + 32, s[1]);
+                    tmem_loaded(s[0]);
+                    tmem_loaded(s[1]);
+                    const uint32_t ex = sb + Geo::oExp + slot(t) * Geo::kExp + 4 * 64 * w;
+                    const float mul = QUANT ? cr * kmul[slot(t)] : cr;
                     const float2 mul2 = make_float2(mul, mul);
+                    float y[64];  // 16-bit pool: raw scores; quantised: y
 #pragma unroll
-                    for (int k = 0; k < kTKeys; k += 4) {
-                        float4 ev = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (QUANT)
-                            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                                         : "=f"(ev.x), "=f"(ev.y), "=f"(ev.z), "=f"(ev.w)
+                    for (int k = 0; k < 64; k += 4) {
+                        const uint32_t* x = &s[k >> 5][k & 31];
+                        if constexpr (QUANT) {
+                            uint32_t e[4];
+                            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                         : "=r"(e[0]), "=r"(e[1]), "=r"(e[2]), "=r"(e[3])
                                          : "r"(ex + 4 * k));
-                        const float2 a = ffma2(make_float2(v[k], v[k + 1]), mul2, make_float2(ev.x, ev.y));
-                        const float2 b = ffma2(make_float2(v[k + 2], v[k + 3]), mul2, make_float2(ev.z, ev.w));
-                        v[k] = a.x;
-                        v[k + 1] = a.y;
-                        v[k + 2] = b.x;
-                        v[k + 3] = b.y;
+#pragma unroll
+                            for (int i = 0; i < 4; i += 2) {
+                                const float2 v = ffma2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), mul2,
+                                                       make_float2(__uint_as_float(e[i] << 16), __uint_as_float(e[i + 1] << 16)));
+                                y[k + i] = v.x;
+                                y[k + i + 1] = v.y;
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) y[k + i] = __uint_as_float(x[i]);
+                        }
                     }
                     if (masked) {
 #pragma unroll
-                        for (int k = 0; k < kTKeys / 32; ++k) {
-                            const uint32_t vis = row_ok ? tree_visible(p, g, tok, k0 + 32 * k - base) : 0u;
-#pragma unroll
-                            for (int b = 0; b < 32; ++b) v[32 * k + b] = vis >> b & 1u ? v[32 * k + b] : NEG_INF;
-                        }
+                        for (int k = 0; k < 64; ++k) y[k] = vis[k >> 5] >> (k & 31) & 1u ? y[k] : NEG_INF;
                     }
                     float mx[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
 #pragma unroll
-                    for (int k = 0; k < kTKeys; k += 8) {
-                        mx[0] = fmax3(mx[0], v[k], v[k + 1]);
-                        mx[1] = fmax3(mx[1], v[k + 2], v[k + 3]);
-                        mx[2] = fmax3(mx[2], v[k + 4], v[k + 5]);
-                        mx[3] = fmax3(mx[3], v[k + 6], v[k + 7]);
+                    for (int k = 0; k < 64; k += 8) {
+                        mx[0] = fmax3(mx[0], y[k], y[k + 1]);
+                        mx[1] = fmax3(mx[1], y[k + 2], y[k + 3]);
+                        mx[2] = fmax3(mx[2], y[k + 4], y[k + 5]);
+                        mx[3] = fmax3(mx[3], y[k + 6], y[k + 7]);
                     }
-                    const float m_tile = fmax3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
+                    float m_tile = fmax3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
+                    if (!QUANT) m_tile *= mul;  // (the scale is positive)
                     const float m_new = m_tile > m_ref + 8.f || m_ref == NEG_INF ? fmaxf(m_ref, m_tile) : m_ref;
-                    const float alpha = i == w || m_new == m_ref ? 1.f : fast_exp2(m_ref - m_new);
+                    const float alpha = j == g.j0 || m_new == m_ref ? 1.f : fast_exp2(m_ref - m_new);
                     m_ref = m_new;
                     const float m_use = m_new == NEG_INF ? 0.f : m_new;
                     const float2 nm2 = make_float2(-m_use, -m_use);
-                    // P over S: 64 columns of pairs, and (SPLIT) the low parts in the next 64
+                    // P of 32 keys goes over their scores: 16 columns of pairs, and (SPLIT) the low parts in the next 16
                     float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                    for (int k = 0; k < kTKeys / 32; ++k) {
+                    for (int k = 0; k < 2; ++k) {
                         uint32_t hi[16], lo[16];
 #pragma unroll
-                        for (int b = 0; b < 32; b += 2) {
-                            float2 x = fadd2(make_float2(v[32 * k + b], v[32 * k + b + 1]), nm2);
-                            x.x = fast_exp2(x.x);
-                            x.y = fast_exp2(x.y);
-                            if constexpr (QUANT) {
-                                float2 iv;
-                                asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
-                                             : "=f"(iv.x), "=f"(iv.y)
-                                             : "r"(ex + 4 * (kTKeys + 32 * k + b)));
-                                ls[(b >> 1) & 1] = ffma2(x, iv, ls[(b >> 1) & 1]);
-                            } else {
-                                ls[(b >> 1) & 1] = fadd2(ls[(b >> 1) & 1], x);
-                            }
-                            hi[b / 2] = Mma<PT>::pack(x.x, x.y);
-                            if (SPLIT) {
-                                const float2 f = fsub2(x, Mma<PT>::unpack(hi[b / 2]));
-                                lo[b / 2] = Mma<PT>::pack(f.x, f.y);
+                        for (int b = 0; b < 32; b += 4) {
+                            uint32_t e[4];
+                            if constexpr (QUANT)
+                                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                             : "=r"(e[0]), "=r"(e[1]), "=r"(e[2]), "=r"(e[3])
+                                             : "r"(ex + 4 * (32 * k + b)));
+#pragma unroll
+                            for (int i = 0; i < 4; i += 2) {
+                                const float2 yy = make_float2(y[32 * k + b + i], y[32 * k + b + i + 1]);
+                                float2 x = QUANT ? fadd2(yy, nm2) : ffma2(yy, mul2, nm2);
+                                x.x = fast_exp2(x.x);
+                                x.y = fast_exp2(x.y);
+                                float2& acc = ls[(i >> 1) & 1];
+                                if constexpr (QUANT)
+                                    acc = ffma2(x, make_float2(__uint_as_float(e[i] & 0xffff0000u), __uint_as_float(e[i + 1] & 0xffff0000u)), acc);
+                                else
+                                    acc = fadd2(acc, x);
+                                const int at = (b + i) / 2;
+                                hi[at] = Mma<PT>::pack(x.x, x.y);
+                                if (SPLIT) {
+                                    const float2 f = fsub2(x, Mma<PT>::unpack(hi[at]));
+                                    lo[at] = Mma<PT>::pack(f.x, f.y);
+                                }
                             }
                         }
-                        tmem_st16(t_s + k * 16, hi);
-                        if (SPLIT) tmem_st16(t_s + kTKeys / 2 + k * 16, lo);
+                        tmem_st16(t_s + k * 32, hi);
+                        if (SPLIT) tmem_st16(t_s + k * 32 + 16, lo);
                     }
                     const float2 lsum = fadd2(ls[0], ls[1]);
                     l = fmaf(l, alpha, lsum.x + lsum.y);
-                    // O_w is rescaled (rarely) after the products of the warpgroup's last tile, which have landed: S
-                    // of this tile was issued after them
+                    // O_w is rescaled (rarely) once the last tile's products have landed
                     if (__any_sync(0xffffffffu, alpha != 1.f)) {
-                        ok = waited(pvd + 8 * w, (uint32_t)((c[w] - 1) & 1)) && ok;
+                        ok = waited(pvd + 8 * ((t - 1) & 1), (uint32_t)(((t - 1) >> 1) & 1)) && ok;
                         tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                         for (int k = 0; k < D / 32; ++k) {
                             float o[32];
                             tmem_ld32(t_o + (uint32_t)w * D + k * 32, o);
@@ -713,82 +755,81 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                 }
                 if (!QUANT && masked) {
                     // V rows nobody sees (past the context, padding) may hold anything, even NaN: zeros before the
-                    // products meet them with P = 0
-                    uint32_t u[4];
-                    tree_union(p, g, k0, u);
-                    ok = waited(vfull + 8 * slot(t + i), ph(t + i)) && ok;
-                    const int rr = (warp & 3) * 32 + lane;
-                    if (!(u[warp & 3] >> lane & 1u)) {
-                        const uint32_t vr = sV + slot(t + i) * kTile + (uint32_t)(rr >> 3) * kGroup + (rr & 7) * 128;
+                    // products meet them with P = 0.  Two threads to a row, one per half of it.
+                    uint32_t u[2];
+                    tree_union<2>(p, g, k0, u);
+                    ok = waited(vfull + 8 * slot(t), ph(t)) && ok;
+                    const int rr = (r & 63), key = 64 * w + rr;
+                    if (!(u[rr >> 5] >> (rr & 31) & 1u)) {
+                        const uint32_t vr = sV + slot(t) * kTile + (uint32_t)(key >> 3) * kGroup + (key & 7) * 128;
 #pragma unroll
-                        for (int k = 0; k < D / 8; ++k)
+                        for (int i = 0; i < D / 16; ++i) {
+                            const int k = (r >> 6) * (D / 16) + i;
                             asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(vr + (k >> 3) * 1024 +
                                                                                           (k & 7) * 16),
                                          "r"(0)
                                          : "memory");
+                        }
                     }
                     fence_proxy_async_smem();
                 }
                 tc_fence_before();
-                mbar_arrive(prdy + 8 * w);
-                ++c[w];
+                mbar_arrive(prdy + 16 * (t & 1) + 8 * w);
             }
-            if (nt > (w ^ 1)) c[w ^ 1] += (nt - (w ^ 1) + 1) / 2;
-            t += nt;
-            // the warpgroups' results: every product of the segment has landed, and Q's space is free
-            ok = waited(qfree, (uint32_t)(seg & 1)) && ok;
-            for (int x = 0; x < 2; ++x)
-                if (nt > x) ok = waited(pvd + 8 * x, (uint32_t)((c[x] - 1) & 1)) && ok;
-            tc_fence_after();
-            float2* xch = reinterpret_cast<float2*>(smem_raw);
-            xch[w * kTRows + r] = make_float2(m_ref, l);
-            asm volatile("bar.sync 1, 256;" ::: "memory");
-            const float2 o0 = xch[r], o1 = xch[kTRows + r];
-            asm volatile("bar.sync 1, 256;" ::: "memory");
-            const float M = fmaxf(o0.x, o1.x);
-            const float f0 = o0.x == NEG_INF ? 0.f : fast_exp2(o0.x - M), f1 = o1.x == NEG_INF ? 0.f : fast_exp2(o1.x - M);
-            const float den = o0.y * f0 + o1.y * f1;  // (a NaN exponential sum stays one)
+            // The two warps of the same rows exchange their maxima, then their sums, and each joins and stores one half
+            // of the columns once the last products have landed.
+            xch[w * kTRows + r] = m_ref;
+            asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+            const float m_other = xch[(w ^ 1) * kTRows + r];
+            asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+            xch[w * kTRows + r] = l;
+            asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+            const float l_other = xch[(w ^ 1) * kTRows + r];
+            asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+            const float M = fmaxf(m_ref, m_other);
+            const float fo = m_ref == NEG_INF ? 0.f : fast_exp2(m_ref - M), fx = m_other == NEG_INF ? 0.f : fast_exp2(m_other - M);
+            const float f0 = w ? fx : fo, f1 = w ? fo : fx;
+            // both warps sum in the same order (a NaN exponential sum stays one)
+            const float den = w ? l_other * f0 + l * f1 : l * f0 + l_other * f1;
             const bool whole = g.j0 == 0 && g.j1 == g.nt;
             const int part = 2 * blockIdx.x + (g.j0 == 0 ? 1 : 0);
+            const size_t orow = ((size_t)(g.qs + tok) * p.H_q + (size_t)g.h * p.G + r % p.G) * D;
             const float inv = den == 0.f ? 0.f : 1.f / den;  // a row that sees nothing is zero
-#pragma unroll
-            for (int k = 0; k < D / 64; ++k) {
-                const int col = w * (D / 2) + 32 * k;
-                float a[32];
-                if (warp_ok) {
+            ok = waited(pvd + 8 * ((t - 1) & 1), (uint32_t)(((t - 1) >> 1) & 1)) && ok;
+            tc_fence_after();
+            if (warp_ok) {
+#pragma unroll 1
+                for (int k = 0; k < D / 64; ++k) {
+                    const int col = w * (D / 2) + 32 * k;
+                    float a[32], b[32];
                     tmem_ld32(t_o + col, a);
-                    if (nt > 1) {
-                        float b[32];
-                        tmem_ld32(t_o + D + col, b);
+                    tmem_ld32(t_o + D + col, b);
+                    // an accumulator whose keys the row does not see holds nothing of it
 #pragma unroll
-                        for (int x = 0; x < 32; ++x) a[x] = f0 == 0.f ? b[x] * f1 : f1 == 0.f ? a[x] * f0 : a[x] * f0 + b[x] * f1;
-                    } else {
+                    for (int x = 0; x < 32; ++x) a[x] = f0 == 0.f ? b[x] * f1 : f1 == 0.f ? a[x] * f0 : a[x] * f0 + b[x] * f1;
+                    if (row_ok && ok) {
+                        if (!whole) {
+                            float4* dst = reinterpret_cast<float4*>(p.part_acc + ((size_t)part * kTRows + r) * D + col);
 #pragma unroll
-                        for (int x = 0; x < 32; ++x) a[x] *= f0;
-                    }
-                }
-                if (row_ok && ok) {
-                    if (!whole) {
-                        float4* dst = reinterpret_cast<float4*>(p.part_acc + ((size_t)part * kTRows + r) * D + col);
+                            for (int x = 0; x < 8; ++x) dst[x] = make_float4(a[4 * x], a[4 * x + 1], a[4 * x + 2], a[4 * x + 3]);
+                        } else {
 #pragma unroll
-                        for (int x = 0; x < 8; ++x) dst[x] = make_float4(a[4 * x], a[4 * x + 1], a[4 * x + 2], a[4 * x + 3]);
-                    } else if (p.out_dtype == PA_F32) {
-                        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + orow + col);
+                            for (int x = 0; x < 32; ++x) a[x] = den == 0.f ? 0.f : a[x] * inv;
+                            if (p.out_dtype == PA_F32) {
+                                float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + orow + col);
 #pragma unroll
-                        for (int x = 0; x < 8; ++x)
-                            dst[x] = den == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                                : make_float4(a[4 * x] * inv, a[4 * x + 1] * inv, a[4 * x + 2] * inv,
-                                                              a[4 * x + 3] * inv);
-                    } else {
-                        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + orow + col);
-                        uint32_t h[16];
+                                for (int x = 0; x < 8; ++x) dst[x] = make_float4(a[4 * x], a[4 * x + 1], a[4 * x + 2], a[4 * x + 3]);
+                            } else {
+                                uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + orow + col);
+                                uint32_t h[16];
 #pragma unroll
-                        for (int x = 0; x < 16; ++x) {
-                            const float lo = den == 0.f ? 0.f : a[2 * x] * inv, up = den == 0.f ? 0.f : a[2 * x + 1] * inv;
-                            h[x] = p.out_dtype == PA_BF16 ? Mma<__nv_bfloat16>::pack(lo, up) : Mma<__half>::pack(lo, up);
+                                for (int x = 0; x < 16; ++x)
+                                    h[x] = p.out_dtype == PA_BF16 ? Mma<__nv_bfloat16>::pack(a[2 * x], a[2 * x + 1])
+                                                                  : Mma<__half>::pack(a[2 * x], a[2 * x + 1]);
+#pragma unroll
+                                for (int x = 0; x < 4; ++x) dst[x] = make_uint4(h[4 * x], h[4 * x + 1], h[4 * x + 2], h[4 * x + 3]);
+                            }
                         }
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) dst[x] = make_uint4(h[4 * x], h[4 * x + 1], h[4 * x + 2], h[4 * x + 3]);
                     }
                 }
             }
@@ -796,8 +837,7 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                 reinterpret_cast<float2*>(p.part_ml)[(size_t)part * kTRows + r] = make_float2(M, den);
             if (tid == 0 && g.j0 == 0 && !whole)
                 p.desc[blockIdx.x] = make_int4(g.s, g.h, g.mt, (int)(1 + (g.nt - g.j1 + run.per - 1) / run.per));
-            tc_fence_before();
-            mbar_arrive(ofree);
+            tc_fence_before();  // O may be started afresh once this thread's next P is ready
         }
     }
     // Nothing issued may still be running when TMEM and shared memory are released: the tensor-core products (the MMA
@@ -814,6 +854,7 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                 for (int b = 0; b < NS && b < n; ++b)
                     mbar_wait_bounded((which ? vfull : kfull) + 8 * b, (uint32_t)(((n - 1 - b) / NS) & 1), nullptr);
             }
+            if (armed[2] > 0) mbar_wait_bounded(qfull, (uint32_t)((armed[2] - 1) & 1), nullptr);
         }
     }
     tc_fence_before();
@@ -907,12 +948,13 @@ size_t tree_workspace_bytes(int N, int H_q, int H_kv, int D, int max_q_len) {
 }
 
 template <typename T, int D, bool QUANT, bool SPLIT>
-static pa_status run_tree(const TreeParams& p, const CUtensorMap& tm, int ctas, cudaStream_t stream) {
+static pa_status run_tree(const TreeParams& p, const CUtensorMap& tm, const CUtensorMap& tm_q, int ctas,
+                          cudaStream_t stream) {
     using Geo = TreeGeo<D, QUANT>;
     auto kern = tree_kernel<T, D, QUANT, SPLIT>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Geo::kSmem);
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(tree)");
-    e = launch_kernel(kern, dim3(ctas), dim3(Geo::kThreads), Geo::kSmem, stream, tm, p);
+    e = launch_kernel(kern, dim3(ctas), dim3(Geo::kThreads), Geo::kSmem, stream, tm, tm_q, p);
     count_launch();
     if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
     e = launch_kernel(tree_merge_kernel<D>, dim3(ctas, (std::min(p.TQ, p.max_q_len) * p.G + 7) / 8), dim3(256), 0, stream, p);
@@ -921,14 +963,15 @@ static pa_status run_tree(const TreeParams& p, const CUtensorMap& tm, int ctas, 
 }
 
 template <int D>
-static pa_status dispatch_tree(const TreeArgs& a, const TreeParams& p, const CUtensorMap& tm, int ctas) {
+static pa_status dispatch_tree(const TreeArgs& a, const TreeParams& p, const CUtensorMap& tm, const CUtensorMap& tm_q,
+                               int ctas) {
     const bool f32 = a.out_dtype == PA_F32;
     if (a.scales)
-        return f32 ? run_tree<__half, D, true, true>(p, tm, ctas, a.stream)
-                   : run_tree<__half, D, true, false>(p, tm, ctas, a.stream);
-    if (a.q_dtype == PA_BF16) return run_tree<__nv_bfloat16, D, false, true>(p, tm, ctas, a.stream);
-    return f32 ? run_tree<__half, D, false, true>(p, tm, ctas, a.stream)
-               : run_tree<__half, D, false, false>(p, tm, ctas, a.stream);
+        return f32 ? run_tree<__half, D, true, true>(p, tm, tm_q, ctas, a.stream)
+                   : run_tree<__half, D, true, false>(p, tm, tm_q, ctas, a.stream);
+    if (a.q_dtype == PA_BF16) return run_tree<__nv_bfloat16, D, false, true>(p, tm, tm_q, ctas, a.stream);
+    return f32 ? run_tree<__half, D, false, true>(p, tm, tm_q, ctas, a.stream)
+               : run_tree<__half, D, false, false>(p, tm, tm_q, ctas, a.stream);
 }
 
 pa_status launch_tree(const TreeArgs& a) {
@@ -966,22 +1009,30 @@ pa_status launch_tree(const TreeArgs& a) {
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return cuda_fail(e, "device query");
     const int ctas = std::max(1, std::min(sms, kTreeMaxCtas));
-    CUtensorMap tm;
+    CUtensorMap tm, tm_q;
+    std::memset(&tm_q, 0, sizeof tm_q);
     pa_status st;
     if (a.scales) {
         st = quant_tensor_map(&tm, a.pool, a.NB, a.H_kv, a.B, a.D);
     } else {
+        const CUtensorMapDataType dt =
+            a.q_dtype == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+        // queries [T][H_q][D]: dims 64 columns, column half, head, token; box = a row tile's half
+        const cuuint64_t qd[4] = {64, (cuuint64_t)a.D / 64, (cuuint64_t)a.H_q, (cuuint64_t)a.T};
+        const cuuint64_t qs[3] = {128, (cuuint64_t)a.D * 2, (cuuint64_t)a.H_q * a.D * 2};
+        const cuuint32_t qb[4] = {64, 1, (cuuint32_t)p.G, (cuuint32_t)p.TQ};
+        st = encode_tensor_map(&tm_q, dt, 4, a.q, qd, qs, qb, CU_TENSOR_MAP_SWIZZLE_128B);
+        if (st != PA_OK) return st;
         // the pool [NB][B][2][H_kv][D]: dims 64 columns, token within a group of 8, column half, group of 8 tokens
         // (over all blocks), K/V x KV head; box = the K or V rows of one block and head
         const cuuint64_t dims[5] = {64, 8, (cuuint64_t)a.D / 64, (cuuint64_t)a.NB * a.B / 8, (cuuint64_t)2 * a.H_kv};
         const cuuint64_t str[4] = {(cuuint64_t)2 * a.H_kv * a.D * 2, 128, (cuuint64_t)8 * 2 * a.H_kv * a.D * 2,
                                    (cuuint64_t)a.D * 2};
         const cuuint32_t box[5] = {64, 8, (cuuint32_t)a.D / 64, (cuuint32_t)(a.B / 8), 1};
-        st = encode_tensor_map(&tm, a.q_dtype == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                               5, a.pool, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B);
+        st = encode_tensor_map(&tm, dt, 5, a.pool, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B);
     }
     if (st != PA_OK) return st;
-    return a.D == 128 ? dispatch_tree<128>(a, p, tm, ctas) : dispatch_tree<64>(a, p, tm, ctas);
+    return a.D == 128 ? dispatch_tree<128>(a, p, tm, tm_q, ctas) : dispatch_tree<64>(a, p, tm, tm_q, ctas);
 }
 
 }  // namespace pa
