@@ -22,7 +22,8 @@
 //
 // Quantised pool: query rows are scaled to fp16's range by a power of two (exact); K8 is converted to fp16 times 2^(ek -
 // emax + 7), emax the tile's largest exponent (a product is off by at most 2^-32 of the largest a key of the tile could
-// give), V8 exactly; y = raw c 2^(emax - 7) + ev, p = 2^(y - M), O += p V8, l += p 2^-ev, as in decode_quant.cu.
+// give), V8 likewise where that is exact (see kTreeSpan); with E the exponent taken out of V (per tile, else per key): y =
+// raw c 2^(emax - 7) + E, p = 2^(y - M), O += p (V 2^-E), l += p 2^-E, as in decode_quant.cu.
 #include <algorithm>
 #include <cstring>
 #include <type_traits>
@@ -41,6 +42,15 @@ constexpr int kTreeMaxCtas = 160;  // CTAs of a call at most (the workspace hold
 // Cost of a unit's start and end (query rows, first scores, joining the warpgroups, storing) in key tiles.
 constexpr int kTreeUnitCost = 3;
 constexpr int kConvWarps = 6;
+// Probabilities are relative to a reference kPHeadroom below the row's maximum, which may grow by 2^8 before O is
+// rescaled: they reach 2^15, the top of fp16's range, so that the smallest keep as many bits as fp16 allows (an absolute
+// 2^-25 is 2^-32 of the largest).
+constexpr float kPHeadroom = 7.f;
+// Quantised V: while the exponents of a tile's scales lie within kTreeSpan of one another, one exponent serves the tile
+// (V8 2^(ev - vmax + 7) is exact in fp16); otherwise (kTreeKeyed) each key's enters the scores.  With the headroom a
+// probability's absolute rounding then weighs no more than it does keyed, where the largest product is the reference.
+constexpr int kTreeSpan = 7;
+constexpr float kTreeKeyed = 1e30f;
 
 struct TreeParams {
     const void* q;
@@ -60,6 +70,18 @@ struct TreeParams {
     uint64_t wait_ns;
     int* err;
 };
+
+// Eight words to one 32-byte sector (32-byte aligned), or to two halves of one.
+__device__ __forceinline__ void st_words8(void* d, const uint32_t* v, bool sector) {
+    if (sector) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(d), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                     "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                     : "memory");
+    } else {
+        static_cast<uint4*>(d)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        static_cast<uint4*>(d)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    }
+}
 
 // ----------------------------------------------------------------------------- work distribution
 
@@ -249,7 +271,7 @@ struct TreeGeo {
                               oBar = oQe + (QUANT ? kTRows : 0);
     static constexpr int kBars = 4 + 4 * NS + 8 + 2 * NR;
     static constexpr uint32_t oSmall = oBar + 8 * kBars;
-    static constexpr size_t kSmem = oSmall + 32;
+    static constexpr size_t kSmem = oSmall + 48;
     static_assert(kSmem <= 232448, "shared memory");
     static_assert(8 * 40 <= kTile, "the Q tile's space also serves the start");
 };
@@ -279,6 +301,7 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     volatile int* armed = abort_flag + 1;  // K, V (quantised: raw) tiles and query tiles whose copies have been issued
     float* kmul = reinterpret_cast<float*>(tmem_slot + 5);  // per V slot: 2^(emax - 7) of the tile's K
+    float* vexp = kmul + NS;  // per V slot: exponent that its V was scaled down by, or kTreeKeyed
     int8_t* qexp = reinterpret_cast<int8_t*>(smem_raw + Geo::oQe);  // per query row: exponent it was scaled down by
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -438,24 +461,23 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                         if (more) issue_s(t + 1);
                         ok = ok && waited(vfull + 8 * slot(t), ph(t));
                         const uint32_t par = (uint32_t)((t >> 1) & 1), rdy = prdy + 16 * (t & 1);
-                        // a segment's first products start O_0 and O_1 afresh: both warpgroups have then read the last's
-                        if (j == g.j0) ok = ok && waited(rdy, par) && waited(rdy + 8, par);
-                        const uint64_t dv = umma_desc(sV + slot(t) * kTile, 1024, kGroup);
-#pragma unroll
-                        for (int w = 0; w < 2; ++w) {
-                            ok = ok && waited(rdy + 8 * w, par);
-                            if (!ok) break;
-                            tc_fence_after();
-                            const uint32_t oc = tmem + 2 * kTKeys + (uint32_t)w * D;
-#pragma unroll
-                            for (int ks = 0; ks < NT; ++ks) {
-                                const uint64_t vd = dv + (uint64_t)((w * NT + ks) * ((2 * kGroup) >> 4));
-                                const uint32_t pk = tmem + (uint32_t)(t & 1) * kTKeys + w * 64 + (ks >> 1) * 32 + (ks & 1) * 8;
-                                umma_f16_ta(oc, pk, vd, idesc_o, j > g.j0 || ks > 0);
-                                if (SPLIT) umma_f16_ta(oc, pk + 16, vd, idesc_o, 1u);
-                            }
-                        }
+                        // (both warpgroups ready also means that both have read the last segment's O)
+                        ok = ok && waited(rdy, par) && waited(rdy + 8, par);
                         if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t dv = umma_desc(sV + slot(t) * kTile, 1024, kGroup);
+                        // products of the two accumulators in turn: a product need not wait for the one before it
+#pragma unroll
+                        for (int ks = 0; ks < NT; ++ks) {
+#pragma unroll
+                            for (int part = 0; part < (SPLIT ? 2 : 1); ++part)
+#pragma unroll
+                                for (int w = 0; w < 2; ++w)
+                                    umma_f16_ta(tmem + 2 * kTKeys + (uint32_t)w * D,
+                                                tmem + (uint32_t)(t & 1) * kTKeys + w * 64 + (ks >> 1) * 32 + (ks & 1) * 8 + part * 16,
+                                                dv + (uint64_t)((w * NT + ks) * ((2 * kGroup) >> 4)), idesc_o,
+                                                j > g.j0 || ks > 0 || part > 0);
+                        }
                         umma_commit(pvd + 8 * (t & 1));
                         umma_commit(vfree + 8 * slot(t));
                     }
@@ -467,8 +489,14 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
             // -------------------------------------------------------- converters (quantised pool)
             if constexpr (QUANT) {
                 const int cw = warp - 10;
-                constexpr int L = D / 16;                // 16-byte pieces of a row
-                constexpr int kSteps = kTKeys * L / 32;  // warp steps of a tile
+                // A warp converts groups of 8 rows, P rows at a time: a lane reads 8 values (of piece `pc` of row `pr`)
+                // and writes 16 bytes.  Both sides are swizzled by the row's place in its group.
+                constexpr int P = 256 / D, L = D / 8;    // rows per step, lanes per row
+                const int pc = lane % L, pr = lane / L;
+                const uint32_t so = D == 128 ? pr * 128 + (((pc >> 1) ^ pr) << 4) + (pc & 1) * 8
+                                             : pr * 64 + (((pc >> 1) ^ (pr >> 1)) << 4) + (pc & 1) * 8;
+                const uint32_t to = (uint32_t)(pc >> 3) * 1024 + pr * 128 + (((pc & 7) ^ pr) << 4);
+                const int mb = ~(B - 1);
                 int t = 0;
                 for (int seg = 0; walk.next(p, g); ++seg) {
                     // the query rows as fp16, four lanes to a row, once the last segment's have been used
@@ -533,79 +561,79 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                         const uint32_t rb = (uint32_t)(t % NR);
                         const uint32_t raw = sb + Geo::oRaw + rb * Geo::kRaw, rsc = sb + Geo::oRawSc + rb * Geo::kRawScales;
                         uint32_t u[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
-                        if (k0 + kTKeys > g.ctx - g.n) tree_union<4>(p, g, k0, u);  // keys past the context are in none
+                        const bool masked = k0 + kTKeys > g.ctx - g.n;
+                        if (masked) tree_union<4>(p, g, k0, u);  // keys past the context are in none
                         ok = waited(rfull + 8 * rb, (uint32_t)((t / NR) & 1)) && ok;
-                        // lane: keys 4 lane .. + 3, all of one block
-                        const uint32_t at = ((uint32_t)(4 * lane) >> p.lgB) * 2 * B + ((4 * lane) & (B - 1));
-                        uint32_t kb;
-                        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(kb) : "r"(rsc + at));
-                        int em = kScaleMin;
+                        // lane: keys 4 lane .. + 3, all of one block; the largest exponents of the keys that are seen
+                        const uint32_t at = rsc + 4 * lane + ((4 * lane) & mb);
+                        uint32_t kb, vb;
+                        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(kb) : "r"(at));
+                        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(vb) : "r"(at + B));
+                        int em = kScaleMin, vm = kScaleMin, vl = kScaleMax;
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            if (u[lane >> 3] >> ((4 * lane + i) & 31) & 1u) em = max(em, scale_of((kb >> 8 * i) & 255));
+                            if (u[lane >> 3] >> ((4 * lane + i) & 31) & 1u) {
+                                em = max(em, scale_of((kb >> 8 * i) & 255));
+                                vm = max(vm, scale_of((vb >> 8 * i) & 255));
+                                vl = min(vl, scale_of((vb >> 8 * i) & 255));
+                            }
                         em = __reduce_max_sync(0xffffffffu, em);
+                        vm = __reduce_max_sync(0xffffffffu, vm);
+                        vl = __reduce_min_sync(0xffffffffu, vl);
+                        const bool keyed = vm - vl > kTreeSpan;
                         const uint32_t sl = slot(t);
-                        // K, then V; piece x: row x / L, 16 elements from 16 (x % L) on
                         for (int which = 0; which < 2; ++which) {
                             if (t >= NS) ok = waited((which ? vfree : kfree) + 8 * sl, ph(t - NS)) && ok;
-                            const uint32_t dst = (which ? sV : sK) + sl * kTile;
-                            for (int st = cw; st < kSteps; st += kConvWarps) {
-                                const int x = st * 32 + lane, r = x / L, c = x % L;
-                                const uint32_t blk = (uint32_t)r >> p.lgB, in = r & (B - 1);
-                                const uint32_t rr = (which ? B : 0) + in;  // row of the block's chunk, swizzled by TMA
-                                const uint32_t src = raw + blk * 2 * B * D + rr * D +
-                                                     (D == 128 ? ((c ^ (rr & 7)) << 4) : ((c ^ (rr >> 1 & 3)) << 4));
-                                uint4 v;
-                                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                             : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                                             : "r"(src));
-                                const bool seen = u[r >> 5] >> (r & 31) & 1u;
-                                uint32_t h[8] = {e4m3x2_to_f16x2(v.x), e4m3x2_to_f16x2(v.x >> 16), e4m3x2_to_f16x2(v.y),
-                                                 e4m3x2_to_f16x2(v.y >> 16), e4m3x2_to_f16x2(v.z),
-                                                 e4m3x2_to_f16x2(v.z >> 16), e4m3x2_to_f16x2(v.w),
-                                                 e4m3x2_to_f16x2(v.w >> 16)};
-                                if (which == 0) {
-                                    uint32_t b;
-                                    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(b) : "r"(rsc + blk * 2 * B + in));
-                                    const __half2 f = __float2half2_rn(pow2i(scale_of((int)b) - em + 7));
+                            const uint32_t dst = (which ? sV : sK) + sl * kTile + to, src0 = raw + so + (which ? B * D : 0);
+                            const int e0 = which ? (keyed ? 0 : vm) : em;
+                            const bool plain = which && keyed;  // V8 as it is
+                            for (int gr = cw; gr < kTKeys / 8; gr += kConvWarps) {
+                                const uint32_t row0 = 8 * gr + ((8 * gr) & mb);
+                                const uint32_t src = src0 + row0 * D, d = dst + gr * kGroup;
+                                uint2 v[8 / P], sc8;
+                                asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                                             : "=r"(sc8.x), "=r"(sc8.y)
+                                             : "r"(rsc + row0 + (which ? B : 0)));
 #pragma unroll
-                                    for (int i = 0; i < 8; ++i) {
-                                        const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&h[i]), f);
-                                        h[i] = *reinterpret_cast<const uint32_t*>(&y);
+                                for (int i = 0; i < 8 / P; ++i)
+                                    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                                                 : "=r"(v[i].x), "=r"(v[i].y)
+                                                 : "r"((src ^ (D == 128 ? (P * i) << 4 : (P * i / 2) << 4)) + P * i * D));
+                                const uint32_t seen = u[gr >> 2] >> (8 * (gr & 3));
+#pragma unroll
+                                for (int i = 0; i < 8 / P; ++i) {
+                                    const int row = P * i + pr;  // of the group
+                                    const uint32_t byte = (P * i < 4 ? sc8.x : sc8.y) >> (8 * (row & 3)) & 255u;
+                                    uint32_t h[4] = {e4m3x2_to_f16x2(v[i].x), e4m3x2_to_f16x2(v[i].x >> 16),
+                                                     e4m3x2_to_f16x2(v[i].y), e4m3x2_to_f16x2(v[i].y >> 16)};
+                                    const __half2 f = __float2half2_rn(plain ? 1.f : pow2i(scale_of((int)byte) - e0 + 7));
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k) {
+                                        const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&h[k]), f);
+                                        h[k] = *reinterpret_cast<const uint32_t*>(&y);
                                     }
-                                }
-                                // rows nobody sees, past the context or padding, may hold anything: zeros
-                                if (!seen) {
-#pragma unroll
-                                    for (int i = 0; i < 8; ++i) h[i] = 0u;
-                                }
-                                // 16-byte pieces 2 c and 2 c + 1 of the row (8 per column half); half the lanes store
-                                // them in the other order, which spreads a quarter warp's stores over all banks
-                                const uint32_t row = dst + (uint32_t)(r >> 3) * kGroup + (uint32_t)(c >> 2) * 1024 + (r & 7) * 128;
-                                const uint32_t flip = D == 128 ? (lane >> 2 & 1) : 0;
-#pragma unroll
-                                for (int o = 0; o < 2; ++o) {
-                                    const uint32_t oo = o ^ flip;
-                                    const uint32_t a = row + ((((c & 3) * 2 + oo) ^ (r & 7)) << 4);
-                                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a),
-                                                 "r"(oo ? h[4] : h[0]), "r"(oo ? h[5] : h[1]), "r"(oo ? h[6] : h[2]),
-                                                 "r"(oo ? h[7] : h[3])
+                                    // rows nobody sees, past the context or padding, may hold anything: zeros
+                                    if (masked && !(seen >> row & 1u)) h[0] = h[1] = h[2] = h[3] = 0u;
+                                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                                     (d ^ ((P * i) << 4)) + P * i * 128),
+                                                 "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
                                                  : "memory");
                                 }
                             }
-                            if (which) {
+                            if (which && keyed) {
                                 uint32_t* ex = reinterpret_cast<uint32_t*>(smem_raw + Geo::oExp + sl * Geo::kExp);
                                 const int key = cw * 32 + lane;
                                 if (key < kTKeys) {
                                     uint32_t b;
-                                    asm volatile("ld.shared.u8 %0, [%1];"
-                                                 : "=r"(b)
-                                                 : "r"(rsc + ((uint32_t)key >> p.lgB) * 2 * B + B + (key & (B - 1))));
+                                    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(b) : "r"(rsc + key + (key & mb) + B));
                                     const int ev = scale_of((int)b);
                                     // both exact in bf16: the upper halves of the fp32 values
                                     ex[key] = __float_as_uint((float)ev) >> 16 | (__float_as_uint(pow2i(-ev)) & 0xffff0000u);
                                 }
-                                if (cw == 0 && lane == 0) kmul[sl] = pow2i(em - 7);
+                            }
+                            if (which && cw == 0 && lane == 0) {
+                                kmul[sl] = pow2i(em - 7);
+                                vexp[sl] = keyed ? kTreeKeyed : (float)(vm - 7);
                             }
                             fence_proxy_async_smem();
                             __syncwarp();
@@ -653,7 +681,10 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                         if (lane == 0) mbar_arrive(qread);
                     }
                 }
-                if (warp_ok) {
+                float alpha = 1.f;
+                // kKeyed: every key has an exponent of its own (else E is the tile's)
+                auto probabilities = [&](auto keyed_c, float E) {
+                    constexpr bool kKeyed = decltype(keyed_c)::value;
                     uint32_t s[2][32];
                     tmem_ld32_async(t_s, s[0]);
                     tmem_ld32_async(t_s + 32, s[1]);
@@ -662,11 +693,11 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                     const uint32_t ex = sb + Geo::oExp + slot(t) * Geo::kExp + 4 * 64 * w;
                     const float mul = QUANT ? cr * kmul[slot(t)] : cr;
                     const float2 mul2 = make_float2(mul, mul);
-                    float y[64];  // 16-bit pool: raw scores; quantised: y
+                    float y[64];  // raw scores; kKeyed: y
 #pragma unroll
                     for (int k = 0; k < 64; k += 4) {
                         const uint32_t* x = &s[k >> 5][k & 31];
-                        if constexpr (QUANT) {
+                        if constexpr (kKeyed) {
                             uint32_t e[4];
                             asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                                          : "=r"(e[0]), "=r"(e[1]), "=r"(e[2]), "=r"(e[3])
@@ -696,12 +727,12 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                         mx[3] = fmax3(mx[3], y[k + 6], y[k + 7]);
                     }
                     float m_tile = fmax3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
-                    if (!QUANT) m_tile *= mul;  // (the scale is positive)
+                    m_tile = (kKeyed ? m_tile : fmaf(m_tile, mul, E)) - kPHeadroom;  // (the scale is positive)
                     const float m_new = m_tile > m_ref + 8.f || m_ref == NEG_INF ? fmaxf(m_ref, m_tile) : m_ref;
-                    const float alpha = j == g.j0 || m_new == m_ref ? 1.f : fast_exp2(m_ref - m_new);
+                    if (j > g.j0 && m_new != m_ref) alpha = fast_exp2(m_ref - m_new);
                     m_ref = m_new;
-                    const float m_use = m_new == NEG_INF ? 0.f : m_new;
-                    const float2 nm2 = make_float2(-m_use, -m_use);
+                    const float off = (kKeyed ? 0.f : E) - (m_new == NEG_INF ? 0.f : m_new);
+                    const float2 off2 = make_float2(off, off);
                     // P of 32 keys goes over their scores: 16 columns of pairs, and (SPLIT) the low parts in the next 16
                     float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -710,18 +741,18 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
 #pragma unroll
                         for (int b = 0; b < 32; b += 4) {
                             uint32_t e[4];
-                            if constexpr (QUANT)
+                            if constexpr (kKeyed)
                                 asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                                              : "=r"(e[0]), "=r"(e[1]), "=r"(e[2]), "=r"(e[3])
                                              : "r"(ex + 4 * (32 * k + b)));
 #pragma unroll
                             for (int i = 0; i < 4; i += 2) {
                                 const float2 yy = make_float2(y[32 * k + b + i], y[32 * k + b + i + 1]);
-                                float2 x = QUANT ? fadd2(yy, nm2) : ffma2(yy, mul2, nm2);
+                                float2 x = kKeyed ? fadd2(yy, off2) : ffma2(yy, mul2, off2);
                                 x.x = fast_exp2(x.x);
                                 x.y = fast_exp2(x.y);
                                 float2& acc = ls[(i >> 1) & 1];
-                                if constexpr (QUANT)
+                                if constexpr (kKeyed)
                                     acc = ffma2(x, make_float2(__uint_as_float(e[i] & 0xffff0000u), __uint_as_float(e[i + 1] & 0xffff0000u)), acc);
                                 else
                                     acc = fadd2(acc, x);
@@ -737,7 +768,20 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                         if (SPLIT) tmem_st16(t_s + k * 32 + 16, lo);
                     }
                     const float2 lsum = fadd2(ls[0], ls[1]);
-                    l = fmaf(l, alpha, lsum.x + lsum.y);
+                    float sum = lsum.x + lsum.y;
+                    if (QUANT && !kKeyed) sum *= pow2i(-(int)E);
+                    l = fmaf(l, alpha, sum);
+                };
+                if (warp_ok) {
+                    if constexpr (QUANT) {
+                        const float E = vexp[slot(t)];
+                        if (E == kTreeKeyed)
+                            probabilities(std::true_type{}, 0.f);
+                        else
+                            probabilities(std::false_type{}, E);
+                    } else {
+                        probabilities(std::false_type{}, 0.f);
+                    }
                     // O_w is rescaled (rarely) once the last tile's products have landed
                     if (__any_sync(0xffffffffu, alpha != 1.f)) {
                         ok = waited(pvd + 8 * ((t - 1) & 1), (uint32_t)(((t - 1) >> 1) & 1)) && ok;
@@ -808,27 +852,26 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
 #pragma unroll
                     for (int x = 0; x < 32; ++x) a[x] = f0 == 0.f ? b[x] * f1 : f1 == 0.f ? a[x] * f0 : a[x] * f0 + b[x] * f1;
                     if (row_ok && ok) {
-                        if (!whole) {
-                            float4* dst = reinterpret_cast<float4*>(p.part_acc + ((size_t)part * kTRows + r) * D + col);
+                        // (whole 32-byte sectors per lane where `out` allows: half the store instructions)
+                        uint32_t h[32];
+                        const bool sector = !whole || (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
+                        if (!whole || p.out_dtype == PA_F32) {
+                            const float f = whole ? inv : 1.f;
 #pragma unroll
-                            for (int x = 0; x < 8; ++x) dst[x] = make_float4(a[4 * x], a[4 * x + 1], a[4 * x + 2], a[4 * x + 3]);
+                            for (int x = 0; x < 32; ++x) h[x] = __float_as_uint(whole && den == 0.f ? 0.f : a[x] * f);
+                            float* dst = whole ? static_cast<float*>(p.out) + orow + col
+                                               : p.part_acc + ((size_t)part * kTRows + r) * D + col;
+#pragma unroll
+                            for (int x = 0; x < 32; x += 8) st_words8(dst + x, h + x, sector);
                         } else {
 #pragma unroll
-                            for (int x = 0; x < 32; ++x) a[x] = den == 0.f ? 0.f : a[x] * inv;
-                            if (p.out_dtype == PA_F32) {
-                                float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + orow + col);
-#pragma unroll
-                                for (int x = 0; x < 8; ++x) dst[x] = make_float4(a[4 * x], a[4 * x + 1], a[4 * x + 2], a[4 * x + 3]);
-                            } else {
-                                uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + orow + col);
-                                uint32_t h[16];
-#pragma unroll
-                                for (int x = 0; x < 16; ++x)
-                                    h[x] = p.out_dtype == PA_BF16 ? Mma<__nv_bfloat16>::pack(a[2 * x], a[2 * x + 1])
-                                                                  : Mma<__half>::pack(a[2 * x], a[2 * x + 1]);
-#pragma unroll
-                                for (int x = 0; x < 4; ++x) dst[x] = make_uint4(h[4 * x], h[4 * x + 1], h[4 * x + 2], h[4 * x + 3]);
+                            for (int x = 0; x < 16; ++x) {
+                                const float lo = den == 0.f ? 0.f : a[2 * x] * inv, up = den == 0.f ? 0.f : a[2 * x + 1] * inv;
+                                h[x] = p.out_dtype == PA_BF16 ? Mma<__nv_bfloat16>::pack(lo, up) : Mma<__half>::pack(lo, up);
                             }
+                            uint16_t* dst = static_cast<uint16_t*>(p.out) + orow + col;
+#pragma unroll
+                            for (int x = 0; x < 16; x += 8) st_words8(dst + 2 * x, h + x, sector);
                         }
                     }
                 }
