@@ -11,12 +11,11 @@
 // A CTA leaves at most two (its first and its last segment), so the workspace has a fixed size.  Roles:
 //   * warps 0-3 and 4-7, two softmax warpgroups: warpgroup w takes keys 64 w .. 64 w + 63 of every tile; each thread owns
 //     one TMEM lane = one query row.  It reads its 64 scores (tcgen05.ld), masks, keeps a running maximum of its own
-//     (its O is rescaled only when that grows by more than 2^8) and writes the probabilities over the scores.  The
-//     warpgroups have accumulators of their own, O_0 and O_1, joined at the segment's end, so they never wait for one
+//     (its O is rescaled only when that grows by more than 2^8) and writes the probabilities to TMEM.  The warpgroups have accumulators of their own, O_0 and O_1, joined at the segment's end, so they never wait for one
 //     another in between;
 //   * warp 8 (TMA): query rows (16-bit pool), K and V tiles into rings, block by block through the block table;
-//   * warp 9 (MMA, one thread): S = Q K^T of the next tile (TMEM columns 128 (t & 1)) while the softmax works on this
-//     one, then O_w += P_w V (columns 256 + D w), P read from TMEM;
+//   * warp 9 (MMA, one thread): S = Q K^T (TMEM columns 0 .. 127) of the next tile as soon as the softmax has read this
+//     one's into registers, then O_w += P_w V (columns 256 + D w), P read from TMEM (columns 128 .. 255);
 //   * quantised pool, warps 10-15: e4m3 tiles from the raw ring to fp16 tiles in the K and V rings, and the query rows.
 // The value product takes P in V's 16-bit type: for bf16, or an fp32 output, as a high and a low part (two products).
 //
@@ -269,7 +268,7 @@ struct TreeGeo {
     static constexpr uint32_t oK = kTile, oV = oK + NS * kTile, oRaw = oV + NS * kTile, oRawSc = oRaw + NR * kRaw,
                               oExp = oRawSc + NR * kRawScales, oXch = oExp + NS * kExp, oQe = oXch + 2 * kTRows * 4,
                               oBar = oQe + (QUANT ? kTRows : 0);
-    static constexpr int kBars = 4 + 4 * NS + 8 + 2 * NR;
+    static constexpr int kBars = 4 + 4 * NS + 5 + 2 * NR;
     static constexpr uint32_t oSmall = oBar + 8 * kBars;
     static constexpr size_t kSmem = oSmall + 48;
     static_assert(kSmem <= 232448, "shared memory");
@@ -292,11 +291,11 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t sb = smem_addr(smem_raw);
     const uint32_t sQ = sb, sK = sb + Geo::oK, sV = sb + Geo::oV, sBar = sb + Geo::oBar;
-    // prdy: per S buffer and warpgroup; sfull, pvd: per S buffer
+    // prdy: one per warpgroup
     const uint32_t qfull = sBar, qfree = qfull + 8, qread = qfree + 8, mmadone = qread + 8,
                    kfull = mmadone + 8, kfree = kfull + 8 * NS,
-                   vfull = kfree + 8 * NS, vfree = vfull + 8 * NS, sfull = vfree + 8 * NS, pvd = sfull + 16,
-                   prdy = pvd + 16, rfull = prdy + 32, rfree = rfull + 8 * NR;
+                   vfull = kfree + 8 * NS, vfree = vfull + 8 * NS, sfull = vfree + 8 * NS, sfree = sfull + 8,
+                   pvd = sfree + 8, prdy = pvd + 8, rfull = prdy + 16, rfree = rfull + 8 * NR;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_raw + Geo::oSmall);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     volatile int* armed = abort_flag + 1;  // K, V (quantised: raw) tiles and query tiles whose copies have been issued
@@ -325,7 +324,9 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
     }
     if (tid == 0) {
         for (int i = 0; i < Geo::kBars; ++i) mbar_init(sBar + 8 * i, 1);
-        for (int i = 0; i < 4; ++i) mbar_init(prdy + 8 * i, 128);
+        mbar_init(sfree, 8);  // one arrival per softmax warp
+        mbar_init(prdy, 128);
+        mbar_init(prdy + 8, 128);
         if (QUANT) {
             mbar_init(qfull, kConvWarps);
             mbar_init(qread, 8);
@@ -436,17 +437,16 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                 js = gs.j0;
                 auto issue_s = [&](int t) {
                     if (js == gs.j0) ok = waited(qfull, (uint32_t)(++segs & 1));
-                    // the buffer is free once the value products have read the P that lay there
-                    ok = ok && (t < 2 || waited(pvd + 8 * (t & 1), (uint32_t)((t / 2 - 1) & 1))) &&
-                         waited(kfull + 8 * slot(t), ph(t));
+                    // S is free once the softmax has read the last tile's into registers
+                    ok = ok && (t == 0 || waited(sfree, (uint32_t)((t - 1) & 1))) && waited(kfull + 8 * slot(t), ph(t));
                     if (!ok) return;
                     tc_fence_after();
                     const uint64_t dk = umma_desc(sK + slot(t) * kTile, 16, kGroup);
 #pragma unroll
                     for (int ks = 0; ks < NK; ++ks)
-                        umma_f16(tmem + (uint32_t)(t & 1) * kTKeys, dq + (ks >> 2) * (kTRegion >> 4) + (ks & 3) * 2,
+                        umma_f16(tmem, dq + (ks >> 2) * (kTRegion >> 4) + (ks & 3) * 2,
                                  dk + (ks >> 2) * (1024 >> 4) + (ks & 3) * 2, idesc_s, ks > 0);
-                    umma_commit(sfull + 8 * (t & 1));
+                    umma_commit(sfull);
                     umma_commit(kfree + 8 * slot(t));
                     if (++js == gs.j1) {
                         umma_commit(qfree);
@@ -460,9 +460,9 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                     for (int j = g.j0; j < g.j1 && ok; ++j, ++t) {
                         if (more) issue_s(t + 1);
                         ok = ok && waited(vfull + 8 * slot(t), ph(t));
-                        const uint32_t par = (uint32_t)((t >> 1) & 1), rdy = prdy + 16 * (t & 1);
+                        const uint32_t par = (uint32_t)(t & 1);
                         // (both warpgroups ready also means that both have read the last segment's O)
-                        ok = ok && waited(rdy, par) && waited(rdy + 8, par);
+                        ok = ok && waited(prdy, par) && waited(prdy + 8, par);
                         if (!ok) break;
                         tc_fence_after();
                         const uint64_t dv = umma_desc(sV + slot(t) * kTile, 1024, kGroup);
@@ -474,11 +474,11 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
 #pragma unroll
                                 for (int w = 0; w < 2; ++w)
                                     umma_f16_ta(tmem + 2 * kTKeys + (uint32_t)w * D,
-                                                tmem + (uint32_t)(t & 1) * kTKeys + w * 64 + (ks >> 1) * 32 + (ks & 1) * 8 + part * 16,
+                                                tmem + kTKeys + w * 64 + (ks >> 1) * 32 + (ks & 1) * 8 + part * 16,
                                                 dv + (uint64_t)((w * NT + ks) * ((2 * kGroup) >> 4)), idesc_o,
                                                 j > g.j0 || ks > 0 || part > 0);
                         }
-                        umma_commit(pvd + 8 * (t & 1));
+                        umma_commit(pvd);
                         umma_commit(vfree + 8 * slot(t));
                     }
                 }
@@ -499,20 +499,29 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                 const int mb = ~(B - 1);
                 int t = 0;
                 for (int seg = 0; walk.next(p, g); ++seg) {
-                    // the query rows as fp16, four lanes to a row, once the last segment's have been used
-                    if (seg > 0) {
-                        ok = waited(qfree, (uint32_t)((seg - 1) & 1)) && ok;
-                        ok = waited(qread, (uint32_t)((seg - 1) & 1)) && ok;
-                    }
+                    // the query rows as fp16, four lanes to a row: read, then written once the last segment's have been used
                     {
-                        constexpr int C = D / 32;  // 16-byte pieces of a row per lane
+                        constexpr int C = D / 32;                                     // 16-byte pieces of a row per lane
+                        constexpr int R = (kTRows / 8 + kConvWarps - 1) / kConvWarps;  // rows per lane
                         const int tok0 = g.mt * p.TQ, rows = min(p.TQ, g.n - tok0) * p.G;
-                        for (int r = cw * 8 + (lane >> 2); r < kTRows; r += 8 * kConvWarps) {
-                            uint4 x[C];
+                        uint4 xs[R][C];
+#pragma unroll
+                        for (int k = 0; k < R; ++k) {
+                            const int r = (cw + k * kConvWarps) * 8 + (lane >> 2);
                             const size_t row = ((size_t)(g.qs + tok0 + r / p.G) * p.H_q + (size_t)g.h * p.G + r % p.G) * D;
                             const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + row);
 #pragma unroll
-                            for (int i = 0; i < C; ++i) x[i] = r < rows ? src[4 * i + (lane & 3)] : make_uint4(0, 0, 0, 0);
+                            for (int i = 0; i < C; ++i) xs[k][i] = r < rows ? src[4 * i + (lane & 3)] : make_uint4(0, 0, 0, 0);
+                        }
+                        if (seg > 0) {
+                            ok = waited(qfree, (uint32_t)((seg - 1) & 1)) && ok;
+                            ok = waited(qread, (uint32_t)((seg - 1) & 1)) && ok;
+                        }
+#pragma unroll
+                        for (int k = 0; k < R; ++k) {
+                            const int r = (cw + k * kConvWarps) * 8 + (lane >> 2);
+                            if (r >= kTRows) break;  // uniform over the warp
+                            uint4 (&x)[C] = xs[k];
                             int e = 0;
                             if (p.q_bf16) {
                                 float a = 0.f;
@@ -525,9 +534,8 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                                         a = fmaxf(a, fmaxf(fabsf(f.x), fabsf(f.y)));
                                     }
                                 }
-                                const unsigned quad = 0xfu << (lane & 28);
-                                a = fmaxf(a, __shfl_xor_sync(quad, a, 1));
-                                a = fmaxf(a, __shfl_xor_sync(quad, a, 2));
+                                a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+                                a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
                                 // largest magnitude to [2^14, 2^15), as in decode_quant.cu
                                 const int ex = (int)(__float_as_uint(a) >> 23) - 127;
                                 e = ex > 127 || a == 0.f ? 0 : max(ex - 14, -126);
@@ -570,9 +578,10 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                         asm volatile("ld.shared.u32 %0, [%1];" : "=r"(kb) : "r"(at));
                         asm volatile("ld.shared.u32 %0, [%1];" : "=r"(vb) : "r"(at + B));
                         int em = kScaleMin, vm = kScaleMin, vl = kScaleMax;
+                        const uint32_t mine = u[lane >> 3] >> (4 * lane & 31);  // bit i: key 4 lane + i is seen
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            if (u[lane >> 3] >> ((4 * lane + i) & 31) & 1u) {
+                            if (mine >> i & 1u) {
                                 em = max(em, scale_of((kb >> 8 * i) & 255));
                                 vm = max(vm, scale_of((vb >> 8 * i) & 255));
                                 vl = min(vl, scale_of((vb >> 8 * i) & 255));
@@ -581,39 +590,57 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                         vm = __reduce_max_sync(0xffffffffu, vm);
                         vl = __reduce_min_sync(0xffffffffu, vl);
                         const bool keyed = vm - vl > kTreeSpan;
+                        // fp16 factors of this lane's four keys, K's and V's (V8 as it is when keyed)
+                        uint32_t fk[2], fv[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            // (a key that nobody sees may lie above the largest: its factor is kept finite)
+                            const int k0_ = min(scale_of((kb >> 16 * i) & 255) - em, 0) + 7, k1_ = min(scale_of((kb >> (16 * i + 8)) & 255) - em, 0) + 7;
+                            const int v0_ = min(scale_of((vb >> 16 * i) & 255) - vm, 0) + 7, v1_ = min(scale_of((vb >> (16 * i + 8)) & 255) - vm, 0) + 7;
+                            fk[i] = Mma<__half>::pack(pow2i(k0_), pow2i(k1_));
+                            fv[i] = keyed ? 0x3c003c00u : Mma<__half>::pack(pow2i(v0_), pow2i(v1_));
+                        }
                         const uint32_t sl = slot(t);
                         for (int which = 0; which < 2; ++which) {
                             if (t >= NS) ok = waited((which ? vfree : kfree) + 8 * sl, ph(t - NS)) && ok;
                             const uint32_t dst = (which ? sV : sK) + sl * kTile + to, src0 = raw + so + (which ? B * D : 0);
-                            const int e0 = which ? (keyed ? 0 : vm) : em;
-                            const bool plain = which && keyed;  // V8 as it is
                             for (int gr = cw; gr < kTKeys / 8; gr += kConvWarps) {
                                 const uint32_t row0 = 8 * gr + ((8 * gr) & mb);
                                 const uint32_t src = src0 + row0 * D, d = dst + gr * kGroup;
-                                uint2 v[8 / P], sc8;
-                                asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
-                                             : "=r"(sc8.x), "=r"(sc8.y)
-                                             : "r"(rsc + row0 + (which ? B : 0)));
+                                uint2 v[8 / P];
 #pragma unroll
                                 for (int i = 0; i < 8 / P; ++i)
                                     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
                                                  : "=r"(v[i].x), "=r"(v[i].y)
                                                  : "r"((src ^ (D == 128 ? (P * i) << 4 : (P * i / 2) << 4)) + P * i * D));
-                                const uint32_t seen = u[gr >> 2] >> (8 * (gr & 3));
+                                if (masked) {  // rows nobody sees, past the context or padding, may hold anything: zeros
+                                    const uint32_t seen = u[gr >> 2] >> (8 * (gr & 3));
+#pragma unroll
+                                    for (int i = 0; i < 8 / P; ++i)
+                                        if (!(seen >> (P * i + pr) & 1u)) v[i] = make_uint2(0u, 0u);
+                                }
 #pragma unroll
                                 for (int i = 0; i < 8 / P; ++i) {
-                                    const int row = P * i + pr;  // of the group
-                                    const uint32_t byte = (P * i < 4 ? sc8.x : sc8.y) >> (8 * (row & 3)) & 255u;
+                                    // row P i + pr of the group: its factor lies with lane 2 gr + row / 4
+                                    const int from = 2 * gr + (P * i) / 4;
+                                    uint32_t f2;
+                                    if constexpr (P == 2) {
+                                        f2 = __shfl_sync(0xffffffffu, which ? fv[i & 1] : fk[i & 1], from);
+                                        f2 = __byte_perm(f2, f2, pr ? 0x3232 : 0x1010);
+                                    } else {
+                                        const uint32_t f01 = __shfl_sync(0xffffffffu, which ? fv[0] : fk[0], from);
+                                        const uint32_t f23 = __shfl_sync(0xffffffffu, which ? fv[1] : fk[1], from);
+                                        f2 = pr & 2 ? f23 : f01;
+                                        f2 = __byte_perm(f2, f2, pr & 1 ? 0x3232 : 0x1010);
+                                    }
                                     uint32_t h[4] = {e4m3x2_to_f16x2(v[i].x), e4m3x2_to_f16x2(v[i].x >> 16),
                                                      e4m3x2_to_f16x2(v[i].y), e4m3x2_to_f16x2(v[i].y >> 16)};
-                                    const __half2 f = __float2half2_rn(plain ? 1.f : pow2i(scale_of((int)byte) - e0 + 7));
 #pragma unroll
                                     for (int k = 0; k < 4; ++k) {
-                                        const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&h[k]), f);
+                                        const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&h[k]),
+                                                                  *reinterpret_cast<const __half2*>(&f2));
                                         h[k] = *reinterpret_cast<const uint32_t*>(&y);
                                     }
-                                    // rows nobody sees, past the context or padding, may hold anything: zeros
-                                    if (masked && !(seen >> row & 1u)) h[0] = h[1] = h[2] = h[3] = 0u;
                                     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
                                                      (d ^ ((P * i) << 4)) + P * i * 128),
                                                  "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
@@ -663,15 +690,15 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
             float m_ref = NEG_INF, l = 0.f;
             for (int j = g.j0; j < g.j1; ++j, ++t) {
                 const int k0 = j * kTKeys + 64 * w;  // the warpgroup's first key
-                const uint32_t par = (uint32_t)((t >> 1) & 1);
-                const uint32_t t_s = lanes + (uint32_t)(t & 1) * kTKeys + (uint32_t)w * 64;
+                const uint32_t par = (uint32_t)(t & 1);
+                const uint32_t t_s = lanes + (uint32_t)w * 64, t_p = t_s + kTKeys;
                 const bool masked = k0 + 64 > base;
                 uint32_t vis[2] = {0u, 0u};
                 if (masked && row_ok) {
 #pragma unroll
                     for (int k = 0; k < 2; ++k) vis[k] = tree_visible(p, g, tok, k0 + 32 * k - base);
                 }
-                ok = waited(sfull + 8 * (t & 1), par) && ok;
+                ok = waited(sfull, par) && ok;
                 tc_fence_after();
                 if (QUANT) {
                     ok = waited(vfull + 8 * slot(t), ph(t)) && ok;  // the tile's exponents
@@ -690,6 +717,8 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                     tmem_ld32_async(t_s + 32, s[1]);
                     tmem_loaded(s[0]);
                     tmem_loaded(s[1]);
+                    tc_fence_before();
+                    if (lane == 0) mbar_arrive(sfree);  // (each load is the whole warp's)
                     const uint32_t ex = sb + Geo::oExp + slot(t) * Geo::kExp + 4 * 64 * w;
                     const float mul = QUANT ? cr * kmul[slot(t)] : cr;
                     const float2 mul2 = make_float2(mul, mul);
@@ -733,7 +762,7 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                     m_ref = m_new;
                     const float off = (kKeyed ? 0.f : E) - (m_new == NEG_INF ? 0.f : m_new);
                     const float2 off2 = make_float2(off, off);
-                    // P of 32 keys goes over their scores: 16 columns of pairs, and (SPLIT) the low parts in the next 16
+                    // P of 32 keys: 16 columns of pairs, and (SPLIT) the low parts in the next 16
                     float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
@@ -764,8 +793,12 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                                 }
                             }
                         }
-                        tmem_st16(t_s + k * 32, hi);
-                        if (SPLIT) tmem_st16(t_s + k * 32 + 16, lo);
+                        if (k == 0 && t > 0) {  // the last tile's products have read its P (and O may be rescaled)
+                            ok = waited(pvd, par ^ 1) && ok;
+                            tc_fence_after();
+                        }
+                        tmem_st16(t_p + k * 32, hi);
+                        if (SPLIT) tmem_st16(t_p + k * 32 + 16, lo);
                     }
                     const float2 lsum = fadd2(ls[0], ls[1]);
                     float sum = lsum.x + lsum.y;
@@ -782,10 +815,8 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                     } else {
                         probabilities(std::false_type{}, 0.f);
                     }
-                    // O_w is rescaled (rarely) once the last tile's products have landed
+                    // O_w is rescaled (rarely)
                     if (__any_sync(0xffffffffu, alpha != 1.f)) {
-                        ok = waited(pvd + 8 * ((t - 1) & 1), (uint32_t)(((t - 1) >> 1) & 1)) && ok;
-                        tc_fence_after();
 #pragma unroll 1
                         for (int k = 0; k < D / 32; ++k) {
                             float o[32];
@@ -796,6 +827,9 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                         }
                     }
                     tmem_wait_st();
+                } else {
+                    if (lane == 0) mbar_arrive(sfree);
+                    if (t > 0) ok = waited(pvd, par ^ 1) && ok;  // in step with the others: prdy counts every thread
                 }
                 if (!QUANT && masked) {
                     // V rows nobody sees (past the context, padding) may hold anything, even NaN: zeros before the
@@ -818,7 +852,7 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                     fence_proxy_async_smem();
                 }
                 tc_fence_before();
-                mbar_arrive(prdy + 16 * (t & 1) + 8 * w);
+                mbar_arrive(prdy + 8 * w);
             }
             // The two warps of the same rows exchange their maxima, then their sums, and each joins and stores one half
             // of the columns once the last products have landed.
@@ -839,39 +873,40 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
             const int part = 2 * blockIdx.x + (g.j0 == 0 ? 1 : 0);
             const size_t orow = ((size_t)(g.qs + tok) * p.H_q + (size_t)g.h * p.G + r % p.G) * D;
             const float inv = den == 0.f ? 0.f : 1.f / den;  // a row that sees nothing is zero
-            ok = waited(pvd + 8 * ((t - 1) & 1), (uint32_t)(((t - 1) >> 1) & 1)) && ok;
+            ok = waited(pvd, (uint32_t)((t - 1) & 1)) && ok;
             tc_fence_after();
             if (warp_ok) {
+                // whole 32-byte sectors per lane where `out` allows: half the store instructions.  (16 columns at a time:
+                // the code of a unit's end is seldom in the instruction cache, so it is kept short.)
+                const bool sector = !whole || (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
+                const bool f32 = !whole || p.out_dtype == PA_F32;
+                const float f = whole ? inv : 1.f, g0 = den == 0.f && whole ? 0.f : f0 * f, g1 = den == 0.f && whole ? 0.f : f1 * f;
+                char* dst = whole ? static_cast<char*>(p.out) + orow * (f32 ? 4 : 2)
+                                  : reinterpret_cast<char*>(p.part_acc + ((size_t)part * kTRows + r) * D);
 #pragma unroll 1
-                for (int k = 0; k < D / 64; ++k) {
-                    const int col = w * (D / 2) + 32 * k;
-                    float a[32], b[32];
-                    tmem_ld32(t_o + col, a);
-                    tmem_ld32(t_o + D + col, b);
+                for (int col = w * (D / 2); col < (w + 1) * (D / 2); col += 16) {
+                    uint32_t a[16], b[16];
+                    tmem_ld16_async(t_o + col, a);
+                    tmem_ld16_async(t_o + D + col, b);
+                    tmem_loaded16(a);
+                    tmem_loaded16(b);
                     // an accumulator whose keys the row does not see holds nothing of it
 #pragma unroll
-                    for (int x = 0; x < 32; ++x) a[x] = f0 == 0.f ? b[x] * f1 : f1 == 0.f ? a[x] * f0 : a[x] * f0 + b[x] * f1;
+                    for (int x = 0; x < 16; ++x)
+                        a[x] = __float_as_uint((g0 == 0.f ? 0.f : __uint_as_float(a[x]) * g0) +
+                                               (g1 == 0.f ? 0.f : __uint_as_float(b[x]) * g1));
                     if (row_ok && ok) {
-                        // (whole 32-byte sectors per lane where `out` allows: half the store instructions)
-                        uint32_t h[32];
-                        const bool sector = !whole || (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
-                        if (!whole || p.out_dtype == PA_F32) {
-                            const float f = whole ? inv : 1.f;
-#pragma unroll
-                            for (int x = 0; x < 32; ++x) h[x] = __float_as_uint(whole && den == 0.f ? 0.f : a[x] * f);
-                            float* dst = whole ? static_cast<float*>(p.out) + orow + col
-                                               : p.part_acc + ((size_t)part * kTRows + r) * D + col;
-#pragma unroll
-                            for (int x = 0; x < 32; x += 8) st_words8(dst + x, h + x, sector);
+                        if (f32) {
+                            st_words8(dst + 4 * col, a, sector);
+                            st_words8(dst + 4 * col + 32, a + 8, sector);
                         } else {
+                            uint32_t h[8];
 #pragma unroll
-                            for (int x = 0; x < 16; ++x) {
-                                const float lo = den == 0.f ? 0.f : a[2 * x] * inv, up = den == 0.f ? 0.f : a[2 * x + 1] * inv;
+                            for (int x = 0; x < 8; ++x) {
+                                const float lo = __uint_as_float(a[2 * x]), up = __uint_as_float(a[2 * x + 1]);
                                 h[x] = p.out_dtype == PA_BF16 ? Mma<__nv_bfloat16>::pack(lo, up) : Mma<__half>::pack(lo, up);
                             }
-                            uint16_t* dst = static_cast<uint16_t*>(p.out) + orow + col;
-#pragma unroll
-                            for (int x = 0; x < 16; x += 8) st_words8(dst + 2 * x, h + x, sector);
+                            st_words8(dst + 2 * col, h, sector);
                         }
                     }
                 }
