@@ -20,8 +20,8 @@
 // The value product takes P in V's 16-bit type: for bf16, or an fp32 output, as a high and a low part (two products).
 //
 // Quantised pool: query rows are scaled to fp16's range by a power of two (exact); K8 is converted to fp16 times 2^(ek -
-// emax + 7), emax the tile's largest exponent (a product is off by at most 2^-32 of the largest a key of the tile could
-// give), V8 likewise where that is exact (see kTreeSpan); with E the exponent taken out of V (per tile, else per key): y =
+// emax + 7), emax the tile's largest exponent (keys 2^22 below it count as zero: a score is off by at most 2^-22 of the
+// largest that a key of the tile could give), V8 likewise where that is exact (see kTreeSpan); with E the exponent taken out of V (per tile, else per key): y =
 // raw c 2^(emax - 7) + E, p = 2^(y - M), O += p (V 2^-E), l += p 2^-E, as in decode_quant.cu.
 #include <algorithm>
 #include <cstring>
@@ -69,6 +69,25 @@ struct TreeParams {
     uint64_t wait_ns;
     int* err;
 };
+
+// Scale bytes, two to a word, held to the range the writer produces.
+__device__ __forceinline__ uint32_t vmin_u16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("min.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t clamp_scales(uint32_t x) {
+    constexpr uint32_t lo = kScaleMin + kScaleBias, hi = kScaleMax + kScaleBias;
+    return vmax_u16x2(vmin_u16x2(x, hi | hi << 16), lo | lo << 16);
+}
+// Two fp16 powers of two with exponent fields x + c (zero where that is not positive; at most 30).
+__device__ __forceinline__ uint32_t scale_factors(uint32_t x, int c) {
+    uint32_t s, d;
+    const uint32_t cc = ((uint32_t)c & 0xffffu) | (uint32_t)c << 16;
+    asm("add.s16x2 %0, %1, %2;" : "=r"(s) : "r"(x), "r"(cc));
+    asm("max.s16x2 %0, %1, %2;" : "=r"(d) : "r"(s), "r"(0u));
+    return d << 10;
+}
 
 // Eight words to one 32-byte sector (32-byte aligned), or to two halves of one.
 __device__ __forceinline__ void st_words8(void* d, const uint32_t* v, bool sector) {
@@ -577,33 +596,34 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                         uint32_t kb, vb;
                         asm volatile("ld.shared.u32 %0, [%1];" : "=r"(kb) : "r"(at));
                         asm volatile("ld.shared.u32 %0, [%1];" : "=r"(vb) : "r"(at + B));
-                        int em = kScaleMin, vm = kScaleMin, vl = kScaleMax;
-                        const uint32_t mine = u[lane >> 3] >> (4 * lane & 31);  // bit i: key 4 lane + i is seen
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (mine >> i & 1u) {
-                                em = max(em, scale_of((kb >> 8 * i) & 255));
-                                vm = max(vm, scale_of((vb >> 8 * i) & 255));
-                                vl = min(vl, scale_of((vb >> 8 * i) & 255));
-                            }
-                        em = __reduce_max_sync(0xffffffffu, em);
-                        vm = __reduce_max_sync(0xffffffffu, vm);
-                        vl = __reduce_min_sync(0xffffffffu, vl);
-                        const bool keyed = vm - vl > kTreeSpan;
-                        // fp16 factors of this lane's four keys, K's and V's (V8 as it is when keyed)
-                        uint32_t fk[2], fv[2];
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            // (a key that nobody sees may lie above the largest: its factor is kept finite)
-                            const int k0_ = min(scale_of((kb >> 16 * i) & 255) - em, 0) + 7, k1_ = min(scale_of((kb >> (16 * i + 8)) & 255) - em, 0) + 7;
-                            const int v0_ = min(scale_of((vb >> 16 * i) & 255) - vm, 0) + 7, v1_ = min(scale_of((vb >> (16 * i + 8)) & 255) - vm, 0) + 7;
-                            fk[i] = Mma<__half>::pack(pow2i(k0_), pow2i(k1_));
-                            fv[i] = keyed ? 0x3c003c00u : Mma<__half>::pack(pow2i(v0_), pow2i(v1_));
+                        uint32_t vlow = vb;  // (for the least of V's)
+                        if (masked) {        // bytes of keys nobody sees: the least scale (for the least of V's: the largest)
+                            const uint32_t m = ((u[lane >> 3] >> (4 * lane & 31) & 0xfu) * 0x00204081u & 0x01010101u) * 255u;
+                            kb = (kb & m) | (~m & 0x57575757u);
+                            vlow = (vb & m) | (~m & 0xa7a7a7a7u);
+                            vb = (vb & m) | (~m & 0x57575757u);
                         }
+                        // pairs of keys (0, 2) and (1, 3): scale bytes held to the range the writer produces
+                        const uint32_t k02 = clamp_scales(kb & 0x00ff00ffu), k13 = clamp_scales(kb >> 8 & 0x00ff00ffu);
+                        const uint32_t v02 = clamp_scales(vb & 0x00ff00ffu), v13 = clamp_scales(vb >> 8 & 0x00ff00ffu);
+                        const uint32_t kx = vmax_u16x2(k02, k13), vx = vmax_u16x2(v02, v13);
+                        const uint32_t vn = vmin_u16x2(clamp_scales(vlow & 0x00ff00ffu), clamp_scales(vlow >> 8 & 0x00ff00ffu));
+                        const int em = (int)__reduce_max_sync(0xffffffffu, max(kx & 0xffffu, kx >> 16));
+                        const int vm = (int)__reduce_max_sync(0xffffffffu, max(vx & 0xffffu, vx >> 16));
+                        const int vl = (int)__reduce_min_sync(0xffffffffu, min(vn & 0xffffu, vn >> 16));
+                        const bool keyed = vm - vl > kTreeSpan;
+                        // fp16 factors 2^(e - max + 7) of this lane's four keys: exponent fields e - max + 7 + 15, 0 (a factor
+                        // of zero) where that is not positive.  V8 as it is when keyed.
+                        const uint32_t fk02 = scale_factors(k02, 22 - em), fk13 = scale_factors(k13, 22 - em);
+                        const uint32_t fv02 = keyed ? 0x3c003c00u : scale_factors(v02, 22 - vm);
+                        const uint32_t fv13 = keyed ? 0x3c003c00u : scale_factors(v13, 22 - vm);
                         const uint32_t sl = slot(t);
+#pragma unroll 1
                         for (int which = 0; which < 2; ++which) {
                             if (t >= NS) ok = waited((which ? vfree : kfree) + 8 * sl, ph(t - NS)) && ok;
+                            const uint32_t f02 = which ? fv02 : fk02, f13 = which ? fv13 : fk13;
                             const uint32_t dst = (which ? sV : sK) + sl * kTile + to, src0 = raw + so + (which ? B * D : 0);
+#pragma unroll 1
                             for (int gr = cw; gr < kTKeys / 8; gr += kConvWarps) {
                                 const uint32_t row0 = 8 * gr + ((8 * gr) & mb);
                                 const uint32_t src = src0 + row0 * D, d = dst + gr * kGroup;
@@ -621,18 +641,12 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                                 }
 #pragma unroll
                                 for (int i = 0; i < 8 / P; ++i) {
-                                    // row P i + pr of the group: its factor lies with lane 2 gr + row / 4
+                                    // row P i + pr of the group: its factor lies with lane 2 gr + row / 4, in f02 or f13 by its
+                                    // last bit (pr's), in the low or high half by the next
                                     const int from = 2 * gr + (P * i) / 4;
-                                    uint32_t f2;
-                                    if constexpr (P == 2) {
-                                        f2 = __shfl_sync(0xffffffffu, which ? fv[i & 1] : fk[i & 1], from);
-                                        f2 = __byte_perm(f2, f2, pr ? 0x3232 : 0x1010);
-                                    } else {
-                                        const uint32_t f01 = __shfl_sync(0xffffffffu, which ? fv[0] : fk[0], from);
-                                        const uint32_t f23 = __shfl_sync(0xffffffffu, which ? fv[1] : fk[1], from);
-                                        f2 = pr & 2 ? f23 : f01;
-                                        f2 = __byte_perm(f2, f2, pr & 1 ? 0x3232 : 0x1010);
-                                    }
+                                    const uint32_t a02 = __shfl_sync(0xffffffffu, f02, from), a13 = __shfl_sync(0xffffffffu, f13, from);
+                                    const uint32_t f = pr & 1 ? a13 : a02;
+                                    const uint32_t f2 = __byte_perm(f, f, P == 2 ? (i & 1 ? 0x3232 : 0x1010) : (pr & 2 ? 0x3232 : 0x1010));
                                     uint32_t h[4] = {e4m3x2_to_f16x2(v[i].x), e4m3x2_to_f16x2(v[i].x >> 16),
                                                      e4m3x2_to_f16x2(v[i].y), e4m3x2_to_f16x2(v[i].y >> 16)};
 #pragma unroll
@@ -659,8 +673,8 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                                 }
                             }
                             if (which && cw == 0 && lane == 0) {
-                                kmul[sl] = pow2i(em - 7);
-                                vexp[sl] = keyed ? kTreeKeyed : (float)(vm - 7);
+                                kmul[sl] = pow2i(em - kScaleBias - 7);
+                                vexp[sl] = keyed ? kTreeKeyed : (float)(vm - kScaleBias - 7);
                             }
                             fence_proxy_async_smem();
                             __syncwarp();
@@ -764,9 +778,9 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                     const float2 off2 = make_float2(off, off);
                     // P of 32 keys: 16 columns of pairs, and (SPLIT) the low parts in the next 16
                     float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    uint32_t hi[2][16], lo[2][16];
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        uint32_t hi[16], lo[16];
 #pragma unroll
                         for (int b = 0; b < 32; b += 4) {
                             uint32_t e[4];
@@ -786,19 +800,22 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                                 else
                                     acc = fadd2(acc, x);
                                 const int at = (b + i) / 2;
-                                hi[at] = Mma<PT>::pack(x.x, x.y);
+                                hi[k][at] = Mma<PT>::pack(x.x, x.y);
                                 if (SPLIT) {
-                                    const float2 f = fsub2(x, Mma<PT>::unpack(hi[at]));
-                                    lo[at] = Mma<PT>::pack(f.x, f.y);
+                                    const float2 f = fsub2(x, Mma<PT>::unpack(hi[k][at]));
+                                    lo[k][at] = Mma<PT>::pack(f.x, f.y);
                                 }
                             }
                         }
-                        if (k == 0 && t > 0) {  // the last tile's products have read its P (and O may be rescaled)
-                            ok = waited(pvd, par ^ 1) && ok;
-                            tc_fence_after();
-                        }
-                        tmem_st16(t_p + k * 32, hi);
-                        if (SPLIT) tmem_st16(t_p + k * 32 + 16, lo);
+                    }
+                    if (t > 0) {  // the last tile's products have read its P (and O may be rescaled)
+                        ok = waited(pvd, par ^ 1) && ok;
+                        tc_fence_after();
+                    }
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        tmem_st16(t_p + k * 32, hi[k]);
+                        if (SPLIT) tmem_st16(t_p + k * 32 + 16, lo[k]);
                     }
                     const float2 lsum = fadd2(ls[0], ls[1]);
                     float sum = lsum.x + lsum.y;
