@@ -14,9 +14,9 @@
 //     (its O is rescaled only when that grows by more than 2^8) and writes the probabilities to TMEM.  The warpgroups have accumulators of their own, O_0 and O_1, joined at the segment's end, so they never wait for one
 //     another in between;
 //   * warp 8 (TMA): query rows (16-bit pool), K and V tiles into rings, block by block through the block table;
-//   * warp 9 (MMA, one thread): S = Q K^T (TMEM columns 0 .. 127) of the next tile as soon as the softmax has read this
-//     one's into registers, then O_w += P_w V (columns 256 + D w), P read from TMEM (columns 128 .. 255);
-//   * quantised pool, warps 10-15: e4m3 tiles from the raw ring to fp16 tiles in the K and V rings, and the query rows.
+//   * warp 9 (one thread): S = Q K^T (TMEM columns 0 .. 127) of the next tile as soon as the softmax has read this one's
+//     into registers; warp 10 (one thread): O_w += P_w V (columns 256 + D w), P read from TMEM (columns 128 .. 255);
+//   * quantised pool, warps 12-19: e4m3 tiles from the raw ring to fp16 tiles in the K and V rings, and the query rows.
 // The value product takes P in V's 16-bit type: for bf16, or an fp32 output, as a high and a low part (two products).
 //
 // Quantised pool: query rows are scaled to fp16's range by a power of two (exact); K8 is converted to fp16 times 2^(ek -
@@ -40,7 +40,7 @@ constexpr uint32_t kTTmem = 512;
 constexpr int kTreeMaxCtas = 160;  // CTAs of a call at most (the workspace holds two partial results for each)
 // Cost of a unit's start and end (query rows, first scores, joining the warpgroups, storing) in key tiles.
 constexpr int kTreeUnitCost = 3;
-constexpr int kConvWarps = 6;
+constexpr int kConvWarps = 8;
 // Probabilities are relative to a reference kPHeadroom below the row's maximum, which may grow by 2^8 before O is
 // rescaled: they reach 2^15, the top of fp16's range, so that the smallest keep as many bits as fp16 allows (an absolute
 // 2^-25 is 2^-32 of the largest).
@@ -80,15 +80,6 @@ __device__ __forceinline__ uint32_t clamp_scales(uint32_t x) {
     constexpr uint32_t lo = kScaleMin + kScaleBias, hi = kScaleMax + kScaleBias;
     return vmax_u16x2(vmin_u16x2(x, hi | hi << 16), lo | lo << 16);
 }
-// Two fp16 powers of two with exponent fields x + c (zero where that is not positive; at most 30).
-__device__ __forceinline__ uint32_t scale_factors(uint32_t x, int c) {
-    uint32_t s, d;
-    const uint32_t cc = ((uint32_t)c & 0xffffu) | (uint32_t)c << 16;
-    asm("add.s16x2 %0, %1, %2;" : "=r"(s) : "r"(x), "r"(cc));
-    asm("max.s16x2 %0, %1, %2;" : "=r"(d) : "r"(s), "r"(0u));
-    return d << 10;
-}
-
 // Eight words to one 32-byte sector (32-byte aligned), or to two halves of one.
 __device__ __forceinline__ void st_words8(void* d, const uint32_t* v, bool sector) {
     if (sector) {
@@ -279,15 +270,15 @@ struct TreeGeo {
     static constexpr uint32_t kRaw = 2u * kTKeys * D, kRawScales = 2 * kTKeys;
     static constexpr uint32_t kExp = QUANT ? kTKeys * 4 : 0;       // per V slot: each key's ev and 2^-ev, as bf16
     // Registers move from the copying and converting warpgroups to the two softmax warpgroups: the launch's share is
-    // 128 (512 threads) or 168 (384) each, and 256 * kMore + (kThreads - 256) * kLess is exactly that total.
-    static constexpr int kThreads = QUANT ? 512 : 384;
-    static constexpr int kMore = QUANT ? 160 : 200, kLess = QUANT ? 96 : 104;
-    static_assert(256 * kMore + (kThreads - 256) * kLess == kThreads * (QUANT ? 128 : 168), "register split");
+    // 96 (640 threads) or 168 (384) each, and 256 * kMore + (kThreads - 256) * kLess is exactly that total.
+    static constexpr int kThreads = QUANT ? 640 : 384;
+    static constexpr int kMore = QUANT ? 144 : 200, kLess = QUANT ? 64 : 104;
+    static_assert(256 * kMore + (kThreads - 256) * kLess == kThreads * (QUANT ? 96 : 168), "register split");
     // Q | K ring | V ring | raw ring | raw scales | exponents | row exchange | query exponents | barriers, small things
     static constexpr uint32_t oK = kTile, oV = oK + NS * kTile, oRaw = oV + NS * kTile, oRawSc = oRaw + NR * kRaw,
                               oExp = oRawSc + NR * kRawScales, oXch = oExp + NS * kExp, oQe = oXch + 2 * kTRows * 4,
                               oBar = oQe + (QUANT ? kTRows : 0);
-    static constexpr int kBars = 4 + 4 * NS + 5 + 2 * NR;
+    static constexpr int kBars = 5 + 4 * NS + 6 + 2 * NR;
     static constexpr uint32_t oSmall = oBar + 8 * kBars;
     static constexpr size_t kSmem = oSmall + 48;
     static_assert(kSmem <= 232448, "shared memory");
@@ -310,11 +301,11 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t sb = smem_addr(smem_raw);
     const uint32_t sQ = sb, sK = sb + Geo::oK, sV = sb + Geo::oV, sBar = sb + Geo::oBar;
-    // prdy: one per warpgroup
-    const uint32_t qfull = sBar, qfree = qfull + 8, qread = qfree + 8, mmadone = qread + 8,
-                   kfull = mmadone + 8, kfree = kfull + 8 * NS,
+    // prdy, pvd: for tiles of either parity (with one P buffer as with two)
+    const uint32_t qfull = sBar, qfree = qfull + 8, qread = qfree + 8, sdone = qread + 8, pdone = sdone + 8,
+                   kfull = pdone + 8, kfree = kfull + 8 * NS,
                    vfull = kfree + 8 * NS, vfree = vfull + 8 * NS, sfull = vfree + 8 * NS, sfree = sfull + 8,
-                   pvd = sfree + 8, prdy = pvd + 8, rfull = prdy + 16, rfree = rfull + 8 * NR;
+                   pvd = sfree + 8, prdy = pvd + 16, rfull = prdy + 16, rfree = rfull + 8 * NR;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_raw + Geo::oSmall);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     volatile int* armed = abort_flag + 1;  // K, V (quantised: raw) tiles and query tiles whose copies have been issued
@@ -344,8 +335,8 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < Geo::kBars; ++i) mbar_init(sBar + 8 * i, 1);
         mbar_init(sfree, 8);  // one arrival per softmax warp
-        mbar_init(prdy, 128);
-        mbar_init(prdy + 8, 128);
+        mbar_init(prdy, 256);
+        mbar_init(prdy + 8, 256);
         if (QUANT) {
             mbar_init(qfull, kConvWarps);
             mbar_init(qread, 8);
@@ -369,6 +360,16 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
         const bool w = mbar_wait_spin(bar, parity, abort_flag, p.wait_ns);
         if (!w) *abort_flag = 1;
         return w;
+    };
+    // two waits at once (each barrier's first look costs about a hundred cycles)
+    auto waited2 = [&](uint32_t a, uint32_t pa, uint32_t b, uint32_t pb) {
+        const bool wa = mbar_try_wait(a, pa), wb = mbar_try_wait(b, pb);
+        return (wa || waited(a, pa)) && (wb || waited(b, pb));
+    };
+    // TMEM columns of P, warpgroup w's 32 keys k of tile t: one buffer of 128 (high parts in 16, low parts in the next 16)
+    // or two of 64 in turn
+    auto p_col = [](int t, int w, int k) {
+        return (uint32_t)(SPLIT ? kTKeys + w * 64 + k * 32 : kTKeys + (t & 1) * 64 + w * 32 + k * 16);
     };
     auto slot = [](int i) { return (uint32_t)(i % NS); };
     auto ph = [](int i) { return (uint32_t)((i / NS) & 1); };
@@ -446,42 +447,38 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                 }
             }
         } else if (warp == 9) {
-            // -------------------------------------------------------- MMA issuer
+            // -------------------------------------------------------- score products
             if (lane == 0) {
                 const uint64_t dq = umma_desc(sQ, 16, 1024);
-                TreeWalk ahead = walk;  // the score products run one tile ahead of the value products
-                TreeSeg gs;
-                int js = 0, segs = -1;
-                bool more = ahead.next(p, gs);
-                js = gs.j0;
-                auto issue_s = [&](int t) {
-                    if (js == gs.j0) ok = waited(qfull, (uint32_t)(++segs & 1));
-                    // S is free once the softmax has read the last tile's into registers
-                    ok = ok && (t == 0 || waited(sfree, (uint32_t)((t - 1) & 1))) && waited(kfull + 8 * slot(t), ph(t));
-                    if (!ok) return;
-                    tc_fence_after();
-                    const uint64_t dk = umma_desc(sK + slot(t) * kTile, 16, kGroup);
+                int t = 0;
+                for (int seg = 0; ok && walk.next(p, g); ++seg) {
+                    ok = waited(qfull, (uint32_t)(seg & 1));
+                    for (int j = g.j0; j < g.j1 && ok; ++j, ++t) {
+                        // S is free once the softmax has read the last tile's into registers
+                        ok = t == 0 ? waited(kfull, 0) : waited2(sfree, (uint32_t)((t - 1) & 1), kfull + 8 * slot(t), ph(t));
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t dk = umma_desc(sK + slot(t) * kTile, 16, kGroup);
 #pragma unroll
-                    for (int ks = 0; ks < NK; ++ks)
-                        umma_f16(tmem, dq + (ks >> 2) * (kTRegion >> 4) + (ks & 3) * 2,
-                                 dk + (ks >> 2) * (1024 >> 4) + (ks & 3) * 2, idesc_s, ks > 0);
-                    umma_commit(sfull);
-                    umma_commit(kfree + 8 * slot(t));
-                    if (++js == gs.j1) {
-                        umma_commit(qfree);
-                        more = ahead.next(p, gs);
-                        js = gs.j0;
+                        for (int ks = 0; ks < NK; ++ks)
+                            umma_f16(tmem, dq + (ks >> 2) * (kTRegion >> 4) + (ks & 3) * 2,
+                                     dk + (ks >> 2) * (1024 >> 4) + (ks & 3) * 2, idesc_s, ks > 0);
+                        umma_commit(sfull);
+                        umma_commit(kfree + 8 * slot(t));
                     }
-                };
-                if (more) issue_s(0);
+                    umma_commit(qfree);
+                }
+                umma_commit(sdone);  // arrives once every product issued above has completed
+            }
+            __syncwarp();
+        } else if (warp == 10) {
+            // -------------------------------------------------------- value products
+            if (lane == 0) {
                 int t = 0;
                 while (ok && walk.next(p, g)) {
                     for (int j = g.j0; j < g.j1 && ok; ++j, ++t) {
-                        if (more) issue_s(t + 1);
-                        ok = ok && waited(vfull + 8 * slot(t), ph(t));
-                        const uint32_t par = (uint32_t)(t & 1);
-                        // (both warpgroups ready also means that both have read the last segment's O)
-                        ok = ok && waited(prdy, par) && waited(prdy + 8, par);
+                        // (every softmax thread ready also means that all have read the last segment's O)
+                        ok = waited2(vfull + 8 * slot(t), ph(t), prdy + 8 * (t & 1), (uint32_t)((t >> 1) & 1));
                         if (!ok) break;
                         tc_fence_after();
                         const uint64_t dv = umma_desc(sV + slot(t) * kTile, 1024, kGroup);
@@ -493,35 +490,32 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
 #pragma unroll
                                 for (int w = 0; w < 2; ++w)
                                     umma_f16_ta(tmem + 2 * kTKeys + (uint32_t)w * D,
-                                                tmem + kTKeys + w * 64 + (ks >> 1) * 32 + (ks & 1) * 8 + part * 16,
+                                                tmem + p_col(t, w, ks >> 1) + (ks & 1) * 8 + part * 16,
                                                 dv + (uint64_t)((w * NT + ks) * ((2 * kGroup) >> 4)), idesc_o,
                                                 j > g.j0 || ks > 0 || part > 0);
                         }
-                        umma_commit(pvd);
+                        umma_commit(pvd + 8 * (t & 1));
                         umma_commit(vfree + 8 * slot(t));
                     }
                 }
-                umma_commit(mmadone);  // arrives once every product issued above has completed
+                umma_commit(pdone);
             }
             __syncwarp();
-        } else {
+        } else if (warp >= 12) {
             // -------------------------------------------------------- converters (quantised pool)
             if constexpr (QUANT) {
-                const int cw = warp - 10;
-                // A warp converts groups of 8 rows, P rows at a time: a lane reads 8 values (of piece `pc` of row `pr`)
-                // and writes 16 bytes.  Both sides are swizzled by the row's place in its group.
-                constexpr int P = 256 / D, L = D / 8;    // rows per step, lanes per row
-                const int pc = lane % L, pr = lane / L;
-                const uint32_t so = D == 128 ? pr * 128 + (((pc >> 1) ^ pr) << 4) + (pc & 1) * 8
-                                             : pr * 64 + (((pc >> 1) ^ (pr >> 1)) << 4) + (pc & 1) * 8;
-                const uint32_t to = (uint32_t)(pc >> 3) * 1024 + pr * 128 + (((pc & 7) ^ pr) << 4);
-                const int mb = ~(B - 1);
+                const int cw = warp - 12;
+                // A lane converts half a row, 16 values at a time, so that the row's factor stays in a register; eight
+                // neighbouring rows' pieces lie in eight different bank groups on both sides, swizzled as they are.
+                const int row = 32 * (cw & 3) + lane, mb = ~(B - 1), c0 = (cw >> 2) * (D / 32);
+                const uint32_t so = (uint32_t)(row + (row & mb)) * D, ro = (uint32_t)(row + (row & mb));
+                const uint32_t to = (uint32_t)(row >> 3) * kGroup + (row & 7) * 128;
                 int t = 0;
                 for (int seg = 0; walk.next(p, g); ++seg) {
                     // the query rows as fp16, four lanes to a row: read, then written once the last segment's have been used
                     {
                         constexpr int C = D / 32;                                     // 16-byte pieces of a row per lane
-                        constexpr int R = (kTRows / 8 + kConvWarps - 1) / kConvWarps;  // rows per lane
+                        constexpr int R = kTRows / 8 / kConvWarps;                    // rows per lane
                         const int tok0 = g.mt * p.TQ, rows = min(p.TQ, g.n - tok0) * p.G;
                         uint4 xs[R][C];
 #pragma unroll
@@ -539,7 +533,6 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
 #pragma unroll
                         for (int k = 0; k < R; ++k) {
                             const int r = (cw + k * kConvWarps) * 8 + (lane >> 2);
-                            if (r >= kTRows) break;  // uniform over the warp
                             uint4 (&x)[C] = xs[k];
                             int e = 0;
                             if (p.q_bf16) {
@@ -612,66 +605,51 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                         const int vm = (int)__reduce_max_sync(0xffffffffu, max(vx & 0xffffu, vx >> 16));
                         const int vl = (int)__reduce_min_sync(0xffffffffu, min(vn & 0xffffu, vn >> 16));
                         const bool keyed = vm - vl > kTreeSpan;
-                        // fp16 factors 2^(e - max + 7) of this lane's four keys: exponent fields e - max + 7 + 15, 0 (a factor
-                        // of zero) where that is not positive.  V8 as it is when keyed.
-                        const uint32_t fk02 = scale_factors(k02, 22 - em), fk13 = scale_factors(k13, 22 - em);
-                        const uint32_t fv02 = keyed ? 0x3c003c00u : scale_factors(v02, 22 - vm);
-                        const uint32_t fv13 = keyed ? 0x3c003c00u : scale_factors(v13, 22 - vm);
+                        // fp16 factors 2^(e - max + 7) of this lane's row: exponent field e - max + 7 + 15, or a factor of zero
+                        // where that is not positive.  V8 as it is when keyed.  A row that nobody sees, past the context or
+                        // padding, may hold anything: it counts as zeros.
+                        const bool seen = u[cw & 3] >> lane & 1u;
+                        uint32_t bk, bv;
+                        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(bk) : "r"(rsc + ro));
+                        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(bv) : "r"(rsc + ro + B));
+                        const int ek = scale_of((int)bk) + kScaleBias, ev = scale_of((int)bv) + kScaleBias;
+                        const uint32_t fk = seen ? (uint32_t)max(ek - em + 22, 0) * 0x04000400u : 0u;
+                        const uint32_t fv = seen ? (keyed ? 0x3c003c00u : (uint32_t)max(ev - vm + 22, 0) * 0x04000400u) : 0u;
                         const uint32_t sl = slot(t);
 #pragma unroll 1
                         for (int which = 0; which < 2; ++which) {
                             if (t >= NS) ok = waited((which ? vfree : kfree) + 8 * sl, ph(t - NS)) && ok;
-                            const uint32_t f02 = which ? fv02 : fk02, f13 = which ? fv13 : fk13;
-                            const uint32_t dst = (which ? sV : sK) + sl * kTile + to, src0 = raw + so + (which ? B * D : 0);
-#pragma unroll 1
-                            for (int gr = cw; gr < kTKeys / 8; gr += kConvWarps) {
-                                const uint32_t row0 = 8 * gr + ((8 * gr) & mb);
-                                const uint32_t src = src0 + row0 * D, d = dst + gr * kGroup;
-                                uint2 v[8 / P];
+                            const uint32_t f2 = which ? fv : fk;
+                            const uint32_t src = raw + so + (which ? B * D : 0), dst = (which ? sV : sK) + sl * kTile + to;
 #pragma unroll
-                                for (int i = 0; i < 8 / P; ++i)
-                                    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
-                                                 : "=r"(v[i].x), "=r"(v[i].y)
-                                                 : "r"((src ^ (D == 128 ? (P * i) << 4 : (P * i / 2) << 4)) + P * i * D));
-                                if (masked) {  // rows nobody sees, past the context or padding, may hold anything: zeros
-                                    const uint32_t seen = u[gr >> 2] >> (8 * (gr & 3));
+                            for (int cc = 0; cc < D / 32; ++cc) {
+                                const int c = c0 + cc;
+                                uint4 v;
+                                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                             : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                                             : "r"(src + (D == 128 ? ((c ^ (row & 7)) << 4) : ((c ^ (row >> 1 & 3)) << 4))));
+                                if (!seen) v = make_uint4(0u, 0u, 0u, 0u);  // (a factor of zero leaves NaN)
+                                uint32_t h[8] = {e4m3x2_to_f16x2(v.x), e4m3x2_to_f16x2(v.x >> 16), e4m3x2_to_f16x2(v.y),
+                                                 e4m3x2_to_f16x2(v.y >> 16), e4m3x2_to_f16x2(v.z),
+                                                 e4m3x2_to_f16x2(v.z >> 16), e4m3x2_to_f16x2(v.w),
+                                                 e4m3x2_to_f16x2(v.w >> 16)};
 #pragma unroll
-                                    for (int i = 0; i < 8 / P; ++i)
-                                        if (!(seen >> (P * i + pr) & 1u)) v[i] = make_uint2(0u, 0u);
+                                for (int k = 0; k < 8; ++k) {
+                                    const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&h[k]),
+                                                              *reinterpret_cast<const __half2*>(&f2));
+                                    h[k] = *reinterpret_cast<const uint32_t*>(&y);
                                 }
 #pragma unroll
-                                for (int i = 0; i < 8 / P; ++i) {
-                                    // row P i + pr of the group: its factor lies with lane 2 gr + row / 4, in f02 or f13 by its
-                                    // last bit (pr's), in the low or high half by the next
-                                    const int from = 2 * gr + (P * i) / 4;
-                                    const uint32_t a02 = __shfl_sync(0xffffffffu, f02, from), a13 = __shfl_sync(0xffffffffu, f13, from);
-                                    const uint32_t f = pr & 1 ? a13 : a02;
-                                    const uint32_t f2 = __byte_perm(f, f, P == 2 ? (i & 1 ? 0x3232 : 0x1010) : (pr & 2 ? 0x3232 : 0x1010));
-                                    uint32_t h[4] = {e4m3x2_to_f16x2(v[i].x), e4m3x2_to_f16x2(v[i].x >> 16),
-                                                     e4m3x2_to_f16x2(v[i].y), e4m3x2_to_f16x2(v[i].y >> 16)};
-#pragma unroll
-                                    for (int k = 0; k < 4; ++k) {
-                                        const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&h[k]),
-                                                                  *reinterpret_cast<const __half2*>(&f2));
-                                        h[k] = *reinterpret_cast<const uint32_t*>(&y);
-                                    }
+                                for (int o = 0; o < 2; ++o)
                                     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                                     (d ^ ((P * i) << 4)) + P * i * 128),
-                                                 "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3])
+                                                     dst + (c >> 2) * 1024 + ((((c & 3) * 2 + o) ^ (row & 7)) << 4)),
+                                                 "r"(h[4 * o]), "r"(h[4 * o + 1]), "r"(h[4 * o + 2]), "r"(h[4 * o + 3])
                                                  : "memory");
-                                }
                             }
-                            if (which && keyed) {
-                                uint32_t* ex = reinterpret_cast<uint32_t*>(smem_raw + Geo::oExp + sl * Geo::kExp);
-                                const int key = cw * 32 + lane;
-                                if (key < kTKeys) {
-                                    uint32_t b;
-                                    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(b) : "r"(rsc + key + (key & mb) + B));
-                                    const int ev = scale_of((int)b);
-                                    // both exact in bf16: the upper halves of the fp32 values
-                                    ex[key] = __float_as_uint((float)ev) >> 16 | (__float_as_uint(pow2i(-ev)) & 0xffff0000u);
-                                }
-                            }
+                            if (which && keyed && c0 == 0)  // both exact in bf16: the upper halves of the fp32 values
+                                reinterpret_cast<uint32_t*>(smem_raw + Geo::oExp + sl * Geo::kExp)[row] =
+                                    __float_as_uint((float)(ev - kScaleBias)) >> 16 |
+                                    (__float_as_uint(pow2i(kScaleBias - ev)) & 0xffff0000u);
                             if (which && cw == 0 && lane == 0) {
                                 kmul[sl] = pow2i(em - kScaleBias - 7);
                                 vexp[sl] = keyed ? kTreeKeyed : (float)(vm - kScaleBias - 7);
@@ -705,7 +683,8 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
             for (int j = g.j0; j < g.j1; ++j, ++t) {
                 const int k0 = j * kTKeys + 64 * w;  // the warpgroup's first key
                 const uint32_t par = (uint32_t)(t & 1);
-                const uint32_t t_s = lanes + (uint32_t)w * 64, t_p = t_s + kTKeys;
+                const uint32_t t_s = lanes + (uint32_t)w * 64;
+                const int tp = SPLIT ? t - 1 : t - 2;  // the tile whose P this one's replaces
                 const bool masked = k0 + 64 > base;
                 uint32_t vis[2] = {0u, 0u};
                 if (masked && row_ok) {
@@ -808,14 +787,14 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                             }
                         }
                     }
-                    if (t > 0) {  // the last tile's products have read its P (and O may be rescaled)
-                        ok = waited(pvd, par ^ 1) && ok;
+                    if (tp >= 0) {  // its products have read it
+                        ok = waited(pvd + 8 * (tp & 1), (uint32_t)((tp >> 1) & 1)) && ok;
                         tc_fence_after();
                     }
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        tmem_st16(t_p + k * 32, hi[k]);
-                        if (SPLIT) tmem_st16(t_p + k * 32 + 16, lo[k]);
+                        tmem_st16(lanes + p_col(t, w, k), hi[k]);
+                        if (SPLIT) tmem_st16(lanes + p_col(t, w, k) + 16, lo[k]);
                     }
                     const float2 lsum = fadd2(ls[0], ls[1]);
                     float sum = lsum.x + lsum.y;
@@ -832,8 +811,10 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                     } else {
                         probabilities(std::false_type{}, 0.f);
                     }
-                    // O_w is rescaled (rarely)
+                    // O_w is rescaled (rarely) once the last tile's products have landed
                     if (__any_sync(0xffffffffu, alpha != 1.f)) {
+                        ok = waited(pvd + 8 * ((t - 1) & 1), (uint32_t)(((t - 1) >> 1) & 1)) && ok;
+                        tc_fence_after();
 #pragma unroll 1
                         for (int k = 0; k < D / 32; ++k) {
                             float o[32];
@@ -846,7 +827,8 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                     tmem_wait_st();
                 } else {
                     if (lane == 0) mbar_arrive(sfree);
-                    if (t > 0) ok = waited(pvd, par ^ 1) && ok;  // in step with the others: prdy counts every thread
+                    // in step with the others: prdy counts every thread
+                    if (tp >= 0) ok = waited(pvd + 8 * (tp & 1), (uint32_t)((tp >> 1) & 1)) && ok;
                 }
                 if (!QUANT && masked) {
                     // V rows nobody sees (past the context, padding) may hold anything, even NaN: zeros before the
@@ -869,7 +851,7 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                     fence_proxy_async_smem();
                 }
                 tc_fence_before();
-                mbar_arrive(prdy + 8 * w);
+                mbar_arrive(prdy + 8 * (t & 1));
             }
             // The two warps of the same rows exchange their maxima, then their sums, and each joins and stores one half
             // of the columns once the last products have landed.
@@ -890,7 +872,7 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
             const int part = 2 * blockIdx.x + (g.j0 == 0 ? 1 : 0);
             const size_t orow = ((size_t)(g.qs + tok) * p.H_q + (size_t)g.h * p.G + r % p.G) * D;
             const float inv = den == 0.f ? 0.f : 1.f / den;  // a row that sees nothing is zero
-            ok = waited(pvd, (uint32_t)((t - 1) & 1)) && ok;
+            ok = waited(pvd + 8 * ((t - 1) & 1), (uint32_t)(((t - 1) >> 1) & 1)) && ok;
             tc_fence_after();
             if (warp_ok) {
                 // whole 32-byte sectors per lane where `out` allows: half the store instructions.  (16 columns at a time:
@@ -935,9 +917,9 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
             tc_fence_before();  // O may be started afresh once this thread's next P is ready
         }
     }
-    // Nothing issued may still be running when TMEM and shared memory are released: the tensor-core products (the MMA
-    // thread's last commit) and the copies (the last arm of every stage; earlier ones were consumed before it).
-    if (warp == 9 && lane == 0) mbar_wait_bounded(mmadone, 0, nullptr);
+    // Nothing issued may still be running when TMEM and shared memory are released: the tensor-core products (their
+    // threads' last commits) and the copies (the last arm of every stage; earlier ones were consumed before it).
+    if ((warp == 9 || warp == 10) && lane == 0) mbar_wait_bounded(warp == 9 ? sdone : pdone, 0, nullptr);
     if (warp == 8 && lane == 0) {
         if constexpr (QUANT) {
             const int n = armed[0];
