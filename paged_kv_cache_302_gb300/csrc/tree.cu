@@ -70,16 +70,14 @@ struct TreeParams {
     int* err;
 };
 
-// Scale bytes, two to a word, held to the range the writer produces.
 __device__ __forceinline__ uint32_t vmin_u16x2(uint32_t a, uint32_t b) {
     uint32_t d;
     asm("min.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
-__device__ __forceinline__ uint32_t clamp_scales(uint32_t x) {
-    constexpr uint32_t lo = kScaleMin + kScaleBias, hi = kScaleMax + kScaleBias;
-    return vmax_u16x2(vmin_u16x2(x, hi | hi << 16), lo | lo << 16);
-}
+// A scale byte held to the range the writer produces.
+__device__ __forceinline__ int clamp_scale(uint32_t b) { return scale_of((int)b) + kScaleBias; }
+
 // Eight words to one 32-byte sector (32-byte aligned), or to two halves of one.
 __device__ __forceinline__ void st_words8(void* d, const uint32_t* v, bool sector) {
     if (sector) {
@@ -583,7 +581,15 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                         uint32_t u[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
                         const bool masked = k0 + kTKeys > g.ctx - g.n;
                         if (masked) tree_union<4>(p, g, k0, u);  // keys past the context are in none
-                        ok = waited(rfull + 8 * rb, (uint32_t)((t / NR) & 1)) && ok;
+                        // the raw tile, and room for it: one wait (the value products of tile t - 2 end long before)
+                        const uint32_t sl = slot(t);
+                        if (t < NS) {
+                            ok = waited(rfull + 8 * rb, (uint32_t)((t / NR) & 1)) && ok;
+                        } else {
+                            const bool k = mbar_try_wait(kfree + 8 * sl, ph(t - NS));
+                            ok = waited2(rfull + 8 * rb, (uint32_t)((t / NR) & 1), vfree + 8 * sl, ph(t - NS)) && ok;
+                            if (!k) ok = waited(kfree + 8 * sl, ph(t - NS)) && ok;
+                        }
                         // lane: keys 4 lane .. + 3, all of one block; the largest exponents of the keys that are seen
                         const uint32_t at = rsc + 4 * lane + ((4 * lane) & mb);
                         uint32_t kb, vb;
@@ -596,14 +602,13 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                             vlow = (vb & m) | (~m & 0xa7a7a7a7u);
                             vb = (vb & m) | (~m & 0x57575757u);
                         }
-                        // pairs of keys (0, 2) and (1, 3): scale bytes held to the range the writer produces
-                        const uint32_t k02 = clamp_scales(kb & 0x00ff00ffu), k13 = clamp_scales(kb >> 8 & 0x00ff00ffu);
-                        const uint32_t v02 = clamp_scales(vb & 0x00ff00ffu), v13 = clamp_scales(vb >> 8 & 0x00ff00ffu);
-                        const uint32_t kx = vmax_u16x2(k02, k13), vx = vmax_u16x2(v02, v13);
-                        const uint32_t vn = vmin_u16x2(clamp_scales(vlow & 0x00ff00ffu), clamp_scales(vlow >> 8 & 0x00ff00ffu));
-                        const int em = (int)__reduce_max_sync(0xffffffffu, max(kx & 0xffffu, kx >> 16));
-                        const int vm = (int)__reduce_max_sync(0xffffffffu, max(vx & 0xffffu, vx >> 16));
-                        const int vl = (int)__reduce_min_sync(0xffffffffu, min(vn & 0xffffu, vn >> 16));
+                        // largest of K's, largest and least of V's, held to the range the writer produces
+                        const uint32_t kx = vmax_u16x2(kb & 0x00ff00ffu, kb >> 8 & 0x00ff00ffu);
+                        const uint32_t vx = vmax_u16x2(vb & 0x00ff00ffu, vb >> 8 & 0x00ff00ffu);
+                        const uint32_t vn = vmin_u16x2(vlow & 0x00ff00ffu, vlow >> 8 & 0x00ff00ffu);
+                        const int em = clamp_scale(__reduce_max_sync(0xffffffffu, max(kx & 0xffffu, kx >> 16)));
+                        const int vm = clamp_scale(__reduce_max_sync(0xffffffffu, max(vx & 0xffffu, vx >> 16)));
+                        const int vl = clamp_scale(__reduce_min_sync(0xffffffffu, min(vn & 0xffffu, vn >> 16)));
                         const bool keyed = vm - vl > kTreeSpan;
                         // fp16 factors 2^(e - max + 7) of this lane's row: exponent field e - max + 7 + 15, or a factor of zero
                         // where that is not positive.  V8 as it is when keyed.  A row that nobody sees, past the context or
@@ -612,23 +617,23 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                         uint32_t bk, bv;
                         asm volatile("ld.shared.u8 %0, [%1];" : "=r"(bk) : "r"(rsc + ro));
                         asm volatile("ld.shared.u8 %0, [%1];" : "=r"(bv) : "r"(rsc + ro + B));
-                        const int ek = scale_of((int)bk) + kScaleBias, ev = scale_of((int)bv) + kScaleBias;
+                        const int ek = clamp_scale(bk), ev = clamp_scale(bv);
                         const uint32_t fk = seen ? (uint32_t)max(ek - em + 22, 0) * 0x04000400u : 0u;
                         const uint32_t fv = seen ? (keyed ? 0x3c003c00u : (uint32_t)max(ev - vm + 22, 0) * 0x04000400u) : 0u;
-                        const uint32_t sl = slot(t);
 #pragma unroll 1
                         for (int which = 0; which < 2; ++which) {
-                            if (t >= NS) ok = waited((which ? vfree : kfree) + 8 * sl, ph(t - NS)) && ok;
                             const uint32_t f2 = which ? fv : fk;
                             const uint32_t src = raw + so + (which ? B * D : 0), dst = (which ? sV : sK) + sl * kTile + to;
+                            uint4 vs[D / 32];  // all read before the first is converted
+#pragma unroll
+                            for (int cc = 0; cc < D / 32; ++cc)
+                                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                             : "=r"(vs[cc].x), "=r"(vs[cc].y), "=r"(vs[cc].z), "=r"(vs[cc].w)
+                                             : "r"(src + (((c0 + cc) ^ (D == 128 ? row & 7 : row >> 1 & 3)) << 4)));
 #pragma unroll
                             for (int cc = 0; cc < D / 32; ++cc) {
                                 const int c = c0 + cc;
-                                uint4 v;
-                                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                             : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                                             : "r"(src + (D == 128 ? ((c ^ (row & 7)) << 4) : ((c ^ (row >> 1 & 3)) << 4))));
-                                if (!seen) v = make_uint4(0u, 0u, 0u, 0u);  // (a factor of zero leaves NaN)
+                                const uint4 v = seen ? vs[cc] : make_uint4(0u, 0u, 0u, 0u);  // (zero times NaN is NaN)
                                 uint32_t h[8] = {e4m3x2_to_f16x2(v.x), e4m3x2_to_f16x2(v.x >> 16), e4m3x2_to_f16x2(v.y),
                                                  e4m3x2_to_f16x2(v.y >> 16), e4m3x2_to_f16x2(v.z),
                                                  e4m3x2_to_f16x2(v.z >> 16), e4m3x2_to_f16x2(v.w),
@@ -691,10 +696,12 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
 #pragma unroll
                     for (int k = 0; k < 2; ++k) vis[k] = tree_visible(p, g, tok, k0 + 32 * k - base);
                 }
-                ok = waited(sfull, par) && ok;
+                if (QUANT)
+                    ok = waited2(sfull, par, vfull + 8 * slot(t), ph(t)) && ok;  // scores, and the tile's exponents
+                else
+                    ok = waited(sfull, par) && ok;
                 tc_fence_after();
                 if (QUANT) {
-                    ok = waited(vfull + 8 * slot(t), ph(t)) && ok;  // the tile's exponents
                     if (j == g.j0) {
                         cr = p.scale_log2 * pow2i((int)qexp[r]);
                         __syncwarp();
