@@ -15,6 +15,7 @@ tensors: qpool [NB, H_kv, 2, B, D] (float8_e4m3fn or uint8) and scales
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import re
@@ -182,19 +183,66 @@ def _quant_cache(qpool, scales):
     """(NB, H_kv, B, D) of a quantised cache, after checking that the two tensors are one."""
     if not isinstance(qpool, torch.Tensor) or not isinstance(scales, torch.Tensor):
         raise PAError(PA_ERR_INVALID, "qpool and scales must be tensors")
+    shape = tuple(qpool.shape)
     if qpool.dtype not in _E4M3_TYPES or scales.dtype not in _SCALE_TYPES:
         raise PAError(PA_ERR_INVALID, "qpool must be float8_e4m3fn or uint8, scales uint8 or float8_e8m0fnu")
-    if qpool.dim() != 5 or qpool.shape[2] != 2 or tuple(scales.shape) != tuple(qpool.shape[:4]):
+    if len(shape) != 5 or shape[2] != 2 or tuple(scales.shape) != shape[:4]:
         raise PAError(PA_ERR_INVALID, "qpool must be [NB, H_kv, 2, B, D] and scales [NB, H_kv, 2, B]")
-    return qpool.shape[0], qpool.shape[1], qpool.shape[3], qpool.shape[4]
+    return shape[0], shape[1], shape[3], shape[4]
 
 
-def _same_device(*tensors):
-    """The tensors live on the current device, where the call's kernels run."""
-    here = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.is_cuda and t.device.index != here:
-            raise PAError(PA_ERR_INVALID, f"tensors must be on the current device (cuda:{here}), got {t.device}")
+_CODES = {torch.float16: PA_F16, torch.bfloat16: PA_BF16, torch.float32: PA_F32}
+
+
+def _code(t: torch.dtype) -> int:
+    c = _CODES.get(t)
+    return _dtype_code(t) if c is None else c
+
+
+def _here(t, name) -> int:
+    """Index of the current device, on which `t` must live (the call's kernels run there)."""
+    d = t.get_device() if isinstance(t, torch.Tensor) else None
+    if d is None or d < 0:
+        raise PAError(PA_ERR_INVALID, f"{name} must be a tensor on a CUDA device")
+    if d != torch._C._cuda_getDevice():
+        raise PAError(PA_ERR_INVALID, f"{name} must be on the current device, got cuda:{d}")
+    return d
+
+
+def _arg(t, name, dev, dtype=None) -> int:
+    """Address of a contiguous tensor on device `dev`.  (These checks run at every call: they are kept cheap.)"""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        raise PAError(PA_ERR_INVALID, f"{name} must be a tensor on the current CUDA device (cuda:{dev})")
+    if dtype is not None and t.dtype != dtype:
+        raise PAError(PA_ERR_INVALID, f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise PAError(PA_ERR_INVALID, f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _out_arg(t, name, dev) -> int:
+    """The same for a tensor that may lie in pinned host memory."""
+    if isinstance(t, torch.Tensor) and t.get_device() < 0 and t.is_pinned() and t.is_contiguous():
+        return t.data_ptr()
+    return _arg(t, name, dev)
+
+
+def _err_arg(t, dev):
+    return None if t is None else _arg(t, "dev_err", dev, torch.int32)
+
+
+def _stream_arg(stream, dev) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+@functools.lru_cache(maxsize=256)
+def _decode_bytes(*shape):
+    return pa_decode_workspace_bytes(*shape)
+
+
+@functools.lru_cache(maxsize=256)
+def _tree_bytes(*shape):
+    return pa_decode_tree_workspace_bytes(*shape)
 
 
 def _dev(t: torch.Tensor, name: str, dtype=None):
@@ -269,11 +317,8 @@ def pa_decode_workspace_bytes(N, H_q, H_kv, D, max_ctx, partition_tokens=0) -> i
 
 
 def _workspace(workspace, nbytes, device):
-    if workspace is None:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if workspace.numel() * workspace.element_size() < nbytes:
-        raise PAError(PA_ERR_INVALID, "workspace too small")
-    return workspace
+    """The caller's workspace (the library checks its size), or a new one."""
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if workspace is None else workspace
 
 
 def pa_decode(out, q, pool, block_tables, ctx_lens, max_ctx, scale=None, partition_tokens=0, workspace=None,
@@ -426,11 +471,11 @@ def pa_reshape_and_cache_quant(k, v, qpool, scales, slot_mapping, dev_err=None, 
     T = k.shape[0]
     if slot_mapping.numel() != T:
         raise PAError(PA_ERR_INVALID, "slot_mapping must have T entries")
-    args = (_dev(k, "k"), _dev(v, "v", k.dtype), _dev(qpool, "qpool"), _dev(scales, "scales"),
-            _dev(slot_mapping, "slot_mapping", torch.int64))
-    _same_device(k, v, qpool, scales, slot_mapping, dev_err)
-    _check(load().pa_reshape_and_cache_quant(*args, T, NB, B, H_kv, D, _dtype_code(k.dtype), _err_ptr(dev_err),
-                                             _stream_ptr(stream)))
+    dev = _here(k, "k")
+    _check((_lib or load()).pa_reshape_and_cache_quant(
+        _arg(k, "k", dev), _arg(v, "v", dev, k.dtype), _arg(qpool, "qpool", dev), _arg(scales, "scales", dev),
+        _arg(slot_mapping, "slot_mapping", dev, torch.int64), T, NB, B, H_kv, D, _code(k.dtype),
+        _err_arg(dev_err, dev), _stream_arg(stream, dev)))
 
 
 def pa_dequant_blocks(dst_pool, qpool, scales, pairs, dev_err=None, stream=None):
@@ -442,11 +487,11 @@ def pa_dequant_blocks(dst_pool, qpool, scales, pairs, dev_err=None, stream=None)
     if pairs.dtype != torch.int64 or (pairs.numel() and (pairs.dim() != 2 or pairs.shape[1] != 2)):
         raise PAError(PA_ERR_INVALID, "pairs must be [n, 2] int64")
     n = pairs.shape[0] if pairs.numel() else 0
-    args = (_dev(dst_pool, "dst_pool"), dst_pool.shape[0], _dev(qpool, "qpool"), _dev(scales, "scales"), NB,
-            _dev(pairs, "pairs", torch.int64) if n else None)
-    _same_device(dst_pool, qpool, scales, pairs, dev_err)
-    _check(load().pa_dequant_blocks(*args, n, B, H_kv, D, _dtype_code(dst_pool.dtype), _err_ptr(dev_err),
-                                    _stream_ptr(stream)))
+    dev = _here(dst_pool, "dst_pool")
+    _check((_lib or load()).pa_dequant_blocks(
+        _arg(dst_pool, "dst_pool", dev), dst_pool.shape[0], _arg(qpool, "qpool", dev), _arg(scales, "scales", dev), NB,
+        _arg(pairs, "pairs", dev) if n else None, n, B, H_kv, D, _code(dst_pool.dtype), _err_arg(dev_err, dev),
+        _stream_arg(stream, dev)))
     return dst_pool
 
 
@@ -461,14 +506,14 @@ def pa_decode_quant(out, q, qpool, scales, block_tables, ctx_lens, max_ctx, scal
     if block_tables.dim() != 2 or block_tables.shape[0] != N or ctx_lens.numel() != N:
         raise PAError(PA_ERR_INVALID, "block_tables must be [N, MB] and ctx_lens [N]")
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-    ws = _workspace(workspace, pa_decode_workspace_bytes(N, H_q, H_kv, D, int(max_ctx), partition_tokens), q.device)
-    args = (_acc(out, "out"), _dtype_code(out.dtype), _dev(q, "q"), _dtype_code(q.dtype), _dev(qpool, "qpool"),
-            _dev(scales, "scales"), _dev(block_tables, "block_tables", torch.int32),
-            _dev(ctx_lens, "ctx_lens", torch.int32))
-    _same_device(out, q, qpool, scales, block_tables, ctx_lens, ws, dev_err)
-    _check(load().pa_decode_quant(*args, N, H_q, H_kv, D, B, block_tables.shape[1], NB, int(max_ctx), scale,
-                                  int(partition_tokens), _dev(ws, "workspace"), ws.numel() * ws.element_size(),
-                                  _err_ptr(dev_err), _events_arg(attend_events, stream), _stream_ptr(stream)))
+    dev = _here(q, "q")
+    ws = _workspace(workspace, _decode_bytes(N, H_q, H_kv, D, int(max_ctx), int(partition_tokens)), q.device)
+    _check((_lib or load()).pa_decode_quant(
+        _out_arg(out, "out", dev), _code(out.dtype), _arg(q, "q", dev), _code(q.dtype), _arg(qpool, "qpool", dev),
+        _arg(scales, "scales", dev), _arg(block_tables, "block_tables", dev, torch.int32),
+        _arg(ctx_lens, "ctx_lens", dev, torch.int32), N, H_q, H_kv, D, B, block_tables.shape[1], NB, int(max_ctx), scale,
+        int(partition_tokens), _arg(ws, "workspace", dev), ws.numel() * ws.element_size(), _err_arg(dev_err, dev),
+        _events_arg(attend_events, stream), _stream_arg(stream, dev)))
     return out
 
 
@@ -495,7 +540,7 @@ def pa_decode_tree(out, q, pool, block_tables, ctx_lens, q_start, tree_mask, max
         if pool.dim() != 5 or pool.shape[2] != 2 or pool.dtype != q.dtype:
             raise PAError(PA_ERR_INVALID, "without scales the pool must be [NB, B, 2, H_kv, D] of q's dtype")
         NB, B, _, H_kv, D2 = pool.shape
-        code = _dtype_code(pool.dtype)
+        code = _code(pool.dtype)
     N = ctx_lens.numel()
     if D2 != D or block_tables.dim() != 2 or block_tables.shape[0] != N or q_start.numel() != N + 1:
         raise PAError(PA_ERR_INVALID, "head dims must agree, block_tables be [N, MB], ctx_lens [N], q_start [N+1]")
@@ -504,15 +549,15 @@ def pa_decode_tree(out, q, pool, block_tables, ctx_lens, q_start, tree_mask, max
     if T == 0 or max_q_len == 0:
         return out
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-    ws = _workspace(workspace, pa_decode_tree_workspace_bytes(N, H_q, H_kv, D, int(max_q_len)), q.device)
-    args = (_dev(out, "out"), _dtype_code(out.dtype), _dev(q, "q"), _dtype_code(q.dtype), _dev(pool, "pool"),
-            _dev(scales, "scales") if scales is not None else None, code,
-            _dev(block_tables, "block_tables", torch.int32), _dev(ctx_lens, "ctx_lens", torch.int32),
-            _dev(q_start, "q_start", torch.int32), _dev(tree_mask, "tree_mask", torch.int32), tree_mask.shape[1])
-    _same_device(out, q, pool, scales, block_tables, ctx_lens, q_start, tree_mask, ws, dev_err)
-    _check(load().pa_decode_tree(*args, N, T, H_q, H_kv, D, B, block_tables.shape[1], NB, int(max_q_len), scale,
-                                 _dev(ws, "workspace"), ws.numel() * ws.element_size(), _err_ptr(dev_err),
-                                 _stream_ptr(stream)))
+    dev = _here(q, "q")
+    ws = _workspace(workspace, _tree_bytes(N, H_q, H_kv, D, int(max_q_len)), q.device)
+    _check((_lib or load()).pa_decode_tree(
+        _arg(out, "out", dev), _code(out.dtype), _arg(q, "q", dev), _code(q.dtype), _arg(pool, "pool", dev),
+        _arg(scales, "scales", dev) if scales is not None else None, code,
+        _arg(block_tables, "block_tables", dev, torch.int32), _arg(ctx_lens, "ctx_lens", dev, torch.int32),
+        _arg(q_start, "q_start", dev, torch.int32), _arg(tree_mask, "tree_mask", dev, torch.int32), tree_mask.shape[1],
+        N, T, H_q, H_kv, D, B, block_tables.shape[1], NB, int(max_q_len), scale, _arg(ws, "workspace", dev),
+        ws.numel() * ws.element_size(), _err_arg(dev_err, dev), _stream_arg(stream, dev)))
     return out
 
 

@@ -196,7 +196,11 @@ pa_status pa_update_block_tables(int32_t* tables, int N, int MB, const int32_t* 
 size_t pa_decode_workspace_bytes(int N, int H_q, int H_kv, int D, int max_ctx, int partition_tokens) {
     WorkspaceLayout L;
     if (!workspace_layout(N, H_q, H_kv, D, max_ctx, partition_tokens, &L)) return 0;
-    return L.total;
+    size_t total = L.total;
+    // a small batch's quantised decode takes shorter partitions, hence more of them
+    if (partition_tokens == 0 && workspace_layout(N, H_q, H_kv, D, max_ctx, quant_partition(N, H_kv, max_ctx), &L))
+        total = total > L.total ? total : L.total;
+    return total;
 }
 
 pa_status pa_decode(void* out, pa_dtype out_dtype, const void* q, const void* pool, const int32_t* block_tables,

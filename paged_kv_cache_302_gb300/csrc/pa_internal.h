@@ -107,6 +107,9 @@ struct WorkspaceLayout {
 // Returns false for invalid arguments.
 bool workspace_layout(int N, int H_q, int H_kv, int D, int max_ctx, int partition_tokens, WorkspaceLayout* out);
 
+// Partition length pa_decode_quant takes for partition_tokens == 0.
+int quant_partition(int N, int H_kv, int max_ctx);
+
 // The schedule of a decode call (work records and partition counts, in the workspace); the attention kernel is
 // launched right after it.  cap: tokens a table row (or a request's buffer) holds; req_ids null for a paged cache.
 pa_status launch_plan(const int32_t* ctx_lens, const int32_t* req_ids, int N, int H_kv, int max_ctx, int cap, int N_max,
