@@ -20,11 +20,11 @@
 namespace pa {
 
 // A consumer warp is bound by the latency of its own chain (scores, maximum, exponentials, products), so the SM needs
-// several: with 32-token stages six CTAs of three stages (D = 128) fit.  Measured on 8-KV-head bf16 caches, 256 sequences of
-// ~1500 tokens / 8 of 32768: 4 CTAs 141 / 103 us, 6 CTAs 133 / 95, 8 CTAs (two stages each) 138 / 101; 64-token
-// stages with 4 CTAs 141 / 97.
+// several: with 32-token stages seven CTAs of three stages (D = 128) fit.  Measured on 256 sequences of ~1500 tokens with
+// 8 KV heads / 8 of 32768 / 64 of ~1000 with 40 KV heads: 4 CTAs 141 / 103 / 125 us, 6 CTAs 131 / 96 / 123, 7 CTAs
+// 131 / 94 / 115, 8 CTAs (two stages each) 138 / 101 / 120; 64-token stages with 4 CTAs 141 / 97 / 120.
 constexpr int kQStageTok = 32;   // tokens of one KV head per pipeline stage
-constexpr int kQCtasPerSm = 6;
+constexpr int kQCtasPerSm = 7;
 constexpr int kQThreads = 64;
 
 enum : int { kQFirst = 1, kQLast = 2, kQDone = 4 };
@@ -59,11 +59,11 @@ struct QuantParams {
 // the query rows, the stage's description and its two barriers.
 template <int D>
 struct QGeo {
-    static constexpr int kStages = D == 128 ? 3 : 6;
     static constexpr uint32_t kSlot = kQStageTok * D * 2;
     static constexpr uint32_t kScales = kQStageTok * 2;
     static constexpr uint32_t kQ = kMaxGroup * D * 2;
     static constexpr uint32_t kPerStage = kSlot + kScales + kQ + sizeof(QStageMeta) + 16;
+    static constexpr int kStages = (233472 / kQCtasPerSm - 1024 - 1024 - 16) / (int)kPerStage;
     static constexpr size_t kSmem = 1024 + (size_t)kStages * kPerStage + 16;
     static_assert(kQCtasPerSm * (kSmem + 1024) <= 233472, "the CTAs of an SM fit its shared memory");
 };
@@ -656,27 +656,13 @@ pa_status quant_tensor_map(CUtensorMap* m, const void* qpool, int NB, int H_kv, 
 // The consumer warps resident on the GPU (kQCtasPerSm on each of its 152 SMs) each take a record at a time, in about
 // 1 us per 32 tokens.  A batch with fewer whole default partitions than warps is cut finer, down to 64 tokens (two
 // stages; shorter ones leave the merge more than they save): one sequence of 1000 tokens and 8 KV heads took 28 us in
-// partitions of 512 and takes a third of that in 64.  A larger one whose whole partitions make few rounds over the
-// warps takes the length among 512 .. 768 that leaves the last round fullest: 8 sequences of 32768 tokens make 4.5
-// rounds of 512 (the last half empty, 95 us) and 4.0 of 576.
+// partitions of 512 and takes 11 in partitions of 64.  (Lengths that would fill the last round over the warps made no
+// difference to larger batches: 8 sequences of 32768 tokens took 96 us with 512, 97 with 576, 95 with 768.)
 int quant_partition(int N, int H_kv, int max_ctx) {
     constexpr long kWarps = 152 * kQCtasPerSm;
-    const long rows = (long)N * H_kv;
-    if (rows * max_ctx < kWarps * kDefaultPartition) {
-        const long pt = (rows * max_ctx + kWarps - 1) / kWarps;
-        return (int)std::min<long>(kDefaultPartition, std::max<long>(64, (pt + kStageTok - 1) / kStageTok * kStageTok));
-    }
-    int best = kDefaultPartition;
-    long cost = 0;
-    for (int pt = kDefaultPartition; pt <= kDefaultPartition * 3 / 2; pt += kStageTok) {
-        const long rounds = (rows * ((max_ctx + pt - 1) / pt) + kWarps - 1) / kWarps, c = rounds * pt;
-        if (pt == kDefaultPartition && rounds > 8) return pt;  // the last round weighs little
-        if (cost == 0 || c < cost - cost / 32) {
-            best = pt;
-            cost = c;
-        }
-    }
-    return best;
+    const long tokens = (long)N * H_kv * max_ctx;
+    const long pt = ((tokens + kWarps - 1) / kWarps + kStageTok - 1) / kStageTok * kStageTok;
+    return (int)std::min<long>(kDefaultPartition, std::max<long>(64, pt));
 }
 
 pa_status launch_decode_quant(const DecodeQuantArgs& a) {
