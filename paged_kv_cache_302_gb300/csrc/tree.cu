@@ -256,6 +256,78 @@ __device__ __forceinline__ void tree_union(const TreeParams& p, const TreeSeg& g
     for (int c = 0; c < NW; ++c) u[c] = __reduce_or_sync(0xffffffffu, v[c]);
 }
 
+// Scores (64 TMEM columns from t_s on) of keys that are not seen become -inf.
+__device__ __forceinline__ void tree_mask_scores(uint32_t t_s, uint32_t see0, uint32_t see1) {
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+        const uint32_t see = (c & 2 ? see1 : see0) >> (16 * (c & 1));
+        uint32_t x[16];
+        tmem_ld16_async(t_s + 16 * c, x);
+        tmem_loaded16(x);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = see >> i & 1u ? x[i] : 0xff800000u;
+        tmem_st16(t_s + 16 * c, x);
+    }
+    tmem_wait_st();
+}
+
+// A row's reference for the probabilities of a tile with the given maximum, and the factor of what was summed before.
+__device__ __forceinline__ float tree_reference(float m_tile, bool first, float& m_ref, float& alpha) {
+    const float m_new = m_tile > m_ref + 8.f || m_ref == -INFINITY ? fmaxf(m_ref, m_tile) : m_ref;
+    alpha = first || m_new == m_ref ? 1.f : fast_exp2(m_ref - m_new);
+    m_ref = m_new;
+    return m_new == -INFINITY ? 0.f : m_new;
+}
+
+// Probabilities of 64 keys with exponents of their own (packed bf16 pairs ev, 2^-ev at shared address ex).  Such tiles are
+// rare and are read twice, 16 columns at a time.  Returns the exponential sum.
+template <typename PT, bool SPLIT>
+__device__ __noinline__ float3 tree_probabilities_keyed(uint32_t t_s, uint32_t t_p, uint32_t ex, float mul, bool first,
+                                                        float m_ref) {
+    float alpha;
+    uint32_t x[16], e[16];
+    auto load = [&](int c) {
+        tmem_ld16_async(t_s + 16 * c, x);
+#pragma unroll
+        for (int i = 0; i < 16; i += 4)
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(e[i]), "=r"(e[i + 1]), "=r"(e[i + 2]), "=r"(e[i + 3])
+                         : "r"(ex + 4 * (16 * c + i)));
+        tmem_loaded16(x);
+    };
+    float m_tile = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+        load(c);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            m_tile = fmaxf(m_tile, fmaf(__uint_as_float(x[i]), mul, __uint_as_float(e[i] << 16)));
+    }
+    const float off = -tree_reference(m_tile - kPHeadroom, first, m_ref, alpha);
+    float sum = 0.f;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+        load(c);
+        uint32_t hi[8], lo[8];
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+            float2 y;
+            y.x = fast_exp2(fmaf(__uint_as_float(x[i]), mul, __uint_as_float(e[i] << 16)) + off);
+            y.y = fast_exp2(fmaf(__uint_as_float(x[i + 1]), mul, __uint_as_float(e[i + 1] << 16)) + off);
+            sum = fmaf(y.x, __uint_as_float(e[i] & 0xffff0000u), fmaf(y.y, __uint_as_float(e[i + 1] & 0xffff0000u), sum));
+            hi[i / 2] = Mma<PT>::pack(y.x, y.y);
+            if (SPLIT) {
+                const float2 f = fsub2(y, Mma<PT>::unpack(hi[i / 2]));
+                lo[i / 2] = Mma<PT>::pack(f.x, f.y);
+            }
+        }
+        const uint32_t pc = t_p + (c >> 1) * (SPLIT ? 32 : 16) + 8 * (c & 1);
+        tmem_st8(pc, hi);
+        if (SPLIT) tmem_st8(pc + 16, lo);
+    }
+    return make_float3(sum, m_ref, alpha);
+}
+
 // ----------------------------------------------------------------------------- the kernel
 
 template <int D, bool QUANT>
@@ -270,7 +342,7 @@ struct TreeGeo {
     // Registers move from the copying and converting warpgroups to the two softmax warpgroups: the launch's share is
     // 96 (640 threads) or 168 (384) each, and 256 * kMore + (kThreads - 256) * kLess is exactly that total.
     static constexpr int kThreads = QUANT ? 640 : 384;
-    static constexpr int kMore = QUANT ? 144 : 200, kLess = QUANT ? 64 : 104;
+    static constexpr int kMore = QUANT ? 120 : 200, kLess = QUANT ? 80 : 104;
     static_assert(256 * kMore + (kThreads - 256) * kLess == kThreads * (QUANT ? 96 : 168), "register split");
     // Q | K ring | V ring | raw ring | raw scales | exponents | row exchange | query exponents | barriers, small things
     static constexpr uint32_t oK = kTile, oV = oK + NS * kTile, oRaw = oV + NS * kTile, oRawSc = oRaw + NR * kRaw,
@@ -285,7 +357,8 @@ struct TreeGeo {
 
 template <typename T, int D, bool QUANT, bool SPLIT>
 __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
-    tree_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUtensorMap tm_q, const TreeParams p) {
+    tree_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUtensorMap tm_q,
+                const __grid_constant__ TreeParams p) {
     using Geo = TreeGeo<D, QUANT>;
     constexpr int NS = Geo::NS, NR = Geo::NR;
     constexpr int NK = D / 16, NT = kTKeys / 32;  // k-steps of S, and of each warpgroup's value product
@@ -691,10 +764,16 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                 const uint32_t t_s = lanes + (uint32_t)w * 64;
                 const int tp = SPLIT ? t - 1 : t - 2;  // the tile whose P this one's replaces
                 const bool masked = k0 + 64 > base;
-                uint32_t vis[2] = {0u, 0u};
-                if (masked && row_ok) {
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) vis[k] = tree_visible(p, g, tok, k0 + 32 * k - base);
+                uint32_t vis[2] = {0xffffffffu, 0xffffffffu};
+                if (masked) {
+#pragma unroll 1
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t v = row_ok ? tree_visible(p, g, tok, k0 + 32 * k - base) : 0u;
+                        if (k == 0)
+                            vis[0] = v;
+                        else
+                            vis[1] = v;
+                    }
                 }
                 if (QUANT)
                     ok = waited2(sfull, par, vfull + 8 * slot(t), ph(t)) && ok;  // scores, and the tile's exponents
@@ -709,9 +788,12 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                     }
                 }
                 float alpha = 1.f;
-                // kKeyed: every key has an exponent of its own (else E is the tile's)
-                auto probabilities = [&](auto keyed_c, float E) {
-                    constexpr bool kKeyed = decltype(keyed_c)::value;
+                auto p_free = [&]() {  // the products have read the P that this tile's replaces
+                    if (tp >= 0) ok = waited(pvd + 8 * (tp & 1), (uint32_t)((tp >> 1) & 1)) && ok;
+                    tc_fence_after();
+                };
+                // E is the exponent of every key: the scores stay in registers.
+                auto probabilities = [&](float mul, float E) {
                     uint32_t s[2][32];
                     tmem_ld32_async(t_s, s[0]);
                     tmem_ld32_async(t_s + 32, s[1]);
@@ -719,85 +801,34 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                     tmem_loaded(s[1]);
                     tc_fence_before();
                     if (lane == 0) mbar_arrive(sfree);  // (each load is the whole warp's)
-                    const uint32_t ex = sb + Geo::oExp + slot(t) * Geo::kExp + 4 * 64 * w;
-                    const float mul = QUANT ? cr * kmul[slot(t)] : cr;
-                    const float2 mul2 = make_float2(mul, mul);
-                    float y[64];  // raw scores; kKeyed: y
-#pragma unroll
-                    for (int k = 0; k < 64; k += 4) {
-                        const uint32_t* x = &s[k >> 5][k & 31];
-                        if constexpr (kKeyed) {
-                            uint32_t e[4];
-                            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                         : "=r"(e[0]), "=r"(e[1]), "=r"(e[2]), "=r"(e[3])
-                                         : "r"(ex + 4 * k));
-#pragma unroll
-                            for (int i = 0; i < 4; i += 2) {
-                                const float2 v = ffma2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), mul2,
-                                                       make_float2(__uint_as_float(e[i] << 16), __uint_as_float(e[i + 1] << 16)));
-                                y[k + i] = v.x;
-                                y[k + i + 1] = v.y;
-                            }
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) y[k + i] = __uint_as_float(x[i]);
-                        }
-                    }
-                    if (masked) {
-#pragma unroll
-                        for (int k = 0; k < 64; ++k) y[k] = vis[k >> 5] >> (k & 31) & 1u ? y[k] : NEG_INF;
-                    }
                     float mx[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
 #pragma unroll
                     for (int k = 0; k < 64; k += 8) {
-                        mx[0] = fmax3(mx[0], y[k], y[k + 1]);
-                        mx[1] = fmax3(mx[1], y[k + 2], y[k + 3]);
-                        mx[2] = fmax3(mx[2], y[k + 4], y[k + 5]);
-                        mx[3] = fmax3(mx[3], y[k + 6], y[k + 7]);
+                        const uint32_t* x = &s[k >> 5][k & 31];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            mx[i] = fmax3(mx[i], __uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
                     }
-                    float m_tile = fmax3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
-                    m_tile = (kKeyed ? m_tile : fmaf(m_tile, mul, E)) - kPHeadroom;  // (the scale is positive)
-                    const float m_new = m_tile > m_ref + 8.f || m_ref == NEG_INF ? fmaxf(m_ref, m_tile) : m_ref;
-                    if (j > g.j0 && m_new != m_ref) alpha = fast_exp2(m_ref - m_new);
-                    m_ref = m_new;
-                    const float off = (kKeyed ? 0.f : E) - (m_new == NEG_INF ? 0.f : m_new);
-                    const float2 off2 = make_float2(off, off);
-                    // P of 32 keys: 16 columns of pairs, and (SPLIT) the low parts in the next 16
+                    const float m_tile = fmaf(fmax3(mx[0], mx[1], fmaxf(mx[2], mx[3])), mul, E) - kPHeadroom;  // (mul > 0)
+                    const float off = E - tree_reference(m_tile, j == g.j0, m_ref, alpha);
+                    const float2 mul2 = make_float2(mul, mul), off2 = make_float2(off, off);
                     float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                     uint32_t hi[2][16], lo[2][16];
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-#pragma unroll
-                        for (int b = 0; b < 32; b += 4) {
-                            uint32_t e[4];
-                            if constexpr (kKeyed)
-                                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                             : "=r"(e[0]), "=r"(e[1]), "=r"(e[2]), "=r"(e[3])
-                                             : "r"(ex + 4 * (32 * k + b)));
-#pragma unroll
-                            for (int i = 0; i < 4; i += 2) {
-                                const float2 yy = make_float2(y[32 * k + b + i], y[32 * k + b + i + 1]);
-                                float2 x = kKeyed ? fadd2(yy, off2) : ffma2(yy, mul2, off2);
-                                x.x = fast_exp2(x.x);
-                                x.y = fast_exp2(x.y);
-                                float2& acc = ls[(i >> 1) & 1];
-                                if constexpr (kKeyed)
-                                    acc = ffma2(x, make_float2(__uint_as_float(e[i] & 0xffff0000u), __uint_as_float(e[i + 1] & 0xffff0000u)), acc);
-                                else
-                                    acc = fadd2(acc, x);
-                                const int at = (b + i) / 2;
-                                hi[k][at] = Mma<PT>::pack(x.x, x.y);
-                                if (SPLIT) {
-                                    const float2 f = fsub2(x, Mma<PT>::unpack(hi[k][at]));
-                                    lo[k][at] = Mma<PT>::pack(f.x, f.y);
-                                }
-                            }
+                    for (int k = 0; k < 64; k += 2) {
+                        float2 x = ffma2(make_float2(__uint_as_float(s[k >> 5][k & 31]), __uint_as_float(s[k >> 5][(k & 31) + 1])),
+                                         mul2, off2);
+                        x.x = fast_exp2(x.x);
+                        x.y = fast_exp2(x.y);
+                        ls[(k >> 1) & 1] = fadd2(ls[(k >> 1) & 1], x);
+                        const uint32_t h = Mma<PT>::pack(x.x, x.y);
+                        hi[k >> 5][(k & 31) / 2] = h;
+                        if (SPLIT) {
+                            const float2 f = fsub2(x, Mma<PT>::unpack(h));
+                            lo[k >> 5][(k & 31) / 2] = Mma<PT>::pack(f.x, f.y);
                         }
                     }
-                    if (tp >= 0) {  // its products have read it
-                        ok = waited(pvd + 8 * (tp & 1), (uint32_t)((tp >> 1) & 1)) && ok;
-                        tc_fence_after();
-                    }
+                    p_free();
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         tmem_st16(lanes + p_col(t, w, k), hi[k]);
@@ -805,30 +836,37 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                     }
                     const float2 lsum = fadd2(ls[0], ls[1]);
                     float sum = lsum.x + lsum.y;
-                    if (QUANT && !kKeyed) sum *= pow2i(-(int)E);
+                    if (QUANT) sum *= pow2i(-(int)E);
                     l = fmaf(l, alpha, sum);
                 };
                 if (warp_ok) {
-                    if constexpr (QUANT) {
-                        const float E = vexp[slot(t)];
-                        if (E == kTreeKeyed)
-                            probabilities(std::true_type{}, 0.f);
-                        else
-                            probabilities(std::false_type{}, E);
+                    const float mul = QUANT ? cr * kmul[slot(t)] : cr;
+                    const float E = QUANT ? vexp[slot(t)] : 0.f;
+                    if (masked) tree_mask_scores(t_s, vis[0], vis[1]);
+                    if (QUANT && E == kTreeKeyed) {
+                        p_free();
+                        const uint32_t ex = sb + Geo::oExp + slot(t) * Geo::kExp + 4 * 64 * w;
+                        const float3 r = tree_probabilities_keyed<PT, SPLIT>(t_s, lanes + p_col(t, w, 0), ex, mul, j == g.j0, m_ref);
+                        m_ref = r.y;
+                        alpha = r.z;
+                        tc_fence_before();
+                        if (lane == 0) mbar_arrive(sfree);
+                        l = fmaf(l, alpha, r.x);
                     } else {
-                        probabilities(std::false_type{}, 0.f);
+                        probabilities(mul, E);
                     }
                     // O_w is rescaled (rarely) once the last tile's products have landed
                     if (__any_sync(0xffffffffu, alpha != 1.f)) {
                         ok = waited(pvd + 8 * ((t - 1) & 1), (uint32_t)(((t - 1) >> 1) & 1)) && ok;
                         tc_fence_after();
 #pragma unroll 1
-                        for (int k = 0; k < D / 32; ++k) {
-                            float o[32];
-                            tmem_ld32(t_o + (uint32_t)w * D + k * 32, o);
+                        for (int k = 0; k < D; k += 16) {
+                            uint32_t o[16];
+                            tmem_ld16_async(t_o + (uint32_t)w * D + k, o);
+                            tmem_loaded16(o);
 #pragma unroll
-                            for (int b = 0; b < 32; ++b) o[b] *= alpha;
-                            tmem_st32(t_o + (uint32_t)w * D + k * 32, o);
+                            for (int b = 0; b < 16; ++b) o[b] = __float_as_uint(__uint_as_float(o[b]) * alpha);
+                            tmem_st16(t_o + (uint32_t)w * D + k, o);
                         }
                     }
                     tmem_wait_st();
