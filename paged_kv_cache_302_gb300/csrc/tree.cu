@@ -279,51 +279,54 @@ __device__ __forceinline__ float tree_reference(float m_tile, bool first, float&
     return m_new == -INFINITY ? 0.f : m_new;
 }
 
-// Probabilities of 64 keys with exponents of their own (packed bf16 pairs ev, 2^-ev at shared address ex).  Such tiles are
-// rare and are read twice, 16 columns at a time.  Returns the exponential sum.
+// Probabilities of 64 keys with exponents of their own (packed bf16 pairs ev, 2^-ev at shared address ex), over the scores
+// at t_s.  Such tiles are rare and are read twice, 32 columns at a time, out of line: with it in line the code of the usual
+// tiles left the instruction cache (a sixth of the time).  Returns the exponential sum, the reference, and the factor of what
+// was summed before.
 template <typename PT, bool SPLIT>
-__device__ __noinline__ float3 tree_probabilities_keyed(uint32_t t_s, uint32_t t_p, uint32_t ex, float mul, bool first,
-                                                        float m_ref) {
-    float alpha;
-    uint32_t x[16], e[16];
-    auto load = [&](int c) {
-        tmem_ld16_async(t_s + 16 * c, x);
-#pragma unroll
-        for (int i = 0; i < 16; i += 4)
-            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(e[i]), "=r"(e[i + 1]), "=r"(e[i + 2]), "=r"(e[i + 3])
-                         : "r"(ex + 4 * (16 * c + i)));
-        tmem_loaded16(x);
+__device__ __noinline__ float3 tree_probabilities_keyed(uint32_t t_s, uint32_t ex, float mul, bool first, float m_ref) {
+    uint32_t x[32] = {}, e[4] = {};
+    auto exponents = [&](int at) {
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(e[0]), "=r"(e[1]), "=r"(e[2]), "=r"(e[3])
+                     : "r"(ex + 4 * at));
     };
-    float m_tile = -INFINITY;
+    auto score = [&](int i, int k) { return fmaf(__uint_as_float(x[i + k]), mul, __uint_as_float(e[k] << 16)); };
+    float m_tile = -INFINITY, alpha, sum = 0.f;
 #pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
-        load(c);
+    for (int c = 0; c < 64; c += 32) {
+        tmem_ld32_async(t_s + c, x);
+        tmem_loaded(x);
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            m_tile = fmaxf(m_tile, fmaf(__uint_as_float(x[i]), mul, __uint_as_float(e[i] << 16)));
+        for (int i = 0; i < 32; i += 4) {
+            exponents(c + i);
+            m_tile = fmax3(fmax3(m_tile, score(i, 0), score(i, 1)), score(i, 2), score(i, 3));
+        }
     }
     const float off = -tree_reference(m_tile - kPHeadroom, first, m_ref, alpha);
-    float sum = 0.f;
 #pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
-        load(c);
-        uint32_t hi[8], lo[8];
+    for (int c = 0; c < 64; c += 32) {
+        tmem_ld32_async(t_s + c, x);
+        tmem_loaded(x);
+        uint32_t hi[16], lo[16];
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-            float2 y;
-            y.x = fast_exp2(fmaf(__uint_as_float(x[i]), mul, __uint_as_float(e[i] << 16)) + off);
-            y.y = fast_exp2(fmaf(__uint_as_float(x[i + 1]), mul, __uint_as_float(e[i + 1] << 16)) + off);
-            sum = fmaf(y.x, __uint_as_float(e[i] & 0xffff0000u), fmaf(y.y, __uint_as_float(e[i + 1] & 0xffff0000u), sum));
-            hi[i / 2] = Mma<PT>::pack(y.x, y.y);
-            if (SPLIT) {
-                const float2 f = fsub2(y, Mma<PT>::unpack(hi[i / 2]));
-                lo[i / 2] = Mma<PT>::pack(f.x, f.y);
+        for (int i = 0; i < 32; i += 4) {
+            exponents(c + i);
+#pragma unroll
+            for (int k = 0; k < 4; k += 2) {
+                const float2 y = make_float2(fast_exp2(score(i, k) + off), fast_exp2(score(i, k + 1) + off));
+                sum = fmaf(y.x, __uint_as_float(e[k] & 0xffff0000u), fmaf(y.y, __uint_as_float(e[k + 1] & 0xffff0000u), sum));
+                const uint32_t h = Mma<PT>::pack(y.x, y.y);
+                hi[(i + k) / 2] = h;
+                if (SPLIT) {
+                    const float2 f = fsub2(y, Mma<PT>::unpack(h));
+                    lo[(i + k) / 2] = Mma<PT>::pack(f.x, f.y);
+                }
             }
         }
-        const uint32_t pc = t_p + (c >> 1) * (SPLIT ? 32 : 16) + 8 * (c & 1);
-        tmem_st8(pc, hi);
-        if (SPLIT) tmem_st8(pc + 16, lo);
+        const uint32_t at = t_s + (SPLIT ? c : c / 2);  // columns whose scores have been read
+        tmem_st16(at, hi);
+        if (SPLIT) tmem_st16(at + 16, lo);
     }
     return make_float3(sum, m_ref, alpha);
 }
@@ -372,11 +375,11 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t sb = smem_addr(smem_raw);
     const uint32_t sQ = sb, sK = sb + Geo::oK, sV = sb + Geo::oV, sBar = sb + Geo::oBar;
-    // prdy, pvd: for tiles of either parity (with one P buffer as with two)
+    // sfull, prdy, pvd: one for each of the two buffers of scores
     const uint32_t qfull = sBar, qfree = qfull + 8, qread = qfree + 8, sdone = qread + 8, pdone = sdone + 8,
                    kfull = pdone + 8, kfree = kfull + 8 * NS,
-                   vfull = kfree + 8 * NS, vfree = vfull + 8 * NS, sfull = vfree + 8 * NS, sfree = sfull + 8,
-                   pvd = sfree + 8, prdy = pvd + 16, rfull = prdy + 16, rfree = rfull + 8 * NR;
+                   vfull = kfree + 8 * NS, vfree = vfull + 8 * NS, sfull = vfree + 8 * NS, pvd = sfull + 16,
+                   prdy = pvd + 16, rfull = prdy + 16, rfree = rfull + 8 * NR;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_raw + Geo::oSmall);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     volatile int* armed = abort_flag + 1;  // K, V (quantised: raw) tiles and query tiles whose copies have been issued
@@ -405,7 +408,6 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
     }
     if (tid == 0) {
         for (int i = 0; i < Geo::kBars; ++i) mbar_init(sBar + 8 * i, 1);
-        mbar_init(sfree, 8);  // one arrival per softmax warp
         mbar_init(prdy, 256);
         mbar_init(prdy + 8, 256);
         if (QUANT) {
@@ -437,11 +439,10 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
         const bool wa = mbar_try_wait(a, pa), wb = mbar_try_wait(b, pb);
         return (wa || waited(a, pa)) && (wb || waited(b, pb));
     };
-    // TMEM columns of P, warpgroup w's 32 keys k of tile t: one buffer of 128 (high parts in 16, low parts in the next 16)
-    // or two of 64 in turn
-    auto p_col = [](int t, int w, int k) {
-        return (uint32_t)(SPLIT ? kTKeys + w * 64 + k * 32 : kTKeys + (t & 1) * 64 + w * 32 + k * 16);
-    };
+    // TMEM columns: the scores of tile t, and on top of a warpgroup's own 64 the P of its 32 keys k (high parts in 16, then
+    // low parts in 16)
+    auto s_col = [](int t) { return (uint32_t)((t & 1) * kTKeys); };
+    auto p_col = [&](int t, int w, int k) { return s_col(t) + (uint32_t)(w * 64 + k * (SPLIT ? 32 : 16)); };
     auto slot = [](int i) { return (uint32_t)(i % NS); };
     auto ph = [](int i) { return (uint32_t)((i / NS) & 1); };
     bool ok = true;
@@ -525,16 +526,17 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                 for (int seg = 0; ok && walk.next(p, g); ++seg) {
                     ok = waited(qfull, (uint32_t)(seg & 1));
                     for (int j = g.j0; j < g.j1 && ok; ++j, ++t) {
-                        // S is free once the softmax has read the last tile's into registers
-                        ok = t == 0 ? waited(kfull, 0) : waited2(sfree, (uint32_t)((t - 1) & 1), kfull + 8 * slot(t), ph(t));
+                        // the buffer is free once the value products of the tile before last have read its P
+                        ok = t < 2 ? waited(kfull + 8 * slot(t), ph(t))
+                                   : waited2(pvd + 8 * (t & 1), (uint32_t)((t - 2) >> 1 & 1), kfull + 8 * slot(t), ph(t));
                         if (!ok) break;
                         tc_fence_after();
                         const uint64_t dk = umma_desc(sK + slot(t) * kTile, 16, kGroup);
 #pragma unroll
                         for (int ks = 0; ks < NK; ++ks)
-                            umma_f16(tmem, dq + (ks >> 2) * (kTRegion >> 4) + (ks & 3) * 2,
+                            umma_f16(tmem + s_col(t), dq + (ks >> 2) * (kTRegion >> 4) + (ks & 3) * 2,
                                      dk + (ks >> 2) * (1024 >> 4) + (ks & 3) * 2, idesc_s, ks > 0);
-                        umma_commit(sfull);
+                        umma_commit(sfull + 8 * (t & 1));
                         umma_commit(kfree + 8 * slot(t));
                     }
                     umma_commit(qfree);
@@ -654,15 +656,8 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                         uint32_t u[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
                         const bool masked = k0 + kTKeys > g.ctx - g.n;
                         if (masked) tree_union<4>(p, g, k0, u);  // keys past the context are in none
-                        // the raw tile, and room for it: one wait (the value products of tile t - 2 end long before)
                         const uint32_t sl = slot(t);
-                        if (t < NS) {
-                            ok = waited(rfull + 8 * rb, (uint32_t)((t / NR) & 1)) && ok;
-                        } else {
-                            const bool k = mbar_try_wait(kfree + 8 * sl, ph(t - NS));
-                            ok = waited2(rfull + 8 * rb, (uint32_t)((t / NR) & 1), vfree + 8 * sl, ph(t - NS)) && ok;
-                            if (!k) ok = waited(kfree + 8 * sl, ph(t - NS)) && ok;
-                        }
+                        ok = waited(rfull + 8 * rb, (uint32_t)((t / NR) & 1)) && ok;
                         // lane: keys 4 lane .. + 3, all of one block; the largest exponents of the keys that are seen
                         const uint32_t at = rsc + 4 * lane + ((4 * lane) & mb);
                         uint32_t kb, vb;
@@ -696,6 +691,7 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
 #pragma unroll 1
                         for (int which = 0; which < 2; ++which) {
                             const uint32_t f2 = which ? fv : fk;
+                            if (t >= NS) ok = waited((which ? vfree : kfree) + 8 * sl, ph(t - NS)) && ok;
                             const uint32_t src = raw + so + (which ? B * D : 0), dst = (which ? sV : sK) + sl * kTile + to;
                             uint4 vs[D / 32];  // all read before the first is converted
 #pragma unroll
@@ -760,9 +756,8 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
             float m_ref = NEG_INF, l = 0.f;
             for (int j = g.j0; j < g.j1; ++j, ++t) {
                 const int k0 = j * kTKeys + 64 * w;  // the warpgroup's first key
-                const uint32_t par = (uint32_t)(t & 1);
-                const uint32_t t_s = lanes + (uint32_t)w * 64;
-                const int tp = SPLIT ? t - 1 : t - 2;  // the tile whose P this one's replaces
+                const uint32_t par = (uint32_t)(t >> 1 & 1);
+                const uint32_t t_s = lanes + s_col(t) + (uint32_t)w * 64;
                 const bool masked = k0 + 64 > base;
                 uint32_t vis[2] = {0xffffffffu, 0xffffffffu};
                 if (masked) {
@@ -776,9 +771,9 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                     }
                 }
                 if (QUANT)
-                    ok = waited2(sfull, par, vfull + 8 * slot(t), ph(t)) && ok;  // scores, and the tile's exponents
+                    ok = waited2(sfull + 8 * (t & 1), par, vfull + 8 * slot(t), ph(t)) && ok;  // scores, and the tile's exponents
                 else
-                    ok = waited(sfull, par) && ok;
+                    ok = waited(sfull + 8 * (t & 1), par) && ok;
                 tc_fence_after();
                 if (QUANT) {
                     if (j == g.j0) {
@@ -788,10 +783,6 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                     }
                 }
                 float alpha = 1.f;
-                auto p_free = [&]() {  // the products have read the P that this tile's replaces
-                    if (tp >= 0) ok = waited(pvd + 8 * (tp & 1), (uint32_t)((tp >> 1) & 1)) && ok;
-                    tc_fence_after();
-                };
                 // E is the exponent of every key: the scores stay in registers.
                 auto probabilities = [&](float mul, float E) {
                     uint32_t s[2][32];
@@ -799,8 +790,6 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                     tmem_ld32_async(t_s + 32, s[1]);
                     tmem_loaded(s[0]);
                     tmem_loaded(s[1]);
-                    tc_fence_before();
-                    if (lane == 0) mbar_arrive(sfree);  // (each load is the whole warp's)
                     float mx[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
 #pragma unroll
                     for (int k = 0; k < 64; k += 8) {
@@ -828,7 +817,6 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                             lo[k >> 5][(k & 31) / 2] = Mma<PT>::pack(f.x, f.y);
                         }
                     }
-                    p_free();
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         tmem_st16(lanes + p_col(t, w, k), hi[k]);
@@ -844,13 +832,10 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                     const float E = QUANT ? vexp[slot(t)] : 0.f;
                     if (masked) tree_mask_scores(t_s, vis[0], vis[1]);
                     if (QUANT && E == kTreeKeyed) {
-                        p_free();
                         const uint32_t ex = sb + Geo::oExp + slot(t) * Geo::kExp + 4 * 64 * w;
-                        const float3 r = tree_probabilities_keyed<PT, SPLIT>(t_s, lanes + p_col(t, w, 0), ex, mul, j == g.j0, m_ref);
+                        const float3 r = tree_probabilities_keyed<PT, SPLIT>(t_s, ex, mul, j == g.j0, m_ref);
                         m_ref = r.y;
                         alpha = r.z;
-                        tc_fence_before();
-                        if (lane == 0) mbar_arrive(sfree);
                         l = fmaf(l, alpha, r.x);
                     } else {
                         probabilities(mul, E);
@@ -870,10 +855,6 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                         }
                     }
                     tmem_wait_st();
-                } else {
-                    if (lane == 0) mbar_arrive(sfree);
-                    // in step with the others: prdy counts every thread
-                    if (tp >= 0) ok = waited(pvd + 8 * (tp & 1), (uint32_t)((tp >> 1) & 1)) && ok;
                 }
                 if (!QUANT && masked) {
                     // V rows nobody sees (past the context, padding) may hold anything, even NaN: zeros before the
