@@ -279,19 +279,19 @@ __device__ __forceinline__ float tree_reference(float m_tile, bool first, float&
     return m_new == -INFINITY ? 0.f : m_new;
 }
 
-// Probabilities of 64 keys with exponents of their own (packed bf16 pairs ev, 2^-ev at shared address ex), over the scores
+// Probabilities of 64 keys with exponents of their own (scale bytes at shared address ex), over the scores
 // at t_s.  Such tiles are rare and are read twice, 32 columns at a time, out of line: with it in line the code of the usual
 // tiles left the instruction cache (a sixth of the time).  Returns the exponential sum, the reference, and the factor of what
 // was summed before.
 template <typename PT, bool SPLIT>
 __device__ __noinline__ float3 tree_probabilities_keyed(uint32_t t_s, uint32_t ex, float mul, bool first, float m_ref) {
-    uint32_t x[32] = {}, e[4] = {};
-    auto exponents = [&](int at) {
-        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(e[0]), "=r"(e[1]), "=r"(e[2]), "=r"(e[3])
-                     : "r"(ex + 4 * at));
+    uint32_t x[32] = {}, e = 0;
+    // of four neighbouring keys: their bytes; y = score + ev, and 2^-ev
+    auto exponents = [&](int at) { asm volatile("ld.shared.u32 %0, [%1];" : "=r"(e) : "r"(ex + at)); };
+    auto score = [&](int i, int k) {
+        return fmaf(__uint_as_float(x[i + k]), mul, (float)((int)(e >> 8 * k & 0xffu) - kScaleBias));
     };
-    auto score = [&](int i, int k) { return fmaf(__uint_as_float(x[i + k]), mul, __uint_as_float(e[k] << 16)); };
+    auto weight = [&](int k) { return pow2i(kScaleBias - (int)(e >> 8 * k & 0xffu)); };
     float m_tile = -INFINITY, alpha, sum = 0.f;
 #pragma unroll 1
     for (int c = 0; c < 64; c += 32) {
@@ -315,7 +315,7 @@ __device__ __noinline__ float3 tree_probabilities_keyed(uint32_t t_s, uint32_t e
 #pragma unroll
             for (int k = 0; k < 4; k += 2) {
                 const float2 y = make_float2(fast_exp2(score(i, k) + off), fast_exp2(score(i, k + 1) + off));
-                sum = fmaf(y.x, __uint_as_float(e[k] & 0xffff0000u), fmaf(y.y, __uint_as_float(e[k + 1] & 0xffff0000u), sum));
+                sum = fmaf(y.x, weight(k), fmaf(y.y, weight(k + 1), sum));
                 const uint32_t h = Mma<PT>::pack(y.x, y.y);
                 hi[(i + k) / 2] = h;
                 if (SPLIT) {
@@ -338,20 +338,22 @@ struct TreeGeo {
     static constexpr int DH = D / 64;
     static constexpr uint32_t kTile = DH * kTRegion;      // one 16-bit tile, [8-row group][column half][8 rows][128 B]
     static constexpr uint32_t kGroup = DH * 1024;
-    static constexpr int NS = QUANT ? 2 : 3;              // K and V ring slots
-    static constexpr int NR = QUANT ? (D == 128 ? 2 : 4) : 0;      // raw ring slots: K and V rows of a tile, scales
+    // V ring slots and K ring slots.  A converted K tile is free again as soon as its score product is done, long before
+    // its V: one slot serves, and the space holds another raw tile on its way.
+    static constexpr int NS = QUANT ? 2 : 3, KS = QUANT ? 1 : 3;
+    static constexpr int NR = QUANT ? (D == 128 ? 3 : 6) : 0;      // raw ring slots: K and V rows of a tile, scales
     static constexpr uint32_t kRaw = 2u * kTKeys * D, kRawScales = 2 * kTKeys;
-    static constexpr uint32_t kExp = QUANT ? kTKeys * 4 : 0;       // per V slot: each key's ev and 2^-ev, as bf16
+    static constexpr uint32_t kExp = QUANT ? kTKeys : 0;           // per V slot: each key's scale byte of V
     // Registers move from the copying and converting warpgroups to the two softmax warpgroups: the launch's share is
     // 96 (640 threads) or 168 (384) each, and 256 * kMore + (kThreads - 256) * kLess is exactly that total.
     static constexpr int kThreads = QUANT ? 640 : 384;
     static constexpr int kMore = QUANT ? 120 : 200, kLess = QUANT ? 80 : 104;
     static_assert(256 * kMore + (kThreads - 256) * kLess == kThreads * (QUANT ? 96 : 168), "register split");
     // Q | K ring | V ring | raw ring | raw scales | exponents | row exchange | query exponents | barriers, small things
-    static constexpr uint32_t oK = kTile, oV = oK + NS * kTile, oRaw = oV + NS * kTile, oRawSc = oRaw + NR * kRaw,
+    static constexpr uint32_t oK = kTile, oV = oK + KS * kTile, oRaw = oV + NS * kTile, oRawSc = oRaw + NR * kRaw,
                               oExp = oRawSc + NR * kRawScales, oXch = oExp + NS * kExp, oQe = oXch + 2 * kTRows * 4,
                               oBar = oQe + (QUANT ? kTRows : 0);
-    static constexpr int kBars = 5 + 4 * NS + 6 + 2 * NR;
+    static constexpr int kBars = 5 + 2 * KS + 2 * NS + 6 + 2 * NR;
     static constexpr uint32_t oSmall = oBar + 8 * kBars;
     static constexpr size_t kSmem = oSmall + 48;
     static_assert(kSmem <= 232448, "shared memory");
@@ -363,7 +365,7 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
     tree_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUtensorMap tm_q,
                 const __grid_constant__ TreeParams p) {
     using Geo = TreeGeo<D, QUANT>;
-    constexpr int NS = Geo::NS, NR = Geo::NR;
+    constexpr int NS = Geo::NS, KS = Geo::KS, NR = Geo::NR;
     constexpr int NK = D / 16, NT = kTKeys / 32;  // k-steps of S, and of each warpgroup's value product
     constexpr bool kBf16 = !QUANT && std::is_same<T, __nv_bfloat16>::value;  // type of the products
     using PT = typename std::conditional<kBf16, __nv_bfloat16, __half>::type;
@@ -377,8 +379,8 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
     const uint32_t sQ = sb, sK = sb + Geo::oK, sV = sb + Geo::oV, sBar = sb + Geo::oBar;
     // sfull, prdy, pvd: one for each of the two buffers of scores
     const uint32_t qfull = sBar, qfree = qfull + 8, qread = qfree + 8, sdone = qread + 8, pdone = sdone + 8,
-                   kfull = pdone + 8, kfree = kfull + 8 * NS,
-                   vfull = kfree + 8 * NS, vfree = vfull + 8 * NS, sfull = vfree + 8 * NS, pvd = sfull + 16,
+                   kfull = pdone + 8, kfree = kfull + 8 * KS,
+                   vfull = kfree + 8 * KS, vfree = vfull + 8 * NS, sfull = vfree + 8 * NS, pvd = sfull + 16,
                    prdy = pvd + 16, rfull = prdy + 16, rfree = rfull + 8 * NR;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_raw + Geo::oSmall);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -413,10 +415,8 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
         if (QUANT) {
             mbar_init(qfull, kConvWarps);
             mbar_init(qread, 8);
-            for (int i = 0; i < NS; ++i) {
-                mbar_init(kfull + 8 * i, kConvWarps);
-                mbar_init(vfull + 8 * i, kConvWarps);
-            }
+            for (int i = 0; i < KS; ++i) mbar_init(kfull + 8 * i, kConvWarps);
+            for (int i = 0; i < NS; ++i) mbar_init(vfull + 8 * i, kConvWarps);
             for (int i = 0; i < NR; ++i) mbar_init(rfree + 8 * i, kConvWarps);
         }
         *abort_flag = 0;
@@ -445,6 +445,8 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
     auto p_col = [&](int t, int w, int k) { return s_col(t) + (uint32_t)(w * 64 + k * (SPLIT ? 32 : 16)); };
     auto slot = [](int i) { return (uint32_t)(i % NS); };
     auto ph = [](int i) { return (uint32_t)((i / NS) & 1); };
+    auto kslot = [](int i) { return (uint32_t)(i % KS); };
+    auto kph = [](int i) { return (uint32_t)((i / KS) & 1); };
     bool ok = true;
     TreeWalk walk;
     walk.start(p, run.s, run.rem, run.hi - run.lo);
@@ -527,17 +529,17 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                     ok = waited(qfull, (uint32_t)(seg & 1));
                     for (int j = g.j0; j < g.j1 && ok; ++j, ++t) {
                         // the buffer is free once the value products of the tile before last have read its P
-                        ok = t < 2 ? waited(kfull + 8 * slot(t), ph(t))
-                                   : waited2(pvd + 8 * (t & 1), (uint32_t)((t - 2) >> 1 & 1), kfull + 8 * slot(t), ph(t));
+                        ok = t < 2 ? waited(kfull + 8 * kslot(t), kph(t))
+                                   : waited2(pvd + 8 * (t & 1), (uint32_t)((t - 2) >> 1 & 1), kfull + 8 * kslot(t), kph(t));
                         if (!ok) break;
                         tc_fence_after();
-                        const uint64_t dk = umma_desc(sK + slot(t) * kTile, 16, kGroup);
+                        const uint64_t dk = umma_desc(sK + kslot(t) * kTile, 16, kGroup);
 #pragma unroll
                         for (int ks = 0; ks < NK; ++ks)
                             umma_f16(tmem + s_col(t), dq + (ks >> 2) * (kTRegion >> 4) + (ks & 3) * 2,
                                      dk + (ks >> 2) * (1024 >> 4) + (ks & 3) * 2, idesc_s, ks > 0);
                         umma_commit(sfull + 8 * (t & 1));
-                        umma_commit(kfree + 8 * slot(t));
+                        umma_commit(kfree + 8 * kslot(t));
                     }
                     umma_commit(qfree);
                 }
@@ -691,8 +693,9 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
 #pragma unroll 1
                         for (int which = 0; which < 2; ++which) {
                             const uint32_t f2 = which ? fv : fk;
-                            if (t >= NS) ok = waited((which ? vfree : kfree) + 8 * sl, ph(t - NS)) && ok;
-                            const uint32_t src = raw + so + (which ? B * D : 0), dst = (which ? sV : sK) + sl * kTile + to;
+                            if (t >= (which ? NS : KS))
+                                ok = waited(which ? vfree + 8 * sl : kfree + 8 * kslot(t), which ? ph(t - NS) : kph(t - KS)) && ok;
+                            const uint32_t src = raw + so + (which ? B * D : 0), dst = (which ? sV + sl * kTile : sK + kslot(t) * kTile) + to;
                             uint4 vs[D / 32];  // all read before the first is converted
 #pragma unroll
                             for (int cc = 0; cc < D / 32; ++cc)
@@ -720,17 +723,14 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                                                  "r"(h[4 * o]), "r"(h[4 * o + 1]), "r"(h[4 * o + 2]), "r"(h[4 * o + 3])
                                                  : "memory");
                             }
-                            if (which && keyed && c0 == 0)  // both exact in bf16: the upper halves of the fp32 values
-                                reinterpret_cast<uint32_t*>(smem_raw + Geo::oExp + sl * Geo::kExp)[row] =
-                                    __float_as_uint((float)(ev - kScaleBias)) >> 16 |
-                                    (__float_as_uint(pow2i(kScaleBias - ev)) & 0xffff0000u);
+                            if (which && keyed && c0 == 0) smem_raw[Geo::oExp + sl * Geo::kExp + row] = (uint8_t)ev;
                             if (which && cw == 0 && lane == 0) {
                                 kmul[sl] = pow2i(em - kScaleBias - 7);
                                 vexp[sl] = keyed ? kTreeKeyed : (float)(vm - kScaleBias - 7);
                             }
                             fence_proxy_async_smem();
                             __syncwarp();
-                            if (lane == 0) mbar_arrive((which ? vfull : kfull) + 8 * sl);
+                            if (lane == 0) mbar_arrive(which ? vfull + 8 * sl : kfull + 8 * kslot(t));
                         }
                         if (lane == 0) mbar_arrive(rfree + 8 * rb);
                     }
@@ -832,7 +832,7 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                     const float E = QUANT ? vexp[slot(t)] : 0.f;
                     if (masked) tree_mask_scores(t_s, vis[0], vis[1]);
                     if (QUANT && E == kTreeKeyed) {
-                        const uint32_t ex = sb + Geo::oExp + slot(t) * Geo::kExp + 4 * 64 * w;
+                        const uint32_t ex = sb + Geo::oExp + slot(t) * Geo::kExp + 64 * w;
                         const float3 r = tree_probabilities_keyed<PT, SPLIT>(t_s, ex, mul, j == g.j0, m_ref);
                         m_ref = r.y;
                         alpha = r.z;
