@@ -309,7 +309,7 @@ pa_status pa_decode_quant(void* out, pa_dtype out_dtype, const void* q, pa_dtype
  * contents need not be initialised, not shared by calls that overlap on the GPU.
  * Results do not depend on the order in which the GPU runs the call's parts.
  * Supported: q_dtype F16/BF16, D in {64, 128}, B in {8, 16, 32}, H_q / H_kv <=
- * 128, N <= 65535, NB*B < 2^31, scale > 0.
+ * 128, N <= 65535, NB*B < 2^31, scale > 0 and finite.
  * ---------------------------------------------------------------------- */
 size_t pa_decode_tree_workspace_bytes(int N, int H_q, int H_kv, int D, int max_q_len);
 pa_status pa_decode_tree(void* out, pa_dtype out_dtype, const void* q, pa_dtype q_dtype, const void* pool,

@@ -1,5 +1,6 @@
 // capi.cpp -- argument validation and dispatch for the device entry points of pa.h.
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
@@ -401,7 +402,7 @@ pa_status pa_decode_tree(void* out, pa_dtype out_dtype, const void* q, pa_dtype 
     if (max_q_len > 32LL * mask_words)
         return fail(PA_ERR_INVALID, "a mask of %d words per row holds %lld drafted tokens, max_q_len is %d", mask_words,
                     32LL * mask_words, max_q_len);
-    if (!(scale > 0.f)) return fail(PA_ERR_INVALID, "scale must be positive");
+    if (!(scale > 0.f && scale < HUGE_VALF)) return fail(PA_ERR_INVALID, "scale must be positive and finite");
     if (T == 0 || max_q_len == 0) return PA_OK;
     if (!out || !q || !pool || !block_tables || !ctx_lens || !q_start || !tree_mask || !workspace)
         return fail(PA_ERR_INVALID, "null pointer argument");

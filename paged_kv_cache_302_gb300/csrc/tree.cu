@@ -11,18 +11,28 @@
 // A CTA leaves at most two (its first and its last segment), so the workspace has a fixed size.  Roles:
 //   * warps 0-3 and 4-7, two softmax warpgroups: warpgroup w takes keys 64 w .. 64 w + 63 of every tile; each thread owns
 //     one TMEM lane = one query row.  It reads its 64 scores (tcgen05.ld), masks, keeps a running maximum of its own
-//     (its O is rescaled only when that grows by more than 2^8) and writes the probabilities to TMEM.  The warpgroups have accumulators of their own, O_0 and O_1, joined at the segment's end, so they never wait for one
-//     another in between;
+//     (its O is rescaled only when that grows by more than 2^8) and writes the probabilities to TMEM, over the scores it
+//     has just read.  The warpgroups have accumulators of their own, O_0 and O_1, joined at the segment's end, so they
+//     never wait for one another in between;
 //   * warp 8 (TMA): query rows (16-bit pool), K and V tiles into rings, block by block through the block table;
-//   * warp 9 (one thread): S = Q K^T (TMEM columns 0 .. 127) of the next tile as soon as the softmax has read this one's
-//     into registers; warp 10 (one thread): O_w += P_w V (columns 256 + D w), P read from TMEM (columns 128 .. 255);
+//   * warp 9 (one thread): S = Q K^T into one of two buffers (TMEM columns 0 .. 127 and 128 .. 255), so that a tile's score
+//     product runs under the softmax of the tile before it; warp 10 (one thread): O_w += P_w V (columns 256 + D w), P read
+//     from TMEM;
 //   * quantised pool, warps 12-19: e4m3 tiles from the raw ring to fp16 tiles in the K and V rings, and the query rows.
 // The value product takes P in V's 16-bit type: for bf16, or an fp32 output, as a high and a low part (two products).
 //
 // Quantised pool: query rows are scaled to fp16's range by a power of two (exact); K8 is converted to fp16 times 2^(ek -
 // emax + 7), emax the tile's largest exponent (keys 2^22 below it count as zero: a score is off by at most 2^-22 of the
-// largest that a key of the tile could give), V8 likewise where that is exact (see kTreeSpan); with E the exponent taken out of V (per tile, else per key): y =
-// raw c 2^(emax - 7) + E, p = 2^(y - M), O += p (V 2^-E), l += p 2^-E, as in decode_quant.cu.
+// largest that a key of the tile could give), V8 likewise where that is exact (see kTreeSpan); with E the exponent taken
+// out of V (per tile, else per key): y = raw c 2^(emax - 7) + E, p = 2^(y - M), O += p (V 2^-E), l += p 2^-E, as in
+// decode_quant.cu.
+//
+// What bounds it, measured at D = 128.  64 sequences with trees of up to 24 tokens, 32 / 8 heads, bf16: 89 us, 4.8 TB/s of
+// K and V (the bytes alone are 64 us; without the products it takes 85: the rest is the start and end of 512 units).  16
+// trees of up to 63 tokens over 4500 quantised tokens each: 115 us, about 2900 cycles per tile of 128 x 128, of which
+// leaving out the conversion to fp16 saves 900, the softmax 300, both products 150; what is left are the waits from role to
+// role.  What the time was spent on before: one score buffer (128 us), spin waits unrolled by the compiler and masked or
+// keyed tiles in line, which pushed the usual tile's code out of the instruction cache (180 us).
 #include <algorithm>
 #include <cstring>
 #include <type_traits>
@@ -38,8 +48,9 @@ constexpr int kTKeys = 128;    // keys per tile (N of S, K of P V)
 constexpr uint32_t kTRegion = kTRows * 128;  // [128 rows][64 columns] 16-bit, 128-byte swizzled
 constexpr uint32_t kTTmem = 512;
 constexpr int kTreeMaxCtas = 160;  // CTAs of a call at most (the workspace holds two partial results for each)
-// Cost of a unit's start and end (query rows, first scores, joining the warpgroups, storing) in key tiles.
-constexpr int kTreeUnitCost = 3;
+// Cost of a unit's start and end (query rows, first scores, joining the warpgroups, storing) in key tiles.  Two to four
+// make no difference (512 units of 13 tiles: 89, 91, 91 us; 6: 97).
+constexpr int kTreeUnitCost = 2;
 constexpr int kConvWarps = 8;
 // Probabilities are relative to a reference kPHeadroom below the row's maximum, which may grow by 2^8 before O is
 // rescaled: they reach 2^15, the top of fp16's range, so that the smallest keep as many bits as fp16 allows (an absolute
@@ -541,7 +552,7 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                         umma_commit(sfull + 8 * (t & 1));
                         umma_commit(kfree + 8 * kslot(t));
                     }
-                    umma_commit(qfree);
+                    if (ok) umma_commit(qfree);  // (never before the rows have landed)
                 }
                 umma_commit(sdone);  // arrives once every product issued above has completed
             }
@@ -694,8 +705,10 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                         for (int which = 0; which < 2; ++which) {
                             const uint32_t f2 = which ? fv : fk;
                             if (t >= (which ? NS : KS))
-                                ok = waited(which ? vfree + 8 * sl : kfree + 8 * kslot(t), which ? ph(t - NS) : kph(t - KS)) && ok;
-                            const uint32_t src = raw + so + (which ? B * D : 0), dst = (which ? sV + sl * kTile : sK + kslot(t) * kTile) + to;
+                                ok = waited(which ? vfree + 8 * sl : kfree + 8 * kslot(t),
+                                            which ? ph(t - NS) : kph(t - KS)) && ok;
+                            const uint32_t src = raw + so + (which ? B * D : 0);
+                            const uint32_t dst = (which ? sV + sl * kTile : sK + kslot(t) * kTile) + to;
                             uint4 vs[D / 32];  // all read before the first is converted
 #pragma unroll
                             for (int cc = 0; cc < D / 32; ++cc)
@@ -732,7 +745,7 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                             __syncwarp();
                             if (lane == 0) mbar_arrive(which ? vfull + 8 * sl : kfull + 8 * kslot(t));
                         }
-                        if (lane == 0) mbar_arrive(rfree + 8 * rb);
+                        if (lane == 0 && ok) mbar_arrive(rfree + 8 * rb);  // (never before its copies have landed)
                     }
                 }
             }
@@ -770,8 +783,8 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                             vis[1] = v;
                     }
                 }
-                if (QUANT)
-                    ok = waited2(sfull + 8 * (t & 1), par, vfull + 8 * slot(t), ph(t)) && ok;  // scores, and the tile's exponents
+                if (QUANT)  // scores, and the tile's exponents
+                    ok = waited2(sfull + 8 * (t & 1), par, vfull + 8 * slot(t), ph(t)) && ok;
                 else
                     ok = waited(sfull + 8 * (t & 1), par) && ok;
                 tc_fence_after();
@@ -805,8 +818,8 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                     uint32_t hi[2][16], lo[2][16];
 #pragma unroll
                     for (int k = 0; k < 64; k += 2) {
-                        float2 x = ffma2(make_float2(__uint_as_float(s[k >> 5][k & 31]), __uint_as_float(s[k >> 5][(k & 31) + 1])),
-                                         mul2, off2);
+                        const uint32_t* y = &s[k >> 5][k & 31];
+                        float2 x = ffma2(make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])), mul2, off2);
                         x.x = fast_exp2(x.x);
                         x.y = fast_exp2(x.y);
                         ls[(k >> 1) & 1] = fadd2(ls[(k >> 1) & 1], x);
@@ -890,7 +903,8 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
             const float l_other = xch[(w ^ 1) * kTRows + r];
             asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
             const float M = fmaxf(m_ref, m_other);
-            const float fo = m_ref == NEG_INF ? 0.f : fast_exp2(m_ref - M), fx = m_other == NEG_INF ? 0.f : fast_exp2(m_other - M);
+            const float fo = m_ref == NEG_INF ? 0.f : fast_exp2(m_ref - M);
+            const float fx = m_other == NEG_INF ? 0.f : fast_exp2(m_other - M);
             const float f0 = w ? fx : fo, f1 = w ? fo : fx;
             // both warps sum in the same order (a NaN exponential sum stays one)
             const float den = w ? l_other * f0 + l * f1 : l * f0 + l_other * f1;
@@ -905,7 +919,8 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                 // the code of a unit's end is seldom in the instruction cache, so it is kept short.)
                 const bool sector = !whole || (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
                 const bool f32 = !whole || p.out_dtype == PA_F32;
-                const float f = whole ? inv : 1.f, g0 = den == 0.f && whole ? 0.f : f0 * f, g1 = den == 0.f && whole ? 0.f : f1 * f;
+                const float f = whole ? inv : 1.f;
+                const float g0 = den == 0.f && whole ? 0.f : f0 * f, g1 = den == 0.f && whole ? 0.f : f1 * f;
                 char* dst = whole ? static_cast<char*>(p.out) + orow * (f32 ? 4 : 2)
                                   : reinterpret_cast<char*>(p.part_acc + ((size_t)part * kTRows + r) * D);
 #pragma unroll 1

@@ -238,7 +238,8 @@ def test_decode_16_bit_outputs(dtype, out):
 def test_decode_random_shapes():
     r = np.random.default_rng(12)
     for i in range(24):
-        N, H, D, B = int(r.integers(1, 9)), int(r.choice([1, 2, 3, 5, 8])), int(r.choice([64, 128])), int(r.choice([8, 16, 32]))
+        N, H = int(r.integers(1, 9)), int(r.choice([1, 2, 3, 5, 8]))
+        D, B = int(r.choice([64, 128])), int(r.choice([8, 16, 32]))
         ctx = r.integers(1, int(r.choice([30, 300, 2500])), size=N).tolist()
         check_decode(Cache(100 + i, ctx, H, D, B, str(r.choice(["f16", "bf16"]))), int(r.integers(1, 9)), seed=i,
                      pt=int(r.choice([0, -1, 64, 160])), scale=float(r.choice([0.05, 0.125, 1.0])))
@@ -420,3 +421,83 @@ def test_a_serving_run_on_the_quantised_cache():
         for j in range(G):
             want, tol = R.attend(R.to64(q[:, h * G + j]), kk, vv, np.zeros(n + chunk), see, 1 / math.sqrt(D), False, True)
             R.close(out[:, h * G + j], want, tol, f"prefill head {h}")
+
+
+class short_waits:
+    """Context in which every wait inside newly launched kernels gives up after 1 ns."""
+
+    def __enter__(self):
+        pa.pa_set_wait_limit_ns(1)
+
+    def __exit__(self, *exc):
+        pa.pa_set_wait_limit_ns(0)
+
+
+@pytest.mark.parametrize("pt", [0, -1])
+def test_decode_timeout_exit_flags_returns_and_leaves_nothing_behind(pt):
+    c = Cache(70, [700, 33, 1500, 2400] * 8, 4, 128, 16, "bf16")
+    q = torch.randn(32, 16, 128).bfloat16().cuda()
+    ws = torch.empty(pa.pa_decode_workspace_bytes(32, 16, 4, 128, 2400, pt), dtype=torch.uint8, device="cuda")
+    ref, out, err = torch.empty(32, 16, 128, device="cuda"), torch.empty(32, 16, 128, device="cuda"), err_word()
+
+    def run(o):
+        pa.pa_decode_quant(o, q, c.qp, c.sc, c.dtab, c.dctx, 2400, partition_tokens=pt, workspace=ws, dev_err=err)
+
+    run(ref)
+    torch.cuda.synchronize()
+    with short_waits():
+        for _ in range(3):
+            run(out)
+        torch.cuda.synchronize()
+    assert err.item() & pa.PA_DEV_ERR_TIMEOUT
+    err.zero_()
+    run(out)
+    assert err.item() == 0 and torch.equal(out, ref)
+
+
+def test_decode_is_the_same_every_time_and_with_the_least_workspace():
+    """Equal calls give equal bits; a workspace that holds the longest partitions only still serves."""
+    c = Cache(71, [2100, 600, 5, 513], 2, 128, 16, "f16")
+    q = torch.randn(4, 8, 128).half().cuda()
+    args = (q, c.qp, c.sc, c.dtab, c.dctx, 2100)
+    a, b = (torch.empty(4, 8, 128, device="cuda") for _ in range(2))
+    pa.pa_decode_quant(a, *args)
+    for _ in range(10):
+        pa.pa_decode_quant(b, *args)
+        assert torch.equal(a, b)
+    least = pa.pa_decode_workspace_bytes(4, 8, 2, 128, 2100, 512)
+    pa.pa_decode_quant(b, *args, partition_tokens=512)
+    ws = torch.full((least + 256,), 0xA5, dtype=torch.uint8, device="cuda")
+    pa.pa_decode_quant(a, *args, partition_tokens=512, workspace=ws[:least])
+    assert torch.equal(a, b) and (ws[least:] == 0xA5).all()
+
+
+def test_decode_of_sequences_that_share_blocks():
+    """Eight sequences on the same prefix blocks, and the same sequence twice."""
+    c = Cache(72, [300, 300], 2, 64, 16, "bf16")
+    tab = c.dtab[:1].repeat(8, 1)
+    q = torch.randn(1, 8, 64).bfloat16().cuda().repeat(8, 1, 1)
+    out = torch.empty(8, 8, 64, device="cuda")
+    pa.pa_decode_quant(out, q, c.qp, c.sc, tab, c.dctx[:1].repeat(8), 300)
+    one = torch.empty(1, 8, 64, device="cuda")
+    pa.pa_decode_quant(one, q[:1], c.qp, c.sc, tab[:1], c.dctx[:1], 300)
+    assert torch.equal(out, out[:1].repeat(8, 1, 1))
+    for h in range(2):
+        k, v, ev = c.rows(0, h)
+        want, tol = R.attend(R.to64(q[0, 4 * h: 4 * h + 4]), k, v, ev, np.ones((4, 300), bool), 1 / 8, True, True)
+        for o in (out, one):                         # partitions may differ in length
+            R.close(o[0, 4 * h: 4 * h + 4], want, tol, f"head {h}")
+
+
+def test_read_into_a_pool_that_is_16_byte_aligned_only():
+    g = torch.Generator().manual_seed(5)
+    qp = torch.randint(0, 120, (4, 2, 2, 8, 64), generator=g, dtype=torch.uint8).cuda()
+    sc = torch.randint(120, 132, (4, 2, 2, 8), generator=g, dtype=torch.uint8).cuda()
+    pairs = torch.tensor([[3, 0], [1, 2]]).cuda()
+    n = 3 * 8 * 2 * 2 * 64
+    base = torch.zeros(n + 16, dtype=torch.float16, device="cuda")
+    odd, even = base[8: 8 + n].view(3, 8, 2, 2, 64), torch.zeros(3, 8, 2, 2, 64, dtype=torch.float16, device="cuda")
+    assert odd.data_ptr() % 32 == 16
+    pa.pa_dequant_blocks(odd, qp, sc, pairs)
+    pa.pa_dequant_blocks(even, qp, sc, pairs)
+    assert torch.equal(odd, even) and even.abs().sum() > 0 and (base[:8] == 0).all() and (base[8 + n:] == 0).all()

@@ -7,7 +7,7 @@ import torch
 
 import _quant_ref as R
 import paged_kv_cache_302_gb300 as pa
-from test_gpu_quant import DT, Cache, err_word
+from test_gpu_quant import DT, Cache, err_word, short_waits
 
 pytestmark = pytest.mark.gpu
 
@@ -123,7 +123,8 @@ def test_tree_16_bit_outputs(quant, dtype):
 def test_tree_long_contexts_are_split_and_joined(quant):
     r = np.random.default_rng(6)
     check(Cache(32, [9000], 2, 128, 32, "bf16", quant=quant), 4, [random_tree(r, 20)])
-    check(Cache(33, [5000, 60, 3000], 3, 64, 8, "f16", quant=quant), 2, [random_tree(r, 70), random_tree(r, 5), random_tree(r, 33)])
+    check(Cache(33, [5000, 60, 3000], 3, 64, 8, "f16", quant=quant), 2,
+          [random_tree(r, 70), random_tree(r, 5), random_tree(r, 33)])
 
 
 @pytest.mark.parametrize("quant", [False, True])
@@ -359,3 +360,70 @@ def test_a_speculative_step_with_the_allocator():
         else:
             pa.pa_decode(out, q.cuda(), c.pool, *args)
         compare(c, G, [np.ones((1, 1), bool)], q, out)
+
+
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+def test_tree_timeout_exit_flags_returns_and_leaves_nothing_behind(quant, out_dtype):
+    c = Cache(70, [1200, 90, 2500, 31] * 6, 4, 128, 16, "bf16", quant=quant)
+    r = np.random.default_rng(3)
+    masks = [random_tree(r, i) for i in (20, 31, 70, 31) * 6]
+    q = torch.randn(sum(m.shape[0] for m in masks), 16, 128).bfloat16().cuda()
+    ref = run_tree(c, q, masks, out_dtype=out_dtype)
+    err = err_word()
+    with short_waits():
+        for _ in range(3):
+            run_tree(c, q, masks, out_dtype=out_dtype, err=err)
+        torch.cuda.synchronize()
+    assert err.item() & pa.PA_DEV_ERR_TIMEOUT
+    err.zero_()
+    assert torch.equal(run_tree(c, q, masks, out_dtype=out_dtype, err=err), ref) and err.item() == 0
+
+
+@pytest.mark.parametrize("quant", [False, True])
+def test_tree_more_sequences_than_threads(quant):
+    """1500 sequences, a third of them without a draft: the runs are cut over several rounds of the block's threads."""
+    r = np.random.default_rng(11)
+    n = [int(x) for x in r.integers(0, 3, size=1500)]
+    n[700] = 9
+    ctx = [x + int(r.integers(0 if x else 1, 40)) for x in n]
+    ctx[1400] += 900
+    check(Cache(80, ctx, 1, 64, 8, "f16", quant=quant), 2,
+          [random_tree(r, x) if x else np.zeros((0, 0), bool) for x in n])
+
+
+@pytest.mark.parametrize("quant", [False, True])
+def test_tree_output_that_is_16_byte_aligned_only(quant):
+    c = Cache(81, [60, 900], 2, 64, 16, "f16", quant=quant)
+    r = np.random.default_rng(12)
+    masks = [random_tree(r, 6), random_tree(r, 7)]
+    q = torch.randn(13, 6, 64).half()
+    for dt in (torch.float32, torch.float16):
+        k = 16 // torch.empty(0, dtype=dt).element_size()
+        base = torch.zeros(13 * 6 * 64 + 2 * k, dtype=dt, device="cuda")
+        out = base[k:-k].view(13, 6, 64)
+        assert out.data_ptr() % 32 == 16
+        run_tree(c, q.cuda(), masks, out=out)
+        compare(c, 3, masks, q, out)
+        assert (base[:k] == 0).all() and (base[-k:] == 0).all()
+
+
+@pytest.mark.parametrize("quant", [False, True])
+def test_tree_blocks_behind_32_bit_offsets(quant):
+    """Pools of 4.9 GB: blocks past 2^31 and 2^32 bytes, two sequences on the same prefix blocks."""
+    H, G, D, B, NB = 8, 2, 128, 16, 150_000 if quant else 75_000
+    ids = [NB * 2 // 5, NB - 1, NB * 9 // 10, 5, NB * 14 // 15]
+    c = Cache(82, [70, 66], H, D, B, "bf16", quant=quant)
+    c.tables = torch.tensor([ids, ids[:4] + [77]], dtype=torch.int32)
+    c.slots = torch.tensor([t[p // B] * B + p % B for t, n in zip(c.tables.tolist(), c.ctx) for p in range(n)])
+    c.k[70:134], c.v[70:134] = c.k[:64].clone(), c.v[:64].clone()
+    c.dtab = c.tables.cuda()
+    if quant:
+        c.qp = torch.zeros(NB, H, 2, B, D, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+        c.sc = torch.zeros(NB, H, 2, B, dtype=torch.uint8, device="cuda")
+        pa.pa_reshape_and_cache_quant(c.k.cuda(), c.v.cuda(), c.qp, c.sc, c.slots.cuda())
+    else:
+        c.pool = torch.zeros(NB, B, 2, H, D, dtype=torch.bfloat16, device="cuda")
+        pa.pa_reshape_and_cache(c.k.cuda(), c.v.cuda(), c.pool, c.slots.cuda())
+    r = np.random.default_rng(13)
+    check(c, G, [random_tree(r, 5), random_tree(r, 2)])

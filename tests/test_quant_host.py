@@ -132,3 +132,10 @@ def test_reference_format_agrees_with_torch():
     # every row lies within 448 of its scale and above half of that
     q, e = R.quantise(np.random.default_rng(0).standard_normal((200, 64)) * np.exp2(np.arange(200.0) - 100)[:, None])
     assert e.min() == 87 and e.max() == 127 + 40 and (np.abs(R.e4m3_decode(q)) <= 448).all()
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.125, float("nan"), float("inf")])
+def test_tree_refuses_scales_that_are_not_positive_numbers(scale):
+    assert pa.load().pa_decode_tree(A[0], F32, A[1], BF16, A[2], None, BF16, A[3], A[4], A[5], A[6], 1, 1, 4, 8, 2, 128, 16,
+                                    4, 4, 4, scale, A[7], 1 << 30, None, None) == INV
+    assert "scale" in pa.last_error()
