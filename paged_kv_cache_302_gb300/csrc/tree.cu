@@ -51,7 +51,7 @@ constexpr int kTreeMaxCtas = 160;  // CTAs of a call at most (the workspace hold
 // Cost of a unit's start and end (query rows, first scores, joining the warpgroups, storing) in key tiles.  Two to four
 // make no difference (512 units of 13 tiles: 89, 91, 91 us; 6: 97).
 constexpr int kTreeUnitCost = 2;
-constexpr int kConvWarps = 8;
+constexpr int kConvWarps = 8;  // two groups of four: one for the even tiles, one for the odd
 // Probabilities are relative to a reference kPHeadroom below the row's maximum, which may grow by 2^8 before O is
 // rescaled: they reach 2^15, the top of fp16's range, so that the smallest keep as many bits as fp16 allows (an absolute
 // 2^-25 is 2^-32 of the largest).
@@ -352,6 +352,7 @@ struct TreeGeo {
     // V ring slots and K ring slots.  A converted K tile is free again as soon as its score product is done, long before
     // its V: one slot serves, and the space holds another raw tile on its way.
     static constexpr int NS = QUANT ? 2 : 3, KS = QUANT ? 1 : 3;
+    static constexpr int KF = QUANT ? 2 : 3;  // "K read" barriers, by tile in turn
     static constexpr int NR = QUANT ? (D == 128 ? 3 : 6) : 0;      // raw ring slots: K and V rows of a tile, scales
     static constexpr uint32_t kRaw = 2u * kTKeys * D, kRawScales = 2 * kTKeys;
     static constexpr uint32_t kExp = QUANT ? kTKeys : 0;           // per V slot: each key's scale byte of V
@@ -364,9 +365,9 @@ struct TreeGeo {
     static constexpr uint32_t oK = kTile, oV = oK + KS * kTile, oRaw = oV + NS * kTile, oRawSc = oRaw + NR * kRaw,
                               oExp = oRawSc + NR * kRawScales, oXch = oExp + NS * kExp, oQe = oXch + 2 * kTRows * 4,
                               oBar = oQe + (QUANT ? kTRows : 0);
-    static constexpr int kBars = 5 + 2 * KS + 2 * NS + 6 + 2 * NR;
+    static constexpr int kBars = 5 + KS + KF + 2 * NS + 6 + 2 * NR;
     static constexpr uint32_t oSmall = oBar + 8 * kBars;
-    static constexpr size_t kSmem = oSmall + 48;
+    static constexpr size_t kSmem = oSmall + 64;
     static_assert(kSmem <= 232448, "shared memory");
     static_assert(8 * 40 <= kTile, "the Q tile's space also serves the start");
 };
@@ -376,7 +377,7 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
     tree_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUtensorMap tm_q,
                 const __grid_constant__ TreeParams p) {
     using Geo = TreeGeo<D, QUANT>;
-    constexpr int NS = Geo::NS, KS = Geo::KS, NR = Geo::NR;
+    constexpr int NS = Geo::NS, KS = Geo::KS, KF = Geo::KF, NR = Geo::NR;
     constexpr int NK = D / 16, NT = kTKeys / 32;  // k-steps of S, and of each warpgroup's value product
     constexpr bool kBf16 = !QUANT && std::is_same<T, __nv_bfloat16>::value;  // type of the products
     using PT = typename std::conditional<kBf16, __nv_bfloat16, __half>::type;
@@ -391,13 +392,15 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
     // sfull, prdy, pvd: one for each of the two buffers of scores
     const uint32_t qfull = sBar, qfree = qfull + 8, qread = qfree + 8, sdone = qread + 8, pdone = sdone + 8,
                    kfull = pdone + 8, kfree = kfull + 8 * KS,
-                   vfull = kfree + 8 * KS, vfree = vfull + 8 * NS, sfull = vfree + 8 * NS, pvd = sfull + 16,
+                   vfull = kfree + 8 * KF, vfree = vfull + 8 * NS, sfull = vfree + 8 * NS, pvd = sfull + 16,
                    prdy = pvd + 16, rfull = prdy + 16, rfree = rfull + 8 * NR;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_raw + Geo::oSmall);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     volatile int* armed = abort_flag + 1;  // K, V (quantised: raw) tiles and query tiles whose copies have been issued
-    float* kmul = reinterpret_cast<float*>(tmem_slot + 5);  // per V slot: 2^(emax - 7) of the tile's K
-    float* vexp = kmul + NS;  // per V slot: exponent that its V was scaled down by, or kTreeKeyed
+    // Of the last four tiles (a tile is converted once the value products of the fourth before it are done): 2^(emax - 7)
+    // of its K; the exponent that its V is scaled down by, or kTreeKeyed.
+    float* kmul = reinterpret_cast<float*>(tmem_slot + 5);
+    float* vexp = kmul + 4;
     int8_t* qexp = reinterpret_cast<int8_t*>(smem_raw + Geo::oQe);  // per query row: exponent it was scaled down by
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -426,9 +429,9 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
         if (QUANT) {
             mbar_init(qfull, kConvWarps);
             mbar_init(qread, 8);
-            for (int i = 0; i < KS; ++i) mbar_init(kfull + 8 * i, kConvWarps);
-            for (int i = 0; i < NS; ++i) mbar_init(vfull + 8 * i, kConvWarps);
-            for (int i = 0; i < NR; ++i) mbar_init(rfree + 8 * i, kConvWarps);
+            for (int i = 0; i < KS; ++i) mbar_init(kfull + 8 * i, kConvWarps / 2);
+            for (int i = 0; i < NS; ++i) mbar_init(vfull + 8 * i, kConvWarps / 2);
+            for (int i = 0; i < NR; ++i) mbar_init(rfree + 8 * i, kConvWarps / 2);
         }
         *abort_flag = 0;
         armed[0] = armed[1] = armed[2] = 0;
@@ -550,7 +553,7 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                             umma_f16(tmem + s_col(t), dq + (ks >> 2) * (kTRegion >> 4) + (ks & 3) * 2,
                                      dk + (ks >> 2) * (1024 >> 4) + (ks & 3) * 2, idesc_s, ks > 0);
                         umma_commit(sfull + 8 * (t & 1));
-                        umma_commit(kfree + 8 * kslot(t));
+                        umma_commit(kfree + 8 * (t % KF));
                     }
                     if (ok) umma_commit(qfree);  // (never before the rows have landed)
                 }
@@ -591,9 +594,10 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
             // -------------------------------------------------------- converters (quantised pool)
             if constexpr (QUANT) {
                 const int cw = warp - 12;
-                // A lane converts half a row, 16 values at a time, so that the row's factor stays in a register; eight
-                // neighbouring rows' pieces lie in eight different bank groups on both sides, swizzled as they are.
-                const int row = 32 * (cw & 3) + lane, mb = ~(B - 1), c0 = (cw >> 2) * (D / 32);
+                // Four warps to a tile, so that one group's waits and scales run under the other's conversion.  A lane
+                // converts a row, 16 values at a time, so that the row's factor stays in a register; eight neighbouring
+                // rows' pieces lie in eight different bank groups on both sides, swizzled as they are.
+                const int row = 32 * (cw & 3) + lane, mb = ~(B - 1);
                 const uint32_t so = (uint32_t)(row + (row & mb)) * D, ro = (uint32_t)(row + (row & mb));
                 const uint32_t to = (uint32_t)(row >> 3) * kGroup + (row & 7) * 128;
                 int t = 0;
@@ -663,6 +667,7 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                         if (lane == 0) mbar_arrive(qfull);
                     }
                     for (int j = g.j0; j < g.j1; ++j, ++t) {
+                        if ((t & 1) != cw >> 2) continue;
                         const int k0 = j * kTKeys;
                         const uint32_t rb = (uint32_t)(t % NR);
                         const uint32_t raw = sb + Geo::oRaw + rb * Geo::kRaw, rsc = sb + Geo::oRawSc + rb * Geo::kRawScales;
@@ -702,13 +707,14 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                         const uint32_t fk = seen ? (uint32_t)max(ek - em + 22, 0) * 0x04000400u : 0u;
                         const uint32_t fv = seen ? (keyed ? 0x3c003c00u : (uint32_t)max(ev - vm + 22, 0) * 0x04000400u) : 0u;
 #pragma unroll 1
-                        for (int which = 0; which < 2; ++which) {
+                        for (int i = 0; i < 4; ++i) {  // K's and V's row, in halves
+                            const int which = i >> 1, c0 = (i & 1) * (D / 32);
                             const uint32_t f2 = which ? fv : fk;
-                            if (t >= (which ? NS : KS))
-                                ok = waited(which ? vfree + 8 * sl : kfree + 8 * kslot(t),
-                                            which ? ph(t - NS) : kph(t - KS)) && ok;
+                            // the last K tile's score product has read it; the last V in this slot is used up
+                            if (i == 0 && t >= 1) ok = waited(kfree + 8 * ((t - 1) % KF), (uint32_t)((t - 1) / KF & 1)) && ok;
+                            if (i == 2 && t >= NS) ok = waited(vfree + 8 * sl, ph(t - NS)) && ok;
                             const uint32_t src = raw + so + (which ? B * D : 0);
-                            const uint32_t dst = (which ? sV + sl * kTile : sK + kslot(t) * kTile) + to;
+                            const uint32_t dst = (which ? sV + sl * kTile : sK) + to;
                             uint4 vs[D / 32];  // all read before the first is converted
 #pragma unroll
                             for (int cc = 0; cc < D / 32; ++cc)
@@ -736,14 +742,15 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                                                  "r"(h[4 * o]), "r"(h[4 * o + 1]), "r"(h[4 * o + 2]), "r"(h[4 * o + 3])
                                                  : "memory");
                             }
-                            if (which && keyed && c0 == 0) smem_raw[Geo::oExp + sl * Geo::kExp + row] = (uint8_t)ev;
-                            if (which && cw == 0 && lane == 0) {
-                                kmul[sl] = pow2i(em - kScaleBias - 7);
-                                vexp[sl] = keyed ? kTreeKeyed : (float)(vm - kScaleBias - 7);
+                            if (i == 2 && keyed) smem_raw[Geo::oExp + sl * Geo::kExp + row] = (uint8_t)ev;
+                            if (i == 1 && row == 0) {
+                                kmul[t & 3] = pow2i(em - kScaleBias - 7);
+                                vexp[t & 3] = keyed ? kTreeKeyed : (float)(vm - kScaleBias - 7);
                             }
+                            if (c0 == 0) continue;
                             fence_proxy_async_smem();
                             __syncwarp();
-                            if (lane == 0) mbar_arrive(which ? vfull + 8 * sl : kfull + 8 * kslot(t));
+                            if (lane == 0) mbar_arrive(which ? vfull + 8 * sl : kfull);
                         }
                         if (lane == 0 && ok) mbar_arrive(rfree + 8 * rb);  // (never before its copies have landed)
                     }
@@ -783,10 +790,7 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                             vis[1] = v;
                     }
                 }
-                if (QUANT)  // scores, and the tile's exponents
-                    ok = waited2(sfull + 8 * (t & 1), par, vfull + 8 * slot(t), ph(t)) && ok;
-                else
-                    ok = waited(sfull + 8 * (t & 1), par) && ok;
+                ok = waited(sfull + 8 * (t & 1), par) && ok;
                 tc_fence_after();
                 if (QUANT) {
                     if (j == g.j0) {
@@ -841,10 +845,11 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                     l = fmaf(l, alpha, sum);
                 };
                 if (warp_ok) {
-                    const float mul = QUANT ? cr * kmul[slot(t)] : cr;
-                    const float E = QUANT ? vexp[slot(t)] : 0.f;
+                    const float mul = QUANT ? cr * kmul[t & 3] : cr;
+                    const float E = QUANT ? vexp[t & 3] : 0.f;
                     if (masked) tree_mask_scores(t_s, vis[0], vis[1]);
                     if (QUANT && E == kTreeKeyed) {
+                        ok = waited(vfull + 8 * slot(t), ph(t)) && ok;  // the exponents, with V
                         const uint32_t ex = sb + Geo::oExp + slot(t) * Geo::kExp + 64 * w;
                         const float3 r = tree_probabilities_keyed<PT, SPLIT>(t_s, ex, mul, j == g.j0, m_ref);
                         m_ref = r.y;
