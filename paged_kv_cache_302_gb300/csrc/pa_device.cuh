@@ -115,32 +115,6 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
     }
 }
 
-// The same wait for hand-offs that usually take well under a microsecond: the clock, whose read takes longer than
-// that, is consulted only every 64 tries (every try when the limit is below a microsecond).  Kept short in code: a
-// kernel whose roles wait at many places fits the instruction cache only so.
-__device__ __forceinline__ bool mbar_wait_spin(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
-    const uint32_t tries = limit_ns < 1000 ? 1 : 64;
-    uint64_t t0 = 0;
-#pragma unroll 1
-    while (true) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, %3;\n\t"
-            "AGAIN:\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-            "@p bra DONE;\n\tsub.u32 n, n, 1;\n\tsetp.ne.u32 q, n, 0;\n\t@q bra AGAIN;\n\t"
-            "DONE:\n\tselp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity), "r"(tries)
-            : "memory");
-        if (ok) return true;
-        if (*abort) return false;
-        const uint64_t now = global_ns();
-        if (t0 == 0) t0 = now;
-        if (now - t0 > limit_ns) return false;
-    }
-}
-
 // ----------------------------------------------------------------------------- TMA
 
 // 5-D tiled tensor load into shared memory, completion counted on `bar`.
@@ -159,15 +133,6 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, uint
         "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
         " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
         "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar), "l"(policy)
-        : "memory");
-}
-
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, uint32_t bar, int c0, int c1, int c2,
-                                            uint64_t policy) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-        " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
-        "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy)
         : "memory");
 }
 

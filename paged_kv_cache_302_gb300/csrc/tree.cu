@@ -27,12 +27,14 @@
 // out of V (per tile, else per key): y = raw c 2^(emax - 7) + E, p = 2^(y - M), O += p (V 2^-E), l += p 2^-E, as in
 // decode_quant.cu.
 //
-// What bounds it, measured at D = 128.  64 sequences with trees of up to 24 tokens, 32 / 8 heads, bf16: 89 us, 4.8 TB/s of
-// K and V (the bytes alone are 64 us; without the products it takes 85: the rest is the start and end of 512 units).  16
-// trees of up to 63 tokens over 4500 quantised tokens each: 115 us, about 2900 cycles per tile of 128 x 128, of which
-// leaving out the conversion to fp16 saves 900, the softmax 300, both products 150; what is left are the waits from role to
-// role.  What the time was spent on before: one score buffer (128 us), spin waits unrolled by the compiler and masked or
-// keyed tiles in line, which pushed the usual tile's code out of the instruction cache (180 us).
+// What bounds it, measured at D = 128.  64 sequences with trees of up to 24 tokens, 32 / 8 heads, bf16: 90 us, 4.8 TB/s of
+// K and V.  The bytes alone are 64 us; inside a run a tile takes about 2700 cycles, 64 KB at 7 TB/s over the GPU, and the
+// rest is the launch, the first tiles and the ends of 512 units.  16 trees of up to 63 tokens over 4500 quantised tokens
+// each: 110 us, about 2800 cycles per tile of 128 x 128, bound by the roles' own instructions and waits (the SM issues 2.1
+// of 4 instructions a cycle, the tensor pipe is 28 % busy, memory 20 %).  Of 117 us with all in place, a copy without
+// the conversion to fp16 took 88, without exponentials 113, without both products 109, without all three 83.  What the
+// time was spent on before: one group of converters (114 us), one score buffer (128), masked and keyed tiles in line (138)
+// and spin waits unrolled by the compiler (180), both of which pushed the usual tile's code out of the instruction cache.
 #include <algorithm>
 #include <cstring>
 #include <type_traits>
@@ -80,6 +82,32 @@ struct TreeParams {
     uint64_t wait_ns;
     int* err;
 };
+
+// mbar_wait_bounded for hand-offs that usually take well under a microsecond: the clock, whose read takes longer than
+// that, is consulted only every 64 tries (every try when the limit is below a microsecond).  Kept short in code: a
+// kernel whose roles wait at many places fits the instruction cache only so.
+__device__ __forceinline__ bool mbar_wait_spin(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
+    const uint32_t tries = limit_ns < 1000 ? 1 : 64;
+    uint64_t t0 = 0;
+#pragma unroll 1
+    while (true) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, %3;\n\t"
+            "AGAIN:\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "@p bra DONE;\n\tsub.u32 n, n, 1;\n\tsetp.ne.u32 q, n, 0;\n\t@q bra AGAIN;\n\t"
+            "DONE:\n\tselp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(tries)
+            : "memory");
+        if (ok) return true;
+        if (*abort) return false;
+        const uint64_t now = global_ns();
+        if (t0 == 0) t0 = now;
+        if (now - t0 > limit_ns) return false;
+    }
+}
 
 __device__ __forceinline__ uint32_t vmin_u16x2(uint32_t a, uint32_t b) {
     uint32_t d;
