@@ -143,8 +143,9 @@ pa_status pa_update_block_tables(int32_t* tables, int N, int MB, const int32_t* 
  * partition_tokens: 0 = default (512; pa_decode_quant takes 64 to 512 by the
  * size of the batch where the workspace has room, which this function grants
  * it, else 512), -1 = one partition per sequence, > 0 = split each context into
- * partitions of that many tokens (a multiple of 32).  max_ctx bounds every context length of the calls that use the
- * workspace.  Returns 0 for invalid arguments.
+ * partitions of that many tokens (a multiple of 32).  max_ctx bounds every
+ * context length of the calls that use the workspace.  Returns 0 for invalid
+ * arguments.
  * ---------------------------------------------------------------------- */
 size_t pa_decode_workspace_bytes(int N, int H_q, int H_kv, int D, int max_ctx, int partition_tokens);
 
@@ -248,7 +249,9 @@ pa_status pa_prefill(void* out, pa_dtype out_dtype, const void* q, const void* p
  * is off by at most 2^-4 of itself, or 2^-10 of 2^e below 2^-6 * 2^e.  A
  * magnitude above 448 * 2^40 (4.9e14) and an infinity become 448 * 2^40; a NaN
  * stays NaN and does not count in the row's maximum.  slot_mapping as
- * pa_reshape_and_cache (negative: padding; >= NB*B: skipped, PA_DEV_ERR_SLOT).
+ * pa_reshape_and_cache (negative: padding; >= NB*B: skipped, PA_DEV_ERR_SLOT;
+ * two tokens with the same slot race, caller error: the row may then hold one's
+ * values under the other's scale).
  *
  * pa_dequant_blocks restores blocks of a 16-bit pool [NB_dst][B][2][H_kv][D] of
  * dtype F16 or BF16 (for pa_prefill over a quantised prefix, or to leave the
@@ -295,8 +298,9 @@ pa_status pa_decode_quant(void* out, pa_dtype out_dtype, const void* q, pa_dtype
  * Bits from n_s on are ignored.  K and V of drafted tokens that no row of the
  * sequence sees (padding), and slots past the context, may hold anything, NaN
  * included; a non-finite V of a drafted token that some rows see can reach the
- * sequence's other rows.  The draft's own K/V must already be in the pool (forking the sequence before the draft and
- * freeing the fork afterwards takes it out again).
+ * sequence's other rows.  The draft's own K/V must already be in the pool
+ * (forking the sequence before the draft and freeing the fork afterwards takes
+ * it out again).
  * q, out: [T][H_q][D] (out F32 or q_dtype); q_start: [N+1] int32, not
  * decreasing, q_start[N] <= T (rows of out past q_start[N] are not written);
  * tree_mask: [T][mask_words] int32 words, max_q_len <= 32 * mask_words;

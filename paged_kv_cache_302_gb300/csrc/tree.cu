@@ -434,6 +434,7 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
 
     griddep_wait();
     griddep_launch_dependents();
+    if (tid == 0) p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);  // before every exit: the merge reads it
     // swizzled tiles need the 1024-byte alignment that dynamic shared memory has when there is no static
     if (sb & 1023u) {
         if (tid == 0) flag_error(p.err, PA_DEV_ERR_TIMEOUT);
@@ -441,7 +442,6 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
     }
     const TreeRun run =
         tree_run<Geo::kThreads>(p, blockIdx.x, gridDim.x, blockIdx.x == 0, reinterpret_cast<int64_t*>(smem_raw));
-    if (tid == 0) p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
     if (run.lo >= run.hi) return;
 
     if (warp == 0) {
