@@ -165,6 +165,11 @@ struct TreeSeg {
     int s, h, mt, j0, j1, nt, ctx, n, qs;
 };
 
+// a / b of positive numbers: a 64-bit division is a long subroutine, and calls whose tiles need one are rare.
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+    return (a | b) >> 32 == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // Walks a CTA's run segment by segment.  Positions count cost: a unit is kTreeUnitCost, then one per tile.
 struct TreeWalk {
     int s, u, o;  // sequence, unit in it, position in the unit
@@ -174,7 +179,7 @@ struct TreeWalk {
         s = s0;
         left = count;
         q = tree_seq(p, s, false);
-        u = (int)(rem / (q.nt + kTreeUnitCost));
+        u = (int)divide(rem, q.nt + kTreeUnitCost);
         o = (int)(rem - (int64_t)u * (q.nt + kTreeUnitCost));
     }
     __device__ __forceinline__ bool next(const TreeParams& p, TreeSeg& g) {
@@ -228,8 +233,7 @@ __device__ __forceinline__ TreeRun tree_run(const TreeParams& p, int cta, int ct
     __syncthreads();
     int64_t total = 0;
     for (int w = 0; w < NW; ++w) total += buf[w];
-    r.per = (total + ctas - 1) / ctas;
-    if (r.per < kTreeUnitCost + 1) r.per = kTreeUnitCost + 1;  // a tile at least
+    r.per = divide(total + ctas - 1, ctas);  // (a run may hold no tile: a small call's tiles each have a CTA)
     r.lo = r.per * cta;
     r.hi = min(r.lo + r.per, total);
     r.s = 0;
@@ -432,6 +436,23 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
     int8_t* qexp = reinterpret_cast<int8_t*>(smem_raw + Geo::oQe);  // per query row: exponent it was scaled down by
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+    // (nothing up to the wait touches global memory: it runs under the kernel before)
+    if (tid < Geo::kBars) {
+        const uint32_t bar = sBar + 8 * tid;
+        int count = 1;
+        if (bar == prdy || bar == prdy + 8) count = 256;
+        if (QUANT) {
+            if (bar == qfull) count = kConvWarps;
+            if (bar == qread) count = 8;
+            if ((bar >= kfull && bar < kfree) || (bar >= vfull && bar < vfree) || bar >= rfree) count = kConvWarps / 2;
+        }
+        mbar_init(bar, count);
+        fence_mbar_init();
+    }
+    if (tid == 0) {
+        *abort_flag = 0;
+        armed[0] = armed[1] = armed[2] = 0;
+    }
     griddep_wait();
     griddep_launch_dependents();
     if (tid == 0) p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);  // before every exit: the merge reads it
@@ -449,21 +470,6 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                      "r"(kTTmem)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    }
-    if (tid == 0) {
-        for (int i = 0; i < Geo::kBars; ++i) mbar_init(sBar + 8 * i, 1);
-        mbar_init(prdy, 256);
-        mbar_init(prdy + 8, 256);
-        if (QUANT) {
-            mbar_init(qfull, kConvWarps);
-            mbar_init(qread, 8);
-            for (int i = 0; i < KS; ++i) mbar_init(kfull + 8 * i, kConvWarps / 2);
-            for (int i = 0; i < NS; ++i) mbar_init(vfull + 8 * i, kConvWarps / 2);
-            for (int i = 0; i < NR; ++i) mbar_init(rfree + 8 * i, kConvWarps / 2);
-        }
-        *abort_flag = 0;
-        armed[0] = armed[1] = armed[2] = 0;
-        fence_mbar_init();
     }
     tc_fence_before();
     __syncthreads();
@@ -987,7 +993,7 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
             if (!whole && row_ok && ok && w == 0)
                 reinterpret_cast<float2*>(p.part_ml)[(size_t)part * kTRows + r] = make_float2(M, den);
             if (tid == 0 && g.j0 == 0 && !whole)
-                p.desc[blockIdx.x] = make_int4(g.s, g.h, g.mt, (int)(1 + (g.nt - g.j1 + run.per - 1) / run.per));
+                p.desc[blockIdx.x] = make_int4(g.s, g.h, g.mt, 1 + (int)divide(g.nt - g.j1 + run.per - 1, run.per));
             tc_fence_before();  // O may be started afresh once this thread's next P is ready
         }
     }
