@@ -747,18 +747,23 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                             // the last K tile's score product has read it; the last V in this slot is used up
                             if (i == 0 && t >= 1) ok = waited(kfree + 8 * ((t - 1) % KF), (uint32_t)((t - 1) / KF & 1)) && ok;
                             if (i == 2 && t >= NS) ok = waited(vfree + 8 * sl, ph(t - NS)) && ok;
-                            const uint32_t src = raw + so + (which ? B * D : 0);
-                            const uint32_t dst = (which ? sV + sl * kTile : sK) + to;
+                            // addresses of the half's pieces differ from its first's in the swizzled bits only
+                            const uint32_t src = raw + so + (which ? B * D : 0) + ((c0 ^ (D == 128 ? row & 7 : row >> 1 & 3)) << 4);
+                            const uint32_t dst = (which ? sV + sl * kTile : sK) + to +
+                                                 (D == 128 ? (i & 1) * 1024 + ((row & 7) << 4) : ((2 * c0) ^ (row & 7)) << 4);
                             uint4 vs[D / 32];  // all read before the first is converted
 #pragma unroll
                             for (int cc = 0; cc < D / 32; ++cc)
                                 asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                                              : "=r"(vs[cc].x), "=r"(vs[cc].y), "=r"(vs[cc].z), "=r"(vs[cc].w)
-                                             : "r"(src + (((c0 + cc) ^ (D == 128 ? row & 7 : row >> 1 & 3)) << 4)));
+                                             : "r"(src ^ (cc << 4)));
+                            if (masked && !seen) {  // (zero times NaN is NaN)
+#pragma unroll
+                                for (int cc = 0; cc < D / 32; ++cc) vs[cc] = make_uint4(0u, 0u, 0u, 0u);
+                            }
 #pragma unroll
                             for (int cc = 0; cc < D / 32; ++cc) {
-                                const int c = c0 + cc;
-                                const uint4 v = seen ? vs[cc] : make_uint4(0u, 0u, 0u, 0u);  // (zero times NaN is NaN)
+                                const uint4 v = vs[cc];
                                 uint32_t h[8] = {e4m3x2_to_f16x2(v.x), e4m3x2_to_f16x2(v.x >> 16), e4m3x2_to_f16x2(v.y),
                                                  e4m3x2_to_f16x2(v.y >> 16), e4m3x2_to_f16x2(v.z),
                                                  e4m3x2_to_f16x2(v.z >> 16), e4m3x2_to_f16x2(v.w),
@@ -771,8 +776,7 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                                 }
 #pragma unroll
                                 for (int o = 0; o < 2; ++o)
-                                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                                     dst + (c >> 2) * 1024 + ((((c & 3) * 2 + o) ^ (row & 7)) << 4)),
+                                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst ^ ((2 * cc + o) << 4)),
                                                  "r"(h[4 * o]), "r"(h[4 * o + 1]), "r"(h[4 * o + 2]), "r"(h[4 * o + 3])
                                                  : "memory");
                             }
