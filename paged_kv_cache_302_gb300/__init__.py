@@ -183,10 +183,10 @@ def _quant_cache(qpool, scales):
     """(NB, H_kv, B, D) of a quantised cache, after checking that the two tensors are one."""
     if not isinstance(qpool, torch.Tensor) or not isinstance(scales, torch.Tensor):
         raise PAError(PA_ERR_INVALID, "qpool and scales must be tensors")
-    shape = tuple(qpool.shape)
+    shape = qpool.shape
     if qpool.dtype not in _E4M3_TYPES or scales.dtype not in _SCALE_TYPES:
         raise PAError(PA_ERR_INVALID, "qpool must be float8_e4m3fn or uint8, scales uint8 or float8_e8m0fnu")
-    if len(shape) != 5 or shape[2] != 2 or tuple(scales.shape) != shape[:4]:
+    if len(shape) != 5 or shape[2] != 2 or scales.shape != shape[:4]:
         raise PAError(PA_ERR_INVALID, "qpool must be [NB, H_kv, 2, B, D] and scales [NB, H_kv, 2, B]")
     return shape[0], shape[1], shape[3], shape[4]
 
@@ -211,13 +211,14 @@ def _here(t, name) -> int:
 
 def _arg(t, name, dev, dtype=None) -> int:
     """Address of a contiguous tensor on device `dev`.  (These checks run at every call: they are kept cheap.)"""
+    if (isinstance(t, torch.Tensor) and t.get_device() == dev and (dtype is None or t.dtype is dtype)
+            and t.is_contiguous()):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor) or t.get_device() != dev:
         raise PAError(PA_ERR_INVALID, f"{name} must be a tensor on the current CUDA device (cuda:{dev})")
     if dtype is not None and t.dtype != dtype:
         raise PAError(PA_ERR_INVALID, f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_contiguous():
-        raise PAError(PA_ERR_INVALID, f"{name} must be contiguous")
-    return t.data_ptr()
+    raise PAError(PA_ERR_INVALID, f"{name} must be contiguous")
 
 
 def _out_arg(t, name, dev) -> int:
@@ -466,9 +467,10 @@ def pa_reshape_and_cache_quant(k, v, qpool, scales, slot_mapping, dev_err=None, 
     """Quantise k, v [T, H_kv, D] into a quantised cache at slot_mapping [T] (int64): e4m3 values with the smallest
     power-of-two scale per (token, head) row that keeps the row within 448."""
     NB, H_kv, B, D = _quant_cache(qpool, scales)
-    if k.dim() != 3 or tuple(k.shape[1:]) != (H_kv, D) or tuple(v.shape) != tuple(k.shape):
+    shape = k.shape
+    if len(shape) != 3 or shape[1] != H_kv or shape[2] != D or v.shape != shape:
         raise PAError(PA_ERR_INVALID, "k and v must be [T, H_kv, D] of the cache's heads and head dim")
-    T = k.shape[0]
+    T = shape[0]
     if slot_mapping.numel() != T:
         raise PAError(PA_ERR_INVALID, "slot_mapping must have T entries")
     dev = _here(k, "k")
@@ -482,7 +484,7 @@ def pa_dequant_blocks(dst_pool, qpool, scales, pairs, dev_err=None, stream=None)
     """dst_pool[dst] = the values of quantised block src, for (src, dst) rows of pairs [n, 2] (int64, device);
     dst_pool [NB_dst, B, 2, H_kv, D] fp16 or bf16."""
     NB, H_kv, B, D = _quant_cache(qpool, scales)
-    if dst_pool.dim() != 5 or tuple(dst_pool.shape[1:]) != (B, 2, H_kv, D):
+    if dst_pool.dim() != 5 or dst_pool.shape[1:] != (B, 2, H_kv, D):
         raise PAError(PA_ERR_INVALID, "dst_pool must be [NB_dst, B, 2, H_kv, D] of the cache's shape")
     if pairs.dtype != torch.int64 or (pairs.numel() and (pairs.dim() != 2 or pairs.shape[1] != 2)):
         raise PAError(PA_ERR_INVALID, "pairs must be [n, 2] int64")
@@ -500,19 +502,23 @@ def pa_decode_quant(out, q, qpool, scales, block_tables, ctx_lens, max_ctx, scal
     """Decode attention over a quantised cache: q [N, H_q, D] fp16 or bf16, out [N, H_q, D] fp32 or q's dtype (on the
     device or in pinned host memory); the workspace is pa_decode's."""
     NB, H_kv, B, D = _quant_cache(qpool, scales)
-    if q.dim() != 3 or q.shape[2] != D or tuple(out.shape) != tuple(q.shape):
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != D or out.shape != shape:
         raise PAError(PA_ERR_INVALID, "q and out must be [N, H_q, D] of the cache's head dim")
-    N, H_q, _ = q.shape
+    N, H_q, _ = shape
     if block_tables.dim() != 2 or block_tables.shape[0] != N or ctx_lens.numel() != N:
         raise PAError(PA_ERR_INVALID, "block_tables must be [N, MB] and ctx_lens [N]")
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
     dev = _here(q, "q")
-    ws = _workspace(workspace, _decode_bytes(N, H_q, H_kv, D, int(max_ctx), int(partition_tokens)), q.device)
+    max_ctx, partition_tokens = int(max_ctx), int(partition_tokens)
+    ws = workspace
+    if ws is None:
+        ws = torch.empty(_decode_bytes(N, H_q, H_kv, D, max_ctx, partition_tokens), dtype=torch.uint8, device=q.device)
     _check((_lib or load()).pa_decode_quant(
         _out_arg(out, "out", dev), _code(out.dtype), _arg(q, "q", dev), _code(q.dtype), _arg(qpool, "qpool", dev),
         _arg(scales, "scales", dev), _arg(block_tables, "block_tables", dev, torch.int32),
-        _arg(ctx_lens, "ctx_lens", dev, torch.int32), N, H_q, H_kv, D, B, block_tables.shape[1], NB, int(max_ctx), scale,
-        int(partition_tokens), _arg(ws, "workspace", dev), ws.numel() * ws.element_size(), _err_arg(dev_err, dev),
+        _arg(ctx_lens, "ctx_lens", dev, torch.int32), N, H_q, H_kv, D, B, block_tables.shape[1], NB, max_ctx, scale,
+        partition_tokens, _arg(ws, "workspace", dev), ws.nbytes, _err_arg(dev_err, dev),
         _events_arg(attend_events, stream), _stream_arg(stream, dev)))
     return out
 
@@ -530,9 +536,10 @@ def pa_decode_tree(out, q, pool, block_tables, ctx_lens, q_start, tree_mask, max
     q_start [N+1] int32; tree_mask [T, W] int32, bit j % 32 of word j // 32 set where a row sees its sequence's
     drafted token j.  pool is a 16-bit pool [NB, B, 2, H_kv, D] of q's dtype, or a quantised cache's qpool with its
     scales."""
-    if q.dim() != 3 or tuple(out.shape) != tuple(q.shape):
+    shape = q.shape
+    if len(shape) != 3 or out.shape != shape:
         raise PAError(PA_ERR_INVALID, "q and out must be [T, H_q, D]")
-    T, H_q, D = q.shape
+    T, H_q, D = shape
     if scales is not None:
         NB, H_kv, B, D2 = _quant_cache(pool, scales)
         code = PA_E4M3
@@ -550,14 +557,17 @@ def pa_decode_tree(out, q, pool, block_tables, ctx_lens, q_start, tree_mask, max
         return out
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
     dev = _here(q, "q")
-    ws = _workspace(workspace, _tree_bytes(N, H_q, H_kv, D, int(max_q_len)), q.device)
+    max_q_len = int(max_q_len)
+    ws = workspace
+    if ws is None:
+        ws = torch.empty(_tree_bytes(N, H_q, H_kv, D, max_q_len), dtype=torch.uint8, device=q.device)
     _check((_lib or load()).pa_decode_tree(
         _arg(out, "out", dev), _code(out.dtype), _arg(q, "q", dev), _code(q.dtype), _arg(pool, "pool", dev),
         _arg(scales, "scales", dev) if scales is not None else None, code,
         _arg(block_tables, "block_tables", dev, torch.int32), _arg(ctx_lens, "ctx_lens", dev, torch.int32),
         _arg(q_start, "q_start", dev, torch.int32), _arg(tree_mask, "tree_mask", dev, torch.int32), tree_mask.shape[1],
-        N, T, H_q, H_kv, D, B, block_tables.shape[1], NB, int(max_q_len), scale, _arg(ws, "workspace", dev),
-        ws.numel() * ws.element_size(), _err_arg(dev_err, dev), _stream_arg(stream, dev)))
+        N, T, H_q, H_kv, D, B, block_tables.shape[1], NB, max_q_len, scale, _arg(ws, "workspace", dev), ws.nbytes,
+        _err_arg(dev_err, dev), _stream_arg(stream, dev)))
     return out
 
 
