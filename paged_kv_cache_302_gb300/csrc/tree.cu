@@ -30,7 +30,7 @@
 // What bounds it, measured at D = 128.  64 sequences with trees of up to 24 tokens, 32 / 8 heads, bf16: 90 us, 4.8 TB/s of
 // K and V.  The bytes alone are 64 us; inside a run a tile takes about 2700 cycles, 64 KB at 7 TB/s over the GPU, and the
 // rest is the launch, the first tiles and the ends of 512 units.  16 trees of up to 63 tokens over 4500 quantised tokens
-// each: 107 us, about 2700 cycles per tile of 128 x 128, bound by the roles' own instructions and waits (the SM issues 2.1
+// each: 110 us, about 2800 cycles per tile of 128 x 128, bound by the roles' own instructions and waits (the SM issues 2.1
 // of 4 instructions a cycle, the tensor pipe is 28 % busy, memory 20 %).  Of 117 us with all in place, a copy without
 // the conversion to fp16 took 88, without exponentials 113, without both products 109, without all three 83.  What the
 // time was spent on before: one group of converters (114 us), one score buffer (128), masked and keyed tiles in line (138)
@@ -175,10 +175,10 @@ struct TreeWalk {
     int s, u, o;  // sequence, unit in it, position in the unit
     int64_t left;
     TreeSeq q;
-    __device__ __forceinline__ void start(const TreeParams& p, int s0, int64_t rem, int64_t count) {
+    __device__ __forceinline__ void start(const TreeSeq& q0, int s0, int64_t rem, int64_t count) {
         s = s0;
         left = count;
-        q = tree_seq(p, s, false);
+        q = q0;
         u = (int)divide(rem, q.nt + kTreeUnitCost);
         o = (int)(rem - (int64_t)u * (q.nt + kTreeUnitCost));
     }
@@ -210,17 +210,47 @@ struct TreeWalk {
 };
 
 // The CTA's run [lo, hi) of the call's cost, and the sequence it starts in with the part of it that lies before.
-// Every thread of the block calls it; `buf`: 40 words of 8 bytes.
+// Every thread of the block calls it; `buf`: 40 words of 8 bytes.  Up to 32 sequences every warp finds it by itself, one
+// lane to a sequence: without barriers and second reads of the lengths the first tiles of 4 sequences start 1 us sooner.
 struct TreeRun {
     int64_t per, lo, hi, rem;
     int s;
+    TreeSeq q;
 };
+
+__device__ __forceinline__ int64_t shfl64(int64_t x, int lane) {
+    return (int64_t)__shfl_sync(0xffffffffu, (unsigned long long)x, lane);
+}
 
 template <int THREADS>
 __device__ __forceinline__ TreeRun tree_run(const TreeParams& p, int cta, int ctas, bool flag, int64_t* buf) {
     constexpr int NW = THREADS / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     TreeRun r;
+    if (p.N <= 32) {
+        TreeSeq q = {};
+        if (lane < p.N) q = tree_seq(p, lane, flag && warp == 0);
+        const int64_t c = tree_cost(p, q);
+        int64_t incl = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t u = (int64_t)__shfl_up_sync(0xffffffffu, (unsigned long long)incl, o);
+            if (lane >= o) incl += u;
+        }
+        const int64_t total = shfl64(incl, 31);
+        r.per = divide(total + ctas - 1, ctas);
+        r.lo = r.per * cta;
+        r.hi = min(r.lo + r.per, total);
+        // the sequence that holds position lo: the first whose end lies past it
+        r.s = max(__ffs(__ballot_sync(0xffffffffu, incl > r.lo)) - 1, 0);
+        r.rem = r.lo - shfl64(incl - c, r.s);
+        r.q.ctx = __shfl_sync(0xffffffffu, q.ctx, r.s);
+        r.q.n = __shfl_sync(0xffffffffu, q.n, r.s);
+        r.q.qs = __shfl_sync(0xffffffffu, q.qs, r.s);
+        r.q.nt = __shfl_sync(0xffffffffu, q.nt, r.s);
+        r.q.nmt = __shfl_sync(0xffffffffu, q.nmt, r.s);
+        return r;
+    }
     int64_t sum = 0, c0 = 0;
     for (int s = tid; s < p.N; s += THREADS) {
         const int64_t c = tree_cost(p, tree_seq(p, s, flag));
@@ -268,6 +298,7 @@ __device__ __forceinline__ TreeRun tree_run(const TreeParams& p, int cta, int ct
     __syncthreads();
     r.s = (int)buf[32];
     r.rem = buf[33];
+    r.q = tree_seq(p, r.s, false);
     return r;
 }
 
@@ -497,7 +528,7 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
     auto kph = [](int i) { return (uint32_t)((i / KS) & 1); };
     bool ok = true;
     TreeWalk walk;
-    walk.start(p, run.s, run.rem, run.hi - run.lo);
+    walk.start(run.q, run.s, run.rem, run.hi - run.lo);
     TreeSeg g;
     const int B = 1 << p.lgB;
 
