@@ -2,19 +2,19 @@
 //
 // The same three kernels as the 16-bit decode (schedule, attention, merge), of which the schedule and the merge are
 // those of decode.cu.  The attention kernel: CTAs of two warps.  Warp 1 (producer) streams each work record's (block,
-// head) chunks into a ring of 32-token stages, one TMA box (K rows, then V rows, swizzled) and one bulk copy of the
-// 2 B scale bytes per block.  Warp 0 (consumer) computes with mma.sync m16n8k16, tokens on M, the <= 8 query heads
-// of the KV head on N:
-//     raw = K8 q'^T,  q' the query in fp16 (bf16 queries scaled row by row with a power of two, exactly);
-//     y_t = raw_t 2^ek_t c + ev_t,  c = scale log2 e 2^(query's exponent), ek_t, ev_t the exponents of the row scales;
-//     p_t = 2^(y_t - M), M the running maximum of y;  O += p V8,  l += p 2^-ev;  out = O / l.
+// head) chunks into a ring of 32-token stages, one TMA box (K rows, then V rows, swizzled) and one bulk copy of the 2 B
+// scale bytes per block.  Warp 0 (consumer) computes with mma.sync m16n8k16, tokens on M, the <= 8 query heads of the
+// KV head on N:
+//     raw = K8 q'^T,  q' the query in fp16 (bf16 queries scaled row by row with a power of two, exactly); y_t = raw_t
+//     2^ek_t c + ev_t,  c = scale log2 e 2^(query's exponent), ek_t, ev_t the exponents of the row scales; p_t = 2^(y_t
+//     - M), M the running maximum of y;  O += p V8,  l += p 2^-ev;  out = O / l.
 // With the exponent of V's scale inside the maximum, p <= 1 weighs the e4m3 values themselves, so p rounds to fp16
 // (here a high and a low part, 2^-22) relative to the largest contribution to the output, whatever the scales' spread.
 // |ev| <= 40 keeps p 2^-ev and l within fp32.  K8 and V8 become fp16 in registers (exact: cvt e4m3x2 -> f16x2).
 //
-// Bound by memory: 2 D + 2 bytes per token and KV head.  256 sequences of ~1500 tokens with 8 KV heads, D = 128 (811 MB):
-// 127 us, 6.4 TB/s; 64 of ~1000 with 40 KV heads (758 MB): 116 us, 6.5 TB/s; 8 of 32768 with 7 query heads to a KV head
-// (541 MB): 92 us, 5.9 TB/s.  One sequence of 1000 tokens: 11 us, the latency of three kernels.
+// Bound by memory: 2 D + 2 bytes per token and KV head.  256 sequences of ~1500 tokens with 8 KV heads, D = 128 (811
+// MB): 127 us, 6.4 TB/s; 64 of ~1000 with 40 KV heads (758 MB): 116 us, 6.5 TB/s; 8 of 32768 with 7 query heads to a KV
+// head (541 MB): 92 us, 5.9 TB/s.  One sequence of 1000 tokens: 11 us, the latency of three kernels.
 #include <algorithm>
 #include <type_traits>
 
@@ -24,8 +24,8 @@
 namespace pa {
 
 // A consumer warp is bound by the latency of its own chain (scores, maximum, exponentials, products), so the SM needs
-// several: with 32-token stages seven CTAs of three stages (D = 128) fit.  Measured on 256 sequences of ~1500 tokens with
-// 8 KV heads / 8 of 32768 / 64 of ~1000 with 40 KV heads: 4 CTAs 141 / 103 / 125 us, 6 CTAs 131 / 96 / 123, 7 CTAs
+// several: with 32-token stages seven CTAs of three stages (D = 128) fit.  Measured on 256 sequences of ~1500 tokens
+// with 8 KV heads / 8 of 32768 / 64 of ~1000 with 40 KV heads: 4 CTAs 141 / 103 / 125 us, 6 CTAs 131 / 96 / 123, 7 CTAs
 // 131 / 94 / 115, 8 CTAs (two stages each) 138 / 101 / 120; 64-token stages with 4 CTAs 141 / 97 / 120.
 constexpr int kQStageTok = 32;   // tokens of one KV head per pipeline stage
 constexpr int kQCtasPerSm = 7;
@@ -508,8 +508,10 @@ __global__ void __launch_bounds__(kQThreads) attend_quant_kernel(const __grid_co
     #pragma unroll
                     for (int i = 0; i < NT / 2; ++i) {
                         // (va, vb) pairs of elements 4 i .. 4 i + 3, then the same of the tokens 8 later
-                        const uint32_t u0 = __byte_perm(w[0][i], w[1][i], 0x5140), u1 = __byte_perm(w[0][i], w[1][i], 0x7362);
-                        const uint32_t u2 = __byte_perm(w[2][i], w[3][i], 0x5140), u3 = __byte_perm(w[2][i], w[3][i], 0x7362);
+                        const uint32_t u0 = __byte_perm(w[0][i], w[1][i], 0x5140);
+                        const uint32_t u1 = __byte_perm(w[0][i], w[1][i], 0x7362);
+                        const uint32_t u2 = __byte_perm(w[2][i], w[3][i], 0x5140);
+                        const uint32_t u3 = __byte_perm(w[2][i], w[3][i], 0x7362);
                         {
                             const uint32_t r0 = e4m3x2_to_f16x2(u0), r1 = e4m3x2_to_f16x2(u0 >> 16),
                                            r2 = e4m3x2_to_f16x2(u2), r3 = e4m3x2_to_f16x2(u2 >> 16);
@@ -672,7 +674,8 @@ int quant_partition(int N, int H_kv, int max_ctx) {
 pa_status launch_decode_quant(const DecodeQuantArgs& a) {
     WorkspaceLayout L;
     const int pt = quant_partition(a.N, a.H_kv, a.max_ctx);
-    if (!(a.partition_tokens == 0 && workspace_layout(a.N, a.H_q, a.H_kv, a.D, a.max_ctx, pt, &L) && L.total <= a.ws_bytes) &&
+    if (!(a.partition_tokens == 0 && workspace_layout(a.N, a.H_q, a.H_kv, a.D, a.max_ctx, pt, &L) &&
+          L.total <= a.ws_bytes) &&
         !workspace_layout(a.N, a.H_q, a.H_kv, a.D, a.max_ctx, a.partition_tokens, &L))
         return fail(PA_ERR_INVALID, "invalid workspace arguments");
     if (a.ws_bytes < L.total) return fail(PA_ERR_INVALID, "workspace too small: %zu < %zu", a.ws_bytes, L.total);

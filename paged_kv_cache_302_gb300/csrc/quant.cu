@@ -9,13 +9,13 @@ namespace pa {
 
 // ----------------------------------------------------------------------------- write
 
-// A row's D / 16 lanes take 16 elements (32 bytes) each, find the row's largest magnitude with xor shuffles -- as 16-bit
-// integers, two at a time: magnitudes order as their bits do -- and write 16 bytes each; lane 0 of the row writes the
-// scale byte.  Rows are numbered (token, K/V, head).  Bound by memory: 4 D bytes read and 2 D + 2 written per (token,
-// head): 16387 tokens of 8 heads (101 MB) take 17.6 us, 5.7 TB/s.  16 elements per lane and one row at a time with 32
-// registers, 8 CTAs on an SM, measured best: 8 elements per lane took 26 us (half as many bytes in flight, the shuffles
-// and the scale shared by half as many elements), two rows at a time with 4 CTAs 19, four with 2 CTAs 25, a CTA for every
-// 32 rows 20.
+// A row's D / 16 lanes take 16 elements (32 bytes) each, find the row's largest magnitude with xor shuffles -- as
+// 16-bit integers, two at a time: magnitudes order as their bits do -- and write 16 bytes each; lane 0 of the row
+// writes the scale byte.  Rows are numbered (token, K/V, head).  Bound by memory: 4 D bytes read and 2 D + 2 written
+// per (token, head): 16387 tokens of 8 heads (101 MB) take 17.6 us, 5.7 TB/s.  16 elements per lane and one row at a
+// time with 32 registers, 8 CTAs on an SM, measured best: 8 elements per lane took 26 us (half as many bytes in flight,
+// the shuffles and the scale shared by half as many elements), two rows at a time with 4 CTAs 19, four with 2 CTAs 25,
+// a CTA for every 32 rows 20.
 constexpr int kQuantThreads = 256;
 constexpr int kQuantCtasPerSm = 8;
 
@@ -123,9 +123,10 @@ pa_status launch_quant_cache(const void* k, const void* v, void* qpool, void* sc
 
 // ----------------------------------------------------------------------------- read
 
-// A row's D / 16 lanes read 16 values each and write 32 bytes each, one whole sector where the pool allows.  grid.x = pair,
-// grid.y = chunk of the block's rows (numbered (head, K/V, token), the order they lie in).  Bound by memory: 4001 blocks of
-// 16 tokens and 8 heads, D = 128 (394 MB read and written): 63.7 us, 6.2 TB/s; with two 16-byte stores per lane 64.4.
+// A row's D / 16 lanes read 16 values each and write 32 bytes each, one whole sector where the pool allows.  grid.x =
+// pair, grid.y = chunk of the block's rows (numbered (head, K/V, token), the order they lie in).  Bound by memory: 4001
+// blocks of 16 tokens and 8 heads, D = 128 (394 MB read and written): 63.7 us, 6.2 TB/s; with two 16-byte stores per
+// lane 64.4.
 constexpr int kDequantThreads = 256;
 
 template <typename T>

@@ -5,36 +5,37 @@
 // M), so each K/V byte serves every row of a tile, and a (sequence, KV head, row tile) is a unit of ceil(ctx / 128) key
 // tiles.
 //
-// tree_kernel: one persistent CTA per SM.  All key tiles of the call, in unit order, are cut into runs of equal cost, one
-// per CTA, so the GPU is evenly loaded whatever the lengths; a CTA walks its run as segments (consecutive tiles of one
-// unit), and a unit that several CTAs share leaves partial results (m, l, unnormalised O) that tree_merge_kernel joins.
-// A CTA leaves at most two (its first and its last segment), so the workspace has a fixed size.  Roles:
-//   * warps 0-3 and 4-7, two softmax warpgroups: warpgroup w takes keys 64 w .. 64 w + 63 of every tile; each thread owns
-//     one TMEM lane = one query row.  It reads its 64 scores (tcgen05.ld), masks, keeps a running maximum of its own
-//     (its O is rescaled only when that grows by more than 2^8) and writes the probabilities to TMEM, over the scores it
-//     has just read.  The warpgroups have accumulators of their own, O_0 and O_1, joined at the segment's end, so they
-//     never wait for one another in between;
+// tree_kernel: one persistent CTA per SM.  All key tiles of the call, in unit order, are cut into runs of equal cost,
+// one per CTA, so the GPU is evenly loaded whatever the lengths; a CTA walks its run as segments (consecutive tiles of
+// one unit), and a unit that several CTAs share leaves partial results (m, l, unnormalised O) that tree_merge_kernel
+// joins.  A CTA leaves at most two (its first and its last segment), so the workspace has a fixed size.  Roles:
+//   * warps 0-3 and 4-7, two softmax warpgroups: warpgroup w takes keys 64 w .. 64 w + 63 of every tile; each thread
+//     owns one TMEM lane = one query row.  It reads its 64 scores (tcgen05.ld), masks, keeps a running maximum of its
+//     own (its O is rescaled only when that grows by more than 2^8) and writes the probabilities to TMEM, over the
+//     scores it has just read.  The warpgroups have accumulators of their own, O_0 and O_1, joined at the segment's
+//     end, so they never wait for one another in between;
 //   * warp 8 (TMA): query rows (16-bit pool), K and V tiles into rings, block by block through the block table;
-//   * warp 9 (one thread): S = Q K^T into one of two buffers (TMEM columns 0 .. 127 and 128 .. 255), so that a tile's score
-//     product runs under the softmax of the tile before it; warp 10 (one thread): O_w += P_w V (columns 256 + D w), P read
-//     from TMEM;
+//   * warp 9 (one thread): S = Q K^T into one of two buffers (TMEM columns 0 .. 127 and 128 .. 255), so that a tile's
+//     score product runs under the softmax of the tile before it; warp 10 (one thread): O_w += P_w V (columns 256 + D
+//     w), P read from TMEM;
 //   * quantised pool, warps 12-19: e4m3 tiles from the raw ring to fp16 tiles in the K and V rings, and the query rows.
 // The value product takes P in V's 16-bit type: for bf16, or an fp32 output, as a high and a low part (two products).
 //
-// Quantised pool: query rows are scaled to fp16's range by a power of two (exact); K8 is converted to fp16 times 2^(ek -
-// emax + 7), emax the tile's largest exponent (keys 2^22 below it count as zero: a score is off by at most 2^-22 of the
-// largest that a key of the tile could give), V8 likewise where that is exact (see kTreeSpan); with E the exponent taken
-// out of V (per tile, else per key): y = raw c 2^(emax - 7) + E, p = 2^(y - M), O += p (V 2^-E), l += p 2^-E, as in
-// decode_quant.cu.
+// Quantised pool: query rows are scaled to fp16's range by a power of two (exact); K8 is converted to fp16 times 2^(ek
+// - emax + 7), emax the tile's largest exponent (keys 2^22 below it count as zero: a score is off by at most 2^-22 of
+// the largest that a key of the tile could give), V8 likewise where that is exact (see kTreeSpan); with E the exponent
+// taken out of V (per tile, else per key): y = raw c 2^(emax - 7) + E, p = 2^(y - M), O += p (V 2^-E), l += p 2^-E, as
+// in decode_quant.cu.
 //
-// What bounds it, measured at D = 128.  64 sequences with trees of up to 24 tokens, 32 / 8 heads, bf16: 90 us, 4.8 TB/s of
-// K and V.  The bytes alone are 64 us; inside a run a tile takes about 2700 cycles, 64 KB at 7 TB/s over the GPU, and the
-// rest is the launch, the first tiles and the ends of 512 units.  16 trees of up to 63 tokens over 4500 quantised tokens
-// each: 110 us, about 2800 cycles per tile of 128 x 128, bound by the roles' own instructions and waits (the SM issues 2.1
-// of 4 instructions a cycle, the tensor pipe is 28 % busy, memory 20 %).  Of 117 us with all in place, a copy without
-// the conversion to fp16 took 88, without exponentials 113, without both products 109, without all three 83.  What the
-// time was spent on before: one group of converters (114 us), one score buffer (128), masked and keyed tiles in line (138)
-// and spin waits unrolled by the compiler (180), both of which pushed the usual tile's code out of the instruction cache.
+// What bounds it, measured at D = 128.  64 sequences with trees of up to 24 tokens, 32 / 8 heads, bf16: 90 us, 4.8 TB/s
+// of K and V.  The bytes alone are 64 us; inside a run a tile takes about 2700 cycles, 64 KB at 7 TB/s over the GPU,
+// and the rest is the launch, the first tiles and the ends of 512 units.  16 trees of up to 63 tokens over 4500
+// quantised tokens each: 110 us, about 2800 cycles per tile of 128 x 128, bound by the roles' own instructions and
+// waits (the SM issues 2.1 of 4 instructions a cycle, the tensor pipe is 28 % busy, memory 20 %).  Of 117 us with all
+// in place, a copy without the conversion to fp16 took 88, without exponentials 113, without both products 109, without
+// all three 83.  What the time was spent on before: one group of converters (114 us), one score buffer (128), masked
+// and keyed tiles in line (138) and spin waits unrolled by the compiler (180), both of which pushed the usual tile's
+// code out of the instruction cache.
 #include <algorithm>
 #include <cstring>
 #include <type_traits>
@@ -55,8 +56,8 @@ constexpr int kTreeMaxCtas = 160;  // CTAs of a call at most (the workspace hold
 constexpr int kTreeUnitCost = 2;
 constexpr int kConvWarps = 8;  // two groups of four: one for the even tiles, one for the odd
 // Probabilities are relative to a reference kPHeadroom below the row's maximum, which may grow by 2^8 before O is
-// rescaled: they reach 2^15, the top of fp16's range, so that the smallest keep as many bits as fp16 allows (an absolute
-// 2^-25 is 2^-32 of the largest).
+// rescaled: they reach 2^15, the top of fp16's range, so that the smallest keep as many bits as fp16 allows (an
+// absolute 2^-25 is 2^-32 of the largest).
 constexpr float kPHeadroom = 7.f;
 // Quantised V: while the exponents of a tile's scales lie within kTreeSpan of one another, one exponent serves the tile
 // (V8 2^(ev - vmax + 7) is exact in fp16); otherwise (kTreeKeyed) each key's enters the scores.  With the headroom a
@@ -120,8 +121,8 @@ __device__ __forceinline__ int clamp_scale(uint32_t b) { return scale_of((int)b)
 // Eight words to one 32-byte sector (32-byte aligned), or to two halves of one.
 __device__ __forceinline__ void st_words8(void* d, const uint32_t* v, bool sector) {
     if (sector) {
-        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(d), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-                     "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(d), "r"(v[0]), "r"(v[1]),
+                     "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                      : "memory");
     } else {
         static_cast<uint4*>(d)[0] = make_uint4(v[0], v[1], v[2], v[3]);
@@ -209,9 +210,9 @@ struct TreeWalk {
     }
 };
 
-// The CTA's run [lo, hi) of the call's cost, and the sequence it starts in with the part of it that lies before.
-// Every thread of the block calls it; `buf`: 40 words of 8 bytes.  Up to 32 sequences every warp finds it by itself, one
-// lane to a sequence: without barriers and second reads of the lengths the first tiles of 4 sequences start 1 us sooner.
+// The CTA's run [lo, hi) of the call's cost, and the sequence it starts in with the part of it that lies before. Every
+// thread of the block calls it; `buf`: 40 words of 8 bytes.  Up to 32 sequences every warp finds it by itself, one lane
+// to a sequence: without barriers and second reads of the lengths the first tiles of 4 sequences start 1 us sooner.
 struct TreeRun {
     int64_t per, lo, hi, rem;
     int s;
@@ -353,10 +354,10 @@ __device__ __forceinline__ float tree_reference(float m_tile, bool first, float&
     return m_new == -INFINITY ? 0.f : m_new;
 }
 
-// Probabilities of 64 keys with exponents of their own (scale bytes at shared address ex), over the scores
-// at t_s.  Such tiles are rare and are read twice, 32 columns at a time, out of line: with it in line the code of the usual
-// tiles left the instruction cache (a sixth of the time).  Returns the exponential sum, the reference, and the factor of what
-// was summed before.
+// Probabilities of 64 keys with exponents of their own (scale bytes at shared address ex), over the scores at t_s.
+// Such tiles are rare and are read twice, 32 columns at a time, out of line: with it in line the code of the usual
+// tiles left the instruction cache (a sixth of the time).  Returns the exponential sum, the reference, and the factor
+// of what was summed before.
 template <typename PT, bool SPLIT>
 __device__ __noinline__ float3 tree_probabilities_keyed(uint32_t t_s, uint32_t ex, float mul, bool first, float m_ref) {
     uint32_t x[32] = {}, e = 0;
@@ -412,8 +413,8 @@ struct TreeGeo {
     static constexpr int DH = D / 64;
     static constexpr uint32_t kTile = DH * kTRegion;      // one 16-bit tile, [8-row group][column half][8 rows][128 B]
     static constexpr uint32_t kGroup = DH * 1024;
-    // V ring slots and K ring slots.  A converted K tile is free again as soon as its score product is done, long before
-    // its V: one slot serves, and the space holds another raw tile on its way.
+    // V ring slots and K ring slots.  A converted K tile is free again as soon as its score product is done, long
+    // before its V: one slot serves, and the space holds another raw tile on its way.
     static constexpr int NS = QUANT ? 2 : 3, KS = QUANT ? 1 : 3;
     static constexpr int KF = QUANT ? 2 : 3;  // "K read" barriers, by tile in turn
     static constexpr int NR = QUANT ? (D == 128 ? 3 : 6) : 0;      // raw ring slots: K and V rows of a tile, scales
@@ -460,8 +461,8 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_raw + Geo::oSmall);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     volatile int* armed = abort_flag + 1;  // K, V (quantised: raw) tiles and query tiles whose copies have been issued
-    // Of the last four tiles (a tile is converted once the value products of the fourth before it are done): 2^(emax - 7)
-    // of its K; the exponent that its V is scaled down by, or kTreeKeyed.
+    // Of the last four tiles (a tile is converted once the value products of the fourth before it are done): 2^(emax -
+    // 7) of its K; the exponent that its V is scaled down by, or kTreeKeyed.
     float* kmul = reinterpret_cast<float*>(tmem_slot + 5);
     float* vexp = kmul + 4;
     int8_t* qexp = reinterpret_cast<int8_t*>(smem_raw + Geo::oQe);  // per query row: exponent it was scaled down by
@@ -518,8 +519,8 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
         const bool wa = mbar_try_wait(a, pa), wb = mbar_try_wait(b, pb);
         return (wa || waited(a, pa)) && (wb || waited(b, pb));
     };
-    // TMEM columns: the scores of tile t, and on top of a warpgroup's own 64 the P of its 32 keys k (high parts in 16, then
-    // low parts in 16)
+    // TMEM columns: the scores of tile t, and on top of a warpgroup's own 64 the P of its 32 keys k (high parts in 16,
+    // then low parts in 16)
     auto s_col = [](int t) { return (uint32_t)((t & 1) * kTKeys); };
     auto p_col = [&](int t, int w, int k) { return s_col(t) + (uint32_t)(w * 64 + k * (SPLIT ? 32 : 16)); };
     auto slot = [](int i) { return (uint32_t)(i % NS); };
@@ -609,7 +610,8 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                     for (int j = g.j0; j < g.j1 && ok; ++j, ++t) {
                         // the buffer is free once the value products of the tile before last have read its P
                         ok = t < 2 ? waited(kfull + 8 * kslot(t), kph(t))
-                                   : waited2(pvd + 8 * (t & 1), (uint32_t)((t - 2) >> 1 & 1), kfull + 8 * kslot(t), kph(t));
+                                   : waited2(pvd + 8 * (t & 1), (uint32_t)((t - 2) >> 1 & 1),
+                                             kfull + 8 * kslot(t), kph(t));
                         if (!ok) break;
                         tc_fence_after();
                         const uint64_t dk = umma_desc(sK + kslot(t) * kTile, 16, kGroup);
@@ -667,19 +669,22 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                 const uint32_t to = (uint32_t)(row >> 3) * kGroup + (row & 7) * 128;
                 int t = 0;
                 for (int seg = 0; walk.next(p, g); ++seg) {
-                    // the query rows as fp16, four lanes to a row: read, then written once the last segment's have been used
+                    // the query rows as fp16, four lanes to a row: read, then written once the last segment's have been
+                    // used
                     {
-                        constexpr int C = D / 32;                                     // 16-byte pieces of a row per lane
-                        constexpr int R = kTRows / 8 / kConvWarps;                    // rows per lane
+                        constexpr int C = D / 32;                   // 16-byte pieces of a row per lane
+                        constexpr int R = kTRows / 8 / kConvWarps;  // rows per lane
                         const int tok0 = g.mt * p.TQ, rows = min(p.TQ, g.n - tok0) * p.G;
                         uint4 xs[R][C];
 #pragma unroll
                         for (int k = 0; k < R; ++k) {
                             const int r = (cw + k * kConvWarps) * 8 + (lane >> 2);
-                            const size_t row = ((size_t)(g.qs + tok0 + r / p.G) * p.H_q + (size_t)g.h * p.G + r % p.G) * D;
+                            const size_t row =
+                                ((size_t)(g.qs + tok0 + r / p.G) * p.H_q + (size_t)g.h * p.G + r % p.G) * D;
                             const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + row);
 #pragma unroll
-                            for (int i = 0; i < C; ++i) xs[k][i] = r < rows ? src[4 * i + (lane & 3)] : make_uint4(0, 0, 0, 0);
+                            for (int i = 0; i < C; ++i)
+                                xs[k][i] = r < rows ? src[4 * i + (lane & 3)] : make_uint4(0, 0, 0, 0);
                         }
                         if (seg > 0) {
                             ok = waited(qfree, (uint32_t)((seg - 1) & 1)) && ok;
@@ -721,8 +726,9 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
 #pragma unroll
                             for (int i = 0; i < C; ++i) {
                                 const int ch = 4 * i + (lane & 3);  // piece of the row
-                                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                                 sQ + (uint32_t)(ch >> 3) * kTRegion + r * 128 + (((ch & 7) ^ (r & 7)) << 4)),
+                                const uint32_t dst =
+                                    sQ + (uint32_t)(ch >> 3) * kTRegion + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+                                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst),
                                              "r"(x[i].x), "r"(x[i].y), "r"(x[i].z), "r"(x[i].w)
                                              : "memory");
                             }
@@ -735,7 +741,8 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                         if ((t & 1) != cw >> 2) continue;
                         const int k0 = j * kTKeys;
                         const uint32_t rb = (uint32_t)(t % NR);
-                        const uint32_t raw = sb + Geo::oRaw + rb * Geo::kRaw, rsc = sb + Geo::oRawSc + rb * Geo::kRawScales;
+                        const uint32_t raw = sb + Geo::oRaw + rb * Geo::kRaw;
+                        const uint32_t rsc = sb + Geo::oRawSc + rb * Geo::kRawScales;
                         uint32_t u[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
                         const bool masked = k0 + kTKeys > g.ctx - g.n;
                         if (masked) tree_union<4>(p, g, k0, u);  // keys past the context are in none
@@ -747,8 +754,9 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                         asm volatile("ld.shared.u32 %0, [%1];" : "=r"(kb) : "r"(at));
                         asm volatile("ld.shared.u32 %0, [%1];" : "=r"(vb) : "r"(at + B));
                         uint32_t vlow = vb;  // (for the least of V's)
-                        if (masked) {        // bytes of keys nobody sees: the least scale (for the least of V's: the largest)
-                            const uint32_t m = ((u[lane >> 3] >> (4 * lane & 31) & 0xfu) * 0x00204081u & 0x01010101u) * 255u;
+                        if (masked) {  // bytes of keys nobody sees: the least scale (for the least of V's: the largest)
+                            const uint32_t four = u[lane >> 3] >> (4 * lane & 31) & 0xfu;
+                            const uint32_t m = (four * 0x00204081u & 0x01010101u) * 255u;
                             kb = (kb & m) | (~m & 0x57575757u);
                             vlow = (vb & m) | (~m & 0xa7a7a7a7u);
                             vb = (vb & m) | (~m & 0x57575757u);
@@ -761,27 +769,31 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                         const int vm = clamp_scale(__reduce_max_sync(0xffffffffu, max(vx & 0xffffu, vx >> 16)));
                         const int vl = clamp_scale(__reduce_min_sync(0xffffffffu, min(vn & 0xffffu, vn >> 16)));
                         const bool keyed = vm - vl > kTreeSpan;
-                        // fp16 factors 2^(e - max + 7) of this lane's row: exponent field e - max + 7 + 15, or a factor of zero
-                        // where that is not positive.  V8 as it is when keyed.  A row that nobody sees, past the context or
-                        // padding, may hold anything: it counts as zeros.
+                        // fp16 factors 2^(e - max + 7) of this lane's row: exponent field e - max + 7 + 15, or a factor
+                        // of zero where that is not positive.  V8 as it is when keyed.  A row that nobody sees, past
+                        // the context or padding, may hold anything: it counts as zeros.
                         const bool seen = u[cw & 3] >> lane & 1u;
                         uint32_t bk, bv;
                         asm volatile("ld.shared.u8 %0, [%1];" : "=r"(bk) : "r"(rsc + ro));
                         asm volatile("ld.shared.u8 %0, [%1];" : "=r"(bv) : "r"(rsc + ro + B));
                         const int ek = clamp_scale(bk), ev = clamp_scale(bv);
                         const uint32_t fk = seen ? (uint32_t)max(ek - em + 22, 0) * 0x04000400u : 0u;
-                        const uint32_t fv = seen ? (keyed ? 0x3c003c00u : (uint32_t)max(ev - vm + 22, 0) * 0x04000400u) : 0u;
+                        const uint32_t scaled = keyed ? 0x3c003c00u : (uint32_t)max(ev - vm + 22, 0) * 0x04000400u;
+                        const uint32_t fv = seen ? scaled : 0u;
 #pragma unroll 1
                         for (int i = 0; i < 4; ++i) {  // K's and V's row, in halves
                             const int which = i >> 1, c0 = (i & 1) * (D / 32);
                             const uint32_t f2 = which ? fv : fk;
                             // the last K tile's score product has read it; the last V in this slot is used up
-                            if (i == 0 && t >= 1) ok = waited(kfree + 8 * ((t - 1) % KF), (uint32_t)((t - 1) / KF & 1)) && ok;
+                            if (i == 0 && t >= 1)
+                                ok = waited(kfree + 8 * ((t - 1) % KF), (uint32_t)((t - 1) / KF & 1)) && ok;
                             if (i == 2 && t >= NS) ok = waited(vfree + 8 * sl, ph(t - NS)) && ok;
                             // addresses of the half's pieces differ from its first's in the swizzled bits only
-                            const uint32_t src = raw + so + (which ? B * D : 0) + ((c0 ^ (D == 128 ? row & 7 : row >> 1 & 3)) << 4);
-                            const uint32_t dst = (which ? sV + sl * kTile : sK) + to +
-                                                 (D == 128 ? (i & 1) * 1024 + ((row & 7) << 4) : ((2 * c0) ^ (row & 7)) << 4);
+                            const uint32_t src =
+                                raw + so + (which ? B * D : 0) + ((c0 ^ (D == 128 ? row & 7 : row >> 1 & 3)) << 4);
+                            const uint32_t dst =
+                                (which ? sV + sl * kTile : sK) + to +
+                                (D == 128 ? (i & 1) * 1024 + ((row & 7) << 4) : ((2 * c0) ^ (row & 7)) << 4);
                             uint4 vs[D / 32];  // all read before the first is converted
 #pragma unroll
                             for (int cc = 0; cc < D / 32; ++cc)
@@ -807,7 +819,8 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                                 }
 #pragma unroll
                                 for (int o = 0; o < 2; ++o)
-                                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst ^ ((2 * cc + o) << 4)),
+                                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                                     dst ^ ((2 * cc + o) << 4)),
                                                  "r"(h[4 * o]), "r"(h[4 * o + 1]), "r"(h[4 * o + 2]), "r"(h[4 * o + 3])
                                                  : "memory");
                             }
@@ -884,7 +897,8 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                         for (int i = 0; i < 4; ++i)
                             mx[i] = fmax3(mx[i], __uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
                     }
-                    const float m_tile = fmaf(fmax3(mx[0], mx[1], fmaxf(mx[2], mx[3])), mul, E) - kPHeadroom;  // (mul > 0)
+                    const float top = fmax3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
+                    const float m_tile = fmaf(top, mul, E) - kPHeadroom;  // (mul > 0)
                     const float off = E - tree_reference(m_tile, j == g.j0, m_ref, alpha);
                     const float2 mul2 = make_float2(mul, mul), off2 = make_float2(off, off);
                     float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -989,8 +1003,8 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
             ok = waited(pvd + 8 * ((t - 1) & 1), (uint32_t)(((t - 1) >> 1) & 1)) && ok;
             tc_fence_after();
             if (warp_ok) {
-                // whole 32-byte sectors per lane where `out` allows: half the store instructions.  (16 columns at a time:
-                // the code of a unit's end is seldom in the instruction cache, so it is kept short.)
+                // whole 32-byte sectors per lane where `out` allows: half the store instructions.  (16 columns at a
+                // time: the code of a unit's end is seldom in the instruction cache, so it is kept short.)
                 const bool sector = !whole || (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
                 const bool f32 = !whole || p.out_dtype == PA_F32;
                 const float f = whole ? inv : 1.f;
@@ -1018,7 +1032,8 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
 #pragma unroll
                             for (int x = 0; x < 8; ++x) {
                                 const float lo = __uint_as_float(a[2 * x]), up = __uint_as_float(a[2 * x + 1]);
-                                h[x] = p.out_dtype == PA_BF16 ? Mma<__nv_bfloat16>::pack(lo, up) : Mma<__half>::pack(lo, up);
+                                h[x] = p.out_dtype == PA_BF16 ? Mma<__nv_bfloat16>::pack(lo, up)
+                                                              : Mma<__half>::pack(lo, up);
                             }
                             st_words8(dst + 2 * col, h, sector);
                         }
@@ -1079,7 +1094,8 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeParams p) {
     for (int v = 0; v < V; ++v) o[v] = 0.f;
     for (int b = 0; b < d.w; b += kChunk) {
         const int n = min(kChunk, d.w - b);
-        const float2 ml = lane < n ? reinterpret_cast<const float2*>(p.part_ml)[at(b + lane)] : make_float2(-INFINITY, 0.f);
+        const float2 ml =
+            lane < n ? reinterpret_cast<const float2*>(p.part_ml)[at(b + lane)] : make_float2(-INFINITY, 0.f);
         float a[kChunk][V];
 #pragma unroll
         for (int j = 0; j < kChunk; ++j)
@@ -1149,7 +1165,8 @@ static pa_status run_tree(const TreeParams& p, const CUtensorMap& tm, const CUte
     e = launch_kernel(kern, dim3(ctas), dim3(Geo::kThreads), Geo::kSmem, stream, tm, tm_q, p);
     count_launch();
     if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
-    e = launch_kernel(tree_merge_kernel<D>, dim3(ctas, (std::min(p.TQ, p.max_q_len) * p.G + 7) / 8), dim3(256), 0, stream, p);
+    const int rows = std::min(p.TQ, p.max_q_len) * p.G;  // of a row tile at most
+    e = launch_kernel(tree_merge_kernel<D>, dim3(ctas, (rows + 7) / 8), dim3(256), 0, stream, p);
     count_launch();
     return e == cudaSuccess ? PA_OK : cuda_fail(e, "tree merge launch");
 }
