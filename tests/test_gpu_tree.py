@@ -427,3 +427,27 @@ def test_tree_blocks_behind_32_bit_offsets(quant):
         pa.pa_reshape_and_cache(c.k.cuda(), c.v.cuda(), c.pool, c.slots.cuda())
     r = np.random.default_rng(13)
     check(c, G, [random_tree(r, 5), random_tree(r, 2)])
+
+
+@pytest.mark.parametrize("quant", [False, True])
+def test_tree_calls_of_small_heads_beside_each_other(quant):
+    """D = 64: two CTAs of the 16-bit kernel fit an SM's shared memory, and the second waits for the first one's tensor
+    memory.  Calls on three streams, each with a workspace of its own, give the bits they give alone."""
+    r = np.random.default_rng(15)
+    c = Cache(90, [3000, 700, 41, 1900] * 10, 2, 64, 16, "f16", quant=quant)
+    masks = [random_tree(r, 16) for _ in c.ctx]
+    q = torch.randn(16 * 40, 8, 64).half().cuda()
+    ref = run_tree(c, q, masks)
+    qs = torch.arange(0, 16 * 41, 16, dtype=torch.int32).cuda()
+    m = pack(masks, 1).cuda()
+    need = pa.pa_decode_tree_workspace_bytes(40, 8, 2, 64, 16)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    outs = [torch.zeros_like(ref) for _ in streams]
+    ws = [torch.empty(need, dtype=torch.uint8, device="cuda") for _ in streams]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for st, o, w in zip(streams, outs, ws):
+            pa.pa_decode_tree(o, q, c.qp if quant else c.pool, c.dtab, c.dctx, qs, m, 16,
+                              scales=c.sc if quant else None, workspace=w, stream=st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, ref) for o in outs)
