@@ -898,7 +898,7 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                             mx[i] = fmax3(mx[i], __uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
                     }
                     const float top = fmax3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
-                    const float m_tile = fmaf(top, mul, E) - kPHeadroom;  // (mul > 0)
+                    const float m_tile = fmaf(top, mul, E) - kPHeadroom;  // (mul > 0: -inf stays so)
                     const float off = E - tree_reference(m_tile, j == g.j0, m_ref, alpha);
                     const float2 mul2 = make_float2(mul, mul), off2 = make_float2(off, off);
                     float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -928,7 +928,10 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
                     l = fmaf(l, alpha, sum);
                 };
                 if (warp_ok) {
-                    const float mul = QUANT ? cr * kmul[t & 3] : cr;
+                    // The product may leave fp32's range downwards (small queries; 2^-47 of a tile that nobody sees), and
+                    // -inf times zero is NaN: it is held to 2^-126.  A raw score is at most 2^39, so that moves a score
+                    // by 2^-87 at most.
+                    const float mul = QUANT ? fmaxf(cr * kmul[t & 3], 0x1p-126f) : cr;
                     const float E = QUANT ? vexp[t & 3] : 0.f;
                     if (masked) tree_mask_scores(t_s, vis[0], vis[1]);
                     if (QUANT && E == kTreeKeyed) {

@@ -451,3 +451,45 @@ def test_tree_calls_of_small_heads_beside_each_other(quant):
                               scales=c.sc if quant else None, workspace=w, stream=st)
     torch.cuda.synchronize()
     assert all(torch.equal(o, ref) for o in outs)
+
+
+@pytest.mark.parametrize("D, B", [(128, 16), (64, 8)])
+def test_tree_quantised_queries_of_extreme_size(D, B):
+    """bf16 queries far outside fp16's range under a tiny scale, over contexts that end inside a key tile: unseen keys
+    count for nothing, whatever a score's factor rounds to."""
+    c = Cache(57, [50, 300], 1, D, B, "bf16")
+    r = np.random.default_rng(16)
+    q = torch.randn(9, 3, D, generator=torch.Generator().manual_seed(2))
+    q[0, 0] *= 1e9
+    q[0, 1] *= 1e-9
+    q[0, 2] = 0
+    q[1, 0, 5] = 3e4
+    q[1:3, 1] *= 1e-30
+    q[5:, 2] *= 1e-36
+    check(c, 3, [random_tree(r, 4), random_tree(r, 5)], q=q.to(torch.bfloat16), scale=1e-9)
+
+
+@pytest.mark.parametrize("keyed", [False, True])
+def test_tree_quantised_small_queries_before_key_tiles_they_do_not_see(keyed):
+    """Causal drafts longer than a key tile, the default scale: later key tiles are seen by no row of the first row
+    tiles, whose queries lie 2^86 and more below one; with V scales close together and far apart."""
+    r = np.random.default_rng(17)
+    c = Cache(58, [300, 420], 1, 64, 16, "bf16")
+    if keyed:
+        g = torch.Generator().manual_seed(1)
+        size = torch.exp2(torch.randint(-18, 14, (c.v.shape[0], 1, 1), generator=g).float())
+        c.v = (torch.randn(c.v.shape, generator=g) * size).to(c.dtype)
+        pa.pa_reshape_and_cache_quant(c.k.cuda(), c.v.cuda(), c.qp, c.sc, c.slots.cuda())
+    q = torch.randn(600, 2, 64, generator=torch.Generator().manual_seed(3))
+    q *= torch.exp2(torch.from_numpy(r.integers(-118, -84, size=(600, 2, 1))).float())
+    check(c, 2, [np.tril(np.ones((300, 300), bool))] * 2, q=q.to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("scale", [1e-25, 1e-38, 3e-44])
+def test_tree_tiny_scales(quant, dtype, scale):
+    """Scales down to fp32's subnormal numbers: nearly uniform weights of what each row sees."""
+    r = np.random.default_rng(18)
+    c = Cache(59, [140, 300], 2, 128, 16, dtype, quant=quant)
+    check(c, 2, [np.tril(np.ones((140, 140), bool)), random_tree(r, 20)], scale=scale)
