@@ -1006,9 +1006,11 @@ __global__ void __launch_bounds__(TreeGeo<D, QUANT>::kThreads, 1)
             ok = waited(pvd + 8 * ((t - 1) & 1), (uint32_t)(((t - 1) >> 1) & 1)) && ok;
             tc_fence_after();
             if (warp_ok) {
-                // whole 32-byte sectors per lane where `out` allows: half the store instructions.  (16 columns at a
-                // time: the code of a unit's end is seldom in the instruction cache, so it is kept short.)
-                const bool sector = !whole || (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
+                // whole 32-byte sectors per lane where `out` or the workspace is aligned to them (a caller need align
+                // either to 16 bytes only): half the store instructions.  (16 columns at a time: the code of a unit's
+                // end is seldom in the instruction cache, so it is kept short.)
+                const void* to = whole ? p.out : p.part_acc;
+                const bool sector = (reinterpret_cast<uintptr_t>(to) & 31u) == 0;
                 const bool f32 = !whole || p.out_dtype == PA_F32;
                 const float f = whole ? inv : 1.f;
                 const float g0 = den == 0.f && whole ? 0.f : f0 * f, g1 = den == 0.f && whole ? 0.f : f1 * f;

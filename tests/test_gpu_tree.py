@@ -493,3 +493,25 @@ def test_tree_tiny_scales(quant, dtype, scale):
     r = np.random.default_rng(18)
     c = Cache(59, [140, 300], 2, 128, 16, dtype, quant=quant)
     check(c, 2, [np.tril(np.ones((140, 140), bool)), random_tree(r, 20)], scale=scale)
+
+
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("D, B", [(128, 16), (64, 8)])
+def test_tree_workspace_that_is_16_byte_aligned_only(quant, D, B):
+    """A workspace cut from a larger buffer at an odd multiple of 16 bytes, sequences long enough for every unit to be
+    shared by several CTAs: the same bits as with an aligned one, and nothing beside it written."""
+    c = Cache(83, [6000, 130, 2500], 2, D, B, "bf16", quant=quant)
+    r = np.random.default_rng(19)
+    masks = [random_tree(r, 20), random_tree(r, 3), random_tree(r, 45)]
+    q = torch.randn(68, 6, D, generator=torch.Generator().manual_seed(4)).bfloat16()
+    need = pa.pa_decode_tree_workspace_bytes(3, 6, 2, D, 45)
+    base = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    for dt in (torch.float32, torch.bfloat16):
+        want = run_tree(c, q.cuda(), masks, out_dtype=dt)
+        compare(c, 3, masks, q, want)
+        for at in (16, 48, 2064):
+            ws = base[at: at + need]
+            assert ws.data_ptr() % 32 == 16
+            assert torch.equal(run_tree(c, q.cuda(), masks, out_dtype=dt, ws=ws), want)
+            assert (base[:at] == 0xA5).all() and (base[at + need:] == 0xA5).all()
+            base.fill_(0xA5)
