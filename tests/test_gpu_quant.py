@@ -501,3 +501,21 @@ def test_read_into_a_pool_that_is_16_byte_aligned_only():
     pa.pa_dequant_blocks(odd, qp, sc, pairs)
     pa.pa_dequant_blocks(even, qp, sc, pairs)
     assert torch.equal(odd, even) and even.abs().sum() > 0 and (base[:8] == 0).all() and (base[8 + n:] == 0).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_decode_workspace_and_output_that_are_16_byte_aligned_only(D):
+    c = Cache(73, [2100, 600, 5, 513], 2, D, 16, "f16")
+    q = torch.randn(4, 8, D, generator=torch.Generator().manual_seed(6)).half().cuda()
+    need = pa.pa_decode_workspace_bytes(4, 8, 2, D, 2100)
+    base = torch.full((need + 64,), 0xA5, dtype=torch.uint8, device="cuda")
+    ws = base[16: 16 + need]
+    for dt in (torch.float32, torch.float16):
+        k = 16 // torch.empty(0, dtype=dt).element_size()
+        outs = torch.zeros(4 * 8 * D + 2 * k, dtype=dt, device="cuda")
+        out, want = outs[k:-k].view(4, 8, D), torch.zeros(4, 8, D, dtype=dt, device="cuda")
+        assert out.data_ptr() % 32 == 16 and ws.data_ptr() % 32 == 16
+        pa.pa_decode_quant(out, q, c.qp, c.sc, c.dtab, c.dctx, 2100, workspace=ws)
+        pa.pa_decode_quant(want, q, c.qp, c.sc, c.dtab, c.dctx, 2100)
+        assert torch.equal(out, want) and (outs[:k] == 0).all() and (outs[-k:] == 0).all()
+        assert (base[:16] == 0xA5).all() and (base[16 + need:] == 0xA5).all()
