@@ -170,12 +170,14 @@ _SCALE_TYPES = (torch.uint8, torch.float8_e8m0fnu)
 
 
 def _block_shape(pool):
-    """(NB, B, 2, H_kv, D, dtype code) of a pool whose blocks are moved whole: 16-bit, or a qpool or its scales
-    (8-bit, any order of the inner dimensions: only their product counts)."""
+    """(NB, B, 2, H_kv, D, dtype code) of a pool whose blocks are moved whole: 16-bit, or a qpool or its scales (whose
+    inner dimensions stand in another order: only their product counts).  The library takes the 2 for granted."""
     if pool.dtype in _E4M3_TYPES + _SCALE_TYPES:
-        if pool.dim() not in (4, 5):
+        if pool.dim() not in (4, 5) or pool.shape[2] != 2:
             raise PAError(PA_ERR_INVALID, "a quantised pool is qpool [NB, H_kv, 2, B, D] or scales [NB, H_kv, 2, B]")
         return tuple(pool.shape) + (() if pool.dim() == 5 else (1,)) + (PA_E4M3,)
+    if pool.dim() != 5 or pool.shape[2] != 2:
+        raise PAError(PA_ERR_INVALID, "a 16-bit pool is [NB, B, 2, H_kv, D]")
     return tuple(pool.shape) + (_dtype_code(pool.dtype),)
 
 

@@ -139,3 +139,20 @@ def test_tree_refuses_scales_that_are_not_positive_numbers(scale):
     assert pa.load().pa_decode_tree(A[0], F32, A[1], BF16, A[2], None, BF16, A[3], A[4], A[5], A[6], 1, 1, 4, 8, 2, 128, 16,
                                     4, 4, 4, scale, A[7], 1 << 30, None, None) == INV
     assert "scale" in pa.last_error()
+
+
+@pytest.mark.parametrize("dtype", [torch.uint8, torch.float8_e4m3fn, torch.bfloat16])
+@pytest.mark.parametrize("shape", [(4, 8, 1, 16, 64), (4, 2, 8, 16, 64), (4, 8, 16, 2, 64), (4, 8, 3, 16, 64)])
+def test_block_moves_refuse_pools_of_another_shape(dtype, shape):
+    """The size of a block counts K and V once each: a pool whose third dimension is not 2 would be moved in blocks of
+    another size than its own, past its end among other places."""
+    pool, pairs = torch.zeros(shape, dtype=torch.uint8).to(dtype), torch.zeros(1, 2, dtype=torch.int64)
+    for move in (lambda: pa.pa_copy_blocks(pool, pairs), lambda: pa.pa_swap_blocks(pool, pool, pairs)):
+        with pytest.raises(pa.PAError, match="pool is "):
+            move()
+
+
+def test_block_moves_refuse_scales_of_another_shape():
+    for shape in ((4, 8, 1, 16), (4, 2, 8, 16), (4, 8, 2)):
+        with pytest.raises(pa.PAError, match="pool is "):
+            pa.pa_copy_blocks(torch.zeros(shape, dtype=torch.uint8), torch.zeros(1, 2, dtype=torch.int64))
