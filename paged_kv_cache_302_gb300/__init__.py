@@ -319,9 +319,17 @@ def pa_decode_workspace_bytes(N, H_q, H_kv, D, max_ctx, partition_tokens=0) -> i
     return int(n)
 
 
-def _workspace(workspace, nbytes, device):
-    """The caller's workspace (the library checks its size), or a new one."""
-    return torch.empty(nbytes, dtype=torch.uint8, device=device) if workspace is None else workspace
+def _workspace(workspace, nbytes, device, stream):
+    """The caller's workspace (the library checks its size), or a new one of the call's stream: it is let go while the
+    kernels may still run, so its memory may go to later work of that stream only."""
+    if workspace is not None:
+        return workspace
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
 def pa_decode(out, q, pool, block_tables, ctx_lens, max_ctx, scale=None, partition_tokens=0, workspace=None,
@@ -337,7 +345,7 @@ def pa_decode(out, q, pool, block_tables, ctx_lens, max_ctx, scale=None, partiti
         raise PAError(PA_ERR_INVALID, "block_tables must be [N, MB] and ctx_lens [N]")
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
     nbytes = pa_decode_workspace_bytes(N, H_q, H_kv, D, int(max_ctx), partition_tokens)
-    ws = _workspace(workspace, nbytes, q.device)
+    ws = _workspace(workspace, nbytes, q.device, stream)
     L = load()
     _check(L.pa_decode(_acc(out, "out"), _dtype_code(out.dtype), _dev(q, "q"), _dev(pool, "pool"),
                        _dev(block_tables, "block_tables", torch.int32), _dev(ctx_lens, "ctx_lens", torch.int32), N,
@@ -422,7 +430,7 @@ def pa_decode_contiguous(out, q, k_buf, v_buf, req_ids, ctx_lens, max_ctx, scale
         raise PAError(PA_ERR_INVALID, "dtype mismatch")
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
     nbytes = pa_decode_workspace_bytes(N, H_q, H_kv, D, int(max_ctx), partition_tokens)
-    ws = _workspace(workspace, nbytes, q.device)
+    ws = _workspace(workspace, nbytes, q.device, stream)
     L = load()
     _check(L.pa_decode_contiguous(_dev(out, "out"), _dtype_code(out.dtype), _dev(q, "q"), _dev(k_buf, "k_buf"),
                                   _dev(v_buf, "v_buf"), _dev(req_ids, "req_ids", torch.int32),
@@ -454,7 +462,7 @@ def pa_prefill(out, q, pool, block_tables, ctx_lens, q_start, max_q_len, scale=N
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
     ws, ws_bytes = None, 0
     if stage_v and pool.dtype == torch.bfloat16:
-        ws = _workspace(workspace, pa_prefill_workspace_bytes(N, H_kv, D, B, MB), q.device)
+        ws = _workspace(workspace, pa_prefill_workspace_bytes(N, H_kv, D, B, MB), q.device, stream)
         ws_bytes = ws.numel() * ws.element_size()
     L = load()
     _check(L.pa_prefill(_dev(out, "out"), _dtype_code(out.dtype), _dev(q, "q"), _dev(pool, "pool"),
@@ -515,7 +523,7 @@ def pa_decode_quant(out, q, qpool, scales, block_tables, ctx_lens, max_ctx, scal
     max_ctx, partition_tokens = int(max_ctx), int(partition_tokens)
     ws = workspace
     if ws is None:
-        ws = torch.empty(_decode_bytes(N, H_q, H_kv, D, max_ctx, partition_tokens), dtype=torch.uint8, device=q.device)
+        ws = _workspace(None, _decode_bytes(N, H_q, H_kv, D, max_ctx, partition_tokens), q.device, stream)
     _check((_lib or load()).pa_decode_quant(
         _out_arg(out, "out", dev), _code(out.dtype), _arg(q, "q", dev), _code(q.dtype), _arg(qpool, "qpool", dev),
         _arg(scales, "scales", dev), _arg(block_tables, "block_tables", dev, torch.int32),
@@ -562,7 +570,7 @@ def pa_decode_tree(out, q, pool, block_tables, ctx_lens, q_start, tree_mask, max
     max_q_len = int(max_q_len)
     ws = workspace
     if ws is None:
-        ws = torch.empty(_tree_bytes(N, H_q, H_kv, D, max_q_len), dtype=torch.uint8, device=q.device)
+        ws = _workspace(None, _tree_bytes(N, H_q, H_kv, D, max_q_len), q.device, stream)
     _check((_lib or load()).pa_decode_tree(
         _arg(out, "out", dev), _code(out.dtype), _arg(q, "q", dev), _code(q.dtype), _arg(pool, "pool", dev),
         _arg(scales, "scales", dev) if scales is not None else None, code,
@@ -649,7 +657,7 @@ def pa_decode_contiguous_raw(out, q, k_ptr: int, v_ptr: int, req_ids, ctx_lens, 
         raise PAError(PA_ERR_INVALID, "shape mismatch")
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
     nbytes = pa_decode_workspace_bytes(N, H_q, H_kv, D, int(max_ctx), partition_tokens)
-    ws = _workspace(workspace, nbytes, q.device)
+    ws = _workspace(workspace, nbytes, q.device, stream)
     L = load()
     _check(L.pa_decode_contiguous(_dev(out, "out"), _dtype_code(out.dtype), _dev(q, "q"), ctypes.c_void_p(int(k_ptr)),
                                   ctypes.c_void_p(int(v_ptr)), _dev(req_ids, "req_ids", torch.int32),

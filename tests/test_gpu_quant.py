@@ -519,3 +519,43 @@ def test_decode_workspace_and_output_that_are_16_byte_aligned_only(D):
         pa.pa_decode_quant(want, q, c.qp, c.sc, c.dtab, c.dctx, 2100)
         assert torch.equal(out, want) and (outs[:k] == 0).all() and (outs[-k:] == 0).all()
         assert (base[:16] == 0xA5).all() and (base[16 + need:] == 0xA5).all()
+
+
+@pytest.mark.parametrize("call", ["decode_quant", "tree", "decode", "prefill"])
+def test_a_workspace_made_by_a_call_on_another_stream_stays_with_that_stream(call, monkeypatch):
+    """The library's own workspace of a call on a side stream does not serve the current stream's next allocation, which
+    may be written while the call's kernels run.  (Nothing is written here: only the addresses are compared.)"""
+    quant = call in ("decode_quant", "tree")
+    c = Cache(74, [2100, 600], 2, 128, 16, "bf16", quant=quant)
+    q = torch.randn(2, 8, 128, generator=torch.Generator().manual_seed(7)).bfloat16().cuda()
+    qs, mask = torch.arange(3, dtype=torch.int32).cuda(), torch.ones(2, 1, dtype=torch.int32).cuda()
+
+    def run(out, **kw):
+        if call == "decode_quant":
+            pa.pa_decode_quant(out, q, c.qp, c.sc, c.dtab, c.dctx, 2100, **kw)
+        elif call == "tree":
+            pa.pa_decode_tree(out, q, c.qp, c.dtab, c.dctx, qs, mask, 1, scales=c.sc, **kw)
+        elif call == "decode":
+            pa.pa_decode(out, q, c.pool, c.dtab, c.dctx, 2100, **kw)
+        else:
+            pa.pa_prefill(out, q, c.pool, c.dtab, c.dctx, qs, 1, **kw)
+
+    ref, out = torch.empty(2, 8, 128, device="cuda"), torch.empty(2, 8, 128, device="cuda")
+    run(ref)
+    torch.cuda.synchronize()
+    made, empty = [], torch.empty
+
+    def recorded(*a, **kw):
+        t = empty(*a, **kw)
+        made.append((t.data_ptr(), t.numel()))
+        return t
+
+    side = torch.cuda.Stream()
+    monkeypatch.setattr(torch, "empty", recorded)
+    run(out, stream=side)
+    monkeypatch.setattr(torch, "empty", empty)
+    (at, size), = made
+    later = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    assert torch.equal(out, ref)
+    assert all(t.data_ptr() + size <= at or at + size <= t.data_ptr() for t in later)

@@ -156,3 +156,31 @@ def test_block_moves_refuse_scales_of_another_shape():
     for shape in ((4, 8, 1, 16), (4, 2, 8, 16), (4, 8, 2)):
         with pytest.raises(pa.PAError, match="pool is "):
             pa.pa_copy_blocks(torch.zeros(shape, dtype=torch.uint8), torch.zeros(1, 2, dtype=torch.int64))
+
+
+def test_a_workspace_made_by_a_call_belongs_to_the_calls_stream(monkeypatch):
+    """Memory let go at the end of a call may serve the stream it was taken under at once: that has to be the stream the
+    kernels run on."""
+    current, seen = [None], []
+
+    class Under:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            current[0] = self.stream
+
+        def __exit__(self, *exc):
+            current[0] = None
+
+    class Stream:
+        cuda_stream = 0x77
+
+    empty = torch.empty
+    monkeypatch.setattr(torch.cuda, "stream", Under)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda ptr, device=None: ptr)
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: (seen.append(current[0]), empty(*a, **kw))[1])
+    mine = empty(64, dtype=torch.uint8)
+    assert pa._workspace(mine, 64, "cpu", Stream()) is mine and seen == []
+    assert pa._workspace(None, 64, "cpu", Stream()).numel() == 64 and seen == [0x77]
+    assert pa._workspace(None, 64, "cpu", None).numel() == 64 and seen == [0x77, None]
