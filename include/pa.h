@@ -142,10 +142,11 @@ pa_status pa_update_block_tables(int32_t* tables, int N, int MB, const int32_t* 
  * Workspace for pa_decode / pa_decode_contiguous / pa_decode_quant, in bytes.
  * partition_tokens: 0 = default (512; pa_decode_quant takes 64 to 512 by the
  * size of the batch where the workspace has room, which this function grants
- * it, else 512), -1 = one partition per sequence, > 0 = split each context into
- * partitions of that many tokens (a multiple of 32).  max_ctx bounds every
- * context length of the calls that use the workspace.  Returns 0 for invalid
- * arguments.
+ * it, else 512; for all of them the length that the environment variable
+ * PA_DECODE_PARTITION names, where it names one), -1 = one partition per
+ * sequence, > 0 = split each context into partitions of that many tokens (a
+ * multiple of 32).  max_ctx bounds every context length of the calls that use
+ * the workspace.  Returns 0 for invalid arguments.
  * ---------------------------------------------------------------------- */
 size_t pa_decode_workspace_bytes(int N, int H_q, int H_kv, int D, int max_ctx, int partition_tokens);
 

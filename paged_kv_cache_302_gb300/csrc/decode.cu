@@ -59,15 +59,19 @@ struct __align__(16) StageMeta {
 
 static size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// Partition length for partition_tokens == 0: kDefaultPartition unless PA_DECODE_PARTITION names another
-// multiple of the stage length (read once; a tuning knob like PA_DECODE_CTAS_PER_SM).
-static int default_partition() {
+int named_partition() {
     static const int pt = [] {
         const char* v = std::getenv("PA_DECODE_PARTITION");
         const int x = (v && *v) ? std::atoi(v) : 0;
-        return x > 0 && x % kStageTok == 0 ? x : kDefaultPartition;
+        return x > 0 && x % kStageTok == 0 ? x : 0;
     }();
     return pt;
+}
+
+// Partition length for partition_tokens == 0.
+static int default_partition() {
+    const int pt = named_partition();
+    return pt ? pt : kDefaultPartition;
 }
 
 bool workspace_layout(int N, int H_q, int H_kv, int D, int max_ctx, int partition_tokens, WorkspaceLayout* L) {

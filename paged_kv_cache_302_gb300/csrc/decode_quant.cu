@@ -665,6 +665,7 @@ pa_status quant_tensor_map(CUtensorMap* m, const void* qpool, int NB, int H_kv, 
 // partitions of 512 and takes 11 in partitions of 64.  (Lengths that would fill the last round over the warps made no
 // difference to larger batches: 8 sequences of 32768 tokens took 96 us with 512, 97 with 576, 95 with 768.)
 int quant_partition(int N, int H_kv, int max_ctx) {
+    if (const int pt = named_partition()) return pt;
     constexpr long kWarps = 152 * kQCtasPerSm;
     const long tokens = (long)N * H_kv * max_ctx;
     const long pt = ((tokens + kWarps - 1) / kWarps + kStageTok - 1) / kStageTok * kStageTok;

@@ -107,6 +107,10 @@ struct WorkspaceLayout {
 // Returns false for invalid arguments.
 bool workspace_layout(int N, int H_q, int H_kv, int D, int max_ctx, int partition_tokens, WorkspaceLayout* out);
 
+// Partition length that PA_DECODE_PARTITION names for the calls that pass partition_tokens == 0, a positive multiple of
+// the stage length (read once; a tuning knob like PA_DECODE_CTAS_PER_SM); 0 when it names none.
+int named_partition();
+
 // Partition length pa_decode_quant takes for partition_tokens == 0.
 int quant_partition(int N, int H_kv, int max_ctx);
 

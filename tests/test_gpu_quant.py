@@ -1,6 +1,9 @@
 """The quantised cache on the GPU: the quantising write and the read bit for bit, decode attention element by element
 against a 64-bit form, with poisoned memory wherever a call has no business."""
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -559,3 +562,28 @@ def test_a_workspace_made_by_a_call_on_another_stream_stays_with_that_stream(cal
     torch.cuda.synchronize()
     assert torch.equal(out, ref)
     assert all(t.data_ptr() + size <= at or at + size <= t.data_ptr() for t in later)
+
+
+_NAMED = """
+import torch
+import paged_kv_cache_302_gb300 as pa
+g = torch.Generator(device="cuda").manual_seed(1)
+NB, H, B, D, ctx = 70, 2, 16, 128, 1100
+qp = torch.empty(NB, H, 2, B, D, dtype=torch.uint8, device="cuda")
+sc = torch.empty(NB, H, 2, B, dtype=torch.uint8, device="cuda")
+k, v = (torch.randn(NB * B, H, D, generator=g, device="cuda").bfloat16() for _ in range(2))
+pa.pa_reshape_and_cache_quant(k, v, qp, sc, torch.arange(NB * B, device="cuda"))
+q = torch.randn(1, 8, D, generator=g, device="cuda").bfloat16()
+tab, n = torch.arange(NB, dtype=torch.int32, device="cuda")[None], torch.tensor([ctx], dtype=torch.int32).cuda()
+outs = {pt: pa.pa_decode_quant(torch.empty(1, 8, D, device="cuda"), q, qp, sc, tab, n, ctx, partition_tokens=pt)
+        for pt in (0, 64, 160)}
+assert torch.equal(outs[0], outs[160]), "the named length"
+assert not torch.equal(outs[0], outs[64])         # sums joined at other places: the lengths can be told apart
+"""
+
+
+def test_decode_takes_the_named_partition_length():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", _NAMED], env={**os.environ, "PA_DECODE_PARTITION": "160"}, cwd=root,
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr

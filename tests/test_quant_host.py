@@ -1,5 +1,9 @@
 """Refusals of the quantised cache's and the tree attention's calls, without a GPU: placeholder addresses are never
 dereferenced, because validation fails first."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -184,3 +188,24 @@ def test_a_workspace_made_by_a_call_belongs_to_the_calls_stream(monkeypatch):
     assert pa._workspace(mine, 64, "cpu", Stream()) is mine and seen == []
     assert pa._workspace(None, 64, "cpu", Stream()).numel() == 64 and seen == [0x77]
     assert pa._workspace(None, 64, "cpu", None).numel() == 64 and seen == [0x77, None]
+
+
+_NAMED = """
+import paged_kv_cache_302_gb300 as pa
+L, size = pa.load(), pa.pa_decode_workspace_bytes
+for shape in ((1, 32, 8, 128, 1000), (1, 32, 8, 128, 20000), (256, 32, 8, 128, 16384), (8, 56, 8, 128, 32768)):
+    assert size(*shape) == size(*shape, 4096), shape
+assert size(256, 32, 8, 128, 16384) < pa.PA_STATIC_WORKSPACE_BYTES < size(256, 32, 8, 128, 16384, 512)
+st = L.pa_decode_no_alloc(*([0x1000, pa.PA_BF16] + [0x1000] * 4 + [256, 32, 8, 128, 16, 1024, 4096, 16384, 0.1, 0,
+                                                                  pa.PA_BF16, None, None, None]))
+assert st == pa.PA_ERR_CUDA, pa.last_error()      # past the check of sizes, to the device that is not there
+"""
+
+
+def test_a_named_partition_length_holds_for_the_sizes_of_every_decode():
+    """PA_DECODE_PARTITION sets what partition_tokens = 0 stands for: the workspace is that length's, and batches that fit
+    the built-in workspace with it are served."""
+    env = {**os.environ, "PA_DECODE_PARTITION": "4096", "CUDA_VISIBLE_DEVICES": ""}
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", _NAMED], env=env, cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
