@@ -587,3 +587,26 @@ def test_decode_takes_the_named_partition_length():
     r = subprocess.run([sys.executable, "-c", _NAMED], env={**os.environ, "PA_DECODE_PARTITION": "160"}, cwd=root,
                        capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr
+
+
+@pytest.mark.skipif("PA_DECODE_PARTITION" in os.environ, reason="a named length holds whatever the workspace")
+def test_decode_takes_the_longest_partitions_where_the_workspace_holds_no_others():
+    """partition_tokens = 0 with a workspace from the least size on: the short partitions of a small batch where they
+    fit, else those of 512 tokens, and nothing behind the workspace written; below the least size a refusal."""
+    c = Cache(75, [2100, 600, 5, 513], 2, 128, 16, "f16")
+    q = torch.randn(4, 8, 128, generator=torch.Generator().manual_seed(8)).half().cuda()
+    args = (q, c.qp, c.sc, c.dtab, c.dctx, 2100)
+    least, room = (pa.pa_decode_workspace_bytes(4, 8, 2, 128, 2100, pt) for pt in (512, 0))
+    assert room == pa.pa_decode_workspace_bytes(4, 8, 2, 128, 2100, 64) > least
+    long, short, out = (torch.empty(4, 8, 128, device="cuda") for _ in range(3))
+    pa.pa_decode_quant(long, *args, partition_tokens=512)
+    pa.pa_decode_quant(short, *args, partition_tokens=64)
+    assert not torch.equal(long, short)              # sums joined at other places: the lengths can be told apart
+    base = torch.empty(room + 256, dtype=torch.uint8, device="cuda")
+    for size, want in ((least, long), (least + 16, long), (room - 1, long), (room, short), (room + 64, short)):
+        base.fill_(0xA5)
+        out.zero_()
+        pa.pa_decode_quant(out, *args, workspace=base[:size])
+        assert torch.equal(out, want) and (base[size:] == 0xA5).all()
+    with pytest.raises(pa.PAError, match="too small"):
+        pa.pa_decode_quant(out, *args, workspace=base[: least - 1])
