@@ -240,6 +240,18 @@ struct Mma<__half> {
     }
 };
 
+// Lane-wise unsigned maximum and minimum of two 16-bit pairs (PTX max.u16x2, min.u16x2).
+__device__ __forceinline__ uint32_t vmax_u16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t vmin_u16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("min.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
 // 2^x by the hardware approximation (PTX ex2.approx.ftz.f32); 2^-inf = +0.
 __device__ __forceinline__ float fast_exp2(float x) {
     float y;

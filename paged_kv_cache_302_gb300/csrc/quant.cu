@@ -19,12 +19,6 @@ namespace pa {
 constexpr int kQuantThreads = 256;
 constexpr int kQuantCtasPerSm = 8;
 
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
-
 template <typename T, int D>
 __global__ void __launch_bounds__(kQuantThreads, kQuantCtasPerSm)
     quant_cache_kernel(const T* __restrict__ k, const T* __restrict__ v, uint8_t* __restrict__ qpool,
@@ -60,9 +54,9 @@ __global__ void __launch_bounds__(kQuantThreads, kQuantCtasPerSm)
         const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
         uint32_t m = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) m = max_u16x2(m, w[j] & 0x7fff7fffu);
+        for (int j = 0; j < 8; ++j) m = vmax_u16x2(m, w[j] & 0x7fff7fffu);
 #pragma unroll
-        for (int o = L / 2; o > 0; o >>= 1) m = max_u16x2(m, __shfl_xor_sync(mask, m, o));
+        for (int o = L / 2; o > 0; o >>= 1) m = vmax_u16x2(m, __shfl_xor_sync(mask, m, o));
         m = max(m & 0xffffu, m >> 16);
         if (m > kInf) {  // a NaN, which counts as nothing
             m = 0;

@@ -110,11 +110,6 @@ __device__ __forceinline__ bool mbar_wait_spin(uint32_t bar, uint32_t parity, vo
     }
 }
 
-__device__ __forceinline__ uint32_t vmin_u16x2(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("min.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
 // A scale byte held to the range the writer produces.
 __device__ __forceinline__ int clamp_scale(uint32_t b) { return scale_of((int)b) + kScaleBias; }
 
