@@ -146,7 +146,9 @@ pa_status pa_update_block_tables(int32_t* tables, int N, int MB, const int32_t* 
  * PA_DECODE_PARTITION names, where it names one), -1 = one partition per
  * sequence, > 0 = split each context into partitions of that many tokens (a
  * multiple of 32).  max_ctx bounds every context length of the calls that use
- * the workspace.  Returns 0 for invalid arguments.
+ * the workspace.  The room for pa_decode_quant's shorter partitions is at most
+ * 9 MB beyond what the calls need (H_q / H_kv <= 8); a workspace without it
+ * still serves every call.  Returns 0 for invalid arguments.
  * ---------------------------------------------------------------------- */
 size_t pa_decode_workspace_bytes(int N, int H_q, int H_kv, int D, int max_ctx, int partition_tokens);
 
@@ -302,6 +304,9 @@ pa_status pa_decode_quant(void* out, pa_dtype out_dtype, const void* q, pa_dtype
  * sequence's other rows.  The draft's own K/V must already be in the pool
  * (forking the sequence before the draft and freeing the fork afterwards takes
  * it out again).
+ * A 16-bit out over an fp16 or a quantised pool is summed from probabilities
+ * rounded to fp16 (off by at most 2^-11 of themselves); an F32 out, and any out
+ * over a bf16 pool, from probabilities in two 16-bit parts.
  * q, out: [T][H_q][D] (out F32 or q_dtype); q_start: [N+1] int32, not
  * decreasing, q_start[N] <= T (rows of out past q_start[N] are not written);
  * tree_mask: [T][mask_words] int32 words, max_q_len <= 32 * mask_words;

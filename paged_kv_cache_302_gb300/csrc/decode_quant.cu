@@ -13,8 +13,8 @@
 // |ev| <= 40 keeps p 2^-ev and l within fp32.  K8 and V8 become fp16 in registers (exact: cvt e4m3x2 -> f16x2).
 //
 // Bound by memory: 2 D + 2 bytes per token and KV head.  256 sequences of ~1500 tokens with 8 KV heads, D = 128 (811
-// MB): 127 us, 6.4 TB/s; 64 of ~1000 with 40 KV heads (758 MB): 116 us, 6.5 TB/s; 8 of 32768 with 7 query heads to a KV
-// head (541 MB): 92 us, 5.9 TB/s.  One sequence of 1000 tokens: 11 us, the latency of three kernels.
+// MB): 132 us, 6.1 TB/s; 64 of ~1000 with 40 KV heads (758 MB): 115 us, 6.6 TB/s; 8 of 32768 with 7 query heads to a KV
+// head (541 MB): 95 us, 5.7 TB/s.  One sequence of 1000 tokens: 11 us, the latency of three kernels.
 #include <algorithm>
 #include <type_traits>
 
@@ -659,8 +659,9 @@ pa_status quant_tensor_map(CUtensorMap* m, const void* qpool, int NB, int H_kv, 
                              D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
-// The consumer warps resident on the GPU (kQCtasPerSm on each of its 152 SMs) each take a record at a time, in about
-// 1 us per 32 tokens.  A batch with fewer whole default partitions than warps is cut finer, down to 64 tokens (two
+// The consumer warps resident on a GB300 (kQCtasPerSm on each of its 152 SMs; the length may not depend on the device at
+// hand, for a workspace is sized by it) each take a record at a time, in about 1 us per 32 tokens.  Where no length is
+// named, a batch with fewer whole default partitions than warps is cut finer, down to 64 tokens (two
 // stages; shorter ones leave the merge more than they save): one sequence of 1000 tokens and 8 KV heads took 28 us in
 // partitions of 512 and takes 11 in partitions of 64.  (Lengths that would fill the last round over the warps made no
 // difference to larger batches: 8 sequences of 32768 tokens took 96 us with 512, 97 with 576, 95 with 768.)

@@ -30,7 +30,7 @@
 // What bounds it, measured at D = 128.  64 sequences with trees of up to 24 tokens, 32 / 8 heads, bf16: 90 us, 4.8 TB/s
 // of K and V.  The bytes alone are 64 us; inside a run a tile takes about 2700 cycles, 64 KB at 7 TB/s over the GPU,
 // and the rest is the launch, the first tiles and the ends of 512 units.  16 trees of up to 63 tokens over 4500
-// quantised tokens each: 110 us, about 2800 cycles per tile of 128 x 128, bound by the roles' own instructions and
+// quantised tokens each: 111 us, about 2800 cycles per tile of 128 x 128, bound by the roles' own instructions and
 // waits (the SM issues 2.1 of 4 instructions a cycle, the tensor pipe is 28 % busy, memory 20 %).  Of 117 us with all
 // in place, a copy without the conversion to fp16 took 88, without exponentials 113, without both products 109, without
 // all three 83.  What the time was spent on before: one group of converters (114 us), one score buffer (128), masked
