@@ -610,3 +610,31 @@ def test_decode_takes_the_longest_partitions_where_the_workspace_holds_no_others
         assert torch.equal(out, want) and (base[size:] == 0xA5).all()
     with pytest.raises(pa.PAError, match="too small"):
         pa.pa_decode_quant(out, *args, workspace=base[: least - 1])
+
+
+@pytest.mark.parametrize("call", ["decode_quant", "tree"])
+def test_calls_without_a_workspace_captured_on_a_forked_stream(call):
+    """A graph whose call runs on a stream forked from the captured one, with the library's own workspace: replays give
+    the eager call's bits, whatever the program allocates and writes in between."""
+    c = Cache(76, [2100, 600], 2, 128, 16, "bf16")
+    q = torch.randn(2, 8, 128, generator=torch.Generator().manual_seed(9)).bfloat16().cuda()
+    qs, mask = torch.arange(3, dtype=torch.int32).cuda(), torch.ones(2, 1, dtype=torch.int32).cuda()
+
+    def run(out, **kw):
+        if call == "decode_quant":
+            return pa.pa_decode_quant(out, q, c.qp, c.sc, c.dtab, c.dctx, 2100, **kw)
+        return pa.pa_decode_tree(out, q, c.qp, c.dtab, c.dctx, qs, mask, 1, scales=c.sc, **kw)
+
+    ref = run(torch.empty(2, 8, 128, device="cuda"))
+    out = torch.zeros_like(ref)
+    main, side, graph = torch.cuda.Stream(), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    main.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=main):
+        side.wait_stream(main)
+        run(out, stream=side)
+        main.wait_stream(side)
+    for _ in range(3):
+        torch.full((64 << 20,), 0xA5, dtype=torch.uint8, device="cuda")
+        out.zero_()
+        graph.replay()
+        assert torch.equal(out, ref)
