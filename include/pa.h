@@ -302,8 +302,8 @@ pa_status pa_decode_quant(void* out, pa_dtype out_dtype, const void* q, pa_dtype
  * sequence sees (padding), and slots past the context, may hold anything, NaN
  * included; a non-finite V of a drafted token that some rows see can reach the
  * sequence's other rows.  The draft's own K/V must already be in the pool
- * (forking the sequence before the draft and freeing the fork afterwards takes
- * it out again).
+ * (pa_compact_tokens moves the accepted ones together afterwards, and
+ * pa_alloc_compact_batch takes the others out).
  * A 16-bit out over an fp16 or a quantised pool is summed from probabilities
  * rounded to fp16 (off by at most 2^-11 of themselves); an F32 out, and any out
  * over a bf16 pool, from probabilities in two 16-bit parts.
@@ -327,6 +327,104 @@ pa_status pa_decode_tree(void* out, pa_dtype out_dtype, const void* q, pa_dtype 
                          const int32_t* q_start, const int32_t* tree_mask, int mask_words, int N, int T, int H_q,
                          int H_kv, int D, int B, int MB, int NB, int max_q_len, float scale, void* workspace,
                          size_t ws_bytes, int* dev_err, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Block-sparse decode: attention over a few blocks of a long context.  Three
+ * calls: key summaries kept beside the cache, the selection of blocks by them,
+ * and the attention over the selected blocks.  All three take a 16-bit pool or
+ * a quantised cache, D in {64, 128}, B in {8, 16, 32}, NB*B and MB*B < 2^31,
+ * N <= 65535, and the last two 1 <= H_q / H_kv <= 8.
+ *
+ * A key summary is a box around the keys of one (block, KV head):
+ *   summaries:  [NB][H_kv][2][D] int8, channel d's least (index 0) and greatest
+ *               (index 1) K over the block's tokens;
+ *   sum_scales: [NB][H_kv] bytes, b standing for 2^(b - 127), 2^e below:
+ * e is the least in [-40, 40] with max |K| <= 127 * 2^e (-40 for keys that are
+ * all zeros), least = floor(min K * 2^-e), greatest = ceil(max K * 2^-e), both
+ * saturating at +-127 (magnitudes above 127 * 2^40, infinities).  A NaN counts as
+ * nothing; a channel that holds only NaN is the box [0, 0].
+ *
+ * pa_summarize_blocks rebuilds, from the pool, the summaries of the blocks that
+ * hold each sequence's newest tokens: after a cache write, or after
+ * pa_compact_tokens.  Sequence s holds ctx_lens[s] tokens, the newest n_s =
+ * q_start[s+1] - q_start[s] of them since its summaries were last rebuilt; the
+ * blocks that these lie in are summarised over all tokens that they hold (at
+ * most up to the context's end: what lies behind may be anything).  q_start:
+ * [N+1] int32, or NULL: n_s = ctx_lens[s].  n_s = 0 is allowed.  A sequence with
+ * n_s outside [0, max_q_len], or a context below n_s or above MB*B, is flagged
+ * PA_DEV_ERR_CTX and left out; a block-table entry outside [0, NB) is flagged
+ * PA_DEV_ERR_BLOCK and skipped.  A block that several sequences share has to
+ * hold as many tokens in each.  pool, scales, kv_dtype: as pa_decode_tree.
+ * max_q_len == 0 is a no-op.
+ *
+ * pa_select_blocks lists top_k blocks for each (sequence, KV head).  Block b's
+ * score is the largest product that its box allows with a query head of the KV
+ * head's group:
+ *     score_b = max_h 2^(e + f_h) * sum_d max(i_hd * least_d, i_hd * greatest_d),
+ * i_hd = q_hd * 2^-f_h rounded to the nearest integer (ties to even, saturating at
+ * +-511, NaN to 0), f_h the least in [-40, 40] with max_d |q_hd| <= 511 * 2^f_h
+ * (-40 for a row of zeros).  The sum is exact, so the selection does not depend
+ * on the order in which the GPU adds.  A context of nb = ceil(ctx / B) blocks
+ * keeps its first sink_blocks, its last recent_blocks and the best others, ties
+ * to the lower block, top_k in all (all nb where nb <= top_k):
+ *   selected: [N][H_kv][top_k] int32, logical blocks ascending, then -1.
+ * A block whose block-table entry is outside [0, NB) is flagged PA_DEV_ERR_BLOCK
+ * and ranks last; a context below 1, above max_ctx or above MB*B is flagged
+ * PA_DEV_ERR_CTX and its lists are all -1.  0 <= sink_blocks, recent_blocks,
+ * their sum <= top_k.  workspace: ws_bytes >= pa_select_workspace_bytes(...) of
+ * device memory, contents need not be initialised, not shared by calls that
+ * overlap on the GPU.
+ *
+ * pa_decode_sparse is pa_decode over the listed blocks: t runs over the tokens
+ * below ctx_lens[s] of the blocks selected[s][h / (H_q / H_kv)][0 .. top_k-1].
+ * Negative entries are skipped, in any place; an entry at or past ceil(ctx / B),
+ * or whose block-table entry is outside [0, NB), is skipped and flagged
+ * PA_DEV_ERR_BLOCK; a block listed twice counts twice.  A list without a block
+ * gives a row of zeros.  Slots past the context may hold anything, NaN included.
+ * A context below 1 or above MB*B is flagged PA_DEV_ERR_CTX and its rows are not
+ * written.  q, out: [N][H_q][D], out F32 or q_dtype, in device memory or pinned
+ * host memory; pool, scales, kv_dtype: as pa_decode_tree; workspace as above, of
+ * pa_decode_sparse_workspace_bytes(...).  scale > 0 and finite.  Results do not
+ * depend on the order in which the GPU runs the call's parts.
+ * ---------------------------------------------------------------------- */
+pa_status pa_summarize_blocks(void* summaries, void* sum_scales, const void* pool, const void* scales,
+                              pa_dtype kv_dtype, const int32_t* block_tables, const int32_t* ctx_lens,
+                              const int32_t* q_start, int N, int H_kv, int D, int B, int MB, int NB, int max_q_len,
+                              int* dev_err, void* stream);
+size_t pa_select_workspace_bytes(int N, int H_kv, int max_ctx, int B);
+pa_status pa_select_blocks(int32_t* selected, const void* q, pa_dtype q_dtype, const void* summaries,
+                           const void* sum_scales, const int32_t* block_tables, const int32_t* ctx_lens, int N, int H_q,
+                           int H_kv, int D, int B, int MB, int NB, int max_ctx, int top_k, int sink_blocks,
+                           int recent_blocks, void* workspace, size_t ws_bytes, int* dev_err, void* stream);
+size_t pa_decode_sparse_workspace_bytes(int N, int H_q, int H_kv, int D, int B, int top_k);
+pa_status pa_decode_sparse(void* out, pa_dtype out_dtype, const void* q, pa_dtype q_dtype, const void* pool,
+                           const void* scales, pa_dtype kv_dtype, const int32_t* block_tables, const int32_t* ctx_lens,
+                           const int32_t* selected, int top_k, int N, int H_q, int H_kv, int D, int B, int MB, int NB,
+                           float scale, void* workspace, size_t ws_bytes, int* dev_err, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Compaction: the kept tokens of a sequence moved together, in place (the
+ * accepted tokens of a drafted tree, what an eviction leaves of a context).
+ * Sequence s holds ctx_lens[s] tokens; those before base[s] stay, and of the
+ * others the n_s = keep_start[s+1] - keep_start[s] at the positions keep[
+ * keep_start[s] .. keep_start[s+1]-1] are kept: the j-th moves, K and V bit for
+ * bit, to position base[s] + j.  The new context is base[s] + n_s; tokens past it
+ * are undefined.  keep: [T] int32, each sequence's positions ascending from
+ * base[s] on, all below ctx_lens[s]; keep_start: [N+1] int32, not decreasing,
+ * within [0, T]; base: [N] int32.
+ * From its first position that is out of order or out of range on, a list is
+ * not followed; that, keep_start or base out of range and a context outside [0,
+ * MB*B] are flagged PA_DEV_ERR_CTX.  A token whose block-table entry, old or new,
+ * is outside [0, NB) is not moved and flagged PA_DEV_ERR_BLOCK.  A block that is
+ * written has to belong to one sequence alone (pa_alloc_compact_batch sees to
+ * that).  Key summaries of blocks from base[s] / B on have to be rebuilt
+ * (pa_summarize_blocks with the new contexts and chunks of n_s).
+ * pool, scales, kv_dtype, sizes: as pa_summarize_blocks.  T == 0 is a no-op.
+ * ---------------------------------------------------------------------- */
+pa_status pa_compact_tokens(void* pool, void* scales, pa_dtype kv_dtype, const int32_t* block_tables,
+                            const int32_t* ctx_lens, const int32_t* base, const int32_t* keep,
+                            const int32_t* keep_start, int N, int T, int H_kv, int D, int B, int MB, int NB,
+                            int* dev_err, void* stream);
 
 /* ------------------------------------------------------------------------
  * pa_decode without a caller-provided workspace.  The pages have no
@@ -450,6 +548,22 @@ pa_status pa_alloc_append_slots(void* alloc, int seq_id, int n, int64_t* slots_o
 pa_status pa_alloc_append_batch(void* alloc, int n_seqs, const int32_t* seq_ids, const int32_t* n_tokens,
                                 int64_t* slots_out, int64_t* cow_pairs_out, int cow_cap, int* n_cow,
                                 int32_t* table_updates_out, int upd_cap, int* n_upd);
+/* Shorten n_seqs distinct sequences to new_lens[i] tokens, the ones from
+ * position base[i] on to be rewritten by pa_compact_tokens (0 <= base[i] <=
+ * new_lens[i] <= the length; base == new_lens drops tokens from the end and
+ * rewrites nothing).  A block that is rewritten and shared is first replaced by
+ * a free one: (old, new) is emitted as a copy pair and the replacement as a table
+ * update, as pa_alloc_append_batch does.  Blocks past the new length lose their
+ * reference, in sequence order, each sequence's in logical order, after every
+ * replacement has been taken; they hold their tokens until a later call hands
+ * them out.  So on the device: the copies, the table updates, then
+ * pa_compact_tokens with the old lengths (the tables' entries past the new ones
+ * are still needed), then whatever writes to blocks allotted later.
+ * table_updates_out (nullable): [upd_cap][3].  The counts may exceed neither
+ * capacity (PA_ERR_INVALID). */
+pa_status pa_alloc_compact_batch(void* alloc, int n_seqs, const int32_t* seq_ids, const int32_t* base,
+                                 const int32_t* new_lens, int64_t* cow_pairs_out, int cow_cap, int* n_cow,
+                                 int32_t* table_updates_out, int upd_cap, int* n_upd);
 pa_status pa_alloc_fork(void* alloc, int parent, int child);          /* child shares all parent blocks */
 pa_status pa_alloc_free_seq(void* alloc, int seq_id);                 /* drop references, recycle blocks */
 pa_status pa_alloc_block_table(void* alloc, int seq_id, int32_t* out, int cap, int* n);

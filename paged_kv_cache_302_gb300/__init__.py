@@ -10,7 +10,8 @@ Layouts (see include/pa.h): pool [NB, B, 2, H_kv, D]; k, v [T, H_kv, D];
 q, out [N, H_q, D]; block_tables [N, MB] int32; ctx_lens [N] int32;
 slot_mapping [T] int64; copy pairs [n, 2] int64.  A quantised cache is two
 tensors: qpool [NB, H_kv, 2, B, D] (float8_e4m3fn or uint8) and scales
-[NB, H_kv, 2, B] (uint8 or float8_e8m0fnu, byte b = 2^(b - 127)).
+[NB, H_kv, 2, B] (uint8 or float8_e8m0fnu, byte b = 2^(b - 127)).  Key summaries
+for block-sparse decode: summaries [NB, H_kv, 2, D] int8, sum_scales [NB, H_kv].
 """
 from __future__ import annotations
 
@@ -106,6 +107,15 @@ def _declare(L):
         "pa_decode_tree": ([P, i32, P, i32, P, P, i32, P, P, P, P, i32, i32, i32, i32, i32, i32, i32, i32, i32, i32,
                             f32, P, sz, P, P], i32),
         "pa_prefill_workspace_bytes": ([i32, i32, i32, i32, i32], sz),
+        "pa_summarize_blocks": ([P, P, P, P, i32, P, P, P, i32, i32, i32, i32, i32, i32, i32, P, P], i32),
+        "pa_select_workspace_bytes": ([i32, i32, i32, i32], sz),
+        "pa_select_blocks": ([P, P, i32, P, P, P, P, i32, i32, i32, i32, i32, i32, i32, i32, i32, i32, i32, P, sz, P,
+                              P], i32),
+        "pa_decode_sparse_workspace_bytes": ([i32, i32, i32, i32, i32, i32], sz),
+        "pa_decode_sparse": ([P, i32, P, i32, P, P, i32, P, P, P, i32, i32, i32, i32, i32, i32, i32, i32, f32, P, sz, P,
+                              P], i32),
+        "pa_compact_tokens": ([P, P, i32, P, P, P, P, P, i32, i32, i32, i32, i32, i32, i32, P, P], i32),
+        "pa_alloc_compact_batch": ([P, i32, P, P, P, P, i32, P, P, i32, P], i32),
         "pa_alloc_fork": ([P, i32, i32], i32),
         "pa_alloc_free_seq": ([P, i32], i32),
         "pa_alloc_block_table": ([P, i32, P, i32, P], i32),
@@ -246,6 +256,16 @@ def _decode_bytes(*shape):
 @functools.lru_cache(maxsize=256)
 def _tree_bytes(*shape):
     return pa_decode_tree_workspace_bytes(*shape)
+
+
+@functools.lru_cache(maxsize=256)
+def _select_bytes(*shape):
+    return pa_select_workspace_bytes(*shape)
+
+
+@functools.lru_cache(maxsize=256)
+def _sparse_bytes(*shape):
+    return pa_decode_sparse_workspace_bytes(*shape)
 
 
 def _dev(t: torch.Tensor, name: str, dtype=None):
@@ -581,6 +601,138 @@ def pa_decode_tree(out, q, pool, block_tables, ctx_lens, q_start, tree_mask, max
     return out
 
 
+def _cache_shape(pool, scales):
+    """(NB, H_kv, B, D, dtype code) of a 16-bit pool, or of a quantised cache's qpool with its scales."""
+    if scales is not None:
+        return _quant_cache(pool, scales) + (PA_E4M3,)
+    shape = pool.shape
+    if len(shape) != 5 or shape[2] != 2 or pool.dtype not in (torch.float16, torch.bfloat16):
+        raise PAError(PA_ERR_INVALID, "without scales the pool must be [NB, B, 2, H_kv, D] fp16 or bf16")
+    return shape[0], shape[3], shape[1], shape[4], _code(pool.dtype)
+
+
+def _summary_shape(summaries, sum_scales):
+    """(NB, H_kv, D) of key summaries, after checking that the two tensors are one."""
+    shape = summaries.shape
+    if summaries.dtype is not torch.int8 or sum_scales.dtype not in _SCALE_TYPES:
+        raise PAError(PA_ERR_INVALID, "summaries must be int8, sum_scales uint8 or float8_e8m0fnu")
+    if len(shape) != 4 or shape[2] != 2 or sum_scales.shape != shape[:2]:
+        raise PAError(PA_ERR_INVALID, "summaries must be [NB, H_kv, 2, D] and sum_scales [NB, H_kv]")
+    return shape[0], shape[1], shape[3]
+
+
+def pa_summarize_blocks(summaries, sum_scales, pool, block_tables, ctx_lens, max_q_len, q_start=None, scales=None,
+                        dev_err=None, stream=None):
+    """Rebuild the key summaries (summaries [NB, H_kv, 2, D] int8, sum_scales [NB, H_kv]) of the blocks that hold each
+    sequence's newest tokens: q_start [N+1] int32 gives their numbers as chunks, None means whole contexts.  pool is a
+    16-bit pool [NB, B, 2, H_kv, D], or a quantised cache's qpool with its scales."""
+    NB, H_kv, B, D, code = _cache_shape(pool, scales)
+    if _summary_shape(summaries, sum_scales) != (NB, H_kv, D):
+        raise PAError(PA_ERR_INVALID, "the summaries are not of this cache's blocks, heads and head dim")
+    N = ctx_lens.numel()
+    if block_tables.dim() != 2 or block_tables.shape[0] != N or (q_start is not None and q_start.numel() != N + 1):
+        raise PAError(PA_ERR_INVALID, "block_tables must be [N, MB], ctx_lens [N], q_start [N+1]")
+    dev = _here(pool, "pool")
+    _check((_lib or load()).pa_summarize_blocks(
+        _arg(summaries, "summaries", dev), _arg(sum_scales, "sum_scales", dev), _arg(pool, "pool", dev),
+        _arg(scales, "scales", dev) if scales is not None else None, code,
+        _arg(block_tables, "block_tables", dev, torch.int32), _arg(ctx_lens, "ctx_lens", dev, torch.int32),
+        _arg(q_start, "q_start", dev, torch.int32) if q_start is not None else None, N, H_kv, D, B,
+        block_tables.shape[1], NB, int(max_q_len), _err_arg(dev_err, dev), _stream_arg(stream, dev)))
+
+
+def pa_select_workspace_bytes(N, H_kv, max_ctx, block_size) -> int:
+    n = load().pa_select_workspace_bytes(N, H_kv, max_ctx, block_size)
+    if n == 0:
+        raise PAError(PA_ERR_INVALID, "invalid selection workspace arguments")
+    return int(n)
+
+
+def pa_select_blocks(selected, q, summaries, sum_scales, block_tables, ctx_lens, max_ctx, block_size, sink_blocks=1,
+                     recent_blocks=1, workspace=None, dev_err=None, stream=None):
+    """List the blocks that decode attention should read: selected [N, H_kv, top_k] int32 receives, for each sequence
+    and KV head, its first sink_blocks, its last recent_blocks and those whose key summaries allow the largest product
+    with q [N, H_q, D] (fp16 or bf16), ascending, then -1."""
+    NB, H_kv, D = _summary_shape(summaries, sum_scales)
+    shape = q.shape
+    N = ctx_lens.numel()
+    if len(shape) != 3 or shape[0] != N or shape[2] != D:
+        raise PAError(PA_ERR_INVALID, "q must be [N, H_q, D] of the summaries' head dim")
+    if selected.dim() != 3 or selected.shape[0] != N or selected.shape[1] != H_kv:
+        raise PAError(PA_ERR_INVALID, "selected must be [N, H_kv, top_k] int32")
+    if block_tables.dim() != 2 or block_tables.shape[0] != N:
+        raise PAError(PA_ERR_INVALID, "block_tables must be [N, MB] and ctx_lens [N]")
+    dev = _here(q, "q")
+    max_ctx, block_size = int(max_ctx), int(block_size)
+    ws = workspace
+    if ws is None:
+        ws = _workspace(None, _select_bytes(N, H_kv, max_ctx, block_size), q.device, stream)
+    _check((_lib or load()).pa_select_blocks(
+        _arg(selected, "selected", dev, torch.int32), _arg(q, "q", dev), _code(q.dtype),
+        _arg(summaries, "summaries", dev), _arg(sum_scales, "sum_scales", dev),
+        _arg(block_tables, "block_tables", dev, torch.int32), _arg(ctx_lens, "ctx_lens", dev, torch.int32), N, shape[1],
+        H_kv, D, block_size, block_tables.shape[1], NB, max_ctx, selected.shape[2], int(sink_blocks),
+        int(recent_blocks), _arg(ws, "workspace", dev), ws.nbytes, _err_arg(dev_err, dev), _stream_arg(stream, dev)))
+    return selected
+
+
+def pa_decode_sparse_workspace_bytes(N, H_q, H_kv, D, block_size, top_k) -> int:
+    n = load().pa_decode_sparse_workspace_bytes(N, H_q, H_kv, D, block_size, top_k)
+    if n == 0:
+        raise PAError(PA_ERR_INVALID, "invalid sparse decode workspace arguments")
+    return int(n)
+
+
+def pa_decode_sparse(out, q, pool, block_tables, ctx_lens, selected, scale=None, scales=None, workspace=None,
+                     dev_err=None, stream=None):
+    """Decode attention over the blocks listed in selected [N, H_kv, top_k] int32 (logical blocks, negative entries are
+    skipped) alone: q, out [N, H_q, D], out fp32 or q's dtype, on the device or in pinned host memory.  pool is a 16-bit
+    pool [NB, B, 2, H_kv, D] of q's dtype, or a quantised cache's qpool with its scales."""
+    NB, H_kv, B, D, code = _cache_shape(pool, scales)
+    shape = q.shape
+    N = ctx_lens.numel()
+    if len(shape) != 3 or shape[0] != N or shape[2] != D or out.shape != shape:
+        raise PAError(PA_ERR_INVALID, "q and out must be [N, H_q, D] of the cache's head dim")
+    if scales is None and pool.dtype is not q.dtype:
+        raise PAError(PA_ERR_INVALID, "a 16-bit pool must be of q's dtype")
+    if selected.dim() != 3 or selected.shape[0] != N or selected.shape[1] != H_kv:
+        raise PAError(PA_ERR_INVALID, "selected must be [N, H_kv, top_k] int32")
+    if block_tables.dim() != 2 or block_tables.shape[0] != N:
+        raise PAError(PA_ERR_INVALID, "block_tables must be [N, MB] and ctx_lens [N]")
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    dev = _here(q, "q")
+    H_q, top_k = shape[1], selected.shape[2]
+    ws = workspace
+    if ws is None:
+        ws = _workspace(None, _sparse_bytes(N, H_q, H_kv, D, B, top_k), q.device, stream)
+    _check((_lib or load()).pa_decode_sparse(
+        _out_arg(out, "out", dev), _code(out.dtype), _arg(q, "q", dev), _code(q.dtype), _arg(pool, "pool", dev),
+        _arg(scales, "scales", dev) if scales is not None else None, code,
+        _arg(block_tables, "block_tables", dev, torch.int32), _arg(ctx_lens, "ctx_lens", dev, torch.int32),
+        _arg(selected, "selected", dev, torch.int32), top_k, N, H_q, H_kv, D, B, block_tables.shape[1], NB, scale,
+        _arg(ws, "workspace", dev), ws.nbytes, _err_arg(dev_err, dev), _stream_arg(stream, dev)))
+    return out
+
+
+def pa_compact_tokens(pool, block_tables, ctx_lens, base, keep, keep_start, scales=None, dev_err=None, stream=None):
+    """Move the kept tokens of each sequence together, in place: of the tokens from position base[s] on, those at the
+    ascending positions keep[keep_start[s]:keep_start[s+1]] go to base[s], base[s] + 1, ... (keep [T], keep_start [N+1],
+    base [N], ctx_lens [N] the lengths before the move; all int32).  pool is a 16-bit pool [NB, B, 2, H_kv, D], or a
+    quantised cache's qpool with its scales."""
+    NB, H_kv, B, D, code = _cache_shape(pool, scales)
+    N = ctx_lens.numel()
+    if block_tables.dim() != 2 or block_tables.shape[0] != N or base.numel() != N or keep_start.numel() != N + 1:
+        raise PAError(PA_ERR_INVALID, "block_tables must be [N, MB], ctx_lens and base [N], keep_start [N+1]")
+    dev = _here(pool, "pool")
+    T = keep.numel()
+    _check((_lib or load()).pa_compact_tokens(
+        _arg(pool, "pool", dev), _arg(scales, "scales", dev) if scales is not None else None, code,
+        _arg(block_tables, "block_tables", dev, torch.int32), _arg(ctx_lens, "ctx_lens", dev, torch.int32),
+        _arg(base, "base", dev, torch.int32), _arg(keep, "keep", dev, torch.int32) if T else None,
+        _arg(keep_start, "keep_start", dev, torch.int32), N, T, H_kv, D, B, block_tables.shape[1], NB,
+        _err_arg(dev_err, dev), _stream_arg(stream, dev)))
+
+
 def pa_write_contiguous(k, v, k_ptr, v_ptr, req_ids, positions, N_max, S_max, dev_err=None, stream=None):
     """Write k, v [T, H_kv, D] into contiguous buffers (device pointers or tensors [N_max, S_max, H_kv, D])."""
     T, H_kv, D = k.shape
@@ -752,6 +904,25 @@ class BlockAllocator:
                                              _i32p(upd) if upd is not None else None, cap, ctypes.byref(nupd)))
         res = (slots[:total], pairs[: 2 * ncow.value].reshape(-1, 2))
         return res + (upd[: nupd.value],) if table_updates else res
+
+    def compact_batch(self, seq_ids, base, new_lens, table_updates: bool = False):
+        """Shorten seq_ids[i] to new_lens[i] tokens, those from base[i] on to be rewritten by pa_compact_tokens; returns
+        the cow_pairs and, with table_updates=True, also the [k, 3] int32 (row, logical block, physical block)
+        updates."""
+        import numpy as np
+        ids, b, nl = (np.ascontiguousarray(x, dtype=np.int32) for x in (seq_ids, base, new_lens))
+        if ids.ndim != 1 or b.shape != ids.shape or nl.shape != ids.shape:
+            raise PAError(PA_ERR_INVALID, "seq_ids, base and new_lens must have one entry per sequence")
+        # at most every block that a rewritten token can lie in
+        cap = min(int(np.maximum(0, (nl - 1) // self.B - b // self.B + 1).sum()), self.NB) + 1
+        pairs = np.zeros(2 * cap, dtype=np.int64)
+        upd = np.empty((cap, 3), dtype=np.int32) if table_updates else None
+        ncow, nupd = ctypes.c_int(0), ctypes.c_int(0)
+        _check(self._L.pa_alloc_compact_batch(self._h, len(ids), _i32p(ids), _i32p(b), _i32p(nl), _i32p(pairs), cap,
+                                              ctypes.byref(ncow), _i32p(upd) if upd is not None else None, cap,
+                                              ctypes.byref(nupd)))
+        cow = pairs[: 2 * ncow.value].reshape(-1, 2)
+        return (cow, upd[: nupd.value]) if table_updates else cow
 
     def fork(self, parent: int, child: int):
         _check(self._L.pa_alloc_fork(self._h, int(parent), int(child)))

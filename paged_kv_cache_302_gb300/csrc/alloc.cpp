@@ -196,6 +196,83 @@ pa_status pa_alloc_append_batch(void* alloc, int n_seqs, const int32_t* seq_ids,
     return PA_OK;
 }
 
+pa_status pa_alloc_compact_batch(void* alloc, int n_seqs, const int32_t* seq_ids, const int32_t* base,
+                                 const int32_t* new_lens, int64_t* cow_pairs_out, int cow_cap, int* n_cow,
+                                 int32_t* table_updates_out, int upd_cap, int* n_upd) {
+    Allocator* A = as_alloc(alloc);
+    if (!A) return fail(PA_ERR_INVALID, "null allocator");
+    if (n_seqs < 0) return fail(PA_ERR_INVALID, "negative n_seqs");
+    if (n_seqs > 0 && (!seq_ids || !base || !new_lens)) return fail(PA_ERR_INVALID, "null argument");
+    // everything that allocates comes before the first change
+    try {
+        std::unordered_set<int> seen;
+        std::unordered_map<int32_t, int> ref_delta;
+        std::vector<Seq*> seqs(n_seqs);
+        int64_t copies = 0;
+        for (int i = 0; i < n_seqs; ++i) {
+            auto it = A->seqs.find(seq_ids[i]);
+            if (it == A->seqs.end()) return fail(PA_ERR_INVALID, "unknown sequence %d", seq_ids[i]);
+            if (!seen.insert(seq_ids[i]).second) return fail(PA_ERR_INVALID, "sequence %d repeated", seq_ids[i]);
+            Seq& s = it->second;
+            if (base[i] < 0 || new_lens[i] < base[i] || new_lens[i] > s.ntok)
+                return fail(PA_ERR_INVALID, "sequence %d: base %d and new length %d of %lld tokens", seq_ids[i], base[i],
+                            new_lens[i], (long long)s.ntok);
+            seqs[i] = &s;
+            if (new_lens[i] == base[i]) continue;
+            for (int b = base[i] / A->B; b <= (new_lens[i] - 1) / A->B; ++b)
+                if (A->ref[s.blocks[b]] > 1 && A->ref[s.blocks[b]] + ref_delta[s.blocks[b]] > 1) {
+                    ref_delta[s.blocks[b]] -= 1;
+                    copies += 1;
+                }
+        }
+        if (copies > 0 && (cow_cap < copies || !cow_pairs_out))
+            return fail(PA_ERR_INVALID, "cow_pairs_out holds %d pairs, the batch copies %lld blocks", cow_cap,
+                        (long long)copies);
+        if (copies > 0 && table_updates_out && upd_cap < copies)
+            return fail(PA_ERR_INVALID, "table_updates_out holds %d entries, the batch sets %lld", upd_cap,
+                        (long long)copies);
+        if (copies > (int64_t)A->free_stack.size())
+            return fail(PA_ERR_OOM, "need %lld blocks, %zu free", (long long)copies, A->free_stack.size());
+        A->free_stack.reserve(A->NB);
+        int64_t k = 0;
+        for (int i = 0; i < n_seqs; ++i) {
+            if (new_lens[i] == base[i]) continue;
+            Seq& s = *seqs[i];
+            for (int b = base[i] / A->B; b <= (new_lens[i] - 1) / A->B; ++b) {
+                const int32_t old = s.blocks[b];
+                if (A->ref[old] <= 1) continue;
+                const int32_t fresh = A->free_stack.back();
+                A->free_stack.pop_back();
+                A->ref[fresh] = 1;
+                A->ref[old] -= 1;
+                s.blocks[b] = fresh;
+                cow_pairs_out[2 * k] = old;
+                cow_pairs_out[2 * k + 1] = fresh;
+                if (table_updates_out) {
+                    table_updates_out[3 * k] = i;
+                    table_updates_out[3 * k + 1] = b;
+                    table_updates_out[3 * k + 2] = fresh;
+                }
+                ++k;
+            }
+        }
+        // only now may blocks go back: a replacement must not be one that a compaction still reads
+        for (int i = 0; i < n_seqs; ++i) {
+            Seq& s = *seqs[i];
+            const size_t left = (size_t)((new_lens[i] + (int64_t)A->B - 1) / A->B);
+            for (size_t b = left; b < s.blocks.size(); ++b)
+                if (--A->ref[s.blocks[b]] == 0) A->free_stack.push_back(s.blocks[b]);
+            s.blocks.resize(left);
+            s.ntok = new_lens[i];
+        }
+        if (n_cow) *n_cow = (int)k;
+        if (n_upd) *n_upd = table_updates_out ? (int)k : 0;
+        return PA_OK;
+    } catch (const std::bad_alloc&) {
+        return fail(PA_ERR_OOM, "host allocation failed");
+    }
+}
+
 pa_status pa_alloc_fork(void* alloc, int parent, int child) {
     Allocator* A = as_alloc(alloc);
     if (!A) return fail(PA_ERR_INVALID, "null allocator");

@@ -441,6 +441,200 @@ pa_status pa_decode_tree(void* out, pa_dtype out_dtype, const void* q, pa_dtype 
     return launch_tree(a);
 }
 
+// ----------------------------------------------------------------------------- block-sparse decode, compaction
+
+// Sizes that the calls over a cache of either kind and its block tables share.
+static pa_status check_paged_cache(pa_dtype kv_dtype, const void* pool, const void* scales, int N, int H_kv, int D, int B,
+                                   int MB, int NB) {
+    if (!kv_dtype_ok(kv_dtype) && kv_dtype != PA_E4M3)
+        return fail(PA_ERR_UNSUPPORTED, "kv_dtype must be F16, BF16 or E4M3");
+    if (N <= 0 || N > 65535 || MB <= 0) return fail(PA_ERR_INVALID, "bad sizes");
+    const pa_status st = check_quant_shape(NB, B, H_kv, D);
+    if (st != PA_OK) return st;
+    if ((long long)MB * B >= (1LL << 31)) return fail(PA_ERR_UNSUPPORTED, "MB * B must be < 2^31");
+    if ((kv_dtype == PA_E4M3) != (scales != nullptr))
+        return fail(PA_ERR_INVALID, "an E4M3 pool needs its scales, another pool has none");
+    if (!aligned16(pool) || !aligned16(scales)) return fail(PA_ERR_INVALID, "pool and scales must be 16-byte aligned");
+    return PA_OK;
+}
+
+// Query heads of the calls that share a KV head's work among its group.
+static pa_status check_group(int H_q, int H_kv) {
+    if (H_q <= 0 || H_q % H_kv) return fail(PA_ERR_INVALID, "H_q (%d) must be a multiple of H_kv (%d)", H_q, H_kv);
+    if (H_q / H_kv > kMaxGroup) return fail(PA_ERR_UNSUPPORTED, "H_q / H_kv must be <= %d", kMaxGroup);
+    return PA_OK;
+}
+
+pa_status pa_summarize_blocks(void* summaries, void* sum_scales, const void* pool, const void* scales,
+                              pa_dtype kv_dtype, const int32_t* block_tables, const int32_t* ctx_lens,
+                              const int32_t* q_start, int N, int H_kv, int D, int B, int MB, int NB, int max_q_len,
+                              int* dev_err, void* stream) {
+    const NvtxRange nvtx_range("pa_summarize_blocks");
+    g_msg[0] = 0;
+    const pa_status st = check_paged_cache(kv_dtype, pool, scales, N, H_kv, D, B, MB, NB);
+    if (st != PA_OK) return st;
+    if (max_q_len < 0) return fail(PA_ERR_INVALID, "bad sizes");
+    if (max_q_len == 0) return PA_OK;
+    if (!summaries || !sum_scales || !pool || !block_tables || !ctx_lens)
+        return fail(PA_ERR_INVALID, "null pointer argument");
+    if (!aligned16(summaries) || !aligned16(sum_scales))
+        return fail(PA_ERR_INVALID, "summaries and sum_scales must be 16-byte aligned");
+    SummarizeArgs a;
+    a.summaries = summaries;
+    a.sum_scales = sum_scales;
+    a.pool = pool;
+    a.scales = scales;
+    a.kv_dtype = kv_dtype;
+    a.tables = block_tables;
+    a.ctx_lens = ctx_lens;
+    a.q_start = q_start;
+    a.N = N;
+    a.H_kv = H_kv;
+    a.D = D;
+    a.B = B;
+    a.MB = MB;
+    a.NB = NB;
+    a.max_q_len = max_q_len;
+    a.dev_err = dev_err;
+    a.stream = static_cast<cudaStream_t>(stream);
+    return launch_summarize(a);
+}
+
+size_t pa_select_workspace_bytes(int N, int H_kv, int max_ctx, int B) {
+    return select_workspace_bytes(N, H_kv, max_ctx, B);
+}
+
+pa_status pa_select_blocks(int32_t* selected, const void* q, pa_dtype q_dtype, const void* summaries,
+                           const void* sum_scales, const int32_t* block_tables, const int32_t* ctx_lens, int N, int H_q,
+                           int H_kv, int D, int B, int MB, int NB, int max_ctx, int top_k, int sink_blocks,
+                           int recent_blocks, void* workspace, size_t ws_bytes, int* dev_err, void* stream) {
+    const NvtxRange nvtx_range("pa_select_blocks");
+    g_msg[0] = 0;
+    if (!kv_dtype_ok(q_dtype)) return fail(PA_ERR_UNSUPPORTED, "q_dtype must be F16 or BF16");
+    pa_status st = check_paged_cache(q_dtype, nullptr, nullptr, N, H_kv, D, B, MB, NB);
+    if (st == PA_OK) st = check_group(H_q, H_kv);
+    if (st != PA_OK) return st;
+    if (max_ctx <= 0 || top_k <= 0) return fail(PA_ERR_INVALID, "max_ctx and top_k must be positive");
+    if (sink_blocks < 0 || recent_blocks < 0 || (long long)sink_blocks + recent_blocks > top_k)
+        return fail(PA_ERR_INVALID, "sink_blocks and recent_blocks must not be negative, nor more than top_k together");
+    if (!selected || !q || !summaries || !sum_scales || !block_tables || !ctx_lens || !workspace)
+        return fail(PA_ERR_INVALID, "null pointer argument");
+    if (!aligned16(selected) || !aligned16(q) || !aligned16(summaries) || !aligned16(sum_scales) ||
+        !aligned16(workspace))
+        return fail(PA_ERR_INVALID, "selected, q, summaries, sum_scales and workspace must be 16-byte aligned");
+    const size_t need = select_workspace_bytes(N, H_kv, max_ctx, B);
+    if (ws_bytes < need) return fail(PA_ERR_INVALID, "workspace too small: %zu < %zu bytes", ws_bytes, need);
+    SelectArgs a;
+    a.selected = selected;
+    a.q = q;
+    a.q_dtype = q_dtype;
+    a.summaries = summaries;
+    a.sum_scales = sum_scales;
+    a.tables = block_tables;
+    a.ctx_lens = ctx_lens;
+    a.N = N;
+    a.H_q = H_q;
+    a.H_kv = H_kv;
+    a.D = D;
+    a.B = B;
+    a.MB = MB;
+    a.NB = NB;
+    a.max_ctx = max_ctx;
+    a.top_k = top_k;
+    a.sink = sink_blocks;
+    a.recent = recent_blocks;
+    a.workspace = workspace;
+    a.dev_err = dev_err;
+    a.stream = static_cast<cudaStream_t>(stream);
+    return launch_select(a);
+}
+
+size_t pa_decode_sparse_workspace_bytes(int N, int H_q, int H_kv, int D, int B, int top_k) {
+    return decode_sparse_workspace_bytes(N, H_q, H_kv, D, B, top_k);
+}
+
+pa_status pa_decode_sparse(void* out, pa_dtype out_dtype, const void* q, pa_dtype q_dtype, const void* pool,
+                           const void* scales, pa_dtype kv_dtype, const int32_t* block_tables, const int32_t* ctx_lens,
+                           const int32_t* selected, int top_k, int N, int H_q, int H_kv, int D, int B, int MB, int NB,
+                           float scale, void* workspace, size_t ws_bytes, int* dev_err, void* stream) {
+    const NvtxRange nvtx_range("pa_decode_sparse");
+    g_msg[0] = 0;
+    if (!kv_dtype_ok(q_dtype)) return fail(PA_ERR_UNSUPPORTED, "q_dtype must be F16 or BF16");
+    if (kv_dtype != PA_E4M3 && kv_dtype != q_dtype)
+        return fail(PA_ERR_UNSUPPORTED, "kv_dtype must be q_dtype or E4M3");
+    if (out_dtype != PA_F32 && out_dtype != q_dtype)
+        return fail(PA_ERR_UNSUPPORTED, "out_dtype must be F32 or the query dtype");
+    pa_status st = check_paged_cache(kv_dtype, pool, scales, N, H_kv, D, B, MB, NB);
+    if (st == PA_OK) st = check_group(H_q, H_kv);
+    if (st != PA_OK) return st;
+    if (top_k <= 0) return fail(PA_ERR_INVALID, "top_k must be positive");
+    if (!(scale > 0.f && scale < HUGE_VALF)) return fail(PA_ERR_INVALID, "scale must be positive and finite");
+    if (!out || !q || !pool || !block_tables || !ctx_lens || !selected || !workspace)
+        return fail(PA_ERR_INVALID, "null pointer argument");
+    if (!aligned16(out) || !aligned16(q) || !aligned16(selected) || !aligned16(workspace))
+        return fail(PA_ERR_INVALID, "out, q, selected and workspace must be 16-byte aligned");
+    const size_t need = decode_sparse_workspace_bytes(N, H_q, H_kv, D, B, top_k);
+    if (need == 0) return fail(PA_ERR_UNSUPPORTED, "too many work records");
+    if (ws_bytes < need) return fail(PA_ERR_INVALID, "workspace too small: %zu < %zu bytes", ws_bytes, need);
+    DecodeSparseArgs a;
+    a.out = out;
+    a.out_dtype = out_dtype;
+    a.q = q;
+    a.q_dtype = q_dtype;
+    a.pool = pool;
+    a.scales = scales;
+    a.kv_dtype = kv_dtype;
+    a.tables = block_tables;
+    a.ctx_lens = ctx_lens;
+    a.selected = selected;
+    a.top_k = top_k;
+    a.N = N;
+    a.H_q = H_q;
+    a.H_kv = H_kv;
+    a.D = D;
+    a.B = B;
+    a.MB = MB;
+    a.NB = NB;
+    a.scale = scale;
+    a.workspace = workspace;
+    a.dev_err = dev_err;
+    a.stream = static_cast<cudaStream_t>(stream);
+    return launch_decode_sparse(a);
+}
+
+pa_status pa_compact_tokens(void* pool, void* scales, pa_dtype kv_dtype, const int32_t* block_tables,
+                            const int32_t* ctx_lens, const int32_t* base, const int32_t* keep,
+                            const int32_t* keep_start, int N, int T, int H_kv, int D, int B, int MB, int NB,
+                            int* dev_err, void* stream) {
+    const NvtxRange nvtx_range("pa_compact_tokens");
+    g_msg[0] = 0;
+    const pa_status st = check_paged_cache(kv_dtype, pool, scales, N, H_kv, D, B, MB, NB);
+    if (st != PA_OK) return st;
+    if (T < 0) return fail(PA_ERR_INVALID, "bad sizes");
+    if (T == 0) return PA_OK;
+    if (!pool || !block_tables || !ctx_lens || !base || !keep || !keep_start)
+        return fail(PA_ERR_INVALID, "null pointer argument");
+    CompactArgs a;
+    a.pool = pool;
+    a.scales = scales;
+    a.kv_dtype = kv_dtype;
+    a.tables = block_tables;
+    a.ctx_lens = ctx_lens;
+    a.base = base;
+    a.keep = keep;
+    a.keep_start = keep_start;
+    a.N = N;
+    a.T = T;
+    a.H_kv = H_kv;
+    a.D = D;
+    a.B = B;
+    a.MB = MB;
+    a.NB = NB;
+    a.dev_err = dev_err;
+    a.stream = static_cast<cudaStream_t>(stream);
+    return launch_compact(a);
+}
+
 size_t pa_prefill_workspace_bytes(int N, int H_kv, int D, int B, int MB) {
     PrefillWorkspace L;
     return prefill_workspace_layout(N, H_kv, D, B, MB, &L) ? L.total : 0;

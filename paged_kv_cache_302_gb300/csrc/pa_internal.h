@@ -85,6 +85,80 @@ struct TreeArgs {
 size_t tree_workspace_bytes(int N, int H_q, int H_kv, int D, int max_q_len);
 pa_status launch_tree(const TreeArgs& a);
 
+// ----------------------------------------------------------------------------- block-sparse decode, compaction
+
+struct SummarizeArgs {
+    void* summaries;
+    void* sum_scales;
+    const void* pool;    // 16-bit pool, or e4m3 qpool
+    const void* scales;  // null for a 16-bit pool
+    int kv_dtype;
+    const int32_t* tables;
+    const int32_t* ctx_lens;
+    const int32_t* q_start;  // null: whole contexts
+    int N, H_kv, D, B, MB, NB, max_q_len;
+    int* dev_err;
+    cudaStream_t stream;
+};
+
+pa_status launch_summarize(const SummarizeArgs& a);
+
+struct SelectArgs {
+    int32_t* selected;
+    const void* q;
+    int q_dtype;
+    const void* summaries;
+    const void* sum_scales;
+    const int32_t* tables;
+    const int32_t* ctx_lens;
+    int N, H_q, H_kv, D, B, MB, NB, max_ctx, top_k, sink, recent;
+    void* workspace;
+    int* dev_err;
+    cudaStream_t stream;
+};
+
+// 0 for invalid arguments.
+size_t select_workspace_bytes(int N, int H_kv, int max_ctx, int B);
+pa_status launch_select(const SelectArgs& a);
+
+struct DecodeSparseArgs {
+    void* out;
+    int out_dtype;
+    const void* q;
+    int q_dtype;
+    const void* pool;    // 16-bit pool of q_dtype, or e4m3 qpool
+    const void* scales;  // null for a 16-bit pool
+    int kv_dtype;
+    const int32_t* tables;
+    const int32_t* ctx_lens;
+    const int32_t* selected;
+    int top_k, N, H_q, H_kv, D, B, MB, NB;
+    float scale;
+    void* workspace;
+    int* dev_err;
+    cudaStream_t stream;
+};
+
+// 0 for invalid arguments.
+size_t decode_sparse_workspace_bytes(int N, int H_q, int H_kv, int D, int B, int top_k);
+pa_status launch_decode_sparse(const DecodeSparseArgs& a);
+
+struct CompactArgs {
+    void* pool;    // 16-bit pool, or e4m3 qpool
+    void* scales;  // null for a 16-bit pool
+    int kv_dtype;
+    const int32_t* tables;
+    const int32_t* ctx_lens;
+    const int32_t* base;
+    const int32_t* keep;
+    const int32_t* keep_start;
+    int N, T, H_kv, D, B, MB, NB;
+    int* dev_err;
+    cudaStream_t stream;
+};
+
+pa_status launch_compact(const CompactArgs& a);
+
 // ----------------------------------------------------------------------------- decode
 
 constexpr int kStageTok = 32;         // tokens of one KV head per pipeline stage

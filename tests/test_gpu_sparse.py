@@ -1,0 +1,400 @@
+"""Block-sparse decode on the GPU: key summaries and block selection number for number, attention over listed blocks
+element by element against a 64-bit form, with poisoned memory wherever a call has no business."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import _quant_ref as R
+import _sparse_ref as S
+import paged_kv_cache_302_gb300 as pa
+
+pytestmark = pytest.mark.gpu
+DT = R.TORCH_DT
+
+
+def err_word():
+    return torch.zeros(1, dtype=torch.int32, device="cuda")
+
+
+def i32(x):
+    return torch.as_tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+
+
+def scales_of(c):
+    return {"scales": c[1]} if len(c) == 2 else {}
+
+
+# ------------------------------------------------------------------------------------------------ summaries
+
+def poisoned_boxes(NB, H, D):
+    return (torch.full((NB, H, 2, D), 55, dtype=torch.int8, device="cuda"),
+            torch.full((NB, H), 0xEE, dtype=torch.uint8, device="cuda"))
+
+
+def want_boxes(host, tables, ctx, n, B, want):
+    """Rebuilds the touched summaries in want = (boxes, bytes), both numpy."""
+    for s, L in enumerate(ctx):
+        if n[s] <= 0:
+            continue
+        for b in range((L - n[s]) // B, -(-L // B)):
+            blk = int(tables[s, b])
+            for h in range(want[0].shape[1]):
+                k, _, _ = S.keys_of(host, [blk], h, min(B, L - b * B))
+                want[0][blk, h], want[1][blk, h] = S.box(k)
+
+
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("H, D, B, ctx, chunk", [
+    (1, 64, 8, [1], [1]), (2, 128, 16, [16, 17, 15, 1], [1, 1, 1, 1]), (3, 64, 32, [33, 100, 5, 64], [2, 40, 0, 64]),
+    (8, 128, 16, [200, 31, 7, 512, 90], [200, 16, 7, 3, 64]), (5, 128, 8, [70, 8], [9, 8]),
+    (40, 64, 16, [37, 2], [20, 2])])
+def test_summaries(H, D, B, ctx, chunk, dtype, quant):
+    g = torch.Generator().manual_seed(H * 100 + D + B)
+    MB = -(-max(ctx) // B) + 2
+    NB = sum(-(-L // B) for L in ctx) + 3
+    c = S.make_cache(g, NB, H, B, D, dtype, quant)
+    tables = S.make_tables(g, ctx, B, MB, NB)
+    # what lies behind a context's end is garbage
+    nan = 0x7F if quant else math.nan
+    for s, L in enumerate(ctx):
+        if L % B:
+            blk = int(tables[s, L // B])
+            if quant:
+                c[0].view(torch.uint8)[blk, :, :, L % B:] = nan
+            else:
+                c[0][blk, L % B:] = nan
+    box, by = poisoned_boxes(NB, H, D)
+    want = box.cpu().numpy().copy(), by.cpu().numpy().copy()
+    want_boxes(S.host_cache(c), tables, ctx, chunk, B, want)
+    err = err_word()
+    qs = i32(np.concatenate([[0], np.cumsum(chunk)]))
+    pa.pa_summarize_blocks(box, by, c[0], tables.cuda(), i32(ctx), max(chunk), q_start=qs, dev_err=err, **scales_of(c))
+    assert np.array_equal(box.cpu().numpy(), want[0]) and np.array_equal(by.cpu().numpy(), want[1]) and err.item() == 0
+    # whole contexts
+    want_boxes(S.host_cache(c), tables, ctx, ctx, B, want)
+    pa.pa_summarize_blocks(box, by, c[0], tables.cuda(), i32(ctx), max(ctx), dev_err=err, **scales_of(c))
+    assert np.array_equal(box.cpu().numpy(), want[0]) and np.array_equal(by.cpu().numpy(), want[1]) and err.item() == 0
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_summaries_of_special_keys(dtype):
+    """Zeros, the type's extremes, bounds of the exponent on both sides, infinities, NaN in some and in all tokens."""
+    D, B, fi = 64, 8, torch.finfo(DT[dtype])
+    values = [0.0, fi.tiny, -fi.tiny, fi.smallest_normal, fi.max, -fi.max, 127.0, 127.5, 126.5, 254.0, 255.0, -127.0,
+              -128.0, 2.0 ** -20, math.inf, -math.inf, math.nan, 63.5, 64.0]
+    x = torch.zeros(len(values) + 3, B, 2, 1, D)
+    for i, v in enumerate(values):
+        x[i, :, 0, 0] = torch.linspace(-1, 1, B * D).view(B, D) * (abs(v) if math.isfinite(v) else 1.0) * 0.3
+        x[i, i % B, 0, 0, 7] = v
+    n = len(values)
+    x[n, :, 0, 0, 3] = math.nan                     # a channel of NaN alone
+    x[n, :, 0, 0, 4] = 2.5
+    x[n + 1, :, 0] = math.nan                       # a block of NaN alone
+    x[n + 2, :, 0, 0, 5] = math.inf                 # nothing but infinities in a channel
+    x = x.to(DT[dtype])
+    NB = x.shape[0]
+    tables = torch.arange(NB, dtype=torch.int32).view(1, NB)
+    box, by = poisoned_boxes(NB, 1, D)
+    pa.pa_summarize_blocks(box, by, x.cuda(), tables.cuda(), i32([NB * B]), NB * B)
+    with np.errstate(invalid="ignore"):
+        for b in range(NB):
+            want, e = S.box(R.to64(x[b, :, 0, 0]))
+            assert by[b, 0].item() == e, b
+            assert np.array_equal(box[b, 0].cpu().numpy(), want), b
+
+
+def test_summaries_of_every_quantised_pattern():
+    """All e4m3 patterns under scales across their range, bytes that no write produces among them."""
+    D, B, NB = 128, 16, 40
+    g = torch.Generator().manual_seed(5)
+    qp = torch.randint(0, 256, (NB, 2, 2, B, D), generator=g, dtype=torch.uint8)
+    sc = torch.randint(0, 256, (NB, 2, 2, B), generator=g, dtype=torch.uint8)
+    sc[::2] = torch.randint(120, 132, sc[::2].shape, generator=g, dtype=torch.uint8)
+    qp[:4] &= 0x8F                                  # small and subnormal values
+    tables = torch.randperm(NB, generator=g).to(torch.int32).view(1, NB)
+    box, by = poisoned_boxes(NB, 2, D)
+    pa.pa_summarize_blocks(box, by, qp.cuda().view(torch.float8_e4m3fn), tables.cuda(), i32([NB * B]), NB * B,
+                           scales=sc.cuda())
+    for b in range(NB):
+        for h in range(2):
+            want, e = S.box(S.keys_of((qp.numpy(), sc.numpy()), [b], h, B)[0])
+            assert by[b, h].item() == e and np.array_equal(box[b, h].cpu().numpy(), want)
+
+
+def test_summaries_flag_and_leave_out_bad_sequences():
+    D, B, NB, MB = 64, 8, 12, 3
+    g = torch.Generator().manual_seed(1)
+    c = S.make_cache(g, NB, 2, B, D, "bf16", False)
+    tables = torch.arange(NB, dtype=torch.int32).view(4, MB)
+    for ctx, qs, top, entry, flag, good in [
+            ([8, 25, 8, 8], [0, 1, 2, 3, 4], 1, None, pa.PA_DEV_ERR_CTX, [0, 2, 3]),      # a context past MB * B
+            ([8, 3, 8, 8], [0, 1, 6, 7, 8], 5, None, pa.PA_DEV_ERR_CTX, [0, 2, 3]),       # a chunk past its context
+            ([8, 8, 8, 8], [0, 1, 4, 5, 6], 2, None, pa.PA_DEV_ERR_CTX, [0, 2, 3]),       # longer than max_q_len
+            ([8, 8, 8, 8], [0, 1, 0, 1, 2], 2, None, pa.PA_DEV_ERR_CTX, [0, 2, 3]),       # q_start descends
+            ([8, -3, 8, 8], None, 8, None, pa.PA_DEV_ERR_CTX, [0, 2, 3]),
+            ([8, 0, 8, 8], None, 8, None, 0, [0, 2, 3]),                                   # nothing there is no error
+            ([8, 8, 8, 8], None, 8, NB, pa.PA_DEV_ERR_BLOCK, [0, 2, 3]),
+            ([8, 8, 8, 8], None, 8, -1, pa.PA_DEV_ERR_BLOCK, [0, 2, 3])]:
+        t = tables.clone()
+        if entry is not None:
+            t[1, 0] = entry
+        box, by = poisoned_boxes(NB, 2, D)
+        want = box.cpu().numpy().copy(), by.cpu().numpy().copy()
+        want_boxes(S.host_cache(c), t[good], [8, 8, 8], [1, 1, 1], B, want)
+        err = err_word()
+        pa.pa_summarize_blocks(box, by, c[0], t.cuda(), i32(ctx), top, q_start=None if qs is None else i32(qs),
+                               dev_err=err)
+        assert err.item() == flag
+        assert np.array_equal(box.cpu().numpy(), want[0]) and np.array_equal(by.cpu().numpy(), want[1])
+
+
+# ------------------------------------------------------------------------------------------------ selection
+
+def check_select(q, box, by, tables, ctx, B, top_k, sink, recent, H, flag=0, max_ctx=None, ctx_flag=()):
+    N, Hq, D = q.shape
+    G = Hq // H
+    sel = torch.full((N, H, top_k), 77, dtype=torch.int32, device="cuda")
+    err = err_word()
+    pa.pa_select_blocks(sel, q.cuda(), box.cuda(), by.cuda(), tables.cuda(), i32(ctx), max_ctx or max(max(ctx), 1), B,
+                        sink_blocks=sink, recent_blocks=recent, dev_err=err)
+    got = sel.cpu().numpy()
+    for s, L in enumerate(ctx):
+        for h in range(H):
+            want = np.full(top_k, -1)
+            if s not in ctx_flag:
+                at = tables[s, : -(-L // B)].numpy()
+                bad = (at < 0) | (at >= box.shape[0])
+                at = np.where(bad, 0, at)
+                x = S.scores(R.to64(q[s, h * G: (h + 1) * G]), box[at, h].numpy(), by[at, h].numpy())
+                want = S.select(np.where(bad, -np.inf, x), top_k, sink, recent)
+            assert np.array_equal(got[s, h], want), (s, h)
+    assert err.item() == flag
+    return sel
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("H, G, D, B, ctx, top_k, sink, recent", [
+    (1, 1, 64, 8, [1], 1, 0, 0), (1, 1, 64, 8, [9], 1, 0, 1), (2, 4, 128, 16, [16, 17, 400, 1000], 8, 1, 1),
+    (3, 3, 64, 32, [1, 2000, 5000, 64], 17, 2, 3), (8, 7, 128, 16, [5000, 4097], 64, 1, 1),
+    (8, 8, 128, 8, [3000, 130, 8000], 33, 0, 0), (5, 2, 128, 16, [700, 1500], 40, 20, 20),
+    (2, 5, 64, 8, [20000, 123], 500, 4, 16), (1, 6, 128, 32, [40000], 1000, 1, 1)])
+def test_selection(H, G, D, B, ctx, top_k, sink, recent, dtype):
+    g = torch.Generator().manual_seed(H * 31 + D + len(ctx))
+    MB = -(-max(ctx) // B) + 1
+    NB = sum(-(-L // B) for L in ctx) + 2
+    box, by = S.make_boxes(g, NB, H, D)
+    tables = S.make_tables(g, ctx, B, MB, NB)
+    q = torch.randn(len(ctx), H * G, D, generator=g).to(DT[dtype])
+    check_select(q, box, by, tables, ctx, B, top_k, sink, recent, H)
+
+
+def test_selection_breaks_ties_by_the_lower_block():
+    """Few distinct boxes, so that most scores are equal, at every place of the cut."""
+    D, B, nb = 64, 8, 700
+    g = torch.Generator().manual_seed(2)
+    few, _ = S.make_boxes(g, 3, 2, D)
+    box = few[torch.randint(0, 3, (nb,), generator=g)]
+    by = torch.full((nb, 2), 124, dtype=torch.uint8)
+    tables = torch.arange(nb, dtype=torch.int32).view(1, nb)
+    q = torch.randn(1, 4, D, generator=g).half()
+    for top_k in (1, 2, 31, 32, 33, 230, 256, 300, 511, 512, 513, 699, 700, 701):
+        check_select(q, box, by, tables, [nb * B - 3], B, top_k, min(1, top_k), 0, 2)
+    # all equal: boxes of zeros, and a query of zeros
+    check_select(q, torch.zeros_like(box), by, tables, [nb * B], B, 100, 1, 1, 2)
+    check_select(torch.zeros_like(q), box, by, tables, [nb * B], B, 100, 1, 1, 2)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_selection_by_special_queries(dtype):
+    """Extremes, subnormals, ties of the rounding, infinities, NaN, heads of very different size, bounds of the exponent,
+    boxes at the integers' ends under scale bytes across the range and outside it."""
+    D, B, nb, fi = 128, 8, 300, torch.finfo(DT[dtype])
+    g = torch.Generator().manual_seed(3)
+    box, _ = S.make_boxes(g, nb, 1, D)
+    box[:40] = 127
+    box[40:80] = -127
+    box[80:100, :, 0] = -127
+    box[80:100, :, 1] = 127
+    by = torch.randint(60, 190, (nb, 1), generator=g, dtype=torch.uint8)
+    by[::3] = 120
+    tables = torch.randperm(nb, generator=g).to(torch.int32).view(1, nb)
+    rows = []
+    for v in (fi.max, -fi.max, fi.tiny, fi.smallest_normal, 511.0, 512.0, 510.0, 0.5, math.inf, -math.inf, math.nan):
+        r = torch.randn(D, generator=g) * (abs(v) if math.isfinite(v) else 1.0) * 0.2
+        r[9] = v
+        rows.append(r)
+    rows.append(torch.arange(D) % 64 * 8.0 - 252 + 0.5)         # halves: ties to even
+    rows.append(torch.full((D,), math.nan))
+    rows.append(torch.full((D,), 511.0))
+    for i in range(0, len(rows) - 1, 2):
+        check_select(torch.stack(rows[i: i + 2])[None].to(DT[dtype]), box, by, tables, [nb * B], B, 50, 1, 1, 1)
+
+
+def test_selection_flags():
+    D, B, nb, H = 64, 8, 64, 2
+    g = torch.Generator().manual_seed(4)
+    box, by = S.make_boxes(g, 3 * nb, H, D)
+    tables = torch.arange(3 * nb, dtype=torch.int32).view(3, nb)
+    q = torch.randn(3, 4, D, generator=g).half()
+    tables[1, 5], tables[1, 20], tables[2, 7] = 3 * nb, -1, 1 << 30
+    check_select(q, box, by, tables, [nb * B] * 3, B, 16, 1, 1, H, flag=pa.PA_DEV_ERR_BLOCK)
+    tables = torch.arange(3 * nb, dtype=torch.int32).view(3, nb)
+    for bad in (0, -5, nb * B + 1):
+        check_select(q, box, by, tables, [500, bad, 300], B, 16, 1, 1, H, flag=pa.PA_DEV_ERR_CTX, ctx_flag=(1,),
+                     max_ctx=nb * B + 8)
+    check_select(q, box, by, tables, [500, 401, 300], B, 16, 1, 1, H, flag=pa.PA_DEV_ERR_CTX, ctx_flag=(0, 1),
+                 max_ctx=400)
+
+
+# ------------------------------------------------------------------------------------------------ attention
+
+def random_lists(g, ctx, H, B, top_k, fill=1.0):
+    """Lists [N, H, top_k] in random order with padding strewn in."""
+    sel = torch.full((len(ctx), H, top_k), -1, dtype=torch.int32)
+    for s, L in enumerate(ctx):
+        nb = -(-L // B)
+        for h in range(H):
+            n = min(nb, max(1, int(top_k * fill)))
+            pick = torch.randperm(nb, generator=g)[:n].to(torch.int32)
+            at = torch.randperm(top_k, generator=g)[:n]
+            sel[s, h, at] = pick
+    return sel
+
+
+def want_sparse(q, host, tables, ctx, sel, B, scale, dtype, quant):
+    """Output rows and their bounds, in 64 bits; duplicates count as often as they stand."""
+    N, Hq, D = q.shape
+    H = sel.shape[1]
+    G = Hq // H
+    out, tol = np.zeros((N, Hq, D)), np.zeros((N, Hq, D))
+    for s, L in enumerate(ctx):
+        nb = -(-L // B)
+        for h in range(H):
+            t = []
+            for e in sel[s, h].tolist():
+                if 0 <= e < nb:
+                    t += range(e * B, min(L, e * B + B))
+            k, v, ev = S.keys_of(host, tables[s, :nb].numpy(), h, L)
+            k, v, ev = k[t], v[t], ev[t]
+            rows = slice(h * G, (h + 1) * G)
+            see = np.ones((G, len(t)), dtype=bool)
+            out[s, rows], tol[s, rows] = R.attend(R.to64(q[s, rows]), k, v, ev, see, scale, True,
+                                                  quant or dtype == "f16")
+    return out, tol
+
+
+@pytest.mark.parametrize("out32", [False, True])
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("H, G, D, B, ctx, top_k", [
+    (1, 1, 64, 8, [1], 1), (1, 8, 128, 16, [17, 300], 5), (2, 4, 128, 16, [1000, 16, 555], 64),
+    (3, 3, 64, 32, [100, 700, 31, 1], 9), (8, 7, 128, 16, [2000, 130], 40), (5, 2, 64, 8, [400, 2500], 257),
+    (2, 5, 128, 32, [3000, 90, 1700], 70), (8, 1, 128, 8, [129] * 20, 12)])
+def test_attention(H, G, D, B, ctx, top_k, dtype, quant, out32):
+    g = torch.Generator().manual_seed(H * 13 + D + top_k)
+    MB = -(-max(ctx) // B) + 1
+    NB = sum(-(-L // B) for L in ctx) + 3
+    c = S.make_cache(g, NB, H, B, D, dtype, quant)
+    tables = S.make_tables(g, ctx, B, MB, NB)
+    host = S.host_cache(c)
+    for s, L in enumerate(ctx):                      # garbage behind the context
+        if L % B:
+            blk = int(tables[s, L // B])
+            if quant:
+                c[0].view(torch.uint8)[blk, :, :, L % B:] = 0x7F
+            else:
+                c[0][blk, L % B:] = math.nan
+    q = torch.randn(len(ctx), H * G, D, generator=g).to(DT[dtype])
+    sel = random_lists(g, ctx, H, B, top_k, fill=0.8)
+    if len(ctx) > 1:
+        sel[-1, 0] = -1                              # a list without a block: zeros
+    out = torch.full(q.shape, math.nan, dtype=torch.float32 if out32 else DT[dtype], device="cuda")
+    err = err_word()
+    pa.pa_decode_sparse(out, q.cuda(), c[0], tables.cuda(), i32(ctx), sel.cuda(), dev_err=err, **scales_of(c))
+    want, tol = want_sparse(q, host, tables, ctx, sel, B, 1 / math.sqrt(D), dtype, quant)
+    R.close(out, want, tol, "sparse decode")
+    assert err.item() == 0
+
+
+@pytest.mark.parametrize("quant", [False, True])
+def test_attention_flags_and_skips_bad_entries(quant):
+    H, G, D, B, top_k = 2, 4, 64, 16, 8
+    ctx = [100, 200, 90]
+    g = torch.Generator().manual_seed(8)
+    c = S.make_cache(g, 40, H, B, D, "bf16", quant)
+    tables = S.make_tables(g, ctx, B, 13, 40)
+    q = torch.randn(3, H * G, D, generator=g).bfloat16()
+    sel = random_lists(g, ctx, H, B, top_k, fill=0.5)
+    host = S.host_cache(c)
+
+    def run(t, lens, lists, flag):
+        out = torch.full(q.shape, 9.0, dtype=torch.float32, device="cuda")
+        err = err_word()
+        pa.pa_decode_sparse(out, q.cuda(), c[0], t.cuda(), i32(lens), lists.cuda(), dev_err=err, **scales_of(c))
+        assert err.item() == flag
+        return out
+
+    bad = sel.clone()
+    bad[0, 1, 3], bad[1, 0, 0], bad[2, 1, 7], bad[2, 0, 2] = 7, 13, 1 << 30, 2 ** 31 - 1
+    want, tol = want_sparse(q, host, tables, ctx, bad, B, 1 / 8, "bf16", quant)
+    R.close(run(tables, ctx, bad, pa.PA_DEV_ERR_BLOCK), want, tol, "entries past the context")
+    t = tables.clone()
+    t[1, 3], t[1, 5] = -1, 40                        # these blocks of sequence 1 cannot be read
+    lists = sel.clone()
+    lists[1, :, :4] = torch.tensor([3, 2, 5, 6], dtype=torch.int32)
+    without = lists.clone()
+    without[(without == 3) | (without == 5)] = torch.where(
+        torch.arange(3).view(3, 1, 1) == 1, -1, lists)[(without == 3) | (without == 5)]
+    want, tol = want_sparse(q, host, tables, ctx, without, B, 1 / 8, "bf16", quant)
+    R.close(run(t, ctx, lists, pa.PA_DEV_ERR_BLOCK), want, tol, "entries without a block")
+    want, tol = want_sparse(q, host, tables, ctx, sel, B, 1 / 8, "bf16", quant)
+    for L in (0, -1, 13 * B + 1):
+        out = run(tables, [100, L, 90], sel, pa.PA_DEV_ERR_CTX)
+        assert (out[1] == 9.0).all()
+        R.close(out[[0, 2]], want[[0, 2]], tol[[0, 2]], "the other sequences")
+
+
+@pytest.mark.parametrize("quant", [False, True])
+def test_attention_counts_repeated_blocks_and_takes_lists_in_any_order(quant):
+    H, G, D, B, ctx = 1, 4, 128, 16, [77]
+    g = torch.Generator().manual_seed(9)
+    c = S.make_cache(g, 8, H, B, D, "f16", quant)
+    tables = S.make_tables(g, ctx, B, 5, 8)
+    q = torch.randn(1, G, D, generator=g).half()
+    sel = torch.tensor([4, 2, 4, -1, 0, 2, 2, -7], dtype=torch.int32).view(1, 1, 8)
+    out = torch.empty(q.shape, dtype=torch.float32, device="cuda")
+    pa.pa_decode_sparse(out, q.cuda(), c[0], tables.cuda(), i32(ctx), sel.cuda(), **scales_of(c))
+    want, tol = want_sparse(q, S.host_cache(c), tables, ctx, sel, B, 1 / math.sqrt(D), "f16", quant)
+    R.close(out, want, tol, "sparse decode")
+
+
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+def test_every_block_listed_is_the_whole_decode(D, quant):
+    H, G, B, ctx = 4, 4, 16, [1000, 33, 512]
+    g = torch.Generator().manual_seed(10)
+    NB = sum(-(-L // B) for L in ctx) + 1
+    c = S.make_cache(g, NB, H, B, D, "bf16", quant)
+    tables = S.make_tables(g, ctx, B, 63, NB).cuda()
+    q = torch.randn(3, H * G, D, generator=g).bfloat16().cuda()
+    box, by = poisoned_boxes(NB, H, D)
+    pa.pa_summarize_blocks(box, by, c[0], tables, i32(ctx), max(ctx), **scales_of(c))
+    sel = torch.empty(3, H, 70, dtype=torch.int32, device="cuda")
+    pa.pa_select_blocks(sel, q, box, by, tables, i32(ctx), max(ctx), B)
+    a, b = (torch.empty(q.shape, dtype=torch.float32, device="cuda") for _ in range(2))
+    pa.pa_decode_sparse(a, q, c[0], tables, i32(ctx), sel, **scales_of(c))
+    if quant:
+        pa.pa_decode_quant(b, q, c[0], c[1], tables, i32(ctx), max(ctx))
+    else:
+        pa.pa_decode(b, q, c[0], tables, i32(ctx), max(ctx))
+    # both are within the 64-bit form's bound; their difference is within twice that
+    lists = [list(range(-(-L // B))) for L in ctx]
+    ref = torch.full((3, H, 63), -1, dtype=torch.int32)
+    for s, x in enumerate(lists):
+        ref[s, :, : len(x)] = torch.tensor(x, dtype=torch.int32)
+    want, tol = want_sparse(q.cpu(), S.host_cache(c), tables.cpu(), ctx, ref, B, 1 / math.sqrt(D), "bf16", quant)
+    R.close(a, want, tol, "sparse decode")
+    R.close(b, want, tol, "whole decode")
