@@ -31,6 +31,7 @@ __device__ __forceinline__ int int_exponent(float a) {
 // L lanes per (block, KV head), each with its own channels, walk the block's tokens.  Minima and maxima that start as
 // NaN ignore NaN elements: the instructions return the other operand.
 constexpr int kSumThreads = 256;
+constexpr int kSumBatch = 8;  // tokens of a block on their way at a time
 
 // K rows of 16 bits: 8 channels per lane, minima and maxima in the rows' own type.
 template <typename T>
@@ -146,22 +147,74 @@ __global__ void __launch_bounds__(kSumThreads) summarize_kernel(const SummaryPar
         if constexpr (kQuant) {
             const uint8_t* k = static_cast<const uint8_t*>(p.pool) + ((int64_t)blk * p.H_kv + h) * (2 * B * D);
             const uint8_t* sc = p.scales + ((int64_t)blk * p.H_kv + h) * (2 * B);
+            uint32_t sw[B / 4];  // the tokens' scale bytes
 #pragma unroll
-            for (int j = 0; j < C; ++j) lo[j] = hi[j] = __uint_as_float(0x7fffffffu);
-#pragma unroll 4
-            for (int t = 0; t < nv; ++t) {
-                const uint4 x = reinterpret_cast<const uint4*>(k + t * D)[sub];
-                const float f = pow2i(scale_of(sc[t]));
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            for (int j = 0; j < B / 8; ++j) {
+                const uint2 x = reinterpret_cast<const uint2*>(sc)[j];
+                sw[2 * j] = x.x;
+                sw[2 * j + 1] = x.y;
+            }
+            auto exponent = [&](int t) { return scale_of((int)(sw[t / 4] >> (8 * (t & 3)) & 0xffu)); };
+            int top = kScaleMin, low = kScaleMax, last = 0;
+#pragma unroll
+            for (int t = 0; t < B; ++t)
+                if (t < nv) {
+                    top = max(top, exponent(t));
+                    low = min(low, exponent(t));
+                    last = exponent(t);
+                }
+            if (top - low <= 15) {
+                // rows in units of the largest scale: e4m3 is a multiple of 2^-9, so down to 2^-15 of it fp16 is exact
+                uint32_t a[8], z[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) a[j] = z[j] = 0x7fff7fffu;
+#pragma unroll
+                for (int t0 = 0; t0 < B; t0 += kSumBatch) {
+                    if (t0 < nv) {
+                        uint4 x[kSumBatch];
+#pragma unroll
+                        for (int t = 0; t < kSumBatch; ++t)  // (past the last token: the last one again)
+                            x[t] = reinterpret_cast<const uint4*>(k + min(t0 + t, nv - 1) * D)[sub];
+#pragma unroll
+                        for (int t = 0; t < kSumBatch; ++t) {
+                            const int e = t0 + t < nv ? exponent(t0 + t) : last;
+                            const __half2 f = __float2half2_rn(pow2i(e - top));
+                            const uint32_t w[4] = {x[t].x, x[t].y, x[t].z, x[t].w};
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const uint32_t q = e4m3x2_to_f16x2(w[j / 2] >> (16 * (j & 1)));
+                                const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&q), f);
+                                const uint32_t v = *reinterpret_cast<const uint32_t*>(&y);
+                                a[j] = Pair<__half>::lo(a[j], v);
+                                z[j] = Pair<__half>::hi(z[j], v);
+                            }
+                        }
+                    }
+                }
+                const float unit = pow2i(top);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    float2 v = Mma<__half>::unpack(e4m3x2_to_f16x2(w[j / 2] >> (16 * (j & 1))));
-                    v.x *= f;
-                    v.y *= f;
-                    lo[2 * j] = fminf(lo[2 * j], v.x);
-                    hi[2 * j] = fmaxf(hi[2 * j], v.x);
-                    lo[2 * j + 1] = fminf(lo[2 * j + 1], v.y);
-                    hi[2 * j + 1] = fmaxf(hi[2 * j + 1], v.y);
+                    const float2 f = Mma<__half>::unpack(a[j]), g = Mma<__half>::unpack(z[j]);
+                    lo[2 * j] = f.x * unit;
+                    lo[2 * j + 1] = f.y * unit;
+                    hi[2 * j] = g.x * unit;
+                    hi[2 * j + 1] = g.y * unit;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < C; ++j) lo[j] = hi[j] = __uint_as_float(0x7fffffffu);
+                for (int t = 0; t < nv; ++t) {
+                    const uint4 x = reinterpret_cast<const uint4*>(k + t * D)[sub];
+                    const float f = pow2i(scale_of(sc[t]));
+                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float2 v = Mma<__half>::unpack(e4m3x2_to_f16x2(w[j / 2] >> (16 * (j & 1))));
+                        lo[2 * j] = fminf(lo[2 * j], v.x * f);
+                        hi[2 * j] = fmaxf(hi[2 * j], v.x * f);
+                        lo[2 * j + 1] = fminf(lo[2 * j + 1], v.y * f);
+                        hi[2 * j + 1] = fmaxf(hi[2 * j + 1], v.y * f);
+                    }
                 }
             }
         } else {
@@ -170,14 +223,22 @@ __global__ void __launch_bounds__(kSumThreads) summarize_kernel(const SummaryPar
             uint32_t a[4], z[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) a[j] = z[j] = 0x7fff7fffu;
-#pragma unroll 8
-            for (int t = 0; t < nv; ++t) {
-                const uint4 x = reinterpret_cast<const uint4*>(k + t * step)[sub];
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    a[j] = Pair<T>::lo(a[j], w[j]);
-                    z[j] = Pair<T>::hi(z[j], w[j]);
+            for (int t0 = 0; t0 < B; t0 += kSumBatch) {
+                if (t0 < nv) {
+                    uint4 x[kSumBatch];
+#pragma unroll
+                    for (int t = 0; t < kSumBatch; ++t)  // (past the last token: the last one again)
+                        x[t] = reinterpret_cast<const uint4*>(k + min(t0 + t, nv - 1) * step)[sub];
+#pragma unroll
+                    for (int t = 0; t < kSumBatch; ++t) {
+                        const uint32_t w[4] = {x[t].x, x[t].y, x[t].z, x[t].w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            a[j] = Pair<T>::lo(a[j], w[j]);
+                            z[j] = Pair<T>::hi(z[j], w[j]);
+                        }
+                    }
                 }
             }
 #pragma unroll
@@ -249,7 +310,7 @@ struct SelectParams {
     const uint8_t* box_scales;
     const int32_t* tables;
     const int32_t* ctx_lens;
-    float* keys;  // [N][H_kv][stride]
+    uint32_t* keys;  // [N][H_kv][stride], ordered as the scores
     int64_t stride;
     int H_kv, G, lgB, MB, NB, max_ctx, top_k, sink, recent;
     int* err;
@@ -261,10 +322,18 @@ __device__ __forceinline__ int context_blocks(const SelectParams& p, int s) {
     return ctx < 1 || ctx > p.max_ctx || ctx > (int64_t)p.MB << p.lgB ? 0 : (ctx + (1 << p.lgB) - 1) >> p.lgB;
 }
 
-// Scores: one warp per (sequence, KV head, 16 blocks), mma.sync m16n8k16 with the blocks on M and the query heads of
-// the KV head on N.  max(q lo, q hi) is q hi for q >= 0 and q lo below, so a box's score is one product of length 2 D,
+// Unsigned integers order as the floats do.
+__device__ __forceinline__ uint32_t ordered(float x) {
+    const uint32_t u = __float_as_uint(x + 0.f);  // -0 counts as 0
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+// Scores: mma.sync m16n8k16 with 16 blocks on M and the query heads of the KV head on N; a warp takes a tile of 16 blocks
+// after another.  max(q lo, q hi) is q hi for q >= 0 and q lo below, so a box's score is one product of length 2 D,
 // [max(q, 0), min(q, 0)] . [hi, lo]; box and query integers are exact in fp16.
 constexpr int kScoreWarps = 8;
+constexpr int kScoreFill = 24;   // warps of an SM that the tiles are spread over first
+constexpr int kScoreTiles = 8;   // tiles of a warp at most
 
 // Four 8-bit integers as two fp16 pairs: v + 128 in the low byte of 0x6400 is 1024 + 128 + v.
 __device__ __forceinline__ void int8x4_to_f16(uint32_t x, uint32_t& a, uint32_t& b) {
@@ -277,7 +346,7 @@ __device__ __forceinline__ void int8x4_to_f16(uint32_t x, uint32_t& a, uint32_t&
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kScoreWarps * 32) score_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(kScoreWarps * 32) score_kernel(const SelectParams p, int tiles_per_warp) {
     constexpr int NC = D / 64;  // 16-byte chunks of a lane: t4, t4 + 4 of each half of the box
     griddep_wait();
     griddep_launch_dependents();
@@ -285,112 +354,120 @@ __global__ void __launch_bounds__(kScoreWarps * 32) score_kernel(const SelectPar
     const int h = blockIdx.y, s = blockIdx.z;
     const int nb = context_blocks(p, s);
     if (nb <= p.top_k) return;  // nothing to choose
-    const int tile = blockIdx.x * kScoreWarps + (threadIdx.x >> 5);
-    if (16 * tile >= nb) return;
+    int tile = blockIdx.x * (kScoreWarps * tiles_per_warp) + (threadIdx.x >> 5);
+    const int end = min((int)(blockIdx.x + 1) * (kScoreWarps * tiles_per_warp), (nb + 15) / 16);
+    if (tile >= end) return;
+    // block ids of this lane's rows of a tile: blocks g4 and g4 + 8
+    auto entry = [&](int t, int r) -> int {
+        const int b = 16 * t + g4 + 8 * r;
+        return t < end && b < nb ? p.tables[(int64_t)s * p.MB + b] : 0;
+    };
+    int blk[2] = {entry(tile, 0), entry(tile, 1)};
     // the query integers of head g4, in the order of the box's bytes: word w of chunk c holds channels 64 c + 16 t4 +
     // 4 w on, the k-columns 2 t4, 2 t4 + 1, 2 t4 + 8, 2 t4 + 9 of k-step (c, w)
-    float x[NC][16];
-    float m = 0.f;
+    uint32_t qi[NC][8];
+    float f0, f1;  // units of heads 2 t4 and 2 t4 + 1
+    {
+        float m = 0.f;
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
+        for (int c = 0; c < NC; ++c)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (g4 < p.G)
-                v = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) +
-                                                   (((int64_t)s * p.H_kv + h) * p.G + g4) * D + 64 * c + 16 * t4)[i];
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            for (int i = 0; i < 2; ++i) {
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (g4 < p.G)
+                    v = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) +
+                                                       (((int64_t)s * p.H_kv + h) * p.G + g4) * D + 64 * c + 16 * t4)[i];
+                qi[c][4 * i] = v.x;
+                qi[c][4 * i + 1] = v.y;
+                qi[c][4 * i + 2] = v.z;
+                qi[c][4 * i + 3] = v.w;
+            }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 f = Mma<T>::unpack(w[j]);
-                x[c][8 * i + 2 * j] = f.x;
-                x[c][8 * i + 2 * j + 1] = f.y;
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 f = Mma<T>::unpack(qi[c][i]);
                 m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));  // (a NaN counts as nothing)
             }
-        }
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    const int f = int_exponent<9>(m);
-    const float inv = pow2i(-f);
-    const float f0 = pow2i(__shfl_sync(0xffffffffu, f, 8 * t4)), f1 = pow2i(__shfl_sync(0xffffffffu, f, 8 * t4 + 4));
-    uint32_t up[NC][4][2], dn[NC][4][2];  // max(q, 0) and min(q, 0)
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        const int f = int_exponent<9>(m);
+        const float inv = pow2i(-f);
+        f0 = pow2i(__shfl_sync(0xffffffffu, f, 8 * t4));
+        f1 = pow2i(__shfl_sync(0xffffffffu, f, 8 * t4 + 4));
+        auto integer = [&](float x) {
+            return x == x ? fminf(fmaxf(rintf(x * inv), -(float)kQueryTop), (float)kQueryTop) : 0.f;
+        };
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
+        for (int c = 0; c < NC; ++c)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float v[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const float y = x[c][2 * i + k];
-                v[k] = y == y ? fminf(fmaxf(rintf(y * inv), -(float)kQueryTop), (float)kQueryTop) : 0.f;
+            for (int i = 0; i < 8; ++i) {
+                const float2 x = Mma<T>::unpack(qi[c][i]);
+                qi[c][i] = Mma<__half>::pack(integer(x.x), integer(x.y));
             }
-            up[c][i / 2][i & 1] = Mma<__half>::pack(fmaxf(v[0], 0.f), fmaxf(v[1], 0.f));
-            dn[c][i / 2][i & 1] = Mma<__half>::pack(fminf(v[0], 0.f), fminf(v[1], 0.f));
-        }
-    // the boxes of blocks g4 and g4 + 8 of the tile
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-    int64_t row[2];
-    bool good[2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const int b = 16 * tile + g4 + 8 * r;
-        const int blk = b < nb ? p.tables[(int64_t)s * p.MB + b] : 0;
-        good[r] = (unsigned)blk < (unsigned)p.NB;
-        if (!good[r] && t4 == 0 && h == 0) flag_error(p.err, PA_DEV_ERR_BLOCK);
-        row[r] = (int64_t)(good[r] ? blk : 0) * p.H_kv + h;
     }
-    uint4 v[2][2][NC];  // [block][lo, hi][chunk]
+    uint32_t* keys = p.keys + ((int64_t)s * p.H_kv + h) * p.stride;
+    for (; tile < end; tile += kScoreWarps) {
+        bool good[2];
+        int64_t row[2];
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
+        for (int r = 0; r < 2; ++r) {
+            good[r] = (unsigned)blk[r] < (unsigned)p.NB;
+            if (!good[r] && t4 == 0 && h == 0) flag_error(p.err, PA_DEV_ERR_BLOCK);
+            row[r] = (int64_t)(good[r] ? blk[r] : 0) * p.H_kv + h;
+        }
+        uint4 v[2][2][NC];  // [block][lo, hi][chunk]
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int c = 0; c < NC; ++c)
+                    v[r][k][c] = reinterpret_cast<const uint4*>(p.boxes + (row[r] * 2 + k) * D + 64 * c)[t4];
+        float unit[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            unit[r] = pow2i(scale_of(p.box_scales[row[r]]));
+            blk[r] = entry(tile + kScoreWarps, r);
+        }
+        float acc[2][4] = {};
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int c = 0; c < NC; ++c)
-                v[r][k][c] = reinterpret_cast<const uint4*>(p.boxes + (row[r] * 2 + k) * D + 64 * c)[t4];
-    float unit[2];
+            for (int c = 0; c < NC; ++c) {
+                const uint32_t w0[4] = {v[0][k][c].x, v[0][k][c].y, v[0][k][c].z, v[0][k][c].w};
+                const uint32_t w1[4] = {v[1][k][c].x, v[1][k][c].y, v[1][k][c].z, v[1][k][c].w};
 #pragma unroll
-    for (int r = 0; r < 2; ++r) unit[r] = pow2i(scale_of(p.box_scales[row[r]]));
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            const uint32_t w0[4] = {v[0][k][c].x, v[0][k][c].y, v[0][k][c].z, v[0][k][c].w};
-            const uint32_t w1[4] = {v[1][k][c].x, v[1][k][c].y, v[1][k][c].z, v[1][k][c].w};
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                uint32_t a0, a1, a2, a3;
-                int8x4_to_f16(w0[w], a0, a2);
-                int8x4_to_f16(w1[w], a1, a3);
-                const uint32_t(&qf)[2] = k ? up[c][w] : dn[c][w];
-                Mma<__half>::run(acc, a0, a1, a2, a3, qf[0], qf[1]);
+                for (int w = 0; w < 4; ++w) {
+                    uint32_t a0, a1, a2, a3;
+                    int8x4_to_f16(w0[w], a0, a2);
+                    int8x4_to_f16(w1[w], a1, a3);
+                    const uint32_t x0 = qi[c][2 * w], x1 = qi[c][2 * w + 1];
+                    // the query's negative half meets lo, its positive half hi
+                    Mma<__half>::run(acc[k], a0, a1, a2, a3, k ? Pair<__half>::hi(x0, 0) : Pair<__half>::lo(x0, 0),
+                                     k ? Pair<__half>::hi(x1, 0) : Pair<__half>::lo(x1, 0));
+                }
             }
-        }
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        float y = -INFINITY;
-        if (2 * t4 < p.G) y = acc[2 * r] * f0;
-        if (2 * t4 + 1 < p.G) y = fmaxf(y, acc[2 * r + 1] * f1);
-        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 1));
-        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 2));
-        const int b = 16 * tile + g4 + 8 * r;
-        if (t4 == 0 && b < nb) p.keys[((int64_t)s * p.H_kv + h) * p.stride + b] = good[r] ? y * unit[r] : -INFINITY;
+        for (int r = 0; r < 2; ++r) {
+            float y = -INFINITY;
+            if (2 * t4 < p.G) y = (acc[0][2 * r] + acc[1][2 * r]) * f0;
+            if (2 * t4 + 1 < p.G) y = fmaxf(y, (acc[0][2 * r + 1] + acc[1][2 * r + 1]) * f1);
+            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 1));
+            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 2));
+            const int b = 16 * tile + g4 + 8 * r;
+            if (t4 == 0 && b < nb) keys[b] = ordered(good[r] ? y * unit[r] : -INFINITY);
+        }
     }
 }
 
-// The top_k of a (sequence, KV head): a radix search from the top digit down for the key of the last one taken, then
-// one pass in index order that lists every key above it and the first ones equal to it.
-constexpr int kTopThreads = 256;
-
-// Unsigned integers order as the floats do.
-__device__ __forceinline__ uint32_t ordered(float x) {
-    const uint32_t u = __float_as_uint(x + 0.f);  // -0 counts as 0
-    return u & 0x80000000u ? ~u : u | 0x80000000u;
-}
-
-__global__ void __launch_bounds__(kTopThreads) top_blocks_kernel(const SelectParams p) {
-    __shared__ int hist[256];
-    __shared__ int warp_sum[2][kTopThreads / 32];
-    __shared__ int s_digit, s_left;
+// The top_k of a (sequence, KV head): one CTA, each thread with neighbouring keys, in registers (K of them) or read anew
+// (K = 0).  The key of the last block taken is found two bits at a time below the bits that all keys share: the largest
+// value that at least `want` keys reach.  One scan then gives every taken block its place.
+template <int THREADS, int K>
+__global__ void __launch_bounds__(THREADS) top_blocks_kernel(const SelectParams p) {
+    constexpr int W = THREADS / 32;
+    __shared__ uint2 s_sum[2][W];
     griddep_wait();
     griddep_launch_dependents();
     const int h = blockIdx.x, s = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -399,75 +476,140 @@ __global__ void __launch_bounds__(kTopThreads) top_blocks_kernel(const SelectPar
     int32_t* out = p.selected + r * p.top_k;
     if (nb == 0 && h == 0 && tid == 0) flag_error(p.err, PA_DEV_ERR_CTX);
     if (nb <= p.top_k) {
-        for (int i = tid; i < p.top_k; i += kTopThreads) out[i] = i < nb ? i : -1;
+        for (int i = tid; i < p.top_k; i += THREADS) out[i] = i < nb ? i : -1;
         return;
     }
-    const float* keys = p.keys + r * p.stride;
-    auto key = [&](int b) -> uint32_t {
-        return b < p.sink || b >= nb - p.recent ? 0xffffffffu : ordered(keys[b]);
-    };
-    uint32_t prefix = 0;
-    int left = p.top_k;  // keys still to take among those that share the prefix
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        hist[tid] = 0;
-        __syncthreads();
-        for (int b = tid; b < nb; b += kTopThreads) {
-            const uint32_t k = key(b);
-            if (shift == 24 || k >> (shift + 8) == prefix >> (shift + 8)) atomicAdd(&hist[k >> shift & 255], 1);
-        }
-        __syncthreads();
-        // keys with a larger digit than tid's
-        int v = hist[255 - tid];
-        const int own_count = v;
+    const uint32_t* keys = p.keys + r * p.stride;
+    const int n = ((nb + THREADS - 1) / THREADS + 3) & ~3;  // keys per thread, in fours (the row is padded to a four)
+    const int b0 = tid * n;
+    // Keys that do not compete count as 0, below every score: blocks kept anyway, places past the context.
+    auto masked = [&](uint32_t k, int b) -> uint32_t { return b < p.sink || b >= nb - p.recent ? 0u : k; };
+    uint32_t reg[K ? K : 1];
+    if constexpr (K > 0) {
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, v, o);
-            if (lane >= o) v += u;
+        for (int i = 0; i < K; i += 4) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (i < n && b0 + i < nb) v = *reinterpret_cast<const uint4*>(keys + b0 + i);
+            reg[i] = masked(v.x, b0 + i);
+            reg[i + 1] = masked(v.y, b0 + i + 1);
+            reg[i + 2] = masked(v.z, b0 + i + 2);
+            reg[i + 3] = masked(v.w, b0 + i + 3);
         }
-        if (lane == 31) warp_sum[0][warp] = v;
-        __syncthreads();
-        int before = 0;
-        for (int w = 0; w < warp; ++w) before += warp_sum[0][w];
-        const int above = before + v - own_count;
-        if (above < left && above + own_count >= left) {
-            s_digit = 255 - tid;
-            s_left = left - above;
-        }
-        __syncthreads();
-        prefix |= (uint32_t)s_digit << shift;
-        left = s_left;
-        __syncthreads();
     }
-    int taken = 0, ties = 0;  // listed, and equal keys met, before the chunk
-    for (int b0 = 0; b0 < nb; b0 += kTopThreads) {
-        const int b = b0 + tid;
-        const uint32_t k = b < nb ? key(b) : 0;
-        const bool eq = b < nb && k == prefix;
-        const unsigned me = __ballot_sync(0xffffffffu, eq);
-        if (lane == 0) warp_sum[0][warp] = __popc(me);
-        __syncthreads();
-        int e = ties + __popc(me & ((1u << lane) - 1u));
-        for (int w = 0; w < kTopThreads / 32; ++w) {
-            if (w < warp) e += warp_sum[0][w];
-            ties += warp_sum[0][w];
+    // f(key, block) for each of this thread's keys
+    auto each = [&](auto f) {
+        if constexpr (K > 0) {
+#pragma unroll
+            for (int i = 0; i < K; i += 4)
+                if (i < n) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) f(reg[i + j], b0 + i + j);
+                }
+        } else {
+            for (int i = 0; i < n && b0 + i < nb; ++i) f(masked(keys[b0 + i], b0 + i), b0 + i);
         }
-        const bool take = b < nb && (k > prefix || (eq && e < left));
-        const unsigned mt = __ballot_sync(0xffffffffu, take);
-        if (lane == 0) warp_sum[1][warp] = __popc(mt);
+    };
+    int turn = 0;
+    // sums over the CTA of two words, by one barrier
+    auto sum2 = [&](uint32_t a, uint32_t b) -> uint2 {
+        a = __reduce_add_sync(0xffffffffu, a);
+        b = __reduce_add_sync(0xffffffffu, b);
+        if (lane == 0) s_sum[turn][warp] = make_uint2(a, b);
         __syncthreads();
-        int at = taken + __popc(mt & ((1u << lane) - 1u));
-        for (int w = 0; w < kTopThreads / 32; ++w) {
-            if (w < warp) at += warp_sum[1][w];
-            taken += warp_sum[1][w];
+        const uint2 v = lane < W ? s_sum[turn][lane] : make_uint2(0, 0);
+        turn ^= 1;
+        return make_uint2(__reduce_add_sync(0xffffffffu, v.x), __reduce_add_sync(0xffffffffu, v.y));
+    };
+    const uint32_t want = (uint32_t)(p.top_k - p.sink - p.recent);  // of the keys that compete, fewer than there are
+    uint32_t cut = 0xffffffffu, left = 0;                           // taken: keys above cut, `left` equal ones
+    if (want > 0) {
+        uint32_t lo = 0xffffffffu, hi = 0;
+        each([&](uint32_t k, int) {
+            if (k) lo = min(lo, k);
+            hi = max(hi, k);
+        });
+        lo = __reduce_min_sync(0xffffffffu, lo);
+        hi = __reduce_max_sync(0xffffffffu, hi);
+        if (lane == 0) s_sum[turn][warp] = make_uint2(lo, hi);
+        __syncthreads();
+        const uint2 v = lane < W ? s_sum[turn][lane] : make_uint2(0xffffffffu, 0);
+        turn ^= 1;
+        lo = __reduce_min_sync(0xffffffffu, v.x);
+        hi = __reduce_max_sync(0xffffffffu, v.y);
+        // bits from `shift` on are the same in all keys
+        int shift = (33 - __clz(lo ^ hi)) & ~1;
+        cut = shift < 32 ? hi >> shift << shift : 0;
+        bool exact = false;  // just `want` keys reach cut
+        while (shift > 0 && !exact) {
+            shift -= 2;
+            const uint32_t c1 = cut + (1u << shift), c2 = cut + (2u << shift), c3 = cut + (3u << shift);
+            uint32_t n1 = 0, n2 = 0, n3 = 0;
+            each([&](uint32_t k, int) {
+                n1 += k >= c1;
+                n2 += k >= c2;
+                n3 += k >= c3;
+            });
+            uint32_t t1, t2, t3;
+            if constexpr (K > 0) {  // counts up to 32768 each
+                const uint2 t = sum2(n1 | n2 << 16, n3);
+                t1 = t.x & 0xffffu;
+                t2 = t.x >> 16;
+                t3 = t.y;
+            } else {
+                const uint2 t = sum2(n1, n2);
+                t1 = t.x;
+                t2 = t.y;
+                t3 = sum2(n3, 0).x;
+            }
+            const uint32_t reach = t3 >= want ? t3 : t2 >= want ? t2 : t1;
+            if (reach >= want) {
+                cut = t3 >= want ? c3 : t2 >= want ? c2 : c1;
+                exact = reach == want;
+            }
         }
-        if (take) out[at] = b;
+        if (exact) {
+            cut -= 1;  // all that reach it are taken
+        } else {
+            uint32_t above = 0;
+            each([&](uint32_t k, int) { above += k > cut; });
+            left = want - sum2(above, 0).x;
+        }
     }
+    // places: blocks kept and keys above cut before this thread's, and equal ones, of which `left` count
+    uint32_t sure = 0, ties = 0;
+    each([&](uint32_t k, int b) {
+        sure += b < p.sink || (b >= nb - p.recent && b < nb) || (k > cut && k != 0);
+        ties += k == cut && left > 0;
+    });
+    uint32_t a = sure, t = ties;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_up_sync(0xffffffffu, t, o);
+        if (lane >= o) {
+            a += x;
+            t += y;
+        }
+    }
+    if (lane == 31) s_sum[turn][warp] = make_uint2(a, t);
+    __syncthreads();
+    const uint2 v = lane < W ? s_sum[turn][lane] : make_uint2(0, 0);
+    a += __reduce_add_sync(0xffffffffu, lane < warp ? v.x : 0u) - sure;
+    t += __reduce_add_sync(0xffffffffu, lane < warp ? v.y : 0u) - ties;
+    each([&](uint32_t k, int b) {
+        const bool is_sure = b < p.sink || (b >= nb - p.recent && b < nb) || (k > cut && k != 0);
+        const bool tie = k == cut && left > 0;
+        if (is_sure || (tie && t < left)) out[a + min(t, left)] = b;
+        a += is_sure;
+        t += tie;
+    });
 }
+
+// Keys of a row, in whole vectors of four.
+static int64_t key_stride(int max_ctx, int B) { return (((int64_t)max_ctx + B - 1) / B + 3) & ~int64_t(3); }
 
 size_t select_workspace_bytes(int N, int H_kv, int max_ctx, int B) {
     if (N <= 0 || N > 65535 || H_kv <= 0 || H_kv > 65535 || max_ctx <= 0 || (B != 8 && B != 16 && B != 32)) return 0;
-    const size_t stride = ((size_t)max_ctx + B - 1) / B;
-    return (size_t)N * H_kv * stride * sizeof(float);
+    return (size_t)N * H_kv * (size_t)key_stride(max_ctx, B) * sizeof(uint32_t);
 }
 
 pa_status launch_select(const SelectArgs& a) {
@@ -478,8 +620,8 @@ pa_status launch_select(const SelectArgs& a) {
     p.box_scales = static_cast<const uint8_t*>(a.sum_scales);
     p.tables = a.tables;
     p.ctx_lens = a.ctx_lens;
-    p.keys = static_cast<float*>(a.workspace);
-    p.stride = ((int64_t)a.max_ctx + a.B - 1) / a.B;
+    p.keys = static_cast<uint32_t*>(a.workspace);
+    p.stride = key_stride(a.max_ctx, a.B);
     p.H_kv = a.H_kv;
     p.G = a.H_q / a.H_kv;
     p.lgB = a.B == 8 ? 3 : a.B == 16 ? 4 : 5;
@@ -490,18 +632,33 @@ pa_status launch_select(const SelectArgs& a) {
     p.sink = a.sink;
     p.recent = a.recent;
     p.err = a.dev_err;
-    const int64_t nb = std::min<int64_t>(p.stride, a.MB);
+    const int64_t nb = std::min<int64_t>(((int64_t)a.max_ctx + a.B - 1) / a.B, a.MB);  // the longest context's
     if (nb > a.top_k) {
-        const unsigned gx = (unsigned)((nb + 16 * kScoreWarps - 1) / (16 * kScoreWarps));
+        // Tiles per warp: the query is made into integers once per warp, so a warp takes more than one tile as soon as
+        // there are more than fill the device.
+        const int64_t tiles = (nb + 15) / 16, fill = (int64_t)sm_count() * kScoreFill;
+        const int per_warp = (int)std::min<int64_t>(kScoreTiles, std::max<int64_t>(1, tiles * a.N * a.H_kv / fill));
+        const int64_t per_cta = (int64_t)kScoreWarps * per_warp;
         auto kern = a.q_dtype == PA_BF16 ? (a.D == 128 ? score_kernel<__nv_bfloat16, 128> : score_kernel<__nv_bfloat16, 64>)
                                          : (a.D == 128 ? score_kernel<__half, 128> : score_kernel<__half, 64>);
-        const cudaError_t e = launch_kernel(kern, dim3(gx, (unsigned)a.H_kv, (unsigned)a.N), dim3(kScoreWarps * 32), 0,
-                                            a.stream, p);
+        const cudaError_t e = launch_kernel(kern, dim3((unsigned)((tiles + per_cta - 1) / per_cta), (unsigned)a.H_kv,
+                                                       (unsigned)a.N),
+                                            dim3(kScoreWarps * 32), 0, a.stream, p, per_warp);
         count_launch();
         if (e != cudaSuccess) return cuda_fail(e, "score launch");
     }
-    const cudaError_t e = launch_kernel(top_blocks_kernel, dim3((unsigned)a.H_kv, (unsigned)a.N), dim3(kTopThreads), 0,
-                                        a.stream, p);
+    // keys in registers up to 16 per thread (32 spill)
+    void (*top)(SelectParams) = top_blocks_kernel<1024, 0>;
+    int threads = 1024;
+    if (nb <= 256 * 8) {
+        top = top_blocks_kernel<256, 8>;
+        threads = 256;
+    } else if (nb <= 1024 * 8) {
+        top = top_blocks_kernel<1024, 8>;
+    } else if (nb <= 1024 * 16) {
+        top = top_blocks_kernel<1024, 16>;
+    }
+    const cudaError_t e = launch_kernel(top, dim3((unsigned)a.H_kv, (unsigned)a.N), dim3((unsigned)threads), 0, a.stream, p);
     count_launch();
     return e == cudaSuccess ? PA_OK : cuda_fail(e, "top_blocks launch");
 }
