@@ -312,7 +312,7 @@ struct SelectParams {
     const int32_t* ctx_lens;
     uint32_t* keys;  // [N][H_kv][stride], ordered as the scores
     int64_t stride;
-    int H_kv, G, lgB, MB, NB, max_ctx, top_k, sink, recent;
+    int N, H_kv, G, lgB, MB, NB, max_ctx, top_k, sink, recent;
     int* err;
 };
 
@@ -328,12 +328,10 @@ __device__ __forceinline__ uint32_t ordered(float x) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Scores: mma.sync m16n8k16 with 16 blocks on M and the query heads of the KV head on N; a warp takes a tile of 16 blocks
-// after another.  max(q lo, q hi) is q hi for q >= 0 and q lo below, so a box's score is one product of length 2 D,
+// Scores: mma.sync m16n8k16 with 16 blocks on M and the query heads of the KV head on N.  max(q lo, q hi) is q hi for q >= 0 and q lo below, so a box's score is one product of length 2 D,
 // [max(q, 0), min(q, 0)] . [hi, lo]; box and query integers are exact in fp16.
 constexpr int kScoreWarps = 8;
-constexpr int kScoreFill = 24;   // warps of an SM that the tiles are spread over first
-constexpr int kScoreTiles = 8;   // tiles of a warp at most
+constexpr int kScoreCtas = 2;  // per SM
 
 // Four 8-bit integers as two fp16 pairs: v + 128 in the low byte of 0x6400 is 1024 + 128 + v.
 __device__ __forceinline__ void int8x4_to_f16(uint32_t x, uint32_t& a, uint32_t& b) {
@@ -345,29 +343,89 @@ __device__ __forceinline__ void int8x4_to_f16(uint32_t x, uint32_t& a, uint32_t&
     b = *reinterpret_cast<const uint32_t*>(&h1);
 }
 
+// Tiles of each row of a sequence with something to choose.
+__device__ __forceinline__ int row_tiles(const SelectParams& p, int s, int& nb) {
+    nb = s < p.N ? context_blocks(p, s) : 0;
+    return nb > p.top_k ? (nb + 15) / 16 : 0;
+}
+
+// The tiles of all rows -- (sequence, KV head) -- in order are cut into runs of equal length, one per warp.  While a tile
+// is scored, the next one's boxes are on their way, and the block ids of the one after that.
 template <typename T, int D>
-__global__ void __launch_bounds__(kScoreWarps * 32) score_kernel(const SelectParams p, int tiles_per_warp) {
+__global__ void __launch_bounds__(kScoreWarps * 32, kScoreCtas) score_kernel(const SelectParams p) {
     constexpr int NC = D / 64;  // 16-byte chunks of a lane: t4, t4 + 4 of each half of the box
     griddep_wait();
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31, g4 = lane >> 2, t4 = lane & 3;
-    const int h = blockIdx.y, s = blockIdx.z;
-    const int nb = context_blocks(p, s);
-    if (nb <= p.top_k) return;  // nothing to choose
-    int tile = blockIdx.x * (kScoreWarps * tiles_per_warp) + (threadIdx.x >> 5);
-    const int end = min((int)(blockIdx.x + 1) * (kScoreWarps * tiles_per_warp), (nb + 15) / 16);
-    if (tile >= end) return;
-    // block ids of this lane's rows of a tile: blocks g4 and g4 + 8
-    auto entry = [&](int t, int r) -> int {
-        const int b = 16 * t + g4 + 8 * r;
-        return t < end && b < nb ? p.tables[(int64_t)s * p.MB + b] : 0;
+    int64_t total = 0;
+    for (int s0 = 0; s0 < p.N; s0 += 32) {
+        int nb;
+        total += __reduce_add_sync(0xffffffffu, row_tiles(p, s0 + lane, nb));
+    }
+    total *= p.H_kv;
+    const int64_t warps = min((int64_t)gridDim.x * kScoreWarps, total);
+    const int64_t w = (int64_t)(threadIdx.x >> 5) * gridDim.x + blockIdx.x;  // neighbouring runs on different SMs
+    if (w >= warps) return;
+    const int64_t u0 = total * w / warps;
+    int left = (int)(total * (w + 1) / warps - u0);
+
+    // A tile of the run, and this lane's block ids in it: blocks g4 and g4 + 8.
+    struct Pos {
+        int s, h, t, tiles, nb, blk[2];
     };
-    int blk[2] = {entry(tile, 0), entry(tile, 1)};
-    // the query integers of head g4, in the order of the box's bytes: word w of chunk c holds channels 64 c + 16 t4 +
-    // 4 w on, the k-columns 2 t4, 2 t4 + 1, 2 t4 + 8, 2 t4 + 9 of k-step (c, w)
-    uint32_t qi[NC][8];
-    float f0, f1;  // units of heads 2 t4 and 2 t4 + 1
+    auto look_up = [&](Pos& x) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int b = 16 * x.t + g4 + 8 * r;
+            x.blk[r] = b < x.nb ? p.tables[(int64_t)x.s * p.MB + b] : 0;
+        }
+    };
+    auto step = [&](Pos x) -> Pos {  // the run's next tile after x
+        if (++x.t == x.tiles) {
+            x.t = 0;
+            if (++x.h == p.H_kv) {
+                x.h = 0;
+                do x.tiles = row_tiles(p, ++x.s, x.nb);
+                while (x.tiles == 0);  // (ends: the run has tiles left)
+            }
+        }
+        look_up(x);
+        return x;
+    };
+    Pos cur;
     {
+        int64_t before = 0;
+        for (int s0 = 0;; s0 += 32) {  // (ends: u0 < total)
+            int nb;
+            const int n = row_tiles(p, s0 + lane, nb);
+            int v = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += x;
+            }
+            const int64_t hi = before + (int64_t)v * p.H_kv;
+            const unsigned hit = __ballot_sync(0xffffffffu, u0 < hi);
+            if (hit) {
+                const int src = __ffs(hit) - 1;
+                cur.s = s0 + src;
+                cur.tiles = __shfl_sync(0xffffffffu, n, src);
+                cur.nb = __shfl_sync(0xffffffffu, nb, src);
+                const int64_t at = u0 - __shfl_sync(0xffffffffu, hi, src) + (int64_t)cur.tiles * p.H_kv;
+                cur.h = (int)(at / cur.tiles);
+                cur.t = (int)(at - (int64_t)cur.h * cur.tiles);
+                break;
+            }
+            before = __shfl_sync(0xffffffffu, hi, 31);
+        }
+        look_up(cur);
+    }
+
+    // The query integers of head g4, in the order of the box's bytes: word w of chunk c holds channels 64 c + 16 t4 + 4 w
+    // on, the k-columns 2 t4, 2 t4 + 1, 2 t4 + 8, 2 t4 + 9 of k-step (c, w).
+    uint32_t qi[NC][8];
+    float f0 = 0.f, f1 = 0.f;  // units of heads 2 t4 and 2 t4 + 1
+    auto load_query = [&](int s, int h) {
         float m = 0.f;
 #pragma unroll
         for (int c = 0; c < NC; ++c)
@@ -405,38 +463,43 @@ __global__ void __launch_bounds__(kScoreWarps * 32) score_kernel(const SelectPar
                 const float2 x = Mma<T>::unpack(qi[c][i]);
                 qi[c][i] = Mma<__half>::pack(integer(x.x), integer(x.y));
             }
-    }
-    uint32_t* keys = p.keys + ((int64_t)s * p.H_kv + h) * p.stride;
-    for (; tile < end; tile += kScoreWarps) {
-        bool good[2];
-        int64_t row[2];
+    };
+    // a tile's boxes: [block g4, g4 + 8][lo, hi][chunk], and the units of the two blocks (0: no such block)
+    struct Tile {
+        uint4 v[2][2][NC];
+        float unit[2];
+    };
+    auto load = [&](const Pos& x, Tile& t) {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-            good[r] = (unsigned)blk[r] < (unsigned)p.NB;
-            if (!good[r] && t4 == 0 && h == 0) flag_error(p.err, PA_DEV_ERR_BLOCK);
-            row[r] = (int64_t)(good[r] ? blk[r] : 0) * p.H_kv + h;
-        }
-        uint4 v[2][2][NC];  // [block][lo, hi][chunk]
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
+            const bool good = (unsigned)x.blk[r] < (unsigned)p.NB;
+            if (!good && t4 == 0 && x.h == 0) flag_error(p.err, PA_DEV_ERR_BLOCK);
+            const int64_t row = (int64_t)(good ? x.blk[r] : 0) * p.H_kv + x.h;
 #pragma unroll
             for (int k = 0; k < 2; ++k)
 #pragma unroll
                 for (int c = 0; c < NC; ++c)
-                    v[r][k][c] = reinterpret_cast<const uint4*>(p.boxes + (row[r] * 2 + k) * D + 64 * c)[t4];
-        float unit[2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            unit[r] = pow2i(scale_of(p.box_scales[row[r]]));
-            blk[r] = entry(tile + kScoreWarps, r);
+                    t.v[r][k][c] = reinterpret_cast<const uint4*>(p.boxes + (row * 2 + k) * D + 64 * c)[t4];
+            t.unit[r] = good ? pow2i(scale_of(p.box_scales[row])) : 0.f;
         }
+    };
+    Tile tile;
+    load(cur, tile);
+    load_query(cur.s, cur.h);
+    Pos nxt = cur;
+    if (left > 1) nxt = step(cur);
+    for (; left > 0; --left) {
+        Tile next;
+        Pos after = nxt;
+        if (left > 1) load(nxt, next);
+        if (left > 2) after = step(nxt);
         float acc[2][4] = {};
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
-                const uint32_t w0[4] = {v[0][k][c].x, v[0][k][c].y, v[0][k][c].z, v[0][k][c].w};
-                const uint32_t w1[4] = {v[1][k][c].x, v[1][k][c].y, v[1][k][c].z, v[1][k][c].w};
+                const uint4 v0 = tile.v[0][k][c], v1 = tile.v[1][k][c];
+                const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
                     uint32_t a0, a1, a2, a3;
@@ -448,6 +511,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) score_kernel(const SelectPar
                                      k ? Pair<__half>::hi(x1, 0) : Pair<__half>::lo(x1, 0));
                 }
             }
+        uint32_t* keys = p.keys + ((int64_t)cur.s * p.H_kv + cur.h) * p.stride;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             float y = -INFINITY;
@@ -455,19 +519,34 @@ __global__ void __launch_bounds__(kScoreWarps * 32) score_kernel(const SelectPar
             if (2 * t4 + 1 < p.G) y = fmaxf(y, (acc[0][2 * r + 1] + acc[1][2 * r + 1]) * f1);
             y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 1));
             y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 2));
-            const int b = 16 * tile + g4 + 8 * r;
-            if (t4 == 0 && b < nb) keys[b] = ordered(good[r] ? y * unit[r] : -INFINITY);
+            const int b = 16 * cur.t + g4 + 8 * r;
+            if (t4 == 0 && b < cur.nb) keys[b] = ordered(tile.unit[r] > 0.f ? y * tile.unit[r] : -INFINITY);
         }
+        if (left > 1 && (nxt.s != cur.s || nxt.h != cur.h)) load_query(nxt.s, nxt.h);
+        tile = next;
+        cur = nxt;
+        nxt = after;
     }
 }
 
 // The top_k of a (sequence, KV head): one CTA, each thread with neighbouring keys, in registers (K of them) or read anew
-// (K = 0).  The key of the last block taken is found two bits at a time below the bits that all keys share: the largest
-// value that at least `want` keys reach.  One scan then gives every taken block its place.
+// (K = 0).  The key of the last block taken is found by a histogram over the eight bits below those that all competing
+// keys share, then among the keys of one bin: ranked against one another where there are no more than threads' worth of
+// them, else by the next eight bits.  One scan then gives every taken block its place.
+constexpr int kBins = 256;
+
+// Key k competes and agrees with the prefix above its low `open` bits.
+__device__ __forceinline__ bool agree(uint32_t k, uint32_t prefix, int open) {
+    return k != 0 && (open == 32 || (k ^ prefix) >> open == 0);
+}
+
 template <int THREADS, int K>
 __global__ void __launch_bounds__(THREADS) top_blocks_kernel(const SelectParams p) {
     constexpr int W = THREADS / 32;
-    __shared__ uint2 s_sum[2][W];
+    static_assert(THREADS >= kBins, "a thread per bin");
+    __shared__ uint2 s_sum[W];
+    __shared__ uint32_t s_bin[kBins], s_list[kBins], s_warp[kBins / 32];
+    __shared__ uint32_t s_digit, s_above, s_count, s_cut, s_left;
     griddep_wait();
     griddep_launch_dependents();
     const int h = blockIdx.x, s = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -509,20 +588,11 @@ __global__ void __launch_bounds__(THREADS) top_blocks_kernel(const SelectParams 
             for (int i = 0; i < n && b0 + i < nb; ++i) f(masked(keys[b0 + i], b0 + i), b0 + i);
         }
     };
-    int turn = 0;
-    // sums over the CTA of two words, by one barrier
-    auto sum2 = [&](uint32_t a, uint32_t b) -> uint2 {
-        a = __reduce_add_sync(0xffffffffu, a);
-        b = __reduce_add_sync(0xffffffffu, b);
-        if (lane == 0) s_sum[turn][warp] = make_uint2(a, b);
-        __syncthreads();
-        const uint2 v = lane < W ? s_sum[turn][lane] : make_uint2(0, 0);
-        turn ^= 1;
-        return make_uint2(__reduce_add_sync(0xffffffffu, v.x), __reduce_add_sync(0xffffffffu, v.y));
-    };
-    const uint32_t want = (uint32_t)(p.top_k - p.sink - p.recent);  // of the keys that compete, fewer than there are
-    uint32_t cut = 0xffffffffu, left = 0;                           // taken: keys above cut, `left` equal ones
+    uint32_t want = (uint32_t)(p.top_k - p.sink - p.recent);  // of the keys that compete, fewer than there are
+    uint32_t cut = 0xffffffffu, ties_taken = 0;               // taken: keys above cut, the first ties_taken equal ones
     if (want > 0) {
+        if (tid < kBins) s_bin[tid] = 0;
+        if (tid == 0) s_count = 0;
         uint32_t lo = 0xffffffffu, hi = 0;
         each([&](uint32_t k, int) {
             if (k) lo = min(lo, k);
@@ -530,56 +600,86 @@ __global__ void __launch_bounds__(THREADS) top_blocks_kernel(const SelectParams 
         });
         lo = __reduce_min_sync(0xffffffffu, lo);
         hi = __reduce_max_sync(0xffffffffu, hi);
-        if (lane == 0) s_sum[turn][warp] = make_uint2(lo, hi);
+        if (lane == 0) s_sum[warp] = make_uint2(lo, hi);
         __syncthreads();
-        const uint2 v = lane < W ? s_sum[turn][lane] : make_uint2(0xffffffffu, 0);
-        turn ^= 1;
+        const uint2 v = lane < W ? s_sum[lane] : make_uint2(0xffffffffu, 0);
         lo = __reduce_min_sync(0xffffffffu, v.x);
         hi = __reduce_max_sync(0xffffffffu, v.y);
-        // bits from `shift` on are the same in all keys
-        int shift = (33 - __clz(lo ^ hi)) & ~1;
-        cut = shift < 32 ? hi >> shift << shift : 0;
-        bool exact = false;  // just `want` keys reach cut
-        while (shift > 0 && !exact) {
-            shift -= 2;
-            const uint32_t c1 = cut + (1u << shift), c2 = cut + (2u << shift), c3 = cut + (3u << shift);
-            uint32_t n1 = 0, n2 = 0, n3 = 0;
+        // the keys that compete agree above their low `open` bits with `prefix`
+        int open = 32 - __clz(lo ^ hi);
+        uint32_t prefix = hi;
+        while (true) {
+            const int shift = max(0, open - 8);
             each([&](uint32_t k, int) {
-                n1 += k >= c1;
-                n2 += k >= c2;
-                n3 += k >= c3;
+                if (agree(k, prefix, open)) atomicAdd(&s_bin[k >> shift & 255], 1u);
             });
-            uint32_t t1, t2, t3;
-            if constexpr (K > 0) {  // counts up to 32768 each
-                const uint2 t = sum2(n1 | n2 << 16, n3);
-                t1 = t.x & 0xffffu;
-                t2 = t.x >> 16;
-                t3 = t.y;
-            } else {
-                const uint2 t = sum2(n1, n2);
-                t1 = t.x;
-                t2 = t.y;
-                t3 = sum2(n3, 0).x;
+            __syncthreads();
+            // thread t: bin 255 - t, and the keys in higher bins
+            uint32_t mine = 0, x = 0;
+            if (tid < kBins) {
+                mine = x = s_bin[kBins - 1 - tid];
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+                    if (lane >= o) x += y;
+                }
+                if (lane == 31) s_warp[warp] = x;
             }
-            const uint32_t reach = t3 >= want ? t3 : t2 >= want ? t2 : t1;
-            if (reach >= want) {
-                cut = t3 >= want ? c3 : t2 >= want ? c2 : c1;
-                exact = reach == want;
+            __syncthreads();
+            if (tid < kBins) {
+                const uint32_t below = lane < warp ? s_warp[lane] : 0u;
+                const uint32_t above = x - mine + __reduce_add_sync(0xffffffffu, below);
+                if (above < want && above + mine >= want) {
+                    s_digit = kBins - 1 - tid;
+                    s_above = above;
+                    s_left = mine;
+                }
             }
-        }
-        if (exact) {
-            cut -= 1;  // all that reach it are taken
-        } else {
-            uint32_t above = 0;
-            each([&](uint32_t k, int) { above += k > cut; });
-            left = want - sum2(above, 0).x;
+            __syncthreads();
+            const uint32_t digit = s_digit, count = s_left;
+            want -= s_above;
+            prefix = (open == 32 ? 0u : prefix >> open << open) | digit << shift;
+            if (count == want) {  // the whole bin
+                cut = prefix ? prefix - 1 : 0;  // (a key that competes is above 0)
+                break;
+            }
+            open = shift;
+            if (shift == 0) {  // equal keys
+                cut = prefix;
+                ties_taken = want;
+                break;
+            }
+            if (count <= kBins) {
+                each([&](uint32_t k, int) {
+                    if (agree(k, prefix, shift)) s_list[atomicAdd(&s_count, 1u)] = k;
+                });
+                __syncthreads();
+                if (tid < (int)count) {
+                    const uint32_t k = s_list[tid];
+                    uint32_t above = 0, equal = 0;
+                    for (uint32_t i = 0; i < count; ++i) {
+                        above += s_list[i] > k;
+                        equal += s_list[i] == k;
+                    }
+                    if (above < want && above + equal >= want) {  // (equal keys write the same)
+                        s_cut = k;
+                        s_above = want - above;
+                    }
+                }
+                __syncthreads();
+                cut = s_cut;
+                ties_taken = s_above;
+                break;
+            }
+            if (tid < kBins) s_bin[tid] = 0;
+            __syncthreads();
         }
     }
-    // places: blocks kept and keys above cut before this thread's, and equal ones, of which `left` count
+    // places: blocks kept and keys above cut before this thread's, and equal ones, of which ties_taken count
     uint32_t sure = 0, ties = 0;
     each([&](uint32_t k, int b) {
-        sure += b < p.sink || (b >= nb - p.recent && b < nb) || (k > cut && k != 0);
-        ties += k == cut && left > 0;
+        sure += b < p.sink || (b >= nb - p.recent && b < nb) || k > cut;
+        ties += k == cut;
     });
     uint32_t a = sure, t = ties;
 #pragma unroll
@@ -590,15 +690,14 @@ __global__ void __launch_bounds__(THREADS) top_blocks_kernel(const SelectParams 
             t += y;
         }
     }
-    if (lane == 31) s_sum[turn][warp] = make_uint2(a, t);
+    if (lane == 31) s_sum[warp] = make_uint2(a, t);
     __syncthreads();
-    const uint2 v = lane < W ? s_sum[turn][lane] : make_uint2(0, 0);
-    a += __reduce_add_sync(0xffffffffu, lane < warp ? v.x : 0u) - sure;
-    t += __reduce_add_sync(0xffffffffu, lane < warp ? v.y : 0u) - ties;
+    const uint2 v = lane < warp ? s_sum[lane] : make_uint2(0, 0);
+    a += __reduce_add_sync(0xffffffffu, v.x) - sure;
+    t += __reduce_add_sync(0xffffffffu, v.y) - ties;
     each([&](uint32_t k, int b) {
-        const bool is_sure = b < p.sink || (b >= nb - p.recent && b < nb) || (k > cut && k != 0);
-        const bool tie = k == cut && left > 0;
-        if (is_sure || (tie && t < left)) out[a + min(t, left)] = b;
+        const bool is_sure = b < p.sink || (b >= nb - p.recent && b < nb) || k > cut, tie = k == cut;
+        if (is_sure || (tie && t < ties_taken)) out[a + min(t, ties_taken)] = b;
         a += is_sure;
         t += tie;
     });
@@ -622,6 +721,7 @@ pa_status launch_select(const SelectArgs& a) {
     p.ctx_lens = a.ctx_lens;
     p.keys = static_cast<uint32_t*>(a.workspace);
     p.stride = key_stride(a.max_ctx, a.B);
+    p.N = a.N;
     p.H_kv = a.H_kv;
     p.G = a.H_q / a.H_kv;
     p.lgB = a.B == 8 ? 3 : a.B == 16 ? 4 : 5;
@@ -634,16 +734,12 @@ pa_status launch_select(const SelectArgs& a) {
     p.err = a.dev_err;
     const int64_t nb = std::min<int64_t>(((int64_t)a.max_ctx + a.B - 1) / a.B, a.MB);  // the longest context's
     if (nb > a.top_k) {
-        // Tiles per warp: the query is made into integers once per warp, so a warp takes more than one tile as soon as
-        // there are more than fill the device.
-        const int64_t tiles = (nb + 15) / 16, fill = (int64_t)sm_count() * kScoreFill;
-        const int per_warp = (int)std::min<int64_t>(kScoreTiles, std::max<int64_t>(1, tiles * a.N * a.H_kv / fill));
-        const int64_t per_cta = (int64_t)kScoreWarps * per_warp;
+        const int64_t tiles = (nb + 15) / 16 * a.N * a.H_kv;
+        const unsigned grid = (unsigned)std::min<int64_t>((tiles + kScoreWarps - 1) / kScoreWarps,
+                                                          (int64_t)sm_count() * kScoreCtas);
         auto kern = a.q_dtype == PA_BF16 ? (a.D == 128 ? score_kernel<__nv_bfloat16, 128> : score_kernel<__nv_bfloat16, 64>)
                                          : (a.D == 128 ? score_kernel<__half, 128> : score_kernel<__half, 64>);
-        const cudaError_t e = launch_kernel(kern, dim3((unsigned)((tiles + per_cta - 1) / per_cta), (unsigned)a.H_kv,
-                                                       (unsigned)a.N),
-                                            dim3(kScoreWarps * 32), 0, a.stream, p, per_warp);
+        const cudaError_t e = launch_kernel(kern, dim3(grid), dim3(kScoreWarps * 32), 0, a.stream, p);
         count_launch();
         if (e != cudaSuccess) return cuda_fail(e, "score launch");
     }

@@ -242,6 +242,11 @@ def test_selection_flags():
     q = torch.randn(3, 4, D, generator=g).half()
     tables[1, 5], tables[1, 20], tables[2, 7] = 3 * nb, -1, 1 << 30
     check_select(q, box, by, tables, [nb * B] * 3, B, 16, 1, 1, H, flag=pa.PA_DEV_ERR_BLOCK)
+    # more bad entries than the list has room to leave out: the lowest of them are listed
+    for n in (nb - 20, nb - 17, nb - 14, nb - 3):
+        t = tables.clone()
+        t[0, 2: 2 + n] = -1
+        check_select(q, box, by, t, [nb * B] * 3, B, 18, 1, 1, H, flag=pa.PA_DEV_ERR_BLOCK)
     tables = torch.arange(3 * nb, dtype=torch.int32).view(3, nb)
     for bad in (0, -5, nb * B + 1):
         check_select(q, box, by, tables, [500, bad, 300], B, 16, 1, 1, H, flag=pa.PA_DEV_ERR_CTX, ctx_flag=(1,),
