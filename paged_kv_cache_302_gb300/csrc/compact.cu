@@ -28,20 +28,60 @@ struct CompactParams {
     int* err;
 };
 
-// The threads of a CTA are 2^lgw columns times the tokens of a quarter chunk, and each takes kMoveUnroll tokens of a
-// chunk.  While chunk c is stored, chunk c + 1 is on its way into registers and the positions of chunk c + 2 are looked
-// up.  One barrier per chunk separates its reads, all issued before, from its writes; four buffers of looked-up
-// positions, because a thread may be one barrier behind another.
+// A CTA's threads are 2^lgw columns times kMoveThreads / 2^lgw tokens, and each takes kMoveUnroll tokens of a chunk.  Chunks
+// go through a ring of shared-memory stages: kMoveStages - 1 of them are on their way while one is stored.  The rows that
+// tokens come from and go to (a list entry and two block-table entries each) are looked up kSpan tokens at a time, in
+// three steps during the first three chunks of the span before, so that no step waits for its own loads.  Every thread
+// stores what it copied itself; the one barrier per chunk puts all reads of a chunk before its first write.
 constexpr int kMoveThreads = 256;
 constexpr int kMoveUnroll = 4;
-constexpr int kMinWidth = 2;  // columns of a CTA: at least one 32-byte sector
-constexpr int kMoveCtas = 152 * 8;
-constexpr int kMaxChunk = kMoveThreads / kMinWidth * kMoveUnroll;
+constexpr int kMoveStages = 3;
+constexpr int kSpan = 1024;
+constexpr int kMinLgw = 2, kMaxLgw = 8;  // columns of a CTA: at least two 32-byte sectors
+constexpr int kLook = kSpan / kMoveThreads;
+constexpr int kMoveCtas = 152 * 2;  // as many as the columns are spread over
+constexpr size_t kMoveSmem = (size_t)kMoveStages * kMoveThreads * kMoveUnroll * 16 + 2 * kSpan * sizeof(int2);
+// the copies of chunk i + kMoveStages - 1 follow chunk i's barrier, the third step comes before that of a span's third
+static_assert(kSpan / ((kMoveThreads >> kMinLgw) * kMoveUnroll) >= kMoveStages + 1, "a span's rows are there in time");
+
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// A sequence's list.
+struct KeepList {
+    const int32_t* keep;
+    const int32_t* table;
+    int n, base, ctx, lgB, NB;
+
+    // Whether the list's token j moves.  `bad` receives the least j that is out of order or out of range.
+    __device__ __forceinline__ bool moves(int64_t j, int src, int before, int* bad) const {
+        if (j >= n) return false;
+        if (src <= before || src < 0 || src >= ctx) {
+            atomicMin(bad, (int)j);
+            return false;
+        }
+        return src != base + j && base + j < ctx;  // (the latter fails only behind an entry out of order)
+    }
+    // Rows (block * B + offset) that it comes from and goes to, of its block-table entries; (-1, -1) without a block.
+    __device__ __forceinline__ int2 rows(int64_t j, int src, int sb, int db, int* err) const {
+        const int B1 = (1 << lgB) - 1;
+        if ((unsigned)sb >= (unsigned)NB || (unsigned)db >= (unsigned)NB) {
+            flag_error(err, PA_DEV_ERR_BLOCK);
+            return make_int2(-1, -1);
+        }
+        return make_int2((sb << lgB) + (src & B1), (db << lgB) + ((base + (int)j) & B1));
+    }
+    __device__ __forceinline__ int block_from(int src) const { return table[src >> lgB]; }
+    __device__ __forceinline__ int block_to(int64_t j) const { return table[(base + (int)j) >> lgB]; }
+    __device__ __forceinline__ int source(int64_t j) const { return j < n ? keep[j] : 0; }
+    __device__ __forceinline__ int source_before(int64_t j) const { return j <= 0 ? base - 1 : j <= n ? keep[j - 1] : 0; }
+};
 
 template <bool kQuant>
-__global__ void __launch_bounds__(kMoveThreads) compact_kernel(const CompactParams p, int lgw) {
-    __shared__ int2 s_row[4][kMaxChunk];  // pool rows (block * B + offset) a token comes from (-1: stays) and goes to
-    __shared__ int s_bad;                 // first entry of the list that is out of order or out of range
+__global__ void __launch_bounds__(kMoveThreads, 3) compact_kernel(const CompactParams p, int lgw) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ int s_bad;  // first entry of the list that is out of order or out of range
     griddep_wait();
     griddep_launch_dependents();
     const int s = blockIdx.y, tid = threadIdx.x;
@@ -50,86 +90,143 @@ __global__ void __launch_bounds__(kMoveThreads) compact_kernel(const CompactPara
         if (blockIdx.x == 0 && tid == 0) flag_error(p.err, PA_DEV_ERR_CTX);
         return;
     }
-    const int n = k1 - k0, per = kMoveThreads >> lgw, chunk = per * kMoveUnroll;
-    const int tok = tid >> lgw, c = (blockIdx.x << lgw) + (tid & ((1 << lgw) - 1));
-    const bool mine = c < p.cols;
-    const int r = c / p.run;
-    const int64_t col = r * p.run_step + (int64_t)(c - r * p.run) * 16;
-    const bool scale_too = kQuant && mine && c == r * p.run;
-    const int runs = p.cols / p.run;
-    const int32_t* table = p.tables + (int64_t)s * p.MB;
-    const int32_t* keep = p.keep + k0;
-    const int B1 = (1 << p.lgB) - 1;
+    const KeepList list = {p.keep + k0, p.tables + (int64_t)s * p.MB, k1 - k0, base, ctx, p.lgB, p.NB};
+    const int n = list.n, B1 = (1 << p.lgB) - 1, runs = kQuant ? p.cols / p.run : 0;
+    if (tid == 0) s_bad = INT_MAX;
+    __syncthreads();
 
-    // looks up the rows of chunk i
-    auto look_up = [&](int i) {
+    if (kQuant && (int)blockIdx.x < runs) {
+        // Scale bytes, one CTA per (head, K or V): a thread per token, its bytes in registers over the barrier.
+        constexpr int kU = 4;
+        auto place = [&](int row) -> int64_t {
+            return (((int64_t)(row >> p.lgB) * runs + blockIdx.x) << p.lgB) + (row & B1);
+        };
+        for (int64_t j0 = 0; j0 < n; j0 += kMoveThreads * kU) {
+            int2 row[kU];
+            uint8_t v[kU];
+            int src[kU], sb[kU], db[kU];
+            bool go[kU];
 #pragma unroll
-        for (int x = 0; x < kMaxChunk / kMoveThreads; ++x) {
-            const int at = tid + x * kMoveThreads;
-            const int64_t j = (int64_t)i * chunk + at;
-            if (at >= chunk) break;
-            int2 row = make_int2(-1, -1);
-            if (j < n) {
-                const int src = keep[j], before = j ? keep[j - 1] : base - 1;
-                if (src <= before || src < 0 || src >= ctx) {
-                    atomicMin(&s_bad, (int)j);
-                } else if (src != base + j && base + j < ctx) {  // (not below src only behind an entry out of order)
-                    const int dst = base + (int)j;
-                    const int sb = table[src >> p.lgB], db = table[dst >> p.lgB];
-                    if ((unsigned)sb < (unsigned)p.NB && (unsigned)db < (unsigned)p.NB)
-                        row = make_int2((sb << p.lgB) + (src & B1), (db << p.lgB) + (dst & B1));
-                    else
-                        flag_error(p.err, PA_DEV_ERR_BLOCK);
-                }
+            for (int u = 0; u < kU; ++u) {
+                const int64_t j = j0 + u * kMoveThreads + tid;
+                src[u] = list.source(j);
+                go[u] = list.moves(j, src[u], list.source_before(j), &s_bad);
             }
-            s_row[i & 3][at] = row;
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                sb[u] = go[u] ? list.block_from(src[u]) : 0;
+                db[u] = go[u] ? list.block_to(j0 + u * kMoveThreads + tid) : 0;
+            }
+#pragma unroll
+            for (int u = 0; u < kU; ++u)
+                row[u] = go[u] ? list.rows(j0 + u * kMoveThreads + tid, src[u], sb[u], db[u], p.err) : make_int2(-1, -1);
+#pragma unroll
+            for (int u = 0; u < kU; ++u) v[u] = row[u].x >= 0 ? p.scales[place(row[u].x)] : (uint8_t)0;
+            __syncthreads();
+            const int bad = s_bad;
+#pragma unroll
+            for (int u = 0; u < kU; ++u)
+                if (row[u].x >= 0 && j0 + u * kMoveThreads + tid < bad) p.scales[place(row[u].y)] = v[u];
+            if (bad < j0 + kMoveThreads * kU) {
+                if (blockIdx.x == 0 && tid == 0) flag_error(p.err, PA_DEV_ERR_CTX);
+                return;
+            }
+            __syncthreads();  // (a thread ahead may lower s_bad for its next tokens)
         }
-    };
+        return;
+    }
+
+    const int per = kMoveThreads >> lgw, chunk = per * kMoveUnroll, tok = tid >> lgw;
+    const int c = (((int)blockIdx.x - runs) << lgw) + (tid & ((1 << lgw) - 1));
+    const bool mine = c < p.cols;
+    const int64_t col = (int64_t)(c / p.run) * p.run_step + (int64_t)(c % p.run) * 16;
+    const uint32_t ring = smem_addr(smem) + tid * 16;  // this thread's vectors: kMoveThreads vectors apart
+    int2* s_row = reinterpret_cast<int2*>(smem + (size_t)kMoveStages * kMoveThreads * kMoveUnroll * 16);
     auto place = [&](int row) -> int64_t {
         return (int64_t)(row >> p.lgB) * p.block_bytes + (row & B1) * p.token_step + col;
     };
-    auto scale_place = [&](int row) -> int64_t { return (((int64_t)(row >> p.lgB) * runs + r) << p.lgB) + (row & B1); };
-    auto load = [&](int i, uint4 (&v)[kMoveUnroll], uint32_t& sc) {
-        sc = 0;
+    auto vector = [&](int stage, int u) -> uint32_t {
+        return ring + (uint32_t)(stage * kMoveUnroll + u) * (kMoveThreads * 16);
+    };
+    auto row_of = [&](int64_t j) -> int2 { return s_row[j & (2 * kSpan - 1)]; };
+    auto copy = [&](int64_t j0, int stage) {  // the chunk from token j0 on
 #pragma unroll
         for (int u = 0; u < kMoveUnroll; ++u) {
-            const int src = s_row[i & 3][u * per + tok].x;
-            if (src < 0 || !mine) continue;
-            v[u] = *reinterpret_cast<const uint4*>(p.data + place(src));
-            if (scale_too) sc |= (uint32_t)p.scales[scale_place(src)] << (8 * u);
+            const int src = row_of(j0 + u * per + tok).x;
+            if (src >= 0 && mine) copy_async16(vector(stage, u), p.data + place(src));
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    int src[kLook], sb[kLook], db[kLook];
+    bool go[kLook];
+    int before[kLook];
+    auto read_entries = [&](int64_t j0) {  // of the span from token j0 on
+#pragma unroll
+        for (int x = 0; x < kLook; ++x) {
+            src[x] = list.source(j0 + x * kMoveThreads + tid);
+            before[x] = list.source_before(j0 + x * kMoveThreads + tid);
         }
     };
-
-    if (tid == 0) s_bad = INT_MAX;
+    auto read_blocks = [&](int64_t j0) {
+#pragma unroll
+        for (int x = 0; x < kLook; ++x) {
+            const int64_t j = j0 + x * kMoveThreads + tid;
+            go[x] = list.moves(j, src[x], before[x], &s_bad);
+            sb[x] = go[x] ? list.block_from(src[x]) : 0;
+            db[x] = go[x] ? list.block_to(j) : 0;
+        }
+    };
+    auto write_rows = [&](int64_t j0) {
+#pragma unroll
+        for (int x = 0; x < kLook; ++x) {
+            const int64_t j = j0 + x * kMoveThreads + tid;
+            s_row[j & (2 * kSpan - 1)] = go[x] ? list.rows(j, src[x], sb[x], db[x], p.err) : make_int2(-1, -1);
+        }
+    };
+    read_entries(0);
+    read_blocks(0);
+    write_rows(0);
     __syncthreads();
-    look_up(0);
-    look_up(1);
-    __syncthreads();
-    uint4 v[kMoveUnroll];
-    uint32_t sc;
-    load(0, v, sc);
-    for (int i = 0; (int64_t)i * chunk < n; ++i) {
-        uint4 next[kMoveUnroll];
-        uint32_t next_sc;
-        load(i + 1, next, next_sc);
-        look_up(i + 2);
-        __syncthreads();  // chunk i is read
-        const int64_t bad = s_bad, j0 = (int64_t)i * chunk;
+#pragma unroll
+    for (int i = 0; i < kMoveStages - 1; ++i) copy(i * chunk, i);
+    int stage = 0;
+    for (int64_t j0 = 0; j0 < n; j0 += chunk) {
+        const int at = (int)j0 & (kSpan - 1);  // in its span
+        const int64_t next = j0 - at + kSpan;
+        if (next < n) {
+            if (at == 0) read_entries(next);
+            if (at == chunk) read_blocks(next);
+        }
+        if (at == 2 * chunk) {
+            if (next >= n) {
+#pragma unroll
+                for (int x = 0; x < kLook; ++x) go[x] = false;  // the copies run past the list's end
+            }
+            write_rows(next);
+        }
+        asm volatile("cp.async.wait_group %0;" ::"n"(kMoveStages - 2) : "memory");
+        __syncthreads();  // the chunk is read
+        const int64_t bad = s_bad;
 #pragma unroll
         for (int u = 0; u < kMoveUnroll; ++u) {
-            const int2 row = s_row[i & 3][u * per + tok];
-            if (row.x < 0 || !mine || j0 + u * per + tok >= bad) continue;
-            *reinterpret_cast<uint4*>(p.data + place(row.y)) = v[u];
-            if (scale_too) p.scales[scale_place(row.y)] = (uint8_t)(sc >> (8 * u));
+            const int64_t j = j0 + u * per + tok;
+            const int2 row = row_of(j);
+            if (row.x < 0 || !mine || j >= bad) continue;
+            uint4 v;
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                         : "r"(vector(stage, u))
+                         : "memory");
+            *reinterpret_cast<uint4*>(p.data + place(row.y)) = v;
         }
         if (bad < j0 + chunk) {
             if (blockIdx.x == 0 && tid == 0) flag_error(p.err, PA_DEV_ERR_CTX);
-            return;
+            break;
         }
-#pragma unroll
-        for (int u = 0; u < kMoveUnroll; ++u) v[u] = next[u];
-        sc = next_sc;
+        copy(j0 + (kMoveStages - 1) * chunk, stage == 0 ? kMoveStages - 1 : stage - 1);
+        if (++stage == kMoveStages) stage = 0;
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 pa_status launch_compact(const CompactArgs& a) {
@@ -153,16 +250,18 @@ pa_status launch_compact(const CompactArgs& a) {
     p.run = quant ? a.D / 16 : p.cols;
     p.run_step = quant ? (int64_t)a.B * a.D : 0;
     p.token_step = quant ? a.D : row;
-    // Columns per CTA: a chunk no longer than the lists are on average, and, as far as a sector per token allows, enough
-    // CTAs to fill the device several times.
+    // Columns per CTA: a chunk no longer than the lists are on average, and, as far as two sectors per token allow, two
+    // CTAs per SM.
     const int64_t mean = a.T / a.N;
-    int lgw = 1;
-    while (lgw < 8 && (1 << lgw) < p.cols &&
+    int lgw = kMinLgw;
+    while (lgw < kMaxLgw && (1 << lgw) < p.cols &&
            ((int64_t)(kMoveThreads >> lgw) * kMoveUnroll > mean || ((int64_t)p.cols * a.N) >> lgw > kMoveCtas))
         ++lgw;
-    const int64_t gx = (p.cols + (1 << lgw) - 1) >> lgw;
-    const cudaError_t e = launch_kernel(quant ? compact_kernel<true> : compact_kernel<false>,
-                                        dim3((unsigned)gx, (unsigned)a.N), dim3(kMoveThreads), 0, a.stream, p, lgw);
+    const int64_t gx = ((p.cols + (1 << lgw) - 1) >> lgw) + (quant ? p.cols / p.run : 0);
+    auto kern = quant ? compact_kernel<true> : compact_kernel<false>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMoveSmem);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(compact)");
+    e = launch_kernel(kern, dim3((unsigned)gx, (unsigned)a.N), dim3(kMoveThreads), kMoveSmem, a.stream, p, lgw);
     count_launch();
     return e == cudaSuccess ? PA_OK : cuda_fail(e, "compact launch");
 }
