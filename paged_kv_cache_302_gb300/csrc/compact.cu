@@ -36,10 +36,10 @@ struct CompactParams {
 constexpr int kMoveThreads = 256;
 constexpr int kMoveUnroll = 4;
 constexpr int kMoveStages = 3;
-constexpr int kSpan = 1024;
-constexpr int kMinLgw = 2, kMaxLgw = 8;  // columns of a CTA: at least two 32-byte sectors
+constexpr int kSpan = 2048;
+constexpr int kMinLgw = 1, kMaxLgw = 8;  // columns of a CTA: at least one 32-byte sector
 constexpr int kLook = kSpan / kMoveThreads;
-constexpr int kMoveCtas = 152 * 2;  // as many as the columns are spread over
+constexpr int kMoveCtas = 152 * 5 / 2;  // as many as the columns are spread over
 constexpr size_t kMoveSmem = (size_t)kMoveStages * kMoveThreads * kMoveUnroll * 16 + 2 * kSpan * sizeof(int2);
 // the copies of chunk i + kMoveStages - 1 follow chunk i's barrier, the third step comes before that of a span's third
 static_assert(kSpan / ((kMoveThreads >> kMinLgw) * kMoveUnroll) >= kMoveStages + 1, "a span's rows are there in time");
@@ -79,7 +79,7 @@ struct KeepList {
 };
 
 template <bool kQuant>
-__global__ void __launch_bounds__(kMoveThreads, 3) compact_kernel(const CompactParams p, int lgw) {
+__global__ void __launch_bounds__(kMoveThreads, 2) compact_kernel(const CompactParams p, int lgw) {
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ int s_bad;  // first entry of the list that is out of order or out of range
     griddep_wait();
