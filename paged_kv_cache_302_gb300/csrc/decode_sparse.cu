@@ -25,6 +25,8 @@ constexpr int kUnitTok = 32;       // tokens of a unit: one pipeline stage
 constexpr int kSpThreads = 64;
 constexpr int kSpCtas16 = 4, kSpCtas8 = 7;  // CTAs per SM over 16-bit and over e4m3 rows
 constexpr int kSpMaxCtas = 152 * kSpCtas8;
+constexpr int kSpMaxCluster = 8;
+constexpr int kSpClusterRows = 152 * 3 / kSpMaxCluster;  // rows whose clusters the device holds at once
 constexpr int kMinUnits = 1;       // units a CTA takes at least
 constexpr int kJoinWarps = 8;
 
@@ -53,6 +55,7 @@ struct SpParams {
     float* part_m;     // [2 * CTAs][G]: part 2 c is of the row that CTA c continues, 2 c + 1 of the one it leaves unfinished
     float* part_l;
     float* part_acc;   // [2 * CTAs][G][D]
+    int cluster;       // CTAs per row where the parts are joined over a cluster
     uint64_t wait_ns;
     int* err;
 };
@@ -68,7 +71,8 @@ struct SpGeo {
     static constexpr int kCtas = kQuant ? kSpCtas8 : kSpCtas16;
     static constexpr int kStages = (233472 / kCtas - 1024 - 1024 - 16) / (int)kPerStage;
     static constexpr size_t kSmem = 1024 + (size_t)kStages * kPerStage + 16;
-    static_assert(kStages >= 2 && kCtas * (kSmem + 1024) <= 233472, "the CTAs of an SM fit its shared memory");
+    static constexpr size_t kShare = (2 * kMaxGroup + kMaxGroup * D) * sizeof(float);
+    static_assert(kSmem % 16 == 0 && kStages >= 2 && kCtas * (kSmem + 1024) <= 233472, "the CTAs of an SM fit its shared memory");
 };
 
 __device__ __forceinline__ uint4 sp_lds128(uint32_t a) {
@@ -84,6 +88,22 @@ __device__ __forceinline__ uint2 sp_lds64(uint32_t a) {
 __device__ __forceinline__ uint32_t sp_lds8(uint32_t a) {
     uint32_t v;
     asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
+}
+
+// All threads of a cluster's CTAs.  (Every wait before it has a limit, and every thread gets here.)
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
+// fp32 at shared-memory address `a` of the cluster's CTA `rank`.
+__device__ __forceinline__ float ld_cluster(uint32_t a, int rank) {
+    float v;
+    asm volatile(
+        "{\n\t.reg .b32 t;\n\tmapa.shared::cluster.u32 t, %1, %2;\n\tld.shared::cluster.f32 %0, [t];\n\t}"
+        : "=f"(v)
+        : "r"(a), "r"(rank)
+        : "memory");
     return v;
 }
 
@@ -128,7 +148,9 @@ struct Run {
     }
 };
 
-template <typename T, bool kQuant, int D, int LGB>
+// kCluster: a cluster of CTAs per row instead, each with an equal part of the list; the parts are joined over the
+// cluster's shared memory.
+template <typename T, bool kQuant, int D, int LGB, bool kCluster>
 __global__ void __launch_bounds__(kSpThreads) attend_sparse_kernel(const __grid_constant__ CUtensorMap tm,
                                                                    const SpParams p) {
     using Geo = SpGeo<kQuant, D>;
@@ -165,53 +187,77 @@ __global__ void __launch_bounds__(kSpThreads) attend_sparse_kernel(const __grid_
     griddep_wait();
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31;
-
-    if (producer) {
-        // ------------------------------------------------------------------ producer warp
-        int64_t total = 0;
-        for (int s0 = 0; s0 < p.N; s0 += 32) {
-            const int s = s0 + lane;
-            const int w = s < p.N ? row_units<LGB>(p, p.ctx_lens[s]) : 0;
-            if (s < p.N && w == 0 && blockIdx.x == 0) flag_error(p.err, PA_DEV_ERR_CTX);
-            total += __reduce_add_sync(0xffffffffu, w);
+    const float NEG_INF = -INFINITY;
+    // this CTA's part of its row for the cluster's join: maxima and sums of the query heads, then their outputs
+    float* share = reinterpret_cast<float*>(smem_raw + Geo::kSmem);
+    if constexpr (kCluster) {
+        const int ctx = p.ctx_lens[blockIdx.x / p.cluster / p.H_kv];
+        if (ctx < 1 || ctx > p.cap) {  // (the whole cluster returns)
+            if (threadIdx.x == 0 && blockIdx.x % (p.cluster * p.H_kv) == 0) flag_error(p.err, PA_DEV_ERR_CTX);
+            return;
         }
-        total *= p.H_kv;
-        const int64_t ctas = max((int64_t)1, min((int64_t)gridDim.x, total / kMinUnits));
-        const int64_t u0 = total * blockIdx.x / ctas, u1 = total * (blockIdx.x + 1) / ctas;
+    }
+
+    auto produce = [&]() {
+        // ------------------------------------------------------------------ producer warp
+        int64_t total = 0, ctas = 1, unit = 0;
         Run<LGB> run;
         run.cta = blockIdx.x;
-        run.left = blockIdx.x < ctas ? u1 - u0 : 0;
-        int64_t unit = u0;  // first unit of the run's current row from here on
-        if (run.left > 0) {
-            int64_t before = 0;
-            for (int s0 = 0;; s0 += 32) {  // (ends: u0 < total)
+        if constexpr (kCluster) {
+            const int row = blockIdx.x / p.cluster, rank = blockIdx.x % p.cluster;
+            // equal shares of whole units, of the list as it lies (an empty share is a list of padding)
+            const int share_len = ((p.top_k + p.cluster - 1) / p.cluster + BPS - 1) / BPS * BPS;
+            run.s = row / p.H_kv;
+            run.h = row % p.H_kv;
+            run.ctx = p.ctx_lens[run.s];
+            run.left = 0;
+            run.e = min(rank * share_len, p.top_k);
+            run.e_end = min(run.e + share_len, p.top_k);
+            run.part = 0;
+            run.first = true;
+            } else {
+            for (int s0 = 0; s0 < p.N; s0 += 32) {
                 const int s = s0 + lane;
-                const int c = s < p.N ? p.ctx_lens[s] : 0;
-                const int w = row_units<LGB>(p, c);
-                int v = w;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int x = __shfl_up_sync(0xffffffffu, v, o);
-                    if (lane >= o) v += x;
-                }
-                const int64_t hi = before + (int64_t)v * p.H_kv;
-                const unsigned hit = __ballot_sync(0xffffffffu, u0 < hi);
-                if (hit) {
-                    const int src = __ffs(hit) - 1;
-                    run.s = s0 + src;
-                    run.units = __shfl_sync(0xffffffffu, w, src);
-                    run.ctx = __shfl_sync(0xffffffffu, c, src);
-                    const int64_t at = u0 - __shfl_sync(0xffffffffu, hi, src) + (int64_t)run.units * p.H_kv;
-                    run.h = (int)(at / run.units);
-                    const int j = (int)(at - (int64_t)run.h * run.units);
-                    unit = u0 - j;
-                    run.enter(p, j, total, ctas, unit);
-                    break;
-                }
-                before = __shfl_sync(0xffffffffu, hi, 31);
+                const int w = s < p.N ? row_units<LGB>(p, p.ctx_lens[s]) : 0;
+                if (s < p.N && w == 0 && blockIdx.x == 0) flag_error(p.err, PA_DEV_ERR_CTX);
+                total += __reduce_add_sync(0xffffffffu, w);
             }
-        } else {
-            run.e = run.e_end = 0;
+            total *= p.H_kv;
+            ctas = max((int64_t)1, min((int64_t)gridDim.x, total / kMinUnits));
+            const int64_t u0 = total * blockIdx.x / ctas, u1 = total * (blockIdx.x + 1) / ctas;
+            run.left = blockIdx.x < ctas ? u1 - u0 : 0;
+            unit = u0;  // first unit of the run's current row from here on
+            if (run.left > 0) {
+                int64_t before = 0;
+                for (int s0 = 0;; s0 += 32) {  // (ends: u0 < total)
+                    const int s = s0 + lane;
+                    const int c = s < p.N ? p.ctx_lens[s] : 0;
+                    const int w = row_units<LGB>(p, c);
+                    int v = w;
+    #pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const int x = __shfl_up_sync(0xffffffffu, v, o);
+                        if (lane >= o) v += x;
+                    }
+                    const int64_t hi = before + (int64_t)v * p.H_kv;
+                    const unsigned hit = __ballot_sync(0xffffffffu, u0 < hi);
+                    if (hit) {
+                        const int src = __ffs(hit) - 1;
+                        run.s = s0 + src;
+                        run.units = __shfl_sync(0xffffffffu, w, src);
+                        run.ctx = __shfl_sync(0xffffffffu, c, src);
+                        const int64_t at = u0 - __shfl_sync(0xffffffffu, hi, src) + (int64_t)run.units * p.H_kv;
+                        run.h = (int)(at / run.units);
+                        const int j = (int)(at - (int64_t)run.h * run.units);
+                        unit = u0 - j;
+                        run.enter(p, j, total, ctas, unit);
+                        break;
+                    }
+                    before = __shfl_sync(0xffffffffu, hi, 31);
+                }
+            } else {
+                run.e = run.e_end = 0;
+            }
         }
         const uint64_t pol = policy_evict_first();
         int slot = 0;
@@ -280,7 +326,7 @@ __global__ void __launch_bounds__(kSpThreads) attend_sparse_kernel(const __grid_
             c.row = c.s = c.h = c.part = c.ctx = 0;
             c.entry = -1;
             c.first = c.last = false;
-            if (run.e >= run.e_end) {
+            if (run.e >= run.e_end && !(kCluster && run.first)) {
                 if (run.left <= 0) return c;
                 unit += run.units;
                 if (++run.h == p.H_kv) {
@@ -366,12 +412,11 @@ __global__ void __launch_bounds__(kSpThreads) attend_sparse_kernel(const __grid_
                 mbar_wait_bounded(full_s + 8 * i, (uint32_t)(m & 1), nullptr, kWaitLimitNs);
             }
         }
-        return;
-    }
+    };
 
     // ---------------------------------------------------------------------- consumer warp
+    auto consume = [&]() {
     const int g4 = lane >> 2, t4 = lane & 3;
-    const float NEG_INF = -INFINITY;
     float O[NT][4];
     uint32_t qf[NT][2];
     float m0 = NEG_INF, m1 = NEG_INF, l0 = 0.f, l1 = 0.f;
@@ -653,7 +698,17 @@ __global__ void __launch_bounds__(kSpThreads) attend_sparse_kernel(const __grid_
                 const float inv = L > 0.f || L != L ? 1.f / L : 0.f;  // an empty list: zeros
                 // element d(i, k): row k of the pair that this thread holds of tile i
                 auto d_of = [&](int i, int k) { return kQuant ? d0 + 2 * i + k : 16 * i + g4 + 8 * k; };
-                if (mt.part < 0) {
+                if constexpr (kCluster) {
+                    if (g4 == 0) {
+                        share[hd] = hh ? m1 : m0;
+                        share[kMaxGroup + hd] = L;
+                    }
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) {
+                        share[2 * kMaxGroup + hd * D + d_of(i, 0)] = O[i][hh];
+                        share[2 * kMaxGroup + hd * D + d_of(i, 1)] = O[i][2 + hh];
+                    }
+                } else if (mt.part < 0) {
                     const int64_t o = ((int64_t)mt.row * p.G + hd) * D;
 #pragma unroll
                     for (int i = 0; i < NT; ++i) {
@@ -688,6 +743,46 @@ __global__ void __launch_bounds__(kSpThreads) attend_sparse_kernel(const __grid_
             slot = 0;
             fphase ^= 1;
         }
+    }
+    };
+    if (producer)
+        produce();
+    else
+        consume();
+
+    if constexpr (kCluster) {
+        // every CTA of the cluster joins its slice of the row's outputs
+        __syncwarp();
+        cluster_sync();
+        const int row = blockIdx.x / p.cluster, rank = blockIdx.x % p.cluster;
+        const uint32_t at = smem_addr(share);
+        const int n = p.G * D;
+        for (int i = rank * kSpThreads + threadIdx.x; i < n; i += p.cluster * kSpThreads) {
+            const int g = i / D;
+            float m[kSpMaxCluster], M = NEG_INF, L = 0.f, o = 0.f;
+#pragma unroll
+            for (int c = 0; c < kSpMaxCluster; ++c) {
+                m[c] = c < p.cluster ? ld_cluster(at + 4 * g, c) : NEG_INF;
+                M = fmaxf(M, m[c]);
+            }
+            if (M > NEG_INF) {  // (else the list is empty)
+#pragma unroll
+                for (int c = 0; c < kSpMaxCluster; ++c) {
+                    if (c >= p.cluster) continue;
+                    const float f = fast_exp2(m[c] - M);
+                    L += f * ld_cluster(at + 4 * (kMaxGroup + g), c);
+                    o += f * ld_cluster(at + 4 * (2 * kMaxGroup + i), c);
+                }
+                o /= L;
+            }
+            const int64_t to = (int64_t)row * n + i;
+            if (p.out_dtype == PA_F32)
+                static_cast<float*>(p.out)[to] = o;
+            else
+                static_cast<T*>(p.out)[to] = from_float<T>(o);
+        }
+        __syncwarp();
+        cluster_sync();  // no CTA leaves while another reads its share
     }
 }
 
@@ -796,15 +891,36 @@ static pa_status run_sparse(const DecodeSparseArgs& a, const SpParams& p, const 
                                5, a.pool, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B);
     }
     if (st != PA_OK) return st;
-    auto kern = attend_sparse_kernel<T, kQuant, D, LGB>;
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Geo::kSmem);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(attend_sparse)");
-    const int grid = std::max(1, std::min(Geo::kCtas * sms, L.ctas));
-    e = launch_kernel(kern, dim3((unsigned)grid), dim3(kSpThreads), Geo::kSmem, a.stream, tm, p);
+    if (p.cluster) {
+        auto kern = attend_sparse_kernel<T, kQuant, D, LGB, true>;
+        constexpr size_t smem = Geo::kSmem + Geo::kShare;
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(attend_sparse)");
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)p.cluster;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(a.N * a.H_kv * p.cluster));
+        cfg.blockDim = dim3(kSpThreads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = a.stream;
+        cfg.attrs = attr;
+        cfg.numAttrs = pdl_enabled() ? 2 : 1;
+        e = cudaLaunchKernelEx(&cfg, kern, tm, p);
+    } else {
+        auto kern = attend_sparse_kernel<T, kQuant, D, LGB, false>;
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Geo::kSmem);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(attend_sparse)");
+        const int grid = std::max(1, std::min(Geo::kCtas * sms, L.ctas));
+        e = launch_kernel(kern, dim3((unsigned)grid), dim3(kSpThreads), Geo::kSmem, a.stream, tm, p);
+    }
     count_launch();
     return e == cudaSuccess ? PA_OK : cuda_fail(e, "attend_sparse launch");
 }
@@ -847,12 +963,14 @@ pa_status launch_decode_sparse(const DecodeSparseArgs& a) {
     p.wait_ns = wait_limit_ns();
     p.err = a.dev_err;
     const bool quant = a.kv_dtype == PA_E4M3;
+    const int64_t rows = (int64_t)a.N * a.H_kv;
+    p.cluster = rows <= kSpClusterRows && a.top_k * a.B >= 2 * kSpMaxCluster * kUnitTok ? kSpMaxCluster : 0;
     pa_status st;
     if (a.q_dtype == PA_BF16)
         st = quant ? run_sparse_shape<__nv_bfloat16, true>(a, p, L) : run_sparse_shape<__nv_bfloat16, false>(a, p, L);
     else
         st = quant ? run_sparse_shape<__half, true>(a, p, L) : run_sparse_shape<__half, false>(a, p, L);
-    if (st != PA_OK) return st;
+    if (st != PA_OK || p.cluster) return st;
     const unsigned grid = (unsigned)(((int64_t)a.N * a.H_q + kJoinWarps - 1) / kJoinWarps);
     auto join = a.out_dtype == PA_F32 ? (a.D == 128 ? join_sparse_kernel<float, 128> : join_sparse_kernel<float, 64>)
                 : a.out_dtype == PA_BF16
