@@ -76,31 +76,44 @@ struct SummaryParams {
     int* err;
 };
 
+// v 2^-e as an integer, rounded down or up, in the low bits of an fp32 number above 2^23 (|v 2^-e| < 2^22).
+__device__ __forceinline__ uint32_t int_down(float v, float inv) {
+    return __float_as_uint(__fmaf_rd(v, inv, 12582912.f));  // 1.5 * 2^23
+}
+__device__ __forceinline__ uint32_t int_up(float v, float inv) {
+    return __float_as_uint(__fmaf_ru(v, inv, 12582912.f));
+}
+
 // One lane's channels of one box: C channels from lo/hi (NaN where the channel has no value), the row's exponent over
 // its L lanes, 8-bit integers out.
 template <int L, int C>
-__device__ __forceinline__ void store_box(const float (&lo)[C], const float (&hi)[C], int8_t* row, int D, int sub,
-                                          uint8_t* scale, unsigned mask) {
+__device__ __forceinline__ void store_box(float (&lo)[C], float (&hi)[C], int8_t* row, int D, int sub, uint8_t* scale,
+                                          unsigned mask) {
     float m = 0.f;
+    bool none = false;
 #pragma unroll
-    for (int i = 0; i < C; ++i) m = fmaxf(m, fmaxf(fabsf(lo[i]), fabsf(hi[i])));
+    for (int i = 0; i < C; ++i) {
+        m = fmaxf(m, fmaxf(fabsf(lo[i]), fabsf(hi[i])));
+        none = none || lo[i] != lo[i];
+    }
 #pragma unroll
     for (int o = L / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(mask, m, o));
     const int e = int_exponent<7>(m);
-    const float inv = pow2i(-e);
+    const float inv = pow2i(-e), top = kBoxTop * pow2i(kScaleMax);
+    if (none || m > top) {  // rare: channels without a value, magnitudes past the largest box
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            lo[i] = lo[i] == lo[i] ? fminf(fmaxf(lo[i], -top), top) : 0.f;
+            hi[i] = hi[i] == hi[i] ? fminf(fmaxf(hi[i], -top), top) : 0.f;
+        }
+    }
     uint32_t wl[C / 4], wh[C / 4];
 #pragma unroll
     for (int i = 0; i < C / 4; ++i) {
-        wl[i] = wh[i] = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            // (what 127 2^40 does not hold saturates; a channel without a value is the box [0, 0])
-            const int a = max(__float2int_rd(fmaxf(lo[4 * i + j] * inv, -1000.f)), -kBoxTop);
-            const int b = min(__float2int_ru(fminf(hi[4 * i + j] * inv, 1000.f)), kBoxTop);
-            const bool some = lo[4 * i + j] == lo[4 * i + j];
-            wl[i] |= (uint32_t)((some ? min(a, kBoxTop) : 0) & 0xff) << (8 * j);
-            wh[i] |= (uint32_t)((some ? max(b, -kBoxTop) : 0) & 0xff) << (8 * j);
-        }
+        wl[i] = __byte_perm(__byte_perm(int_down(lo[4 * i], inv), int_down(lo[4 * i + 1], inv), 0x0040),
+                            __byte_perm(int_down(lo[4 * i + 2], inv), int_down(lo[4 * i + 3], inv), 0x0040), 0x5410);
+        wh[i] = __byte_perm(__byte_perm(int_up(hi[4 * i], inv), int_up(hi[4 * i + 1], inv), 0x0040),
+                            __byte_perm(int_up(hi[4 * i + 2], inv), int_up(hi[4 * i + 3], inv), 0x0040), 0x5410);
     }
     if constexpr (C == 8) {
         reinterpret_cast<uint2*>(row)[sub] = make_uint2(wl[0], wl[1]);
@@ -154,17 +167,26 @@ __global__ void __launch_bounds__(kSumThreads) summarize_kernel(const SummaryPar
                 sw[2 * j] = x.x;
                 sw[2 * j + 1] = x.y;
             }
-            auto exponent = [&](int t) { return scale_of((int)(sw[t / 4] >> (8 * (t & 3)) & 0xffu)); };
-            int top = kScaleMin, low = kScaleMax, last = 0;
+            // the largest and the least byte of the block's tokens (those past the last one repeat it)
+            uint32_t top2 = 0, low2 = 0x00ff00ffu;
+            if (nv < B) {
+                const uint32_t last = (uint32_t)sc[nv - 1] * 0x01010101u;
 #pragma unroll
-            for (int t = 0; t < B; ++t)
-                if (t < nv) {
-                    top = max(top, exponent(t));
-                    low = min(low, exponent(t));
-                    last = exponent(t);
+                for (int j = 0; j < B / 4; ++j) {
+                    const int in = min(max(nv - 4 * j, 0), 4);  // bytes of the word that count
+                    const uint32_t keep = in == 4 ? 0xffffffffu : (1u << (8 * in)) - 1u;
+                    sw[j] = (sw[j] & keep) | (last & ~keep);
                 }
-            if (top - low <= 15) {
-                // rows in units of the largest scale: e4m3 is a multiple of 2^-9, so down to 2^-15 of it fp16 is exact
+            }
+#pragma unroll
+            for (int j = 0; j < B / 4; ++j) {
+                const uint32_t even = sw[j] & 0x00ff00ffu, odd = sw[j] >> 8 & 0x00ff00ffu;
+                top2 = vmax_u16x2(top2, vmax_u16x2(even, odd));
+                low2 = vmin_u16x2(low2, vmin_u16x2(even, odd));
+            }
+            const int top = (int)max(top2 & 0xffffu, top2 >> 16), low = (int)min(low2 & 0xffffu, low2 >> 16);
+            if (top - low <= 14 && low >= kScaleMin + kScaleBias && top <= kScaleMax + kScaleBias) {
+                // rows in units of the largest scale: e4m3 is a multiple of 2^-9, so down to 2^-14 of it fp16 is exact
                 uint32_t a[8], z[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) a[j] = z[j] = 0x7fff7fffu;
@@ -177,13 +199,14 @@ __global__ void __launch_bounds__(kSumThreads) summarize_kernel(const SummaryPar
                             x[t] = reinterpret_cast<const uint4*>(k + min(t0 + t, nv - 1) * D)[sub];
 #pragma unroll
                         for (int t = 0; t < kSumBatch; ++t) {
-                            const int e = t0 + t < nv ? exponent(t0 + t) : last;
-                            const __half2 f = __float2half2_rn(pow2i(e - top));
+                            const int byte = (int)(sw[(t0 + t) / 4] >> (8 * (t & 3)) & 0xffu);
+                            const uint32_t f = (uint32_t)(byte - top + 15) * 0x04000400u;  // 2^(byte - top), twice
                             const uint32_t w[4] = {x[t].x, x[t].y, x[t].z, x[t].w};
 #pragma unroll
                             for (int j = 0; j < 8; ++j) {
                                 const uint32_t q = e4m3x2_to_f16x2(w[j / 2] >> (16 * (j & 1)));
-                                const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&q), f);
+                                const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&q),
+                                                          *reinterpret_cast<const __half2*>(&f));
                                 const uint32_t v = *reinterpret_cast<const uint32_t*>(&y);
                                 a[j] = Pair<__half>::lo(a[j], v);
                                 z[j] = Pair<__half>::hi(z[j], v);
@@ -191,7 +214,7 @@ __global__ void __launch_bounds__(kSumThreads) summarize_kernel(const SummaryPar
                         }
                     }
                 }
-                const float unit = pow2i(top);
+                const float unit = pow2i(top - kScaleBias);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const float2 f = Mma<__half>::unpack(a[j]), g = Mma<__half>::unpack(z[j]);
