@@ -30,7 +30,7 @@ __device__ __forceinline__ int int_exponent(float a) {
 
 // L lanes per (block, KV head), each with its own channels, walk the block's tokens.  Minima and maxima that start as
 // NaN ignore NaN elements: the instructions return the other operand.
-constexpr int kSumThreads = 256;
+constexpr int kSumThreads = 128;
 constexpr int kSumBatch = 8;  // tokens of a block on their way at a time
 
 // K rows of 16 bits: 8 channels per lane, minima and maxima in the rows' own type.
