@@ -353,8 +353,8 @@ __device__ __forceinline__ uint32_t ordered(float x) {
 
 // Scores: mma.sync m16n8k16 with 16 blocks on M and the query heads of the KV head on N.  max(q lo, q hi) is q hi for q >= 0 and q lo below, so a box's score is one product of length 2 D,
 // [max(q, 0), min(q, 0)] . [hi, lo]; box and query integers are exact in fp16.
-constexpr int kScoreWarps = 8;
-constexpr int kScoreCtas = 2;  // per SM
+constexpr int kScoreWarps = 4;
+constexpr int kScoreCtas = 4;  // per SM
 
 // Four 8-bit integers as two fp16 pairs: v + 128 in the low byte of 0x6400 is 1024 + 128 + v.
 __device__ __forceinline__ void int8x4_to_f16(uint32_t x, uint32_t& a, uint32_t& b) {
@@ -446,8 +446,8 @@ __global__ void __launch_bounds__(kScoreWarps * 32, kScoreCtas) score_kernel(con
 
     // The query integers of head g4, in the order of the box's bytes: word w of chunk c holds channels 64 c + 16 t4 + 4 w
     // on, the k-columns 2 t4, 2 t4 + 1, 2 t4 + 8, 2 t4 + 9 of k-step (c, w).
-    uint32_t qi[NC][8];
-    float f0 = 0.f, f1 = 0.f;  // units of heads 2 t4 and 2 t4 + 1
+    uint32_t up[NC][8], dn[NC][8];  // max(q, 0) and min(q, 0)
+    float f0 = 0.f, f1 = 0.f;       // units of heads 2 t4 and 2 t4 + 1
     auto load_query = [&](int s, int h) {
         float m = 0.f;
 #pragma unroll
@@ -458,16 +458,16 @@ __global__ void __launch_bounds__(kScoreWarps * 32, kScoreCtas) score_kernel(con
                 if (g4 < p.G)
                     v = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) +
                                                        (((int64_t)s * p.H_kv + h) * p.G + g4) * D + 64 * c + 16 * t4)[i];
-                qi[c][4 * i] = v.x;
-                qi[c][4 * i + 1] = v.y;
-                qi[c][4 * i + 2] = v.z;
-                qi[c][4 * i + 3] = v.w;
+                up[c][4 * i] = v.x;
+                up[c][4 * i + 1] = v.y;
+                up[c][4 * i + 2] = v.z;
+                up[c][4 * i + 3] = v.w;
             }
 #pragma unroll
         for (int c = 0; c < NC; ++c)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float2 f = Mma<T>::unpack(qi[c][i]);
+                const float2 f = Mma<T>::unpack(up[c][i]);
                 m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));  // (a NaN counts as nothing)
             }
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
@@ -483,56 +483,60 @@ __global__ void __launch_bounds__(kScoreWarps * 32, kScoreCtas) score_kernel(con
         for (int c = 0; c < NC; ++c)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float2 x = Mma<T>::unpack(qi[c][i]);
-                qi[c][i] = Mma<__half>::pack(integer(x.x), integer(x.y));
+                const float2 x = Mma<T>::unpack(up[c][i]);
+                const uint32_t q = Mma<__half>::pack(integer(x.x), integer(x.y));
+                up[c][i] = Pair<__half>::hi(q, 0);
+                dn[c][i] = Pair<__half>::lo(q, 0);
             }
     };
-    // a tile's boxes: [block g4, g4 + 8][lo, hi][chunk], and the units of the two blocks (0: no such block)
-    struct Tile {
-        uint4 v[2][2][NC];
-        float unit[2];
-    };
-    auto load = [&](const Pos& x, Tile& t) {
+    // A tile's boxes: [block g4, g4 + 8][lo, hi][chunk], and the units of the two blocks (0: no such block).  As soon as a
+    // piece has been multiplied, its registers receive the next tile's.
+    uint4 v[2][2][NC];
+    float unit[2], next_unit[2] = {0.f, 0.f};
+    const int8_t* box[2];
+    auto find = [&](const Pos& x, float (&unit)[2]) {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const bool good = (unsigned)x.blk[r] < (unsigned)p.NB;
             if (!good && t4 == 0 && x.h == 0) flag_error(p.err, PA_DEV_ERR_BLOCK);
             const int64_t row = (int64_t)(good ? x.blk[r] : 0) * p.H_kv + x.h;
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-#pragma unroll
-                for (int c = 0; c < NC; ++c)
-                    t.v[r][k][c] = reinterpret_cast<const uint4*>(p.boxes + (row * 2 + k) * D + 64 * c)[t4];
-            t.unit[r] = good ? pow2i(scale_of(p.box_scales[row])) : 0.f;
+            box[r] = p.boxes + row * 2 * D + 16 * t4;
+            unit[r] = good ? pow2i(scale_of(p.box_scales[row])) : 0.f;
         }
     };
-    Tile tile;
-    load(cur, tile);
+    auto load = [&](int k, int c) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) v[r][k][c] = *reinterpret_cast<const uint4*>(box[r] + k * D + 64 * c);
+    };
+    find(cur, unit);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int c = 0; c < NC; ++c) load(k, c);
     load_query(cur.s, cur.h);
     Pos nxt = cur;
     if (left > 1) nxt = step(cur);
     for (; left > 0; --left) {
-        Tile next;
         Pos after = nxt;
-        if (left > 1) load(nxt, next);
+        if (left > 1) find(nxt, next_unit);
         if (left > 2) after = step(nxt);
         float acc[2][4] = {};
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
-                const uint4 v0 = tile.v[0][k][c], v1 = tile.v[1][k][c];
-                const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
+                const uint32_t w0[4] = {v[0][k][c].x, v[0][k][c].y, v[0][k][c].z, v[0][k][c].w};
+                const uint32_t w1[4] = {v[1][k][c].x, v[1][k][c].y, v[1][k][c].z, v[1][k][c].w};
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
                     uint32_t a0, a1, a2, a3;
                     int8x4_to_f16(w0[w], a0, a2);
                     int8x4_to_f16(w1[w], a1, a3);
-                    const uint32_t x0 = qi[c][2 * w], x1 = qi[c][2 * w + 1];
                     // the query's negative half meets lo, its positive half hi
-                    Mma<__half>::run(acc[k], a0, a1, a2, a3, k ? Pair<__half>::hi(x0, 0) : Pair<__half>::lo(x0, 0),
-                                     k ? Pair<__half>::hi(x1, 0) : Pair<__half>::lo(x1, 0));
+                    const uint32_t* q = k ? up[c] : dn[c];
+                    Mma<__half>::run(acc[k], a0, a1, a2, a3, q[2 * w], q[2 * w + 1]);
                 }
+                if (left > 1) load(k, c);
             }
         uint32_t* keys = p.keys + ((int64_t)cur.s * p.H_kv + cur.h) * p.stride;
 #pragma unroll
@@ -543,10 +547,10 @@ __global__ void __launch_bounds__(kScoreWarps * 32, kScoreCtas) score_kernel(con
             y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 1));
             y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 2));
             const int b = 16 * cur.t + g4 + 8 * r;
-            if (t4 == 0 && b < cur.nb) keys[b] = ordered(tile.unit[r] > 0.f ? y * tile.unit[r] : -INFINITY);
+            if (t4 == 0 && b < cur.nb) keys[b] = ordered(unit[r] > 0.f ? y * unit[r] : -INFINITY);
+            unit[r] = next_unit[r];
         }
         if (left > 1 && (nxt.s != cur.s || nxt.h != cur.h)) load_query(nxt.s, nxt.h);
-        tile = next;
         cur = nxt;
         nxt = after;
     }
