@@ -17,6 +17,7 @@
 #include <type_traits>
 
 #include "quant.cuh"
+#include "runs.cuh"
 #include "tensor_map.h"
 
 namespace pa {
@@ -118,32 +119,27 @@ __device__ __forceinline__ int row_units(const SpParams& p, int ctx) {
 // The run of a CTA, walked chunk by chunk of at most 32 list entries.  Everything is uniform over the warp.
 template <int LGB>
 struct Run {
-    int s, h;              // row
-    int units;             // of a row of this sequence
+    int s, h;      // row
+    int units;     // of a row of this sequence
     int ctx;
-    int64_t left;          // units of the run from this segment's first on
-    int e, e_end;          // list entries of the segment still to come
+    int unit;      // the row's first
+    int left;      // units of the run behind this segment
+    int e, e_end;  // list entries of the segment still to come
     int part;
-    bool first;            // the next chunk is the segment's first
-    int cta;
-
-    __device__ __forceinline__ bool done() const { return left <= 0; }
+    bool first;    // the next chunk is the segment's first
 
     // Enters the segment that starts at unit j of the row and sets the row's cuts.
-    __device__ __forceinline__ void enter(const SpParams& p, int j, int64_t total, int64_t ctas, int64_t unit) {
+    __device__ __forceinline__ void enter(const SpParams& p, int j, const Cut& cut) {
         constexpr int kPerUnit = kUnitTok >> LGB;
+        const int cta = blockIdx.x;
         const bool to_end = units - j <= left;
-        const int j1 = to_end ? units : j + (int)left;
+        const int j1 = to_end ? units : j + left;
         part = j > 0 ? 2 * cta : to_end ? -1 : 2 * cta + 1;
         e = j * kPerUnit;
         e_end = to_end ? p.top_k : j1 * kPerUnit;  // (what stands behind the last unit is padding, or counts here)
         first = true;
-        if (j == 0 && (threadIdx.x & 31) == 0) {
-            // the CTA that takes a row's last unit: the one whose run [c total / ctas, ...) holds it
-            const int64_t last = unit + units - 1;
-            const int64_t c1 = ((last + 1) * ctas + total - 1) / total - 1;
-            p.cuts[(int64_t)s * p.H_kv + h] = to_end ? make_int2(-1, -1) : make_int2(cta, (int)c1);
-        }
+        if (j == 0 && (threadIdx.x & 31) == 0)
+            p.cuts[(int64_t)s * p.H_kv + h] = to_end ? make_int2(-1, -1) : make_int2(cta, cut.run_of(unit + units - 1));
         left -= j1 - j;
     }
 };
@@ -200,63 +196,39 @@ __global__ void __launch_bounds__(kSpThreads) attend_sparse_kernel(const __grid_
 
     auto produce = [&]() {
         // ------------------------------------------------------------------ producer warp
-        int64_t total = 0, ctas = 1, unit = 0;
         Run<LGB> run;
-        run.cta = blockIdx.x;
+        const auto units_of = [&](int s) { return row_units<LGB>(p, p.ctx_lens[s]); };
+        const RowScan<decltype(units_of)> scan(units_of, kCluster ? 0 : p.N, p.H_kv);
+        const int total = kCluster ? 1 : scan.total();
+        const int ctas = max(1, min((int)gridDim.x, total / kMinUnits));
+        const Cut cut(total, ctas);
+        run.e = run.e_end = run.left = 0;
+        run.first = false;
         if constexpr (kCluster) {
             const int row = blockIdx.x / p.cluster, rank = blockIdx.x % p.cluster;
             // equal shares of whole units, of the list as it lies (an empty share is a list of padding)
-            const int share_len = ((p.top_k + p.cluster - 1) / p.cluster + BPS - 1) / BPS * BPS;
+            const int len = ((p.top_k + p.cluster - 1) / p.cluster + BPS - 1) / BPS * BPS;
             run.s = row / p.H_kv;
             run.h = row % p.H_kv;
             run.ctx = p.ctx_lens[run.s];
-            run.left = 0;
-            run.e = min(rank * share_len, p.top_k);
-            run.e_end = min(run.e + share_len, p.top_k);
+            run.e = min(rank * len, p.top_k);
+            run.e_end = min(run.e + len, p.top_k);
             run.part = 0;
             run.first = true;
-            } else {
-            for (int s0 = 0; s0 < p.N; s0 += 32) {
-                const int s = s0 + lane;
-                const int w = s < p.N ? row_units<LGB>(p, p.ctx_lens[s]) : 0;
-                if (s < p.N && w == 0 && blockIdx.x == 0) flag_error(p.err, PA_DEV_ERR_CTX);
-                total += __reduce_add_sync(0xffffffffu, w);
+        } else {
+            if (blockIdx.x == 0) {
+                for (int s = lane; s < p.N; s += 32)
+                    if (units_of(s) == 0) flag_error(p.err, PA_DEV_ERR_CTX);
             }
-            total *= p.H_kv;
-            ctas = max((int64_t)1, min((int64_t)gridDim.x, total / kMinUnits));
-            const int64_t u0 = total * blockIdx.x / ctas, u1 = total * (blockIdx.x + 1) / ctas;
-            run.left = blockIdx.x < ctas ? u1 - u0 : 0;
-            unit = u0;  // first unit of the run's current row from here on
-            if (run.left > 0) {
-                int64_t before = 0;
-                for (int s0 = 0;; s0 += 32) {  // (ends: u0 < total)
-                    const int s = s0 + lane;
-                    const int c = s < p.N ? p.ctx_lens[s] : 0;
-                    const int w = row_units<LGB>(p, c);
-                    int v = w;
-    #pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const int x = __shfl_up_sync(0xffffffffu, v, o);
-                        if (lane >= o) v += x;
-                    }
-                    const int64_t hi = before + (int64_t)v * p.H_kv;
-                    const unsigned hit = __ballot_sync(0xffffffffu, u0 < hi);
-                    if (hit) {
-                        const int src = __ffs(hit) - 1;
-                        run.s = s0 + src;
-                        run.units = __shfl_sync(0xffffffffu, w, src);
-                        run.ctx = __shfl_sync(0xffffffffu, c, src);
-                        const int64_t at = u0 - __shfl_sync(0xffffffffu, hi, src) + (int64_t)run.units * p.H_kv;
-                        run.h = (int)(at / run.units);
-                        const int j = (int)(at - (int64_t)run.h * run.units);
-                        unit = u0 - j;
-                        run.enter(p, j, total, ctas, unit);
-                        break;
-                    }
-                    before = __shfl_sync(0xffffffffu, hi, 31);
-                }
-            } else {
-                run.e = run.e_end = 0;
+            if ((int)blockIdx.x < ctas && total > 0) {
+                const int u0 = cut.start(blockIdx.x);
+                run.left = cut.start(blockIdx.x + 1) - u0;
+                int first;
+                run.s = scan.find(u0, run.units, first);
+                run.ctx = p.ctx_lens[run.s];
+                run.h = (u0 - first) / run.units;
+                run.unit = first + run.h * run.units;
+                run.enter(p, u0 - run.unit, cut);
             }
         }
         const uint64_t pol = policy_evict_first();
@@ -328,7 +300,7 @@ __global__ void __launch_bounds__(kSpThreads) attend_sparse_kernel(const __grid_
             c.first = c.last = false;
             if (run.e >= run.e_end && !(kCluster && run.first)) {
                 if (run.left <= 0) return c;
-                unit += run.units;
+                run.unit += run.units;
                 if (++run.h == p.H_kv) {
                     run.h = 0;
                     do {  // (ends: the run has units left)
@@ -337,7 +309,7 @@ __global__ void __launch_bounds__(kSpThreads) attend_sparse_kernel(const __grid_
                         run.units = row_units<LGB>(p, run.ctx);
                     } while (run.units == 0);
                 }
-                run.enter(p, 0, total, ctas, unit);
+                run.enter(p, 0, cut);
             }
             c.some = true;
             c.s = run.s;
@@ -858,7 +830,7 @@ static bool sparse_layout(int N, int H_q, int H_kv, int D, int B, int top_k, Spa
         (B != 8 && B != 16 && B != 32) || top_k <= 0)
         return false;
     const int64_t rows = (int64_t)N * H_kv, units = ((int64_t)top_k * B + kUnitTok - 1) / kUnitTok;
-    if (units > (1LL << 31) / rows || rows * (H_q / H_kv) > 0x7fffffffLL) return false;
+    if (units >= (1LL << 31) / rows || rows * (H_q / H_kv) > 0x7fffffffLL) return false;
     auto align = [](size_t x) { return (x + 255) & ~size_t(255); };
     L->ctas = (int)std::min<int64_t>(kSpMaxCtas, rows * units);
     const size_t parts = (size_t)2 * L->ctas * (H_q / H_kv);

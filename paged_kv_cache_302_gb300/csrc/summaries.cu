@@ -12,6 +12,7 @@
 #include <type_traits>
 
 #include "quant.cuh"
+#include "runs.cuh"
 
 namespace pa {
 
@@ -367,8 +368,8 @@ __device__ __forceinline__ void int8x4_to_f16(uint32_t x, uint32_t& a, uint32_t&
 }
 
 // Tiles of each row of a sequence with something to choose.
-__device__ __forceinline__ int row_tiles(const SelectParams& p, int s, int& nb) {
-    nb = s < p.N ? context_blocks(p, s) : 0;
+__device__ __forceinline__ int row_tiles(const SelectParams& p, int s) {
+    const int nb = context_blocks(p, s);
     return nb > p.top_k ? (nb + 15) / 16 : 0;
 }
 
@@ -380,17 +381,14 @@ __global__ void __launch_bounds__(kScoreWarps * 32, kScoreCtas) score_kernel(con
     griddep_wait();
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31, g4 = lane >> 2, t4 = lane & 3;
-    int64_t total = 0;
-    for (int s0 = 0; s0 < p.N; s0 += 32) {
-        int nb;
-        total += __reduce_add_sync(0xffffffffu, row_tiles(p, s0 + lane, nb));
-    }
-    total *= p.H_kv;
-    const int64_t warps = min((int64_t)gridDim.x * kScoreWarps, total);
-    const int64_t w = (int64_t)(threadIdx.x >> 5) * gridDim.x + blockIdx.x;  // neighbouring runs on different SMs
+    const auto tiles_of = [&](int s) { return row_tiles(p, s); };
+    const RowScan<decltype(tiles_of)> scan(tiles_of, p.N, p.H_kv);
+    const int total = scan.total(), warps = min((int)gridDim.x * kScoreWarps, total);
+    const int w = (int)(threadIdx.x >> 5) * gridDim.x + blockIdx.x;  // neighbouring runs on different SMs
     if (w >= warps) return;
-    const int64_t u0 = total * w / warps;
-    int left = (int)(total * (w + 1) / warps - u0);
+    const Cut cut(total, warps);
+    const int u0 = cut.start(w);
+    int left = cut.start(w + 1) - u0;
 
     // A tile of the run, and this lane's block ids in it: blocks g4 and g4 + 8.
     struct Pos {
@@ -408,48 +406,27 @@ __global__ void __launch_bounds__(kScoreWarps * 32, kScoreCtas) score_kernel(con
             x.t = 0;
             if (++x.h == p.H_kv) {
                 x.h = 0;
-                do x.tiles = row_tiles(p, ++x.s, x.nb);
+                do x.tiles = row_tiles(p, ++x.s);
                 while (x.tiles == 0);  // (ends: the run has tiles left)
+                x.nb = context_blocks(p, x.s);
             }
         }
         look_up(x);
         return x;
     };
     Pos cur;
-    {
-        int64_t before = 0;
-        for (int s0 = 0;; s0 += 32) {  // (ends: u0 < total)
-            int nb;
-            const int n = row_tiles(p, s0 + lane, nb);
-            int v = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int x = __shfl_up_sync(0xffffffffu, v, o);
-                if (lane >= o) v += x;
-            }
-            const int64_t hi = before + (int64_t)v * p.H_kv;
-            const unsigned hit = __ballot_sync(0xffffffffu, u0 < hi);
-            if (hit) {
-                const int src = __ffs(hit) - 1;
-                cur.s = s0 + src;
-                cur.tiles = __shfl_sync(0xffffffffu, n, src);
-                cur.nb = __shfl_sync(0xffffffffu, nb, src);
-                const int64_t at = u0 - __shfl_sync(0xffffffffu, hi, src) + (int64_t)cur.tiles * p.H_kv;
-                cur.h = (int)(at / cur.tiles);
-                cur.t = (int)(at - (int64_t)cur.h * cur.tiles);
-                break;
-            }
-            before = __shfl_sync(0xffffffffu, hi, 31);
-        }
-        look_up(cur);
-    }
+    int first;
+    cur.s = scan.find(u0, cur.tiles, first);
+    cur.h = (u0 - first) / cur.tiles;
+    cur.t = u0 - first - cur.h * cur.tiles;
+    cur.nb = context_blocks(p, cur.s);
+    look_up(cur);
 
     // The query integers of head g4, in the order of the box's bytes: word w of chunk c holds channels 64 c + 16 t4 + 4 w
     // on, the k-columns 2 t4, 2 t4 + 1, 2 t4 + 8, 2 t4 + 9 of k-step (c, w).
     uint32_t up[NC][8], dn[NC][8];  // max(q, 0) and min(q, 0)
     float f0 = 0.f, f1 = 0.f;       // units of heads 2 t4 and 2 t4 + 1
-    auto load_query = [&](int s, int h) {
-        float m = 0.f;
+    auto read_query = [&](int s, int h) {
 #pragma unroll
         for (int c = 0; c < NC; ++c)
 #pragma unroll
@@ -463,6 +440,9 @@ __global__ void __launch_bounds__(kScoreWarps * 32, kScoreCtas) score_kernel(con
                 up[c][4 * i + 2] = v.z;
                 up[c][4 * i + 3] = v.w;
             }
+    };
+    auto make_query = [&]() {
+        float m = 0.f;
 #pragma unroll
         for (int c = 0; c < NC; ++c)
 #pragma unroll
@@ -508,12 +488,13 @@ __global__ void __launch_bounds__(kScoreWarps * 32, kScoreCtas) score_kernel(con
 #pragma unroll
         for (int r = 0; r < 2; ++r) v[r][k][c] = *reinterpret_cast<const uint4*>(box[r] + k * D + 64 * c);
     };
+    read_query(cur.s, cur.h);
     find(cur, unit);
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
         for (int c = 0; c < NC; ++c) load(k, c);
-    load_query(cur.s, cur.h);
+    make_query();
     Pos nxt = cur;
     if (left > 1) nxt = step(cur);
     for (; left > 0; --left) {
@@ -550,7 +531,10 @@ __global__ void __launch_bounds__(kScoreWarps * 32, kScoreCtas) score_kernel(con
             if (t4 == 0 && b < cur.nb) keys[b] = ordered(unit[r] > 0.f ? y * unit[r] : -INFINITY);
             unit[r] = next_unit[r];
         }
-        if (left > 1 && (nxt.s != cur.s || nxt.h != cur.h)) load_query(nxt.s, nxt.h);
+        if (left > 1 && (nxt.s != cur.s || nxt.h != cur.h)) {
+            read_query(nxt.s, nxt.h);
+            make_query();
+        }
         cur = nxt;
         nxt = after;
     }
@@ -762,6 +746,7 @@ pa_status launch_select(const SelectArgs& a) {
     const int64_t nb = std::min<int64_t>(((int64_t)a.max_ctx + a.B - 1) / a.B, a.MB);  // the longest context's
     if (nb > a.top_k) {
         const int64_t tiles = (nb + 15) / 16 * a.N * a.H_kv;
+        if (tiles >= 1LL << 31) return fail(PA_ERR_UNSUPPORTED, "too many blocks to score");
         const unsigned grid = (unsigned)std::min<int64_t>((tiles + kScoreWarps - 1) / kScoreWarps,
                                                           (int64_t)sm_count() * kScoreCtas);
         auto kern = a.q_dtype == PA_BF16 ? (a.D == 128 ? score_kernel<__nv_bfloat16, 128> : score_kernel<__nv_bfloat16, 64>)
