@@ -13,7 +13,8 @@ LIB = os.path.join(OUT_DIR, "libpa.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 SOURCES = ["decode.cu", "prefill.cu", "cache_ops.cu", "capi.cpp", "alloc.cpp", "vkv.cpp", "static_ws.cu",
-           "quant.cu", "decode_quant.cu", "tree.cu", "summaries.cu", "decode_sparse.cu", "compact.cu"]
+           "quant.cu", "decode_quant.cu", "tree.cu", "summaries.cu", "select.cu", "decode_sparse.cu",
+           "compact.cu"]
 GENCODE = "arch=compute_103a,code=sm_103a"
 
 

@@ -16,6 +16,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "cluster.cuh"
 #include "quant.cuh"
 #include "runs.cuh"
 #include "tensor_map.h"
@@ -89,22 +90,6 @@ __device__ __forceinline__ uint2 sp_lds64(uint32_t a) {
 __device__ __forceinline__ uint32_t sp_lds8(uint32_t a) {
     uint32_t v;
     asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
-    return v;
-}
-
-// All threads of a cluster's CTAs.  (Every wait before it has a limit, and every thread gets here.)
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-}
-
-// fp32 at shared-memory address `a` of the cluster's CTA `rank`.
-__device__ __forceinline__ float ld_cluster(uint32_t a, int rank) {
-    float v;
-    asm volatile(
-        "{\n\t.reg .b32 t;\n\tmapa.shared::cluster.u32 t, %1, %2;\n\tld.shared::cluster.f32 %0, [t];\n\t}"
-        : "=f"(v)
-        : "r"(a), "r"(rank)
-        : "memory");
     return v;
 }
 
@@ -723,7 +708,7 @@ __global__ void __launch_bounds__(kSpThreads) attend_sparse_kernel(const __grid_
         consume();
 
     if constexpr (kCluster) {
-        // every CTA of the cluster joins its slice of the row's outputs
+        // every CTA of the cluster joins its slice of the row's outputs (every wait before has a limit: all get here)
         __syncwarp();
         cluster_sync();
         const int row = blockIdx.x / p.cluster, rank = blockIdx.x % p.cluster;
@@ -872,20 +857,8 @@ static pa_status run_sparse(const DecodeSparseArgs& a, const SpParams& p, const 
         constexpr size_t smem = Geo::kSmem + Geo::kShare;
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(attend_sparse)");
-        cudaLaunchAttribute attr[2];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = (unsigned)p.cluster;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[1].val.programmaticStreamSerializationAllowed = 1;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)(a.N * a.H_kv * p.cluster));
-        cfg.blockDim = dim3(kSpThreads);
-        cfg.dynamicSmemBytes = smem;
-        cfg.stream = a.stream;
-        cfg.attrs = attr;
-        cfg.numAttrs = pdl_enabled() ? 2 : 1;
-        e = cudaLaunchKernelEx(&cfg, kern, tm, p);
+        e = launch_clusters(kern, p.cluster, dim3((unsigned)(a.N * a.H_kv * p.cluster)), dim3(kSpThreads), smem, a.stream, tm,
+                            p);
     } else {
         auto kern = attend_sparse_kernel<T, kQuant, D, LGB, false>;
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Geo::kSmem);

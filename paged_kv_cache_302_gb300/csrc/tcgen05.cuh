@@ -1,6 +1,7 @@
 // tcgen05.cuh -- 5th-generation tensor core (tcgen05) and TMEM wrappers, packed fp32 pairs.
 #pragma once
 
+#include "cluster.cuh"
 #include "pa_device.cuh"
 
 namespace pa {
@@ -66,17 +67,6 @@ __device__ __forceinline__ void tma_load_5d_mc(uint32_t dst, const void* tmap, u
         ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8, %9;" ::"r"(dst),
         "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar), "h"(mask), "l"(policy)
         : "memory");
-}
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-
-// Every thread of both CTAs of the cluster: writes before it are visible to the other CTA after it.
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
