@@ -333,7 +333,8 @@ pa_status pa_decode_tree(void* out, pa_dtype out_dtype, const void* q, pa_dtype 
  * calls: key summaries kept beside the cache, the selection of blocks by them,
  * and the attention over the selected blocks.  All three take a 16-bit pool or
  * a quantised cache, D in {64, 128}, B in {8, 16, 32}, NB*B and MB*B < 2^31,
- * N <= 65535, and the last two 1 <= H_q / H_kv <= 8.
+ * N <= 65535, and the last two 1 <= H_q / H_kv <= 8 and top_k <= 2^28.
+ * sum_scales may lie at any address, selected at any multiple of four.
  *
  * A key summary is a box around the keys of one (block, KV head):
  *   summaries:  [NB][H_kv][2][D] int8, channel d's least (index 0) and greatest

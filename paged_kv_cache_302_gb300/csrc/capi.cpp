@@ -477,8 +477,7 @@ pa_status pa_summarize_blocks(void* summaries, void* sum_scales, const void* poo
     if (max_q_len == 0) return PA_OK;
     if (!summaries || !sum_scales || !pool || !block_tables || !ctx_lens)
         return fail(PA_ERR_INVALID, "null pointer argument");
-    if (!aligned16(summaries) || !aligned16(sum_scales))
-        return fail(PA_ERR_INVALID, "summaries and sum_scales must be 16-byte aligned");
+    if (!aligned16(summaries)) return fail(PA_ERR_INVALID, "summaries must be 16-byte aligned");
     SummarizeArgs a;
     a.summaries = summaries;
     a.sum_scales = sum_scales;
@@ -515,13 +514,13 @@ pa_status pa_select_blocks(int32_t* selected, const void* q, pa_dtype q_dtype, c
     if (st == PA_OK) st = check_group(H_q, H_kv);
     if (st != PA_OK) return st;
     if (max_ctx <= 0 || top_k <= 0) return fail(PA_ERR_INVALID, "max_ctx and top_k must be positive");
+    if (top_k > kMaxTopK) return fail(PA_ERR_UNSUPPORTED, "top_k must be <= %d", kMaxTopK);
     if (sink_blocks < 0 || recent_blocks < 0 || (long long)sink_blocks + recent_blocks > top_k)
         return fail(PA_ERR_INVALID, "sink_blocks and recent_blocks must not be negative, nor more than top_k together");
     if (!selected || !q || !summaries || !sum_scales || !block_tables || !ctx_lens || !workspace)
         return fail(PA_ERR_INVALID, "null pointer argument");
-    if (!aligned16(selected) || !aligned16(q) || !aligned16(summaries) || !aligned16(sum_scales) ||
-        !aligned16(workspace))
-        return fail(PA_ERR_INVALID, "selected, q, summaries, sum_scales and workspace must be 16-byte aligned");
+    if (!aligned16(q) || !aligned16(summaries) || !aligned16(workspace))
+        return fail(PA_ERR_INVALID, "q, summaries and workspace must be 16-byte aligned");
     const size_t need = select_workspace_bytes(N, H_kv, max_ctx, B);
     if (ws_bytes < need) return fail(PA_ERR_INVALID, "workspace too small: %zu < %zu bytes", ws_bytes, need);
     SelectArgs a;
@@ -568,11 +567,12 @@ pa_status pa_decode_sparse(void* out, pa_dtype out_dtype, const void* q, pa_dtyp
     if (st == PA_OK) st = check_group(H_q, H_kv);
     if (st != PA_OK) return st;
     if (top_k <= 0) return fail(PA_ERR_INVALID, "top_k must be positive");
+    if (top_k > kMaxTopK) return fail(PA_ERR_UNSUPPORTED, "top_k must be <= %d", kMaxTopK);
     if (!(scale > 0.f && scale < HUGE_VALF)) return fail(PA_ERR_INVALID, "scale must be positive and finite");
     if (!out || !q || !pool || !block_tables || !ctx_lens || !selected || !workspace)
         return fail(PA_ERR_INVALID, "null pointer argument");
-    if (!aligned16(out) || !aligned16(q) || !aligned16(selected) || !aligned16(workspace))
-        return fail(PA_ERR_INVALID, "out, q, selected and workspace must be 16-byte aligned");
+    if (!aligned16(out) || !aligned16(q) || !aligned16(workspace))
+        return fail(PA_ERR_INVALID, "out, q and workspace must be 16-byte aligned");
     const size_t need = decode_sparse_workspace_bytes(N, H_q, H_kv, D, B, top_k);
     if (need == 0) return fail(PA_ERR_UNSUPPORTED, "too many work records");
     if (ws_bytes < need) return fail(PA_ERR_INVALID, "workspace too small: %zu < %zu bytes", ws_bytes, need);

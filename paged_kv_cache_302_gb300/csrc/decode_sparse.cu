@@ -288,8 +288,11 @@ __global__ void __launch_bounds__(kSpThreads) attend_sparse_kernel(const __grid_
                 run.unit += run.units;
                 if (++run.h == p.H_kv) {
                     run.h = 0;
-                    do {  // (ends: the run has units left)
-                        ++run.s;
+                    do {  // (the run has units left, so a sequence follows)
+                        if (++run.s >= p.N) {
+                            run.left = 0;
+                            return c;
+                        }
                         run.ctx = p.ctx_lens[run.s];
                         run.units = row_units<LGB>(p, run.ctx);
                     } while (run.units == 0);
@@ -314,7 +317,7 @@ __global__ void __launch_bounds__(kSpThreads) attend_sparse_kernel(const __grid_
         auto look_up = [&](const Chunk& c, int& nv) -> int {
             nv = 0;
             if (!c.some || c.entry < 0) return -1;
-            if (c.entry >= (c.ctx + B - 1) >> LGB) return -1;
+            if (c.entry >= min((c.ctx + B - 1) >> LGB, p.MB)) return -1;
             nv = min(B, c.ctx - (c.entry << LGB));
             return p.tables[(int64_t)c.s * p.MB + c.entry];
         };
@@ -499,7 +502,7 @@ __global__ void __launch_bounds__(kSpThreads) attend_sparse_kernel(const __grid_
             constexpr bool kFull = decltype(full_c)::value;
             float y[NSUB][4];                   // scores in base-2 units
             [[maybe_unused]] float iv[NSUB][2]; // 2^-ev of tokens rt and rt + 8 (e4m3)
-            float x0 = NEG_INF, x1 = NEG_INF;
+            float top0 = NEG_INF, top1 = NEG_INF;
 #pragma unroll
             for (int j = 0; j < NSUB; ++j) {
                 float a[4] = {0.f, 0.f, 0.f, 0.f}, b[4] = {0.f, 0.f, 0.f, 0.f};
@@ -528,29 +531,29 @@ __global__ void __launch_bounds__(kSpThreads) attend_sparse_kernel(const __grid_
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     const int tok = 16 * j + 8 * half + rt;
-                    float f0 = c0, f1 = c1, add = 0.f;
+                    float x0 = a[2 * half] + b[2 * half], x1 = a[2 * half + 1] + b[2 * half + 1], add = 0.f;
                     if constexpr (kQuant) {
                         const uint32_t at = scb + qsc_ofs(16 * j + 8 * half) + rt;
                         const float fk = pow2i(scale_of((int)sp_lds8(at)));
                         const int ev = scale_of((int)sp_lds8(at + B));
-                        f0 *= fk;
-                        f1 *= fk;
+                        x0 *= fk;  // (before the query's factor, which may be as large as fp32 allows)
+                        x1 *= fk;
                         add = (float)ev;
                         iv[j][half] = pow2i(-ev);
                     }
                     const bool in = kFull || (mt.seen >> tok & 1u);
-                    y[j][2 * half] = in ? fmaf(a[2 * half] + b[2 * half], f0, add) : NEG_INF;
-                    y[j][2 * half + 1] = in ? fmaf(a[2 * half + 1] + b[2 * half + 1], f1, add) : NEG_INF;
+                    y[j][2 * half] = in ? fmaf(x0, c0, add) : NEG_INF;
+                    y[j][2 * half + 1] = in ? fmaf(x1, c1, add) : NEG_INF;
                 }
-                x0 = fmaxf(x0, fmaxf(y[j][0], y[j][2]));
-                x1 = fmaxf(x1, fmaxf(y[j][1], y[j][3]));
+                top0 = fmaxf(top0, fmaxf(y[j][0], y[j][2]));
+                top1 = fmaxf(top1, fmaxf(y[j][1], y[j][3]));
             }
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) {
-                x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, o));
-                x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, o));
+                top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, o));
+                top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, o));
             }
-            rescale(fmaxf(m0, x0), fmaxf(m1, x1));
+            rescale(fmaxf(m0, top0), fmaxf(m1, top1));
             if constexpr (!kQuant) {
                 // V rows of tokens that take no part may hold anything (even NaN): they become zeros
                 if (!kFull) {
@@ -909,7 +912,7 @@ pa_status launch_decode_sparse(const DecodeSparseArgs& a) {
     p.err = a.dev_err;
     const bool quant = a.kv_dtype == PA_E4M3;
     const int64_t rows = (int64_t)a.N * a.H_kv;
-    p.cluster = rows <= kSpClusterRows && a.top_k * a.B >= 2 * kSpMaxCluster * kUnitTok ? kSpMaxCluster : 0;
+    p.cluster = rows <= kSpClusterRows && (int64_t)a.top_k * a.B >= 2 * kSpMaxCluster * kUnitTok ? kSpMaxCluster : 0;
     pa_status st;
     if (a.q_dtype == PA_BF16)
         st = quant ? run_sparse_shape<__nv_bfloat16, true>(a, p, L) : run_sparse_shape<__nv_bfloat16, false>(a, p, L);

@@ -87,6 +87,8 @@ pa_status launch_tree(const TreeArgs& a);
 
 // ----------------------------------------------------------------------------- block-sparse decode, compaction
 
+constexpr int kMaxTopK = 1 << 28;  // entries of a list: as many blocks as a context can have
+
 struct SummarizeArgs {
     void* summaries;
     void* sum_scales;

@@ -42,10 +42,13 @@ struct RowScan {
         for (int s = kScanSeqs + (threadIdx.x & 31); s < N; s += 32) t += units(s);
         return __reduce_add_sync(0xffffffffu, t) * H_kv;
     }
-    // The sequence that holds unit u (below the total): its units per row in `n`, its first unit in `first`.
+    // The sequence that holds unit u (below the total): its units per row in `n`, its first unit in `first`.  (The last
+    // one, should the lengths have changed since: nothing is ever looked up behind the batch.)
     __device__ __forceinline__ int find(int u, int& n, int& first) const {
         const int lane = threadIdx.x & 31;
         int before = 0, s = -1;
+        n = 1;
+        first = u;
         auto look = [&](int s0, int x) {
             int v = x;
 #pragma unroll
@@ -66,8 +69,8 @@ struct RowScan {
 #pragma unroll
         for (int i = 0; i < kScanSeqs / 32; ++i)
             if (s < 0 && 32 * i < N) look(32 * i, w[i]);
-        for (int s0 = kScanSeqs; s < 0; s0 += 32) look(s0, s0 + lane < N ? units(s0 + lane) : 0);
-        return s;
+        for (int s0 = kScanSeqs; s < 0 && s0 < N; s0 += 32) look(s0, s0 + lane < N ? units(s0 + lane) : 0);
+        return s < 0 ? N - 1 : s;
     }
 };
 

@@ -230,8 +230,10 @@ __global__ void __launch_bounds__(kScoreWarps * 32, kScoreCtas) score_kernel(con
             y.t = 0;
             if (++y.h == p.H_kv) {
                 y.h = 0;
-                do y.tiles = row_tiles(p, ++y.s);
-                while (y.tiles == 0);  // (ends: the run has tiles left)
+                while (y.s + 1 < p.N) {  // (the run has tiles left, so a sequence follows)
+                    y.tiles = row_tiles(p, ++y.s);
+                    if (y.tiles > 0) break;
+                }
                 y.nb = context_blocks(p, y.s);
             }
         }

@@ -3,6 +3,7 @@ import numpy as np
 import pytest
 import torch
 
+import _quant_ref as R
 import _sparse_ref as S
 import paged_kv_cache_302_gb300 as pa
 
@@ -134,3 +135,171 @@ def test_list_offsets_out_of_range_are_flagged():
             move(want, tables, B, [(s, 20 + j, j) for s in good for j in range(10)])
         assert torch.equal(pool.view(torch.int16).cpu(), want[0])
         assert err.item() == pa.PA_DEV_ERR_CTX
+
+
+@pytest.mark.parametrize("quant", [False, True])
+def test_blocks_past_32_bits_and_streams(quant):
+    """A pool of more than 2^32 bytes, three sequences' lists, on a stream of its own and captured into a graph."""
+    g = torch.Generator().manual_seed(6)
+    B, H, D = 16, 8, 128
+    NB = 140000 if quant else 70000
+    ctx = [300, 77, 150]
+    small = random_cache(g, 40, H, B, D, quant)
+    big = [torch.empty((NB,) + tuple(x.shape[1:]), dtype=x.dtype, device="cuda") for x in small]
+    at = torch.cat([torch.arange(20), torch.arange(NB - 20, NB)])
+    for x, y in zip(big, small):
+        x[at.cuda()] = y.cuda()
+    low = S.make_tables(g, ctx, B, 19, 40)
+    high = torch.where(low < 40, at[low.clamp(max=39).long()].to(torch.int32), low).cuda()
+    r = np.random.default_rng(6)
+    base = [0, 3, 100]
+    keeps = [np.sort(r.choice(L - b, (L - b) // 2, replace=False)) + b for L, b in zip(ctx, base)]
+    bits = tuple((x.view(torch.int16) if x.dtype == torch.float16 else x).clone() for x in small)
+    moves = [(s, int(k), base[s] + j) for s, keep in enumerate(keeps) for j, k in enumerate(keep)]
+    ks = np.cumsum([0] + [len(k) for k in keeps])
+    args = (high, i32(ctx), i32(base), i32(np.concatenate(keeps)), i32(ks))
+    kw = {"scales": big[1]} if quant else {}
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    pa.pa_compact_tokens(big[0], *args, stream=stream, **kw)
+    with torch.cuda.graph(graph, stream=stream):
+        pa.pa_compact_tokens(big[0], *args, **kw)
+    graph.replay()
+    torch.cuda.synchronize()
+    for _ in range(2):
+        move(bits, low, B, moves)
+    for x, y in zip(big, bits):
+        x = x[at.cuda()]
+        assert torch.equal((x.view(torch.int16) if x.dtype == torch.float16 else x).cpu(), y)
+
+
+@pytest.mark.parametrize("quant", [False, True])
+def test_many_short_lists_and_one_long(quant):
+    g = torch.Generator().manual_seed(7)
+    B, H, D = 8, 2, 64
+    ctx = [40] * 600 + [9000]
+    r = np.random.default_rng(7)
+    base = [int(r.integers(0, 30)) for _ in ctx[:-1]] + [10]
+    keeps = [np.sort(r.choice(L - b, int(r.integers(0, min(12, L - b))), replace=False)) + b
+             for L, b in zip(ctx[:-1], base)] + [np.sort(r.choice(8990, 6000, replace=False)) + 10]
+    NB = sum(-(-L // B) for L in ctx) + 1
+    run(random_cache(g, NB, H, B, D, quant), S.make_tables(g, ctx, B, 1130, NB), ctx, base, keeps, B)
+
+
+@pytest.mark.parametrize("quant", [False, True])
+def test_a_generation_with_drafts_forks_and_evictions(quant):
+    """The calls as a server uses them: prompts written, summaries built, a fork, drafts appended and verified as a tree,
+    the accepted ones compacted with the allocator's replacements, summaries of what changed rebuilt, a prefix evicted,
+    blocks selected and attended -- against a plain list of every sequence's tokens."""
+    H, G, D, B, top_k, MB = 2, 4, 64, 8, 6, 20
+    gen = torch.Generator().manual_seed(8)
+    r = np.random.default_rng(8)
+    NB = 64
+    alloc = pa.BlockAllocator(NB, B)
+    pool = torch.zeros(NB, B, 2, H, D, dtype=torch.bfloat16, device="cuda")
+    if quant:
+        cache = (torch.zeros(NB, H, 2, B, D, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn),
+                 torch.zeros(NB, H, 2, B, dtype=torch.uint8, device="cuda"))
+    else:
+        cache = (pool,)
+    kw = {"scales": cache[1]} if quant else {}
+    box = torch.zeros(NB, H, 2, D, dtype=torch.int8, device="cuda")
+    by = torch.zeros(NB, H, dtype=torch.uint8, device="cuda")
+    tokens = {}                                          # sequence -> its K, V rows in order
+    err = err_word()
+
+    def copies(pairs):
+        for x in cache + (box, by):
+            if x.dtype == torch.int8 or x.dim() == 2:    # summaries are a block's like its tokens
+                for a, b in np.asarray(pairs).tolist():
+                    x[b] = x[a]
+            elif len(pairs):
+                pa.pa_copy_blocks(x, torch.from_numpy(np.ascontiguousarray(pairs)).cuda(), dev_err=err)
+
+    def append(s, n):
+        k, v = (torch.randn(n, H, D, generator=gen).bfloat16() for _ in range(2))
+        slots, cow = alloc.append_slots(s, n)
+        copies(cow)
+        write = pa.pa_reshape_and_cache_quant if quant else pa.pa_reshape_and_cache
+        write(k.cuda(), v.cuda(), *cache, torch.from_numpy(slots).cuda(), dev_err=err)
+        tokens[s] = tokens.get(s, []) + [(k[i], v[i]) for i in range(n)]
+
+    def tables(seqs):
+        t, ctx = alloc.block_tables(seqs, MB)
+        return torch.from_numpy(t).cuda(), torch.from_numpy(ctx).cuda()
+
+    def summarize(seqs, n):
+        t, ctx = tables(seqs)
+        pa.pa_summarize_blocks(box, by, cache[0], t, ctx, max(max(n), 1), q_start=i32(np.cumsum([0] + list(n))),
+                               dev_err=err, **kw)
+
+    def compact(seqs, base, keeps):
+        t, ctx = alloc.block_tables(seqs, MB)
+        new = [b + len(k) for b, k in zip(base, keeps)]
+        cow, upd = alloc.compact_batch(seqs, base, new, table_updates=True)
+        copies(cow)
+        t = torch.from_numpy(t).cuda()
+        if len(upd):
+            pa.pa_update_block_tables(t, torch.from_numpy(upd).cuda(), dev_err=err)
+        pa.pa_compact_tokens(cache[0], t, torch.from_numpy(ctx).cuda(), i32(base), i32(np.concatenate(keeps)),
+                             i32(np.cumsum([0] + [len(k) for k in keeps])), dev_err=err, **kw)
+        for s, b, k in zip(seqs, base, keeps):
+            tokens[s] = tokens[s][:b] + [tokens[s][i] for i in k]
+        summarize(seqs, [n - b for n, b in zip(new, base)])
+
+    def check(seqs):
+        """Every sequence's tokens in the pool, its summaries, the selection by them, and the attention."""
+        t, ctx = tables(seqs)
+        q = torch.randn(len(seqs), H * G, D, generator=gen).bfloat16()
+        sel = torch.empty(len(seqs), H, top_k, dtype=torch.int32, device="cuda")
+        pa.pa_select_blocks(sel, q.cuda(), box, by, t, ctx, MB * B, B, dev_err=err)
+        out = torch.empty(q.shape, dtype=torch.float32, device="cuda")
+        pa.pa_decode_sparse(out, q.cuda(), cache[0], t, ctx, sel, dev_err=err, **kw)
+        host, bb, ss = S.host_cache(cache), box.cpu().numpy(), by.cpu().numpy()
+        for i, s in enumerate(seqs):
+            L, blocks = len(tokens[s]), alloc.block_table(s)
+            assert alloc.seq_len(s) == L == int(ctx[i])
+            for h in range(H):
+                k, v, ev = S.keys_of(host, blocks, h, L)
+                want = np.stack([x[0][h].double().numpy() for x in tokens[s]])
+                if quant:
+                    want = R.values(*R.quantise(want))
+                assert np.array_equal(k, want)
+                x = np.array([S.box(k[b * B: b * B + B])[0] for b in range(len(blocks))])
+                assert np.array_equal(bb[blocks, h], x)
+                rows = slice(h * G, h * G + G)
+                pick = S.select(S.scores(R.to64(q[i, rows]), bb[blocks, h], ss[blocks, h]), top_k, 1, 1)
+                assert np.array_equal(sel[i, h].cpu().numpy(), pick)
+                at = np.concatenate([np.arange(b * B, min(L, b * B + B)) for b in pick if b >= 0])
+                want, tol = R.attend(R.to64(q[i, rows]), k[at], v[at], ev[at], np.ones((G, len(at)), bool), 1 / 8, True, quant)
+                R.close(out[i, rows], want, tol, "attention")
+        assert err.item() == 0
+
+    for s, n in enumerate((50, 7, 90)):
+        alloc.add_seq(s)
+        append(s, n)
+    summarize([0, 1, 2], [50, 7, 90])
+    check([0, 1, 2])
+    alloc.fork(0, 3)
+    tokens[3] = list(tokens[0])
+    check([0, 1, 2, 3])
+    for _ in range(3):                                   # drafts, some of them accepted
+        seqs = [0, 1, 2, 3]
+        base = [len(tokens[s]) for s in seqs]
+        for s in seqs:
+            append(s, 9)
+        keeps = [np.sort(r.choice(9, int(r.integers(0, 6)), replace=False)) + b for b in base]
+        compact(seqs, base, keeps)
+        check(seqs)
+    alloc.fork(2, 4)
+    tokens[4] = list(tokens[2])
+    L = len(tokens[2])                                   # eviction from shared blocks: 4 keeps what it has
+    compact([2, 0], [4, 10], [np.sort(r.choice(L - 4, L // 2, replace=False)) + 4, np.arange(10, 30)])
+    check([0, 1, 2, 3, 4])
+    for s in (0, 2, 4):
+        append(s, 1)
+    summarize([0, 2, 4], [1, 1, 1])
+    check([0, 1, 2, 3, 4])
+    for s in range(5):
+        alloc.free_seq(s)
+    assert alloc.num_free() == NB

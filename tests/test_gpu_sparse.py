@@ -405,3 +405,262 @@ def test_every_block_listed_is_the_whole_decode(D, quant):
     want, tol = want_sparse(q.cpu(), S.host_cache(c), tables.cpu(), ctx, ref, B, 1 / math.sqrt(D), "bf16", quant)
     R.close(a, want, tol, "sparse decode")
     R.close(b, want, tol, "whole decode")
+
+
+# ------------------------------------------------------------------------------------------------ the calls in use
+
+class Step:
+    """A batch with its cache, summaries and queries, and one decode step over it: rebuild, select, attend."""
+
+    def __init__(self, seed, ctx, H, G, D, B, dtype, quant, top_k, extra=0):
+        g = torch.Generator().manual_seed(seed)
+        self.ctx, self.H, self.B, self.D, self.top_k = ctx, H, B, D, top_k
+        self.NB = sum(-(-L // B) for L in ctx) + 3
+        self.cache = S.make_cache(g, self.NB, H, B, D, dtype, quant)
+        self.tables = S.make_tables(g, ctx, B, -(-max(ctx) // B) + extra, self.NB).cuda()
+        self.q = torch.randn(len(ctx), H * G, D, generator=g).to(DT[dtype]).cuda()
+        self.dctx = i32(ctx)
+
+    def buffers(self):
+        N = len(self.ctx)
+        nan = torch.full(self.q.shape, math.nan, dtype=self.q.dtype, device="cuda")
+        return poisoned_boxes(self.NB, self.H, self.D) + (
+            torch.full((N, self.H, self.top_k), -9, dtype=torch.int32, device="cuda"), nan,
+            torch.full((pa.pa_select_workspace_bytes(N, self.H, max(self.ctx), self.B),), 0xFF, dtype=torch.uint8,
+                       device="cuda"),
+            torch.full((pa.pa_decode_sparse_workspace_bytes(N, self.q.shape[1], self.H, self.D, self.B, self.top_k),), 0xFF,
+                       dtype=torch.uint8, device="cuda"))
+
+    def run(self, b, stream=None):
+        box, by, sel, out, ws1, ws2 = b
+        kw = dict(stream=stream, **scales_of(self.cache))
+        pa.pa_summarize_blocks(box, by, self.cache[0], self.tables, self.dctx, max(self.ctx), **kw)
+        pa.pa_select_blocks(sel, self.q, box, by, self.tables, self.dctx, max(self.ctx), self.B, workspace=ws1,
+                            stream=stream)
+        pa.pa_decode_sparse(out, self.q, self.cache[0], self.tables, self.dctx, sel, workspace=ws2, **kw)
+        return sel, out
+
+
+SHAPES = [([3000, 700, 41, 1900] * 3, 2, 4, 64, 16, "f16", False, 20), ([5000] * 12, 8, 2, 128, 16, "bf16", True, 64),
+          ([900, 20000], 4, 8, 128, 8, "bf16", False, 100)]
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+def test_steps_side_by_side_give_the_bits_they_give_alone(shape):
+    """Three streams, each with buffers and workspaces of its own, poisoned before; and again with the library's own
+    workspaces."""
+    st = Step(3, *shape[:7], shape[7])
+    sel, out = st.run(st.buffers())
+    bufs = [st.buffers() for _ in range(3)]
+    streams = [torch.cuda.Stream() for _ in bufs]
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for s, b in zip(streams, bufs):
+            st.run(b, s)
+    torch.cuda.synchronize()
+    for b in bufs:
+        assert torch.equal(b[2], sel) and torch.equal(b[3], out)
+    bufs = [st.buffers()[:4] + (None, None) for _ in streams]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for s, b in zip(streams, bufs):
+            st.run(b, s)
+    torch.cuda.synchronize()
+    for b in bufs:
+        assert torch.equal(b[2], sel) and torch.equal(b[3], out)
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+def test_captured_step_follows_what_its_inputs_hold(shape):
+    """One graph, replayed with other queries, lengths and tables in the same tensors."""
+    st = Step(4, *shape[:7], shape[7])
+    b = st.buffers()
+    stream = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(stream):
+        st.run(b)
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g, stream=stream):
+            st.run(b)
+    for seed in (0, 1, 2):
+        r = np.random.default_rng(seed)
+        st.q.copy_(torch.randn(st.q.shape, generator=torch.Generator().manual_seed(seed)))
+        st.dctx.copy_(i32([int(r.integers(1, L + 1)) for L in st.ctx]))
+        b[3].fill_(math.nan)
+        g.replay()
+        torch.cuda.synchronize()
+        sel, out = b[2].clone(), b[3].clone()
+        fresh = st.buffers()
+        fresh[0].copy_(b[0])
+        fresh[1].copy_(b[1])
+        st.run(fresh)
+        assert torch.equal(sel, fresh[2]) and torch.equal(out, fresh[3])
+
+
+def test_attention_into_pinned_host_memory():
+    for ctx, quant in (([700, 90], False), ([500] * 40, True)):
+        st = Step(5, ctx, 2, 4, 128, 16, "bf16", quant, 20)
+        sel, out = st.run(st.buffers())
+        host = torch.full(out.shape, math.nan, dtype=out.dtype).pin_memory()
+        pa.pa_decode_sparse(host, st.q, st.cache[0], st.tables, st.dctx, sel, **scales_of(st.cache))
+        torch.cuda.synchronize()
+        assert torch.equal(host, out.cpu())
+
+
+def test_workspaces_and_lists_at_odd_addresses():
+    """Workspaces of the least size at odd multiples of 16 bytes inside a poisoned buffer, lists at odd multiples of four,
+    scale bytes at odd ones: the same bits, and nothing beside them written."""
+    for ctx in ([900, 3000, 15], [2000] * 30):
+        st = Step(6, ctx, 2, 4, 64, 16, "bf16", False, 33)
+        box, by, sel, out, ws1, ws2 = st.buffers()
+        want = [x.clone() for x in st.run((box, by, sel, out, ws1, ws2))]
+        n1, n2 = ws1.numel(), ws2.numel()
+        base = torch.full((n1 + n2 + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+        big_sel = torch.full((sel.numel() + 7,), -9, dtype=torch.int32, device="cuda")
+        big_by = torch.full((by.numel() + 9,), 0xA5, dtype=torch.uint8, device="cuda")
+        sel2, by2 = big_sel[3: 3 + sel.numel()].view(sel.shape), big_by[5: 5 + by.numel()].view(by.shape)
+        b1, b2 = base[16: 16 + n1], base[n1 + 2048 - n1 % 16 + 16: n1 + 2048 - n1 % 16 + 16 + n2]
+        box.fill_(0)
+        got = st.run((box, by2, sel2, torch.full_like(out, math.nan), b1, b2))
+        used = st.tables[st.tables < st.NB].long()       # (the others keep each buffer's own poison)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(by2[used], by[used])
+        assert (big_sel[:3] == -9).all() and (big_sel[3 + sel.numel():] == -9).all()
+        assert (big_by[:5] == 0xA5).all() and (big_by[5 + by.numel():] == 0xA5).all()
+        assert (base[:16] == 0xA5).all() and (base[16 + n1: n1 + 2048 - n1 % 16 + 16] == 0xA5).all()
+        assert (base[n1 + 2048 - n1 % 16 + 16 + n2:] == 0xA5).all()
+
+
+@pytest.mark.parametrize("quant", [False, True])
+def test_offsets_past_32_bits(quant):
+    """Blocks at the far end of a pool of more than 2^32 bytes and (16 bit) 2^31 elements."""
+    H, G, D, B, top_k = 8, 4, 128, 16, 6
+    NB = 140000 if quant else 70000
+    ctx = [150, 97]
+    g = torch.Generator().manual_seed(11)
+    small = S.make_cache(g, 24, H, B, D, "bf16", quant)
+    big = tuple(torch.empty((NB,) + tuple(x.shape[1:]), dtype=x.dtype, device="cuda") for x in small)
+    at = torch.cat([torch.arange(8), torch.arange(NB - 16, NB)])
+    raw = lambda x: x.view(torch.uint8) if x.dtype == torch.float8_e4m3fn else x  # noqa: E731
+    for x, y in zip(big, small):
+        raw(x)[at.cuda()] = raw(y)
+    low = S.make_tables(g, ctx, B, 10, 24)
+    high = torch.where(low < 24, at[low.clamp(max=23).long()].to(torch.int32), low)
+    q = torch.randn(2, H * G, D, generator=g).bfloat16().cuda()
+    res = []
+    for cache, tables, nb in ((small, low.cuda(), 24), (big, high.cuda(), NB)):
+        box = torch.zeros((nb, H, 2, D), dtype=torch.int8, device="cuda")
+        by = torch.zeros((nb, H), dtype=torch.uint8, device="cuda")
+        err = err_word()
+        pa.pa_summarize_blocks(box, by, cache[0], tables, i32(ctx), 150, dev_err=err, **scales_of(cache))
+        sel = torch.empty(2, H, top_k, dtype=torch.int32, device="cuda")
+        pa.pa_select_blocks(sel, q, box, by, tables, i32(ctx), 150, B, dev_err=err)
+        out = torch.empty(q.shape, dtype=torch.float32, device="cuda")
+        pa.pa_decode_sparse(out, q, cache[0], tables, i32(ctx), sel, dev_err=err, **scales_of(cache))
+        assert err.item() == 0
+        res.append((sel, out))
+    assert torch.equal(res[0][0], res[1][0]) and torch.equal(res[0][1], res[1][1])
+
+
+def test_many_sequences():
+    """More sequences than one pass over the lengths takes, bad ones among them, more rows than the device's CTAs."""
+    N, H, G, D, B, top_k = 1500, 2, 2, 64, 8, 4
+    r = np.random.default_rng(12)
+    ctx = r.integers(1, 90, size=N)
+    bad = r.choice(N, 40, replace=False)
+    g = torch.Generator().manual_seed(12)
+    NB = int(sum(-(-ctx // B))) + 1
+    c = S.make_cache(g, NB, H, B, D, "f16", False)
+    tables = S.make_tables(g, ctx.tolist(), B, 12, NB)
+    lens = ctx.copy()
+    lens[bad] = r.choice([0, -1, 97], size=40)
+    q = torch.randn(N, H * G, D, generator=g).half()
+    box, by = poisoned_boxes(NB, H, D)
+    err = err_word()
+    pa.pa_summarize_blocks(box, by, c[0], tables.cuda(), i32(ctx), 90, dev_err=err)
+    assert err.item() == 0
+    sel = check_select(q, box.cpu(), by.cpu(), tables, lens.clip(0, 97).tolist(), B, top_k, 1, 1, H,
+                       flag=pa.PA_DEV_ERR_CTX, max_ctx=96, ctx_flag=set(bad.tolist()))
+    out = torch.full(q.shape, 5.0, dtype=torch.float32, device="cuda")
+    pa.pa_decode_sparse(out, q.cuda(), c[0], tables.cuda(), i32(lens), sel, dev_err=err)
+    assert err.item() == pa.PA_DEV_ERR_CTX and (out[torch.from_numpy(bad)] == 5.0).all()
+    good = np.setdiff1d(np.arange(N), bad)
+    want, tol = want_sparse(q[good], S.host_cache(c), tables[good], ctx[good].tolist(), sel.cpu()[good], B, 1 / 8, "f16",
+                            False)
+    R.close(out[torch.from_numpy(good)], want, tol, "many sequences")
+
+
+@pytest.mark.parametrize("rows", ["few", "many"])
+def test_quantised_attention_with_queries_and_scales_of_extreme_size(rows):
+    """bf16 queries from fp32's subnormal numbers to its largest, scale bytes at both ends: finite, and within bounds where
+    the scores themselves fit fp32."""
+    H, G, D, B, top_k = 1, 6, 128, 16, 8
+    ctx = [130, 100] if rows == "few" else [130, 100] * 40
+    g = torch.Generator().manual_seed(13)
+    NB = sum(-(-L // B) for L in ctx) + 1
+    c = S.make_cache(g, NB, H, B, D, "bf16", True)
+    c[1][:] = torch.randint(120, 132, c[1].shape, generator=g, dtype=torch.uint8).cuda()
+    c[1][::3, :, 1] = 87
+    c[1][1::3, :, 1] = 167
+    tables = S.make_tables(g, ctx, B, 9, NB)
+    q = torch.randn(len(ctx), H * G, D, generator=g)
+    q[:, 1] *= 1e-38
+    q[:, 2] *= 2.0 ** -120
+    q[:, 3] = 0
+    q[:, 4] *= 1e30
+    q[:, 5, 1:] *= 1e-10
+    q = q.bfloat16()
+    sel = random_lists(g, ctx, H, B, top_k)
+    for scale in (1e-31, 3e-44):
+        out = torch.full(q.shape, math.nan, dtype=torch.float32, device="cuda")
+        pa.pa_decode_sparse(out, q.cuda(), c[0], tables.cuda(), i32(ctx), sel.cuda(), scale=scale, scales=c[1])
+        want, tol = want_sparse(q, S.host_cache(c), tables, ctx, sel, B, float(np.float32(scale)), "bf16", True)
+        R.close(out, want, tol, f"scale {scale}")
+
+
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("N", [2, 30])
+def test_waits_that_run_out_flag_and_leave_the_gpu_usable(N, quant):
+    """A limit of 1 ns on every wait: the call returns with the flag (few rows join over clusters, many by a second
+    kernel), and the next one gives the bits of one before."""
+    st = Step(14, [2000] * N, 4, 4, 128, 16, "bf16", quant, 60)
+    b = st.buffers()
+    sel, out = (x.clone() for x in st.run(b))
+    err = err_word()
+    pa.pa_set_wait_limit_ns(1)
+    try:
+        for _ in range(3):
+            pa.pa_decode_sparse(torch.empty_like(out), st.q, st.cache[0], st.tables, st.dctx, sel, workspace=b[5],
+                                dev_err=err, **scales_of(st.cache))
+        torch.cuda.synchronize()
+    finally:
+        pa.pa_set_wait_limit_ns(0)
+    assert err.item() == pa.PA_DEV_ERR_TIMEOUT
+    again = torch.full_like(out, math.nan)
+    err.zero_()
+    pa.pa_decode_sparse(again, st.q, st.cache[0], st.tables, st.dctx, sel, workspace=b[5], dev_err=err,
+                        **scales_of(st.cache))
+    torch.cuda.synchronize()
+    assert err.item() == 0 and torch.equal(again, out)
+
+
+def test_tensors_of_another_place_are_refused():
+    st = Step(15, [100, 50], 2, 2, 64, 16, "f16", False, 4)
+    box, by, sel, out, ws1, ws2 = st.buffers()
+    args = (sel, st.q, box, by, st.tables, st.dctx, 100, 16)
+    for i in range(6):
+        with pytest.raises(pa.PAError):
+            pa.pa_select_blocks(*[x.cpu() if j == i else x for j, x in enumerate(args)])
+    args = (out, st.q, st.cache[0], st.tables, st.dctx, sel)
+    for i in range(6):
+        with pytest.raises(pa.PAError):
+            pa.pa_decode_sparse(*[x.cpu() if j == i else x for j, x in enumerate(args)])
+    with pytest.raises(pa.PAError):
+        pa.pa_select_blocks(sel.transpose(0, 1).contiguous().transpose(0, 1), st.q, box, by, st.tables, st.dctx, 100, 16)
+    with pytest.raises(pa.PAError):
+        pa.pa_select_blocks(sel.long(), st.q, box, by, st.tables, st.dctx, 100, 16)
+    with pytest.raises(pa.PAError):
+        pa.pa_decode_sparse(out.half().float()[:, :, ::2], st.q, st.cache[0], st.tables, st.dctx, sel)
+    with pytest.raises(pa.PAError, match="workspace"):
+        pa.pa_decode_sparse(out, st.q, st.cache[0], st.tables, st.dctx, sel, workspace=ws2[:16])
+    with pytest.raises(pa.PAError, match="workspace"):
+        pa.pa_select_blocks(sel, st.q, box, by, st.tables, st.dctx, 100, 16, workspace=ws1[:16])

@@ -56,17 +56,17 @@ def test_calls_refuse_caches(call, kw, status):
 
 @pytest.mark.parametrize("call, kw, status", [
     (summarize, dict(mq=-1), INV), (summarize, dict(box=None), INV), (summarize, dict(by=None), INV),
-    (summarize, dict(box=A[0] + 8), INV), (summarize, dict(by=A[1] + 4), INV),
+    (summarize, dict(box=A[0] + 8), INV),
     (select, dict(qdt=F32), UNS), (select, dict(qdt=E4M3), UNS), (select, dict(Hq=7), INV), (select, dict(Hq=18), UNS),
     (select, dict(Hq=0), INV), (select, dict(mc=0), INV), (select, dict(k=0), INV), (select, dict(sink=-1), INV),
     (select, dict(rec=-1), INV), (select, dict(sink=2, rec=1), INV), (select, dict(sink=2 ** 31 - 1, rec=2 ** 31 - 1), INV),
     (select, dict(ws=None), INV), (select, dict(wsb=15), INV), (select, dict(q=A[1] + 2), INV),
-    (select, dict(sel=A[0] + 4), INV), (select, dict(sel=None), INV), (select, dict(by=None), INV),
+    (select, dict(sel=None), INV), (select, dict(k=(1 << 28) + 1), UNS), (select, dict(box=A[2] + 8), INV), (select, dict(by=None), INV),
     (decode, dict(qdt=F32), UNS), (decode, dict(kdt=F16), UNS), (decode, dict(odt=F16), UNS), (decode, dict(Hq=7), INV),
     (decode, dict(Hq=18), UNS), (decode, dict(k=0), INV), (decode, dict(scale=0.0), INV), (decode, dict(scale=-1.0), INV),
     (decode, dict(scale=float("nan")), INV), (decode, dict(scale=float("inf")), INV), (decode, dict(ws=None), INV),
     (decode, dict(wsb=0), INV), (decode, dict(out=A[0] + 8), INV), (decode, dict(q=A[1] + 2), INV),
-    (decode, dict(sel=None), INV), (compact, dict(T=-1), INV), (compact, dict(keep=None), INV),
+    (decode, dict(sel=None), INV), (decode, dict(k=(1 << 28) + 1), UNS), (decode, dict(k=1 << 28, N=4000), UNS), (compact, dict(T=-1), INV), (compact, dict(keep=None), INV),
     (compact, dict(base=None), INV), (compact, dict(ks=None), INV)])
 def test_calls_refuse_their_own(call, kw, status):
     assert call(**kw) == status and pa.last_error()
