@@ -28,7 +28,14 @@ constexpr int kSpThreads = 64;
 constexpr int kSpCtas16 = 4, kSpCtas8 = 7;  // CTAs per SM over 16-bit and over e4m3 rows
 constexpr int kSpMaxCtas = 152 * kSpCtas8;
 constexpr int kSpMaxCluster = 8;
-constexpr int kSpClusterRows = 152 * 3 / kSpMaxCluster;  // rows whose clusters the device holds at once
+// Batches that take a cluster per row: as many rows as the device holds clusters of at once (72 over 16-bit rows, four CTAs
+// on an SM, 124 over e4m3 rows, seven; one row more starts a second round).  One kernel instead of two: 8 rows of 64
+// blocks of 16 tokens 6.7 us against 9.4, 64 rows 8.5 against 11.8, 72 rows of 256 blocks 26.8 against 30.3.  Over e4m3
+// rows the SMs that hold more clusters than others finish last once lists are long: 64 rows of 128 blocks 14.5 us against
+// 14.7, of 192 blocks 19.4 against 17.7, so longer lists take runs from 57 rows on.
+constexpr int kSpClusterRows16 = 72, kSpClusterRows8 = 120;
+constexpr int kSpClusterRowsLong = 56, kSpLongTokens = 2048;
+
 constexpr int kMinUnits = 1;       // units a CTA takes at least
 constexpr int kJoinWarps = 8;
 
@@ -73,8 +80,8 @@ struct SpGeo {
     static constexpr int kCtas = kQuant ? kSpCtas8 : kSpCtas16;
     static constexpr int kStages = (233472 / kCtas - 1024 - 1024 - 16) / (int)kPerStage;
     static constexpr size_t kSmem = 1024 + (size_t)kStages * kPerStage + 16;
-    static constexpr size_t kShare = (2 * kMaxGroup + kMaxGroup * D) * sizeof(float);
-    static_assert(kSmem % 16 == 0 && kStages >= 2 && kCtas * (kSmem + 1024) <= 233472, "the CTAs of an SM fit its shared memory");
+    static_assert((2 * kMaxGroup + kMaxGroup * D) * sizeof(float) <= kSlot, "a part fits a stage");
+    static_assert(kStages >= 2 && kCtas * (kSmem + 1024) <= 233472, "the CTAs of an SM fit its shared memory");
 };
 
 __device__ __forceinline__ uint4 sp_lds128(uint32_t a) {
@@ -169,8 +176,9 @@ __global__ void __launch_bounds__(kSpThreads) attend_sparse_kernel(const __grid_
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31;
     const float NEG_INF = -INFINITY;
-    // this CTA's part of its row for the cluster's join: maxima and sums of the query heads, then their outputs
-    float* share = reinterpret_cast<float*>(smem_raw + Geo::kSmem);
+    // This CTA's part of its row for the cluster's join: maxima and sums of the query heads, then their outputs.  It lies
+    // in the ring, which is empty by then: a cluster's CTA has one segment.
+    float* share = reinterpret_cast<float*>(base);
     if constexpr (kCluster) {
         const int ctx = p.ctx_lens[blockIdx.x / p.cluster / p.H_kv];
         if (ctx < 1 || ctx > p.cap) {  // (the whole cluster returns)
@@ -857,11 +865,10 @@ static pa_status run_sparse(const DecodeSparseArgs& a, const SpParams& p, const 
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (p.cluster) {
         auto kern = attend_sparse_kernel<T, kQuant, D, LGB, true>;
-        constexpr size_t smem = Geo::kSmem + Geo::kShare;
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Geo::kSmem);
         if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(attend_sparse)");
-        e = launch_clusters(kern, p.cluster, dim3((unsigned)(a.N * a.H_kv * p.cluster)), dim3(kSpThreads), smem, a.stream, tm,
-                            p);
+        e = launch_clusters(kern, p.cluster, dim3((unsigned)(a.N * a.H_kv * p.cluster)), dim3(kSpThreads), Geo::kSmem,
+                            a.stream, tm, p);
     } else {
         auto kern = attend_sparse_kernel<T, kQuant, D, LGB, false>;
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Geo::kSmem);
@@ -912,7 +919,10 @@ pa_status launch_decode_sparse(const DecodeSparseArgs& a) {
     p.err = a.dev_err;
     const bool quant = a.kv_dtype == PA_E4M3;
     const int64_t rows = (int64_t)a.N * a.H_kv;
-    p.cluster = rows <= kSpClusterRows && (int64_t)a.top_k * a.B >= 2 * kSpMaxCluster * kUnitTok ? kSpMaxCluster : 0;
+    const int64_t tokens = (int64_t)a.top_k * a.B;
+    const int64_t limit = !quant ? kSpClusterRows16 : tokens > kSpLongTokens ? kSpClusterRowsLong : kSpClusterRows8;
+    // (a list shorter than two units per CTA leaves a cluster nothing to share)
+    p.cluster = rows <= limit && tokens >= 2 * kSpMaxCluster * kUnitTok ? kSpMaxCluster : 0;
     pa_status st;
     if (a.q_dtype == PA_BF16)
         st = quant ? run_sparse_shape<__nv_bfloat16, true>(a, p, L) : run_sparse_shape<__nv_bfloat16, false>(a, p, L);
