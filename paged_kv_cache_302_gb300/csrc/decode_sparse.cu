@@ -35,8 +35,6 @@ constexpr int kSpMaxCluster = 8;
 // 14.7, of 192 blocks 19.4 against 17.7, so longer lists take runs from 57 rows on.
 constexpr int kSpClusterRows16 = 72, kSpClusterRows8 = 120;
 constexpr int kSpClusterRowsLong = 56, kSpLongTokens = 2048;
-
-constexpr int kMinUnits = 1;       // units a CTA takes at least
 constexpr int kJoinWarps = 8;
 
 enum : int { kSpFirst = 1, kSpLast = 2, kSpDone = 4 };
@@ -193,7 +191,7 @@ __global__ void __launch_bounds__(kSpThreads) attend_sparse_kernel(const __grid_
         const auto units_of = [&](int s) { return row_units<LGB>(p, p.ctx_lens[s]); };
         const RowScan<decltype(units_of)> scan(units_of, kCluster ? 0 : p.N, p.H_kv);
         const int total = kCluster ? 1 : scan.total();
-        const int ctas = max(1, min((int)gridDim.x, total / kMinUnits));
+        const int ctas = max(1, min((int)gridDim.x, total));
         const Cut cut(total, ctas);
         run.e = run.e_end = run.left = 0;
         run.first = false;
@@ -921,8 +919,7 @@ pa_status launch_decode_sparse(const DecodeSparseArgs& a) {
     const int64_t rows = (int64_t)a.N * a.H_kv;
     const int64_t tokens = (int64_t)a.top_k * a.B;
     const int64_t limit = !quant ? kSpClusterRows16 : tokens > kSpLongTokens ? kSpClusterRowsLong : kSpClusterRows8;
-    // (a list shorter than two units per CTA leaves a cluster nothing to share)
-    p.cluster = rows <= limit && tokens >= 2 * kSpMaxCluster * kUnitTok ? kSpMaxCluster : 0;
+    p.cluster = rows <= limit ? kSpMaxCluster : 0;
     pa_status st;
     if (a.q_dtype == PA_BF16)
         st = quant ? run_sparse_shape<__nv_bfloat16, true>(a, p, L) : run_sparse_shape<__nv_bfloat16, false>(a, p, L);
