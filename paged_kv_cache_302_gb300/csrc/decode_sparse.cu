@@ -27,14 +27,15 @@ constexpr int kUnitTok = 32;       // tokens of a unit: one pipeline stage
 constexpr int kSpThreads = 64;
 constexpr int kSpCtas16 = 4, kSpCtas8 = 7;  // CTAs per SM over 16-bit and over e4m3 rows
 constexpr int kSpMaxCtas = 152 * kSpCtas8;
+// Calls that take a cluster per row: the largest size, up to 8, at which the device holds the clusters of all rows at once
+// (four CTAs on an SM over 16-bit rows, seven over e4m3 rows, not quite all of them in clusters), provided that a CTA's
+// share of the list is short.  One kernel instead of two, and nothing to find: over 16-bit rows 8 rows of 1024 tokens take
+// 6.7 us against 9.4 by runs, 144 rows of 512 tokens 11.6 against 14.0, 512 rows of 256 tokens 18.1 against 19.7; 192
+// rows of 2048 tokens, 1024 to a CTA, 39.1 against 38.1.  Over e4m3 rows 112 rows of 1024 tokens take 11.5 us against
+// 14.7, 256 rows 18.2 against 20.6, 144 rows of 2048 tokens, 512 to a CTA, 25.7 against 22.0.
 constexpr int kSpMaxCluster = 8;
-// Batches that take a cluster per row: as many rows as the device holds clusters of at once (72 over 16-bit rows, four CTAs
-// on an SM, 124 over e4m3 rows, seven; one row more starts a second round).  One kernel instead of two: 8 rows of 64
-// blocks of 16 tokens 6.7 us against 9.4, 64 rows 8.5 against 11.8, 72 rows of 256 blocks 26.8 against 30.3.  Over e4m3
-// rows the SMs that hold more clusters than others finish last once lists are long: 64 rows of 128 blocks 14.5 us against
-// 14.7, of 192 blocks 19.4 against 17.7, so longer lists take runs from 57 rows on.
-constexpr int kSpClusterRows16 = 72, kSpClusterRows8 = 120;
-constexpr int kSpClusterRowsLong = 56, kSpLongTokens = 2048;
+constexpr int kSpRoom16 = 576, kSpRoom8 = 992;    // CTAs that the device holds in clusters
+constexpr int kSpShare16 = 512, kSpShare8 = 256;  // tokens of a CTA's share
 constexpr int kJoinWarps = 8;
 
 enum : int { kSpFirst = 1, kSpLast = 2, kSpDone = 4 };
@@ -917,9 +918,12 @@ pa_status launch_decode_sparse(const DecodeSparseArgs& a) {
     p.err = a.dev_err;
     const bool quant = a.kv_dtype == PA_E4M3;
     const int64_t rows = (int64_t)a.N * a.H_kv;
-    const int64_t tokens = (int64_t)a.top_k * a.B;
-    const int64_t limit = !quant ? kSpClusterRows16 : tokens > kSpLongTokens ? kSpClusterRowsLong : kSpClusterRows8;
-    p.cluster = rows <= limit ? kSpMaxCluster : 0;
+    int size = kSpMaxCluster;
+    while (size > 1 && rows * size > (quant ? kSpRoom8 : kSpRoom16)) size /= 2;
+    p.cluster = rows * size <= (quant ? kSpRoom8 : kSpRoom16) &&
+                        (int64_t)a.top_k * a.B <= (int64_t)size * (quant ? kSpShare8 : kSpShare16)
+                    ? size
+                    : 0;
     pa_status st;
     if (a.q_dtype == PA_BF16)
         st = quant ? run_sparse_shape<__nv_bfloat16, true>(a, p, L) : run_sparse_shape<__nv_bfloat16, false>(a, p, L);

@@ -299,7 +299,9 @@ def want_sparse(q, host, tables, ctx, sel, B, scale, dtype, quant):
     (1, 1, 64, 8, [1], 1), (1, 8, 128, 16, [17, 300], 5), (2, 4, 128, 16, [1000, 16, 555], 64),
     (3, 3, 64, 32, [100, 700, 31, 1], 9), (8, 7, 128, 16, [2000, 130], 40), (5, 2, 64, 8, [400, 2500], 257),
     (2, 5, 128, 32, [3000, 90, 1700], 70), (8, 1, 128, 8, [129] * 20, 12),
-    (8, 4, 128, 16, [1, 900, 333, 50] * 6, 48), (7, 3, 64, 32, [40, 2000, 700] * 9, 50), (1, 2, 64, 8, [300] * 90, 70)])
+    (8, 4, 128, 16, [1, 900, 333, 50] * 6, 48), (7, 3, 64, 32, [40, 2000, 700] * 9, 50), (1, 2, 64, 8, [300] * 90, 70),
+    (8, 4, 128, 16, [700, 90] * 9, 30), (4, 2, 64, 32, [600, 31, 200] * 25, 7), (16, 1, 128, 8, [200, 60, 500] * 11, 33),
+    (16, 3, 64, 16, [500] * 70, 9)])
 def test_attention(H, G, D, B, ctx, top_k, dtype, quant, out32):
     g = torch.Generator().manual_seed(H * 13 + D + top_k)
     MB = -(-max(ctx) // B) + 1
