@@ -1,8 +1,8 @@
 // select.cu -- the blocks of each (sequence, KV head) that block-sparse decode reads, by their key summaries.
 //
 // Two kernels per call: the scores (the format and the score are in summary.cuh), then the top_k of each row -- one
-// (sequence, KV head).  Few rows take one kernel instead, a cluster of CTAs per row, whose scores meet in the shared
-// memory of one of them.
+// (sequence, KV head).  Up to a few hundred rows take one kernel instead, a cluster of CTAs per row, whose scores meet in
+// the shared memory of one of them.
 #include <algorithm>
 #include <type_traits>
 
@@ -22,6 +22,7 @@ struct SelectParams {
     uint32_t* keys;  // [N][H_kv][stride], ordered as the scores
     int64_t stride;
     int N, H_kv, G, lgB, MB, NB, max_ctx, top_k, sink, recent;
+    int cluster;  // CTAs per row where a row is selected by one cluster
     int* err;
 };
 
@@ -426,20 +427,32 @@ __global__ void __launch_bounds__(THREADS) top_blocks_kernel(const SelectParams 
         top_blocks<THREADS, K>(p, nb, p.keys + r * p.stride, p.selected + r * p.top_k);
 }
 
-// Few rows: a cluster per row.  Its warps score a tile each in turn and leave the keys in the first CTA's shared memory,
-// which then lists the row's blocks.
+// Rows whose clusters the device holds at once: a cluster of up to 8 CTAs per row, whose warps score the row's tiles in
+// turn and leave the keys in the first CTA's shared memory, which then lists the row's blocks.  Against two kernels, 8 rows
+// of 1024 blocks take 4.7 us instead of 5.6, 64 rows 9.0 instead of 11.3, 304 rows (one CTA each) 21 instead of 25; 320
+// rows, which no longer fit, 35 instead of 27.  Half the cluster size serves better as long as a warp has no more than two
+// tiles: 64 rows of 256 blocks 5.0 us with 2 CTAs, 5.3 with 4.
 constexpr int kRowCluster = 8;
 constexpr int kRowThreads = 256;
-constexpr int kClusterRows = 152 * 2 / kRowCluster;  // rows whose clusters the device holds at once
-constexpr int kClusterBlocks = kRowThreads * 8;      // keys that the first CTA's threads hold in registers
+constexpr int kRowCtas = 152 * 2;                // CTAs that the device holds at once
+constexpr int kRowBlocks = kRowThreads * 8;      // keys that the first CTA's threads hold in registers
+
+// CTAs per row for rows of up to nb blocks; 0: two kernels.
+static int row_cluster(int64_t rows, int64_t nb) {
+    int size = kRowCluster;
+    while (size > 1 && rows * size > kRowCtas) size /= 2;
+    if (rows * size > kRowCtas || nb > kRowBlocks) return 0;
+    while (size > 1 && 2 * rows * size > kRowCtas && nb <= 2 * 16 * (kRowThreads / 32) * (size / 2)) size /= 2;
+    return size;
+}
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kRowThreads, 2) select_row_kernel(const SelectParams p) {
-    __shared__ __align__(16) uint32_t s_keys[kClusterBlocks];
+    __shared__ __align__(16) uint32_t s_keys[kRowBlocks];
     cluster_arrive();
     griddep_wait();
     griddep_launch_dependents();
-    const int rank = blockIdx.x % kRowCluster, r = blockIdx.x / kRowCluster;
+    const int rank = blockIdx.x % p.cluster, r = blockIdx.x / p.cluster;
     Tile x;
     x.s = r / p.H_kv;
     x.h = r - x.s * p.H_kv;
@@ -451,18 +464,18 @@ __global__ void __launch_bounds__(kRowThreads, 2) select_row_kernel(const Select
         if (rank == 0) all_blocks(p, x.nb, out);
         return;
     }
-    constexpr int kWarps = kRowCluster * kRowThreads / 32;
+    const int warps = p.cluster * (kRowThreads / 32);
     x.tiles = (x.nb + 15) / 16;
-    x.t = (int)(threadIdx.x >> 5) * kRowCluster + rank;
+    x.t = (int)(threadIdx.x >> 5) * p.cluster + rank;
     if (x.t < x.tiles) {
         const uint32_t keys = map_cluster(smem_addr(s_keys), 0);
         Scorer<T, D> scorer(p);
-        scorer.run(x, (x.tiles - x.t + kWarps - 1) / kWarps, [&](Tile& y) { y.t += kWarps; },
+        scorer.run(x, (x.tiles - x.t + warps - 1) / warps, [&](Tile& y) { y.t += warps; },
                    [&](const Tile&, int b, uint32_t key) { st_cluster(keys + 4 * b, key); });
     }
     __syncwarp();
     cluster_sync();
-    if (rank == 0) top_blocks<kRowThreads, kClusterBlocks / kRowThreads>(p, x.nb, s_keys, out);
+    if (rank == 0) top_blocks<kRowThreads, kRowBlocks / kRowThreads>(p, x.nb, s_keys, out);
 }
 
 // Keys of a row, in whole vectors of four.
@@ -503,12 +516,14 @@ pa_status launch_select(const SelectArgs& a) {
     p.recent = a.recent;
     p.err = a.dev_err;
     const int64_t nb = std::min<int64_t>(((int64_t)a.max_ctx + a.B - 1) / a.B, a.MB);  // the longest context's
-    if (nb > a.top_k && nb <= kClusterBlocks && (int64_t)a.N * a.H_kv <= kClusterRows) {
+    const int64_t rows = (int64_t)a.N * a.H_kv;
+    p.cluster = nb > a.top_k ? row_cluster(rows, nb) : 0;
+    if (p.cluster) {
         auto kern = a.q_dtype == PA_BF16
                         ? (a.D == 128 ? select_row_kernel<__nv_bfloat16, 128> : select_row_kernel<__nv_bfloat16, 64>)
                         : (a.D == 128 ? select_row_kernel<__half, 128> : select_row_kernel<__half, 64>);
-        const cudaError_t e = launch_clusters(kern, kRowCluster, dim3((unsigned)(a.N * a.H_kv * kRowCluster)),
-                                              dim3(kRowThreads), 0, a.stream, p);
+        const cudaError_t e = launch_clusters(kern, p.cluster, dim3((unsigned)(rows * p.cluster)), dim3(kRowThreads), 0,
+                                              a.stream, p);
         count_launch();
         return e == cudaSuccess ? PA_OK : cuda_fail(e, "select_row launch");
     }
