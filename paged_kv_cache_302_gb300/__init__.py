@@ -18,6 +18,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import math
+import operator
 import os
 import re
 import threading
@@ -61,6 +62,12 @@ def load(build: bool = True) -> ctypes.CDLL:
             _declare(L)
             _lib = L
     return _lib
+
+
+class _Int:
+    """A C int parameter: ctypes passes a Python int as one by itself, at a third of c_int's cost (a call has a dozen)."""
+
+    from_param = operator.index
 
 
 def _declare(L):
@@ -129,7 +136,7 @@ def _declare(L):
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
-        fn.argtypes = args
+        fn.argtypes = [_Int if a is i32 else a for a in args]
         fn.restype = res
     del i64
 
@@ -204,6 +211,7 @@ def _quant_cache(qpool, scales):
 
 
 _CODES = {torch.float16: PA_F16, torch.bfloat16: PA_BF16, torch.float32: PA_F32}
+_POOL_CODES = {torch.float16: PA_F16, torch.bfloat16: PA_BF16}
 
 
 def _code(t: torch.dtype) -> int:
@@ -213,8 +221,11 @@ def _code(t: torch.dtype) -> int:
 
 def _here(t, name) -> int:
     """Index of the current device, on which `t` must live (the call's kernels run there)."""
-    d = t.get_device() if isinstance(t, torch.Tensor) else None
-    if d is None or d < 0:
+    try:
+        d = t.get_device()
+    except AttributeError:
+        d = -1
+    if d < 0:
         raise PAError(PA_ERR_INVALID, f"{name} must be a tensor on a CUDA device")
     if d != torch._C._cuda_getDevice():
         raise PAError(PA_ERR_INVALID, f"{name} must be on the current device, got cuda:{d}")
@@ -223,9 +234,11 @@ def _here(t, name) -> int:
 
 def _arg(t, name, dev, dtype=None) -> int:
     """Address of a contiguous tensor on device `dev`.  (These checks run at every call: they are kept cheap.)"""
-    if (isinstance(t, torch.Tensor) and t.get_device() == dev and (dtype is None or t.dtype is dtype)
-            and t.is_contiguous()):
-        return t.data_ptr()
+    try:
+        if t.get_device() == dev and (dtype is None or t.dtype is dtype) and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor) or t.get_device() != dev:
         raise PAError(PA_ERR_INVALID, f"{name} must be a tensor on the current CUDA device (cuda:{dev})")
     if dtype is not None and t.dtype != dtype:
@@ -606,19 +619,22 @@ def _cache_shape(pool, scales):
     if scales is not None:
         return _quant_cache(pool, scales) + (PA_E4M3,)
     shape = pool.shape
-    if len(shape) != 5 or shape[2] != 2 or pool.dtype not in (torch.float16, torch.bfloat16):
+    code = _POOL_CODES.get(pool.dtype)
+    if code is None or len(shape) != 5 or shape[2] != 2:
         raise PAError(PA_ERR_INVALID, "without scales the pool must be [NB, B, 2, H_kv, D] fp16 or bf16")
-    return shape[0], shape[3], shape[1], shape[4], _code(pool.dtype)
+    NB, B, _, H_kv, D = shape
+    return NB, H_kv, B, D, code
 
 
 def _summary_shape(summaries, sum_scales):
     """(NB, H_kv, D) of key summaries, after checking that the two tensors are one."""
-    shape = summaries.shape
     if summaries.dtype is not torch.int8 or sum_scales.dtype not in _SCALE_TYPES:
         raise PAError(PA_ERR_INVALID, "summaries must be int8, sum_scales uint8 or float8_e8m0fnu")
+    shape = summaries.shape
     if len(shape) != 4 or shape[2] != 2 or sum_scales.shape != shape[:2]:
         raise PAError(PA_ERR_INVALID, "summaries must be [NB, H_kv, 2, D] and sum_scales [NB, H_kv]")
-    return shape[0], shape[1], shape[3]
+    NB, H_kv, _, D = shape
+    return NB, H_kv, D
 
 
 def pa_summarize_blocks(summaries, sum_scales, pool, block_tables, ctx_lens, max_q_len, q_start=None, scales=None,
