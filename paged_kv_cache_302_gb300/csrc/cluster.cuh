@@ -1,6 +1,8 @@
 // cluster.cuh -- thread-block clusters: barrier, distributed shared memory, launch.
 #pragma once
 
+#include <atomic>
+
 #include "pa_device.cuh"
 
 namespace pa {
@@ -62,5 +64,37 @@ static cudaError_t launch_clusters(void (*kern)(KArgs...), int size, dim3 grid, 
     cfg.numAttrs = pdl_enabled() ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
+
+// Host: how many clusters of 1, 2, 4 or 8 CTAs of a kernel the current device holds at once (its SMs come in groups that a
+// cluster does not cross, so that not all of them fill up).  Asked once per device and kernel.
+class ClusterRoom {
+public:
+    template <typename... KArgs>
+    cudaError_t get(void (*kern)(KArgs...), int size, int threads, size_t smem, int* clusters) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        const int k = size == 8 ? 3 : size == 4 ? 2 : size == 2 ? 1 : 0;
+        std::atomic<int>* slot = dev < kDevices ? &known_[dev][k] : nullptr;
+        if (slot && (*clusters = slot->load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)size;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)size);
+        cfg.blockDim = dim3((unsigned)threads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(clusters, kern, &cfg);
+        if (e == cudaSuccess && slot) slot->store(*clusters, std::memory_order_relaxed);
+        return e;
+    }
+
+private:
+    static constexpr int kDevices = 64;
+    std::atomic<int> known_[kDevices][4] = {};
+};
 
 }  // namespace pa

@@ -28,14 +28,15 @@ constexpr int kSpThreads = 64;
 constexpr int kSpCtas16 = 4, kSpCtas8 = 7;  // CTAs per SM over 16-bit and over e4m3 rows
 constexpr int kSpMaxCtas = 152 * kSpCtas8;
 // Calls that take a cluster per row: the largest size, up to 8, at which the device holds the clusters of all rows at once
-// (four CTAs on an SM over 16-bit rows, seven over e4m3 rows, not quite all of them in clusters), provided that a CTA's
-// share of the list is short.  One kernel instead of two, and nothing to find: over 16-bit rows 8 rows of 1024 tokens take
-// 6.7 us against 9.4 by runs, 144 rows of 512 tokens 11.6 against 14.0, 512 rows of 256 tokens 18.1 against 19.7; 192
-// rows of 2048 tokens, 1024 to a CTA, 39.1 against 38.1.  Over e4m3 rows 112 rows of 1024 tokens take 11.5 us against
-// 14.7, 256 rows 18.2 against 20.6, 144 rows of 2048 tokens, 512 to a CTA, 25.7 against 22.0.
+// (four CTAs on an SM over 16-bit rows, seven over e4m3 rows), provided that a CTA's share of the list is short.  One kernel instead of two, and nothing to find: over 16-bit rows 8 rows of 1024
+// tokens take 6.7 us against 9.4 by runs, 144 rows of 512 tokens 11.6 against 14.0, 512 rows of 256 tokens 18.1 against
+// 19.7; 192 rows of 2048 tokens, 1024 to a CTA, 39.1 against 38.1.  Over e4m3 rows 112 rows of 1024 tokens take 11.5 us
+// against 14.7, 256 rows 18.2 against 20.6; 144 rows of 2048 tokens, 512 to a CTA, 25.7 against 22.0, but 256 such rows,
+// which nearly fill the device, 28.2 against 31.7.
 constexpr int kSpMaxCluster = 8;
-constexpr int kSpRoom16 = 576, kSpRoom8 = 992;    // CTAs that the device holds in clusters
 constexpr int kSpShare16 = 512, kSpShare8 = 256;  // tokens of a CTA's share
+constexpr int kSpShare8Full = 512;                // the same where the clusters fill seven eighths of the device
+
 constexpr int kJoinWarps = 8;
 
 enum : int { kSpFirst = 1, kSpLast = 2, kSpDone = 4 };
@@ -842,8 +843,9 @@ size_t decode_sparse_workspace_bytes(int N, int H_q, int H_kv, int D, int B, int
 }
 
 template <typename T, bool kQuant, int D, int LGB>
-static pa_status run_sparse(const DecodeSparseArgs& a, const SpParams& p, const SparseLayout& L) {
+static pa_status run_sparse(const DecodeSparseArgs& a, SpParams& p, const SparseLayout& L) {
     using Geo = SpGeo<kQuant, D>;
+    constexpr int B = 1 << LGB;
     CUtensorMap tm;
     pa_status st;
     if (kQuant) {
@@ -862,11 +864,24 @@ static pa_status run_sparse(const DecodeSparseArgs& a, const SpParams& p, const 
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    auto in_cluster = attend_sparse_kernel<T, kQuant, D, LGB, true>;
+    e = cudaFuncSetAttribute(in_cluster, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Geo::kSmem);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(attend_sparse)");
+    static ClusterRoom room;
+    const int64_t rows = (int64_t)a.N * a.H_kv, tokens = (int64_t)a.top_k * B;
+    constexpr int kShare = kQuant ? kSpShare8 : kSpShare16, kShareFull = kQuant ? kSpShare8Full : kSpShare16;
+    p.cluster = 0;
+    for (int size = kSpMaxCluster; size > 0; size /= 2) {
+        if (tokens > (int64_t)size * kShareFull) break;
+        int held = 0;
+        e = room.get(in_cluster, size, kSpThreads, Geo::kSmem, &held);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveClusters(attend_sparse)");
+        if (rows > held) continue;
+        if (tokens <= (int64_t)size * (8 * rows >= 7 * (int64_t)held ? kShareFull : kShare)) p.cluster = size;
+        break;
+    }
     if (p.cluster) {
-        auto kern = attend_sparse_kernel<T, kQuant, D, LGB, true>;
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Geo::kSmem);
-        if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(attend_sparse)");
-        e = launch_clusters(kern, p.cluster, dim3((unsigned)(a.N * a.H_kv * p.cluster)), dim3(kSpThreads), Geo::kSmem,
+        e = launch_clusters(in_cluster, p.cluster, dim3((unsigned)(rows * p.cluster)), dim3(kSpThreads), Geo::kSmem,
                             a.stream, tm, p);
     } else {
         auto kern = attend_sparse_kernel<T, kQuant, D, LGB, false>;
@@ -880,7 +895,7 @@ static pa_status run_sparse(const DecodeSparseArgs& a, const SpParams& p, const 
 }
 
 template <typename T, bool kQuant>
-static pa_status run_sparse_shape(const DecodeSparseArgs& a, const SpParams& p, const SparseLayout& L) {
+static pa_status run_sparse_shape(const DecodeSparseArgs& a, SpParams& p, const SparseLayout& L) {
     if (a.D == 128)
         return a.B == 8    ? run_sparse<T, kQuant, 128, 3>(a, p, L)
                : a.B == 16 ? run_sparse<T, kQuant, 128, 4>(a, p, L)
@@ -917,13 +932,6 @@ pa_status launch_decode_sparse(const DecodeSparseArgs& a) {
     p.wait_ns = wait_limit_ns();
     p.err = a.dev_err;
     const bool quant = a.kv_dtype == PA_E4M3;
-    const int64_t rows = (int64_t)a.N * a.H_kv;
-    int size = kSpMaxCluster;
-    while (size > 1 && rows * size > (quant ? kSpRoom8 : kSpRoom16)) size /= 2;
-    p.cluster = rows * size <= (quant ? kSpRoom8 : kSpRoom16) &&
-                        (int64_t)a.top_k * a.B <= (int64_t)size * (quant ? kSpShare8 : kSpShare16)
-                    ? size
-                    : 0;
     pa_status st;
     if (a.q_dtype == PA_BF16)
         st = quant ? run_sparse_shape<__nv_bfloat16, true>(a, p, L) : run_sparse_shape<__nv_bfloat16, false>(a, p, L);

@@ -434,17 +434,7 @@ __global__ void __launch_bounds__(THREADS) top_blocks_kernel(const SelectParams 
 // tiles: 64 rows of 256 blocks 5.0 us with 2 CTAs, 5.3 with 4.
 constexpr int kRowCluster = 8;
 constexpr int kRowThreads = 256;
-constexpr int kRowCtas = 152 * 2;                // CTAs that the device holds at once
-constexpr int kRowBlocks = kRowThreads * 8;      // keys that the first CTA's threads hold in registers
-
-// CTAs per row for rows of up to nb blocks; 0: two kernels.
-static int row_cluster(int64_t rows, int64_t nb) {
-    int size = kRowCluster;
-    while (size > 1 && rows * size > kRowCtas) size /= 2;
-    if (rows * size > kRowCtas || nb > kRowBlocks) return 0;
-    while (size > 1 && 2 * rows * size > kRowCtas && nb <= 2 * 16 * (kRowThreads / 32) * (size / 2)) size /= 2;
-    return size;
-}
+constexpr int kRowBlocks = kRowThreads * 8;  // keys that the first CTA's threads hold in registers
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kRowThreads, 2) select_row_kernel(const SelectParams p) {
@@ -517,15 +507,42 @@ pa_status launch_select(const SelectArgs& a) {
     p.err = a.dev_err;
     const int64_t nb = std::min<int64_t>(((int64_t)a.max_ctx + a.B - 1) / a.B, a.MB);  // the longest context's
     const int64_t rows = (int64_t)a.N * a.H_kv;
-    p.cluster = nb > a.top_k ? row_cluster(rows, nb) : 0;
-    if (p.cluster) {
-        auto kern = a.q_dtype == PA_BF16
-                        ? (a.D == 128 ? select_row_kernel<__nv_bfloat16, 128> : select_row_kernel<__nv_bfloat16, 64>)
-                        : (a.D == 128 ? select_row_kernel<__half, 128> : select_row_kernel<__half, 64>);
-        const cudaError_t e = launch_clusters(kern, p.cluster, dim3((unsigned)(rows * p.cluster)), dim3(kRowThreads), 0,
-                                              a.stream, p);
-        count_launch();
-        return e == cudaSuccess ? PA_OK : cuda_fail(e, "select_row launch");
+    if (nb > a.top_k && nb <= kRowBlocks) {
+        void (*kern)(SelectParams);
+        ClusterRoom* room;
+        auto pick = [&](auto q, auto d) {
+            static ClusterRoom of_kernel;
+            kern = select_row_kernel<decltype(q), decltype(d)::value>;
+            room = &of_kernel;
+        };
+        auto by_dim = [&](auto q) {
+            if (a.D == 128)
+                pick(q, std::integral_constant<int, 128>());
+            else
+                pick(q, std::integral_constant<int, 64>());
+        };
+        if (a.q_dtype == PA_BF16)
+            by_dim(__nv_bfloat16());
+        else
+            by_dim(__half());
+        p.cluster = 0;
+        for (int size = kRowCluster; size > 0; size /= 2) {
+            int held = 0;
+            const cudaError_t e = room->get(kern, size, kRowThreads, 0, &held);
+            if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveClusters(select_row)");
+            const bool enough = size == 1 || nb > 2 * 16 * (kRowThreads / 32) * (size / 2);
+            // (half the room where half the size would do)
+            if (rows <= (enough ? held : held / 2)) {
+                p.cluster = size;
+                break;
+            }
+        }
+        if (p.cluster) {
+            const cudaError_t e = launch_clusters(kern, p.cluster, dim3((unsigned)(rows * p.cluster)), dim3(kRowThreads), 0,
+                                                  a.stream, p);
+            count_launch();
+            return e == cudaSuccess ? PA_OK : cuda_fail(e, "select_row launch");
+        }
     }
     if (nb > a.top_k) {
         const int64_t tiles = (nb + 15) / 16 * a.N * a.H_kv;
