@@ -246,10 +246,9 @@ __global__ void __launch_bounds__(kScoreWarps * 32, kScoreCtas) score_kernel(con
 }
 
 // The top_k of a row with more blocks than that: one CTA, each thread with neighbouring keys, in registers (K of them) or read anew
-// (K = 0).  The key of the last block taken is found by a histogram over the eight bits below those that all competing
-// keys share, then among the keys of one bin: ranked against one another where there are no more than threads' worth of
-// them, else by the next eight bits.  One scan then gives every taken block its place.
-constexpr int kBins = 256;
+// (K = 0).  The key of the last block taken is found by a histogram over the bits below those that all competing keys
+// share, eight at a time (seven for 128 threads), then among the keys of one bin: ranked against one another where there
+// are no more than bins, else by their next bits.  One scan then gives every taken block its place.
 
 // Key k competes and agrees with the prefix above its low `open` bits.
 __device__ __forceinline__ bool agree(uint32_t k, uint32_t prefix, int open) {
@@ -259,6 +258,7 @@ __device__ __forceinline__ bool agree(uint32_t k, uint32_t prefix, int open) {
 template <int THREADS, int K>
 __device__ __forceinline__ void top_blocks(const SelectParams& p, int nb, const uint32_t* keys, int32_t* out) {
     constexpr int W = THREADS / 32;
+    constexpr int kBits = THREADS >= 256 ? 8 : 7, kBins = 1 << kBits;  // a bin per thread
     static_assert(THREADS >= kBins, "a thread per bin");
     __shared__ uint2 s_sum[W];
     __shared__ uint32_t s_bin[kBins], s_list[kBins], s_warp[kBins / 32];
@@ -314,9 +314,9 @@ __device__ __forceinline__ void top_blocks(const SelectParams& p, int nb, const 
         int open = 32 - __clz(lo ^ hi);
         uint32_t prefix = hi;
         while (true) {
-            const int shift = max(0, open - 8);
+            const int shift = max(0, open - kBits);
             each([&](uint32_t k, int) {
-                if (agree(k, prefix, open)) atomicAdd(&s_bin[k >> shift & 255], 1u);
+                if (agree(k, prefix, open)) atomicAdd(&s_bin[k >> shift & (kBins - 1)], 1u);
             });
             __syncthreads();
             // thread t: bin 255 - t, and the keys in higher bins
@@ -432,13 +432,16 @@ __global__ void __launch_bounds__(THREADS) top_blocks_kernel(const SelectParams 
 // of 1024 blocks take 4.7 us instead of 5.6, 64 rows 9.0 instead of 11.3, 304 rows (one CTA each) 21 instead of 25; 320
 // rows, which no longer fit, 35 instead of 27.  Half the cluster size serves better as long as a warp has no more than two
 // tiles: 64 rows of 256 blocks 5.0 us with 2 CTAs, 5.3 with 4.
+// Twice as many rows fit as CTAs of half the threads, which serve short rows: 512 rows of 256 blocks 12.8 us against 17.3
+// with two kernels, 512 rows of up to 1024 blocks 31 against 25.
 constexpr int kRowCluster = 8;
-constexpr int kRowThreads = 256;
-constexpr int kRowBlocks = kRowThreads * 8;  // keys that the first CTA's threads hold in registers
+constexpr int kRowThreads = 256, kRowBlocks = kRowThreads * 8;    // (eight keys to a thread of the first CTA)
+constexpr int kShortThreads = 128, kShortBlocks = kShortThreads * 4;
+constexpr int kShortMax = 256;  // blocks of a row that still is a short one
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kRowThreads, 2) select_row_kernel(const SelectParams p) {
-    __shared__ __align__(16) uint32_t s_keys[kRowBlocks];
+template <typename T, int D, int THREADS, int BLOCKS>
+__global__ void __launch_bounds__(THREADS, 512 / THREADS) select_row_kernel(const SelectParams p) {
+    __shared__ __align__(16) uint32_t s_keys[BLOCKS];
     cluster_arrive();
     griddep_wait();
     griddep_launch_dependents();
@@ -454,7 +457,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) select_row_kernel(const Select
         if (rank == 0) all_blocks(p, x.nb, out);
         return;
     }
-    const int warps = p.cluster * (kRowThreads / 32);
+    const int warps = p.cluster * (THREADS / 32);
     x.tiles = (x.nb + 15) / 16;
     x.t = (int)(threadIdx.x >> 5) * p.cluster + rank;
     if (x.t < x.tiles) {
@@ -465,7 +468,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) select_row_kernel(const Select
     }
     __syncwarp();
     cluster_sync();
-    if (rank == 0) top_blocks<kRowThreads, kRowBlocks / kRowThreads>(p, x.nb, s_keys, out);
+    if (rank == 0) top_blocks<THREADS, BLOCKS / THREADS>(p, x.nb, s_keys, out);
 }
 
 // Keys of a row, in whole vectors of four.
@@ -509,11 +512,14 @@ pa_status launch_select(const SelectArgs& a) {
     const int64_t rows = (int64_t)a.N * a.H_kv;
     if (nb > a.top_k && nb <= kRowBlocks) {
         void (*kern)(SelectParams);
-        ClusterRoom* room;
+        void (*shorter)(SelectParams);
+        ClusterRoom *room, *shorter_room;
         auto pick = [&](auto q, auto d) {
-            static ClusterRoom of_kernel;
-            kern = select_row_kernel<decltype(q), decltype(d)::value>;
-            room = &of_kernel;
+            static ClusterRoom of_kern, of_shorter;
+            kern = select_row_kernel<decltype(q), decltype(d)::value, kRowThreads, kRowBlocks>;
+            shorter = select_row_kernel<decltype(q), decltype(d)::value, kShortThreads, kShortBlocks>;
+            room = &of_kern;
+            shorter_room = &of_shorter;
         };
         auto by_dim = [&](auto q) {
             if (a.D == 128)
@@ -537,9 +543,20 @@ pa_status launch_select(const SelectArgs& a) {
                 break;
             }
         }
+        int threads = kRowThreads;
+        if (!p.cluster && nb <= kShortMax) {
+            int held = 0;
+            const cudaError_t e = shorter_room->get(shorter, 1, kShortThreads, 0, &held);
+            if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveClusters(select_row)");
+            if (rows <= held) {
+                p.cluster = 1;
+                kern = shorter;
+                threads = kShortThreads;
+            }
+        }
         if (p.cluster) {
-            const cudaError_t e = launch_clusters(kern, p.cluster, dim3((unsigned)(rows * p.cluster)), dim3(kRowThreads), 0,
-                                                  a.stream, p);
+            const cudaError_t e = launch_clusters(kern, p.cluster, dim3((unsigned)(rows * p.cluster)),
+                                                  dim3((unsigned)threads), 0, a.stream, p);
             count_launch();
             return e == cudaSuccess ? PA_OK : cuda_fail(e, "select_row launch");
         }

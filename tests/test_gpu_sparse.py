@@ -182,7 +182,8 @@ def check_select(q, box, by, tables, ctx, B, top_k, sink, recent, H, flag=0, max
     (8, 8, 128, 8, [3000, 130, 8000], 33, 0, 0), (5, 2, 128, 16, [700, 1500], 40, 20, 20),
     (2, 5, 64, 8, [20000, 123], 500, 4, 16), (1, 6, 128, 32, [40000], 1000, 1, 1),
     (1, 2, 64, 8, [70000], 300, 1, 2), (1, 1, 64, 8, [140000, 3], 2000, 1, 1), (8, 1, 64, 16, [700, 90, 3000] * 3, 9, 1, 1),
-    (16, 2, 128, 8, [2000, 64] * 9, 30, 1, 0), (16, 1, 64, 32, [900] * 20, 5, 0, 1)])
+    (16, 2, 128, 8, [2000, 64] * 9, 30, 1, 0), (16, 1, 64, 32, [900] * 20, 5, 0, 1),
+    (16, 2, 128, 8, [700, 2048, 9] * 7, 40, 1, 1), (40, 1, 64, 16, [4000, 33] * 5, 17, 2, 0)])
 def test_selection(H, G, D, B, ctx, top_k, sink, recent, dtype):
     g = torch.Generator().manual_seed(H * 31 + D + len(ctx))
     MB = -(-max(ctx) // B) + 1
