@@ -65,7 +65,7 @@ def load(build: bool = True) -> ctypes.CDLL:
 
 
 class _Int:
-    """A C int parameter: ctypes passes a Python int as one by itself, at a third of c_int's cost (a call has a dozen)."""
+    """A C int parameter: ctypes passes a Python int as one by itself, cheaper than through c_int (a call has a dozen)."""
 
     from_param = operator.index
 

@@ -444,8 +444,8 @@ pa_status pa_decode_tree(void* out, pa_dtype out_dtype, const void* q, pa_dtype 
 // ----------------------------------------------------------------------------- block-sparse decode, compaction
 
 // Sizes that the calls over a cache of either kind and its block tables share.
-static pa_status check_paged_cache(pa_dtype kv_dtype, const void* pool, const void* scales, int N, int H_kv, int D, int B,
-                                   int MB, int NB) {
+static pa_status check_paged_cache(pa_dtype kv_dtype, const void* pool, const void* scales, int N, int H_kv, int D,
+                                   int B, int MB, int NB) {
     if (!kv_dtype_ok(kv_dtype) && kv_dtype != PA_E4M3)
         return fail(PA_ERR_UNSUPPORTED, "kv_dtype must be F16, BF16 or E4M3");
     if (N <= 0 || N > 65535 || MB <= 0) return fail(PA_ERR_INVALID, "bad sizes");

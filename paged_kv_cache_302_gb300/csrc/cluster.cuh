@@ -18,8 +18,8 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// The same in two halves, neither of which orders memory: after the second every CTA of the cluster has started, so that
-// its shared memory may be written.
+// The same in two halves, neither of which orders memory: after the second every CTA of the cluster has started, so
+// that its shared memory may be written.
 __device__ __forceinline__ void cluster_arrive() {
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 }
@@ -47,8 +47,8 @@ __device__ __forceinline__ void st_cluster(uint32_t a, uint32_t v) {
 
 // Host: as launch_kernel, in clusters of `size` CTAs.
 template <typename... KArgs, typename... Args>
-static cudaError_t launch_clusters(void (*kern)(KArgs...), int size, dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-                                   Args&&... args) {
+static cudaError_t launch_clusters(void (*kern)(KArgs...), int size, dim3 grid, dim3 block, size_t smem,
+                                   cudaStream_t st, Args&&... args) {
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = (unsigned)size;
@@ -65,8 +65,8 @@ static cudaError_t launch_clusters(void (*kern)(KArgs...), int size, dim3 grid, 
     return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
 
-// Host: how many clusters of 1, 2, 4 or 8 CTAs of a kernel the current device holds at once (its SMs come in groups that a
-// cluster does not cross, so that not all of them fill up).  Asked once per device and kernel.
+// Host: how many clusters of 1, 2, 4 or 8 CTAs of a kernel the current device holds at once (its SMs come in groups
+// that a cluster does not cross, so that not all of them fill up).  Asked once per device and kernel.
 class ClusterRoom {
 public:
     template <typename... KArgs>

@@ -5,14 +5,20 @@
 // equal length, one run per CTA, so that every CTA reads as much as the others whatever the batch.  A row that lies
 // inside a run is finished there; of a row that a cut divides, each CTA writes its part's maximum, sum and output, and
 // join_sparse_kernel joins them.  A CTA is two warps.  Warp 0 (producer) finds the run, walks the lists, drops padding
-// and bad entries, and streams the blocks' K and V of the row's head through a ring of shared-memory stages of 32 tokens
-// by TMA, the row's query heads with its first stage.  Warp 1 (consumer) computes with mma.sync m16n8k16 (tokens on M,
-// the <= 8 query heads of the KV head on N) and an online softmax in base 2, over 16-bit rows as
+// and bad entries, and streams the blocks' K and V of the row's head through a ring of shared-memory stages of 32
+// tokens by TMA, the row's query heads with its first stage.  Warp 1 (consumer) computes with mma.sync m16n8k16 (tokens
+// on M, the <= 8 query heads of the KV head on N) and an online softmax in base 2, over 16-bit rows as
 //     S^T = K Q^T,  O^T += V^T P^T  with P in a high and a low 16-bit part,
 // and over e4m3 rows (quant.cuh) with rows converted to fp16 in registers, exactly, as
 //     raw = K8 q'^T,  y = raw 2^ek c + ev,  p = 2^(y - M),  O += p V8,  l += p 2^-ev:
 // the exponent of V's scale inside the maximum keeps p <= 1 next to the e4m3 values it weighs, |ev| <= 40 keeps l in
 // fp32.  q' is the query in fp16, a bf16 one scaled row by row with a power of two.
+// Short lists and few rows take one kernel instead, a cluster of CTAs per row (below).
+//
+// Bound by memory, 4 D (2 D + 2) bytes per listed token and head: 64 sequences of 128 blocks of 16 tokens, 8 heads (528
+// MB) take 87 us, 6.1 TB/s, a plain kernel with a CTA per row 556; 16 of 256 blocks over e4m3 rows (136 MB) 33.4 us,
+// 4.1 TB/s: five of them pass before the first block arrives (lengths, list, block table, block), three in the join.
+// One sequence of 64 blocks, by clusters: 6.7 us on the device.
 #include <algorithm>
 #include <type_traits>
 
@@ -27,16 +33,16 @@ constexpr int kUnitTok = 32;       // tokens of a unit: one pipeline stage
 constexpr int kSpThreads = 64;
 constexpr int kSpCtas16 = 4, kSpCtas8 = 7;  // CTAs per SM over 16-bit and over e4m3 rows
 constexpr int kSpMaxCtas = 152 * kSpCtas8;
-// Calls that take a cluster per row: the largest size, up to 8, at which the device holds the clusters of all rows at once
-// (four CTAs on an SM over 16-bit rows, seven over e4m3 rows), provided that a CTA's share of the list is short.  One kernel instead of two, and nothing to find: over 16-bit rows 8 rows of 1024
-// tokens take 6.7 us against 9.4 by runs, 144 rows of 512 tokens 11.6 against 14.0, 512 rows of 256 tokens 18.1 against
-// 19.7; 192 rows of 2048 tokens, 1024 to a CTA, 39.1 against 38.1.  Over e4m3 rows 112 rows of 1024 tokens take 11.5 us
-// against 14.7, 256 rows 18.2 against 20.6; 144 rows of 2048 tokens, 512 to a CTA, 25.7 against 22.0, but 256 such rows,
-// which nearly fill the device, 28.2 against 31.7.
+// Calls that take a cluster per row: the largest size, up to 8, at which the device holds the clusters of all rows at
+// once (four CTAs on an SM over 16-bit rows, seven over e4m3 rows), provided that a CTA's share of the list is short.
+// One kernel instead of two, and nothing to find: over 16-bit rows 8 rows of 1024 tokens take 6.7 us against 9.4 by
+// runs, 144 rows of 512 tokens 11.6 against 14.0, 512 rows of 256 tokens 18.1 against 19.7; 192 rows of 2048 tokens,
+// 1024 to a CTA, 39.1 against 38.1.  Over e4m3 rows 112 rows of 1024 tokens take 11.5 us against 14.7, 256 rows 18.2
+// against 20.6; 144 rows of 2048 tokens, 512 to a CTA, 25.7 against 22.0, but 256 such rows, which nearly fill the
+// device, 28.2 against 31.7.
 constexpr int kSpMaxCluster = 8;
 constexpr int kSpShare16 = 512, kSpShare8 = 256;  // tokens of a CTA's share
 constexpr int kSpShare8Full = 512;                // the same where the clusters fill seven eighths of the device
-
 constexpr int kJoinWarps = 8;
 
 enum : int { kSpFirst = 1, kSpLast = 2, kSpDone = 4 };
@@ -61,7 +67,7 @@ struct SpParams {
     int64_t cap;       // tokens a block-table row holds
     float scale_log2;
     int2* cuts;        // [N * H_kv]: first and last CTA of a divided row, (-1, -1) for a whole one
-    float* part_m;     // [2 * CTAs][G]: part 2 c is of the row that CTA c continues, 2 c + 1 of the one it leaves unfinished
+    float* part_m;     // [2 * CTAs][G]: part 2 c of the row that CTA c continues, 2 c + 1 of the one it leaves open
     float* part_l;
     float* part_acc;   // [2 * CTAs][G][D]
     int cluster;       // CTAs per row where the parts are joined over a cluster
@@ -176,8 +182,8 @@ __global__ void __launch_bounds__(kSpThreads) attend_sparse_kernel(const __grid_
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31;
     const float NEG_INF = -INFINITY;
-    // This CTA's part of its row for the cluster's join: maxima and sums of the query heads, then their outputs.  It lies
-    // in the ring, which is empty by then: a cluster's CTA has one segment.
+    // This CTA's part of its row for the cluster's join: maxima and sums of the query heads, then their outputs.  It
+    // lies in the ring, which is empty by then: a cluster's CTA has one segment.
     float* share = reinterpret_cast<float*>(base);
     if constexpr (kCluster) {
         const int ctx = p.ctx_lens[blockIdx.x / p.cluster / p.H_kv];
@@ -247,7 +253,7 @@ __global__ void __launch_bounds__(kSpThreads) attend_sparse_kernel(const __grid_
                 const int src = rest ? __ffs(rest) - 1 : 0;
                 rest &= rest - 1;
                 const int n = __shfl_sync(0xffffffffu, nv, src), e = __shfl_sync(0xffffffffu, blk, src);
-                if (i < nb) seen |= (B == 32 ? (n >= 32 ? 0xffffffffu : (1u << n) - 1u) : ((1u << n) - 1u) << (i * B % 32));
+                if (i < nb) seen |= (n < 32 ? (1u << n) - 1u : 0xffffffffu) << (i * B % 32);
                 if (i == b) mine = e;
             }
             if (lane == 0) {
@@ -257,10 +263,10 @@ __global__ void __launch_bounds__(kSpThreads) attend_sparse_kernel(const __grid_
                 m.seen = seen;
                 m.part = part;
                 meta[slot] = m;
-                mbar_arrive_expect_tx(bar, (uint32_t)nb * (kBox + (kQuant ? 2 * B : 0)) + (first ? (uint32_t)p.G * D * 2 : 0u));
+                const uint32_t q_bytes = first ? (uint32_t)p.G * D * 2 : 0u;
+                mbar_arrive_expect_tx(bar, (uint32_t)nb * (kBox + (kQuant ? 2 * B : 0)) + q_bytes);
                 if (first)
-                    bulk_load(q_s + slot * Geo::kQ, static_cast<const T*>(p.q) + (int64_t)row * p.G * D, (uint32_t)p.G * D * 2,
-                              bar);
+                    bulk_load(q_s + slot * Geo::kQ, static_cast<const T*>(p.q) + (int64_t)row * p.G * D, q_bytes, bar);
             }
             __syncwarp();
             if (b < nb) {
@@ -268,8 +274,8 @@ __global__ void __launch_bounds__(kSpThreads) attend_sparse_kernel(const __grid_
                     if (lane < 16)
                         tma_load_3d(slots_s + slot * Geo::kSlot + b * kBox, &tm, bar, 0, 0, mine * p.H_kv + h, pol);
                     else
-                        bulk_load(sc_s + slot * Geo::kScales + b * 2 * B, p.scales + ((int64_t)mine * p.H_kv + h) * (2 * B),
-                                  2 * B, bar);
+                        bulk_load(sc_s + slot * Geo::kScales + b * 2 * B,
+                                  p.scales + ((int64_t)mine * p.H_kv + h) * (2 * B), 2 * B, bar);
                 } else if (lane < 16) {
                     tma_load_5d(slots_s + slot * Geo::kSlot + b * kBox, &tm, bar, 0, mine * B, 0, h, 0, pol);
                 }
@@ -384,334 +390,339 @@ __global__ void __launch_bounds__(kSpThreads) attend_sparse_kernel(const __grid_
 
     // ---------------------------------------------------------------------- consumer warp
     auto consume = [&]() {
-    const int g4 = lane >> 2, t4 = lane & 3;
-    float O[NT][4];
-    uint32_t qf[NT][2];
-    float m0 = NEG_INF, m1 = NEG_INF, l0 = 0.f, l1 = 0.f;
-    float c0 = p.scale_log2, c1 = p.scale_log2;  // raw scores of heads 2 t4, 2 t4 + 1 to base-2 units
-    int slot = 0;
-    uint32_t fphase = 0;
+        const int g4 = lane >> 2, t4 = lane & 3;
+        float O[NT][4];
+        uint32_t qf[NT][2];
+        float m0 = NEG_INF, m1 = NEG_INF, l0 = 0.f, l1 = 0.f;
+        float c0 = p.scale_log2, c1 = p.scale_log2;  // raw scores of heads 2 t4, 2 t4 + 1 to base-2 units
+        int slot = 0;
+        uint32_t fphase = 0;
 
-    // Addresses.  e4m3: the thread holds token rt (and rt + 8) of each tile of K, in an order of the 8 rows that
-    // spreads the 16- and 8-byte reads of both products over all banks under the stage's swizzle, and of V^T the
-    // elements from d0 on of tokens va, vb (and + 8), the ones whose probabilities the score product left in rows 2 t4
-    // and 2 t4 + 1.  16 bit: ldmatrix rows.
-    auto row_token = [](int i) -> int {
-        return D == 128 ? ((i >> 1) | ((i & 1) << 2)) : (int)((0x65742130u >> (4 * i)) & 7u);
-    };
-    const int rt = kQuant ? row_token(g4) : g4;
-    auto qtok_ofs = [](int n) -> uint32_t { return (uint32_t)((n >> LGB) * 2 * B + (n & (B - 1))) * D; };
-    auto qsc_ofs = [](int n) -> uint32_t { return (uint32_t)((n >> LGB) * 2 * B + (n & (B - 1))); };
-    const uint32_t qk_ofs = D == 128 ? rt * 128 + ((t4 ^ rt) << 4) : rt * 64 + ((t4 ^ (rt >> 1 & 3)) << 4);
-    const int va = row_token(2 * t4), vb = row_token(2 * t4 + 1);
-    const int vch = D == 128 ? row_token(g4) : g4;
-    const int d0 = vch * 2 * NT;
-    auto qv_ofs = [&](int tok) -> uint32_t {
-        return (uint32_t)(B * D) + (D == 128 ? tok * 128 + ((vch ^ tok) << 4)
-                                             : tok * 64 + (((vch >> 1) ^ (tok >> 1 & 3)) << 4) + ((vch & 1) << 3));
-    };
-    uint32_t kofs[NSUB][DH], kx[NSUB][DH], vofs[NSUB][DH], vx[NSUB][DH];
-    if constexpr (!kQuant) {
-        const int k_tok = (lane & 7) + ((lane >> 3) & 1) * 8, k_hi = lane >> 4;
-        const int v_tok = (lane & 7) + ((lane >> 4) & 1) * 8, v_hi = (lane >> 3) & 1;
-#pragma unroll
-        for (int j = 0; j < NSUB; ++j)
-#pragma unroll
-            for (int dh = 0; dh < DH; ++dh) {
-                int tok = 16 * j + k_tok;
-                int row = (tok >> LGB) * (2 * DH * B) + dh * B + (tok & (B - 1));
-                kofs[j][dh] = (uint32_t)row * 128;
-                kx[j][dh] = (uint32_t)((k_hi ^ (row & 7)) << 4);
-                tok = 16 * j + v_tok;
-                row = (tok >> LGB) * (2 * DH * B) + (DH + dh) * B + (tok & (B - 1));
-                vofs[j][dh] = (uint32_t)row * 128;
-                vx[j][dh] = (uint32_t)((v_hi ^ (row & 7)) << 4);
-            }
-    }
-
-    while (true) {
-        if (!mbar_wait_bounded(full_s + 8 * slot, fphase, abort_flag, p.wait_ns)) {
-            if (lane == 0) {
-                flag_error(p.err, PA_DEV_ERR_TIMEOUT);
-                *abort_flag = 1;
-            }
-            break;
-        }
-        const SpMeta mt = meta[slot];
-        if (mt.flags & kSpDone) break;
-        const uint32_t kv = slots_s + slot * Geo::kSlot, scb = sc_s + slot * Geo::kScales;
-        if (mt.flags & kSpFirst) {
-            if constexpr (kQuant) {
-                float a = 0.f;
-                const uint32_t qrow = q_s + slot * Geo::kQ + g4 * D * 2 + t4 * 32;
-#pragma unroll
-                for (int w = 0; w < NT; ++w) {
-                    const uint2 x = g4 < p.G ? sp_lds64(qrow + (w >> 2) * 128 + (w & 3) * 8) : make_uint2(0, 0);
-                    qf[w][0] = x.x;
-                    qf[w][1] = x.y;
-                    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-                        const float2 f0 = Mma<T>::unpack(x.x), f1 = Mma<T>::unpack(x.y);
-                        a = fmaxf(a, fmaxf(fmaxf(fabsf(f0.x), fabsf(f0.y)), fmaxf(fabsf(f1.x), fabsf(f1.y))));
-                    }
-                }
-                c0 = c1 = p.scale_log2;
-                if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-                    // The row's largest magnitude goes to [2^14, 2^15): elements down to 2^-28 of it are normal fp16
-                    // numbers and exact, smaller ones are off by at most 2^-40 of it.
-                    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
-                    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
-                    const int ex = (int)(__float_as_uint(a) >> 23) - 127;
-                    const int e = ex > 127 || a == 0.f ? 0 : max(ex - 14, -126);
-                    const float inv = pow2i(-e);
-#pragma unroll
-                    for (int w = 0; w < NT; ++w)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const float2 f = Mma<T>::unpack(qf[w][i]);
-                            qf[w][i] = Mma<__half>::pack(f.x * inv, f.y * inv);
-                        }
-                    const float up = pow2i(e);
-                    c0 *= __shfl_sync(0xffffffffu, up, 8 * t4);  // lane 4 n holds head n's
-                    c1 *= __shfl_sync(0xffffffffu, up, 8 * t4 + 4);
-                }
-            } else {
-                const uint8_t* qs = q_g + (size_t)slot * Geo::kQ;
-#pragma unroll
-                for (int ks = 0; ks < NT; ++ks) {
-                    const int d = 16 * ks + 2 * t4;
-                    qf[ks][0] = g4 < p.G ? *reinterpret_cast<const uint32_t*>(qs + ((size_t)g4 * D + d) * 2) : 0u;
-                    qf[ks][1] = g4 < p.G ? *reinterpret_cast<const uint32_t*>(qs + ((size_t)g4 * D + d + 8) * 2) : 0u;
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < NT; ++i) O[i][0] = O[i][1] = O[i][2] = O[i][3] = 0.f;
-            m0 = m1 = NEG_INF;
-            l0 = l1 = 0.f;
-        }
-        // the running maximum moves to n0, n1
-        auto rescale = [&](float n0, float n1) {
-            const float a0 = fast_exp2(m0 - n0), a1 = fast_exp2(m1 - n1);
-            m0 = n0;
-            m1 = n1;
-            if (__any_sync(0xffffffffu, a0 != 1.f || a1 != 1.f)) {
-#pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    O[i][0] *= a0;
-                    O[i][1] *= a1;
-                    O[i][2] *= a0;
-                    O[i][3] *= a1;
-                }
-                l0 *= a0;
-                l1 *= a1;
-            }
+        // Addresses.  e4m3: the thread holds token rt (and rt + 8) of each tile of K, in an order of the 8 rows that
+        // spreads the 16- and 8-byte reads of both products over all banks under the stage's swizzle, and of V^T the
+        // elements from d0 on of tokens va, vb (and + 8), the ones whose probabilities the score product left in rows 2
+        // t4 and 2 t4 + 1.  16 bit: ldmatrix rows.
+        auto row_token = [](int i) -> int {
+            return D == 128 ? ((i >> 1) | ((i & 1) << 2)) : (int)((0x65742130u >> (4 * i)) & 7u);
         };
-        // one copy for whole stages, without a branch between the tiles, and one for the others
-        auto stage = [&](auto full_c) {
-            constexpr bool kFull = decltype(full_c)::value;
-            float y[NSUB][4];                   // scores in base-2 units
-            [[maybe_unused]] float iv[NSUB][2]; // 2^-ev of tokens rt and rt + 8 (e4m3)
-            float top0 = NEG_INF, top1 = NEG_INF;
+        const int rt = kQuant ? row_token(g4) : g4;
+        auto qtok_ofs = [](int n) -> uint32_t { return (uint32_t)((n >> LGB) * 2 * B + (n & (B - 1))) * D; };
+        auto qsc_ofs = [](int n) -> uint32_t { return (uint32_t)((n >> LGB) * 2 * B + (n & (B - 1))); };
+        const uint32_t qk_ofs = D == 128 ? rt * 128 + ((t4 ^ rt) << 4) : rt * 64 + ((t4 ^ (rt >> 1 & 3)) << 4);
+        const int va = row_token(2 * t4), vb = row_token(2 * t4 + 1);
+        const int vch = D == 128 ? row_token(g4) : g4;
+        const int d0 = vch * 2 * NT;
+        auto qv_ofs = [&](int tok) -> uint32_t {
+            return (uint32_t)(B * D) + (D == 128 ? tok * 128 + ((vch ^ tok) << 4)
+                                                 : tok * 64 + (((vch >> 1) ^ (tok >> 1 & 3)) << 4) + ((vch & 1) << 3));
+        };
+        uint32_t kofs[NSUB][DH], kx[NSUB][DH], vofs[NSUB][DH], vx[NSUB][DH];
+        if constexpr (!kQuant) {
+            const int k_tok = (lane & 7) + ((lane >> 3) & 1) * 8, k_hi = lane >> 4;
+            const int v_tok = (lane & 7) + ((lane >> 4) & 1) * 8, v_hi = (lane >> 3) & 1;
 #pragma unroll
-            for (int j = 0; j < NSUB; ++j) {
-                float a[4] = {0.f, 0.f, 0.f, 0.f}, b[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int j = 0; j < NSUB; ++j)
+#pragma unroll
+                for (int dh = 0; dh < DH; ++dh) {
+                    int tok = 16 * j + k_tok;
+                    int row = (tok >> LGB) * (2 * DH * B) + dh * B + (tok & (B - 1));
+                    kofs[j][dh] = (uint32_t)row * 128;
+                    kx[j][dh] = (uint32_t)((k_hi ^ (row & 7)) << 4);
+                    tok = 16 * j + v_tok;
+                    row = (tok >> LGB) * (2 * DH * B) + (DH + dh) * B + (tok & (B - 1));
+                    vofs[j][dh] = (uint32_t)row * 128;
+                    vx[j][dh] = (uint32_t)((v_hi ^ (row & 7)) << 4);
+                }
+        }
+
+        while (true) {
+            if (!mbar_wait_bounded(full_s + 8 * slot, fphase, abort_flag, p.wait_ns)) {
+                if (lane == 0) {
+                    flag_error(p.err, PA_DEV_ERR_TIMEOUT);
+                    *abort_flag = 1;
+                }
+                break;
+            }
+            const SpMeta mt = meta[slot];
+            if (mt.flags & kSpDone) break;
+            const uint32_t kv = slots_s + slot * Geo::kSlot, scb = sc_s + slot * Geo::kScales;
+            if (mt.flags & kSpFirst) {
                 if constexpr (kQuant) {
+                    float a = 0.f;
+                    const uint32_t qrow = q_s + slot * Geo::kQ + g4 * D * 2 + t4 * 32;
 #pragma unroll
-                    for (int c = 0; c < NT / 4; ++c) {
-                        const uint4 lo = sp_lds128(kv + qtok_ofs(16 * j) + (qk_ofs ^ (c * 64)));
-                        const uint4 hi = sp_lds128(kv + qtok_ofs(16 * j + 8) + (qk_ofs ^ (c * 64)));
-                        const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
+                    for (int w = 0; w < NT; ++w) {
+                        const uint2 x = g4 < p.G ? sp_lds64(qrow + (w >> 2) * 128 + (w & 3) * 8) : make_uint2(0, 0);
+                        qf[w][0] = x.x;
+                        qf[w][1] = x.y;
+                        if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+                            const float2 f0 = Mma<T>::unpack(x.x), f1 = Mma<T>::unpack(x.y);
+                            a = fmaxf(a, fmaxf(fmaxf(fabsf(f0.x), fabsf(f0.y)), fmaxf(fabsf(f1.x), fabsf(f1.y))));
+                        }
+                    }
+                    c0 = c1 = p.scale_log2;
+                    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+                        // The row's largest magnitude goes to [2^14, 2^15): elements down to 2^-28 of it are normal
+                        // fp16 numbers and exact, smaller ones are off by at most 2^-40 of it.
+                        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+                        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
+                        const int ex = (int)(__float_as_uint(a) >> 23) - 127;
+                        const int e = ex > 127 || a == 0.f ? 0 : max(ex - 14, -126);
+                        const float inv = pow2i(-e);
 #pragma unroll
-                        for (int w = 0; w < 4; ++w)
-                            Mma<__half>::run(w & 1 ? b : a, e4m3x2_to_f16x2(wl[w]), e4m3x2_to_f16x2(wh[w]),
-                                             e4m3x2_to_f16x2(wl[w] >> 16), e4m3x2_to_f16x2(wh[w] >> 16),
-                                             qf[4 * c + w][0], qf[4 * c + w][1]);
+                        for (int w = 0; w < NT; ++w)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const float2 f = Mma<T>::unpack(qf[w][i]);
+                                qf[w][i] = Mma<__half>::pack(f.x * inv, f.y * inv);
+                            }
+                        const float up = pow2i(e);
+                        c0 *= __shfl_sync(0xffffffffu, up, 8 * t4);  // lane 4 n holds head n's
+                        c1 *= __shfl_sync(0xffffffffu, up, 8 * t4 + 4);
                     }
                 } else {
+                    const uint8_t* qs = q_g + (size_t)slot * Geo::kQ;
 #pragma unroll
                     for (int ks = 0; ks < NT; ++ks) {
-                        const int dh = ks >> 2;
-                        const uint32_t addr = kv + kofs[j][dh] + ((uint32_t)(((ks & 3) * 2) << 4) ^ kx[j][dh]);
-                        uint32_t r0, r1, r2, r3;
-                        ldmatrix_x4(addr, r0, r1, r2, r3);
-                        Mma<T>::run(ks & 1 ? b : a, r0, r1, r2, r3, qf[ks][0], qf[ks][1]);
+                        const int d = 16 * ks + 2 * t4;
+                        const uint32_t* row = reinterpret_cast<const uint32_t*>(qs + ((size_t)g4 * D + d) * 2);
+                        qf[ks][0] = g4 < p.G ? row[0] : 0u;
+                        qf[ks][1] = g4 < p.G ? row[4] : 0u;
                     }
                 }
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int tok = 16 * j + 8 * half + rt;
-                    float x0 = a[2 * half] + b[2 * half], x1 = a[2 * half + 1] + b[2 * half + 1], add = 0.f;
+                for (int i = 0; i < NT; ++i) O[i][0] = O[i][1] = O[i][2] = O[i][3] = 0.f;
+                m0 = m1 = NEG_INF;
+                l0 = l1 = 0.f;
+            }
+            // the running maximum moves to n0, n1
+            auto rescale = [&](float n0, float n1) {
+                const float a0 = fast_exp2(m0 - n0), a1 = fast_exp2(m1 - n1);
+                m0 = n0;
+                m1 = n1;
+                if (__any_sync(0xffffffffu, a0 != 1.f || a1 != 1.f)) {
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) {
+                        O[i][0] *= a0;
+                        O[i][1] *= a1;
+                        O[i][2] *= a0;
+                        O[i][3] *= a1;
+                    }
+                    l0 *= a0;
+                    l1 *= a1;
+                }
+            };
+            // one copy for whole stages, without a branch between the tiles, and one for the others
+            auto stage = [&](auto full_c) {
+                constexpr bool kFull = decltype(full_c)::value;
+                float y[NSUB][4];                   // scores in base-2 units
+                [[maybe_unused]] float iv[NSUB][2]; // 2^-ev of tokens rt and rt + 8 (e4m3)
+                float top0 = NEG_INF, top1 = NEG_INF;
+#pragma unroll
+                for (int j = 0; j < NSUB; ++j) {
+                    float a[4] = {0.f, 0.f, 0.f, 0.f}, b[4] = {0.f, 0.f, 0.f, 0.f};
                     if constexpr (kQuant) {
-                        const uint32_t at = scb + qsc_ofs(16 * j + 8 * half) + rt;
-                        const float fk = pow2i(scale_of((int)sp_lds8(at)));
-                        const int ev = scale_of((int)sp_lds8(at + B));
-                        x0 *= fk;  // (before the query's factor, which may be as large as fp32 allows)
-                        x1 *= fk;
-                        add = (float)ev;
-                        iv[j][half] = pow2i(-ev);
-                    }
-                    const bool in = kFull || (mt.seen >> tok & 1u);
-                    y[j][2 * half] = in ? fmaf(x0, c0, add) : NEG_INF;
-                    y[j][2 * half + 1] = in ? fmaf(x1, c1, add) : NEG_INF;
-                }
-                top0 = fmaxf(top0, fmaxf(y[j][0], y[j][2]));
-                top1 = fmaxf(top1, fmaxf(y[j][1], y[j][3]));
-            }
 #pragma unroll
-            for (int o = 4; o < 32; o <<= 1) {
-                top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, o));
-                top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, o));
-            }
-            rescale(fmaxf(m0, top0), fmaxf(m1, top1));
-            if constexpr (!kQuant) {
-                // V rows of tokens that take no part may hold anything (even NaN): they become zeros
-                if (!kFull) {
-                    for (int c = lane; c < kUnitTok * DH * 8; c += 32) {
-                        const int tok = c / (DH * 8), dh = c / 8 % DH, ch = c & 7;
-                        if (mt.seen >> tok & 1u) continue;
-                        const int row = (tok >> LGB) * (2 * DH * B) + (DH + dh) * B + (tok & (B - 1));
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(kv + (uint32_t)row * 128 + ch * 16),
-                                     "r"(0)
-                                     : "memory");
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
-            }
+                        for (int c = 0; c < NT / 4; ++c) {
+                            const uint4 lo = sp_lds128(kv + qtok_ofs(16 * j) + (qk_ofs ^ (c * 64)));
+                            const uint4 hi = sp_lds128(kv + qtok_ofs(16 * j + 8) + (qk_ofs ^ (c * 64)));
+                            const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-            for (int j = 0; j < NSUB; ++j) {
-                // probabilities as a high and a low 16-bit part, transposed into B fragments
-                using P = typename std::conditional<kQuant, __half, T>::type;
-                const float p0 = fast_exp2(y[j][0] - m0), p1 = fast_exp2(y[j][1] - m1);
-                const float p2 = fast_exp2(y[j][2] - m0), p3 = fast_exp2(y[j][3] - m1);
-                if constexpr (kQuant) {
-                    l0 = fmaf(p0, iv[j][0], fmaf(p2, iv[j][1], l0));
-                    l1 = fmaf(p1, iv[j][0], fmaf(p3, iv[j][1], l1));
-                } else {
-                    l0 += p0 + p2;
-                    l1 += p1 + p3;
-                }
-                const uint32_t h01 = Mma<P>::pack(p0, p1), h23 = Mma<P>::pack(p2, p3);
-                const float2 f01 = Mma<P>::unpack(h01), f23 = Mma<P>::unpack(h23);
-                const uint32_t lo01 = Mma<P>::pack(p0 - f01.x, p1 - f01.y), lo23 = Mma<P>::pack(p2 - f23.x, p3 - f23.y);
-                const uint32_t bh0 = movmatrix_trans(h01), bh1 = movmatrix_trans(h23);
-                const uint32_t bl0 = movmatrix_trans(lo01), bl1 = movmatrix_trans(lo23);
-                if constexpr (kQuant) {
-                    uint32_t w[4][NT / 2];  // tokens va, vb, va + 8, vb + 8
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        const uint32_t at = kv + qtok_ofs(16 * j + 8 * (t >> 1)) + qv_ofs(t & 1 ? vb : va);
-                        if constexpr (D == 128) {
-                            const uint4 x = sp_lds128(at);
-                            w[t][0] = x.x;
-                            w[t][1] = x.y;
-                            w[t][2] = x.z;
-                            w[t][3] = x.w;
-                        } else {
-                            const uint2 x = sp_lds64(at);
-                            w[t][0] = x.x;
-                            w[t][1] = x.y;
+                            for (int w = 0; w < 4; ++w)
+                                Mma<__half>::run(w & 1 ? b : a, e4m3x2_to_f16x2(wl[w]), e4m3x2_to_f16x2(wh[w]),
+                                                 e4m3x2_to_f16x2(wl[w] >> 16), e4m3x2_to_f16x2(wh[w] >> 16),
+                                                 qf[4 * c + w][0], qf[4 * c + w][1]);
                         }
-                        if (!kFull) {  // (as above)
-                            const bool in = mt.seen >> (16 * j + 8 * (t >> 1) + (t & 1 ? vb : va)) & 1u;
+                    } else {
 #pragma unroll
-                            for (int i = 0; i < NT / 2; ++i) w[t][i] = in ? w[t][i] : 0u;
+                        for (int ks = 0; ks < NT; ++ks) {
+                            const int dh = ks >> 2;
+                            const uint32_t addr = kv + kofs[j][dh] + ((uint32_t)(((ks & 3) * 2) << 4) ^ kx[j][dh]);
+                            uint32_t r0, r1, r2, r3;
+                            ldmatrix_x4(addr, r0, r1, r2, r3);
+                            Mma<T>::run(ks & 1 ? b : a, r0, r1, r2, r3, qf[ks][0], qf[ks][1]);
                         }
                     }
 #pragma unroll
-                    for (int i = 0; i < NT / 2; ++i) {
-                        // (va, vb) pairs of elements 4 i .. 4 i + 3, then the same of the tokens 8 later
-                        const uint32_t u[2] = {__byte_perm(w[0][i], w[1][i], 0x5140), __byte_perm(w[0][i], w[1][i], 0x7362)};
-                        const uint32_t z[2] = {__byte_perm(w[2][i], w[3][i], 0x5140), __byte_perm(w[2][i], w[3][i], 0x7362)};
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const uint32_t r0 = e4m3x2_to_f16x2(u[k]), r1 = e4m3x2_to_f16x2(u[k] >> 16),
-                                           r2 = e4m3x2_to_f16x2(z[k]), r3 = e4m3x2_to_f16x2(z[k] >> 16);
-                            Mma<__half>::run(O[2 * i + k], r0, r1, r2, r3, bh0, bh1);
-                            Mma<__half>::run(O[2 * i + k], r0, r1, r2, r3, bl0, bl1);
+                    for (int half = 0; half < 2; ++half) {
+                        const int tok = 16 * j + 8 * half + rt;
+                        float x0 = a[2 * half] + b[2 * half], x1 = a[2 * half + 1] + b[2 * half + 1], add = 0.f;
+                        if constexpr (kQuant) {
+                            const uint32_t at = scb + qsc_ofs(16 * j + 8 * half) + rt;
+                            const float fk = pow2i(scale_of((int)sp_lds8(at)));
+                            const int ev = scale_of((int)sp_lds8(at + B));
+                            x0 *= fk;  // (before the query's factor, which may be as large as fp32 allows)
+                            x1 *= fk;
+                            add = (float)ev;
+                            iv[j][half] = pow2i(-ev);
                         }
+                        const bool in = kFull || (mt.seen >> tok & 1u);
+                        y[j][2 * half] = in ? fmaf(x0, c0, add) : NEG_INF;
+                        y[j][2 * half + 1] = in ? fmaf(x1, c1, add) : NEG_INF;
                     }
-                } else {
+                    top0 = fmaxf(top0, fmaxf(y[j][0], y[j][2]));
+                    top1 = fmaxf(top1, fmaxf(y[j][1], y[j][3]));
+                }
 #pragma unroll
-                    for (int i = 0; i < NT; ++i) {
-                        const int dh = i >> 2;
-                        const uint32_t addr = kv + vofs[j][dh] + ((uint32_t)(((i & 3) * 2) << 4) ^ vx[j][dh]);
-                        uint32_t r0, r1, r2, r3;
-                        ldmatrix_x4_trans(addr, r0, r1, r2, r3);
-                        Mma<T>::run(O[i], r0, r1, r2, r3, bh0, bh1);
-                        Mma<T>::run(O[i], r0, r1, r2, r3, bl0, bl1);
+                for (int o = 4; o < 32; o <<= 1) {
+                    top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, o));
+                    top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, o));
+                }
+                rescale(fmaxf(m0, top0), fmaxf(m1, top1));
+                if constexpr (!kQuant) {
+                    // V rows of tokens that take no part may hold anything (even NaN): they become zeros
+                    if (!kFull) {
+                        for (int c = lane; c < kUnitTok * DH * 8; c += 32) {
+                            const int tok = c / (DH * 8), dh = c / 8 % DH, ch = c & 7;
+                            if (mt.seen >> tok & 1u) continue;
+                            const int row = (tok >> LGB) * (2 * DH * B) + (DH + dh) * B + (tok & (B - 1));
+                            const uint32_t at = kv + (uint32_t)row * 128 + ch * 16;
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
                     }
                 }
-            }
-        };
-        if (mt.seen == 0xffffffffu)
-            stage(std::true_type{});
-        else if (mt.seen)
-            stage(std::false_type{});
-        __syncwarp();
-        if (lane == 0) mbar_arrive(empty_s + 8 * slot);
+#pragma unroll
+                for (int j = 0; j < NSUB; ++j) {
+                    // probabilities as a high and a low 16-bit part, transposed into B fragments
+                    using P = typename std::conditional<kQuant, __half, T>::type;
+                    const float p0 = fast_exp2(y[j][0] - m0), p1 = fast_exp2(y[j][1] - m1);
+                    const float p2 = fast_exp2(y[j][2] - m0), p3 = fast_exp2(y[j][3] - m1);
+                    if constexpr (kQuant) {
+                        l0 = fmaf(p0, iv[j][0], fmaf(p2, iv[j][1], l0));
+                        l1 = fmaf(p1, iv[j][0], fmaf(p3, iv[j][1], l1));
+                    } else {
+                        l0 += p0 + p2;
+                        l1 += p1 + p3;
+                    }
+                    const uint32_t h01 = Mma<P>::pack(p0, p1), h23 = Mma<P>::pack(p2, p3);
+                    const float2 f01 = Mma<P>::unpack(h01), f23 = Mma<P>::unpack(h23);
+                    const uint32_t lo01 = Mma<P>::pack(p0 - f01.x, p1 - f01.y);
+                    const uint32_t lo23 = Mma<P>::pack(p2 - f23.x, p3 - f23.y);
+                    const uint32_t bh0 = movmatrix_trans(h01), bh1 = movmatrix_trans(h23);
+                    const uint32_t bl0 = movmatrix_trans(lo01), bl1 = movmatrix_trans(lo23);
+                    if constexpr (kQuant) {
+                        uint32_t w[4][NT / 2];  // tokens va, vb, va + 8, vb + 8
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) {
+                            const uint32_t at = kv + qtok_ofs(16 * j + 8 * (t >> 1)) + qv_ofs(t & 1 ? vb : va);
+                            if constexpr (D == 128) {
+                                const uint4 x = sp_lds128(at);
+                                w[t][0] = x.x;
+                                w[t][1] = x.y;
+                                w[t][2] = x.z;
+                                w[t][3] = x.w;
+                            } else {
+                                const uint2 x = sp_lds64(at);
+                                w[t][0] = x.x;
+                                w[t][1] = x.y;
+                            }
+                            if (!kFull) {  // (as above)
+                                const bool in = mt.seen >> (16 * j + 8 * (t >> 1) + (t & 1 ? vb : va)) & 1u;
+#pragma unroll
+                                for (int i = 0; i < NT / 2; ++i) w[t][i] = in ? w[t][i] : 0u;
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < NT / 2; ++i) {
+                            // (va, vb) pairs of elements 4 i .. 4 i + 3, then the same of the tokens 8 later
+                            const uint32_t u[2] = {__byte_perm(w[0][i], w[1][i], 0x5140),
+                                                   __byte_perm(w[0][i], w[1][i], 0x7362)};
+                            const uint32_t z[2] = {__byte_perm(w[2][i], w[3][i], 0x5140),
+                                                   __byte_perm(w[2][i], w[3][i], 0x7362)};
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const uint32_t r0 = e4m3x2_to_f16x2(u[k]), r1 = e4m3x2_to_f16x2(u[k] >> 16),
+                                               r2 = e4m3x2_to_f16x2(z[k]), r3 = e4m3x2_to_f16x2(z[k] >> 16);
+                                Mma<__half>::run(O[2 * i + k], r0, r1, r2, r3, bh0, bh1);
+                                Mma<__half>::run(O[2 * i + k], r0, r1, r2, r3, bl0, bl1);
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < NT; ++i) {
+                            const int dh = i >> 2;
+                            const uint32_t addr = kv + vofs[j][dh] + ((uint32_t)(((i & 3) * 2) << 4) ^ vx[j][dh]);
+                            uint32_t r0, r1, r2, r3;
+                            ldmatrix_x4_trans(addr, r0, r1, r2, r3);
+                            Mma<T>::run(O[i], r0, r1, r2, r3, bh0, bh1);
+                            Mma<T>::run(O[i], r0, r1, r2, r3, bl0, bl1);
+                        }
+                    }
+                }
+            };
+            if (mt.seen == 0xffffffffu)
+                stage(std::true_type{});
+            else if (mt.seen)
+                stage(std::false_type{});
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty_s + 8 * slot);
 
-        if (mt.flags & kSpLast) {
-            float L0 = l0, L1 = l1;
+            if (mt.flags & kSpLast) {
+                float L0 = l0, L1 = l1;
 #pragma unroll
-            for (int o = 4; o < 32; o <<= 1) {
-                L0 += __shfl_xor_sync(0xffffffffu, L0, o);
-                L1 += __shfl_xor_sync(0xffffffffu, L1, o);
-            }
-            const uint64_t keep = policy_evict_last();  // the join reads the parts right after this kernel
+                for (int o = 4; o < 32; o <<= 1) {
+                    L0 += __shfl_xor_sync(0xffffffffu, L0, o);
+                    L1 += __shfl_xor_sync(0xffffffffu, L1, o);
+                }
+                const uint64_t keep = policy_evict_last();  // the join reads the parts right after this kernel
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-                const int hd = 2 * t4 + hh;
-                if (hd >= p.G) continue;
-                const float L = hh ? L1 : L0;
-                const float inv = L > 0.f || L != L ? 1.f / L : 0.f;  // an empty list: zeros
-                // element d(i, k): row k of the pair that this thread holds of tile i
-                auto d_of = [&](int i, int k) { return kQuant ? d0 + 2 * i + k : 16 * i + g4 + 8 * k; };
-                if constexpr (kCluster) {
-                    if (g4 == 0) {
-                        share[hd] = hh ? m1 : m0;
-                        share[kMaxGroup + hd] = L;
-                    }
-#pragma unroll
-                    for (int i = 0; i < NT; ++i) {
-                        share[2 * kMaxGroup + hd * D + d_of(i, 0)] = O[i][hh];
-                        share[2 * kMaxGroup + hd * D + d_of(i, 1)] = O[i][2 + hh];
-                    }
-                } else if (mt.part < 0) {
-                    const int64_t o = ((int64_t)mt.row * p.G + hd) * D;
-#pragma unroll
-                    for (int i = 0; i < NT; ++i) {
-                        const float v0 = O[i][hh] * inv, v1 = O[i][2 + hh] * inv;
-                        if (kQuant && p.out_dtype == PA_F32) {
-                            *reinterpret_cast<float2*>(static_cast<float*>(p.out) + o + d_of(i, 0)) = make_float2(v0, v1);
-                        } else if (kQuant) {
-                            *reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + o + d_of(i, 0)) = Mma<T>::pack(v0, v1);
-                        } else if (p.out_dtype == PA_F32) {
-                            static_cast<float*>(p.out)[o + d_of(i, 0)] = v0;
-                            static_cast<float*>(p.out)[o + d_of(i, 1)] = v1;
-                        } else {
-                            static_cast<T*>(p.out)[o + d_of(i, 0)] = from_float<T>(v0);
-                            static_cast<T*>(p.out)[o + d_of(i, 1)] = from_float<T>(v1);
+                for (int hh = 0; hh < 2; ++hh) {
+                    const int hd = 2 * t4 + hh;
+                    if (hd >= p.G) continue;
+                    const float L = hh ? L1 : L0;
+                    const float inv = L > 0.f || L != L ? 1.f / L : 0.f;  // an empty list: zeros
+                    // element d(i, k): row k of the pair that this thread holds of tile i
+                    auto d_of = [&](int i, int k) { return kQuant ? d0 + 2 * i + k : 16 * i + g4 + 8 * k; };
+                    if constexpr (kCluster) {
+                        if (g4 == 0) {
+                            share[hd] = hh ? m1 : m0;
+                            share[kMaxGroup + hd] = L;
                         }
-                    }
-                } else {
-                    const int64_t r = (int64_t)mt.part * p.G + hd;
 #pragma unroll
-                    for (int i = 0; i < NT; ++i) {
-                        st_hint(p.part_acc + r * D + d_of(i, 0), O[i][hh], keep);
-                        st_hint(p.part_acc + r * D + d_of(i, 1), O[i][2 + hh], keep);
-                    }
-                    if (g4 == 0) {
-                        st_hint(p.part_m + r, hh ? m1 : m0, keep);
-                        st_hint(p.part_l + r, L, keep);
+                        for (int i = 0; i < NT; ++i) {
+                            share[2 * kMaxGroup + hd * D + d_of(i, 0)] = O[i][hh];
+                            share[2 * kMaxGroup + hd * D + d_of(i, 1)] = O[i][2 + hh];
+                        }
+                    } else if (mt.part < 0) {
+                        const int64_t o = ((int64_t)mt.row * p.G + hd) * D;
+#pragma unroll
+                        for (int i = 0; i < NT; ++i) {
+                            const float v0 = O[i][hh] * inv, v1 = O[i][2 + hh] * inv;
+                            if (kQuant && p.out_dtype == PA_F32) {
+                                float* to = static_cast<float*>(p.out) + o + d_of(i, 0);
+                                *reinterpret_cast<float2*>(to) = make_float2(v0, v1);
+                            } else if (kQuant) {
+                                T* to = static_cast<T*>(p.out) + o + d_of(i, 0);
+                                *reinterpret_cast<uint32_t*>(to) = Mma<T>::pack(v0, v1);
+                            } else if (p.out_dtype == PA_F32) {
+                                static_cast<float*>(p.out)[o + d_of(i, 0)] = v0;
+                                static_cast<float*>(p.out)[o + d_of(i, 1)] = v1;
+                            } else {
+                                static_cast<T*>(p.out)[o + d_of(i, 0)] = from_float<T>(v0);
+                                static_cast<T*>(p.out)[o + d_of(i, 1)] = from_float<T>(v1);
+                            }
+                        }
+                    } else {
+                        const int64_t r = (int64_t)mt.part * p.G + hd;
+#pragma unroll
+                        for (int i = 0; i < NT; ++i) {
+                            st_hint(p.part_acc + r * D + d_of(i, 0), O[i][hh], keep);
+                            st_hint(p.part_acc + r * D + d_of(i, 1), O[i][2 + hh], keep);
+                        }
+                        if (g4 == 0) {
+                            st_hint(p.part_m + r, hh ? m1 : m0, keep);
+                            st_hint(p.part_l + r, L, keep);
+                        }
                     }
                 }
             }
+            if (++slot == nstage) {
+                slot = 0;
+                fphase ^= 1;
+            }
         }
-        if (++slot == nstage) {
-            slot = 0;
-            fphase ^= 1;
-        }
-    }
     };
     if (producer)
         produce();
@@ -851,7 +862,8 @@ static pa_status run_sparse(const DecodeSparseArgs& a, SpParams& p, const Sparse
     if (kQuant) {
         st = quant_tensor_map(&tm, a.pool, a.NB, a.H_kv, a.B, D);
     } else {
-        // dims (innermost first): 64 columns, token (NB*B), column half, kv head, K/V; one box is a block's rows of a head
+        // dims (innermost first): 64 columns, token (NB*B), column half, kv head, K/V; one box is a block's rows of a
+        // head
         const cuuint64_t dims[5] = {64, (cuuint64_t)a.NB * a.B, D / 64, (cuuint64_t)a.H_kv, 2};
         const cuuint64_t str[4] = {(cuuint64_t)4 * a.H_kv * D, 128, (cuuint64_t)2 * D, (cuuint64_t)2 * a.H_kv * D};
         const cuuint32_t box[5] = {64, (cuuint32_t)a.B, D / 64, 1, 2};
@@ -907,7 +919,8 @@ static pa_status run_sparse_shape(const DecodeSparseArgs& a, SpParams& p, const 
 
 pa_status launch_decode_sparse(const DecodeSparseArgs& a) {
     SparseLayout L;
-    if (!sparse_layout(a.N, a.H_q, a.H_kv, a.D, a.B, a.top_k, &L)) return fail(PA_ERR_UNSUPPORTED, "too many work records");
+    if (!sparse_layout(a.N, a.H_q, a.H_kv, a.D, a.B, a.top_k, &L))
+        return fail(PA_ERR_UNSUPPORTED, "too many work records");
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
     SpParams p;
     p.out = a.out;

@@ -1,8 +1,8 @@
 // runs.cuh -- the work of a batch cut into runs of equal length.
 //
 // A row is one (sequence, KV head); all H_kv rows of a sequence have the same number of units, which follows from its
-// context.  The units of all rows, in order, are cut into `parts` runs whose lengths differ by at most one.  A warp finds
-// its run by itself: it reads the lengths once, the first kScanSeqs of them in one go.
+// context.  The units of all rows, in order, are cut into `parts` runs whose lengths differ by at most one.  A warp
+// finds its run by itself: it reads the lengths once, the first kScanSeqs of them in one go.
 #pragma once
 
 #include "pa_device.cuh"

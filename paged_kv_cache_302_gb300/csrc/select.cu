@@ -1,8 +1,12 @@
 // select.cu -- the blocks of each (sequence, KV head) that block-sparse decode reads, by their key summaries.
 //
 // Two kernels per call: the scores (the format and the score are in summary.cuh), then the top_k of each row -- one
-// (sequence, KV head).  Up to a few hundred rows take one kernel instead, a cluster of CTAs per row, whose scores meet in
-// the shared memory of one of them.
+// (sequence, KV head).  Up to a few hundred rows take one kernel instead, a cluster of CTAs per row, whose scores meet
+// in the shared memory of one of them.
+//
+// Bound by the boxes' bytes, 2 D + 1 per (block, head), and by the latency around them.  64 sequences of up to 16384
+// tokens (8 heads, 74 MB of boxes) take 25.7 us, of which 16 stream the boxes at 4.6 TB/s and 5 find the top_k; 16 of
+// 32768 (68 MB, one kernel) 21 us; 1 of 16384 4.7 us on the device, a chain of five dependent reads and the search.
 #include <algorithm>
 #include <type_traits>
 
@@ -38,8 +42,8 @@ __device__ __forceinline__ uint32_t ordered(float x) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Scores: mma.sync m16n8k16 with 16 blocks on M and the query heads of the KV head on N.  max(q lo, q hi) is q hi for q >=
-// 0 and q lo below, so a box's score is one product of length 2 D, [max(q, 0), min(q, 0)] . [hi, lo]; box and query
+// Scores: mma.sync m16n8k16 with 16 blocks on M and the query heads of the KV head on N.  max(q lo, q hi) is q hi for q
+// >= 0 and q lo below, so a box's score is one product of length 2 D, [max(q, 0), min(q, 0)] . [hi, lo]; box and query
 // integers are exact in fp16.
 constexpr int kScoreWarps = 4;
 constexpr int kScoreCtas = 4;  // per SM
@@ -49,7 +53,8 @@ __device__ __forceinline__ void int8x4_to_f16(uint32_t x, uint32_t& a, uint32_t&
     const uint32_t u = x ^ 0x80808080u;
     const __half2 bias = __floats2half2_rn(1152.f, 1152.f);
     uint32_t r0 = __byte_perm(u, 0x64646464u, 0x4140), r1 = __byte_perm(u, 0x64646464u, 0x4342);
-    const __half2 h0 = __hsub2(*reinterpret_cast<__half2*>(&r0), bias), h1 = __hsub2(*reinterpret_cast<__half2*>(&r1), bias);
+    const __half2 h0 = __hsub2(*reinterpret_cast<__half2*>(&r0), bias);
+    const __half2 h1 = __hsub2(*reinterpret_cast<__half2*>(&r1), bias);
     a = *reinterpret_cast<const uint32_t*>(&h0);
     b = *reinterpret_cast<const uint32_t*>(&h1);
 }
@@ -59,8 +64,8 @@ struct Tile {
     int s, h, t, tiles, nb, blk[2];  // tiles, nb: of the row
 };
 
-// One warp's state.  The tile's boxes lie in registers; as soon as a piece has been multiplied, its registers receive the
-// next tile's.
+// One warp's state.  The tile's boxes lie in registers; as soon as a piece has been multiplied, its registers receive
+// the next tile's.
 template <typename T, int D>
 struct Scorer {
     static constexpr int NC = D / 64;  // 16-byte chunks of a lane: t4, t4 + 4 of each half of a box
@@ -91,8 +96,8 @@ struct Scorer {
             for (int i = 0; i < 2; ++i) {
                 uint4 x = make_uint4(0, 0, 0, 0);
                 if (g4 < p.G)
-                    x = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) +
-                                                       (((int64_t)s * p.H_kv + h) * p.G + g4) * D + 64 * c + 16 * t4)[i];
+                    x = reinterpret_cast<const uint4*>(
+                        static_cast<const T*>(p.q) + (((int64_t)s * p.H_kv + h) * p.G + g4) * D + 64 * c + 16 * t4)[i];
                 up[c][4 * i] = x.x;
                 up[c][4 * i + 1] = x.y;
                 up[c][4 * i + 2] = x.z;
@@ -245,10 +250,10 @@ __global__ void __launch_bounds__(kScoreWarps * 32, kScoreCtas) score_kernel(con
     });
 }
 
-// The top_k of a row with more blocks than that: one CTA, each thread with neighbouring keys, in registers (K of them) or read anew
-// (K = 0).  The key of the last block taken is found by a histogram over the bits below those that all competing keys
-// share, eight at a time (seven for 128 threads), then among the keys of one bin: ranked against one another where there
-// are no more than bins, else by their next bits.  One scan then gives every taken block its place.
+// The top_k of a row with more blocks than that: one CTA, each thread with neighbouring keys, in registers (K of them)
+// or read anew (K = 0).  The key of the last block taken is found by a histogram over the bits below those that all
+// competing keys share, eight at a time (seven for 128 threads), then among the keys of one bin: ranked against one
+// another where there are no more than bins, else by their next bits.  One scan then gives every taken block its place.
 
 // Key k competes and agrees with the prefix above its low `open` bits.
 __device__ __forceinline__ bool agree(uint32_t k, uint32_t prefix, int open) {
@@ -428,12 +433,12 @@ __global__ void __launch_bounds__(THREADS) top_blocks_kernel(const SelectParams 
 }
 
 // Rows whose clusters the device holds at once: a cluster of up to 8 CTAs per row, whose warps score the row's tiles in
-// turn and leave the keys in the first CTA's shared memory, which then lists the row's blocks.  Against two kernels, 8 rows
-// of 1024 blocks take 4.7 us instead of 5.6, 64 rows 9.0 instead of 11.3, 304 rows (one CTA each) 21 instead of 25; 320
-// rows, which no longer fit, 35 instead of 27.  Half the cluster size serves better as long as a warp has no more than two
-// tiles: 64 rows of 256 blocks 5.0 us with 2 CTAs, 5.3 with 4.
-// Twice as many rows fit as CTAs of half the threads, which serve short rows: 512 rows of 256 blocks 12.8 us against 17.3
-// with two kernels, 512 rows of up to 1024 blocks 31 against 25.
+// turn and leave the keys in the first CTA's shared memory, which then lists the row's blocks.  Against two kernels, 8
+// rows of 1024 blocks take 4.7 us instead of 5.6, 64 rows 9.0 instead of 11.3, 304 rows (one CTA each) 21 instead of
+// 25; 320 rows, which no longer fit, 35 instead of 27.  Half the cluster size serves better as long as a warp has no
+// more than two tiles: 64 rows of 256 blocks 5.0 us with 2 CTAs, 5.3 with 4. Twice as many rows fit as CTAs of half the
+// threads, which serve short rows: 512 rows of 256 blocks 12.8 us against 17.3 with two kernels, 512 rows of up to 1024
+// blocks 31 against 25.
 constexpr int kRowCluster = 8;
 constexpr int kRowThreads = 256, kRowBlocks = kRowThreads * 8;    // (eight keys to a thread of the first CTA)
 constexpr int kShortThreads = 128, kShortBlocks = kShortThreads * 4;
@@ -566,8 +571,9 @@ pa_status launch_select(const SelectArgs& a) {
         if (tiles >= 1LL << 31) return fail(PA_ERR_UNSUPPORTED, "too many blocks to score");
         const unsigned grid = (unsigned)std::min<int64_t>((tiles + kScoreWarps - 1) / kScoreWarps,
                                                           (int64_t)sm_count() * kScoreCtas);
-        auto kern = a.q_dtype == PA_BF16 ? (a.D == 128 ? score_kernel<__nv_bfloat16, 128> : score_kernel<__nv_bfloat16, 64>)
-                                         : (a.D == 128 ? score_kernel<__half, 128> : score_kernel<__half, 64>);
+        auto kern = a.q_dtype == PA_BF16
+                        ? (a.D == 128 ? score_kernel<__nv_bfloat16, 128> : score_kernel<__nv_bfloat16, 64>)
+                        : (a.D == 128 ? score_kernel<__half, 128> : score_kernel<__half, 64>);
         const cudaError_t e = launch_kernel(kern, dim3(grid), dim3(kScoreWarps * 32), 0, a.stream, p);
         count_launch();
         if (e != cudaSuccess) return cuda_fail(e, "score launch");
@@ -583,7 +589,8 @@ pa_status launch_select(const SelectArgs& a) {
     } else if (nb <= 1024 * 16) {
         top = top_blocks_kernel<1024, 16>;
     }
-    const cudaError_t e = launch_kernel(top, dim3((unsigned)a.H_kv, (unsigned)a.N), dim3((unsigned)threads), 0, a.stream, p);
+    const cudaError_t e =
+        launch_kernel(top, dim3((unsigned)a.H_kv, (unsigned)a.N), dim3((unsigned)threads), 0, a.stream, p);
     count_launch();
     return e == cudaSuccess ? PA_OK : cuda_fail(e, "top_blocks launch");
 }

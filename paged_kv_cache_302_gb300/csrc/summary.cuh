@@ -1,4 +1,5 @@
-// summary.cuh -- the format of key summaries, shared by the kernel that makes them and the one that selects blocks by them.
+// summary.cuh -- the format of key summaries, shared by the kernel that makes them and the one that selects blocks by
+// them.
 //
 // A summary is a box around the keys of one (block, KV head): per channel the least and the greatest K of the block's
 // tokens, as integers of 8 bits in units of one power of two,
