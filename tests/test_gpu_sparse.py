@@ -1,6 +1,9 @@
 """Block-sparse decode on the GPU: key summaries and block selection number for number, attention over listed blocks
 element by element against a 64-bit form, with poisoned memory wherever a call has no business."""
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -303,7 +306,8 @@ def want_sparse(q, host, tables, ctx, sel, B, scale, dtype, quant):
     (2, 5, 128, 32, [3000, 90, 1700], 70), (8, 1, 128, 8, [129] * 20, 12),
     (8, 4, 128, 16, [1, 900, 333, 50] * 6, 48), (7, 3, 64, 32, [40, 2000, 700] * 9, 50), (1, 2, 64, 8, [300] * 90, 70),
     (8, 4, 128, 16, [700, 90] * 9, 30), (4, 2, 64, 32, [600, 31, 200] * 25, 7), (16, 1, 128, 8, [200, 60, 500] * 11, 33),
-    (16, 3, 64, 16, [500] * 70, 9)])
+    (16, 1, 64, 16, [500, 33] * 20, 9), (2, 4, 128, 16, [9000, 300, 5000], 300), (3, 2, 64, 32, [12000, 40], 160),
+    (1, 7, 128, 8, [6000], 700), (40, 2, 64, 16, [600, 900] * 4, 40)])
 def test_attention(H, G, D, B, ctx, top_k, dtype, quant, out32):
     g = torch.Generator().manual_seed(H * 13 + D + top_k)
     MB = -(-max(ctx) // B) + 1
@@ -331,8 +335,9 @@ def test_attention(H, G, D, B, ctx, top_k, dtype, quant, out32):
 
 
 @pytest.mark.parametrize("quant", [False, True])
-def test_attention_flags_and_skips_bad_entries(quant):
-    H, G, D, B, top_k = 2, 4, 64, 16, 8
+@pytest.mark.parametrize("top_k", [8, 600])          # in clusters; in runs
+def test_attention_flags_and_skips_bad_entries(quant, top_k):
+    H, G, D, B = 2, 4, 64, 16
     ctx = [100, 200, 90]
     g = torch.Generator().manual_seed(8)
     c = S.make_cache(g, 40, H, B, D, "bf16", quant)
@@ -369,13 +374,14 @@ def test_attention_flags_and_skips_bad_entries(quant):
 
 
 @pytest.mark.parametrize("quant", [False, True])
-def test_attention_counts_repeated_blocks_and_takes_lists_in_any_order(quant):
+@pytest.mark.parametrize("times", [1, 101])          # in clusters; in runs
+def test_attention_counts_repeated_blocks_and_takes_lists_in_any_order(quant, times):
     H, G, D, B, ctx = 1, 4, 128, 16, [77]
     g = torch.Generator().manual_seed(9)
     c = S.make_cache(g, 8, H, B, D, "f16", quant)
     tables = S.make_tables(g, ctx, B, 5, 8)
     q = torch.randn(1, G, D, generator=g).half()
-    sel = torch.tensor([4, 2, 4, -1, 0, 2, 2, -7], dtype=torch.int32).view(1, 1, 8)
+    sel = torch.tensor([4, 2, 4, -1, 0, 2, 2, -7] * times, dtype=torch.int32).view(1, 1, -1)
     out = torch.empty(q.shape, dtype=torch.float32, device="cuda")
     pa.pa_decode_sparse(out, q.cuda(), c[0], tables.cuda(), i32(ctx), sel.cuda(), **scales_of(c))
     want, tol = want_sparse(q, S.host_cache(c), tables, ctx, sel, B, 1 / math.sqrt(D), "f16", quant)
@@ -446,7 +452,8 @@ class Step:
 
 
 SHAPES = [([3000, 700, 41, 1900] * 3, 2, 4, 64, 16, "f16", False, 20), ([5000] * 12, 8, 2, 128, 16, "bf16", True, 64),
-          ([900, 20000], 4, 8, 128, 8, "bf16", False, 100)]
+          ([900, 20000], 4, 8, 128, 8, "bf16", False, 100), ([9000, 700, 41, 6000], 2, 4, 128, 16, "bf16", False, 300),
+          ([9000, 700, 41, 6000] * 8, 4, 2, 64, 32, "f16", True, 150)]
 
 
 @pytest.mark.parametrize("shape", SHAPES)
@@ -622,11 +629,11 @@ def test_quantised_attention_with_queries_and_scales_of_extreme_size(rows):
 
 
 @pytest.mark.parametrize("quant", [False, True])
-@pytest.mark.parametrize("N", [2, 30])
-def test_waits_that_run_out_flag_and_leave_the_gpu_usable(N, quant):
-    """A limit of 1 ns on every wait: the call returns with the flag (few rows join over clusters, many by a second
-    kernel), and the next one gives the bits of one before."""
-    st = Step(14, [2000] * N, 4, 4, 128, 16, "bf16", quant, 60)
+@pytest.mark.parametrize("N, top_k", [(2, 60), (30, 60), (4, 300)])
+def test_waits_that_run_out_flag_and_leave_the_gpu_usable(N, top_k, quant):
+    """A limit of 1 ns on every wait: the call returns with the flag (short lists join over clusters, long ones by a
+    second kernel), and the next one gives the bits of one before."""
+    st = Step(14, [5000] * N, 4, 4, 128, 16, "bf16", quant, top_k)
     b = st.buffers()
     sel, out = (x.clone() for x in st.run(b))
     err = err_word()
@@ -668,3 +675,42 @@ def test_tensors_of_another_place_are_refused():
         pa.pa_decode_sparse(out, st.q, st.cache[0], st.tables, st.dctx, sel, workspace=ws2[:16])
     with pytest.raises(pa.PAError, match="workspace"):
         pa.pa_select_blocks(sel, st.q, box, by, st.tables, st.dctx, 100, 16, workspace=ws1[:16])
+
+
+_FIRST = """
+import torch
+import paged_kv_cache_302_gb300 as pa
+pool = torch.randn(40, 16, 2, 2, 64, device="cuda").half()
+tab = torch.randperm(40, device="cuda").int().view(1, 40)
+ctx = torch.tensor([630], dtype=torch.int32, device="cuda")
+q = torch.randn(1, 8, 64, device="cuda").half()
+box = torch.zeros(40, 2, 2, 64, dtype=torch.int8, device="cuda")
+by = torch.zeros(40, 2, dtype=torch.uint8, device="cuda")
+sel = torch.zeros(1, 2, 9, dtype=torch.int32, device="cuda")
+out, ref = torch.zeros_like(q), torch.zeros_like(q)
+ks = torch.tensor([0, 300], dtype=torch.int32, device="cuda")
+keep, base = torch.arange(300, 600, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+def step(o):
+    pa.pa_summarize_blocks(box, by, pool, tab, ctx, 630)
+    pa.pa_select_blocks(sel, q, box, by, tab, ctx, 640, 16)
+    pa.pa_decode_sparse(o, q, pool, tab, ctx, sel)
+g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+torch.cuda.synchronize()
+with torch.cuda.graph(g, stream=s):
+    step(out)
+    pa.pa_compact_tokens(pool, tab, ctx, base, keep, ks)
+before = pool.clone()
+g.replay()
+torch.cuda.synchronize()
+assert not torch.equal(pool, before)
+pool.copy_(before)
+step(ref)
+assert torch.equal(out, ref) and out.abs().max() > 0
+"""
+
+
+def test_calls_captured_before_any_other():
+    """A process whose first calls are captured into a graph."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", _FIRST], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
