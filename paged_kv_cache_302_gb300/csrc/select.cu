@@ -5,8 +5,8 @@
 // in the shared memory of one of them.
 //
 // Bound by the boxes' bytes, 2 D + 1 per (block, head), and by the latency around them.  64 sequences of up to 16384
-// tokens (8 heads, 74 MB of boxes) take 25.7 us, of which 16 stream the boxes at 4.6 TB/s and 5 find the top_k; 16 of
-// 32768 (68 MB, one kernel) 21 us; 1 of 16384 4.7 us on the device, a chain of five dependent reads and the search.
+// tokens (8 heads, 74 MB of boxes) take 24.5 us, of which 15 stream the boxes at 4.9 TB/s and 5 find the top_k; 16 of
+// 32768 (68 MB, one kernel) 20 us; 1 of 16384 4.7 us on the device, a chain of five dependent reads and the search.
 #include <algorithm>
 #include <type_traits>
 
@@ -46,7 +46,7 @@ __device__ __forceinline__ uint32_t ordered(float x) {
 // >= 0 and q lo below, so a box's score is one product of length 2 D, [max(q, 0), min(q, 0)] . [hi, lo]; box and query
 // integers are exact in fp16.
 constexpr int kScoreWarps = 4;
-constexpr int kScoreCtas = 4;  // per SM
+constexpr int kScoreCtas = 5;  // per SM: 96 registers
 
 // Four 8-bit integers as two fp16 pairs: v + 128 in the low byte of 0x6400 is 1024 + 128 + v.
 __device__ __forceinline__ void int8x4_to_f16(uint32_t x, uint32_t& a, uint32_t& b) {
@@ -71,11 +71,12 @@ struct Scorer {
     static constexpr int NC = D / 64;  // 16-byte chunks of a lane: t4, t4 + 4 of each half of a box
     const SelectParams& p;
     const int g4, t4;
-    // The query integers of head g4 in two halves, max(q, 0) and min(q, 0), in the order of the box's bytes: word w of
-    // chunk c holds channels 64 c + 16 t4 + 4 w on, the k-columns 2 t4, 2 t4 + 1, 2 t4 + 8, 2 t4 + 9 of k-step (c, w).
-    uint32_t up[NC][8], dn[NC][8];
-    float f0, f1;          // units of heads 2 t4 and 2 t4 + 1
-    uint4 v[2][2][NC];     // [block g4, g4 + 8][lo, hi][chunk]
+    // The query integers of head g4, in the order of the box's bytes: word w of chunk c holds channels 64 c + 16 t4 +
+    // 4 w on, the k-columns 2 t4, 2 t4 + 1, 2 t4 + 8, 2 t4 + 9 of k-step (c, w).  Their halves max(q, 0) and min(q, 0)
+    // are taken anew for each product: kept, they cost the registers of one CTA in five (25.7 us against 24.5).
+    uint32_t qi[NC][8];
+    float f0, f1;                 // units of heads 2 t4 and 2 t4 + 1
+    uint4 v[2][2][NC];            // [block g4, g4 + 8][lo, hi][chunk]
     float unit[2], next_unit[2];  // of the two blocks (0: no such block)
     const int8_t* box[2];
 
@@ -98,10 +99,10 @@ struct Scorer {
                 if (g4 < p.G)
                     x = reinterpret_cast<const uint4*>(
                         static_cast<const T*>(p.q) + (((int64_t)s * p.H_kv + h) * p.G + g4) * D + 64 * c + 16 * t4)[i];
-                up[c][4 * i] = x.x;
-                up[c][4 * i + 1] = x.y;
-                up[c][4 * i + 2] = x.z;
-                up[c][4 * i + 3] = x.w;
+                qi[c][4 * i] = x.x;
+                qi[c][4 * i + 1] = x.y;
+                qi[c][4 * i + 2] = x.z;
+                qi[c][4 * i + 3] = x.w;
             }
     }
     __device__ __forceinline__ void make_query() {  // of what read_query brought
@@ -110,7 +111,7 @@ struct Scorer {
         for (int c = 0; c < NC; ++c)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float2 f = Mma<T>::unpack(up[c][i]);
+                const float2 f = Mma<T>::unpack(qi[c][i]);
                 m = fmaxf(m, fmaxf(fabsf(f.x), fabsf(f.y)));  // (a NaN counts as nothing)
             }
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
@@ -126,10 +127,9 @@ struct Scorer {
         for (int c = 0; c < NC; ++c)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float2 x = Mma<T>::unpack(up[c][i]);
+                const float2 x = Mma<T>::unpack(qi[c][i]);
                 const uint32_t q = Mma<__half>::pack(integer(x.x), integer(x.y));
-                up[c][i] = Pair<__half>::hi(q, 0);
-                dn[c][i] = Pair<__half>::lo(q, 0);
+                qi[c][i] = q;
             }
     }
     __device__ __forceinline__ void find(const Tile& x, float (&u)[2]) {
@@ -181,8 +181,9 @@ struct Scorer {
                         int8x4_to_f16(w0[w], a0, a2);
                         int8x4_to_f16(w1[w], a1, a3);
                         // the query's negative half meets lo, its positive half hi
-                        const uint32_t* q = k ? up[c] : dn[c];
-                        Mma<__half>::run(acc[k], a0, a1, a2, a3, q[2 * w], q[2 * w + 1]);
+                        const uint32_t x0 = qi[c][2 * w], x1 = qi[c][2 * w + 1];
+                        Mma<__half>::run(acc[k], a0, a1, a2, a3, k ? Pair<__half>::hi(x0, 0) : Pair<__half>::lo(x0, 0),
+                                         k ? Pair<__half>::hi(x1, 0) : Pair<__half>::lo(x1, 0));
                     }
                     if (left > 1) load(k, c);
                 }
@@ -418,12 +419,15 @@ __device__ __forceinline__ void all_blocks(const SelectParams& p, int nb, int32_
     for (int i = threadIdx.x; i < p.top_k; i += blockDim.x) out[i] = i < nb ? i : -1;
 }
 
+// (Where the scores' kernel runs before this one, its CTAs let this one start only once every kernel before them has
+// finished: the lengths are read without waiting for the scores.)
 template <int THREADS, int K>
-__global__ void __launch_bounds__(THREADS) top_blocks_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(THREADS) top_blocks_kernel(const SelectParams p, int early) {
+    const int h = blockIdx.x, s = blockIdx.y;
+    int nb = early ? context_blocks(p, s) : 0;
     griddep_wait();
     griddep_launch_dependents();
-    const int h = blockIdx.x, s = blockIdx.y;
-    const int nb = context_blocks(p, s);
+    if (!early) nb = context_blocks(p, s);
     const int64_t r = (int64_t)s * p.H_kv + h;
     if (nb == 0 && h == 0 && threadIdx.x == 0) flag_error(p.err, PA_DEV_ERR_CTX);
     if (nb <= p.top_k)
@@ -579,7 +583,7 @@ pa_status launch_select(const SelectArgs& a) {
         if (e != cudaSuccess) return cuda_fail(e, "score launch");
     }
     // keys in registers up to 16 per thread (32 spill)
-    void (*top)(SelectParams) = top_blocks_kernel<1024, 0>;
+    void (*top)(SelectParams, int) = top_blocks_kernel<1024, 0>;
     int threads = 1024;
     if (nb <= 256 * 8) {
         top = top_blocks_kernel<256, 8>;
@@ -590,7 +594,8 @@ pa_status launch_select(const SelectArgs& a) {
         top = top_blocks_kernel<1024, 16>;
     }
     const cudaError_t e =
-        launch_kernel(top, dim3((unsigned)a.H_kv, (unsigned)a.N), dim3((unsigned)threads), 0, a.stream, p);
+        launch_kernel(top, dim3((unsigned)a.H_kv, (unsigned)a.N), dim3((unsigned)threads), 0, a.stream, p,
+                      nb > a.top_k ? 1 : 0);
     count_launch();
     return e == cudaSuccess ? PA_OK : cuda_fail(e, "top_blocks launch");
 }
