@@ -646,7 +646,8 @@ def pa_summarize_blocks(summaries, sum_scales, pool, block_tables, ctx_lens, max
     if _summary_shape(summaries, sum_scales) != (NB, H_kv, D):
         raise PAError(PA_ERR_INVALID, "the summaries are not of this cache's blocks, heads and head dim")
     N = ctx_lens.numel()
-    if block_tables.dim() != 2 or block_tables.shape[0] != N or (q_start is not None and q_start.numel() != N + 1):
+    tables = block_tables.shape
+    if len(tables) != 2 or tables[0] != N or (q_start is not None and q_start.numel() != N + 1):
         raise PAError(PA_ERR_INVALID, "block_tables must be [N, MB], ctx_lens [N], q_start [N+1]")
     dev = _here(pool, "pool")
     _check((_lib or load()).pa_summarize_blocks(
@@ -654,7 +655,7 @@ def pa_summarize_blocks(summaries, sum_scales, pool, block_tables, ctx_lens, max
         _arg(scales, "scales", dev) if scales is not None else None, code,
         _arg(block_tables, "block_tables", dev, torch.int32), _arg(ctx_lens, "ctx_lens", dev, torch.int32),
         _arg(q_start, "q_start", dev, torch.int32) if q_start is not None else None, N, H_kv, D, B,
-        block_tables.shape[1], NB, int(max_q_len), _err_arg(dev_err, dev), _stream_arg(stream, dev)))
+        tables[1], NB, int(max_q_len), _err_arg(dev_err, dev), _stream_arg(stream, dev)))
 
 
 def pa_select_workspace_bytes(N, H_kv, max_ctx, block_size) -> int:
@@ -674,9 +675,11 @@ def pa_select_blocks(selected, q, summaries, sum_scales, block_tables, ctx_lens,
     N = ctx_lens.numel()
     if len(shape) != 3 or shape[0] != N or shape[2] != D:
         raise PAError(PA_ERR_INVALID, "q must be [N, H_q, D] of the summaries' head dim")
-    if selected.dim() != 3 or selected.shape[0] != N or selected.shape[1] != H_kv:
+    lists = selected.shape
+    if len(lists) != 3 or lists[0] != N or lists[1] != H_kv:
         raise PAError(PA_ERR_INVALID, "selected must be [N, H_kv, top_k] int32")
-    if block_tables.dim() != 2 or block_tables.shape[0] != N:
+    tables = block_tables.shape
+    if len(tables) != 2 or tables[0] != N:
         raise PAError(PA_ERR_INVALID, "block_tables must be [N, MB] and ctx_lens [N]")
     dev = _here(q, "q")
     max_ctx, block_size = int(max_ctx), int(block_size)
@@ -687,7 +690,7 @@ def pa_select_blocks(selected, q, summaries, sum_scales, block_tables, ctx_lens,
         _arg(selected, "selected", dev, torch.int32), _arg(q, "q", dev), _code(q.dtype),
         _arg(summaries, "summaries", dev), _arg(sum_scales, "sum_scales", dev),
         _arg(block_tables, "block_tables", dev, torch.int32), _arg(ctx_lens, "ctx_lens", dev, torch.int32), N, shape[1],
-        H_kv, D, block_size, block_tables.shape[1], NB, max_ctx, selected.shape[2], int(sink_blocks),
+        H_kv, D, block_size, tables[1], NB, max_ctx, lists[2], int(sink_blocks),
         int(recent_blocks), _arg(ws, "workspace", dev), ws.nbytes, _err_arg(dev_err, dev), _stream_arg(stream, dev)))
     return selected
 
@@ -711,13 +714,15 @@ def pa_decode_sparse(out, q, pool, block_tables, ctx_lens, selected, scale=None,
         raise PAError(PA_ERR_INVALID, "q and out must be [N, H_q, D] of the cache's head dim")
     if scales is None and pool.dtype is not q.dtype:
         raise PAError(PA_ERR_INVALID, "a 16-bit pool must be of q's dtype")
-    if selected.dim() != 3 or selected.shape[0] != N or selected.shape[1] != H_kv:
+    lists = selected.shape
+    if len(lists) != 3 or lists[0] != N or lists[1] != H_kv:
         raise PAError(PA_ERR_INVALID, "selected must be [N, H_kv, top_k] int32")
-    if block_tables.dim() != 2 or block_tables.shape[0] != N:
+    tables = block_tables.shape
+    if len(tables) != 2 or tables[0] != N:
         raise PAError(PA_ERR_INVALID, "block_tables must be [N, MB] and ctx_lens [N]")
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
     dev = _here(q, "q")
-    H_q, top_k = shape[1], selected.shape[2]
+    H_q, top_k = shape[1], lists[2]
     ws = workspace
     if ws is None:
         ws = _workspace(None, _sparse_bytes(N, H_q, H_kv, D, B, top_k), q.device, stream)
@@ -725,7 +730,7 @@ def pa_decode_sparse(out, q, pool, block_tables, ctx_lens, selected, scale=None,
         _out_arg(out, "out", dev), _code(out.dtype), _arg(q, "q", dev), _code(q.dtype), _arg(pool, "pool", dev),
         _arg(scales, "scales", dev) if scales is not None else None, code,
         _arg(block_tables, "block_tables", dev, torch.int32), _arg(ctx_lens, "ctx_lens", dev, torch.int32),
-        _arg(selected, "selected", dev, torch.int32), top_k, N, H_q, H_kv, D, B, block_tables.shape[1], NB, scale,
+        _arg(selected, "selected", dev, torch.int32), top_k, N, H_q, H_kv, D, B, tables[1], NB, scale,
         _arg(ws, "workspace", dev), ws.nbytes, _err_arg(dev_err, dev), _stream_arg(stream, dev)))
     return out
 
@@ -737,7 +742,8 @@ def pa_compact_tokens(pool, block_tables, ctx_lens, base, keep, keep_start, scal
     quantised cache's qpool with its scales."""
     NB, H_kv, B, D, code = _cache_shape(pool, scales)
     N = ctx_lens.numel()
-    if block_tables.dim() != 2 or block_tables.shape[0] != N or base.numel() != N or keep_start.numel() != N + 1:
+    tables = block_tables.shape
+    if len(tables) != 2 or tables[0] != N or base.numel() != N or keep_start.numel() != N + 1:
         raise PAError(PA_ERR_INVALID, "block_tables must be [N, MB], ctx_lens and base [N], keep_start [N+1]")
     dev = _here(pool, "pool")
     T = keep.numel()
@@ -745,7 +751,7 @@ def pa_compact_tokens(pool, block_tables, ctx_lens, base, keep, keep_start, scal
         _arg(pool, "pool", dev), _arg(scales, "scales", dev) if scales is not None else None, code,
         _arg(block_tables, "block_tables", dev, torch.int32), _arg(ctx_lens, "ctx_lens", dev, torch.int32),
         _arg(base, "base", dev, torch.int32), _arg(keep, "keep", dev, torch.int32) if T else None,
-        _arg(keep_start, "keep_start", dev, torch.int32), N, T, H_kv, D, B, block_tables.shape[1], NB,
+        _arg(keep_start, "keep_start", dev, torch.int32), N, T, H_kv, D, B, tables[1], NB,
         _err_arg(dev_err, dev), _stream_arg(stream, dev)))
 
 
