@@ -18,7 +18,7 @@
 // Bound by memory, 4 D (2 D + 2) bytes per listed token and head: 64 sequences of 128 blocks of 16 tokens, 8 heads (528
 // MB) take 87 us, 6.1 TB/s, a plain kernel with a CTA per row 556; 16 of 256 blocks over e4m3 rows (136 MB) 33.4 us,
 // 4.1 TB/s: five of them pass before the first block arrives (lengths, list, block table, block), three in the join.
-// One sequence of 64 blocks, by clusters: 6.7 us on the device.
+// One sequence of 64 blocks, by clusters: 6.5 us on the device.
 #include <algorithm>
 #include <type_traits>
 
@@ -185,8 +185,16 @@ __global__ void __launch_bounds__(kSpThreads) attend_sparse_kernel(const __grid_
     // This CTA's part of its row for the cluster's join: maxima and sums of the query heads, then their outputs.  It
     // lies in the ring, which is empty by then: a cluster's CTA has one segment.
     float* share = reinterpret_cast<float*>(base);
+    // A cluster's CTA takes an equal share of whole units, of the list as it lies (an empty share is a list of padding).
+    // Its first entries are on their way beside the length.
+    [[maybe_unused]] int share0 = 0, share1 = 0, entry0 = -1;
     if constexpr (kCluster) {
-        const int ctx = p.ctx_lens[blockIdx.x / p.cluster / p.H_kv];
+        const int row = blockIdx.x / p.cluster, rank = blockIdx.x % p.cluster;
+        const int len = ((p.top_k + p.cluster - 1) / p.cluster + BPS - 1) / BPS * BPS;
+        share0 = min(rank * len, p.top_k);
+        share1 = min(share0 + len, p.top_k);
+        if (producer && share0 + lane < share1) entry0 = p.selected[(int64_t)row * p.top_k + share0 + lane];
+        const int ctx = p.ctx_lens[row / p.H_kv];
         if (ctx < 1 || ctx > p.cap) {  // (the whole cluster returns)
             if (threadIdx.x == 0 && blockIdx.x % (p.cluster * p.H_kv) == 0) flag_error(p.err, PA_DEV_ERR_CTX);
             return;
@@ -204,14 +212,12 @@ __global__ void __launch_bounds__(kSpThreads) attend_sparse_kernel(const __grid_
         run.e = run.e_end = run.left = 0;
         run.first = false;
         if constexpr (kCluster) {
-            const int row = blockIdx.x / p.cluster, rank = blockIdx.x % p.cluster;
-            // equal shares of whole units, of the list as it lies (an empty share is a list of padding)
-            const int len = ((p.top_k + p.cluster - 1) / p.cluster + BPS - 1) / BPS * BPS;
+            const int row = blockIdx.x / p.cluster;
             run.s = row / p.H_kv;
             run.h = row % p.H_kv;
             run.ctx = p.ctx_lens[run.s];
-            run.e = min(rank * len, p.top_k);
-            run.e_end = min(run.e + len, p.top_k);
+            run.e = share0;
+            run.e_end = share1;
             run.part = 0;
             run.first = true;
         } else {
@@ -321,7 +327,10 @@ __global__ void __launch_bounds__(kSpThreads) attend_sparse_kernel(const __grid_
             c.ctx = run.ctx;
             c.first = run.first;
             const int n = min(32, run.e_end - run.e);
-            if (lane < n) c.entry = p.selected[(int64_t)c.row * p.top_k + run.e + lane];
+            if (kCluster && run.first)
+                c.entry = entry0;
+            else if (lane < n)
+                c.entry = p.selected[(int64_t)c.row * p.top_k + run.e + lane];
             run.first = false;
             run.e += n;
             c.last = run.e >= run.e_end;
