@@ -31,18 +31,27 @@ namespace pa {
 
 constexpr int kUnitTok = 32;       // tokens of a unit: one pipeline stage
 constexpr int kSpThreads = 64;
-constexpr int kSpCtas16 = 4, kSpCtas8 = 7;  // CTAs per SM over 16-bit and over e4m3 rows
-constexpr int kSpMaxCtas = 152 * kSpCtas8;
+// Units of a run at least: few long rows are not cut into more parts than the join is worth.  8 rows of 4096 tokens,
+// D = 128, e4m3: 12.9 us, 14.2 with six, 21.0 with one; of 8192 tokens 17.2, 16.6, 22.8.
+constexpr int kMinRun = 4;
+
+// CTAs per SM.  Fewer leave a CTA more stages in flight, more run more consumer chains beside one another: e4m3, D =
+// 128, 1024 rows of 2048 tokens 79 us with seven, 81 with six, 86 with eight; 16 bits, D = 128, the same 137 with four,
+// 139 with three, 140 with five; e4m3, D = 64, 512 such rows 32 with eight or ten, 34 with nine or seven; 16 bits, D =
+// 64, the same 54 with six or seven, 63 with five or eight, but 224 rows of 4096 tokens 44 with six, 232 rows 60 with
+// seven.
+constexpr int sparse_ctas(bool quant, int D) { return D == 128 ? (quant ? 7 : 4) : quant ? 8 : 6; }
+constexpr int kSpMaxCtas = 152 * sparse_ctas(true, 64);
 // Calls that take a cluster per row: the largest size, up to 8, at which the device holds the clusters of all rows at
-// once (four CTAs on an SM over 16-bit rows, seven over e4m3 rows), provided that a CTA's share of the list is short.
-// One kernel instead of two, and nothing to find: over 16-bit rows 8 rows of 1024 tokens take 6.7 us against 9.4 by
-// runs, 144 rows of 512 tokens 11.6 against 14.0, 512 rows of 256 tokens 18.1 against 19.7; 192 rows of 2048 tokens,
-// 1024 to a CTA, 39.1 against 38.1.  Over e4m3 rows 112 rows of 1024 tokens take 11.5 us against 14.7, 256 rows 18.2
-// against 20.6; 144 rows of 2048 tokens, 512 to a CTA, 25.7 against 22.0, but 256 such rows, which nearly fill the
-// device, 28.2 against 31.7.
+// once, provided that a CTA's share of the list is short.  One kernel instead of two, and nothing to find.  By clusters
+// against by runs, 256 tokens to a CTA, D = 128: 48 rows over e4m3 12.7 us against 13.9, 232 rows 17.5 against 18.8; 24
+// rows over 16 bits 11.5 against 12.7, 128 rows 16.1 against 17.7.  Longer shares pay where the clusters fill seven
+// eighths of the device and equal runs have little to gain: 504 rows of 1024 tokens over e4m3 28.8 against 29.7 (312
+// such rows 26.9 against 22.1; 504 rows of 2048 even), 72 rows of 8192 tokens over 16 bits 49.3 against 51.7 (24 rows
+// of 4096 18.4 against 17.2).
 constexpr int kSpMaxCluster = 8;
-constexpr int kSpShare16 = 512, kSpShare8 = 256;  // tokens of a CTA's share
-constexpr int kSpShare8Full = 512;                // the same where the clusters fill seven eighths of the device
+constexpr int kSpShare = 256;                              // tokens of a CTA's share
+constexpr int kSpShareFull16 = 1024, kSpShareFull8 = 512;  // the same on a device that is seven eighths full
 constexpr int kJoinWarps = 8;
 
 enum : int { kSpFirst = 1, kSpLast = 2, kSpDone = 4 };
@@ -83,7 +92,7 @@ struct SpGeo {
     static constexpr uint32_t kScales = kQuant ? kUnitTok * 2 : 0;
     static constexpr uint32_t kQ = kMaxGroup * D * 2;
     static constexpr uint32_t kPerStage = kSlot + kScales + kQ + sizeof(SpMeta) + 16;
-    static constexpr int kCtas = kQuant ? kSpCtas8 : kSpCtas16;
+    static constexpr int kCtas = sparse_ctas(kQuant, D);
     static constexpr int kStages = (233472 / kCtas - 1024 - 1024 - 16) / (int)kPerStage;
     static constexpr size_t kSmem = 1024 + (size_t)kStages * kPerStage + 16;
     static_assert((2 * kMaxGroup + kMaxGroup * D) * sizeof(float) <= kSlot, "a part fits a stage");
@@ -185,8 +194,8 @@ __global__ void __launch_bounds__(kSpThreads) attend_sparse_kernel(const __grid_
     // This CTA's part of its row for the cluster's join: maxima and sums of the query heads, then their outputs.  It
     // lies in the ring, which is empty by then: a cluster's CTA has one segment.
     float* share = reinterpret_cast<float*>(base);
-    // A cluster's CTA takes an equal share of whole units, of the list as it lies (an empty share is a list of padding).
-    // Its first entries are on their way beside the length.
+    // A cluster's CTA takes an equal share of whole units, of the list as it lies (an empty share is a list of
+    // padding). Its first entries are on their way beside the length.
     [[maybe_unused]] int share0 = 0, share1 = 0, entry0 = -1;
     if constexpr (kCluster) {
         const int row = blockIdx.x / p.cluster, rank = blockIdx.x % p.cluster;
@@ -207,7 +216,7 @@ __global__ void __launch_bounds__(kSpThreads) attend_sparse_kernel(const __grid_
         const auto units_of = [&](int s) { return row_units<LGB>(p, p.ctx_lens[s]); };
         const RowScan<decltype(units_of)> scan(units_of, kCluster ? 0 : p.N, p.H_kv);
         const int total = kCluster ? 1 : scan.total();
-        const int ctas = max(1, min((int)gridDim.x, total));
+        const int ctas = max(1, min((int)gridDim.x, (total + kMinRun - 1) / kMinRun));
         const Cut cut(total, ctas);
         run.e = run.e_end = run.left = 0;
         run.first = false;
@@ -778,8 +787,10 @@ __global__ void __launch_bounds__(kSpThreads) attend_sparse_kernel(const __grid_
 template <typename OutT, int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_sparse_kernel(const SpParams p) {
     constexpr int V = D / 32, kBatch = 8;
+    // (Without an early start for the next kernel: what comes in beside CTAs of this one lies so in the SM's shared
+    // memory that its last CTA may find no room until its first one ends.  Calls after calls over 1024 rows of 2048
+    // tokens, 16 bits, D = 128: 137 us, 162 with it; 8 rows 0.2 us more.)
     griddep_wait();
-    griddep_launch_dependents();
     const int lane = threadIdx.x & 31;
     const int64_t r = (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
     if (r >= (int64_t)p.N * p.H_kv * p.G) return;
@@ -848,7 +859,7 @@ static bool sparse_layout(int N, int H_q, int H_kv, int D, int B, int top_k, Spa
     const int64_t rows = (int64_t)N * H_kv, units = ((int64_t)top_k * B + kUnitTok - 1) / kUnitTok;
     if (units >= (1LL << 31) / rows || rows * (H_q / H_kv) > 0x7fffffffLL) return false;
     auto align = [](size_t x) { return (x + 255) & ~size_t(255); };
-    L->ctas = (int)std::min<int64_t>(kSpMaxCtas, rows * units);
+    L->ctas = (int)std::min<int64_t>(kSpMaxCtas, (rows * units + kMinRun - 1) / kMinRun);
     const size_t parts = (size_t)2 * L->ctas * (H_q / H_kv);
     L->m = align((size_t)rows * sizeof(int2));
     L->l = align(L->m + parts * sizeof(float));
@@ -890,7 +901,7 @@ static pa_status run_sparse(const DecodeSparseArgs& a, SpParams& p, const Sparse
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(attend_sparse)");
     static ClusterRoom room;
     const int64_t rows = (int64_t)a.N * a.H_kv, tokens = (int64_t)a.top_k * B;
-    constexpr int kShare = kQuant ? kSpShare8 : kSpShare16, kShareFull = kQuant ? kSpShare8Full : kSpShare16;
+    constexpr int kShareFull = kQuant ? kSpShareFull8 : kSpShareFull16;
     p.cluster = 0;
     for (int size = kSpMaxCluster; size > 0; size /= 2) {
         if (tokens > (int64_t)size * kShareFull) break;
@@ -898,7 +909,7 @@ static pa_status run_sparse(const DecodeSparseArgs& a, SpParams& p, const Sparse
         e = room.get(in_cluster, size, kSpThreads, Geo::kSmem, &held);
         if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveClusters(attend_sparse)");
         if (rows > held) continue;
-        if (tokens <= (int64_t)size * (8 * rows >= 7 * (int64_t)held ? kShareFull : kShare)) p.cluster = size;
+        if (tokens <= (int64_t)size * (8 * rows >= 7 * (int64_t)held ? kShareFull : kSpShare)) p.cluster = size;
         break;
     }
     if (p.cluster) {
