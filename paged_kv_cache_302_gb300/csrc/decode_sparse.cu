@@ -16,8 +16,8 @@
 // Short lists and few rows take one kernel instead, a cluster of CTAs per row (below).
 //
 // Bound by memory, 4 D (2 D + 2) bytes per listed token and head: 64 sequences of 128 blocks of 16 tokens, 8 heads (528
-// MB) take 87 us, 6.1 TB/s, a plain kernel with a CTA per row 556; 16 of 256 blocks over e4m3 rows (136 MB) 33.4 us,
-// 4.1 TB/s: five of them pass before the first block arrives (lengths, list, block table, block), three in the join.
+// MB) take 83 us, 6.4 TB/s, a plain kernel with a CTA per row 556; 16 of 256 blocks over e4m3 rows (136 MB) 31.6 us,
+// 4.3 TB/s: five of them pass before the first block arrives (lengths, list, block table, block), three in the join.
 // One sequence of 64 blocks, by clusters: 6.5 us on the device.
 #include <algorithm>
 #include <type_traits>

@@ -389,6 +389,32 @@ def test_attention_counts_repeated_blocks_and_takes_lists_in_any_order(quant, ti
 
 
 @pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("H, D, B, ctx", [
+    (1, 64, 8, [1]), (1, 128, 8, [33]), (2, 64, 16, [64]), (1, 64, 8, [97]), (1, 128, 16, [128]), (1, 64, 32, [129]),
+    (1, 128, 8, [160]), (3, 64, 16, [96]), (2, 128, 32, [150, 1]), (3, 64, 8, [32, 96, 64, 31]), (1, 64, 16, [2300]),
+    (1, 128, 8, [2100, 1, 2000])])
+def test_attention_of_few_units_by_runs(H, D, B, ctx, quant):
+    """Long lists over short contexts: fewer units than a run takes, one more, rows cut at every place."""
+    G, top_k = 4, 300
+    g = torch.Generator().manual_seed(sum(ctx) + D + B)
+    MB, NB = -(-max(ctx) // B), sum(-(-L // B) for L in ctx) + 2
+    c = S.make_cache(g, NB, H, B, D, "bf16", quant)
+    tables = S.make_tables(g, ctx, B, MB, NB)
+    q = torch.randn(len(ctx), H * G, D, generator=g).bfloat16()
+    sel = torch.full((len(ctx), H, top_k), -1, dtype=torch.int32)
+    for s, L in enumerate(ctx):
+        for h in range(H):
+            pick = torch.randperm(-(-L // B), generator=g)[:top_k].to(torch.int32)
+            sel[s, h, : len(pick)] = pick
+    out = torch.full(q.shape, math.nan, dtype=torch.float32, device="cuda")
+    err = err_word()
+    pa.pa_decode_sparse(out, q.cuda(), c[0], tables.cuda(), i32(ctx), sel.cuda(), dev_err=err, **scales_of(c))
+    want, tol = want_sparse(q, S.host_cache(c), tables, ctx, sel, B, 1 / math.sqrt(D), "bf16", quant)
+    R.close(out, want, tol, "sparse decode")
+    assert err.item() == 0
+
+
+@pytest.mark.parametrize("quant", [False, True])
 @pytest.mark.parametrize("D", [64, 128])
 def test_every_block_listed_is_the_whole_decode(D, quant):
     H, G, B, ctx = 4, 4, 16, [1000, 33, 512]
