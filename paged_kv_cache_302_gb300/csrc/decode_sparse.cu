@@ -16,7 +16,7 @@
 // Short lists and few rows take one kernel instead, a cluster of CTAs per row (below).
 //
 // Bound by memory, 4 D (2 D + 2) bytes per listed token and head: 64 sequences of 128 blocks of 16 tokens, 8 heads (528
-// MB) take 83 us, 6.4 TB/s, a plain kernel with a CTA per row 556; 16 of 256 blocks over e4m3 rows (136 MB) 31.6 us,
+// MB) take 83-86 us, 6.3 TB/s, a plain kernel with a CTA per row 556; 16 of 256 blocks over e4m3 rows (136 MB) 31.6 us,
 // 4.3 TB/s: five of them pass before the first block arrives (lengths, list, block table, block), three in the join.
 // One sequence of 64 blocks, by clusters: 6.5 us on the device.
 #include <algorithm>
@@ -31,8 +31,8 @@ namespace pa {
 
 constexpr int kUnitTok = 32;       // tokens of a unit: one pipeline stage
 constexpr int kSpThreads = 64;
-// Units of a run at least: few long rows are not cut into more parts than the join is worth.  8 rows of 4096 tokens,
-// D = 128, e4m3: 12.9 us, 14.2 with six, 21.0 with one; of 8192 tokens 17.2, 16.6, 22.8.
+// No more runs than one for this many units: few long rows are not cut into more parts than the join is worth.  8 rows
+// of 4096 tokens, D = 128, e4m3: 12.9 us, 14.2 with six, 21.0 with one; of 8192 tokens 17.2, 16.6, 22.8.
 constexpr int kMinRun = 4;
 
 // CTAs per SM.  Fewer leave a CTA more stages in flight, more run more consumer chains beside one another: e4m3, D =
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kSpThreads) attend_sparse_kernel(const __grid_
         const auto units_of = [&](int s) { return row_units<LGB>(p, p.ctx_lens[s]); };
         const RowScan<decltype(units_of)> scan(units_of, kCluster ? 0 : p.N, p.H_kv);
         const int total = kCluster ? 1 : scan.total();
-        const int ctas = max(1, min((int)gridDim.x, (total + kMinRun - 1) / kMinRun));
+        const int ctas = min((int)gridDim.x, (total - 1) / kMinRun + 1);
         const Cut cut(total, ctas);
         run.e = run.e_end = run.left = 0;
         run.first = false;
