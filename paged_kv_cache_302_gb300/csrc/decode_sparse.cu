@@ -73,6 +73,7 @@ struct SpParams {
     const int32_t* ctx_lens;
     const int32_t* selected;
     int top_k, N, H_kv, G, MB, NB;
+    int ctas;          // CTAs that the workspace has parts for
     int64_t cap;       // tokens a block-table row holds
     float scale_log2;
     int2* cuts;        // [N * H_kv]: first and last CTA of a divided row, (-1, -1) for a whole one
@@ -382,6 +383,10 @@ __global__ void __launch_bounds__(kSpThreads) attend_sparse_kernel(const __grid_
             blk = blk1;
             nv = nv1;
             nxt = after;
+        }
+        if constexpr (!kCluster) {
+            // a wait that ran out: the run's other rows still get their cuts, which the join reads
+            while (!ok && nxt.some) nxt = next_chunk();
         }
         if (ok && lane == 0) {
             ok = mbar_wait_bounded(empty_s + 8 * slot, ephase ^ 1, abort_flag, p.wait_ns);
@@ -799,7 +804,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_sparse_kernel(const SpPa
     const int ctx = p.ctx_lens[row / p.H_kv];
     if (ctx < 1 || ctx > p.cap) return;
     const int2 cut = p.cuts[row];
-    if (cut.x < 0) return;
+    // A whole row, or no cuts at all, should the lengths have changed since: no part is looked up behind the workspace's.
+    if (cut.x < 0 || cut.y < cut.x || cut.y >= p.ctas) return;
     const int n = cut.y - cut.x + 1;
     auto part = [&](int i) -> int64_t { return (int64_t)(2 * (cut.x + i) + (i == 0 ? 1 : 0)) * p.G + g; };
     float M = -INFINITY, L = 0.f, o[V];
@@ -956,6 +962,7 @@ pa_status launch_decode_sparse(const DecodeSparseArgs& a) {
     p.G = a.H_q / a.H_kv;
     p.MB = a.MB;
     p.NB = a.NB;
+    p.ctas = L.ctas;
     p.cap = (int64_t)a.MB * a.B;
     p.scale_log2 = (float)((double)a.scale * 1.4426950408889634);  // log2(e)
     p.cuts = reinterpret_cast<int2*>(ws);

@@ -680,6 +680,41 @@ def test_waits_that_run_out_flag_and_leave_the_gpu_usable(N, top_k, quant):
     assert err.item() == 0 and torch.equal(again, out)
 
 
+@pytest.mark.parametrize("quant", [False, True])
+def test_rows_that_a_timeout_leaves_out_are_not_joined(quant):
+    """Forty whole rows to a CTA, none divided, in a workspace whose cuts and parts are those of no call (in range all the
+    same): after waits of 1 ns every row is as it was or as it should be, never made up from the workspace."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    H, G, D, B, top_k, NB = 8, 4, 128, 16, 2, 64
+    N = 40 * (7 if quant else 4) * sms // H              # CTAs per SM of the two kernels
+    g = torch.Generator().manual_seed(16)
+    c = S.make_cache(g, NB, H, B, D, "bf16", quant)
+    tables = torch.randint(0, NB, (N, 2), generator=g).to(torch.int32).cuda()
+    q = torch.randn(N, H * G, D, generator=g).bfloat16().cuda()
+    ctx = i32([2 * B] * N)
+    sel = torch.tensor([0, 1], dtype=torch.int32, device="cuda").expand(N, H, 2).contiguous()
+    ws = torch.zeros(pa.pa_decode_sparse_workspace_bytes(N, H * G, H, D, B, top_k), dtype=torch.uint8, device="cuda")
+    err = err_word()
+    clean = torch.full(q.shape, math.nan, device="cuda")
+    pa.pa_decode_sparse(clean, q, c[0], tables, ctx, sel, workspace=ws, dev_err=err, **scales_of(c))
+    assert err.item() == 0 and not clean.isnan().any()
+    left = 0
+    for _ in range(3):
+        ws[: 8 * N * H].fill_(0)                         # cuts (0, 0)
+        ws[8 * N * H:].view(torch.float32).fill_(1.0)
+        out = torch.full_like(clean, 9.0)
+        pa.pa_set_wait_limit_ns(1)
+        try:
+            pa.pa_decode_sparse(out, q, c[0], tables, ctx, sel, workspace=ws, dev_err=err, **scales_of(c))
+            torch.cuda.synchronize()
+        finally:
+            pa.pa_set_wait_limit_ns(0)
+        untouched, right = (out == 9.0).all(-1), (out == clean).all(-1)
+        assert (untouched | right).all()
+        left += int(untouched.sum())
+    assert left > 0 and err.item() == pa.PA_DEV_ERR_TIMEOUT
+
+
 def test_tensors_of_another_place_are_refused():
     st = Step(15, [100, 50], 2, 2, 64, 16, "f16", False, 4)
     box, by, sel, out, ws1, ws2 = st.buffers()
