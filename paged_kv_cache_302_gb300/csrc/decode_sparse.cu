@@ -767,7 +767,7 @@ __global__ void __launch_bounds__(kSpThreads) attend_sparse_kernel(const __grid_
                 m[c] = c < p.cluster ? ld_cluster(at + 4 * g, c) : NEG_INF;
                 M = fmaxf(M, m[c]);
             }
-            if (M > NEG_INF) {  // (else the list is empty)
+            if (M > NEG_INF) {
 #pragma unroll
                 for (int c = 0; c < kSpMaxCluster; ++c) {
                     if (c >= p.cluster) continue;
@@ -776,6 +776,8 @@ __global__ void __launch_bounds__(kSpThreads) attend_sparse_kernel(const __grid_
                     o += f * ld_cluster(at + 4 * (2 * kMaxGroup + i), c);
                 }
                 o /= L;
+            } else {  // no score, or none that is a number: zeros, or NaN like the sums
+                for (int c = 0; c < p.cluster; ++c) o += ld_cluster(at + 4 * (kMaxGroup + g), c);
             }
             const int64_t to = (int64_t)row * n + i;
             if (p.out_dtype == PA_F32)
@@ -831,7 +833,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_sparse_kernel(const SpPa
 #pragma unroll
         for (int k = kBatch / 2; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
         top = fmaxf(M, __shfl_sync(0xffffffffu, top, 0));
-        if (top == -INFINITY) continue;  // only empty parts so far
+        if (top == -INFINITY) {  // only parts without a score so far, or with none that is a number: sums of 0 or NaN
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) L += __shfl_sync(0xffffffffu, l, j);
+            continue;
+        }
         const float f = fast_exp2(M - top), w = fast_exp2(m - top);
         M = top;
         L *= f;
@@ -845,7 +851,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_sparse_kernel(const SpPa
             for (int v = 0; v < V; ++v) o[v] += wj * a[j][v];
         }
     }
-    const float inv = M > -INFINITY ? 1.f / L : 0.f;
+    const float inv = M > -INFINITY ? 1.f / L : L;
     OutT* out = static_cast<OutT*>(p.out) + r * D + lane * V;
 #pragma unroll
     for (int v = 0; v < V; ++v) out[v] = from_float<OutT>(o[v] * inv);

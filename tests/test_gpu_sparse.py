@@ -388,6 +388,55 @@ def test_attention_counts_repeated_blocks_and_takes_lists_in_any_order(quant, ti
     R.close(out, want, tol, "sparse decode")
 
 
+@pytest.mark.parametrize("out32", [False, True])
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("N, L, top_k", [
+    (3, 500, 20), (3, 9000, 600), (700, 60, 4)])     # in clusters; in runs, rows divided; in runs, most rows whole
+def test_attention_with_nan_in_queries_and_keys(N, L, top_k, D, quant, out32):
+    """A NaN in one head's query, in every listed key of a KV head, in one listed key: these rows are NaN and no other is;
+    lists without a block give zeros beside them, NaN query or not."""
+    H, G, B, NB = 2, 4, 16, 600
+    g = torch.Generator().manual_seed(N + D)
+    c = S.make_cache(g, NB, H, B, D, "bf16", quant)
+    tables = torch.stack([torch.randperm(NB - 2, generator=g)[: -(-L // B)] for _ in range(N)]).to(torch.int32)
+    q = torch.randn(N, H * G, D, generator=g).bfloat16()
+    ctx = [L] * N
+    sel = random_lists(g, ctx, H, B, top_k)
+    sel[1, 1] = -1                                   # no block
+    bad = torch.zeros(N, H * G, dtype=torch.bool)
+    for s, h in ((0, 1), (1, 2), (1, 6), (N - 1, 0)):
+        q[s, h, 5] = math.nan
+        bad[s, h] = h != 6                           # (sequence 1's second KV head has no block)
+    tables[2, :] = NB - 1                            # a sequence whose second KV head's keys are all NaN
+    pick = sel[0, 1][sel[0, 1] >= 0][0].item()       # and one whose second KV head has one such key
+    tables[0, pick] = NB - 2
+    if quant:
+        c[0].view(torch.uint8)[NB - 1, 1, 0, :, 3] = 0x7F
+        c[0].view(torch.uint8)[NB - 2, 1, 0, 1, 9] = 0xFF
+    else:
+        c[0][NB - 1, :, 0, 1, 3] = math.nan
+        c[0][NB - 2, 1, 0, 1, 9] = math.nan
+    bad[2, G:] = bad[0, G:] = True
+    out = torch.full(q.shape, 9.0, dtype=torch.float32 if out32 else q.dtype, device="cuda")
+    err = err_word()
+    pa.pa_decode_sparse(out, q.cuda(), c[0], tables.cuda(), i32(ctx), sel.cuda(), dev_err=err, **scales_of(c))
+    assert err.item() == 0
+    nan = out.isnan().cpu()
+    assert torch.equal(nan.all(-1), bad) and torch.equal(nan.any(-1), bad)
+    assert (out[1, G:] == 0).all()
+    some = [0, 1, 2, N - 1]                          # the rows beside them
+    for h in range(H):
+        k = [S.keys_of(S.host_cache(c), tables[s].numpy(), h, L) for s in some]
+        for i, s in enumerate(some):
+            rows = [r for r in range(h * G, h * G + G) if not bad[s, r]]
+            t = [x for e in sel[s, h].tolist() if e >= 0 for x in range(e * B, min(L, e * B + B))]
+            if rows and t:
+                want, tol = R.attend(R.to64(q[s, rows]), k[i][0][t], k[i][1][t], k[i][2][t], np.ones((len(rows), len(t)), bool),
+                                     1 / math.sqrt(D), True, quant)
+                R.close(out[s, rows], want, tol, "rows beside NaN")
+
+
 @pytest.mark.parametrize("quant", [False, True])
 @pytest.mark.parametrize("H, D, B, ctx", [
     (1, 64, 8, [1]), (1, 128, 8, [33]), (2, 64, 16, [64]), (1, 64, 8, [97]), (1, 128, 16, [128]), (1, 64, 32, [129]),
