@@ -414,9 +414,16 @@ __device__ __forceinline__ void top_blocks(const SelectParams& p, int nb, const 
     });
 }
 
-// The list of a row with no more blocks than top_k: all of them.
-__device__ __forceinline__ void all_blocks(const SelectParams& p, int nb, int32_t* out) {
-    for (int i = threadIdx.x; i < p.top_k; i += blockDim.x) out[i] = i < nb ? i : -1;
+// The list of a row with no more blocks than top_k: all of them.  No score has looked at their block-table entries: the
+// sequence's first row does.
+__device__ __forceinline__ void all_blocks(const SelectParams& p, int s, int h, int nb, int32_t* out) {
+    const int32_t* table = p.tables + (int64_t)s * p.MB;
+    bool bad = false;
+    for (int i = threadIdx.x; i < p.top_k; i += blockDim.x) {
+        if (h == 0 && i < nb) bad = bad || (unsigned)table[i] >= (unsigned)p.NB;
+        out[i] = i < nb ? i : -1;
+    }
+    if (bad) flag_error(p.err, PA_DEV_ERR_BLOCK);
 }
 
 // (Where the scores' kernel runs before this one, its CTAs let this one start only once every kernel before them has
@@ -431,7 +438,7 @@ __global__ void __launch_bounds__(THREADS) top_blocks_kernel(const SelectParams 
     const int64_t r = (int64_t)s * p.H_kv + h;
     if (nb == 0 && h == 0 && threadIdx.x == 0) flag_error(p.err, PA_DEV_ERR_CTX);
     if (nb <= p.top_k)
-        all_blocks(p, nb, p.selected + r * p.top_k);
+        all_blocks(p, s, h, nb, p.selected + r * p.top_k);
     else
         top_blocks<THREADS, K>(p, nb, p.keys + r * p.stride, p.selected + r * p.top_k);
 }
@@ -463,7 +470,7 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) select_row_kernel(cons
     cluster_wait();
     if (x.nb <= p.top_k) {  // (the whole cluster returns)
         if (x.nb == 0 && x.h == 0 && rank == 0 && threadIdx.x == 0) flag_error(p.err, PA_DEV_ERR_CTX);
-        if (rank == 0) all_blocks(p, x.nb, out);
+        if (rank == 0) all_blocks(p, x.s, x.h, x.nb, out);
         return;
     }
     const int warps = p.cluster * (THREADS / 32);

@@ -260,6 +260,26 @@ def test_selection_flags():
                  max_ctx=400)
 
 
+@pytest.mark.parametrize("N", [3, 700])              # one kernel, a cluster per row; two kernels
+@pytest.mark.parametrize("lens, MB", [([40, 8, 128], 16), ([40, 8, 4000], 500)])
+def test_selection_flags_entries_of_contexts_that_it_lists_whole(lens, MB, N):
+    """Contexts of no more than top_k blocks, alone and beside a longer one: every entry is looked at, the last one too, and
+    none behind the context."""
+    D, B, H, top_k = 64, 8, 2, 16
+    g = torch.Generator().manual_seed(5)
+    box, by = S.make_boxes(g, MB, H, D)
+    ctx = (lens * N)[:N]
+    tables = torch.full((N, MB), -1, dtype=torch.int32)
+    for s, L in enumerate(ctx):
+        tables[s, : -(-L // B)] = torch.randperm(MB, generator=g)[: -(-L // B)].to(torch.int32)
+    q = torch.randn(N, 4, D, generator=g).half()
+    check_select(q, box, by, tables, ctx, B, top_k, 1, 1, H, max_ctx=MB * B)
+    for s, b, entry in ((0, 0, MB), (0, 4, -1), (1, 0, 1 << 30), (N - 2, 0, -2 ** 31)):
+        t = tables.clone()
+        t[s, b] = entry
+        check_select(q, box, by, t, ctx, B, top_k, 1, 1, H, flag=pa.PA_DEV_ERR_BLOCK, max_ctx=MB * B)
+
+
 # ------------------------------------------------------------------------------------------------ attention
 
 def random_lists(g, ctx, H, B, top_k, fill=1.0):
