@@ -354,8 +354,11 @@ pa_status pa_decode_tree(void* out, pa_dtype out_dtype, const void* q, pa_dtype 
  * [N+1] int32, or NULL: n_s = ctx_lens[s].  n_s = 0 is allowed.  A sequence with
  * n_s outside [0, max_q_len], or a context below n_s or above MB*B, is flagged
  * PA_DEV_ERR_CTX and left out; a block-table entry outside [0, NB) is flagged
- * PA_DEV_ERR_BLOCK and skipped.  A block that several sequences share has to
- * hold as many tokens in each.  pool, scales, kv_dtype: as pa_decode_tree.
+ * PA_DEV_ERR_BLOCK and skipped.  A block that several sequences share is
+ * summarised through one that holds the most of its tokens (its box covers the
+ * others' too); sequences of one call that rebuild it have to hold as many of
+ * them.  Blocks that pa_copy_blocks or pa_swap_blocks fill need their summaries
+ * copied along, or rebuilt.  pool, scales, kv_dtype: as pa_decode_tree.
  * max_q_len == 0 is a no-op.
  *
  * pa_select_blocks lists top_k blocks for each (sequence, KV head).  Block b's
@@ -418,8 +421,10 @@ pa_status pa_decode_sparse(void* out, pa_dtype out_dtype, const void* q, pa_dtyp
  * MB*B] are flagged PA_DEV_ERR_CTX.  A token whose block-table entry, old or new,
  * is outside [0, NB) is not moved and flagged PA_DEV_ERR_BLOCK.  A block that is
  * written has to belong to one sequence alone (pa_alloc_compact_batch sees to
- * that).  Key summaries of blocks from base[s] / B on have to be rebuilt
- * (pa_summarize_blocks with the new contexts and chunks of n_s).
+ * that).  Key summaries of blocks from base[s] / B on have to be rebuilt:
+ * pa_summarize_blocks with the new contexts and chunks of n_s, or of 1 where n_s =
+ * 0 and base[s] is inside a block that no other sequence shares (its box still
+ * covers the tokens that went).  Truncation alone asks for the same.
  * pool, scales, kv_dtype, sizes: as pa_summarize_blocks.  T == 0 is a no-op.
  * ---------------------------------------------------------------------- */
 pa_status pa_compact_tokens(void* pool, void* scales, pa_dtype kv_dtype, const int32_t* block_tables,

@@ -303,3 +303,66 @@ def test_a_generation_with_drafts_forks_and_evictions(quant):
     for s in range(5):
         alloc.free_seq(s)
     assert alloc.num_free() == NB
+
+
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("base", [21, 24, 3])
+def test_summaries_after_drafts_of_which_nothing_is_kept(base, quant):
+    """Drafts written and summarised, none accepted (or a context cut back further): the header's procedure, a chunk of 1
+    where base lies inside a block, makes every box its tokens' again.  A fork that is cut back leaves the box of the block it
+    still shares as the longer sequence needs it."""
+    H, D, B, NB, MB = 2, 64, 8, 24, 8
+    gen = torch.Generator().manual_seed(base)
+    alloc = pa.BlockAllocator(NB, B)
+    if quant:
+        cache = (torch.zeros(NB, H, 2, B, D, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn),
+                 torch.zeros(NB, H, 2, B, dtype=torch.uint8, device="cuda"))
+    else:
+        cache = (torch.zeros(NB, B, 2, H, D, dtype=torch.bfloat16, device="cuda"),)
+    kw = {"scales": cache[1]} if quant else {}
+    box = torch.zeros(NB, H, 2, D, dtype=torch.int8, device="cuda")
+    by = torch.zeros(NB, H, dtype=torch.uint8, device="cuda")
+    err = err_word()
+
+    def append(s, n, size):
+        slots, cow = alloc.append_slots(s, n)
+        for x in cache if len(cow) else ():
+            pa.pa_copy_blocks(x, torch.from_numpy(np.ascontiguousarray(cow)).cuda(), dev_err=err)
+        k, v = ((size * torch.randn(n, H, D, generator=gen)).bfloat16().cuda() for _ in range(2))
+        write = pa.pa_reshape_and_cache_quant if quant else pa.pa_reshape_and_cache
+        write(k, v, *cache, torch.from_numpy(slots).cuda(), dev_err=err)
+
+    def summarize(s, n):
+        t, ctx = alloc.block_tables([s], MB)
+        pa.pa_summarize_blocks(box, by, cache[0], torch.from_numpy(t).cuda(), torch.from_numpy(ctx).cuda(), max(n, 1),
+                               q_start=i32([0, n]), dev_err=err, **kw)
+
+    def as_defined(s):
+        """Per block and head, whether its summary is that of the sequence's tokens."""
+        blocks, L = alloc.block_table(s), alloc.seq_len(s)
+        res = []
+        for b, blk in enumerate(blocks):
+            for h in range(H):
+                want, e = S.box(S.keys_of(S.host_cache(cache), [blk], h, min(B, L - b * B))[0])
+                res.append(np.array_equal(box[blk, h].cpu().numpy(), want) and by[blk, h].item() == e)
+        return np.array(res)
+
+    alloc.add_seq(0)
+    append(0, 24 if base == 24 else 21, 1.0)
+    summarize(0, alloc.seq_len(0))
+    alloc.fork(0, 1)
+    append(0, 9, 50.0)
+    summarize(0, 9)
+    assert as_defined(0).all()
+    cow = alloc.compact_batch([0], [base], [base])
+    assert len(cow) == 0 and alloc.seq_len(0) == base
+    shared = base == 3                               # the first block is the fork's too
+    if base % B and not shared:
+        assert not as_defined(0).all()               # nothing kept, nothing rebuilt by a chunk of 0
+        summarize(0, 1)
+    if not shared:
+        assert as_defined(0).all()
+    assert as_defined(1).all()                       # (the shared block's box covers both sequences' tokens)
+    alloc.fork(1, 2)
+    alloc.compact_batch([2], [18], [18])
+    assert as_defined(1).all() and err.item() == 0
