@@ -42,7 +42,8 @@ class PAError(RuntimeError):
         self.status = status
 
 
-_lib = None
+_lib = None       # as load() gives it
+_calls = None     # the same library, for the calls below
 _lock = threading.Lock()
 
 
@@ -52,25 +53,34 @@ def library_path() -> str:
 
 def load(build: bool = True) -> ctypes.CDLL:
     """Load libpa.so (compiling it first when it is missing or stale)."""
-    global _lib
+    global _lib, _calls
     with _lock:
         if _lib is None:
             path = _build.build() if build else _build.LIB
             if not os.path.exists(path):
                 raise RuntimeError(f"libpa.so not found at {path}")
-            L = ctypes.CDLL(path)
-            _declare(L)
-            _lib = L
+            lib, calls = ctypes.CDLL(path), ctypes.CDLL(path)
+            _declare(lib, ctypes.c_int)
+            _declare(calls, _Int)
+            _lib, _calls = lib, calls
     return _lib
 
 
+def _quick() -> ctypes.CDLL:
+    """The library for calls whose integers are Python's own."""
+    if _calls is None:
+        load()
+    return _calls
+
+
 class _Int:
-    """A C int parameter: ctypes passes a Python int as one by itself, cheaper than through c_int (a call has a dozen)."""
+    """A C int parameter: ctypes passes a Python int as one by itself, cheaper than through c_int (a call has a dozen),
+    which takes c_int instances too."""
 
     from_param = operator.index
 
 
-def _declare(L):
+def _declare(L, int_type):
     P, i32, i64, sz, f32, u64 = (ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float,
                                  ctypes.c_uint64)
     sig = {
@@ -136,7 +146,7 @@ def _declare(L):
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
-        fn.argtypes = [_Int if a is i32 else a for a in args]
+        fn.argtypes = [int_type if a is i32 else a for a in args]
         fn.restype = res
     del i64
 
@@ -329,7 +339,7 @@ def pa_reshape_and_cache(k, v, pool, slot_mapping, dev_err=None, stream=None):
         raise PAError(PA_ERR_INVALID, "shape/dtype mismatch between k, v and pool")
     if slot_mapping.numel() != T:
         raise PAError(PA_ERR_INVALID, "slot_mapping must have T entries")
-    L = load()
+    L = _quick()
     _check(L.pa_reshape_and_cache(_dev(k, "k"), _dev(v, "v", k.dtype), _dev(pool, "pool"),
                                   _dev(slot_mapping, "slot_mapping", torch.int64), T, NB, B, H_kv, D,
                                   _dtype_code(k.dtype), _err_ptr(dev_err), _stream_ptr(stream)))
@@ -340,7 +350,7 @@ def pa_copy_blocks(pool, pairs, dev_err=None, stream=None):
     calls, one with its qpool and one with its scales."""
     NB, B, _, H_kv, D, code = _block_shape(pool)
     n = pairs.shape[0] if pairs.numel() else 0
-    L = load()
+    L = _quick()
     _check(L.pa_copy_blocks(_dev(pool, "pool"), _dev(pairs, "pairs", torch.int64) if n else None, n, NB, B, H_kv, D,
                             code, _err_ptr(dev_err), _stream_ptr(stream)))
 
@@ -379,7 +389,7 @@ def pa_decode(out, q, pool, block_tables, ctx_lens, max_ctx, scale=None, partiti
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
     nbytes = pa_decode_workspace_bytes(N, H_q, H_kv, D, int(max_ctx), partition_tokens)
     ws = _workspace(workspace, nbytes, q.device, stream)
-    L = load()
+    L = _quick()
     _check(L.pa_decode(_acc(out, "out"), _dtype_code(out.dtype), _dev(q, "q"), _dev(pool, "pool"),
                        _dev(block_tables, "block_tables", torch.int32), _dev(ctx_lens, "ctx_lens", torch.int32), N,
                        H_q, H_kv, D, B, MB, NB, int(max_ctx), scale, int(partition_tokens), _dev(ws, "workspace"),
@@ -408,7 +418,7 @@ def pa_swap_blocks(dst_pool, src_pool, pairs, dev_err=None, stream=None):
     if pairs.dtype != torch.int64:
         raise PAError(PA_ERR_INVALID, "pairs must be int64")
     n = pairs.shape[0] if pairs.numel() else 0
-    L = load()
+    L = _quick()
     _check(L.pa_swap_blocks(_acc(dst_pool, "dst_pool"), NBd, _acc(src_pool, "src_pool"), NBs,
                             _acc(pairs, "pairs") if n else None, n, B, H_kv, D, code,
                             _err_ptr(dev_err), _stream_ptr(stream)))
@@ -418,7 +428,7 @@ def pa_update_block_tables(tables, updates, dev_err=None, stream=None):
     """Apply (row, logical block, physical block) updates [n, 3] (int32, device) to tables [N, MB]."""
     N, MB = tables.shape
     n = updates.shape[0] if updates.numel() else 0
-    L = load()
+    L = _quick()
     _check(L.pa_update_block_tables(_dev(tables, "tables", torch.int32), N, MB,
                                     _dev(updates, "updates", torch.int32) if n else None, n, _err_ptr(dev_err),
                                     _stream_ptr(stream)))
@@ -443,7 +453,7 @@ def pa_decode_no_alloc(out, q, pool, block_tables, ctx_lens, max_ctx, scale=None
     if tuple(block_tables.shape) != (N, MB) or ctx_lens.numel() != N:
         raise PAError(PA_ERR_INVALID, "block_tables must be [N, MB] and ctx_lens [N]")
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-    L = load()
+    L = _quick()
     _check(L.pa_decode_no_alloc(_acc(out, "out"), _dtype_code(out.dtype), _dev(q, "q"), _dev(pool, "pool"),
                                 _dev(block_tables, "block_tables", torch.int32),
                                 _dev(ctx_lens, "ctx_lens", torch.int32), N, H_q, H_kv, D, B, MB, NB, int(max_ctx),
@@ -464,7 +474,7 @@ def pa_decode_contiguous(out, q, k_buf, v_buf, req_ids, ctx_lens, max_ctx, scale
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
     nbytes = pa_decode_workspace_bytes(N, H_q, H_kv, D, int(max_ctx), partition_tokens)
     ws = _workspace(workspace, nbytes, q.device, stream)
-    L = load()
+    L = _quick()
     _check(L.pa_decode_contiguous(_dev(out, "out"), _dtype_code(out.dtype), _dev(q, "q"), _dev(k_buf, "k_buf"),
                                   _dev(v_buf, "v_buf"), _dev(req_ids, "req_ids", torch.int32),
                                   _dev(ctx_lens, "ctx_lens", torch.int32), N, H_q, H_kv, D, N_max, S_max,
@@ -497,7 +507,7 @@ def pa_prefill(out, q, pool, block_tables, ctx_lens, q_start, max_q_len, scale=N
     if stage_v and pool.dtype == torch.bfloat16:
         ws = _workspace(workspace, pa_prefill_workspace_bytes(N, H_kv, D, B, MB), q.device, stream)
         ws_bytes = ws.numel() * ws.element_size()
-    L = load()
+    L = _quick()
     _check(L.pa_prefill(_dev(out, "out"), _dtype_code(out.dtype), _dev(q, "q"), _dev(pool, "pool"),
                         _dev(block_tables, "block_tables", torch.int32), _dev(ctx_lens, "ctx_lens", torch.int32),
                         _dev(q_start, "q_start", torch.int32), N, T, H_q, H_kv, D, B, MB, NB, int(max_q_len), scale,
@@ -517,7 +527,7 @@ def pa_reshape_and_cache_quant(k, v, qpool, scales, slot_mapping, dev_err=None, 
     if slot_mapping.numel() != T:
         raise PAError(PA_ERR_INVALID, "slot_mapping must have T entries")
     dev = _here(k, "k")
-    _check((_lib or load()).pa_reshape_and_cache_quant(
+    _check((_calls or _quick()).pa_reshape_and_cache_quant(
         _arg(k, "k", dev), _arg(v, "v", dev, k.dtype), _arg(qpool, "qpool", dev), _arg(scales, "scales", dev),
         _arg(slot_mapping, "slot_mapping", dev, torch.int64), T, NB, B, H_kv, D, _code(k.dtype),
         _err_arg(dev_err, dev), _stream_arg(stream, dev)))
@@ -533,7 +543,7 @@ def pa_dequant_blocks(dst_pool, qpool, scales, pairs, dev_err=None, stream=None)
         raise PAError(PA_ERR_INVALID, "pairs must be [n, 2] int64")
     n = pairs.shape[0] if pairs.numel() else 0
     dev = _here(dst_pool, "dst_pool")
-    _check((_lib or load()).pa_dequant_blocks(
+    _check((_calls or _quick()).pa_dequant_blocks(
         _arg(dst_pool, "dst_pool", dev), dst_pool.shape[0], _arg(qpool, "qpool", dev), _arg(scales, "scales", dev), NB,
         _arg(pairs, "pairs", dev) if n else None, n, B, H_kv, D, _code(dst_pool.dtype), _err_arg(dev_err, dev),
         _stream_arg(stream, dev)))
@@ -557,7 +567,7 @@ def pa_decode_quant(out, q, qpool, scales, block_tables, ctx_lens, max_ctx, scal
     ws = workspace
     if ws is None:
         ws = _workspace(None, _decode_bytes(N, H_q, H_kv, D, max_ctx, partition_tokens), q.device, stream)
-    _check((_lib or load()).pa_decode_quant(
+    _check((_calls or _quick()).pa_decode_quant(
         _out_arg(out, "out", dev), _code(out.dtype), _arg(q, "q", dev), _code(q.dtype), _arg(qpool, "qpool", dev),
         _arg(scales, "scales", dev), _arg(block_tables, "block_tables", dev, torch.int32),
         _arg(ctx_lens, "ctx_lens", dev, torch.int32), N, H_q, H_kv, D, B, block_tables.shape[1], NB, max_ctx, scale,
@@ -604,7 +614,7 @@ def pa_decode_tree(out, q, pool, block_tables, ctx_lens, q_start, tree_mask, max
     ws = workspace
     if ws is None:
         ws = _workspace(None, _tree_bytes(N, H_q, H_kv, D, max_q_len), q.device, stream)
-    _check((_lib or load()).pa_decode_tree(
+    _check((_calls or _quick()).pa_decode_tree(
         _arg(out, "out", dev), _code(out.dtype), _arg(q, "q", dev), _code(q.dtype), _arg(pool, "pool", dev),
         _arg(scales, "scales", dev) if scales is not None else None, code,
         _arg(block_tables, "block_tables", dev, torch.int32), _arg(ctx_lens, "ctx_lens", dev, torch.int32),
@@ -650,7 +660,7 @@ def pa_summarize_blocks(summaries, sum_scales, pool, block_tables, ctx_lens, max
     if len(tables) != 2 or tables[0] != N or (q_start is not None and q_start.numel() != N + 1):
         raise PAError(PA_ERR_INVALID, "block_tables must be [N, MB], ctx_lens [N], q_start [N+1]")
     dev = _here(pool, "pool")
-    _check((_lib or load()).pa_summarize_blocks(
+    _check((_calls or _quick()).pa_summarize_blocks(
         _arg(summaries, "summaries", dev), _arg(sum_scales, "sum_scales", dev), _arg(pool, "pool", dev),
         _arg(scales, "scales", dev) if scales is not None else None, code,
         _arg(block_tables, "block_tables", dev, torch.int32), _arg(ctx_lens, "ctx_lens", dev, torch.int32),
@@ -686,7 +696,7 @@ def pa_select_blocks(selected, q, summaries, sum_scales, block_tables, ctx_lens,
     ws = workspace
     if ws is None:
         ws = _workspace(None, _select_bytes(N, H_kv, max_ctx, block_size), q.device, stream)
-    _check((_lib or load()).pa_select_blocks(
+    _check((_calls or _quick()).pa_select_blocks(
         _arg(selected, "selected", dev, torch.int32), _arg(q, "q", dev), _code(q.dtype),
         _arg(summaries, "summaries", dev), _arg(sum_scales, "sum_scales", dev),
         _arg(block_tables, "block_tables", dev, torch.int32), _arg(ctx_lens, "ctx_lens", dev, torch.int32), N, shape[1],
@@ -726,7 +736,7 @@ def pa_decode_sparse(out, q, pool, block_tables, ctx_lens, selected, scale=None,
     ws = workspace
     if ws is None:
         ws = _workspace(None, _sparse_bytes(N, H_q, H_kv, D, B, top_k), q.device, stream)
-    _check((_lib or load()).pa_decode_sparse(
+    _check((_calls or _quick()).pa_decode_sparse(
         _out_arg(out, "out", dev), _code(out.dtype), _arg(q, "q", dev), _code(q.dtype), _arg(pool, "pool", dev),
         _arg(scales, "scales", dev) if scales is not None else None, code,
         _arg(block_tables, "block_tables", dev, torch.int32), _arg(ctx_lens, "ctx_lens", dev, torch.int32),
@@ -747,7 +757,7 @@ def pa_compact_tokens(pool, block_tables, ctx_lens, base, keep, keep_start, scal
         raise PAError(PA_ERR_INVALID, "block_tables must be [N, MB], ctx_lens and base [N], keep_start [N+1]")
     dev = _here(pool, "pool")
     T = keep.numel()
-    _check((_lib or load()).pa_compact_tokens(
+    _check((_calls or _quick()).pa_compact_tokens(
         _arg(pool, "pool", dev), _arg(scales, "scales", dev) if scales is not None else None, code,
         _arg(block_tables, "block_tables", dev, torch.int32), _arg(ctx_lens, "ctx_lens", dev, torch.int32),
         _arg(base, "base", dev, torch.int32), _arg(keep, "keep", dev, torch.int32) if T else None,
@@ -762,7 +772,7 @@ def pa_write_contiguous(k, v, k_ptr, v_ptr, req_ids, positions, N_max, S_max, de
     def ptr(x):
         return _dev(x, "buffer") if isinstance(x, torch.Tensor) else ctypes.c_void_p(int(x))
 
-    L = load()
+    L = _quick()
     _check(L.pa_write_contiguous(_dev(k, "k"), _dev(v, "v", k.dtype), ptr(k_ptr), ptr(v_ptr),
                                  _dev(req_ids, "req_ids", torch.int32), _dev(positions, "positions", torch.int32), T,
                                  int(N_max), int(S_max), H_kv, D, _dtype_code(k.dtype), _err_ptr(dev_err),
@@ -847,7 +857,7 @@ def pa_partition_reduce(out, part_m2, part_l, part_acc, nparts, dev_err=None, st
     R, P, D = part_acc.shape
     if tuple(part_m2.shape) != (R, P) or tuple(part_l.shape) != (R, P) or tuple(out.shape) != (R, D):
         raise PAError(PA_ERR_INVALID, "shape mismatch")
-    L = load()
+    L = _quick()
     _check(L.pa_partition_reduce(_dev(out, "out"), _dtype_code(out.dtype), _dev(part_m2, "part_m2", torch.float32),
                                  _dev(part_l, "part_l", torch.float32), _dev(part_acc, "part_acc", torch.float32),
                                  _dev(nparts, "nparts", torch.int32), R, P, D, _err_ptr(dev_err),

@@ -335,3 +335,23 @@ def test_allocator_import_rejects_inconsistent_states():
         s[seq0 + 1] += 4 * int(s[2])                                       # tokens no longer match the blocks
         return s
     bad(wrong_len)
+
+
+def test_integers_of_every_kind_are_taken_as_c_ints():
+    """c_int instances, numpy integers and booleans pass wherever a Python int does; floats and None do not."""
+    L, c = pa.load(), ctypes.c_int
+    want = L.pa_decode_workspace_bytes(4, 32, 8, 128, 1000, 0)
+    assert L.pa_decode_workspace_bytes(c(4), c(32), c(8), c(128), c(1000), c(0)) == want > 0
+    assert pa.pa_decode_workspace_bytes(c(4), np.int64(32), np.int32(8), c(128), c(1000), False) == want
+    assert pa.pa_prefill_workspace_bytes(c(4), c(8), c(128), c(16), c(64)) > 0
+    assert pa.pa_decode_tree_workspace_bytes(c(4), c(32), c(8), c(128), c(9)) > 0
+    assert pa.pa_select_workspace_bytes(c(4), c(8), c(1000), c(16)) == pa.pa_select_workspace_bytes(4, 8, 1000, 16)
+    assert pa.pa_decode_sparse_workspace_bytes(c(4), c(32), c(8), c(128), c(16), c(9)) > 0
+    a = pa.BlockAllocator(8, 4)
+    a.add_seq(3)
+    a.append_slots(3, 6)
+    assert L.pa_alloc_fork(a._h, c(3), c(4)) == pa.PA_OK and a.seq_len(4) == 6 and a.refcount(0) == 2
+    assert L.pa_copy_blocks(0x1000, None, c(0), c(8), c(16), c(2), c(64), c(pa.PA_F16), None, None) == pa.PA_OK
+    for bad in (4.0, None, "4"):
+        with pytest.raises((ctypes.ArgumentError, TypeError)):
+            L.pa_decode_workspace_bytes(bad, 32, 8, 128, 1000, 0)
