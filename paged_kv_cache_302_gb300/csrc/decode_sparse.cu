@@ -119,9 +119,10 @@ __device__ __forceinline__ uint32_t sp_lds8(uint32_t a) {
 // Units of every row of a sequence of ctx tokens (0: the context is out of range).
 template <int LGB>
 __device__ __forceinline__ int row_units(const SpParams& p, int ctx) {
+    constexpr int kPerUnit = kUnitTok >> LGB;  // (in blocks: a list's tokens may be 2^31)
     if (ctx < 1 || ctx > p.cap) return 0;
     const int nb = (ctx + (1 << LGB) - 1) >> LGB;
-    return ((min(nb, p.top_k) << LGB) + kUnitTok - 1) / kUnitTok;
+    return (min(nb, p.top_k) + kPerUnit - 1) / kPerUnit;
 }
 
 // The run of a CTA, walked chunk by chunk of at most 32 list entries.  Everything is uniform over the warp.

@@ -603,6 +603,34 @@ def test_captured_step_follows_what_its_inputs_hold(shape):
         assert torch.equal(sel, fresh[2]) and torch.equal(out, fresh[3])
 
 
+@pytest.mark.parametrize("quant", [False, True])
+def test_attention_over_a_list_of_nearly_2_31_tokens(quant):
+    """As many tokens as block tables can name, through a table whose entries are all one block: the softmax over its tokens,
+    the last five counting once less.  Each of a CTA's fp32 additions, four to a unit, is off by at most 2^-22 of the sum so
+    far."""
+    H, G, D, B, NB = 1, 2, 64, 16, 2
+    MB = 2 ** 27 - 1
+    L = MB * B - 5
+    g = torch.Generator().manual_seed(17)
+    c = S.make_cache(g, NB, H, B, D, "bf16", quant)
+    q = torch.randn(1, G, D, generator=g).bfloat16()
+    tables = torch.ones(1, MB, dtype=torch.int32, device="cuda")
+    sel = torch.arange(MB, dtype=torch.int32, device="cuda").view(1, 1, MB)
+    out = torch.full(q.shape, 1e9, device="cuda")
+    err = err_word()
+    pa.pa_decode_sparse(out, q.cuda(), c[0], tables, i32([L]), sel, dev_err=err, **scales_of(c))
+    assert err.item() == 0
+    k, v, ev = S.keys_of(S.host_cache(c), [1], 0, B)
+    n = np.where(np.arange(B) < B - 5, MB, MB - 1.0)
+    s = R.to64(q[0]) @ k.T / 8
+    w = n * np.exp(s - s.max(axis=1, keepdims=True))
+    want, mag = (w @ v) / w.sum(axis=1, keepdims=True), (w @ np.abs(v)) / w.sum(axis=1, keepdims=True)
+    _, tol = R.attend(R.to64(q[0]), k, v, ev, np.ones((G, len(n)), bool), 1 / 8, True, quant)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    steps = 4 * 2 * (MB * B // 32 // (sms * 4) + 1)      # (four CTAs per SM or more; numerator and denominator)
+    R.close(out[0], want, tol * 2 + steps * 2.0 ** -22 * mag, "long list")
+
+
 def test_attention_into_pinned_host_memory():
     for ctx, quant in (([700, 90], False), ([500] * 40, True)):
         st = Step(5, ctx, 2, 4, 128, 16, "bf16", quant, 20)
