@@ -94,15 +94,12 @@ __global__ void __launch_bounds__(kSumThreads) summarize_kernel(const SummaryPar
         const int64_t sb = u / p.H_kv;
         const int h = (int)(u - sb * p.H_kv), s = (int)(sb / p.touched), i = (int)(sb - (int64_t)s * p.touched);
         const int ctx = p.ctx_lens[s];
-        int n = ctx;
-        if (p.q_start) {
-            const int q0 = p.q_start[s];
-            n = p.q_start[s + 1] - q0;
-        }
-        if (n < 0 || n > p.max_q_len || ctx < n || ctx > p.MB * B) {
+        const int64_t chunk = p.q_start ? (int64_t)p.q_start[s + 1] - p.q_start[s] : ctx;
+        if (chunk < 0 || chunk > p.max_q_len || ctx < chunk || ctx > p.MB * B) {
             if (i == 0 && h == 0 && sub == 0) flag_error(p.err, PA_DEV_ERR_CTX);
             continue;
         }
+        const int n = (int)chunk;
         const int b = ((ctx - n) >> LGB) + i;
         if (n == 0 || b * (int64_t)B >= ctx) continue;
         const int blk = p.tables[(int64_t)s * p.MB + b];

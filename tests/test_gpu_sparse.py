@@ -154,6 +154,18 @@ def test_summaries_flag_and_leave_out_bad_sequences():
         assert np.array_equal(box.cpu().numpy(), want[0]) and np.array_equal(by.cpu().numpy(), want[1])
 
 
+def test_summaries_flag_chunks_past_32_bits():
+    """Offsets whose difference is 1 only modulo 2^32 are no chunk of one token."""
+    D, B, NB = 64, 8, 4
+    c = S.make_cache(torch.Generator().manual_seed(2), NB, 2, B, D, "bf16", False)
+    for qs in ([2 ** 31 - 1, -2 ** 31], [-2 ** 31, 2 ** 31 - 1]):
+        box, by = poisoned_boxes(NB, 2, D)
+        err = err_word()
+        pa.pa_summarize_blocks(box, by, c[0], torch.arange(NB, dtype=torch.int32, device="cuda").view(1, NB), i32([20]), 4,
+                               q_start=i32(qs), dev_err=err)
+        assert err.item() == pa.PA_DEV_ERR_CTX and (box == 55).all() and (by == 0xEE).all()
+
+
 # ------------------------------------------------------------------------------------------------ selection
 
 def check_select(q, box, by, tables, ctx, B, top_k, sink, recent, H, flag=0, max_ctx=None, ctx_flag=()):
