@@ -417,14 +417,16 @@ pa_status pa_decode_sparse(void* out, pa_dtype out_dtype, const void* q, pa_dtyp
  * base[s] on, all below ctx_lens[s]; keep_start: [N+1] int32, not decreasing,
  * within [0, T]; base: [N] int32.
  * From its first position that is out of order or out of range on, a list is
- * not followed; that, keep_start or base out of range and a context outside [0,
- * MB*B] are flagged PA_DEV_ERR_CTX.  A token whose block-table entry, old or new,
- * is outside [0, NB) is not moved and flagged PA_DEV_ERR_BLOCK.  A block that is
- * written has to belong to one sequence alone (pa_alloc_compact_batch sees to
- * that).  Key summaries of blocks from base[s] / B on have to be rebuilt:
- * pa_summarize_blocks with the new contexts and chunks of n_s, or of 1 where n_s =
- * 0 and base[s] is inside a block that no other sequence shares (its box still
- * covers the tokens that went).  Truncation alone asks for the same.
+ * not followed (bad block-table entries of tokens behind it may be flagged all
+ * the same); that, keep_start or base out of range and a context outside [0,
+ * MB*B] are flagged PA_DEV_ERR_CTX.  A token that would move from or to a
+ * block-table entry outside [0, NB) stays and is flagged PA_DEV_ERR_BLOCK (one
+ * kept where it is needs no entry).  A block that is written has to belong to
+ * one sequence alone (pa_alloc_compact_batch sees to that).  Key summaries of
+ * blocks from base[s] / B on have to be rebuilt: pa_summarize_blocks with the new
+ * contexts and chunks of n_s, or of 1 where n_s = 0 and base[s] is inside a block
+ * that no other sequence shares (its box still covers the tokens that went).
+ * Truncation alone asks for the same.
  * pool, scales, kv_dtype, sizes: as pa_summarize_blocks.  T == 0 is a no-op.
  * ---------------------------------------------------------------------- */
 pa_status pa_compact_tokens(void* pool, void* scales, pa_dtype kv_dtype, const int32_t* block_tables,

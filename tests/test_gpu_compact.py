@@ -117,6 +117,21 @@ def test_tokens_without_a_block_stay_and_are_flagged(quant):
     run(c, t, [L], [0], [keep], B, flag=pa.PA_DEV_ERR_BLOCK, moves=moves)
 
 
+@pytest.mark.parametrize("quant", [False, True])
+def test_entries_of_tokens_that_stay_are_not_looked_at(quant):
+    g = torch.Generator().manual_seed(10)
+    B, H, D, L = 8, 2, 64, 4000
+    c = random_cache(g, 502, H, B, D, quant)
+    tables = S.make_tables(g, [L], B, 500, 502)
+    keep = np.r_[np.arange(16, 800), np.arange(900, 1000)]
+    t = tables.clone()
+    t[0, 2:90] = -1                                  # of tokens that are kept where they are
+    run(c, t, [L], [16], [keep], B, moves=[(0, int(k), 800 + j) for j, k in enumerate(keep[784:])])
+    t = tables.clone()
+    t[0, 100:113] = -1                               # of the places that the others move to
+    run(c, t, [L], [16], [keep], B, flag=pa.PA_DEV_ERR_BLOCK, moves=[])
+
+
 def test_list_offsets_out_of_range_are_flagged():
     g = torch.Generator().manual_seed(5)
     B, H, D, ctx = 8, 1, 64, [50, 50, 50]
