@@ -386,9 +386,9 @@ pa_status pa_decode_tree(void* out, pa_dtype out_dtype, const void* q, pa_dtype 
  * PA_DEV_ERR_BLOCK; a block listed twice counts twice.  A list without a block
  * gives a row of zeros.  Slots past the context may hold anything, NaN included.
  * A context below 1 or above MB*B is flagged PA_DEV_ERR_CTX and its rows are not
- * written.  q, out: [N][H_q][D], out F32 or q_dtype, in device memory or pinned
- * host memory; pool, scales, kv_dtype: as pa_decode_tree; workspace as above, of
- * pa_decode_sparse_workspace_bytes(...).  scale > 0 and finite.  Results do not
+ * written.  q: [N][H_q][D] in device memory; out: the same of F32 or q_dtype, in
+ * device memory or pinned host memory; pool, scales, kv_dtype: as pa_decode_tree;
+ * workspace as above, of pa_decode_sparse_workspace_bytes(...).  scale > 0 and finite.  Results do not
  * depend on the order in which the GPU runs the call's parts.
  * ---------------------------------------------------------------------- */
 pa_status pa_summarize_blocks(void* summaries, void* sum_scales, const void* pool, const void* scales,
