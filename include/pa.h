@@ -367,8 +367,9 @@ pa_status pa_decode_tree(void* out, pa_dtype out_dtype, const void* q, pa_dtype 
  *     score_b = max_h 2^(e + f_h) * sum_d max(i_hd * least_d, i_hd * greatest_d),
  * i_hd = q_hd * 2^-f_h rounded to the nearest integer (ties to even, saturating at
  * +-511, NaN to 0), f_h the least in [-40, 40] with max_d |q_hd| <= 511 * 2^f_h
- * (-40 for a row of zeros).  The sum is exact, so the selection does not depend
- * on the order in which the GPU adds.  A context of nb = ceil(ctx / B) blocks
+ * (-40 for a row of zeros).  So a key's product with q_h exceeds its block's score
+ * by no more than 2^(f_h - 1) * sum_d |K_d|, saturation apart.  The sum is exact,
+ * and the selection does not depend on the order in which the GPU adds.  A context of nb = ceil(ctx / B) blocks
  * keeps its first sink_blocks, its last recent_blocks and the best others, ties
  * to the lower block, top_k in all (all nb where nb <= top_k):
  *   selected: [N][H_kv][top_k] int32, logical blocks ascending, then -1.
@@ -388,8 +389,9 @@ pa_status pa_decode_tree(void* out, pa_dtype out_dtype, const void* q, pa_dtype 
  * A context below 1 or above MB*B is flagged PA_DEV_ERR_CTX and its rows are not
  * written.  q: [N][H_q][D] in device memory; out: the same of F32 or q_dtype, in
  * device memory or pinned host memory; pool, scales, kv_dtype: as pa_decode_tree;
- * workspace as above, of pa_decode_sparse_workspace_bytes(...).  scale > 0 and finite.  Results do not
- * depend on the order in which the GPU runs the call's parts.
+ * workspace as above, of pa_decode_sparse_workspace_bytes(...).  scale > 0 and
+ * finite.  Results do not depend on the order in which the GPU runs the call's
+ * parts.
  * ---------------------------------------------------------------------- */
 pa_status pa_summarize_blocks(void* summaries, void* sum_scales, const void* pool, const void* scales,
                               pa_dtype kv_dtype, const int32_t* block_tables, const int32_t* ctx_lens,

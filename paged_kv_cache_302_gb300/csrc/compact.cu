@@ -47,7 +47,7 @@ constexpr int kMoveStages = 3;
 constexpr int kSpan = 2048;
 constexpr int kMinLgw = 1, kMaxLgw = 8;  // columns of a CTA: at least one 32-byte sector
 constexpr int kLook = kSpan / kMoveThreads;
-constexpr int kMoveCtas = 152 * 5 / 2;  // as many as the columns are spread over
+constexpr int kMoveCtas = 152 * 5 / 2;  // as many as the columns are spread over (time only; by the device built for)
 constexpr size_t kMoveSmem = (size_t)kMoveStages * kMoveThreads * kMoveUnroll * 16 + 2 * kSpan * sizeof(int2);
 // the copies of chunk i + kMoveStages - 1 follow chunk i's barrier, the third step comes before that of a span's third
 static_assert(kSpan / ((kMoveThreads >> kMinLgw) * kMoveUnroll) >= kMoveStages + 1, "a span's rows are there in time");

@@ -41,6 +41,7 @@ constexpr int kMinRun = 4;
 // 64, the same 54 with six or seven, 63 with five or eight, but 224 rows of 4096 tokens 44 with six, 232 rows 60 with
 // seven.
 constexpr int sparse_ctas(bool quant, int D) { return D == 128 ? (quant ? 7 : 4) : quant ? 8 : 6; }
+// Of the workspace, whose size is asked without a device: one with more SMs than 152 takes no more CTAs.
 constexpr int kSpMaxCtas = 152 * sparse_ctas(true, 64);
 // Calls that take a cluster per row: the largest size, up to 8, at which the device holds the clusters of all rows at
 // once, provided that a CTA's share of the list is short.  One kernel instead of two, and nothing to find.  By clusters
@@ -807,7 +808,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_sparse_kernel(const SpPa
     const int ctx = p.ctx_lens[row / p.H_kv];
     if (ctx < 1 || ctx > p.cap) return;
     const int2 cut = p.cuts[row];
-    // A whole row, or no cuts at all, should the lengths have changed since: no part is looked up behind the workspace's.
+    // A whole row.  (Or no cuts at all, should the lengths have changed since: no part is looked up behind the
+    // workspace's.)
     if (cut.x < 0 || cut.y < cut.x || cut.y >= p.ctas) return;
     const int n = cut.y - cut.x + 1;
     auto part = [&](int i) -> int64_t { return (int64_t)(2 * (cut.x + i) + (i == 0 ? 1 : 0)) * p.G + g; };

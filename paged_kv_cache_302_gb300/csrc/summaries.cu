@@ -11,10 +11,11 @@ namespace pa {
 // ignore NaN elements: the instructions return the other operand.  16-bit rows are compared as they are, two channels
 // at a time; e4m3 rows as fp16 pairs in units of the block's largest scale, exact while the scales lie within 2^14 of
 // one another (fp32 otherwise).  A box is rounded to integers by a multiply-add with directed rounding that leaves the
-// integer in the low bits. Bound by memory: 8 contexts of 16384 tokens with 8 heads (285 MB) take 46 us, 6.2 TB/s; 32
-// ragged chunks over e4m3 (101 MB) 22.5 us, 4.5 TB/s, its ALU pipe half busy.  CTAs of 128 threads took 46 us where 256
-// took 48 (the last wave is shorter); 16 tokens on their way at a time instead of 8 46 and 51, 4 of them 51.  Over e4m3
-// minima and maxima in fp32 took 50 us, fp16 pairs with a rounding function per channel 26.
+// integer in the low bits.  Bound by memory: 8 contexts of 16384 tokens with 8 heads (285 MB) take 46 us, 6.2 TB/s; 32
+// ragged chunks over e4m3 (101 MB) 22.5 us, 4.5 TB/s, are bound by latency: rows wait for the scale bytes, one read more
+// in the chain, with 40 % of the SM's warps resident; the ALU pipe and the issue slots are half busy.  CTAs of 128
+// threads took 46 us where 256 took 48 (the last wave is shorter); 16 tokens on their way at a time instead of 8 46 and
+// 51, 4 of them 51.  Over e4m3 minima and maxima in fp32 took 50 us, fp16 pairs with a rounding function per channel 26.
 constexpr int kSumThreads = 128;
 constexpr int kSumBatch = 8;  // tokens of a block on their way at a time
 

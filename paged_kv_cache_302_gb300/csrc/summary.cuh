@@ -5,10 +5,11 @@
 // tokens, as integers of 8 bits in units of one power of two,
 //     lo_d = floor(min_t K_td 2^-e),  hi_d = ceil(max_t K_td 2^-e),  e the least with max |K| <= 127 2^e:
 //   summaries [NB][H_kv][2][D] int8 (lo, hi), sum_scales [NB][H_kv] bytes, b standing for 2^(b - 127).
-// No key of the block has a larger product with a query q than sum_d max(q_d lo_d, q_d hi_d) 2^e: that sum is the
-// block's score.  With q in integers of 9 bits and a sign (q_d 2^-f rounded, f the least with max |q| <= 511 2^f) every
-// sum is an integer below 128 * 127 * 511 < 2^23, hence exact in fp32 in any order: the selection does not depend on
-// how the sum is split.
+// No key of the block has a larger product with a query q than sum_d max(q_d lo_d, q_d hi_d) 2^e (as long as none
+// saturates).  A block's score is that sum for q in integers of 9 bits and a sign (q_d 2^-f rounded, f the least with
+// max |q| <= 511 2^f): it bounds the products with q itself up to the rounding, 2^(f - 1) sum_d |K_d|.  Every such sum
+// is an integer below 128 * 127 * 511 < 2^23, hence exact in fp32 in any order: the selection does not depend on how
+// the sum is split.
 #pragma once
 
 #include "quant.cuh"
